@@ -447,7 +447,7 @@ def prepare(case, seed):
                   "k": torch.empty((case["T"], h, d), **bf), "v": torch.empty((case["T"], h, d), **bf)}
         elif case["op"] == "fork":
             s |= {"src": ints([0] * case["forks"]), "dst": ints(list(range(1, 1 + case["forks"]))), "lens": torch.empty(cfg.seqs, dtype=torch.int32, device="cuda"),
-                  "keep": ints([v + [-1] * (8 - len(v)) for v in keeps(case)])}
+                  "keep": ints([sum(1 << j for j in v) for v in keeps(case)])}
             for i in range(case["layers"]):
                 _rows_in(s, i, ints([0]), 8, x["pk"][i][None], x["pv"][i][None])
             for name in "kv":
