@@ -451,3 +451,221 @@ class TreePlanner:
 
     def counts(self) -> np.ndarray:
         return np.array([[self.state.counts[d][b] for b in range(_TREE_BINS)] for d in range(_TREE_ROWS)])
+
+
+# ----------------------------------------------------------------------------- 8-bit key/value cache
+# (include/woq_kv8.h)
+
+KV8_INT8, KV8_E4M3 = 0, 1
+KV8_BLOCK, KV8_ROWS, KV8_MAX_SEQS = 64, 8, 1024
+WOQ_DEVERR_PAGES = 0x4
+WOQ_DEVERR_STATE = 0x8
+WOQ_DEVERR_POSITION = 0x10
+
+
+class KV8Config(ctypes.Structure):
+    """woq_kv8_config of include/woq_kv8.h."""
+    _fields_ = [("format", ctypes.c_int), ("layers", ctypes.c_int), ("kv_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("seqs", ctypes.c_int), ("max_tokens", ctypes.c_int),
+                ("pages", ctypes.c_int)]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("table", _P), ("positions", _I), ("rot_dim", _I), ("interleaved", _I), ("axes", _I), ("pos", _P),
+                ("axis_of", _P)]
+
+
+class Rope:
+    """Rotary arguments of an append (woq_rope): table fp32 [positions, rot_dim / 2, 2] from woq_rope_table;
+    pos int32 [axes, rows] (device); axis_of: the axis of each frequency (host integers; None: all 0)."""
+
+    def __init__(self, table, pos, axis_of=None, interleaved: bool = False):
+        self.table, self.pos, self.interleaved = table, pos, bool(interleaved)
+        self.axis_of = None if axis_of is None else np.ascontiguousarray(axis_of, dtype=np.uint8)
+
+    def _struct(self, rows: int) -> _Rope:
+        t, pos = self.table, self.pos
+        if t.dim() != 3 or t.shape[2] != 2:
+            raise ValueError("rope table: expected [positions, rot_dim / 2, 2]")
+        if pos.dim() != 2 or pos.shape[1] != rows:
+            raise ValueError(f"rope positions: expected [axes, {rows}], got {tuple(pos.shape)}")
+        if t.is_floating_point() is False or pos.is_floating_point():
+            raise ValueError("rope: the table is fp32, the positions int32")
+        if self.axis_of is not None and self.axis_of.size != t.shape[1]:
+            raise ValueError(f"rope axis_of: expected {t.shape[1]} entries, got {self.axis_of.size}")
+        return _Rope(_dptr(t, "rope table", 4), t.shape[0], 2 * t.shape[1], int(self.interleaved), pos.shape[0],
+                     _dptr(pos, "rope positions", 4), None if self.axis_of is None else _hptr(self.axis_of))
+
+
+_CP = ctypes.POINTER(KV8Config)
+_RP = ctypes.POINTER(_Rope)
+for _name, (_args, _res) in {
+    "woq_kv8_bytes": ([_CP], _Z),
+    "woq_kv8_page_offset": ([_CP, _I], _Z),
+    "woq_kv8_init": ([_CP, _P, _Z, _P], _I),
+    "woq_rope_table": ([ctypes.c_double, _I, _I, _P, _P], _I),
+    "woq_kv8_append_rows": ([_CP, _P, _Z, _I, _P, _I, _I, _P, _I, _I, _I, _RP, _P, _P], _I),
+    "woq_kv8_append_prompt": ([_CP, _P, _Z, _I, _I, _I, _P, _I, _I, _I, _RP, _P, _P], _I),
+    "woq_kv8_accept": ([_CP, _P, _Z, _P, _I, _P, _P], _I),
+    "woq_kv8_extend": ([_CP, _P, _Z, _I, _I, _P], _I),
+    "woq_kv8_attention_workspace": ([_CP, _I, _I, _I], _Z),
+    "woq_kv8_attention": ([_CP, _P, _Z, _I, _P, _I, _I, _P, _I, _P, ctypes.c_float, _I, _I, _P, _P, _Z, _P], _I),
+    "woq_kv8_fork": ([_CP, _P, _Z, _P, _P, _I, _P], _I),
+    "woq_kv8_free": ([_CP, _P, _Z, _P, _I, _P], _I),
+    "woq_kv8_copy": ([_CP, _P, _Z, _CP, _P, _Z, _P, _P, _I, _P], _I),
+    "woq_kv8_compact": ([_CP, _P, _Z, _I, _P], _I),
+    "woq_kv8_read": ([_CP, _P, _Z, _I, _I, _I, _I, _P, _P, _P], _I),
+    "woq_kv8_state": ([_CP, _P, _Z, _P, _P, _P, _P], _I),
+}.items():
+    _f = getattr(lib, _name)
+    _f.argtypes = _args
+    _f.restype = _res
+
+
+def woq_kv8_bytes(cfg: KV8Config) -> int:
+    return lib.woq_kv8_bytes(ctypes.byref(cfg))
+
+
+def woq_kv8_page_offset(cfg: KV8Config, page: int) -> int:
+    return lib.woq_kv8_page_offset(ctypes.byref(cfg), page)
+
+
+def woq_kv8_attention_workspace(cfg: KV8Config, n: int, rows: int, q_heads: int) -> int:
+    return lib.woq_kv8_attention_workspace(ctypes.byref(cfg), n, rows, q_heads)
+
+
+def _cache_args(cfg: KV8Config, cache):
+    return ctypes.byref(cfg), _dptr(cache, "cache", 1), _nbytes(cache)
+
+
+def _ints(t, name: str, numel: int):
+    if t is not None and t.is_floating_point():
+        raise ValueError(f"{name}: expected 32-bit integers, got {t.dtype}")
+    return _dptr(t, name, 4, numel)
+
+
+def _bf16(t, name: str, numel: int):
+    if t is not None and not str(t.dtype).endswith("bfloat16"):
+        raise ValueError(f"{name}: expected bfloat16, got {t.dtype}")
+    return _dptr(t, name, 2, numel)
+
+
+def woq_kv8_init(cfg: KV8Config, cache, stream=None) -> None:
+    """Make an empty cache of a uint8 tensor of woq_kv8_bytes(cfg) bytes."""
+    _check(lib.woq_kv8_init(*_cache_args(cfg, cache), _stream(stream)), "woq_kv8_init")
+
+
+def woq_rope_table(theta: float, rot_dim: int, table, stream=None) -> None:
+    """Fill table (fp32 [positions, rot_dim / 2, 2]) with cos and sin of each position and frequency."""
+    positions = table.shape[0]
+    _check(lib.woq_rope_table(theta, rot_dim, positions, _dptr(table, "table", 4, positions * rot_dim),
+                              _stream(stream)), "woq_rope_table")
+
+
+def _qkv(cfg, qkv, q_heads, q_out, rope):
+    """Arguments of an append from qkv [rows, >= (q_heads + 2 kv_heads) head_dim] (rows may be strided)."""
+    rows = _rows(qkv, "qkv")
+    need = (q_heads + 2 * cfg.kv_heads) * cfg.head_dim
+    kind = str(qkv.dtype).rsplit(".", 1)[-1]
+    if kind not in ("bfloat16", "float32"):
+        raise ValueError(f"qkv: expected bfloat16 or float32, got {qkv.dtype}")
+    if qkv.shape[1] < need or (rows > 0 and qkv.stride(1) != 1):
+        raise ValueError(f"qkv: rows of at least {need} neighbouring elements are needed, got {tuple(qkv.shape)}")
+    stride = qkv.stride(0) if rows > 1 else -(-max(qkv.shape[1], need) // 8) * 8
+    if stride < need:
+        raise ValueError(f"qkv: rows overlap (row stride {stride}, {need} elements a row)")
+    if not getattr(qkv, "is_cuda", False):
+        raise ValueError("qkv: expected a CUDA tensor")
+    _dptr(qkv[:1, :1].reshape(-1), "qkv")  # device check; the view itself need not be contiguous
+    r = None if rope is None else rope._struct(rows)
+    return (ctypes.c_void_p(qkv.data_ptr()), int(kind == "float32"), stride, q_heads,
+            None if r is None else ctypes.byref(r), _bf16(q_out, "q_out", rows * q_heads * cfg.head_dim))
+
+
+def woq_kv8_append_rows(cfg: KV8Config, cache, layer: int, seqs, rows: int, qkv, q_heads: int, q_out, rope=None,
+                        stream=None) -> None:
+    """`rows` draft rows behind each sequence of seqs (int32 [n]; None: as many as qkv has, from 0 on):
+    qkv [n * rows, ...] rotated, queries to q_out, keys and values into the cache."""
+    total = _rows(qkv, "qkv")
+    n = total // max(rows, 1) if seqs is None else seqs.numel()
+    if n * rows != total:
+        raise ValueError(f"qkv: {total} rows, the call needs {n} x {rows}")
+    args = _qkv(cfg, qkv, q_heads, q_out, rope)
+    _check(lib.woq_kv8_append_rows(*_cache_args(cfg, cache), layer, _ints(seqs, "seqs", n), n, rows, *args,
+                                   _stream(stream)), "woq_kv8_append_rows")
+
+
+def woq_kv8_append_prompt(cfg: KV8Config, cache, layer: int, seq: int, qkv, q_heads: int, q_out, rope=None,
+                          stream=None) -> None:
+    """Fill the last tokens of a sequence (those of its last woq_kv8_extend) in one layer."""
+    args = _qkv(cfg, qkv, q_heads, q_out, rope)
+    _check(lib.woq_kv8_append_prompt(*_cache_args(cfg, cache), layer, seq, _rows(qkv, "qkv"), *args,
+                                     _stream(stream)), "woq_kv8_append_prompt")
+
+
+def woq_kv8_extend(cfg: KV8Config, cache, seq: int, tokens: int, stream=None) -> None:
+    _check(lib.woq_kv8_extend(*_cache_args(cfg, cache), seq, tokens, _stream(stream)), "woq_kv8_extend")
+
+
+def woq_kv8_accept(cfg: KV8Config, cache, seqs, keep, stream=None) -> None:
+    """Take the draft rows of each mask of keep (int32 [n], bit j: row j) into the sequences."""
+    n = keep.numel()
+    if seqs is not None and seqs.numel() != n:
+        raise ValueError(f"keep: {n} entries for {seqs.numel()} sequences")
+    _check(lib.woq_kv8_accept(*_cache_args(cfg, cache), _ints(seqs, "seqs", n), n, _ints(keep, "keep", n),
+                              _stream(stream)), "woq_kv8_accept")
+
+
+def woq_kv8_attention(cfg: KV8Config, cache, layer: int, seqs, rows: int, q, q_heads: int, out, ws, scale: float,
+                      window: int = 0, sinks: int = 0, vis=None, stream=None) -> None:
+    """Attention of `rows` rows of each sequence of seqs (int32 [n]; None: as many as q has, from 0 on):
+    q, out bf16 [n * rows, q_heads, head_dim]; vis int32 [n, rows], the draft rows each row sees (None: a chain)."""
+    per = max(1, rows * q_heads * cfg.head_dim)
+    n = q.numel() // per if seqs is None else seqs.numel()
+    if n * per != q.numel():
+        raise ValueError(f"q: {q.numel()} elements, the call needs {n} x {per}")
+    _check(lib.woq_kv8_attention(*_cache_args(cfg, cache), layer, _ints(seqs, "seqs", n), n, rows,
+                                 _bf16(q, "q", n * per), q_heads, _ints(vis, "vis", n * rows), float(scale), window,
+                                 sinks, _bf16(out, "out", n * per), _dptr(ws, "ws", 1), _nbytes(ws),
+                                 _stream(stream)), "woq_kv8_attention")
+
+
+def woq_kv8_fork(cfg: KV8Config, cache, src, dst, stream=None) -> None:
+    n = dst.numel()
+    _check(lib.woq_kv8_fork(*_cache_args(cfg, cache), _ints(src, "src", n), _ints(dst, "dst", n), n,
+                            _stream(stream)), "woq_kv8_fork")
+
+
+def woq_kv8_free(cfg: KV8Config, cache, seqs, stream=None) -> None:
+    _check(lib.woq_kv8_free(*_cache_args(cfg, cache), _ints(seqs, "seqs", seqs.numel()), seqs.numel(),
+                            _stream(stream)), "woq_kv8_free")
+
+
+def woq_kv8_copy(src_cfg: KV8Config, src, dst_cfg: KV8Config, dst, src_seqs, dst_seqs, stream=None) -> None:
+    """Copies of sequences, with pages of their own, in the same cache or another."""
+    n = dst_seqs.numel()
+    _check(lib.woq_kv8_copy(*_cache_args(src_cfg, src), *_cache_args(dst_cfg, dst), _ints(src_seqs, "src_seqs", n),
+                            _ints(dst_seqs, "dst_seqs", n), n, _stream(stream)), "woq_kv8_copy")
+
+
+def woq_kv8_compact(cfg: KV8Config, cache, limit: int, stream=None) -> None:
+    _check(lib.woq_kv8_compact(*_cache_args(cfg, cache), limit, _stream(stream)), "woq_kv8_compact")
+
+
+def woq_kv8_read(cfg: KV8Config, cache, layer: int, seq: int, first: int, k, v, stream=None) -> None:
+    """Tokens first .. of a sequence back in bf16: k, v [count, kv_heads, head_dim], or with layer = -1
+    [layers, count, kv_heads, head_dim]."""
+    layers = cfg.layers if layer < 0 else 1
+    per = layers * cfg.kv_heads * cfg.head_dim
+    count = k.numel() // max(per, 1)
+    if count * per != k.numel() or v.numel() != k.numel():
+        raise ValueError(f"k, v: {k.numel()} and {v.numel()} elements, expected the same multiple of {per}")
+    _check(lib.woq_kv8_read(*_cache_args(cfg, cache), layer, seq, first, count, _bf16(k, "k", -1), _bf16(v, "v", -1),
+                            _stream(stream)), "woq_kv8_read")
+
+
+def woq_kv8_state(cfg: KV8Config, cache, lens=None, refs=None, table=None, stream=None) -> None:
+    """Copies of the lengths [seqs], page reference counts [pages] and page tables [seqs, ceil(max_tokens / 64)]."""
+    blocks = -(-cfg.max_tokens // KV8_BLOCK)
+    _check(lib.woq_kv8_state(*_cache_args(cfg, cache), _ints(lens, "lens", cfg.seqs), _ints(refs, "refs", cfg.pages),
+                             _ints(table, "table", cfg.seqs * blocks), _stream(stream)), "woq_kv8_state")

@@ -11,6 +11,16 @@
 
 namespace woq {
 
+// A failed CUDA call: remembered for woq_last_cuda_error (per thread) and cleared from the
+// runtime's error state, so that it does not surface again in the caller's next call.
+static thread_local int t_last_cuda_error = 0;
+int cuda_result(cudaError_t e) {
+  if (e == cudaSuccess) return WOQ_OK;
+  t_last_cuda_error = (int)e;
+  (void)cudaGetLastError();
+  return WOQ_ERR_CUDA;
+}
+
 namespace {
 
 constexpr int kMaxDevices = 64;
@@ -29,16 +39,6 @@ std::atomic<long long> g_wait_ns{0};
 uint64_t wait_bound_ns() {
   const long long v = g_wait_ns.load(std::memory_order_relaxed);
   return v > 0 ? (uint64_t)v : dev::kWaitLimitNs;
-}
-
-// A failed CUDA call: remembered for woq_last_cuda_error (per thread) and cleared from the
-// runtime's error state, so that it does not surface again in the caller's next call.
-thread_local int t_last_cuda_error = 0;
-int cuda_result(cudaError_t e) {
-  if (e == cudaSuccess) return WOQ_OK;
-  t_last_cuda_error = (int)e;
-  (void)cudaGetLastError();
-  return WOQ_ERR_CUDA;
 }
 
 int current_device() {

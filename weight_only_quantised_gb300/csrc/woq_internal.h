@@ -32,6 +32,9 @@ constexpr int kStageBlocks = 4;
 constexpr int kThreads = (kConsumerWarps + 1) * 32;
 constexpr int kMaxStages = 8;
 
+// WOQ_OK or WOQ_ERR_CUDA; a failure is kept for woq_last_cuda_error (per thread) and cleared from
+// the runtime's error state
+int cuda_result(cudaError_t e);
 int sm_count();                       // SMs of the current device (cached per device)
 int max_dynamic_smem();               // opt-in shared memory per block of the current device
 int choose_consumer(int bits, int M);  // kern::Consumer the launch table picks for (bits, M)

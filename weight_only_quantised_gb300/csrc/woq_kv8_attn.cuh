@@ -1,0 +1,745 @@
+// Attention of a few rows over the 8-bit cache.
+//
+//   out = sum_j softmax_j(scale q . k_j) v_j      q: rows * group queries of one kv head
+//
+// The keys and values of a long context are read once and used by few queries, so the bound is HBM:
+// 2 D bytes per (token, head) plus 16 per block, while the operations stay below what the
+// tensor cores do in that time for up to 16 queries (mma.sync m16n8k16 f16 with fp32 sums runs at
+// about 512 multiply-adds a clock and SM here; 16 queries need 440 at the copy peak).
+//
+// Split: the (entry, kv head) items are laid end to end, each as its blocks and one unit for its
+// tail, and every CTA takes an equal share of the units (one CTA per SM; fewer CTAs while a share
+// would be below least_units), so the load is even whatever the lengths are.  Lengths are read on the
+// device.  An item that lies in several CTAs leaves fp32 partials (maximum, sum, weighted values);
+// the CTA that counts in last joins them in CTA order, so the result does not depend on the run.
+//
+// CTA: one producer warp copies whole records (16 KB at D = 128, one bulk copy each) into a ring;
+// each consumer warp takes whole blocks by itself, with its own running maximum and sums
+// in registers, so the main loop has no barrier but the ring's.  With more than 8 QT queries the
+// warps form groups, each for its own queries, that all read the block from shared memory.
+//
+// Block: scores transposed, S^T = K Q^T (tokens x queries), so that both codes operands are the
+// 16-row one and the 8-wide one is the queries: nothing is padded beyond 8 queries.  Codes
+// become f16 in registers, exactly (int8: a byte permute into 1024 + 128 + c and a subtraction; e4m3: one
+// conversion); queries are bf16 scaled by a power of two into f16, exactly but for elements below
+// 2^-24 of the row's largest.  Weights are 2^(s - m) in fp32 for the sum, rounded to f16 (11 bits) for
+// the product; m is raised only when a score passes it by 7, and weights carry a factor 2^7, so
+// f16 holds them to 2^-31 of the largest.  movmatrix turns the score fragments into the other
+// product's operand: O^T = V^T P^T, from the transposed value codes.  Each block's product is
+// scaled by its value scale in fp32.
+//
+// Tail: at most 63 tokens and the draft rows, bf16, straight from global memory; same fragments with
+// bf16 products, 16 tokens per warp, weights as two bf16 parts (16 bits).
+#pragma once
+
+#include <atomic>
+
+#include "woq_internal.h"
+#include "woq_kv8_device.cuh"
+
+namespace woq {
+namespace kv8 {
+
+constexpr float kRaise = 7.0f;    // a score may pass the running maximum by this (log2) before it is raised
+constexpr float kOffset = 7.0f;   // weights carry 2^kOffset
+constexpr int kMergePad = 4;      // floats behind each row of the merge buffer (bank spread)
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(x));
+  return d;
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// What an entry's rows see of its blocks: [0, head_blocks) and [from, full).
+struct Span {
+  int len, full, head_blocks, from, units;  // units: blocks seen and the tail
+};
+
+__device__ __forceinline__ Span span_of(int len, int window, int sinks) {
+  Span s;
+  s.len = len;
+  s.full = len / kKv8Block;
+  s.head_blocks = 0;
+  s.from = 0;
+  if (window > 0 && len > window) {  // no row sees tokens in [sinks, len - window)
+    s.from = (len - window) / kKv8Block;
+    s.head_blocks = (sinks + kKv8Block - 1) / kKv8Block;
+    if (s.head_blocks >= s.from) s.head_blocks = s.from;
+  }
+  s.units = s.head_blocks + (s.full - s.from) + 1;
+  return s;
+}
+
+// Running state of a warp's queries: columns 2t, 2t + 1 of each tile of 8.
+template <int D, int QT>
+struct State {
+  float m[QT][2], l[QT][2];
+  float o[D / 16][QT][4];  // rows g, g + 8 of each 16 elements
+};
+
+template <int D, int QT>
+__device__ __forceinline__ void clear(State<D, QT>& st) {
+#pragma unroll
+  for (int q = 0; q < QT; ++q) {
+    st.m[q][0] = st.m[q][1] = -INFINITY;
+    st.l[q][0] = st.l[q][1] = 0.0f;
+  }
+#pragma unroll
+  for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+    for (int q = 0; q < QT; ++q)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) st.o[j][q][i] = 0.0f;
+}
+
+// Raise the maxima to cover mx (per column, the same in the lanes of a column) where it passes them
+// by more than kRaise, and scale what was summed.
+template <int D, int QT>
+__device__ __forceinline__ void raise(State<D, QT>& st, const float (&mx)[QT][2]) {
+  bool up = false;
+#pragma unroll
+  for (int q = 0; q < QT; ++q) up |= mx[q][0] > st.m[q][0] + kRaise || mx[q][1] > st.m[q][1] + kRaise;
+  if (!__any_sync(~0u, up)) return;
+#pragma unroll
+  for (int q = 0; q < QT; ++q) {
+    float a[2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const float n = fmaxf(st.m[q][c], mx[q][c]);
+      a[c] = n == -INFINITY ? 1.0f : exp2_approx(st.m[q][c] - n);
+      st.m[q][c] = n;
+      st.l[q][c] *= a[c];
+    }
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j) {
+      st.o[j][q][0] *= a[0];
+      st.o[j][q][1] *= a[1];
+      st.o[j][q][2] *= a[0];
+      st.o[j][q][3] *= a[1];
+    }
+  }
+}
+
+__device__ __forceinline__ float column_max(float x) {  // over the lanes that share t
+  x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
+  x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
+  return fmaxf(x, __shfl_xor_sync(~0u, x, 16));
+}
+
+// What the lane knows about its columns' rows for the masks: first place seen by the window, draft mask.
+template <int QT>
+struct Columns {
+  int low[QT][2];       // places >= low are in the window
+  uint32_t vis[QT][2];  // draft rows seen
+};
+
+// One block of codes at `rec` (shared memory), first token `token0`.
+template <int FMT, int D, int QT>
+__device__ __forceinline__ void block_step(State<D, QT>& st, const uint8_t* rec, const uint32_t (&qf)[QT][D / 16][2],
+                                           const float (&coef)[QT][2], const Columns<QT>& col, int token0, bool masked,
+                                           int sinks, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+  const float ks = *reinterpret_cast<const float*>(rec + 128 * D);
+  const float vs = *reinterpret_cast<const float*>(rec + 128 * D + 4);
+  const uint8_t* kc = rec + t * 128 + g * 16;
+  float s[4][QT][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int q = 0; q < QT; ++q)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) s[i][q][c] = 0.0f;
+#pragma unroll
+  for (int c = 0; c < D / 64; ++c) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint4 x = *reinterpret_cast<const uint4*>(kc + (2 * i * (D / 16) + 4 * c) * 128);
+      const uint4 y = *reinterpret_cast<const uint4*>(kc + ((2 * i + 1) * (D / 16) + 4 * c) * 128);
+      const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t a[4];
+        f16x4_of_codes<FMT>(xs[k], a[0], a[2]);
+        f16x4_of_codes<FMT>(ys[k], a[1], a[3]);
+#pragma unroll
+        for (int q = 0; q < QT; ++q) mma_f16(s[i][q], a, qf[q][4 * c + k][0], qf[q][4 * c + k][1]);
+      }
+    }
+  }
+  float mx[QT][2];
+#pragma unroll
+  for (int q = 0; q < QT; ++q) {
+    const float f0 = coef[q][0] * ks, f1 = coef[q][1] * ks;
+    mx[q][0] = mx[q][1] = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      s[i][q][0] *= f0;
+      s[i][q][1] *= f1;
+      s[i][q][2] *= f0;
+      s[i][q][3] *= f1;
+      if (masked) {
+        const int tok = token0 + 16 * (g >> 1) + 4 * i + (g & 1);
+        if (tok >= sinks) {
+          if (tok < col.low[q][0]) s[i][q][0] = -INFINITY;
+          if (tok < col.low[q][1]) s[i][q][1] = -INFINITY;
+        }
+        if (tok + 2 >= sinks) {
+          if (tok + 2 < col.low[q][0]) s[i][q][2] = -INFINITY;
+          if (tok + 2 < col.low[q][1]) s[i][q][3] = -INFINITY;
+        }
+      }
+      mx[q][0] = fmaxf(mx[q][0], fmaxf(s[i][q][0], s[i][q][2]));
+      mx[q][1] = fmaxf(mx[q][1], fmaxf(s[i][q][1], s[i][q][3]));
+    }
+    mx[q][0] = column_max(mx[q][0]);
+    mx[q][1] = column_max(mx[q][1]);
+  }
+  raise(st, mx);
+  uint32_t pb[4][QT][2];
+#pragma unroll
+  for (int q = 0; q < QT; ++q) {
+    const float r0 = (st.m[q][0] == -INFINITY ? 0.0f : st.m[q][0]) - kOffset;
+    const float r1 = (st.m[q][1] == -INFINITY ? 0.0f : st.m[q][1]) - kOffset;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float p0 = exp2_approx(s[i][q][0] - r0), p1 = exp2_approx(s[i][q][1] - r1);
+      const float p2 = exp2_approx(s[i][q][2] - r0), p3 = exp2_approx(s[i][q][3] - r1);
+      st.l[q][0] += p0 + p2;
+      st.l[q][1] += p1 + p3;
+      pb[i][q][0] = transpose8x8(pack_f16(p0, p1));
+      pb[i][q][1] = transpose8x8(pack_f16(p2, p3));
+    }
+  }
+  const uint8_t* vc = rec + 64 * D + t * 128 + g * 16;
+#pragma unroll
+  for (int j = 0; j < D / 16; ++j) {
+    const uint4 x = *reinterpret_cast<const uint4*>(vc + 2 * j * 512);
+    const uint4 y = *reinterpret_cast<const uint4*>(vc + (2 * j + 1) * 512);
+    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+    float acc[QT][4];
+#pragma unroll
+    for (int q = 0; q < QT; ++q)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[q][c] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t a[4];
+      f16x4_of_codes<FMT>(xs[i], a[0], a[2]);
+      f16x4_of_codes<FMT>(ys[i], a[1], a[3]);
+#pragma unroll
+      for (int q = 0; q < QT; ++q) mma_f16(acc[q], a, pb[i][q][0], pb[i][q][1]);
+    }
+#pragma unroll
+    for (int q = 0; q < QT; ++q)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) st.o[j][q][c] = fmaf(vs, acc[q][c], st.o[j][q][c]);
+  }
+}
+
+// Tail tile i: i < 4: tokens 16 t' + 4 i + {0 .. 3} of the tail (t' = 0 .. 3), in the order of the
+// key rows of a block; i = 4: tail rows 64 .. 71.  there: rows of the tail that anything may be seen of.
+template <int D, int QT>
+__device__ __forceinline__ void tail_step(State<D, QT>& st, const uint16_t* tail, int i, int in_tail, int len, int there,
+                                          const uint16_t* const (&qrow)[QT], float scale_log2, const Columns<QT>& col,
+                                          int sinks, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+  const int r0 = i < 4 ? 16 * (g >> 1) + 4 * i + (g & 1) : 64 + g;
+  const int r1 = i < 4 ? r0 + 2 : kKv8Tail;
+  float s[QT][4];
+#pragma unroll
+  for (int q = 0; q < QT; ++q)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) s[q][c] = 0.0f;
+#pragma unroll
+  for (int c = 0; c < D / 64; ++c) {
+    uint32_t x[8], y[8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint4 a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
+      if (r0 < there) a = *reinterpret_cast<const uint4*>(tail + r0 * D + 16 * (4 * c + t) + 8 * h);
+      if (r1 < there) b = *reinterpret_cast<const uint4*>(tail + r1 * D + 16 * (4 * c + t) + 8 * h);
+      x[4 * h] = a.x, x[4 * h + 1] = a.y, x[4 * h + 2] = a.z, x[4 * h + 3] = a.w;
+      y[4 * h] = b.x, y[4 * h + 1] = b.y, y[4 * h + 2] = b.z, y[4 * h + 3] = b.w;
+    }
+#pragma unroll
+    for (int q = 0; q < QT; ++q) {
+      uint32_t w[8];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint4 a = {0, 0, 0, 0};
+        if (qrow[q]) a = *reinterpret_cast<const uint4*>(qrow[q] + 16 * (4 * c + t) + 8 * h);
+        w[4 * h] = a.x, w[4 * h + 1] = a.y, w[4 * h + 2] = a.z, w[4 * h + 3] = a.w;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t a[4] = {x[2 * k], y[2 * k], x[2 * k + 1], y[2 * k + 1]};
+        mma_bf16(s[q], a, w[2 * k], w[2 * k + 1]);
+      }
+    }
+  }
+  // whether the column's row sees tail row r
+  auto sees = [&](int r, uint32_t vis, int low) {
+    if (r >= there) return false;
+    const int draft = r - in_tail;
+    int place = len + draft;
+    if (draft >= 0) {
+      if (!((vis >> draft) & 1u)) return false;
+      place = len + __popc(vis & ((1u << draft) - 1u));
+    }
+    return place < sinks || place >= low;
+  };
+  float mx[QT][2];
+#pragma unroll
+  for (int q = 0; q < QT; ++q) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      s[q][c] = sees(r0, col.vis[q][c], col.low[q][c]) ? s[q][c] * scale_log2 : -INFINITY;
+      s[q][2 + c] = sees(r1, col.vis[q][c], col.low[q][c]) ? s[q][2 + c] * scale_log2 : -INFINITY;
+      mx[q][c] = column_max(fmaxf(s[q][c], s[q][2 + c]));
+    }
+  }
+  raise(st, mx);
+  uint32_t hi[QT][2], lo[QT][2];
+#pragma unroll
+  for (int q = 0; q < QT; ++q) {
+    float p[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const float r = (st.m[q][c & 1] == -INFINITY ? 0.0f : st.m[q][c & 1]) - kOffset;
+      p[c] = exp2_approx(s[q][c] - r);
+      st.l[q][c & 1] += p[c];
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t u = pack_bf16(p[2 * h], p[2 * h + 1]);
+      const float f0 = __uint_as_float(u << 16), f1 = __uint_as_float(u & 0xFFFF0000u);
+      hi[q][h] = transpose8x8(u);
+      lo[q][h] = transpose8x8(pack_bf16(p[2 * h] - f0, p[2 * h + 1] - f1));
+    }
+  }
+  const uint16_t* tv = tail + kKv8Tail * D;
+#pragma unroll
+  for (int j = 0; j < D / 16; ++j) {
+    const uint16_t* v0 = tv + (16 * j + g) * kKv8Tail;
+    const uint16_t* v1 = v0 + 8 * kKv8Tail;
+    uint32_t a[4];
+    if (i < 4) {
+      const uint2 x = *reinterpret_cast<const uint2*>(v0 + 16 * t + 4 * i);
+      const uint2 y = *reinterpret_cast<const uint2*>(v1 + 16 * t + 4 * i);
+      a[0] = x.x, a[1] = y.x, a[2] = x.y, a[3] = y.y;
+    } else {
+      a[0] = *reinterpret_cast<const uint32_t*>(v0 + 64 + 2 * t);
+      a[1] = *reinterpret_cast<const uint32_t*>(v1 + 64 + 2 * t);
+      a[2] = a[3] = 0u;
+    }
+#pragma unroll
+    for (int q = 0; q < QT; ++q) {
+      mma_bf16(st.o[j][q], a, hi[q][0], hi[q][1]);
+      mma_bf16(st.o[j][q], a, lo[q][0], lo[q][1]);
+    }
+  }
+}
+
+// Queries of the lane's column n = g as operands, scaled by 2^-e to below 2; returns 2^e.
+template <int D, int QT>
+__device__ __forceinline__ void load_queries(uint32_t (&qf)[QT][D / 16][2], float (&unit)[QT],
+                                             const uint16_t* const (&qrow)[QT], int lane) {
+  const int t = lane & 3;
+#pragma unroll
+  for (int q = 0; q < QT; ++q) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint4 a = {0, 0, 0, 0};
+        if (qrow[q]) a = *reinterpret_cast<const uint4*>(qrow[q] + 16 * (4 * c + t) + 8 * h);
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          qf[q][4 * c + 2 * h + (k >> 1)][k & 1] = w[k];
+          top = dev::bf16x2_absmax(top, w[k]);
+        }
+      }
+    }
+    float m = dev::bf16x2_absmax_to_float(top);
+    m = fmaxf(m, __shfl_xor_sync(~0u, m, 1));
+    m = fmaxf(m, __shfl_xor_sync(~0u, m, 2));
+    int e = (int)(__float_as_uint(m) >> 23) - 127;  // m = 0 or subnormal: -127
+    e = e < -126 ? -126 : e > 126 ? 126 : e;
+    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+    unit[q] = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t w = qf[q][k][h];
+        qf[q][k][h] = pack_f16(__uint_as_float(w << 16) * down, __uint_as_float(w & 0xFFFF0000u) * down);
+      }
+  }
+}
+
+constexpr int kMaxStages = 32;
+// Shared memory: barriers, flags, units and lengths of the entries; the merge buffer; the ring.
+struct Misc {
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  int fail, last;
+  int entries[];  // [n + 1] units of one head of the entries before, [n] lengths (-1: out of range)
+};
+__host__ __device__ inline int misc_bytes(int n) { return (int)((sizeof(Misc) + (size_t)(2 * n + 1) * 4 + 127) / 128 * 128); }
+__host__ __device__ inline int merge_bytes(int warps, int qt, int dim) {
+  return (warps * 8 * qt * (dim + kMergePad + 2) * 4 + 127) / 128 * 128;
+}
+
+// Share c of `units` over `ctas`: [begin, end).
+__device__ __forceinline__ long long share_begin(long long units, int c, int ctas) { return units * c / ctas; }
+// The CTA whose share holds unit u.
+__device__ __forceinline__ int share_of(long long units, int ctas, long long u) {
+  int c = (int)((u * ctas) / units);
+  while (share_begin(units, c + 1, ctas) <= u) ++c;
+  while (share_begin(units, c, ctas) > u) --c;
+  return c;
+}
+
+template <int FMT, int D, int QT>
+__global__ void __launch_bounds__(352, 1) attn_kernel(const __grid_constant__ Kv8Attn p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  Misc& misc = *reinterpret_cast<Misc*>(smem);
+  int* prefix = misc.entries;
+  int* lens = prefix + p.n + 1;
+  const Kv8View& v = p.v;
+  const int W = p.warps, G = p.query_groups, WG = W / G, S = p.stages;
+  const int R = p.rows * p.group;
+  constexpr int kRecord = 128 * D + 16;
+  constexpr int kRow = D + kMergePad;
+  float* merge = reinterpret_cast<float*>(smem + misc_bytes(p.n));  // [W][8 QT][D + pad]
+  float* warp_ml = merge + (size_t)W * 8 * QT * kRow;               // [W][8 QT][2]
+  uint8_t* ring = smem + misc_bytes(p.n) + merge_bytes(W, QT, D);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  if (tid == 0) {
+    for (int i = 0; i < S; ++i) {
+      dev::mbar_init(&misc.full[i], 1);
+      dev::mbar_init(&misc.empty[i], (uint32_t)G);
+    }
+    misc.fail = 0;
+    dev::fence_mbar_init();
+  }
+  dev::pdl_wait_prior_grids();
+  dev::pdl_launch_dependents();
+  if (!header_ok(v)) return;
+
+  // lengths and units of the entries
+  if (warp == 0) {
+    int run = 0;
+    for (int e0 = 0; e0 < p.n; e0 += 32) {
+      const int e = e0 + lane;
+      int units = 0;
+      if (e < p.n) {
+        const int seq = p.seqs ? p.seqs[e] : e;
+        const bool there = seq >= 0 && seq < v.seqs;
+        if (!there && blockIdx.x == 0) flag(v, WOQ_DEVERR_STATE);
+        lens[e] = there ? v.lens_p()[seq] : -1;
+        units = there ? span_of(lens[e], p.window, p.sinks).units : 1;
+      }
+      int y = units;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int z = __shfl_up_sync(~0u, y, d);
+        if (lane >= d) y += z;
+      }
+      if (e < p.n) prefix[e] = run + y - units;
+      run += __shfl_sync(~0u, y, 31);
+    }
+    if (lane == 0) prefix[p.n] = run;
+  }
+  __syncthreads();
+  const long long units = (long long)prefix[p.n] * v.heads;
+  long long want = (units + p.least_units - 1) / p.least_units;
+  const int ctas = want < (long long)gridDim.x ? (int)want : (int)gridDim.x;
+  if ((int)blockIdx.x >= ctas) return;
+  const long long begin = share_begin(units, blockIdx.x, ctas), end = share_begin(units, blockIdx.x + 1, ctas);
+
+  // the item that holds unit u: entry, head, first unit
+  auto locate = [&](long long u, int* entry, int* head, long long* item_begin) {
+    int lo = 0, hi = p.n - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if ((long long)prefix[mid] * v.heads <= u) lo = mid; else hi = mid - 1;
+    }
+    const int per = prefix[lo + 1] - prefix[lo];
+    const long long first = (long long)prefix[lo] * v.heads;
+    *entry = lo;
+    *head = (int)((u - first) / per);
+    *item_begin = first + (long long)*head * per;
+  };
+
+  if (warp == W) {  // producer
+    int issued = 0;
+    for (long long u = begin; u < end;) {
+      int e, head;
+      long long ib;
+      locate(u, &e, &head, &ib);
+      const int per = prefix[e + 1] - prefix[e];
+      const long long stop = ib + per < end ? ib + per : end;
+      const int b0 = (int)(u - ib), b1 = (int)(stop - ib) < per - 1 ? (int)(stop - ib) : per - 1;  // the tail is per - 1
+      if (b0 < b1) {
+        const Span sp = span_of(lens[e], p.window, p.sinks);
+        const int32_t* table = v.table_row(p.seqs ? p.seqs[e] : e);
+        for (int c0 = b0; c0 < b1; c0 += 32) {
+          const int k = c0 + lane;
+          int page = 0;
+          if (k < b1) page = table[k < sp.head_blocks ? k : sp.from + (k - sp.head_blocks)];
+          const int some = b1 - c0 < 32 ? b1 - c0 : 32;
+          for (int i = 0; i < some; ++i) {
+            const int pg = __shfl_sync(~0u, page, i);
+            const int stage = issued % S;
+            bool ok = true;
+            if (issued >= S) ok = dev::mbar_wait_bounded(&misc.empty[stage], (uint32_t)((issued / S - 1) & 1));
+            if (!__all_sync(~0u, ok)) {
+              // consumers stopped: nothing more is issued; copies in flight are waited for below
+              misc.fail = 1;
+              u = end;
+              break;
+            }
+            if (lane == 0) {
+              dev::mbar_arrive_expect_tx(&misc.full[stage], kRecord);
+              dev::bulk_copy_g2s(ring + (size_t)stage * kRecord, v.record(pg, p.layer, head), kRecord, &misc.full[stage]);
+            }
+            ++issued;
+          }
+          if (u >= end) break;
+        }
+      }
+      if (u >= end) break;
+      u = stop;
+    }
+    // copies in flight end before this CTA's shared memory is given up
+    for (int i = issued > S ? issued - S : 0; i < issued; ++i)
+      dev::mbar_wait_bounded(&misc.full[i % S], (uint32_t)((i / S) & 1));
+    return;
+  }
+
+  const int group = warp % G, slot = warp / G;
+  const int g = lane >> 2, t = lane & 3;
+  const int consumers = W * 32;
+  int taken = 0;  // blocks of this CTA that earlier items had
+  for (long long u = begin; u < end;) {
+    int e, head;
+    long long ib;
+    locate(u, &e, &head, &ib);
+    const int per = prefix[e + 1] - prefix[e];
+    const long long stop = ib + per < end ? ib + per : end;
+    const int len = lens[e];
+    const bool there = len >= 0;
+    const Span sp = span_of(there ? len : 0, p.window, p.sinks);
+    const bool has_tail = stop == ib + per && there;
+    const int b0 = (int)(u - ib), b1 = (int)(stop - ib) < per - 1 ? (int)(stop - ib) : per - 1;
+    const int seq = p.seqs ? p.seqs[e] : e;
+
+    // queries and what their rows see
+    const uint16_t* qrow[QT];
+    Columns<QT> col;
+    int low_max = 0;
+    uint32_t any_vis = 0;
+#pragma unroll
+    for (int q = 0; q < QT; ++q) {
+      const int base = (group * QT + q) * 8;
+      const int n = base + g;
+      qrow[q] = n < R ? p.q + (((size_t)e * p.rows + n / p.group) * p.q_heads + (size_t)head * p.group + n % p.group) * D
+                      : nullptr;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int k = base + 2 * t + c, m = k < R ? k / p.group : 0;
+        const uint32_t vis = (p.vis ? p.vis[(size_t)e * p.rows + m] : (2u << m) - 1u) & 0xFFu;
+        col.vis[q][c] = vis;
+        any_vis |= vis;
+        col.low[q][c] = p.window > 0 ? len + __popc(vis) - p.window : 0;
+        low_max = max(low_max, col.low[q][c]);
+      }
+    }
+    low_max = __reduce_max_sync(~0u, low_max);
+    State<D, QT> st;
+    clear(st);
+    uint32_t qf[QT][D / 16][2];
+    float unit[QT], coef[QT][2];
+    load_queries<D, QT>(qf, unit, qrow, lane);
+#pragma unroll
+    for (int q = 0; q < QT; ++q) {
+      coef[q][0] = __shfl_sync(~0u, unit[q], 8 * t) * p.scale_log2;  // lane 4 g' holds column g'
+      coef[q][1] = __shfl_sync(~0u, unit[q], 8 * t + 4) * p.scale_log2;
+    }
+    if (has_tail) {
+      const uint16_t* tail = v.tail(p.layer, seq, head);
+      const int in_tail = len - sp.full * kKv8Block;
+      const int there = in_tail + 32 - __clz((int)__reduce_or_sync(~0u, any_vis));  // at most 63 + 8
+      for (int i = slot; i < 5; i += WG)
+        if (there > (i < 4 ? 4 * i : 64))
+          tail_step<D, QT>(st, tail, i, in_tail, len, there, qrow, p.scale_log2, col, p.sinks, lane);
+    }
+    bool ok = true;
+    int k = b0 + ((slot - taken) % WG + WG) % WG;  // ring positions taken + (k - b0) = slot mod WG
+    for (; k < b1 && ok; k += WG) {
+      const int at = taken + (k - b0), stage = at % S;
+      ok = dev::mbar_wait_bounded(&misc.full[stage], (uint32_t)((at / S) & 1));
+      if (!__all_sync(~0u, ok)) {
+        ok = false;
+        break;
+      }
+      const int blk = k < sp.head_blocks ? k : sp.from + (k - sp.head_blocks);
+      const int token0 = blk * kKv8Block;
+      block_step<FMT, D, QT>(st, ring + (size_t)stage * kRecord, qf, coef, col, token0,
+                             token0 < low_max && token0 + kKv8Block > p.sinks, p.sinks, lane);
+      __syncwarp();
+      if (lane == 0) dev::mbar_arrive(&misc.empty[stage]);
+    }
+    if (!ok && lane == 0) misc.fail = 1;
+    taken += b1 > b0 ? b1 - b0 : 0;
+
+    // join the warps: sums over the lanes of a column, then over the warps of the group
+#pragma unroll
+    for (int q = 0; q < QT; ++q)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float l = st.l[q][c];
+        l += __shfl_xor_sync(~0u, l, 4);
+        l += __shfl_xor_sync(~0u, l, 8);
+        l += __shfl_xor_sync(~0u, l, 16);
+        if (g == 0) {
+          const int row = warp * 8 * QT + 8 * q + 2 * t + c;
+          warp_ml[2 * row] = st.m[q][c];
+          warp_ml[2 * row + 1] = l;
+        }
+      }
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+      for (int q = 0; q < QT; ++q)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          merge[(size_t)(warp * 8 * QT + 8 * q + 2 * t + (c & 1)) * kRow + 16 * j + g + 8 * (c >> 1)] = st.o[j][q][c];
+    dev::named_barrier_sync(1, consumers);
+    if (misc.fail) {  // a wait ran out: nothing of this item is written
+      if (tid == 0) flag(v, WOQ_DEVERR_TIMEOUT);
+      return;
+    }
+    const bool whole = u == ib && stop == ib + per;
+    const int mine = ib <= begin ? 0 : 1;  // partial slots: the item that holds the share's first unit, and the other
+    float* part = p.parts + ((size_t)blockIdx.x * 2 + mine) * R * (D + 2);
+    for (int x = tid; x < R * (D / 4); x += consumers) {
+      const int n = x / (D / 4), d = (x % (D / 4)) * 4, gr = n / (8 * QT), in = n % (8 * QT);
+      float m = -INFINITY;
+      for (int w = 0; w < WG; ++w) m = fmaxf(m, warp_ml[2 * ((w * G + gr) * 8 * QT + in)]);
+      float4 o = {0, 0, 0, 0};
+      float l = 0.0f;
+      for (int w = 0; w < WG; ++w) {
+        const int row = (w * G + gr) * 8 * QT + in;
+        const float mw = warp_ml[2 * row];
+        const float f = mw == -INFINITY ? (warp_ml[2 * row + 1] == 0.0f ? 0.0f : 1.0f) : exp2_approx(mw - m);
+        const float4 y = *reinterpret_cast<const float4*>(merge + (size_t)row * kRow + d);
+        o.x += f * y.x;
+        o.y += f * y.y;
+        o.z += f * y.z;
+        o.w += f * y.w;
+        l += f * warp_ml[2 * row + 1];
+      }
+      if (whole) {
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        uint16_t* out = p.out + (((size_t)e * p.rows + n / p.group) * p.q_heads + (size_t)head * p.group + n % p.group) * D + d;
+        *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+      } else {
+        float* to = part + (size_t)n * (D + 2);
+        *reinterpret_cast<float2*>(to + 2 + d) = make_float2(o.x, o.y);
+        *reinterpret_cast<float2*>(to + 4 + d) = make_float2(o.z, o.w);
+        if (d == 0) *reinterpret_cast<float2*>(to) = make_float2(m, l);
+      }
+    }
+    if (!whole) {
+      const int c0 = share_of(units, ctas, ib), c1 = share_of(units, ctas, ib + per - 1);
+      __threadfence();
+      dev::named_barrier_sync(1, consumers);
+      uint32_t* ticket = p.tickets + (size_t)e * v.heads + head;
+      if (tid == 0) misc.last = dev::atomic_add_acq_rel_gpu(ticket, 1u) == (uint32_t)(c1 - c0);
+      dev::named_barrier_sync(1, consumers);
+      if (misc.last) {
+        __threadfence();
+        for (int x = tid; x < R * (D / 2); x += consumers) {
+          const int n = x / (D / 2), d = (x % (D / 2)) * 2;
+          float m = -INFINITY;
+          for (int c = c0; c <= c1; ++c) {
+            const int which = ib <= share_begin(units, c, ctas) ? 0 : 1;
+            m = fmaxf(m, __ldcg(p.parts + (((size_t)c * 2 + which) * R + n) * (D + 2)));
+          }
+          float2 o = {0, 0};
+          float l = 0.0f;
+          for (int c = c0; c <= c1; ++c) {
+            const int which = ib <= share_begin(units, c, ctas) ? 0 : 1;
+            const float* from = p.parts + (((size_t)c * 2 + which) * R + n) * (D + 2);
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(from));
+            const float2 y = __ldcg(reinterpret_cast<const float2*>(from + 2 + d));
+            const float f = ml.x == -INFINITY ? (ml.y == 0.0f ? 0.0f : 1.0f) : exp2_approx(ml.x - m);
+            o.x += f * y.x;
+            o.y += f * y.y;
+            l += f * ml.y;
+          }
+          const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+          uint16_t* out = p.out + (((size_t)e * p.rows + n / p.group) * p.q_heads + (size_t)head * p.group + n % p.group) * D + d;
+          *reinterpret_cast<uint32_t*>(out) = pack_bf16(o.x * inv, o.y * inv);
+        }
+        if (tid == 0) *ticket = 0u;
+      }
+    }
+    dev::named_barrier_sync(1, consumers);  // the merge buffer is free again
+    u = stop;
+  }
+}
+
+template <int FMT, int D, int QT>
+cudaError_t launch_attn(const Kv8Attn& p, int ctas, int smem, cudaStream_t stream) {
+  auto kernel = attn_kernel<FMT, D, QT>;
+  static std::atomic<unsigned long long> configured{0};
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (device & 63);
+  if (!(configured.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, max_dynamic_smem());
+    if (e != cudaSuccess) return e;
+    configured.fetch_or(bit);
+  }
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3((unsigned)ctas);
+  lc.blockDim = dim3((unsigned)(p.warps + 1) * 32);
+  lc.dynamicSmemBytes = (size_t)smem;
+  lc.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  return cudaLaunchKernelEx(&lc, kernel, p);
+}
+
+}  // namespace kv8
+}  // namespace woq
