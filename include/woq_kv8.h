@@ -141,7 +141,8 @@ WOQ_API int woq_kv8_append_prompt(const woq_kv8_config* cfg, void* cache, size_t
 /* ---------------------------------------------------------------------------
  * Attention of `rows` rows of each of n sequences (the draft rows' queries).
  *   q, out: device bf16 [n][rows][q_heads][head_dim]; q_heads a multiple of kv_heads, query head
- *   i reads kv head i / (q_heads / kv_heads); rows * q_heads / kv_heads <= 128 (head_dim 256: 64).
+ *   i reads kv head i / (q_heads / kv_heads); rows * q_heads / kv_heads <= 128 (head_dim 256: 56);
+ *   n * kv_heads * (ceil(max_tokens / 64) + 2) < 2^31 - 2^16.
  *   vis: device uint32 [n][rows], bit j: draft row j is seen (bits 0 .. 7); NULL: row m sees
  *   draft rows 0 .. m.  Only rows that were appended may be seen.
  *   A row sees, in this order, the sequence's tokens and the draft rows of its vis; with
@@ -161,6 +162,21 @@ WOQ_API int woq_kv8_attention(const woq_kv8_config* cfg, void* cache, size_t cac
                               const int32_t* seqs, int n, int rows, const void* q, int q_heads, const uint32_t* vis,
                               float scale, int window, int sinks, void* out, void* ws, size_t ws_bytes,
                               woq_stream_t stream);
+
+/* The attention's launch shape for n sequences of `rows` rows, worked out on the host without launching
+ * anything; sms, smem_max: the device to plan for (0 for either = the current device's value).
+ * WOQ_ERR_NULL, WOQ_ERR_SHAPE (arguments that woq_kv8_attention refuses, or nothing fits smem_max),
+ * WOQ_ERR_CUDA. */
+typedef struct {
+  int ctas;         /* grid: one CTA per SM; those beyond the work end at once */
+  int warps;        /* consumer warps of a CTA (one more copies) */
+  int query_groups; /* warps that read the same block, each for its own queries */
+  int stages;       /* ring stages of one block each: a multiple of warps / query_groups */
+  int least_units;  /* blocks (and tails) a CTA takes at least */
+  int smem_bytes;   /* dynamic shared memory of a CTA */
+} woq_kv8_plan;
+WOQ_API int woq_kv8_plan_attention(const woq_kv8_config* cfg, int n, int rows, int q_heads, int sms, int smem_max,
+                                   woq_kv8_plan* out);
 
 /* ---------------------------------------------------------------------------
  * Pages

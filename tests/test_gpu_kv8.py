@@ -255,7 +255,7 @@ def test_rows_and_groups(fmt, rows, group):
     c.attend([0], rows, group, g)
 
 
-@pytest.mark.parametrize("dim,rows,group", [(64, 8, 16), (64, 2, 7), (256, 8, 8), (256, 3, 4), (256, 5, 5)])
+@pytest.mark.parametrize("dim,rows,group", [(64, 8, 16), (64, 2, 7), (256, 8, 7), (256, 3, 4), (256, 5, 5)])
 def test_rows_and_groups_of_other_heads(dim, rows, group):
     c = Cache(fmt=rows % 2, dim=dim, heads=1)
     g = gen(rows * 31 + group)

@@ -104,16 +104,25 @@ def _dptr(t, name: str = "tensor", itemsize: int = 0, numel: int = -1):
         return None
     if not getattr(t, "is_cuda", False):
         raise ValueError(f"{name}: expected a CUDA tensor")
-    import torch
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name}: tensor is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if t.get_device() != _current_device():
+        raise ValueError(f"{name}: tensor is on {t.device}, the current device is cuda:{_current_device()}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous tensor")
     if itemsize and t.element_size() != itemsize:
         raise ValueError(f"{name}: expected {itemsize}-byte elements, got {t.dtype}")
     if numel >= 0 and t.numel() < numel:
         raise ValueError(f"{name}: {t.numel()} elements, the call needs {numel}")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
+
+
+def _current_device() -> int:
+    # bound on first use (importing this package does not import torch): the runtime's own query,
+    # without the lazy-initialisation check that torch.cuda.current_device makes on every call (a CUDA
+    # tensor is at hand wherever this is asked)
+    global _current_device
+    import torch
+    _current_device = torch._C._cuda_getDevice
+    return _current_device()
 
 
 def _rows(t, name: str) -> int:
@@ -124,14 +133,22 @@ def _rows(t, name: str) -> int:
 
 
 def _nbytes(t) -> int:
-    return 0 if t is None else t.numel() * t.element_size()
+    return 0 if t is None else t.nbytes
 
 
 def _stream(stream):
     if stream is None:
-        import torch
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+        return _current_raw_stream(_current_device())
+    return stream.cuda_stream
+
+
+def _current_raw_stream(device: int) -> int:
+    # the current stream's handle without a Stream object, bound like _current_device
+    global _current_raw_stream
+    import torch
+    torch.cuda.current_stream()  # initialises CUDA (or says why it cannot)
+    _current_raw_stream = torch._C._cuda_getCurrentRawStream
+    return _current_raw_stream(device)
 
 
 def _hptr(a: np.ndarray):
@@ -489,12 +506,17 @@ class Rope:
             raise ValueError("rope table: expected [positions, rot_dim / 2, 2]")
         if pos.dim() != 2 or pos.shape[1] != rows:
             raise ValueError(f"rope positions: expected [axes, {rows}], got {tuple(pos.shape)}")
-        if t.is_floating_point() is False or pos.is_floating_point():
-            raise ValueError("rope: the table is fp32, the positions int32")
         if self.axis_of is not None and self.axis_of.size != t.shape[1]:
             raise ValueError(f"rope axis_of: expected {t.shape[1]} entries, got {self.axis_of.size}")
-        return _Rope(_dptr(t, "rope table", 4), t.shape[0], 2 * t.shape[1], int(self.interleaved), pos.shape[0],
-                     _dptr(pos, "rope positions", 4), None if self.axis_of is None else _hptr(self.axis_of))
+        return _Rope(_typed(t, "rope table", "float32", 4, -1), t.shape[0], 2 * t.shape[1], int(self.interleaved),
+                     pos.shape[0], _ints(pos, "rope positions", -1),
+                     None if self.axis_of is None else self.axis_of.ctypes.data)
+
+
+class KV8Plan(ctypes.Structure):
+    """woq_kv8_plan of include/woq_kv8.h."""
+    _fields_ = [("ctas", ctypes.c_int), ("warps", ctypes.c_int), ("query_groups", ctypes.c_int), ("stages", ctypes.c_int),
+                ("least_units", ctypes.c_int), ("smem_bytes", ctypes.c_int)]
 
 
 _CP = ctypes.POINTER(KV8Config)
@@ -510,6 +532,7 @@ for _name, (_args, _res) in {
     "woq_kv8_extend": ([_CP, _P, _Z, _I, _I, _P], _I),
     "woq_kv8_attention_workspace": ([_CP, _I, _I, _I], _Z),
     "woq_kv8_attention": ([_CP, _P, _Z, _I, _P, _I, _I, _P, _I, _P, ctypes.c_float, _I, _I, _P, _P, _Z, _P], _I),
+    "woq_kv8_plan_attention": ([_CP, _I, _I, _I, _I, _I, ctypes.POINTER(KV8Plan)], _I),
     "woq_kv8_fork": ([_CP, _P, _Z, _P, _P, _I, _P], _I),
     "woq_kv8_free": ([_CP, _P, _Z, _P, _I, _P], _I),
     "woq_kv8_copy": ([_CP, _P, _Z, _CP, _P, _Z, _P, _P, _I, _P], _I),
@@ -534,20 +557,39 @@ def woq_kv8_attention_workspace(cfg: KV8Config, n: int, rows: int, q_heads: int)
     return lib.woq_kv8_attention_workspace(ctypes.byref(cfg), n, rows, q_heads)
 
 
+def woq_kv8_plan_attention(cfg: KV8Config, n: int, rows: int, q_heads: int, sms: int = 0, smem_max: int = 0) -> dict:
+    """The attention's launch shape on the current device, or on one with sms SMs and smem_max bytes of
+    opt-in shared memory per block; nothing is launched."""
+    plan = KV8Plan()
+    _check(lib.woq_kv8_plan_attention(ctypes.byref(cfg), n, rows, q_heads, sms, smem_max, ctypes.byref(plan)),
+           "woq_kv8_plan_attention")
+    return {name: getattr(plan, name) for name, _ in KV8Plan._fields_}
+
+
 def _cache_args(cfg: KV8Config, cache):
     return ctypes.byref(cfg), _dptr(cache, "cache", 1), _nbytes(cache)
 
 
+_KINDS = {"int32": ("torch.int32", "torch.uint32"), "bfloat16": ("torch.bfloat16",), "float32": ("torch.float32",)}
+_KIND_OF = {}  # torch.dtype -> its name (filled as dtypes are met)
+
+
+def _typed(t, name: str, kind: str, itemsize: int, numel: int):
+    if t is not None:
+        have = _KIND_OF.get(t.dtype)
+        if have is None:
+            have = _KIND_OF[t.dtype] = str(t.dtype)
+        if have not in _KINDS[kind]:
+            raise ValueError(f"{name}: expected {kind}, got {t.dtype}")
+    return _dptr(t, name, itemsize, numel)
+
+
 def _ints(t, name: str, numel: int):
-    if t is not None and t.is_floating_point():
-        raise ValueError(f"{name}: expected 32-bit integers, got {t.dtype}")
-    return _dptr(t, name, 4, numel)
+    return _typed(t, name, "int32", 4, numel)
 
 
 def _bf16(t, name: str, numel: int):
-    if t is not None and not str(t.dtype).endswith("bfloat16"):
-        raise ValueError(f"{name}: expected bfloat16, got {t.dtype}")
-    return _dptr(t, name, 2, numel)
+    return _typed(t, name, "bfloat16", 2, numel)
 
 
 def woq_kv8_init(cfg: KV8Config, cache, stream=None) -> None:
@@ -566,20 +608,21 @@ def _qkv(cfg, qkv, q_heads, q_out, rope):
     """Arguments of an append from qkv [rows, >= (q_heads + 2 kv_heads) head_dim] (rows may be strided)."""
     rows = _rows(qkv, "qkv")
     need = (q_heads + 2 * cfg.kv_heads) * cfg.head_dim
-    kind = str(qkv.dtype).rsplit(".", 1)[-1]
-    if kind not in ("bfloat16", "float32"):
+    size = {"torch.bfloat16": 2, "torch.float32": 4}.get(str(qkv.dtype))
+    if size is None:
         raise ValueError(f"qkv: expected bfloat16 or float32, got {qkv.dtype}")
-    if qkv.shape[1] < need or (rows > 0 and qkv.stride(1) != 1):
+    width, (stride, inner) = qkv.shape[1], qkv.stride()
+    if width < need or (rows > 0 and inner != 1):
         raise ValueError(f"qkv: rows of at least {need} neighbouring elements are needed, got {tuple(qkv.shape)}")
-    stride = qkv.stride(0) if rows > 1 else -(-max(qkv.shape[1], need) // 8) * 8
+    if rows <= 1:
+        stride = -(-width // 8) * 8  # one row: its stride says nothing
     if stride < need:
         raise ValueError(f"qkv: rows overlap (row stride {stride}, {need} elements a row)")
-    if not getattr(qkv, "is_cuda", False):
-        raise ValueError("qkv: expected a CUDA tensor")
-    _dptr(qkv[:1, :1].reshape(-1), "qkv")  # device check; the view itself need not be contiguous
+    # the rows may be strided: the first alone is contiguous
+    ptr = _dptr(qkv if qkv.is_contiguous() else qkv[0], "qkv")
     r = None if rope is None else rope._struct(rows)
-    return (ctypes.c_void_p(qkv.data_ptr()), int(kind == "float32"), stride, q_heads,
-            None if r is None else ctypes.byref(r), _bf16(q_out, "q_out", rows * q_heads * cfg.head_dim))
+    return (ptr, int(size == 4), stride, q_heads, None if r is None else ctypes.byref(r),
+            _bf16(q_out, "q_out", rows * q_heads * cfg.head_dim))
 
 
 def woq_kv8_append_rows(cfg: KV8Config, cache, layer: int, seqs, rows: int, qkv, q_heads: int, q_out, rope=None,

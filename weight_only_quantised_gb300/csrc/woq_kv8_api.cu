@@ -101,7 +101,14 @@ int fill_append(const Kv8View& v, int layer, const void* qkv, int dtype, int row
   return WOQ_OK;
 }
 
-int query_limit(int dim) { return dim == 256 ? 64 : 128; }
+int query_limit(int dim) { return dim == 256 ? 56 : 128; }  // one group of 8 queries per warp, 7 warps
+
+// What the attention takes of sequences, rows and heads (its unit counts fit 32 bits).
+bool attn_shape_ok(const Kv8View& v, int n, int rows, int q_heads) {
+  return n >= 0 && n <= kKv8MaxSeqs && rows >= 1 && rows <= WOQ_KV8_ROWS && q_heads >= 1 && q_heads <= 4096 &&
+         q_heads % v.heads == 0 && rows * (q_heads / v.heads) <= query_limit(v.dim) &&
+         (long long)n * v.heads * (v.blocks + 2) <= 0x7FFF0000ll;
+}
 
 // Workspace of the attention: [status 256 B][tickets][partials]
 size_t attn_parts_offset(const Kv8View& v, int n) { return 256 + ((size_t)n * v.heads * 4 + 255) / 256 * 256; }
@@ -109,21 +116,31 @@ size_t attn_parts_offset(const Kv8View& v, int n) { return 256 + ((size_t)n * v.
 }  // namespace
 
 // Query tiles per warp: two as soon as there is more than one tile (head_dim 256: always one; its 16
-// fragments of weighted values take twice the registers).  Warps come in whole groups: 8 to 10.
+// fragments of weighted values take twice the registers).  Warps come in whole groups, as many
+// as leave each warp two stages of the ring at least.
+//
+// The stages are a multiple of a group's warps.  Block b goes to warp b % per of each group and to stage
+// b % stages, so then a stage always serves the same warps.  Otherwise a warp could wait for
+// block b while the copy of block b - stages, another warp's, is still under way (copies end in
+// any order): a wait on a barrier's parity two phases ahead returns at once.
 int kv8_attn_plan(Kv8Attn* p, int smem_max) {
   const int queries = p->rows * p->group, dim = p->v.dim;
   const int tiles = (queries + 7) / 8;
   p->tiles = tiles > 1 && dim < 256 ? 2 : 1;
   p->query_groups = (tiles + p->tiles - 1) / p->tiles;
-  const int per = p->query_groups <= 4 ? (p->query_groups == 3 ? 3 : 8 / p->query_groups) : p->query_groups == 5 ? 2 : 1;
-  p->warps = per * p->query_groups;
   p->least_units = 8;
-  const int fixed = kv8::misc_bytes(p->n) + kv8::merge_bytes(p->warps, p->tiles, dim), record = 128 * dim + 16;
-  int stages = (smem_max - fixed) / record;
-  if (stages > kv8::kMaxStages) stages = kv8::kMaxStages;
-  if (stages < 2) return 0;
-  p->stages = stages;
-  return fixed + stages * record;
+  const int record = 128 * dim + 16, most = kv8::max_warps(p->tiles);
+  for (int per = most / p->query_groups; per >= 1; --per) {
+    const int warps = per * p->query_groups;
+    const int fixed = kv8::misc_bytes(p->n) + kv8::merge_bytes(warps, p->tiles, dim);
+    int stages = (smem_max - fixed) / record;
+    stages = (stages < kv8::kMaxStages ? stages : kv8::kMaxStages) / per * per;
+    if (stages < 2 * per) continue;
+    p->warps = warps;
+    p->stages = stages;
+    return fixed + stages * record;
+  }
+  return 0;
 }
 
 }  // namespace woq
@@ -211,12 +228,29 @@ int woq_kv8_extend(const woq_kv8_config* cfg, void* cache, size_t cache_bytes, i
 
 size_t woq_kv8_attention_workspace(const woq_kv8_config* cfg, int n, int rows, int q_heads) {
   Kv8View v;
-  if (!cfg || !make_view(*cfg, &v) || n < 0 || n > kKv8MaxSeqs || rows < 1 || rows > WOQ_KV8_ROWS || q_heads < 1 ||
-      q_heads % v.heads || rows * (q_heads / v.heads) > query_limit(v.dim))
-    return 0;
+  if (!cfg || !make_view(*cfg, &v) || !attn_shape_ok(v, n, rows, q_heads)) return 0;
   const int sms = sm_count();
   if (sms <= 0) return 0;
   return attn_parts_offset(v, n) + (size_t)2 * sms * rows * (q_heads / v.heads) * (v.dim + 2) * 4;
+}
+
+int woq_kv8_plan_attention(const woq_kv8_config* cfg, int n, int rows, int q_heads, int sms, int smem_max,
+                           woq_kv8_plan* out) {
+  if (!cfg || !out) return WOQ_ERR_NULL;
+  Kv8View v;
+  if (!make_view(*cfg, &v) || !attn_shape_ok(v, n, rows, q_heads) || sms < 0 || smem_max < 0) return WOQ_ERR_SHAPE;
+  if (sms == 0) sms = sm_count();
+  if (smem_max == 0) smem_max = max_dynamic_smem();
+  if (sms <= 0 || smem_max <= 0) return WOQ_ERR_CUDA;
+  Kv8Attn p = {};
+  p.v = v;
+  p.n = n;
+  p.rows = rows;
+  p.group = q_heads / v.heads;
+  const int smem = kv8_attn_plan(&p, smem_max);
+  if (smem == 0) return WOQ_ERR_SHAPE;
+  *out = woq_kv8_plan{sms, p.warps, p.query_groups, p.stages, p.least_units, smem};
+  return WOQ_OK;
 }
 
 int woq_kv8_attention(const woq_kv8_config* cfg, void* cache, size_t cache_bytes, int layer, const int32_t* seqs, int n,
@@ -225,8 +259,7 @@ int woq_kv8_attention(const woq_kv8_config* cfg, void* cache, size_t cache_bytes
   Kv8View v;
   if (const int e = open_cache(cfg, cache, cache_bytes, &v)) return e;
   if (const int e = check_list(seqs, n, false)) return e;
-  if (layer < 0 || layer >= v.layers || rows < 1 || rows > WOQ_KV8_ROWS || q_heads < 1 || q_heads > 4096 ||
-      q_heads % v.heads || rows * (q_heads / v.heads) > query_limit(v.dim) || !isfinite(scale) || window < 0 ||
+  if (layer < 0 || layer >= v.layers || !attn_shape_ok(v, n, rows, q_heads) || !isfinite(scale) || window < 0 ||
       window > 1 << 30 || sinks < 0 || sinks > 1 << 30)
     return WOQ_ERR_SHAPE;
   if (n == 0) return WOQ_OK;

@@ -14,8 +14,8 @@
 // the CTA that counts in last joins them in CTA order, so the result does not depend on the run.
 //
 // CTA: one producer warp copies whole records (16 KB at D = 128, one bulk copy each) into a ring;
-// each consumer warp takes whole blocks by itself, with its own running maximum and sums
-// in registers, so the main loop has no barrier but the ring's.  With more than 8 QT queries the
+// each consumer warp takes whole blocks by itself (always from the same stages, in order), with its own running
+// maximum and sums in registers, so the main loop has no barrier but the ring's.  With more than 8 QT queries the
 // warps form groups, each for its own queries, that all read the block from shared memory.
 //
 // Block: scores transposed, S^T = K Q^T (tokens x queries), so that both codes operands are the
@@ -266,6 +266,23 @@ __device__ __forceinline__ void tail_step(State<D, QT>& st, const uint16_t* tail
   const int g = lane >> 2, t = lane & 3;
   const int r0 = i < 4 ? 16 * (g >> 1) + 4 * i + (g & 1) : 64 + g;
   const int r1 = i < 4 ? r0 + 2 : kKv8Tail;
+  // values first: their loads are under way while the scores are worked out
+  const uint16_t* tv = tail + kKv8Tail * D;
+  uint32_t va[D / 16][4];
+#pragma unroll
+  for (int j = 0; j < D / 16; ++j) {
+    const uint16_t* v0 = tv + (16 * j + g) * kKv8Tail;
+    const uint16_t* v1 = v0 + 8 * kKv8Tail;
+    if (i < 4) {
+      const uint2 x = *reinterpret_cast<const uint2*>(v0 + 16 * t + 4 * i);
+      const uint2 y = *reinterpret_cast<const uint2*>(v1 + 16 * t + 4 * i);
+      va[j][0] = x.x, va[j][1] = y.x, va[j][2] = x.y, va[j][3] = y.y;
+    } else {
+      va[j][0] = *reinterpret_cast<const uint32_t*>(v0 + 64 + 2 * t);
+      va[j][1] = *reinterpret_cast<const uint32_t*>(v1 + 64 + 2 * t);
+      va[j][2] = va[j][3] = 0u;
+    }
+  }
   float s[QT][4];
 #pragma unroll
   for (int q = 0; q < QT; ++q)
@@ -338,27 +355,13 @@ __device__ __forceinline__ void tail_step(State<D, QT>& st, const uint16_t* tail
       lo[q][h] = transpose8x8(pack_bf16(p[2 * h] - f0, p[2 * h + 1] - f1));
     }
   }
-  const uint16_t* tv = tail + kKv8Tail * D;
 #pragma unroll
-  for (int j = 0; j < D / 16; ++j) {
-    const uint16_t* v0 = tv + (16 * j + g) * kKv8Tail;
-    const uint16_t* v1 = v0 + 8 * kKv8Tail;
-    uint32_t a[4];
-    if (i < 4) {
-      const uint2 x = *reinterpret_cast<const uint2*>(v0 + 16 * t + 4 * i);
-      const uint2 y = *reinterpret_cast<const uint2*>(v1 + 16 * t + 4 * i);
-      a[0] = x.x, a[1] = y.x, a[2] = x.y, a[3] = y.y;
-    } else {
-      a[0] = *reinterpret_cast<const uint32_t*>(v0 + 64 + 2 * t);
-      a[1] = *reinterpret_cast<const uint32_t*>(v1 + 64 + 2 * t);
-      a[2] = a[3] = 0u;
-    }
+  for (int j = 0; j < D / 16; ++j)
 #pragma unroll
     for (int q = 0; q < QT; ++q) {
-      mma_bf16(st.o[j][q], a, hi[q][0], hi[q][1]);
-      mma_bf16(st.o[j][q], a, lo[q][0], lo[q][1]);
+      mma_bf16(st.o[j][q], va[j], hi[q][0], hi[q][1]);
+      mma_bf16(st.o[j][q], va[j], lo[q][0], lo[q][1]);
     }
-  }
 }
 
 // Queries of the lane's column n = g as operands, scaled by 2^-e to below 2; returns 2^e.
@@ -401,6 +404,9 @@ __device__ __forceinline__ void load_queries(uint32_t (&qf)[QT][D / 16][2], floa
 }
 
 constexpr int kMaxStages = 32;
+// Most consumer warps: with one query tile per warp 7 (and the producer: two per sub-partition, so 255
+// registers each); with two, where the tensor cores set the pace, 10.
+__host__ __device__ constexpr int max_warps(int tiles) { return tiles == 1 ? 7 : 10; }
 // Shared memory: barriers, flags, units and lengths of the entries; the merge buffer; the ring.
 struct Misc {
   uint64_t full[kMaxStages], empty[kMaxStages];
@@ -412,18 +418,14 @@ __host__ __device__ inline int merge_bytes(int warps, int qt, int dim) {
   return (warps * 8 * qt * (dim + kMergePad + 2) * 4 + 127) / 128 * 128;
 }
 
-// Share c of `units` over `ctas`: [begin, end).
-__device__ __forceinline__ long long share_begin(long long units, int c, int ctas) { return units * c / ctas; }
-// The CTA whose share holds unit u.
-__device__ __forceinline__ int share_of(long long units, int ctas, long long u) {
-  int c = (int)((u * ctas) / units);
-  while (share_begin(units, c + 1, ctas) <= u) ++c;
-  while (share_begin(units, c, ctas) > u) --c;
-  return c;
+// What the joining of partials does with one: its weight against the common maximum m.  A part whose
+// maximum is -inf has seen nothing (sum 0) or only scores that are not numbers (sum NaN: kept).
+__device__ __forceinline__ float part_factor(float pm, float pl, float m) {
+  return pm == -INFINITY ? (pl == 0.0f ? 0.0f : 1.0f) : exp2_approx(pm - m);
 }
 
 template <int FMT, int D, int QT>
-__global__ void __launch_bounds__(352, 1) attn_kernel(const __grid_constant__ Kv8Attn p) {
+__global__ void __launch_bounds__(32 * (max_warps(QT) + 1), 1) attn_kernel(const __grid_constant__ Kv8Attn p) {
   extern __shared__ __align__(128) uint8_t smem[];
   Misc& misc = *reinterpret_cast<Misc*>(smem);
   int* prefix = misc.entries;
@@ -448,9 +450,9 @@ __global__ void __launch_bounds__(352, 1) attn_kernel(const __grid_constant__ Kv
   }
   dev::pdl_wait_prior_grids();
   dev::pdl_launch_dependents();
-  if (!header_ok(v)) return;
-
-  // lengths and units of the entries
+  // lengths and units of the entries (the header's check is read beside them, not before)
+  const uint4 header = *reinterpret_cast<const uint4*>(v.base);
+  const bool ours = header.y == kKv8Magic && header.z == v.hash;
   if (warp == 0) {
     int run = 0;
     for (int e0 = 0; e0 < p.n; e0 += 32) {
@@ -459,7 +461,7 @@ __global__ void __launch_bounds__(352, 1) attn_kernel(const __grid_constant__ Kv
       if (e < p.n) {
         const int seq = p.seqs ? p.seqs[e] : e;
         const bool there = seq >= 0 && seq < v.seqs;
-        if (!there && blockIdx.x == 0) flag(v, WOQ_DEVERR_STATE);
+        if (!there && ours && blockIdx.x == 0) flag(v, WOQ_DEVERR_STATE);
         lens[e] = there ? v.lens_p()[seq] : -1;
         units = there ? span_of(lens[e], p.window, p.sinks).units : 1;
       }
@@ -474,36 +476,38 @@ __global__ void __launch_bounds__(352, 1) attn_kernel(const __grid_constant__ Kv
     }
     if (lane == 0) prefix[p.n] = run;
   }
+  if (!ours) {
+    if (header.y == kKv8Magic && tid == 0) flag(v, WOQ_DEVERR_HEADER);
+    return;
+  }
   __syncthreads();
-  const long long units = (long long)prefix[p.n] * v.heads;
-  long long want = (units + p.least_units - 1) / p.least_units;
-  const int ctas = want < (long long)gridDim.x ? (int)want : (int)gridDim.x;
-  if ((int)blockIdx.x >= ctas) return;
-  const long long begin = share_begin(units, blockIdx.x, ctas), end = share_begin(units, blockIdx.x + 1, ctas);
+  // this CTA's units: `share` of them (the last may have fewer); all counts fit 32 bits (checked on the host)
+  const int units = prefix[p.n] * v.heads;
+  const int share = max(p.least_units, (units + (int)gridDim.x - 1) / (int)gridDim.x);
+  const int begin = (int)blockIdx.x * share, end = min(begin + share, units);
+  if (begin >= units) return;
 
   // the item that holds unit u: entry, head, first unit
-  auto locate = [&](long long u, int* entry, int* head, long long* item_begin) {
+  auto locate = [&](int u, int* entry, int* head, int* item_begin) {
     int lo = 0, hi = p.n - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if ((long long)prefix[mid] * v.heads <= u) lo = mid; else hi = mid - 1;
+      if (prefix[mid] * v.heads <= u) lo = mid; else hi = mid - 1;
     }
-    const int per = prefix[lo + 1] - prefix[lo];
-    const long long first = (long long)prefix[lo] * v.heads;
+    const int per = prefix[lo + 1] - prefix[lo], first = prefix[lo] * v.heads;
     *entry = lo;
-    *head = (int)((u - first) / per);
-    *item_begin = first + (long long)*head * per;
+    *head = (u - first) / per;
+    *item_begin = first + *head * per;
   };
 
   if (warp == W) {  // producer
     int issued = 0;
-    for (long long u = begin; u < end;) {
-      int e, head;
-      long long ib;
+    for (int u = begin; u < end;) {
+      int e, head, ib;
       locate(u, &e, &head, &ib);
       const int per = prefix[e + 1] - prefix[e];
-      const long long stop = ib + per < end ? ib + per : end;
-      const int b0 = (int)(u - ib), b1 = (int)(stop - ib) < per - 1 ? (int)(stop - ib) : per - 1;  // the tail is per - 1
+      const int stop = min(ib + per, end);
+      const int b0 = u - ib, b1 = min(stop - ib, per - 1);  // the tail is unit per - 1
       if (b0 < b1) {
         const Span sp = span_of(lens[e], p.window, p.sinks);
         const int32_t* table = v.table_row(p.seqs ? p.seqs[e] : e);
@@ -545,17 +549,16 @@ __global__ void __launch_bounds__(352, 1) attn_kernel(const __grid_constant__ Kv
   const int g = lane >> 2, t = lane & 3;
   const int consumers = W * 32;
   int taken = 0;  // blocks of this CTA that earlier items had
-  for (long long u = begin; u < end;) {
-    int e, head;
-    long long ib;
+  for (int u = begin; u < end;) {
+    int e, head, ib;
     locate(u, &e, &head, &ib);
     const int per = prefix[e + 1] - prefix[e];
-    const long long stop = ib + per < end ? ib + per : end;
+    const int stop = min(ib + per, end);
     const int len = lens[e];
     const bool there = len >= 0;
     const Span sp = span_of(there ? len : 0, p.window, p.sinks);
     const bool has_tail = stop == ib + per && there;
-    const int b0 = (int)(u - ib), b1 = (int)(stop - ib) < per - 1 ? (int)(stop - ib) : per - 1;
+    const int b0 = u - ib, b1 = min(stop - ib, per - 1);
     const int seq = p.seqs ? p.seqs[e] : e;
 
     // queries and what their rows see
@@ -599,7 +602,7 @@ __global__ void __launch_bounds__(352, 1) attn_kernel(const __grid_constant__ Kv
           tail_step<D, QT>(st, tail, i, in_tail, len, there, qrow, p.scale_log2, col, p.sinks, lane);
     }
     bool ok = true;
-    int k = b0 + ((slot - taken) % WG + WG) % WG;  // ring positions taken + (k - b0) = slot mod WG
+    int k = b0 + ((slot - taken) % WG + WG) % WG;  // ring positions taken + (k - b0) = slot mod WG (S a multiple of WG)
     for (; k < b1 && ok; k += WG) {
       const int at = taken + (k - b0), stage = at % S;
       ok = dev::mbar_wait_bounded(&misc.full[stage], (uint32_t)((at / S) & 1));
@@ -647,27 +650,35 @@ __global__ void __launch_bounds__(352, 1) attn_kernel(const __grid_constant__ Kv
     const bool whole = u == ib && stop == ib + per;
     const int mine = ib <= begin ? 0 : 1;  // partial slots: the item that holds the share's first unit, and the other
     float* part = p.parts + ((size_t)blockIdx.x * 2 + mine) * R * (D + 2);
+    uint16_t* out0 = p.out + ((size_t)e * p.rows * p.q_heads + (size_t)head * p.group) * D;
     for (int x = tid; x < R * (D / 4); x += consumers) {
-      const int n = x / (D / 4), d = (x % (D / 4)) * 4, gr = n / (8 * QT), in = n % (8 * QT);
-      float m = -INFINITY;
-      for (int w = 0; w < WG; ++w) m = fmaxf(m, warp_ml[2 * ((w * G + gr) * 8 * QT + in)]);
+      const int n = x / (D / 4), d = (x % (D / 4)) * 4;
+      const int row0 = (n / (8 * QT)) * 8 * QT + n % (8 * QT);  // of warp `group`; the group's warps are G apart
+      float pm[8], pl[8], m = -INFINITY, l = 0.0f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        const float2 ml = w < WG ? *reinterpret_cast<const float2*>(warp_ml + 2 * (row0 + w * G * 8 * QT))
+                                 : make_float2(-INFINITY, 0.0f);
+        pm[w] = ml.x;
+        pl[w] = ml.y;
+        m = fmaxf(m, ml.x);
+      }
       float4 o = {0, 0, 0, 0};
-      float l = 0.0f;
-      for (int w = 0; w < WG; ++w) {
-        const int row = (w * G + gr) * 8 * QT + in;
-        const float mw = warp_ml[2 * row];
-        const float f = mw == -INFINITY ? (warp_ml[2 * row + 1] == 0.0f ? 0.0f : 1.0f) : exp2_approx(mw - m);
-        const float4 y = *reinterpret_cast<const float4*>(merge + (size_t)row * kRow + d);
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        if (w >= WG) break;
+        const float f = part_factor(pm[w], pl[w], m);
+        const float4 y = *reinterpret_cast<const float4*>(merge + (size_t)(row0 + w * G * 8 * QT) * kRow + d);
         o.x += f * y.x;
         o.y += f * y.y;
         o.z += f * y.z;
         o.w += f * y.w;
-        l += f * warp_ml[2 * row + 1];
+        l += f * pl[w];
       }
       if (whole) {
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        uint16_t* out = p.out + (((size_t)e * p.rows + n / p.group) * p.q_heads + (size_t)head * p.group + n % p.group) * D + d;
-        *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+        *reinterpret_cast<uint2*>(out0 + ((size_t)(n / p.group) * p.q_heads + n % p.group) * D + d) =
+            make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
       } else {
         float* to = part + (size_t)n * (D + 2);
         *reinterpret_cast<float2*>(to + 2 + d) = make_float2(o.x, o.y);
@@ -676,36 +687,57 @@ __global__ void __launch_bounds__(352, 1) attn_kernel(const __grid_constant__ Kv
       }
     }
     if (!whole) {
-      const int c0 = share_of(units, ctas, ib), c1 = share_of(units, ctas, ib + per - 1);
-      __threadfence();
+      // CTAs c0 .. c1 share the item; the one that counts in last joins their partials in CTA order
+      const int c0 = ib / share, c1 = (ib + per - 1) / share;
       dev::named_barrier_sync(1, consumers);
       uint32_t* ticket = p.tickets + (size_t)e * v.heads + head;
       if (tid == 0) misc.last = dev::atomic_add_acq_rel_gpu(ticket, 1u) == (uint32_t)(c1 - c0);
       dev::named_barrier_sync(1, consumers);
       if (misc.last) {
-        __threadfence();
-        for (int x = tid; x < R * (D / 2); x += consumers) {
-          const int n = x / (D / 2), d = (x % (D / 2)) * 2;
+        // a warp per query: lanes hold 32 parts' maxima and sums at a time, then a slice of the head each.
+        // The item is the first of each CTA's slots but perhaps of c0's, where it may be the second.
+        const size_t step = (size_t)2 * R * (D + 2);
+        const float* parts = p.parts + (size_t)c0 * step;
+        const size_t first = ib > c0 * share ? step / 2 : 0;
+        const int np = c1 - c0 + 1;
+        for (int n = warp; n < R; n += W) {
+          const float* at = parts + (size_t)n * (D + 2);
           float m = -INFINITY;
-          for (int c = c0; c <= c1; ++c) {
-            const int which = ib <= share_begin(units, c, ctas) ? 0 : 1;
-            m = fmaxf(m, __ldcg(p.parts + (((size_t)c * 2 + which) * R + n) * (D + 2)));
-          }
-          float2 o = {0, 0};
+          for (int c = lane; c < np; c += 32) m = fmaxf(m, __ldcg(at + c * step + (c == 0 ? first : 0)));
+#pragma unroll
+          for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
           float l = 0.0f;
-          for (int c = c0; c <= c1; ++c) {
-            const int which = ib <= share_begin(units, c, ctas) ? 0 : 1;
-            const float* from = p.parts + (((size_t)c * 2 + which) * R + n) * (D + 2);
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(from));
-            const float2 y = __ldcg(reinterpret_cast<const float2*>(from + 2 + d));
-            const float f = ml.x == -INFINITY ? (ml.y == 0.0f ? 0.0f : 1.0f) : exp2_approx(ml.x - m);
-            o.x += f * y.x;
-            o.y += f * y.y;
-            l += f * ml.y;
+          float2 o[D / 64];
+#pragma unroll
+          for (int j = 0; j < D / 64; ++j) o[j] = make_float2(0.0f, 0.0f);
+          for (int cc = 0; cc < np; cc += 32) {
+            const int c = cc + lane;
+            float f = 0.0f;
+            if (c < np) {
+              const float2 ml = __ldcg(reinterpret_cast<const float2*>(at + c * step + (c == 0 ? first : 0)));
+              f = part_factor(ml.x, ml.y, m);
+              l += f * ml.y;
+            }
+            const int some = min(32, np - cc);
+#pragma unroll 8
+            for (int i = 0; i < some; ++i) {
+              const float fi = __shfl_sync(~0u, f, i);
+              const float* from = at + (size_t)(cc + i) * step + (cc + i == 0 ? first : 0) + 2;
+#pragma unroll
+              for (int j = 0; j < D / 64; ++j) {
+                const float2 y = __ldcg(reinterpret_cast<const float2*>(from + 64 * j + 2 * lane));
+                o[j].x += fi * y.x;
+                o[j].y += fi * y.y;
+              }
+            }
           }
+#pragma unroll
+          for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
           const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-          uint16_t* out = p.out + (((size_t)e * p.rows + n / p.group) * p.q_heads + (size_t)head * p.group + n % p.group) * D + d;
-          *reinterpret_cast<uint32_t*>(out) = pack_bf16(o.x * inv, o.y * inv);
+#pragma unroll
+          for (int j = 0; j < D / 64; ++j)
+            *reinterpret_cast<uint32_t*>(out0 + ((size_t)(n / p.group) * p.q_heads + n % p.group) * D + 64 * j + 2 * lane) =
+                pack_bf16(o[j].x * inv, o[j].y * inv);
         }
         if (tid == 0) *ticket = 0u;
       }
