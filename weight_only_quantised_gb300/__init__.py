@@ -493,24 +493,30 @@ class _Rope(ctypes.Structure):
 
 
 class Rope:
-    """Rotary arguments of an append (woq_rope): table fp32 [positions, rot_dim / 2, 2] from woq_rope_table;
-    pos int32 [axes, rows] (device); axis_of: the axis of each frequency (host integers; None: all 0)."""
+    """Rotary arguments of appends (woq_rope), checked once: table fp32 [positions, rot_dim / 2, 2] from
+    woq_rope_table; pos int32 [axes, rows] (device; its contents may change from call to call); axis_of: the axis
+    of each frequency (host integers; None: all 0)."""
 
     def __init__(self, table, pos, axis_of=None, interleaved: bool = False):
-        self.table, self.pos, self.interleaved = table, pos, bool(interleaved)
-        self.axis_of = None if axis_of is None else np.ascontiguousarray(axis_of, dtype=np.uint8)
-
-    def _struct(self, rows: int) -> _Rope:
-        t, pos = self.table, self.pos
-        if t.dim() != 3 or t.shape[2] != 2:
+        if table.dim() != 3 or table.shape[2] != 2:
             raise ValueError("rope table: expected [positions, rot_dim / 2, 2]")
-        if pos.dim() != 2 or pos.shape[1] != rows:
-            raise ValueError(f"rope positions: expected [axes, {rows}], got {tuple(pos.shape)}")
-        if self.axis_of is not None and self.axis_of.size != t.shape[1]:
-            raise ValueError(f"rope axis_of: expected {t.shape[1]} entries, got {self.axis_of.size}")
-        return _Rope(_typed(t, "rope table", "float32", 4, -1), t.shape[0], 2 * t.shape[1], int(self.interleaved),
-                     pos.shape[0], _ints(pos, "rope positions", -1),
-                     None if self.axis_of is None else self.axis_of.ctypes.data)
+        if pos.dim() != 2:
+            raise ValueError(f"rope positions: expected [axes, rows], got {tuple(pos.shape)}")
+        axis_of = None if axis_of is None else np.array(axis_of, dtype=np.uint8)
+        if axis_of is not None and axis_of.size != table.shape[1]:
+            raise ValueError(f"rope axis_of: expected {table.shape[1]} entries, got {axis_of.size}")
+        self._args = _Rope(_f32(table, "rope table", -1), table.shape[0], 2 * table.shape[1], int(bool(interleaved)),
+                           pos.shape[0], _ints(pos, "rope positions", -1),
+                           None if axis_of is None else axis_of.ctypes.data)
+        self._held = table, pos, axis_of
+        self._rows, self._device = pos.shape[1], pos.get_device()
+
+    def _ref(self, rows: int):
+        if rows != self._rows:
+            raise ValueError(f"rope positions: expected [axes, {rows}], got {tuple(self._held[1].shape)}")
+        if self._device != _current_device():
+            raise ValueError(f"rope: tensors are on cuda:{self._device}, the current device is cuda:{_current_device()}")
+        return ctypes.byref(self._args)
 
 
 class KV8Plan(ctypes.Structure):
@@ -570,26 +576,37 @@ def _cache_args(cfg: KV8Config, cache):
     return ctypes.byref(cfg), _dptr(cache, "cache", 1), _nbytes(cache)
 
 
-_KINDS = {"int32": ("torch.int32", "torch.uint32"), "bfloat16": ("torch.bfloat16",), "float32": ("torch.float32",)}
-_KIND_OF = {}  # torch.dtype -> its name (filled as dtypes are met)
+_DTYPES = {}  # element type -> the torch dtypes that hold it (bound on first use)
 
 
-def _typed(t, name: str, kind: str, itemsize: int, numel: int):
-    if t is not None:
-        have = _KIND_OF.get(t.dtype)
-        if have is None:
-            have = _KIND_OF[t.dtype] = str(t.dtype)
-        if have not in _KINDS[kind]:
-            raise ValueError(f"{name}: expected {kind}, got {t.dtype}")
-    return _dptr(t, name, itemsize, numel)
+def _dtypes(kind: str):
+    import torch
+    _DTYPES.update(int32=(torch.int32, getattr(torch, "uint32", torch.int32)), bfloat16=(torch.bfloat16,),
+                   float32=(torch.float32,), qkv={torch.bfloat16: 0, torch.float32: 1})
+    return _DTYPES[kind]
+
+
+def _typed(t, name: str, kind: str, numel: int):
+    """Device pointer of a contiguous tensor of the kind with at least numel elements (None -> NULL)."""
+    if t is None:
+        return None
+    if t.dtype not in (_DTYPES.get(kind) or _dtypes(kind)):
+        raise ValueError(f"{name}: expected {kind}, got {t.dtype}")
+    if not (t.is_cuda and t.is_contiguous() and t.get_device() == _current_device()) or t.numel() < numel:
+        return _dptr(t, name, 0, numel)  # says what is wrong
+    return t.data_ptr()
 
 
 def _ints(t, name: str, numel: int):
-    return _typed(t, name, "int32", 4, numel)
+    return _typed(t, name, "int32", numel)
 
 
 def _bf16(t, name: str, numel: int):
-    return _typed(t, name, "bfloat16", 2, numel)
+    return _typed(t, name, "bfloat16", numel)
+
+
+def _f32(t, name: str, numel: int):
+    return _typed(t, name, "float32", numel)
 
 
 def woq_kv8_init(cfg: KV8Config, cache, stream=None) -> None:
@@ -608,8 +625,8 @@ def _qkv(cfg, qkv, q_heads, q_out, rope):
     """Arguments of an append from qkv [rows, >= (q_heads + 2 kv_heads) head_dim] (rows may be strided)."""
     rows = _rows(qkv, "qkv")
     need = (q_heads + 2 * cfg.kv_heads) * cfg.head_dim
-    size = {"torch.bfloat16": 2, "torch.float32": 4}.get(str(qkv.dtype))
-    if size is None:
+    kind = (_DTYPES.get("qkv") or _dtypes("qkv")).get(qkv.dtype)
+    if kind is None:
         raise ValueError(f"qkv: expected bfloat16 or float32, got {qkv.dtype}")
     width, (stride, inner) = qkv.shape[1], qkv.stride()
     if width < need or (rows > 0 and inner != 1):
@@ -620,8 +637,7 @@ def _qkv(cfg, qkv, q_heads, q_out, rope):
         raise ValueError(f"qkv: rows overlap (row stride {stride}, {need} elements a row)")
     # the rows may be strided: the first alone is contiguous
     ptr = _dptr(qkv if qkv.is_contiguous() else qkv[0], "qkv")
-    r = None if rope is None else rope._struct(rows)
-    return (ptr, int(size == 4), stride, q_heads, None if r is None else ctypes.byref(r),
+    return (ptr, kind, stride, q_heads, None if rope is None else rope._ref(rows),
             _bf16(q_out, "q_out", rows * q_heads * cfg.head_dim))
 
 

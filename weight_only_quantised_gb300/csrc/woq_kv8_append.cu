@@ -19,6 +19,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
 __global__ void __launch_bounds__(256) rope_table_kernel(double theta, int half, int positions, float2* table) {
+  begin_after_prior();
   const long long n = (long long)half * positions;
   for (long long u = (long long)blockIdx.x * blockDim.x + threadIdx.x; u < n; u += (long long)gridDim.x * blockDim.x) {
     const int i = (int)(u % half);
@@ -45,16 +46,34 @@ struct Angles {
   float4 cs[2];  // c, s, c, s
 };
 
+// The row's positions on each axis; one outside the table is reported and taken as 0.
+struct Places {
+  int p[4];
+  __device__ __forceinline__ int of(int axis) const { return axis < 2 ? (axis ? p[1] : p[0]) : (axis == 2 ? p[2] : p[3]); }
+};
+
+__device__ __forceinline__ Places load_places(const Kv8Rope& r, int row, int rows, bool* bad) {
+  Places a;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    a.p[i] = r.half > 0 && i < r.axes ? r.pos[(size_t)i * rows + row] : 0;
+    if (a.p[i] < 0 || (r.half > 0 && a.p[i] >= r.positions)) {
+      *bad = true;
+      a.p[i] = 0;
+    }
+  }
+  return a;
+}
+
 __device__ __forceinline__ Angles load_angles(const Kv8Rope& r, const uint8_t* axis, int row, int rows, int lane,
                                               bool* bad) {
   Angles a;
+  const Places pl = load_places(r, row, rows, bad);
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const int i = 2 * lane + 64 * j;
     if (i >= r.half) break;
-    int p0 = r.pos[(size_t)axis[i] * rows + row], p1 = r.pos[(size_t)axis[i + 1] * rows + row];
-    if (p0 < 0 || p0 >= r.positions) { *bad = true; p0 = 0; }
-    if (p1 < 0 || p1 >= r.positions) { *bad = true; p1 = 0; }
+    const int p0 = pl.of(axis[i]), p1 = pl.of(axis[i + 1]);
     const float2* t = reinterpret_cast<const float2*>(r.table);
     const float2 x = __ldg(t + (size_t)p0 * r.half + i), y = __ldg(t + (size_t)p1 * r.half + i + 1);
     a.cs[j] = make_float4(x.x, x.y, y.x, y.y);
@@ -101,6 +120,85 @@ __device__ __forceinline__ void plain_row(const void* x, long long at, int dim, 
     const float2 u = load2<F32>(x, at + d);
     emit(d, pack_bf16(u.x, u.y));
   }
+}
+
+// The same in 16-byte vectors, for heads that are rotated as a whole: half / 8 lanes a row, each for eight
+// frequencies i0 .. i0 + 7 and their sixteen elements, two runs of eight (i0 and half + i0, or 2 i0 and
+// 2 i0 + 8 if interleaved).
+struct Angles8 {
+  float2 cs[8];
+};
+
+__device__ __forceinline__ Angles8 load_angles8(const Kv8Rope& r, const uint8_t* axis, const Places& pl, int i0) {
+  Angles8 a;
+  const float2* t = reinterpret_cast<const float2*>(r.table);
+  if (r.axes == 1) {
+    const float4* from = reinterpret_cast<const float4*>(t + (size_t)pl.p[0] * r.half + i0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float4 x = __ldg(from + j);
+      a.cs[2 * j] = make_float2(x.x, x.y);
+      a.cs[2 * j + 1] = make_float2(x.z, x.w);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a.cs[j] = __ldg(t + (size_t)pl.of(axis[i0 + j]) * r.half + i0 + j);
+  }
+  return a;
+}
+
+// Eight neighbouring elements from a 16-byte boundary.
+template <bool F32>
+struct Run8 {
+  uint4 w[F32 ? 2 : 1];
+  __device__ __forceinline__ void load(const void* base, long long at) {
+    const uint4* p = F32 ? reinterpret_cast<const uint4*>(static_cast<const float*>(base) + at)
+                         : reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at);
+    w[0] = __ldcs(p);
+    if constexpr (F32) w[1] = __ldcs(p + 1);
+  }
+  __device__ __forceinline__ float operator[](int i) const {  // i a compile-time constant
+    if constexpr (F32) {
+      const uint4& v = w[i >> 2];
+      return __uint_as_float((i & 3) == 0 ? v.x : (i & 3) == 1 ? v.y : (i & 3) == 2 ? v.z : v.w);
+    } else {
+      const uint32_t v = (i >> 1) == 0 ? w[0].x : (i >> 1) == 1 ? w[0].y : (i >> 1) == 2 ? w[0].z : w[0].w;
+      return __uint_as_float((i & 1) ? v & 0xFFFF0000u : v << 16);
+    }
+  }
+  __device__ __forceinline__ uint4 rounded() const {
+    return make_uint4(pack_bf16((*this)[0], (*this)[1]), pack_bf16((*this)[2], (*this)[3]), pack_bf16((*this)[4], (*this)[5]),
+                      pack_bf16((*this)[6], (*this)[7]));
+  }
+};
+
+template <bool F32>
+__device__ __forceinline__ void rotate8(const Run8<F32>& x, const Run8<F32>& y, const Angles8& a, bool interleaved,
+                                        uint4* u, uint4* v) {
+  uint32_t o[8];
+  if (interleaved) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 p = turn(x[2 * j], x[2 * j + 1], a.cs[j].x, a.cs[j].y);
+      const float2 q = turn(y[2 * j], y[2 * j + 1], a.cs[4 + j].x, a.cs[4 + j].y);
+      o[j] = pack_bf16(p.x, p.y);
+      o[4 + j] = pack_bf16(q.x, q.y);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 p = turn(x[2 * j], y[2 * j], a.cs[2 * j].x, a.cs[2 * j].y);
+      const float2 q = turn(x[2 * j + 1], y[2 * j + 1], a.cs[2 * j + 1].x, a.cs[2 * j + 1].y);
+      o[j] = pack_bf16(p.x, q.x);
+      o[4 + j] = pack_bf16(p.y, q.y);
+    }
+  }
+  *u = make_uint4(o[0], o[1], o[2], o[3]);
+  *v = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+__device__ __forceinline__ bool not_finite8(const uint4& x) {
+  return bf16_pair_not_finite(x.x) || bf16_pair_not_finite(x.y) || bf16_pair_not_finite(x.z) || bf16_pair_not_finite(x.w);
 }
 
 // 64 rows of bf16 in shared memory, rows of D elements, 16-byte vectors swizzled.
@@ -183,20 +281,39 @@ __device__ __forceinline__ void quantise_any(const Kv8View& v, const uint16_t* k
   else quantise_block<WOQ_KV8_E4M3>(kt, vt, v.dim, bad, rec, sh);
 }
 
-// Rows r0 .. r1 - 1 of a tail into the tiles; returns whether this thread met one that is not finite.
-__device__ bool tail_to_tiles(const uint16_t* tail, int r0, int r1, int D, uint16_t* kt, uint16_t* vt) {
+// Rows 0 .. r1 - 1 of a tail into the tiles, with the rows from `at` on taken at the set bits of keep behind it
+// (row at + j: the j-th bit); returns whether this thread met a key that is not finite.
+__device__ __forceinline__ int kept_row(int r, int at, uint32_t keep) { return r < at ? r : at + (int)__fns(keep, 0, r - at + 1); }
+
+__device__ bool tail_to_tiles(const uint16_t* tail, int r1, int at, uint32_t keep, int D, uint16_t* kt, uint16_t* vt) {
   bool bad = false;
-  for (int u = threadIdx.x; u < (r1 - r0) * (D / 8); u += kThreads) {
-    const int r = r0 + u / (D / 8), d = (u % (D / 8)) * 8;
-    const uint4 x = *reinterpret_cast<const uint4*>(tail + (size_t)r * D + d);
-    bad |= bf16_pair_not_finite(x.x) || bf16_pair_not_finite(x.y) || bf16_pair_not_finite(x.z) ||
-           bf16_pair_not_finite(x.w);
+#pragma unroll 4
+  for (int u = threadIdx.x; u < r1 * (D / 8); u += kThreads) {
+    const int r = u / (D / 8), d = (u % (D / 8)) * 8;
+    const uint4 x = *reinterpret_cast<const uint4*>(tail + (size_t)kept_row(r, at, keep) * D + d);
+    bad |= not_finite8(x);
     *reinterpret_cast<uint4*>(kt + tile_at(r, d, D)) = x;
   }
   const uint16_t* tv = tail + (size_t)kKv8Tail * D;
-  for (int u = threadIdx.x; u < (r1 - r0) * D; u += kThreads) {
-    const int d = u / (r1 - r0), r = r0 + u % (r1 - r0);
-    vt[tile_at(r, d, D)] = tv[(size_t)d * kKv8Tail + r];
+  const int octets = (r1 + 7) / 8;
+#pragma unroll 4
+  for (int u = threadIdx.x; u < octets * D; u += kThreads) {  // lanes take neighbouring elements
+    const int d = u % D, r = (u / D) * 8;
+    uint32_t x[4];
+    if (r + 8 <= at) {
+      const uint4 y = *reinterpret_cast<const uint4*>(tv + (size_t)d * kKv8Tail + r);
+      x[0] = y.x, x[1] = y.y, x[2] = y.z, x[3] = y.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = r + 2 * i < r1 ? tv[(size_t)d * kKv8Tail + kept_row(r + 2 * i, at, keep)] : 0u;
+        const uint32_t hi = r + 2 * i + 1 < r1 ? tv[(size_t)d * kKv8Tail + kept_row(r + 2 * i + 1, at, keep)] : 0u;
+        x[i] = lo | hi << 16;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (r + i < r1) vt[tile_at(r + i, d, D)] = (uint16_t)(x[i >> 1] >> (16 * (i & 1)));
   }
   return bad;
 }
@@ -208,34 +325,57 @@ __device__ __forceinline__ void stage_axes(const Kv8Rope& r, uint8_t* axis) {
   __syncthreads();
 }
 
-// Queries of a prompt: a warp per row, the row's angles in registers for all of its heads.
-template <bool F32>
+// Queries of a prompt: a warp per row, the row's angles in registers for all of its heads.  VEC: heads
+// rotated as a whole, half / 8 lanes a head (a warp turns 4 heads of 128 at once, with 16-byte loads, five
+// steps of them under way).
+template <bool F32, bool VEC>
 __global__ void __launch_bounds__(kThreads) prompt_q_kernel(const __grid_constant__ Kv8Append p) {
   __shared__ uint8_t axis[128];
-  if (!header_ok(p.v)) return;
   stage_axes(p.rope, axis);
+  begin_after_prior();
+  if (!header_ok(p.v)) return;
   const int lane = threadIdx.x & 31, row = blockIdx.x * kWarps + (threadIdx.x >> 5), D = p.v.dim;
   if (row >= p.rows) return;
   bool bad = false;
-  const Angles ang = load_angles(p.rope, axis, row, p.rows, lane, &bad);
-  if (__any_sync(~0u, bad) && lane == 0) flag(p.v, WOQ_DEVERR_POSITION);
   const long long at = (long long)row * p.row_stride;
   uint16_t* out = p.q_out + (size_t)row * p.q_heads * D;
+  if constexpr (VEC) {
+    const Places pl = load_places(p.rope, row, p.rows, &bad);
+    const int lanes = p.rope.half / 8, i0 = (lane % lanes) * 8, step = 32 / lanes;
+    const int d0 = p.rope.interleaved ? 2 * i0 : i0, d1 = p.rope.interleaved ? d0 + 8 : p.rope.half + i0;
+    const Angles8 ang = load_angles8(p.rope, axis, pl, i0);
+#pragma unroll 5
+    for (int h = lane / lanes; h < p.q_heads; h += step) {
+      Run8<F32> x, y;
+      x.load(p.qkv, at + h * D + d0);
+      y.load(p.qkv, at + h * D + d1);
+      uint4 u, v;
+      rotate8<F32>(x, y, ang, p.rope.interleaved, &u, &v);
+      *reinterpret_cast<uint4*>(out + h * D + d0) = u;
+      *reinterpret_cast<uint4*>(out + h * D + d1) = v;
+    }
+  } else {
+    const Angles ang = load_angles(p.rope, axis, row, p.rows, lane, &bad);
 #pragma unroll 4
-  for (int h = 0; h < p.q_heads; ++h)
-    rotate_row<F32>(p.qkv, at + (long long)h * D, D, p.rope, ang, lane,
-                    [&](int d, uint32_t x) { *reinterpret_cast<uint32_t*>(out + (size_t)h * D + d) = x; });
+    for (int h = 0; h < p.q_heads; ++h)
+      rotate_row<F32>(p.qkv, at + (long long)h * D, D, p.rope, ang, lane,
+                      [&](int d, uint32_t x) { *reinterpret_cast<uint32_t*>(out + (size_t)h * D + d) = x; });
+  }
+  if (__any_sync(~0u, bad) && lane == 0) flag(p.v, WOQ_DEVERR_POSITION);
 }
 
 // Keys and values of a prompt: grid (blocks, heads).  Block b of the sequence goes to its page if
 // it is full, else to the tail.  The first block may have rows in the tail already; the CTA that reads
 // those also writes the tail's new rows, after it (no other CTA writes what it reads).
-template <bool F32>
+template <bool F32, bool VEC>
 __global__ void __launch_bounds__(kThreads) prompt_kv_kernel(const __grid_constant__ Kv8Append p) {
   extern __shared__ __align__(16) uint16_t tiles[];
   __shared__ uint8_t axis[128];
+  __shared__ int odd_row[kKv8Block];
   __shared__ BlockShared sh;
   const Kv8View& v = p.v;
+  stage_axes(p.rope, axis);
+  begin_after_prior();
   if (!header_ok(v)) return;
   const int seq = p.n, T = p.rows, D = v.dim, head = blockIdx.y;
   const int len = v.lens_p()[seq], start = len - T;
@@ -243,7 +383,6 @@ __global__ void __launch_bounds__(kThreads) prompt_kv_kernel(const __grid_consta
     if (threadIdx.x == 0) flag(v, WOQ_DEVERR_STATE);
     return;
   }
-  stage_axes(p.rope, axis);
   uint16_t *kt = tiles, *vt = tiles + 64 * D;
   uint16_t* tail = v.tail(p.layer, seq, head);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -254,9 +393,53 @@ __global__ void __launch_bounds__(kThreads) prompt_kv_kernel(const __grid_consta
   for (;;) {
     const int r0 = b == first ? start - first * kKv8Block : 0;  // rows of this call: r0 .. r1 - 1
     const int r1 = b == full ? len - full * kKv8Block : kKv8Block;
-    bool bad = b < full && tail_to_tiles(tail, 0, r0, D, kt, vt);
+    bool bad = b < full && tail_to_tiles(tail, r0, r0, 0, D, kt, vt);
+    if constexpr (VEC) {
+      if (threadIdx.x < kKv8Block) odd_row[threadIdx.x] = 0;
+      __syncthreads();
+      bool far = false;
+      const int lanes = p.rope.half / 8, per = kThreads / lanes, i0 = ((int)threadIdx.x % lanes) * 8;
+      const int d0 = p.rope.interleaved ? 2 * i0 : i0, d1 = p.rope.interleaved ? d0 + 8 : p.rope.half + i0;
+      const long long base = (long long)(b * kKv8Block - start) * p.row_stride + (long long)(p.q_heads + head) * D;
 #pragma unroll 2
-    for (int r = r0 + warp; r < r1; r += kWarps) {
+      for (int r = r0 + (int)threadIdx.x / lanes; r < r1; r += per) {
+        const int row = b * kKv8Block + r - start;
+        Run8<F32> x, y;
+        x.load(p.qkv, base + (long long)r * p.row_stride + d0);
+        y.load(p.qkv, base + (long long)r * p.row_stride + d1);
+        const Places pl = load_places(p.rope, row, T, &far);
+        const Angles8 ang = load_angles8(p.rope, axis, pl, i0);
+        uint4 u, w;
+        rotate8<F32>(x, y, ang, p.rope.interleaved, &u, &w);
+        if (not_finite8(u) || not_finite8(w)) odd_row[r] = 1;
+        *reinterpret_cast<uint4*>(kt + tile_at(r, d0, D)) = u;
+        *reinterpret_cast<uint4*>(kt + tile_at(r, d1, D)) = w;
+      }
+      const int vper = kThreads / (D / 8), vd = ((int)threadIdx.x % (D / 8)) * 8;
+#pragma unroll 4
+      for (int r = r0 + (int)threadIdx.x / (D / 8); r < r1; r += vper) {
+        Run8<F32> x;
+        x.load(p.qkv, base + (long long)r * p.row_stride + (long long)v.heads * D + vd);
+        const uint4 u = x.rounded();
+        if (not_finite8(u)) odd_row[r] = 1;
+        *reinterpret_cast<uint4*>(vt + tile_at(r, vd, D)) = u;
+      }
+      if (__any_sync(~0u, far) && lane == 0) flag(v, WOQ_DEVERR_POSITION);
+      __syncthreads();
+      const int mine = (int)threadIdx.x < kKv8Block ? odd_row[threadIdx.x] : 0;
+      if (__syncthreads_or(mine)) {  // a key that is not finite, or its value: the key becomes NaN and the value 0
+        bad = true;
+        for (int r = r0 + warp; r < r1; r += kWarps) {
+          if (!odd_row[r]) continue;
+          for (int d = 2 * lane; d < D; d += 64) {
+            *reinterpret_cast<uint32_t*>(kt + tile_at(r, d, D)) = 0x7FC07FC0u;
+            *reinterpret_cast<uint32_t*>(vt + tile_at(r, d, D)) = 0u;
+          }
+        }
+      }
+    }
+#pragma unroll 2
+    for (int r = r0 + warp; !VEC && r < r1; r += kWarps) {
       const int row = b * kKv8Block + r - start;
       const long long at = (long long)row * p.row_stride + (long long)(p.q_heads + head) * D;
       bool far = false, odd = false;
@@ -306,8 +489,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
   __shared__ uint8_t axis[128];
   const Kv8View& v = p.v;
   stage_axes(p.rope, axis);
-  dev::pdl_wait_prior_grids();
-  dev::pdl_launch_dependents();
+  begin_after_prior();
   if (!header_ok(v)) return;
   const int lane = threadIdx.x & 31, D = v.dim, slots = p.q_heads + v.heads;
   const long long u = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -372,35 +554,33 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
 __global__ void __launch_bounds__(kThreads) accept_kernel(const __grid_constant__ Kv8View v) {
   extern __shared__ __align__(16) uint16_t tiles[];
   __shared__ BlockShared sh;
+  begin_after_prior();
   if (!header_ok(v)) return;
   const int4 m = v.moves_p()[blockIdx.x];
   const uint32_t keep = (uint32_t)m.y;
   if (keep == 0) return;
   const int D = v.dim, at = m.x % kKv8Block, kept = __popc(keep);
   uint16_t* tail = v.tail(blockIdx.z, m.w, blockIdx.y);
-  uint16_t* tv = tail + (size_t)kKv8Tail * D;
-  if ((keep & (keep + 1)) != 0) {  // not already in place
-    for (int d = threadIdx.x; d < D; d += kThreads) {  // a thread moves one element of every row
-      uint32_t left = keep;
-      for (int j = 0; j < kept; ++j) {
-        const int from = __ffs(left) - 1;
-        left &= left - 1;
-        tail[(size_t)(at + j) * D + d] = tail[(size_t)(at + from) * D + d];
-        tv[(size_t)d * kKv8Tail + at + j] = tv[(size_t)d * kKv8Tail + at + from];
-      }
-    }
+  if (m.z >= 0) {  // rows 0 .. 63 to the page
+    uint16_t *kt = tiles, *vt = tiles + 64 * D;
+    const bool bad = __syncthreads_or(tail_to_tiles(tail, kKv8Block, at, keep, D, kt, vt));
+    quantise_any(v, kt, vt, bad, v.record(m.z, blockIdx.z, blockIdx.y), sh);
+  } else if ((keep & (keep + 1)) == 0) {
+    return;  // in place already
   }
-  if (m.z < 0) return;
-  __syncthreads();
-  uint16_t *kt = tiles, *vt = tiles + 64 * D;
-  const bool bad = __syncthreads_or(tail_to_tiles(tail, 0, kKv8Block, D, kt, vt));
-  quantise_any(v, kt, vt, bad, v.record(m.z, blockIdx.z, blockIdx.y), sh);
-  const int rest = at + kept - kKv8Block;
-  for (int d = threadIdx.x; d < D; d += kThreads) {
-    for (int j = 0; j < rest; ++j) {
-      tail[(size_t)j * D + d] = tail[(size_t)(kKv8Block + j) * D + d];
-      tv[(size_t)d * kKv8Tail + j] = tv[(size_t)d * kKv8Tail + kKv8Block + j];
-    }
+  // the other kept rows, each to its place in the tail: a thread moves one element of all of them (at most 8,
+  // read before the first is written; rows that move lie at or behind the places they move to)
+  const int first = m.z >= 0 ? kKv8Block : at, count = at + kept - first, to = m.z >= 0 ? 0 : at;
+  for (int u = threadIdx.x; u < 2 * D; u += kThreads) {
+    uint16_t* x = u < D ? tail + u : tail + (size_t)kKv8Tail * D + (size_t)(u - D) * kKv8Tail;
+    const int step = u < D ? D : 1;
+    uint16_t y[WOQ_KV8_ROWS];
+#pragma unroll
+    for (int j = 0; j < WOQ_KV8_ROWS; ++j)
+      if (j < count) y[j] = x[kept_row(first + j, at, keep) * step];
+#pragma unroll
+    for (int j = 0; j < WOQ_KV8_ROWS; ++j)
+      if (j < count) x[(to + j) * step] = y[j];
   }
 }
 
@@ -409,23 +589,14 @@ __global__ void __launch_bounds__(kThreads) accept_kernel(const __grid_constant_
 cudaError_t launch_rope_table(double theta, int half, int positions, float* table, cudaStream_t s) {
   const long long n = (long long)half * positions;
   const long long blocks = (n + 255) / 256;
-  kv8::rope_table_kernel<<<(unsigned)(blocks < 4096 ? blocks : 4096), 256, 0, s>>>(theta, half, positions,
-                                                                                  reinterpret_cast<float2*>(table));
-  return cudaGetLastError();
+  return kv8::launch(kv8::rope_table_kernel, (unsigned)(blocks < 4096 ? blocks : 4096), 256, 0, s, theta, half, positions,
+                     reinterpret_cast<float2*>(table));
 }
 
 cudaError_t launch_kv8_append_rows(const Kv8Append& p, cudaStream_t s) {
   const long long units = (long long)p.n * p.rows * (p.q_heads + p.v.heads);
-  cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3((unsigned)((units + kv8::kWarps - 1) / kv8::kWarps));
-  lc.blockDim = dim3(kv8::kThreads);
-  lc.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  lc.attrs = attr;
-  lc.numAttrs = 1;
-  return p.f32 ? cudaLaunchKernelEx(&lc, kv8::rows_kernel<true>, p) : cudaLaunchKernelEx(&lc, kv8::rows_kernel<false>, p);
+  const unsigned blocks = (unsigned)((units + kv8::kWarps - 1) / kv8::kWarps);
+  return kv8::launch(p.f32 ? kv8::rows_kernel<true> : kv8::rows_kernel<false>, blocks, kv8::kThreads, 0, s, p);
 }
 
 // The tiles of a block take 256 D bytes: above 48 KB the kernel's limit is raised (head_dim 256).
@@ -435,30 +606,28 @@ static cudaError_t allow_tiles(K kernel, int bytes) {
                            : cudaSuccess;
 }
 
-cudaError_t launch_kv8_prompt(const Kv8Append& p, cudaStream_t s) {
+template <bool F32, bool VEC>
+static cudaError_t launch_prompt(const Kv8Append& p, cudaStream_t s) {
   const int smem = 256 * p.v.dim;
   const dim3 grid((unsigned)((p.rows - 1) / kKv8Block + 2), (unsigned)p.v.heads);
-  cudaError_t e;
-  if (p.f32) {
-    if ((e = allow_tiles(kv8::prompt_kv_kernel<true>, smem)) != cudaSuccess) return e;
-    kv8::prompt_kv_kernel<true><<<grid, kv8::kThreads, smem, s>>>(p);
-  } else {
-    if ((e = allow_tiles(kv8::prompt_kv_kernel<false>, smem)) != cudaSuccess) return e;
-    kv8::prompt_kv_kernel<false><<<grid, kv8::kThreads, smem, s>>>(p);
-  }
-  if ((e = cudaGetLastError()) != cudaSuccess || p.q_heads == 0) return e;
+  cudaError_t e = allow_tiles(kv8::prompt_kv_kernel<F32, VEC>, smem);
+  if (e != cudaSuccess) return e;
+  e = kv8::launch(kv8::prompt_kv_kernel<F32, VEC>, grid, kv8::kThreads, smem, s, p);
+  if (e != cudaSuccess || p.q_heads == 0) return e;
   const unsigned blocks = (unsigned)((p.rows + kv8::kWarps - 1) / kv8::kWarps);
-  if (p.f32) kv8::prompt_q_kernel<true><<<blocks, kv8::kThreads, 0, s>>>(p);
-  else kv8::prompt_q_kernel<false><<<blocks, kv8::kThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  return kv8::launch(kv8::prompt_q_kernel<F32, VEC>, blocks, kv8::kThreads, 0, s, p);
+}
+
+cudaError_t launch_kv8_prompt(const Kv8Append& p, cudaStream_t s) {
+  if (p.rope.half * 2 == p.v.dim) return p.f32 ? launch_prompt<true, true>(p, s) : launch_prompt<false, true>(p, s);
+  return p.f32 ? launch_prompt<true, false>(p, s) : launch_prompt<false, false>(p, s);
 }
 
 cudaError_t launch_kv8_accept_rows(const Kv8View& v, int n, cudaStream_t s) {
   const int smem = 256 * v.dim;
   const cudaError_t e = allow_tiles(kv8::accept_kernel, smem);
   if (e != cudaSuccess) return e;
-  kv8::accept_kernel<<<dim3((unsigned)n, (unsigned)v.heads, (unsigned)v.layers), kv8::kThreads, smem, s>>>(v);
-  return cudaGetLastError();
+  return kv8::launch(kv8::accept_kernel, dim3((unsigned)n, (unsigned)v.heads, (unsigned)v.layers), kv8::kThreads, smem, s, v);
 }
 
 }  // namespace woq

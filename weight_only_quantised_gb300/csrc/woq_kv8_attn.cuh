@@ -7,11 +7,14 @@
 // tensor cores do in that time for up to 16 queries (mma.sync m16n8k16 f16 with fp32 sums runs at
 // about 512 multiply-adds a clock and SM here; 16 queries need 440 at the copy peak).
 //
-// Split: the (entry, kv head) items are laid end to end, each as its blocks and one unit for its
-// tail, and every CTA takes an equal share of the units (one CTA per SM; fewer CTAs while a share
-// would be below least_units), so the load is even whatever the lengths are.  Lengths are read on the
-// device.  An item that lies in several CTAs leaves fp32 partials (maximum, sum, weighted values);
-// the CTA that counts in last joins them in CTA order, so the result does not depend on the run.
+// Split: an item (entry, kv head) is its blocks and one unit for its tail.  With at most as many items
+// as CTAs (one CTA per SM) every item is cut into equal pieces, one piece per CTA, the longer items
+// into more; a CTA that held the end of one item and the beginning of another would wait twice for
+// the tail, the joining of its warps and the counting in (131,071 tokens, 8 heads: 62 us against 5x).
+// Items of up to kWhole units stay whole: joining partials costs as much as those blocks.  With more items the
+// units are laid end to end and every CTA takes an equal share.  Lengths are read on the device, so
+// this plan is made there.  An item in several CTAs leaves fp32 partials (maximum, sum, weighted
+// values); the CTA that counts in last joins them in CTA order, so the result does not depend on the run.
 //
 // CTA: one producer warp copies whole records (16 KB at D = 128, one bulk copy each) into a ring;
 // each consumer warp takes whole blocks by itself (always from the same stages, in order), with its own running
@@ -411,9 +414,15 @@ __host__ __device__ constexpr int max_warps(int tiles) { return tiles == 1 ? 7 :
 struct Misc {
   uint64_t full[kMaxStages], empty[kMaxStages];
   int fail, last;
-  int entries[];  // [n + 1] units of one head of the entries before, [n] lengths (-1: out of range)
+  int share;      // units of a piece, 0: more items than CTAs
+  // [n + 1] units of one head of the entries before, [n] lengths (-1: out of range), [n + 1] pieces (CTAs) of
+  // the entries before
+  int entries[];
 };
-__host__ __device__ inline int misc_bytes(int n) { return (int)((sizeof(Misc) + (size_t)(2 * n + 1) * 4 + 127) / 128 * 128); }
+__host__ __device__ inline int misc_bytes(int n) { return (int)((sizeof(Misc) + (size_t)(3 * n + 2) * 4 + 127) / 128 * 128); }
+constexpr int kWhole = 24;  // units of an item that is not cut
+
+__device__ __forceinline__ int pieces_of(int units, int share) { return units <= kWhole ? 1 : (units + share - 1) / share; }
 __host__ __device__ inline int merge_bytes(int warps, int qt, int dim) {
   return (warps * 8 * qt * (dim + kMergePad + 2) * 4 + 127) / 128 * 128;
 }
@@ -430,6 +439,7 @@ __global__ void __launch_bounds__(32 * (max_warps(QT) + 1), 1) attn_kernel(const
   Misc& misc = *reinterpret_cast<Misc*>(smem);
   int* prefix = misc.entries;
   int* lens = prefix + p.n + 1;
+  int* cuts = lens + p.n;
   const Kv8View& v = p.v;
   const int W = p.warps, G = p.query_groups, WG = W / G, S = p.stages;
   const int R = p.rows * p.group;
@@ -448,8 +458,7 @@ __global__ void __launch_bounds__(32 * (max_warps(QT) + 1), 1) attn_kernel(const
     misc.fail = 0;
     dev::fence_mbar_init();
   }
-  dev::pdl_wait_prior_grids();
-  dev::pdl_launch_dependents();
+  begin_after_prior();
   // lengths and units of the entries (the header's check is read beside them, not before)
   const uint4 header = *reinterpret_cast<const uint4*>(v.base);
   const bool ours = header.y == kKv8Magic && header.z == v.hash;
@@ -475,17 +484,62 @@ __global__ void __launch_bounds__(32 * (max_warps(QT) + 1), 1) attn_kernel(const
       run += __shfl_sync(~0u, y, 31);
     }
     if (lane == 0) prefix[p.n] = run;
+    // the least share with which all pieces have a CTA
+    int share = 0;
+    if (p.n * v.heads <= (int)gridDim.x) {
+      __syncwarp();
+      const int room = (int)gridDim.x / v.heads;  // pieces of one head
+      share = max(p.least_units, (run + room - 1) / room);
+      for (;;) {
+        int total = 0;
+        for (int e0 = 0; e0 < p.n; e0 += 32) {
+          const int e = e0 + lane;
+          int y = e < p.n ? pieces_of(prefix[e + 1] - prefix[e], share) : 0;
+          const int own = y;
+#pragma unroll
+          for (int d = 1; d < 32; d <<= 1) {
+            const int z = __shfl_up_sync(~0u, y, d);
+            if (lane >= d) y += z;
+          }
+          if (e < p.n) cuts[e] = (total + y - own) * v.heads;
+          total += __shfl_sync(~0u, y, 31);
+        }
+        if (lane == 0) cuts[p.n] = total * v.heads;
+        if (total <= room) break;
+        share += share / 8 + 1;  // ends: with a share beyond the longest item there are n <= room pieces
+      }
+    }
+    if (lane == 0) misc.share = share;
   }
   if (!ours) {
     if (header.y == kKv8Magic && tid == 0) flag(v, WOQ_DEVERR_HEADER);
     return;
   }
   __syncthreads();
-  // this CTA's units: `share` of them (the last may have fewer); all counts fit 32 bits (checked on the host)
-  const int units = prefix[p.n] * v.heads;
-  const int share = max(p.least_units, (units + (int)gridDim.x - 1) / (int)gridDim.x);
-  const int begin = (int)blockIdx.x * share, end = min(begin + share, units);
-  if (begin >= units) return;
+  // this CTA's units [begin, end), of all items laid end to end; all counts fit 32 bits (checked on the host)
+  const bool cut = misc.share > 0;
+  int begin, end, share, piece0 = 0, pieces = 0;  // cut: the item's first CTA and their number; else: units of a CTA
+  if (cut) {
+    if ((int)blockIdx.x >= cuts[p.n]) return;
+    int lo = 0, hi = p.n - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (cuts[mid] <= (int)blockIdx.x) lo = mid; else hi = mid - 1;
+    }
+    const int per = prefix[lo + 1] - prefix[lo];
+    pieces = (cuts[lo + 1] - cuts[lo]) / v.heads;
+    const int head = ((int)blockIdx.x - cuts[lo]) / pieces, j = ((int)blockIdx.x - cuts[lo]) % pieces;
+    piece0 = (int)blockIdx.x - j;
+    share = 0;
+    begin = prefix[lo] * v.heads + head * per + (int)((long long)per * j / pieces);
+    end = prefix[lo] * v.heads + head * per + (int)((long long)per * (j + 1) / pieces);
+  } else {
+    const int units = prefix[p.n] * v.heads;
+    share = max(p.least_units, (units + (int)gridDim.x - 1) / (int)gridDim.x);
+    begin = (int)blockIdx.x * share;
+    end = min(begin + share, units);
+    if (begin >= units) return;
+  }
 
   // the item that holds unit u: entry, head, first unit
   auto locate = [&](int u, int* entry, int* head, int* item_begin) {
@@ -648,7 +702,7 @@ __global__ void __launch_bounds__(32 * (max_warps(QT) + 1), 1) attn_kernel(const
       return;
     }
     const bool whole = u == ib && stop == ib + per;
-    const int mine = ib <= begin ? 0 : 1;  // partial slots: the item that holds the share's first unit, and the other
+    const int mine = ib <= begin || cut ? 0 : 1;  // partial slots: the item that holds the share's first unit, and the other
     float* part = p.parts + ((size_t)blockIdx.x * 2 + mine) * R * (D + 2);
     uint16_t* out0 = p.out + ((size_t)e * p.rows * p.q_heads + (size_t)head * p.group) * D;
     for (int x = tid; x < R * (D / 4); x += consumers) {
@@ -688,7 +742,7 @@ __global__ void __launch_bounds__(32 * (max_warps(QT) + 1), 1) attn_kernel(const
     }
     if (!whole) {
       // CTAs c0 .. c1 share the item; the one that counts in last joins their partials in CTA order
-      const int c0 = ib / share, c1 = (ib + per - 1) / share;
+      const int c0 = cut ? piece0 : ib / share, c1 = cut ? piece0 + pieces - 1 : (ib + per - 1) / share;
       dev::named_barrier_sync(1, consumers);
       uint32_t* ticket = p.tickets + (size_t)e * v.heads + head;
       if (tid == 0) misc.last = dev::atomic_add_acq_rel_gpu(ticket, 1u) == (uint32_t)(c1 - c0);
@@ -698,7 +752,7 @@ __global__ void __launch_bounds__(32 * (max_warps(QT) + 1), 1) attn_kernel(const
         // The item is the first of each CTA's slots but perhaps of c0's, where it may be the second.
         const size_t step = (size_t)2 * R * (D + 2);
         const float* parts = p.parts + (size_t)c0 * step;
-        const size_t first = ib > c0 * share ? step / 2 : 0;
+        const size_t first = !cut && ib > c0 * share ? step / 2 : 0;
         const int np = c1 - c0 + 1;
         for (int n = warp; n < R; n += W) {
           const float* at = parts + (size_t)n * (D + 2);
@@ -760,17 +814,7 @@ cudaError_t launch_attn(const Kv8Attn& p, int ctas, int smem, cudaStream_t strea
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit);
   }
-  cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3((unsigned)ctas);
-  lc.blockDim = dim3((unsigned)(p.warps + 1) * 32);
-  lc.dynamicSmemBytes = (size_t)smem;
-  lc.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  lc.attrs = attr;
-  lc.numAttrs = 1;
-  return cudaLaunchKernelEx(&lc, kernel, p);
+  return launch(kernel, dim3((unsigned)ctas), (p.warps + 1) * 32, (size_t)smem, stream, p);
 }
 
 }  // namespace kv8

@@ -11,6 +11,30 @@
 namespace woq {
 namespace kv8 {
 
+// Every kernel of the cache is launched with programmatic dependent launch and begins with this: it may be
+// scheduled while the kernel before it ends, reads and writes nothing until that one has completed, and only then
+// lets its own successor be scheduled (in that order: a linear reads its weights before its own wait, so
+// whoever wrote them must be complete by the time this kernel lets it start).
+__device__ __forceinline__ void begin_after_prior() {
+  dev::pdl_wait_prior_grids();
+  dev::pdl_launch_dependents();
+}
+
+template <class... P, class... A>
+inline cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A&&... args) {
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = grid;
+  lc.blockDim = dim3((unsigned)threads);
+  lc.dynamicSmemBytes = smem;
+  lc.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  return cudaLaunchKernelEx(&lc, kernel, P(args)...);
+}
+
 __device__ __forceinline__ void flag(const Kv8View& v, uint32_t bits) { atomicOr(v.status(), bits); }
 
 // Whether the buffer is a cache of this config.  A cache of another config gets the status bit;

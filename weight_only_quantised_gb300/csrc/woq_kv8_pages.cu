@@ -64,6 +64,7 @@ __device__ __forceinline__ bool mark(MetaShared& sh, int seq) {
 __device__ __forceinline__ bool in_range(const Kv8View& v, int seq) { return seq >= 0 && seq < v.seqs; }
 
 __global__ void __launch_bounds__(256) init_kernel(Kv8View v) {
+  begin_after_prior();
   if (threadIdx.x == 0) {
     uint32_t* h = v.status();
     h[0] = 0;
@@ -75,6 +76,7 @@ __global__ void __launch_bounds__(256) init_kernel(Kv8View v) {
 
 __global__ void __launch_bounds__(kMetaThreads) extend_kernel(Kv8View v, int seq, int tokens) {
   __shared__ MetaShared sh;
+  begin_after_prior();
   if (!header_ok(v)) return;
   const int len = v.lens_p()[seq];
   bool ok = true;
@@ -109,6 +111,7 @@ __global__ void __launch_bounds__(kMetaThreads) extend_kernel(Kv8View v, int seq
 __global__ void __launch_bounds__(kMetaThreads)
     accept_meta_kernel(Kv8View v, const int32_t* seqs, int n, const uint32_t* keep) {
   __shared__ MetaShared sh;
+  begin_after_prior();
   if (!header_ok(v)) return;
   clear_used(sh);
   const int e = threadIdx.x;
@@ -179,6 +182,7 @@ __device__ __forceinline__ bool check_pairs(const Kv8View& sv, const Kv8View& dv
 __global__ void __launch_bounds__(kMetaThreads)
     fork_meta_kernel(Kv8View v, const int32_t* src, const int32_t* dst, int n) {
   __shared__ MetaShared sh;
+  begin_after_prior();
   if (!header_ok(v)) return;
   int s = 0, d = 0, len = 0;
   const bool ok = check_pairs(v, v, src, dst, n, true, sh, &s, &d, &len);
@@ -198,6 +202,7 @@ __global__ void __launch_bounds__(kMetaThreads)
     copy_meta_kernel(Kv8View sv, Kv8View dv, const int32_t* src, const int32_t* dst, int n, int same) {
   __shared__ MetaShared sh;
   __shared__ int offs[kKv8MaxSeqs + 1];
+  begin_after_prior();
   if (!header_ok(dv)) return;
   const uint4 hs = *reinterpret_cast<const uint4*>(sv.base);
   int s = 0, d = 0, len = 0;
@@ -247,6 +252,7 @@ __global__ void __launch_bounds__(kMetaThreads)
 
 __global__ void __launch_bounds__(kMetaThreads) free_kernel(Kv8View v, const int32_t* seqs, int n) {
   __shared__ MetaShared sh;
+  begin_after_prior();
   if (!header_ok(v)) return;
   clear_used(sh);
   const int e = threadIdx.x;
@@ -270,6 +276,7 @@ __global__ void __launch_bounds__(kMetaThreads) free_kernel(Kv8View v, const int
 
 __global__ void __launch_bounds__(kMetaThreads) compact_meta_kernel(Kv8View v, int limit) {
   __shared__ MetaShared sh;
+  begin_after_prior();
   if (!header_ok(v)) return;
   int32_t* refs = v.refs_p();
   int need = 0;
@@ -306,6 +313,7 @@ __global__ void __launch_bounds__(kMetaThreads) compact_meta_kernel(Kv8View v, i
 // Table entries of moved pages after compact_meta_kernel (a page at or above the limit that a
 // sequence holds has just been moved).
 __global__ void __launch_bounds__(256) remap_kernel(Kv8View v, int limit) {
+  begin_after_prior();
   if (!header_ok(v) || v.pairs_p()[0] == 0) return;
   for (int seq = blockIdx.y; seq < v.seqs; seq += gridDim.y) {
     const int blocks = v.lens_p()[seq] / kKv8Block;
@@ -320,6 +328,7 @@ constexpr int kCopyVecs = 4 * kCopyThreads;  // 16-byte vectors of one segment
 
 // Copies the pages of pairs[]: {page of sv, page of dv}.
 __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(Kv8View sv, Kv8View dv) {
+  begin_after_prior();
   if (!header_ok(dv)) return;
   const int count = dv.pairs_p()[0];
   const int2* pairs = reinterpret_cast<const int2*>(dv.pairs_p()) + 1;
@@ -343,13 +352,22 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(Kv8View sv, Kv
 // Tails of moves[]: grid (entries, heads, layers).  share: the page-table row of the source too, and
 // a reference on each of its pages (fork).
 __global__ void __launch_bounds__(256) copy_tails_kernel(Kv8View sv, Kv8View dv, int share) {
+  begin_after_prior();
   if (!header_ok(dv)) return;
   const int4 m = dv.moves_p()[blockIdx.x];
   if (!m.z) return;
-  const uint4* from = reinterpret_cast<const uint4*>(sv.tail(blockIdx.z, m.x, blockIdx.y));
-  uint4* to = reinterpret_cast<uint4*>(dv.tail(blockIdx.z, m.y, blockIdx.y));
-  const int vecs = (int)(dv.tail_elems() / 8);
-  for (int i = threadIdx.x; i < vecs; i += blockDim.x) to[i] = from[i];
+  const uint16_t* from = sv.tail(blockIdx.z, m.x, blockIdx.y);
+  uint16_t* to = dv.tail(blockIdx.z, m.y, blockIdx.y);
+  // the tokens and the draft rows behind them: so many rows of keys, and octets of the values' rows
+  const int D = dv.dim, rows = dv.lens_p()[m.y] % kKv8Block + WOQ_KV8_ROWS, octets = (rows + 7) / 8;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < rows * (D / 8); i += blockDim.x)
+    reinterpret_cast<uint4*>(to)[i] = reinterpret_cast<const uint4*>(from)[i];
+#pragma unroll 4
+  for (int i = threadIdx.x; i < octets * D; i += blockDim.x) {
+    const int at = kKv8Tail * D + (i / octets) * kKv8Tail + (i % octets) * 8;
+    *reinterpret_cast<uint4*>(to + at) = *reinterpret_cast<const uint4*>(from + at);
+  }
   if (share && blockIdx.y == 0 && blockIdx.z == 0) {
     for (int b = threadIdx.x; b < m.w; b += blockDim.x) {
       const int page = sv.table_row(m.x)[b];
@@ -416,6 +434,7 @@ __device__ void read_record(const Kv8View& v, const uint8_t* rec, uint32_t* smem
 __global__ void __launch_bounds__(256)
     read_kernel(Kv8View v, int layer, int seq, int first, int count, uint16_t* k, uint16_t* vals) {
   __shared__ uint32_t smem[64 * 256 / 128 * 33];
+  begin_after_prior();
   if (!header_ok(v)) return;
   const int len = v.lens_p()[seq];
   if ((long long)first + count > (long long)len + WOQ_KV8_ROWS) {
@@ -437,10 +456,29 @@ __global__ void __launch_bounds__(256)
   const uint16_t* tail = v.tail(l, seq, head);
   const int t0 = b * kKv8Block > first ? b * kKv8Block : first;
   const int t1 = (b + 1) * kKv8Block < first + count ? (b + 1) * kKv8Block : first + count;
-  for (int u = threadIdx.x; u < (t1 - t0) * D; u += blockDim.x) {
-    const int tok = t0 + u / D, d = u % D, r = tok - full * kKv8Block;  // r < 72: checked above
-    k[(size_t)(tok - first) * row + d] = tail[(size_t)r * D + d];
-    vals[(size_t)(tok - first) * row + d] = tail[(size_t)kKv8Tail * D + (size_t)d * kKv8Tail + r];
+  const int shift = full * kKv8Block;  // tail rows are token - shift, below 72 (checked above)
+#pragma unroll 2
+  for (int u = threadIdx.x; u < (t1 - t0) * (D / 8); u += blockDim.x) {
+    const int tok = t0 + u / (D / 8), d = (u % (D / 8)) * 8;
+    *reinterpret_cast<uint4*>(k + (size_t)(tok - first) * row + d) =
+        *reinterpret_cast<const uint4*>(tail + (size_t)(tok - shift) * D + d);
+  }
+  // values: eight tokens of two elements, then a pair for each token
+  const int o0 = (t0 - shift) / 8, octets = (t1 - shift + 7) / 8 - o0;
+  const uint16_t* tv = tail + (size_t)kKv8Tail * D;
+#pragma unroll 2
+  for (int u = threadIdx.x; u < octets * (D / 2); u += blockDim.x) {
+    const int d = (u % (D / 2)) * 2, r = (o0 + u / (D / 2)) * 8;
+    const uint4 a = *reinterpret_cast<const uint4*>(tv + (size_t)d * kKv8Tail + r);
+    const uint4 b = *reinterpret_cast<const uint4*>(tv + (size_t)(d + 1) * kKv8Tail + r);
+    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int tok = shift + r + i;
+      if (tok >= t0 && tok < t1)
+        *reinterpret_cast<uint32_t*>(vals + (size_t)(tok - first) * row + d) =
+            __byte_perm(x[i >> 1], y[i >> 1], (i & 1) ? 0x7632 : 0x5410);
+    }
   }
 }
 
@@ -449,23 +487,19 @@ __global__ void __launch_bounds__(256)
 cudaError_t launch_kv8_init(const Kv8View& v, cudaStream_t s) {
   const cudaError_t e = cudaMemsetAsync(v.base, 0, v.pool, s);
   if (e != cudaSuccess) return e;
-  kv8::init_kernel<<<1, 32, 0, s>>>(v);
-  return cudaGetLastError();
+  return kv8::launch(kv8::init_kernel, 1, 32, 0, s, v);
 }
 
 cudaError_t launch_kv8_extend(const Kv8View& v, int seq, int tokens, cudaStream_t s) {
-  kv8::extend_kernel<<<1, kv8::kMetaThreads, 0, s>>>(v, seq, tokens);
-  return cudaGetLastError();
+  return kv8::launch(kv8::extend_kernel, 1, kv8::kMetaThreads, 0, s, v, seq, tokens);
 }
 
 cudaError_t launch_kv8_accept_meta(const Kv8View& v, const int32_t* seqs, int n, const uint32_t* keep, cudaStream_t s) {
-  kv8::accept_meta_kernel<<<1, kv8::kMetaThreads, 0, s>>>(v, seqs, n, keep);
-  return cudaGetLastError();
+  return kv8::launch(kv8::accept_meta_kernel, 1, kv8::kMetaThreads, 0, s, v, seqs, n, keep);
 }
 
 cudaError_t launch_kv8_free(const Kv8View& v, const int32_t* seqs, int n, cudaStream_t s) {
-  kv8::free_kernel<<<1, kv8::kMetaThreads, 0, s>>>(v, seqs, n);
-  return cudaGetLastError();
+  return kv8::launch(kv8::free_kernel, 1, kv8::kMetaThreads, 0, s, v, seqs, n);
 }
 
 static dim3 per_tail(const Kv8View& v, int n) { return dim3((unsigned)n, (unsigned)v.heads, (unsigned)v.layers); }
@@ -473,36 +507,34 @@ static dim3 per_tail(const Kv8View& v, int n) { return dim3((unsigned)n, (unsign
 static cudaError_t copy_pages(const Kv8View& src, const Kv8View& dst, cudaStream_t s) {
   const int sms = sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  kv8::copy_pages_kernel<<<8 * sms, kv8::kCopyThreads, 0, s>>>(src, dst);
-  return cudaGetLastError();
+  return kv8::launch(kv8::copy_pages_kernel, 8 * sms, kv8::kCopyThreads, 0, s, src, dst);
 }
 
 cudaError_t launch_kv8_fork(const Kv8View& v, const int32_t* src, const int32_t* dst, int n, cudaStream_t s) {
-  kv8::fork_meta_kernel<<<1, kv8::kMetaThreads, 0, s>>>(v, src, dst, n);
-  kv8::copy_tails_kernel<<<per_tail(v, n), 256, 0, s>>>(v, v, 1);
-  return cudaGetLastError();
+  const cudaError_t e = kv8::launch(kv8::fork_meta_kernel, 1, kv8::kMetaThreads, 0, s, v, src, dst, n);
+  return e != cudaSuccess ? e : kv8::launch(kv8::copy_tails_kernel, per_tail(v, n), 256, 0, s, v, v, 1);
 }
 
 cudaError_t launch_kv8_copy(const Kv8View& src, const Kv8View& dst, const int32_t* src_seqs, const int32_t* dst_seqs,
                             int n, cudaStream_t s) {
-  kv8::copy_meta_kernel<<<1, kv8::kMetaThreads, 0, s>>>(src, dst, src_seqs, dst_seqs, n, src.base == dst.base);
-  kv8::copy_tails_kernel<<<per_tail(dst, n), 256, 0, s>>>(src, dst, 0);
-  return copy_pages(src, dst, s);
+  const int same = src.base == dst.base;
+  cudaError_t e = kv8::launch(kv8::copy_meta_kernel, 1, kv8::kMetaThreads, 0, s, src, dst, src_seqs, dst_seqs, n, same);
+  if (e == cudaSuccess) e = kv8::launch(kv8::copy_tails_kernel, per_tail(dst, n), 256, 0, s, src, dst, 0);
+  return e != cudaSuccess ? e : copy_pages(src, dst, s);
 }
 
 cudaError_t launch_kv8_compact(const Kv8View& v, int limit, cudaStream_t s) {
-  kv8::compact_meta_kernel<<<1, kv8::kMetaThreads, 0, s>>>(v, limit);
-  const int rows = v.seqs < 256 ? v.seqs : 256;
-  kv8::remap_kernel<<<dim3(8, (unsigned)rows), 256, 0, s>>>(v, limit);
-  return copy_pages(v, v, s);
+  cudaError_t e = kv8::launch(kv8::compact_meta_kernel, 1, kv8::kMetaThreads, 0, s, v, limit);
+  const dim3 grid(8, (unsigned)(v.seqs < 256 ? v.seqs : 256));
+  if (e == cudaSuccess) e = kv8::launch(kv8::remap_kernel, grid, 256, 0, s, v, limit);
+  return e != cudaSuccess ? e : copy_pages(v, v, s);
 }
 
 cudaError_t launch_kv8_read(const Kv8View& v, int layer, int layers, int seq, int first, int count, uint16_t* k,
                             uint16_t* vals, cudaStream_t s) {
   const int blocks = (first + count - 1) / kKv8Block - first / kKv8Block + 1;
-  kv8::read_kernel<<<dim3((unsigned)blocks, (unsigned)v.heads, (unsigned)layers), 256, 0, s>>>(v, layer, seq, first,
-                                                                                              count, k, vals);
-  return cudaGetLastError();
+  const dim3 grid((unsigned)blocks, (unsigned)v.heads, (unsigned)layers);
+  return kv8::launch(kv8::read_kernel, grid, 256, 0, s, v, layer, seq, first, count, k, vals);
 }
 
 }  // namespace woq
