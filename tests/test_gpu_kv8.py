@@ -255,7 +255,8 @@ def test_rows_and_groups(fmt, rows, group):
     c.attend([0], rows, group, g)
 
 
-@pytest.mark.parametrize("dim,rows,group", [(64, 8, 16), (64, 2, 7), (256, 8, 7), (256, 3, 4), (256, 5, 5)])
+@pytest.mark.parametrize("dim,rows,group", [(64, 8, 16), (64, 2, 7), (64, 6, 4), (64, 7, 4), (64, 8, 5), (256, 8, 7), (256, 3, 4),
+                                            (256, 5, 5)])
 def test_rows_and_groups_of_other_heads(dim, rows, group):
     c = Cache(fmt=rows % 2, dim=dim, heads=1)
     g = gen(rows * 31 + group)
@@ -295,6 +296,7 @@ def test_window_and_sinks(fmt, window, sinks):
     for s, n in enumerate(lens):
         c.prompt(s, g, n)
     c.draft([0, 1, 2, 3], g, 4)
+    c.attend([0, 1, 2, 3], 4, 2, g, window=window, sinks=sinks)
     c.attend([0, 1, 2, 3], 4, 3, g, window=window, sinks=sinks)
     c.attend([3, 0], 4, 3, g, window=window, sinks=sinks, vis=[[1, 3, 5, 0], [8, 9, 15, 2]])
 
@@ -311,7 +313,7 @@ def test_unequal_sequences_in_any_order(fmt):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
-@pytest.mark.parametrize("group,rows", [(5, 1), (5, 8)])
+@pytest.mark.parametrize("group,rows", [(5, 1), (4, 3), (5, 4), (5, 8), (7, 8)])
 def test_long_context_over_many_ctas(fmt, group, rows):
     c = Cache(fmt=fmt, heads=8, max_tokens=9000, pages=150)
     g = gen(1)
@@ -320,19 +322,20 @@ def test_long_context_over_many_ctas(fmt, group, rows):
     c.attend([0], rows, group, g)
 
 
-def test_peaked_and_flat_scores():
+@pytest.mark.parametrize("hq", [4, 20, 48])
+def test_peaked_and_flat_scores(hq):
     """One token that outweighs all others far into the sequence, growing scores, and equal scores."""
     c = Cache(heads=1, max_tokens=700)
     g = gen(2)
     k, v = kv(g, 640, 1, 128, 0.3), kv(g, 640, 1, 128)
-    q = torch.ones((1, 4, 128), dtype=torch.bfloat16)
+    q = torch.ones((1, hq, 128), dtype=torch.bfloat16)
     k[500] = 4.0
     k[:, 0, :] += (torch.arange(640) / 200)[:, None].to(torch.bfloat16)
     woq.woq_kv8_extend(c.cfg, c.buf, 0, 640)
     c.fill(0, 0, k, v)
     c.draft([0], g, 1)
     for scale in (1.0, 0.01, 0.0, -1.0):
-        c.attend([0], 1, 4, g, q=q, scale=scale)
+        c.attend([0], 1, hq, g, q=q, scale=scale)
 
 
 @pytest.mark.parametrize("size", [2.0 ** -120, 2.0 ** 60])
@@ -346,7 +349,8 @@ def test_queries_far_from_one(size):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
-def test_values_that_are_not_finite_reach_only_rows_that_see_them(fmt):
+@pytest.mark.parametrize("hq", [2, 5, 9])
+def test_values_that_are_not_finite_reach_only_rows_that_see_them(fmt, hq):
     c = Cache(fmt=fmt, heads=1, max_tokens=400)
     g = gen(5)
     c.prompt(0, g, 190)
@@ -357,12 +361,12 @@ def test_values_that_are_not_finite_reach_only_rows_that_see_them(fmt):
     woq.woq_kv8_append_rows(c.cfg, c.buf, 0, ints([0]), 3, x, 0, None)
     m = c.model[0][0]
     m.pk, m.pv = k, v
-    ws = torch.zeros(woq.woq_kv8_attention_workspace(c.cfg, 1, 4, 2), dtype=torch.uint8, device=DEV)
-    q = torch.randn((4, 2, 128), generator=g).to(torch.bfloat16)
-    out = torch.empty((4, 2, 128), dtype=torch.bfloat16, device=DEV)
+    ws = torch.zeros(woq.woq_kv8_attention_workspace(c.cfg, 1, 4, hq), dtype=torch.uint8, device=DEV)
+    q = torch.randn((4, hq, 128), generator=g).to(torch.bfloat16)
+    out = torch.empty((4, hq, 128), dtype=torch.bfloat16, device=DEV)
 
     def run(vis, window=0, sinks=0):
-        woq.woq_kv8_attention(c.cfg, c.buf, 0, ints([0]), 4, q.to(DEV), 2, out, ws, 0.1, vis=ints([vis]), window=window, sinks=sinks)
+        woq.woq_kv8_attention(c.cfg, c.buf, 0, ints([0]), 4, q.to(DEV), hq, out, ws, 0.1, vis=ints([vis]), window=window, sinks=sinks)
         return out.cpu()
 
     o = run([0b001, 0b011, 0b101, 0])

@@ -115,7 +115,8 @@ size_t attn_parts_offset(const Kv8View& v, int n) { return 256 + ((size_t)n * v.
 
 }  // namespace
 
-// Query tiles per warp: two as soon as there is more than one tile (head_dim 256: always one; its 16
+// A team per block for 2 to 5 tiles of 8 queries (head_dim 64 and 128), else a warp per block.  There query
+// tiles per warp: two as soon as there is more than one tile (head_dim 256: always one; its 16
 // fragments of weighted values take twice the registers).  Warps come in whole groups, as many
 // as leave each warp two stages of the ring at least.
 //
@@ -126,10 +127,23 @@ size_t attn_parts_offset(const Kv8View& v, int n) { return 256 + ((size_t)n * v.
 int kv8_attn_plan(Kv8Attn* p, int smem_max) {
   const int queries = p->rows * p->group, dim = p->v.dim;
   const int tiles = (queries + 7) / 8;
+  p->team = tiles > 1 && tiles <= 5 && dim < 256;
+  p->least_units = 8;
+  const int record = 128 * dim + 16;
+  if (p->team) {
+    p->tiles = tiles;
+    p->query_groups = 4;  // the team's warps all read its blocks
+    p->warps = 4 * kv8::kTeams;
+    const int fixed = kv8::misc_bytes(p->n) + kv8::team_fixed_bytes(tiles, dim);
+    int stages = (smem_max - fixed) / record;
+    stages = (stages < kv8::kMaxStages ? stages : kv8::kMaxStages) / kv8::kTeams * kv8::kTeams;
+    if (stages < 2 * kv8::kTeams) return 0;
+    p->stages = stages;
+    return fixed + stages * record;
+  }
   p->tiles = tiles > 1 && dim < 256 ? 2 : 1;
   p->query_groups = (tiles + p->tiles - 1) / p->tiles;
-  p->least_units = 8;
-  const int record = 128 * dim + 16, most = kv8::max_warps(p->tiles);
+  const int most = kv8::max_warps(p->tiles);
   for (int per = most / p->query_groups; per >= 1; --per) {
     const int warps = per * p->query_groups;
     const int fixed = kv8::misc_bytes(p->n) + kv8::merge_bytes(warps, p->tiles, dim);
@@ -286,8 +300,10 @@ int woq_kv8_attention(const woq_kv8_config* cfg, void* cache, size_t cache_bytes
   p.sinks = sinks;
   const int smem = kv8_attn_plan(&p, smem_max);
   if (smem == 0) return WOQ_ERR_SHAPE;
-  return cuda_result(v.fmt == WOQ_KV8_INT8 ? launch_kv8_attn_int8(p, sms, smem, (cudaStream_t)stream)
-                                           : launch_kv8_attn_e4m3(p, sms, smem, (cudaStream_t)stream));
+  const bool int8 = v.fmt == WOQ_KV8_INT8;
+  const auto launch = p.team ? (int8 ? launch_kv8_team_int8 : launch_kv8_team_e4m3)
+                             : (int8 ? launch_kv8_attn_int8 : launch_kv8_attn_e4m3);
+  return cuda_result(launch(p, sms, smem, (cudaStream_t)stream));
 }
 
 int woq_kv8_fork(const woq_kv8_config* cfg, void* cache, size_t cache_bytes, const int32_t* src, const int32_t* dst,

@@ -260,6 +260,18 @@ __device__ __forceinline__ void block_step(State<D, QT>& st, const uint8_t* rec,
   }
 }
 
+// Whether a row with draft mask vis and window from place `low` sees row r of the tail (in_tail tokens, then drafts).
+__device__ __forceinline__ bool tail_sees(int r, uint32_t vis, int low, int in_tail, int there, int len, int sinks) {
+  if (r >= there) return false;
+  const int draft = r - in_tail;
+  int place = len + draft;
+  if (draft >= 0) {
+    if (!((vis >> draft) & 1u)) return false;
+    place = len + __popc(vis & ((1u << draft) - 1u));
+  }
+  return place < sinks || place >= low;
+}
+
 // Tail tile i: i < 4: tokens 16 t' + 4 i + {0 .. 3} of the tail (t' = 0 .. 3), in the order of the
 // key rows of a block; i = 4: tail rows 64 .. 71.  there: rows of the tail that anything may be seen of.
 template <int D, int QT>
@@ -318,24 +330,14 @@ __device__ __forceinline__ void tail_step(State<D, QT>& st, const uint16_t* tail
       }
     }
   }
-  // whether the column's row sees tail row r
-  auto sees = [&](int r, uint32_t vis, int low) {
-    if (r >= there) return false;
-    const int draft = r - in_tail;
-    int place = len + draft;
-    if (draft >= 0) {
-      if (!((vis >> draft) & 1u)) return false;
-      place = len + __popc(vis & ((1u << draft) - 1u));
-    }
-    return place < sinks || place >= low;
-  };
   float mx[QT][2];
 #pragma unroll
   for (int q = 0; q < QT; ++q) {
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      s[q][c] = sees(r0, col.vis[q][c], col.low[q][c]) ? s[q][c] * scale_log2 : -INFINITY;
-      s[q][2 + c] = sees(r1, col.vis[q][c], col.low[q][c]) ? s[q][2 + c] * scale_log2 : -INFINITY;
+      s[q][c] = tail_sees(r0, col.vis[q][c], col.low[q][c], in_tail, there, len, sinks) ? s[q][c] * scale_log2 : -INFINITY;
+      s[q][2 + c] =
+          tail_sees(r1, col.vis[q][c], col.low[q][c], in_tail, there, len, sinks) ? s[q][2 + c] * scale_log2 : -INFINITY;
       mx[q][c] = column_max(fmaxf(s[q][c], s[q][2 + c]));
     }
   }
@@ -433,31 +435,22 @@ __device__ __forceinline__ float part_factor(float pm, float pl, float m) {
   return pm == -INFINITY ? (pl == 0.0f ? 0.0f : 1.0f) : exp2_approx(pm - m);
 }
 
-template <int FMT, int D, int QT>
-__global__ void __launch_bounds__(32 * (max_warps(QT) + 1), 1) attn_kernel(const __grid_constant__ Kv8Attn p) {
-  extern __shared__ __align__(128) uint8_t smem[];
-  Misc& misc = *reinterpret_cast<Misc*>(smem);
-  int* prefix = misc.entries;
-  int* lens = prefix + p.n + 1;
-  int* cuts = lens + p.n;
-  const Kv8View& v = p.v;
-  const int W = p.warps, G = p.query_groups, WG = W / G, S = p.stages;
-  const int R = p.rows * p.group;
-  constexpr int kRecord = 128 * D + 16;
-  constexpr int kRow = D + kMergePad;
-  float* merge = reinterpret_cast<float*>(smem + misc_bytes(p.n));  // [W][8 QT][D + pad]
-  float* warp_ml = merge + (size_t)W * 8 * QT * kRow;               // [W][8 QT][2]
-  uint8_t* ring = smem + misc_bytes(p.n) + merge_bytes(W, QT, D);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+__device__ __forceinline__ int* lens_of(const Kv8Attn& p, Misc& misc) { return misc.entries + p.n + 1; }
 
-  if (tid == 0) {
-    for (int i = 0; i < S; ++i) {
-      dev::mbar_init(&misc.full[i], 1);
-      dev::mbar_init(&misc.empty[i], (uint32_t)G);
-    }
-    misc.fail = 0;
-    dev::fence_mbar_init();
-  }
+// This CTA's units [begin, end), of all items laid end to end.  All counts fit 32 bits (checked on the host).
+struct Plan {
+  int begin, end;
+  bool cut;            // pieces of items, one per CTA
+  int piece0, pieces;  // cut: the item's first CTA and their number
+  int share;           // else: units of a CTA
+};
+
+// Waits for the prior grid, reads the lengths and finds this CTA's share; false: nothing to do.  All threads.
+__device__ __forceinline__ bool make_plan(const Kv8Attn& p, Misc& misc, int tid, Plan& pl) {
+  const Kv8View& v = p.v;
+  const int lane = tid & 31, warp = tid >> 5;
+  int* lens = lens_of(p, misc);
+  int* cuts = lens + p.n;
   begin_after_prior();
   // lengths and units of the entries (the header's check is read beside them, not before)
   const uint4 header = *reinterpret_cast<const uint4*>(v.base);
@@ -480,13 +473,13 @@ __global__ void __launch_bounds__(32 * (max_warps(QT) + 1), 1) attn_kernel(const
         const int z = __shfl_up_sync(~0u, y, d);
         if (lane >= d) y += z;
       }
-      if (e < p.n) prefix[e] = run + y - units;
+      if (e < p.n) misc.entries[e] = run + y - units;
       run += __shfl_sync(~0u, y, 31);
     }
-    if (lane == 0) prefix[p.n] = run;
+    if (lane == 0) misc.entries[p.n] = run;
     // the least share with which all pieces have a CTA
     int share = 0;
-    if (p.n * v.heads <= (int)gridDim.x) {
+    if (ours && p.n * v.heads <= (int)gridDim.x) {
       __syncwarp();
       const int room = (int)gridDim.x / v.heads;  // pieces of one head
       share = max(p.least_units, (run + room - 1) / room);
@@ -494,7 +487,7 @@ __global__ void __launch_bounds__(32 * (max_warps(QT) + 1), 1) attn_kernel(const
         int total = 0;
         for (int e0 = 0; e0 < p.n; e0 += 32) {
           const int e = e0 + lane;
-          int y = e < p.n ? pieces_of(prefix[e + 1] - prefix[e], share) : 0;
+          int y = e < p.n ? pieces_of(misc.entries[e + 1] - misc.entries[e], share) : 0;
           const int own = y;
 #pragma unroll
           for (int d = 1; d < 32; d <<= 1) {
@@ -513,89 +506,229 @@ __global__ void __launch_bounds__(32 * (max_warps(QT) + 1), 1) attn_kernel(const
   }
   if (!ours) {
     if (header.y == kKv8Magic && tid == 0) flag(v, WOQ_DEVERR_HEADER);
-    return;
+    return false;
   }
   __syncthreads();
   // this CTA's units [begin, end), of all items laid end to end; all counts fit 32 bits (checked on the host)
   const bool cut = misc.share > 0;
-  int begin, end, share, piece0 = 0, pieces = 0;  // cut: the item's first CTA and their number; else: units of a CTA
+  int begin, end, share = 0, piece0 = 0, pieces = 0;
   if (cut) {
-    if ((int)blockIdx.x >= cuts[p.n]) return;
+    if ((int)blockIdx.x >= cuts[p.n]) return false;
     int lo = 0, hi = p.n - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (cuts[mid] <= (int)blockIdx.x) lo = mid; else hi = mid - 1;
     }
-    const int per = prefix[lo + 1] - prefix[lo];
+    const int per = misc.entries[lo + 1] - misc.entries[lo];
     pieces = (cuts[lo + 1] - cuts[lo]) / v.heads;
     const int head = ((int)blockIdx.x - cuts[lo]) / pieces, j = ((int)blockIdx.x - cuts[lo]) % pieces;
     piece0 = (int)blockIdx.x - j;
-    share = 0;
-    begin = prefix[lo] * v.heads + head * per + (int)((long long)per * j / pieces);
-    end = prefix[lo] * v.heads + head * per + (int)((long long)per * (j + 1) / pieces);
+    begin = misc.entries[lo] * v.heads + head * per + (int)((long long)per * j / pieces);
+    end = misc.entries[lo] * v.heads + head * per + (int)((long long)per * (j + 1) / pieces);
   } else {
-    const int units = prefix[p.n] * v.heads;
+    const int units = misc.entries[p.n] * v.heads;
     share = max(p.least_units, (units + (int)gridDim.x - 1) / (int)gridDim.x);
     begin = (int)blockIdx.x * share;
     end = min(begin + share, units);
-    if (begin >= units) return;
+    if (begin >= units) return false;
   }
+  pl = Plan{begin, end, cut, piece0, pieces, share};
+  return true;
+}
 
-  // the item that holds unit u: entry, head, first unit
-  auto locate = [&](int u, int* entry, int* head, int* item_begin) {
-    int lo = 0, hi = p.n - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (prefix[mid] * v.heads <= u) lo = mid; else hi = mid - 1;
-    }
-    const int per = prefix[lo + 1] - prefix[lo], first = prefix[lo] * v.heads;
-    *entry = lo;
-    *head = (u - first) / per;
-    *item_begin = first + *head * per;
-  };
+// The item that holds unit u: entry, head, first unit.
+__device__ __forceinline__ void locate(const Kv8Attn& p, const Misc& misc, int u, int* entry, int* head, int* item_begin) {
+  const int* prefix = misc.entries;
+  int lo = 0, hi = p.n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (prefix[mid] * p.v.heads <= u) lo = mid; else hi = mid - 1;
+  }
+  const int per = prefix[lo + 1] - prefix[lo], first = prefix[lo] * p.v.heads;
+  *entry = lo;
+  *head = (u - first) / per;
+  *item_begin = first + *head * per;
+}
 
-  if (warp == W) {  // producer
-    int issued = 0;
-    for (int u = begin; u < end;) {
-      int e, head, ib;
-      locate(u, &e, &head, &ib);
-      const int per = prefix[e + 1] - prefix[e];
-      const int stop = min(ib + per, end);
-      const int b0 = u - ib, b1 = min(stop - ib, per - 1);  // the tail is unit per - 1
-      if (b0 < b1) {
-        const Span sp = span_of(lens[e], p.window, p.sinks);
-        const int32_t* table = v.table_row(p.seqs ? p.seqs[e] : e);
-        for (int c0 = b0; c0 < b1; c0 += 32) {
-          const int k = c0 + lane;
-          int page = 0;
-          if (k < b1) page = table[k < sp.head_blocks ? k : sp.from + (k - sp.head_blocks)];
-          const int some = b1 - c0 < 32 ? b1 - c0 : 32;
-          for (int i = 0; i < some; ++i) {
-            const int pg = __shfl_sync(~0u, page, i);
-            const int stage = issued % S;
-            bool ok = true;
-            if (issued >= S) ok = dev::mbar_wait_bounded(&misc.empty[stage], (uint32_t)((issued / S - 1) & 1));
-            if (!__all_sync(~0u, ok)) {
-              // consumers stopped: nothing more is issued; copies in flight are waited for below
-              misc.fail = 1;
-              u = end;
-              break;
-            }
-            if (lane == 0) {
-              dev::mbar_arrive_expect_tx(&misc.full[stage], kRecord);
-              dev::bulk_copy_g2s(ring + (size_t)stage * kRecord, v.record(pg, p.layer, head), kRecord, &misc.full[stage]);
-            }
-            ++issued;
+// The producer warp: the records of this CTA's blocks, in order, into the ring's stages.
+template <int D>
+__device__ __forceinline__ void produce(const Kv8Attn& p, Misc& misc, const Plan& pl, uint8_t* ring, int lane) {
+  constexpr int kRecord = 128 * D + 16;
+  const Kv8View& v = p.v;
+  const int S = p.stages;
+  int issued = 0;
+  for (int u = pl.begin; u < pl.end;) {
+    int e, head, ib;
+    locate(p, misc, u, &e, &head, &ib);
+    const int per = misc.entries[e + 1] - misc.entries[e];
+    const int stop = min(ib + per, pl.end);
+    const int b0 = u - ib, b1 = min(stop - ib, per - 1);  // the tail is unit per - 1
+    if (b0 < b1) {
+      const Span sp = span_of(lens_of(p, misc)[e], p.window, p.sinks);
+      const int32_t* table = v.table_row(p.seqs ? p.seqs[e] : e);
+      for (int c0 = b0; c0 < b1; c0 += 32) {
+        const int k = c0 + lane;
+        int page = 0;
+        if (k < b1) page = table[k < sp.head_blocks ? k : sp.from + (k - sp.head_blocks)];
+        const int some = b1 - c0 < 32 ? b1 - c0 : 32;
+        for (int i = 0; i < some; ++i) {
+          const int pg = __shfl_sync(~0u, page, i);
+          const int stage = issued % S;
+          bool ok = true;
+          if (issued >= S) ok = dev::mbar_wait_bounded(&misc.empty[stage], (uint32_t)((issued / S - 1) & 1));
+          if (!__all_sync(~0u, ok)) {
+            // the consumers stopped (they report it): nothing more is issued; copies in flight are waited for below
+              u = pl.end;
+            break;
           }
-          if (u >= end) break;
+          if (lane == 0) {
+            dev::mbar_arrive_expect_tx(&misc.full[stage], kRecord);
+            dev::bulk_copy_g2s(ring + (size_t)stage * kRecord, v.record(pg, p.layer, head), kRecord, &misc.full[stage]);
+          }
+          ++issued;
+        }
+        if (u >= pl.end) break;
+      }
+    }
+    if (u >= pl.end) break;
+    u = stop;
+  }
+  // copies in flight end before this CTA's shared memory is given up
+  for (int i = issued > S ? issued - S : 0; i < issued; ++i)
+    dev::mbar_wait_bounded(&misc.full[i % S], (uint32_t)((i / S) & 1));
+}
+
+// The item's result, or this CTA's part of it, from `sets` sets of partials (at most 8) that the consumers left in
+// shared memory: set w, query n at row n + w * stride of merge ([D] floats) and of ml_of (maximum, sum).
+// All consumers; the caller has synchronised them.
+template <int D>
+__device__ __forceinline__ void finish(const Kv8Attn& p, Misc& misc, const Plan& pl, const float* merge, const float* ml_of,
+                                       int sets, int stride, int e, int head, int ib, int per, int tid, int consumers) {
+  constexpr int kRow = D + kMergePad;
+  const Kv8View& v = p.v;
+  const int R = p.rows * p.group, lane = tid & 31;
+      const bool whole = pl.cut ? pl.pieces == 1 : ib >= pl.begin && ib + per <= pl.end;
+      const int mine = ib <= pl.begin || pl.cut ? 0 : 1;  // partial slots: the item that holds the share's first unit, and the other
+      float* part = p.parts + ((size_t)blockIdx.x * 2 + mine) * R * (D + 2);
+      uint16_t* out0 = p.out + ((size_t)e * p.rows * p.q_heads + (size_t)head * p.group) * D;
+      for (int x = tid; x < R * (D / 4); x += consumers) {
+        const int n = x / (D / 4), d = (x % (D / 4)) * 4;
+            float pm[8], pl[8], m = -INFINITY, l = 0.0f;
+  #pragma unroll
+        for (int w = 0; w < 8; ++w) {
+          const float2 ml = w < sets ? *reinterpret_cast<const float2*>(ml_of + 2 * (n + w * stride))
+                                   : make_float2(-INFINITY, 0.0f);
+          pm[w] = ml.x;
+          pl[w] = ml.y;
+          m = fmaxf(m, ml.x);
+        }
+        float4 o = {0, 0, 0, 0};
+  #pragma unroll
+        for (int w = 0; w < 8; ++w) {
+          if (w >= sets) break;
+          const float f = part_factor(pm[w], pl[w], m);
+          const float4 y = *reinterpret_cast<const float4*>(merge + (size_t)(n + w * stride) * kRow + d);
+          o.x += f * y.x;
+          o.y += f * y.y;
+          o.z += f * y.z;
+          o.w += f * y.w;
+          l += f * pl[w];
+        }
+        if (whole) {
+          const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+          *reinterpret_cast<uint2*>(out0 + ((size_t)(n / p.group) * p.q_heads + n % p.group) * D + d) =
+              make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+        } else {
+          float* to = part + (size_t)n * (D + 2);
+          *reinterpret_cast<float2*>(to + 2 + d) = make_float2(o.x, o.y);
+          *reinterpret_cast<float2*>(to + 4 + d) = make_float2(o.z, o.w);
+          if (d == 0) *reinterpret_cast<float2*>(to) = make_float2(m, l);
         }
       }
-      if (u >= end) break;
-      u = stop;
+      if (!whole) {
+        // CTAs c0 .. c1 share the item; the one that counts in last joins their partials in CTA order
+        const int c0 = pl.cut ? pl.piece0 : ib / pl.share, c1 = pl.cut ? pl.piece0 + pl.pieces - 1 : (ib + per - 1) / pl.share;
+        dev::named_barrier_sync(1, consumers);
+        uint32_t* ticket = p.tickets + (size_t)e * v.heads + head;
+        if (tid == 0) misc.last = dev::atomic_add_acq_rel_gpu(ticket, 1u) == (uint32_t)(c1 - c0);
+        dev::named_barrier_sync(1, consumers);
+        if (misc.last) {
+          // a warp per query: lanes hold 32 parts' maxima and sums at a time, then a slice of the head each.
+          // The item is the first of each CTA's slots but perhaps of c0's, where it may be the second.
+          const size_t step = (size_t)2 * R * (D + 2);
+          const float* parts = p.parts + (size_t)c0 * step;
+          const size_t first = !pl.cut && ib > c0 * pl.share ? step / 2 : 0;
+          const int np = c1 - c0 + 1;
+          for (int n = tid >> 5; n < R; n += consumers >> 5) {
+            const float* at = parts + (size_t)n * (D + 2);
+            float m = -INFINITY;
+            for (int c = lane; c < np; c += 32) m = fmaxf(m, __ldcg(at + c * step + (c == 0 ? first : 0)));
+  #pragma unroll
+            for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
+            float l = 0.0f;
+            float2 o[D / 64];
+  #pragma unroll
+            for (int j = 0; j < D / 64; ++j) o[j] = make_float2(0.0f, 0.0f);
+            for (int cc = 0; cc < np; cc += 32) {
+              const int c = cc + lane;
+              float f = 0.0f;
+              if (c < np) {
+                const float2 ml = __ldcg(reinterpret_cast<const float2*>(at + c * step + (c == 0 ? first : 0)));
+                f = part_factor(ml.x, ml.y, m);
+                l += f * ml.y;
+              }
+              const int some = min(32, np - cc);
+  #pragma unroll 8
+              for (int i = 0; i < some; ++i) {
+                const float fi = __shfl_sync(~0u, f, i);
+                const float* from = at + (size_t)(cc + i) * step + (cc + i == 0 ? first : 0) + 2;
+  #pragma unroll
+                for (int j = 0; j < D / 64; ++j) {
+                  const float2 y = __ldcg(reinterpret_cast<const float2*>(from + 64 * j + 2 * lane));
+                  o[j].x += fi * y.x;
+                  o[j].y += fi * y.y;
+                }
+              }
+            }
+  #pragma unroll
+            for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  #pragma unroll
+            for (int j = 0; j < D / 64; ++j)
+              *reinterpret_cast<uint32_t*>(out0 + ((size_t)(n / p.group) * p.q_heads + n % p.group) * D + 64 * j + 2 * lane) =
+                  pack_bf16(o[j].x * inv, o[j].y * inv);
+          }
+          if (tid == 0) *ticket = 0u;
+        }
+      }
+}
+
+template <int FMT, int D, int QT>
+__global__ void __launch_bounds__(32 * (max_warps(QT) + 1), 1) attn_kernel(const __grid_constant__ Kv8Attn p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  Misc& misc = *reinterpret_cast<Misc*>(smem);
+  const Kv8View& v = p.v;
+  const int W = p.warps, G = p.query_groups, WG = W / G, S = p.stages;
+  const int R = p.rows * p.group;
+  constexpr int kRecord = 128 * D + 16;
+  constexpr int kRow = D + kMergePad;
+  float* merge = reinterpret_cast<float*>(smem + misc_bytes(p.n));  // [W][8 QT][D + pad]
+  float* warp_ml = merge + (size_t)W * 8 * QT * kRow;               // [W][8 QT][2]
+  uint8_t* ring = smem + misc_bytes(p.n) + merge_bytes(W, QT, D);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  if (tid == 0) {
+    for (int i = 0; i < S; ++i) {
+      dev::mbar_init(&misc.full[i], 1);
+      dev::mbar_init(&misc.empty[i], (uint32_t)G);
     }
-    // copies in flight end before this CTA's shared memory is given up
-    for (int i = issued > S ? issued - S : 0; i < issued; ++i)
-      dev::mbar_wait_bounded(&misc.full[i % S], (uint32_t)((i / S) & 1));
+    misc.fail = 0;
+    dev::fence_mbar_init();
+  }
+  Plan pl;
+  if (!make_plan(p, misc, tid, pl)) return;
+  if (warp == W) {
+    produce<D>(p, misc, pl, ring, lane);
     return;
   }
 
@@ -603,12 +736,12 @@ __global__ void __launch_bounds__(32 * (max_warps(QT) + 1), 1) attn_kernel(const
   const int g = lane >> 2, t = lane & 3;
   const int consumers = W * 32;
   int taken = 0;  // blocks of this CTA that earlier items had
-  for (int u = begin; u < end;) {
+  for (int u = pl.begin; u < pl.end;) {
     int e, head, ib;
-    locate(u, &e, &head, &ib);
-    const int per = prefix[e + 1] - prefix[e];
-    const int stop = min(ib + per, end);
-    const int len = lens[e];
+    locate(p, misc, u, &e, &head, &ib);
+    const int per = misc.entries[e + 1] - misc.entries[e];
+    const int stop = min(ib + per, pl.end);
+    const int len = lens_of(p, misc)[e];
     const bool there = len >= 0;
     const Span sp = span_of(there ? len : 0, p.window, p.sinks);
     const bool has_tail = stop == ib + per && there;
@@ -701,120 +834,545 @@ __global__ void __launch_bounds__(32 * (max_warps(QT) + 1), 1) attn_kernel(const
       if (tid == 0) flag(v, WOQ_DEVERR_TIMEOUT);
       return;
     }
-    const bool whole = u == ib && stop == ib + per;
-    const int mine = ib <= begin || cut ? 0 : 1;  // partial slots: the item that holds the share's first unit, and the other
-    float* part = p.parts + ((size_t)blockIdx.x * 2 + mine) * R * (D + 2);
-    uint16_t* out0 = p.out + ((size_t)e * p.rows * p.q_heads + (size_t)head * p.group) * D;
-    for (int x = tid; x < R * (D / 4); x += consumers) {
-      const int n = x / (D / 4), d = (x % (D / 4)) * 4;
-      const int row0 = (n / (8 * QT)) * 8 * QT + n % (8 * QT);  // of warp `group`; the group's warps are G apart
-      float pm[8], pl[8], m = -INFINITY, l = 0.0f;
-#pragma unroll
-      for (int w = 0; w < 8; ++w) {
-        const float2 ml = w < WG ? *reinterpret_cast<const float2*>(warp_ml + 2 * (row0 + w * G * 8 * QT))
-                                 : make_float2(-INFINITY, 0.0f);
-        pm[w] = ml.x;
-        pl[w] = ml.y;
-        m = fmaxf(m, ml.x);
-      }
-      float4 o = {0, 0, 0, 0};
-#pragma unroll
-      for (int w = 0; w < 8; ++w) {
-        if (w >= WG) break;
-        const float f = part_factor(pm[w], pl[w], m);
-        const float4 y = *reinterpret_cast<const float4*>(merge + (size_t)(row0 + w * G * 8 * QT) * kRow + d);
-        o.x += f * y.x;
-        o.y += f * y.y;
-        o.z += f * y.z;
-        o.w += f * y.w;
-        l += f * pl[w];
-      }
-      if (whole) {
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        *reinterpret_cast<uint2*>(out0 + ((size_t)(n / p.group) * p.q_heads + n % p.group) * D + d) =
-            make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-      } else {
-        float* to = part + (size_t)n * (D + 2);
-        *reinterpret_cast<float2*>(to + 2 + d) = make_float2(o.x, o.y);
-        *reinterpret_cast<float2*>(to + 4 + d) = make_float2(o.z, o.w);
-        if (d == 0) *reinterpret_cast<float2*>(to) = make_float2(m, l);
-      }
-    }
-    if (!whole) {
-      // CTAs c0 .. c1 share the item; the one that counts in last joins their partials in CTA order
-      const int c0 = cut ? piece0 : ib / share, c1 = cut ? piece0 + pieces - 1 : (ib + per - 1) / share;
-      dev::named_barrier_sync(1, consumers);
-      uint32_t* ticket = p.tickets + (size_t)e * v.heads + head;
-      if (tid == 0) misc.last = dev::atomic_add_acq_rel_gpu(ticket, 1u) == (uint32_t)(c1 - c0);
-      dev::named_barrier_sync(1, consumers);
-      if (misc.last) {
-        // a warp per query: lanes hold 32 parts' maxima and sums at a time, then a slice of the head each.
-        // The item is the first of each CTA's slots but perhaps of c0's, where it may be the second.
-        const size_t step = (size_t)2 * R * (D + 2);
-        const float* parts = p.parts + (size_t)c0 * step;
-        const size_t first = !cut && ib > c0 * share ? step / 2 : 0;
-        const int np = c1 - c0 + 1;
-        for (int n = warp; n < R; n += W) {
-          const float* at = parts + (size_t)n * (D + 2);
-          float m = -INFINITY;
-          for (int c = lane; c < np; c += 32) m = fmaxf(m, __ldcg(at + c * step + (c == 0 ? first : 0)));
-#pragma unroll
-          for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
-          float l = 0.0f;
-          float2 o[D / 64];
-#pragma unroll
-          for (int j = 0; j < D / 64; ++j) o[j] = make_float2(0.0f, 0.0f);
-          for (int cc = 0; cc < np; cc += 32) {
-            const int c = cc + lane;
-            float f = 0.0f;
-            if (c < np) {
-              const float2 ml = __ldcg(reinterpret_cast<const float2*>(at + c * step + (c == 0 ? first : 0)));
-              f = part_factor(ml.x, ml.y, m);
-              l += f * ml.y;
-            }
-            const int some = min(32, np - cc);
-#pragma unroll 8
-            for (int i = 0; i < some; ++i) {
-              const float fi = __shfl_sync(~0u, f, i);
-              const float* from = at + (size_t)(cc + i) * step + (cc + i == 0 ? first : 0) + 2;
-#pragma unroll
-              for (int j = 0; j < D / 64; ++j) {
-                const float2 y = __ldcg(reinterpret_cast<const float2*>(from + 64 * j + 2 * lane));
-                o[j].x += fi * y.x;
-                o[j].y += fi * y.y;
-              }
-            }
-          }
-#pragma unroll
-          for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
-          const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
-          for (int j = 0; j < D / 64; ++j)
-            *reinterpret_cast<uint32_t*>(out0 + ((size_t)(n / p.group) * p.q_heads + n % p.group) * D + 64 * j + 2 * lane) =
-                pack_bf16(o[j].x * inv, o[j].y * inv);
-        }
-        if (tid == 0) *ticket = 0u;
-      }
-    }
+    finish<D>(p, misc, pl, merge, warp_ml, WG, G * 8 * QT, e, head, ib, per, tid, consumers);
     dev::named_barrier_sync(1, consumers);  // the merge buffer is free again
     u = stop;
   }
 }
 
-template <int FMT, int D, int QT>
+// ---------------------------------------------------------------------------------------------------
+// More than 8 queries: teams of four warps per block.
+//
+// With more tiles of queries, warps that each take a whole block would have to share out the
+// queries and every one of them would turn the block's codes into f16 again, and few warps of many
+// registers leave the tensor pipe waiting (40 queries: 25 % busy, 107 us at 65,531 tokens).  Here the four
+// warps of a team share out the block instead: each works out the scores of 16 of its tokens (a
+// quarter of the keys) for all NT tiles of queries, leaves the weights in shared memory, and
+// after one barrier sums its quarter of the elements over all 64 tokens (a quarter of the values).  Codes are
+// converted once, and a thread holds the weighted values of 2 NT fragments only.
+//
+// The running maxima belong to the team: weights are formed against them at once, and a score
+// that passes its maximum by more than kRaise raises a flag that all four warps see behind that
+// barrier; then (rarely) they agree on new maxima and form the weights again.
+constexpr int kTeams = 2;
+
+// Shared memory of one team: weights, twice (for two blocks in turn), column maxima of its warps, flags.
+template <int NT>
+struct TeamShared {
+  uint4 weights[2][NT][2][32];  // [buffer][tile][pair of 16-token steps][lane]: operands of both steps
+  float top[4][8 * NT];
+  int raise[2];
+};
+
+__host__ __device__ constexpr int team_bytes(int nt) { return (2 * nt * 2 * 32 * 16 + 4 * 8 * nt * 4 + 8 + 127) / 128 * 128; }
+// Queries as operands in shared memory: [tile][16 elements each][lane][2], kept there from four tiles on.
+__host__ __device__ constexpr int query_bytes(int nt, int dim) { return nt >= 4 ? nt * (dim / 16) * 32 * 8 : 0; }
+// All that is not the ring: the join's buffer, the teams', the queries, and what their rows see.
+__host__ __device__ constexpr int sight_bytes(int nt) { return (2 * 8 * nt * 4 + 127) / 128 * 128; }
+__host__ __device__ inline int team_fixed_bytes(int nt, int dim) {
+  return merge_bytes(kTeams, nt, dim) + kTeams * team_bytes(nt) + query_bytes(nt, dim) + sight_bytes(nt);
+}
+
+template <int D, int NT>
+struct TeamState {
+  float m[NT][2], l[NT][2];  // maxima (the same in the team's warps), sums over this lane's tokens
+  float o[D / 64][NT][4];
+};
+
+__device__ __forceinline__ void team_sync(int team) { dev::named_barrier_sync(2 + team, 128); }
+
+// Weights against the maxima, rounded; their sums into l.
+template <int D, int NT>
+__device__ __forceinline__ void weigh(TeamState<D, NT>& st, const float (&s)[NT][4], float (&w)[NT][4], float (&l)[NT][2]) {
+#pragma unroll
+  for (int q = 0; q < NT; ++q) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const float r = (st.m[q][c] == -INFINITY ? 0.0f : st.m[q][c]) - kOffset;
+      w[q][c] = exp2_approx(s[q][c] - r);
+      w[q][2 + c] = exp2_approx(s[q][2 + c] - r);
+      l[q][c] = w[q][c] + w[q][2 + c];
+    }
+  }
+}
+
+// Agree on maxima that cover s, and scale what was summed.  The team's warps, between two barriers.
+template <int D, int NT>
+__device__ __forceinline__ void raise_team(TeamState<D, NT>& st, TeamShared<NT>& ts, const float (&s)[NT][4], int wi, int team,
+                                           int lane) {
+  const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int q = 0; q < NT; ++q)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const float x = column_max(fmaxf(s[q][c], s[q][2 + c]));
+      if (g == 0) ts.top[wi][8 * q + 2 * t + c] = x;
+    }
+  team_sync(team);
+#pragma unroll
+  for (int q = 0; q < NT; ++q) {
+    float a[2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      float n = st.m[q][c];
+#pragma unroll
+      for (int w = 0; w < 4; ++w) n = fmaxf(n, ts.top[w][8 * q + 2 * t + c]);
+      a[c] = n == -INFINITY ? 1.0f : exp2_approx(st.m[q][c] - n);
+      st.m[q][c] = n;
+      st.l[q][c] *= a[c];
+    }
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j) {
+      st.o[j][q][0] *= a[0];
+      st.o[j][q][1] *= a[1];
+      st.o[j][q][2] *= a[0];
+      st.o[j][q][3] *= a[1];
+    }
+  }
+}
+
+template <int D, int NT>
+__device__ __forceinline__ bool passes(const TeamState<D, NT>& st, const float (&s)[NT][4]) {
+  bool up = false;
+#pragma unroll
+  for (int q = 0; q < NT; ++q)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) up |= fmaxf(s[q][c], s[q][2 + c]) > st.m[q][c] + kRaise;
+  return __any_sync(~0u, up);
+}
+
+// This warp's 16 tokens' weights (f16) into buffer `buf`.
+template <int NT>
+__device__ __forceinline__ void put_weights(TeamShared<NT>& ts, int buf, const float (&w)[NT][4], int wi, int lane) {
+#pragma unroll
+  for (int q = 0; q < NT; ++q)
+    reinterpret_cast<uint2*>(&ts.weights[buf][q][wi >> 1][lane])[wi & 1] =
+        make_uint2(transpose8x8(pack_f16(w[q][0], w[q][1])), transpose8x8(pack_f16(w[q][2], w[q][3])));
+}
+
+template <int FMT, int D, int NT, class Queries>
+__device__ __forceinline__ void team_block(TeamState<D, NT>& st, TeamShared<NT>& ts, const uint8_t* rec, const Queries& queries,
+                                           const float (&coef)[NT][2], const int* low, int token0, bool masked, int sinks,
+                                           int buf, int wi, int team, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+  const float ks = *reinterpret_cast<const float*>(rec + 128 * D);
+  const float vs = *reinterpret_cast<const float*>(rec + 128 * D + 4);
+  const uint8_t* kc = rec + (2 * wi * (D / 16) + t) * 128 + g * 16;
+  float s[NT][4];
+#pragma unroll
+  for (int q = 0; q < NT; ++q)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) s[q][c] = 0.0f;
+#pragma unroll
+  for (int c = 0; c < D / 64; ++c) {
+    const uint4 x = *reinterpret_cast<const uint4*>(kc + 4 * c * 128);
+    const uint4 y = *reinterpret_cast<const uint4*>(kc + (D / 16 + 4 * c) * 128);
+    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      uint32_t a[4];
+      f16x4_of_codes<FMT>(xs[k], a[0], a[2]);
+      f16x4_of_codes<FMT>(ys[k], a[1], a[3]);
+#pragma unroll
+      for (int q = 0; q < NT; ++q) {
+        const uint2 b = queries(q, 4 * c + k);
+        mma_f16(s[q], a, b.x, b.y);
+      }
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < NT; ++q) {
+    const float f0 = coef[q][0] * ks, f1 = coef[q][1] * ks;
+    s[q][0] *= f0;
+    s[q][1] *= f1;
+    s[q][2] *= f0;
+    s[q][3] *= f1;
+  }
+  if (masked) {
+    const int tok = token0 + 16 * (g >> 1) + 4 * wi + (g & 1);
+#pragma unroll
+    for (int q = 0; q < NT; ++q)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int lo = low[8 * q + 2 * t + c];
+        if (tok >= sinks && tok < lo) s[q][c] = -INFINITY;
+        if (tok + 2 >= sinks && tok + 2 < lo) s[q][2 + c] = -INFINITY;
+      }
+  }
+  float w[NT][4], l[NT][2];
+  if (passes(st, s) && lane == 0) ts.raise[buf] = 1;
+  weigh(st, s, w, l);
+  put_weights<NT>(ts, buf, w, wi, lane);
+  team_sync(team);
+  if (ts.raise[buf]) {
+    raise_team(st, ts, s, wi, team, lane);  // its barrier: every warp has read the flag
+    if (wi == 0 && lane == 0) ts.raise[buf] = 0;
+    weigh(st, s, w, l);
+    put_weights<NT>(ts, buf, w, wi, lane);
+    team_sync(team);
+  }
+#pragma unroll
+  for (int q = 0; q < NT; ++q) {
+    st.l[q][0] += l[q][0];
+    st.l[q][1] += l[q][1];
+  }
+  const uint8_t* vc = rec + 64 * D + t * 128 + g * 16 + wi * (D / 64) * 1024;
+  uint4 vx[D / 64], vy[D / 64];
+  float acc[D / 64][NT][4];
+#pragma unroll
+  for (int j = 0; j < D / 64; ++j) {
+    vx[j] = *reinterpret_cast<const uint4*>(vc + 2 * j * 512);
+    vy[j] = *reinterpret_cast<const uint4*>(vc + (2 * j + 1) * 512);
+#pragma unroll
+    for (int q = 0; q < NT; ++q)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[j][q][c] = 0.0f;
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint4 pb[NT];
+#pragma unroll
+    for (int q = 0; q < NT; ++q) pb[q] = ts.weights[buf][q][h][lane];
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j) {
+      uint32_t a[4];
+      f16x4_of_codes<FMT>(h ? vx[j].z : vx[j].x, a[0], a[2]);
+      f16x4_of_codes<FMT>(h ? vy[j].z : vy[j].x, a[1], a[3]);
+#pragma unroll
+      for (int q = 0; q < NT; ++q) mma_f16(acc[j][q], a, pb[q].x, pb[q].y);
+      f16x4_of_codes<FMT>(h ? vx[j].w : vx[j].y, a[0], a[2]);
+      f16x4_of_codes<FMT>(h ? vy[j].w : vy[j].y, a[1], a[3]);
+#pragma unroll
+      for (int q = 0; q < NT; ++q) mma_f16(acc[j][q], a, pb[q].z, pb[q].w);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+    for (int q = 0; q < NT; ++q)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) st.o[j][q][c] = fmaf(vs, acc[j][q][c], st.o[j][q][c]);
+}
+
+// The tail, or (over = true) its rows 64 .. 71: as team_block, from bf16 in global memory; weights as two
+// bf16 parts, the high ones in buffer 0 and the low ones in buffer 1.
+template <int D, int NT>
+__device__ void team_tail(TeamState<D, NT>& st, TeamShared<NT>& ts, const uint16_t* tail, bool over, int in_tail, int len,
+                          int there, const Kv8Attn& p, const uint16_t* q0, const int* low, const uint32_t* vis, int wi, int team,
+                          int lane) {
+  const int g = lane >> 2, t = lane & 3;
+  const bool mine = !over || wi == 0;  // this warp has tokens
+  const int r0 = over ? 64 + g : 16 * (g >> 1) + 4 * wi + (g & 1), r1 = over ? kKv8Tail : r0 + 2;
+  const int R = p.rows * p.group;
+  float s[NT][4];
+#pragma unroll
+  for (int q = 0; q < NT; ++q)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) s[q][c] = mine ? 0.0f : -INFINITY;
+  if (mine) {
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) {
+      uint32_t x[8], y[8];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint4 a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
+        if (r0 < there) a = *reinterpret_cast<const uint4*>(tail + r0 * D + 16 * (4 * c + t) + 8 * h);
+        if (r1 < there) b = *reinterpret_cast<const uint4*>(tail + r1 * D + 16 * (4 * c + t) + 8 * h);
+        x[4 * h] = a.x, x[4 * h + 1] = a.y, x[4 * h + 2] = a.z, x[4 * h + 3] = a.w;
+        y[4 * h] = b.x, y[4 * h + 1] = b.y, y[4 * h + 2] = b.z, y[4 * h + 3] = b.w;
+      }
+#pragma unroll
+      for (int q = 0; q < NT; ++q) {
+        const int n = 8 * q + g;
+        const uint16_t* qr = n < R ? q0 + ((size_t)(n / p.group) * p.q_heads + n % p.group) * D : nullptr;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint4 b = {0, 0, 0, 0};
+          if (qr) b = *reinterpret_cast<const uint4*>(qr + 16 * (4 * c + t) + 8 * h);
+          const uint32_t a0[4] = {x[4 * h], y[4 * h], x[4 * h + 1], y[4 * h + 1]};
+          const uint32_t a1[4] = {x[4 * h + 2], y[4 * h + 2], x[4 * h + 3], y[4 * h + 3]};
+          mma_bf16(s[q], a0, b.x, b.y);
+          mma_bf16(s[q], a1, b.z, b.w);
+        }
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < NT; ++q)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int k = 8 * q + 2 * t + c;
+        s[q][c] = tail_sees(r0, vis[k], low[k], in_tail, there, len, p.sinks) ? s[q][c] * p.scale_log2 : -INFINITY;
+        s[q][2 + c] = tail_sees(r1, vis[k], low[k], in_tail, there, len, p.sinks) ? s[q][2 + c] * p.scale_log2 : -INFINITY;
+      }
+  }
+  raise_team(st, ts, s, wi, team, lane);
+  float w[NT][4], l[NT][2];
+  weigh(st, s, w, l);
+#pragma unroll
+  for (int q = 0; q < NT; ++q) {
+    st.l[q][0] += l[q][0];
+    st.l[q][1] += l[q][1];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t u = pack_bf16(w[q][2 * h], w[q][2 * h + 1]);
+      const float f0 = __uint_as_float(u << 16), f1 = __uint_as_float(u & 0xFFFF0000u);
+      reinterpret_cast<uint32_t*>(&ts.weights[0][q][wi >> 1][lane])[2 * (wi & 1) + h] = transpose8x8(u);
+      reinterpret_cast<uint32_t*>(&ts.weights[1][q][wi >> 1][lane])[2 * (wi & 1) + h] =
+          transpose8x8(pack_bf16(w[q][2 * h] - f0, w[q][2 * h + 1] - f1));
+    }
+  }
+  team_sync(team);
+  const uint16_t* tv = tail + kKv8Tail * D + wi * (D / 4) * kKv8Tail;
+#pragma unroll
+  for (int j = 0; j < D / 64; ++j) {
+    const uint16_t* v0 = tv + (16 * j + g) * kKv8Tail;
+    const uint16_t* v1 = v0 + 8 * kKv8Tail;
+    uint4 x[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}}, y[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+    if (over) {
+      x[0].x = *reinterpret_cast<const uint32_t*>(v0 + 64 + 2 * t);
+      y[0].x = *reinterpret_cast<const uint32_t*>(v1 + 64 + 2 * t);
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        x[h] = *reinterpret_cast<const uint4*>(v0 + 16 * t + 8 * h);
+        y[h] = *reinterpret_cast<const uint4*>(v1 + 16 * t + 8 * h);
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t a0[4] = {x[h].x, y[h].x, x[h].y, y[h].y}, a1[4] = {x[h].z, y[h].z, x[h].w, y[h].w};
+#pragma unroll
+      for (int q = 0; q < NT; ++q)
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+          const uint4 b = ts.weights[part][q][h][lane];
+          mma_bf16(st.o[j][q], a0, b.x, b.y);
+          mma_bf16(st.o[j][q], a1, b.z, b.w);
+        }
+    }
+  }
+  team_sync(team);  // the buffers are free again
+}
+
+template <int FMT, int D, int NT>
+__global__ void __launch_bounds__(32 * (4 * kTeams + 1), 1) attn_team_kernel(const __grid_constant__ Kv8Attn p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  constexpr bool kShared = NT >= 4;  // queries in shared memory
+  constexpr int kRecord = 128 * D + 16, kRow = D + kMergePad, W = 4 * kTeams, kQueries = 8 * NT;
+  Misc& misc = *reinterpret_cast<Misc*>(smem);
+  float* merge = reinterpret_cast<float*>(smem + misc_bytes(p.n));  // [teams][8 NT][D + pad]
+  float* team_ml = merge + kTeams * kQueries * kRow;                // [teams][8 NT][2]
+  uint8_t* at_teams = smem + misc_bytes(p.n) + merge_bytes(kTeams, NT, D);
+  uint2* shared_q = reinterpret_cast<uint2*>(at_teams + kTeams * team_bytes(NT));
+  int* low = reinterpret_cast<int*>(at_teams + kTeams * team_bytes(NT) + query_bytes(NT, D));  // [8 NT]
+  uint32_t* vis = reinterpret_cast<uint32_t*>(low + kQueries);                                                 // [8 NT]
+  uint8_t* ring = smem + misc_bytes(p.n) + team_fixed_bytes(NT, D);
+  const Kv8View& v = p.v;
+  const int S = p.stages, R = p.rows * p.group;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  if (tid == 0) {
+    for (int i = 0; i < S; ++i) {
+      dev::mbar_init(&misc.full[i], 1);
+      dev::mbar_init(&misc.empty[i], 4);
+    }
+    misc.fail = 0;
+    dev::fence_mbar_init();
+  }
+  const int team = (warp >> 2) % kTeams, wi = warp & 3;
+  TeamShared<NT>& ts = *reinterpret_cast<TeamShared<NT>*>(at_teams + team * team_bytes(NT));
+  if (warp < W && wi == 0 && lane < 2) ts.raise[lane] = 0;
+  Plan pl;
+  if (!make_plan(p, misc, tid, pl)) return;
+  if (warp == W) {
+    produce<D>(p, misc, pl, ring, lane);
+    return;
+  }
+
+  int taken = 0;
+  for (int u = pl.begin; u < pl.end;) {
+    int e, head, ib;
+    locate(p, misc, u, &e, &head, &ib);
+    const int per = misc.entries[e + 1] - misc.entries[e];
+    const int stop = min(ib + per, pl.end);
+    const int len = lens_of(p, misc)[e];
+    const bool there = len >= 0;
+    const Span sp = span_of(there ? len : 0, p.window, p.sinks);
+    const bool has_tail = stop == ib + per && there;
+    const int b0 = u - ib, b1 = min(stop - ib, per - 1), blocks = max(0, b1 - b0);
+    const uint16_t* q0 = p.q + ((size_t)e * p.rows * p.q_heads + (size_t)head * p.group) * D;
+
+    // what the rows see
+    int low_max = 0;
+    uint32_t any_vis = 0;
+    for (int k = lane; k < kQueries; k += 32) {
+      const int m = k < R ? k / p.group : 0;
+      const uint32_t x = (p.vis ? p.vis[(size_t)e * p.rows + m] : (2u << m) - 1u) & 0xFFu;
+      const int lo = p.window > 0 ? len + __popc(x) - p.window : 0;
+      any_vis |= x;
+      low_max = max(low_max, lo);
+      if (warp == 0) {
+        low[k] = lo;
+        vis[k] = x;
+      }
+    }
+    low_max = __reduce_max_sync(~0u, low_max);
+    any_vis = __reduce_or_sync(~0u, any_vis);
+    // queries
+    uint32_t qf[kShared ? 1 : NT][D / 16][2];
+    float coef[NT][2];
+    if constexpr (kShared) {
+      float* units = team_ml;  // [8 NT], until the first join
+      for (int q = warp; q < NT; q += W) {
+        const int n = 8 * q + g;
+        const uint16_t* qrow[1] = {n < R ? q0 + ((size_t)(n / p.group) * p.q_heads + n % p.group) * D : nullptr};
+        float unit[1];
+        uint32_t f[1][D / 16][2];
+        load_queries<D, 1>(f, unit, qrow, lane);
+        if (t == 0) units[n] = unit[0];
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) shared_q[(q * (D / 16) + k) * 32 + lane] = make_uint2(f[0][k][0], f[0][k][1]);
+      }
+      dev::named_barrier_sync(1, W * 32);
+#pragma unroll
+      for (int q = 0; q < NT; ++q)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) coef[q][c] = units[8 * q + 2 * t + c] * p.scale_log2;
+    } else {
+      const uint16_t* qrow[NT];
+      float unit[NT];
+#pragma unroll
+      for (int q = 0; q < NT; ++q) {
+        const int n = 8 * q + g;
+        qrow[q] = n < R ? q0 + ((size_t)(n / p.group) * p.q_heads + n % p.group) * D : nullptr;
+      }
+      load_queries<D, NT>(qf, unit, qrow, lane);
+#pragma unroll
+      for (int q = 0; q < NT; ++q) {
+        coef[q][0] = __shfl_sync(~0u, unit[q], 8 * t) * p.scale_log2;
+        coef[q][1] = __shfl_sync(~0u, unit[q], 8 * t + 4) * p.scale_log2;
+      }
+      dev::named_barrier_sync(1, W * 32);
+    }
+    auto queries = [&](int q, int k) {
+      if constexpr (kShared) return shared_q[(q * (D / 16) + k) * 32 + lane];
+      else return make_uint2(qf[q][k][0], qf[q][k][1]);
+    };
+    TeamState<D, NT> st;
+#pragma unroll
+    for (int q = 0; q < NT; ++q) {
+      st.m[q][0] = st.m[q][1] = -INFINITY;
+      st.l[q][0] = st.l[q][1] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) st.o[j][q][c] = 0.0f;
+    }
+    if (has_tail && team == (taken + blocks) % kTeams) {  // the team whose turn comes next after the blocks
+      const uint16_t* tail = v.tail(p.layer, p.seqs ? p.seqs[e] : e, head);
+      const int in_tail = len - sp.full * kKv8Block, rows = in_tail + 32 - __clz((int)any_vis);  // at most 63 + 8
+      if (rows > 0) team_tail<D, NT>(st, ts, tail, false, in_tail, len, rows, p, q0, low, vis, wi, team, lane);
+      if (rows > 64) team_tail<D, NT>(st, ts, tail, true, in_tail, len, rows, p, q0, low, vis, wi, team, lane);
+    }
+    bool ok = true;
+    int k = b0 + ((team - taken) % kTeams + kTeams) % kTeams;  // S is a multiple of the teams
+    for (int buf = 0; k < b1; k += kTeams, buf ^= 1) {
+      const int at = taken + (k - b0), stage = at % S;
+      // after a wait that ran out the warp goes on without waits (the team's barriers need it) but releases no stage,
+      // so that the producer stops too; nothing of the item is written
+      if (ok) ok = __all_sync(~0u, dev::mbar_wait_bounded(&misc.full[stage], (uint32_t)((at / S) & 1)));
+      const int blk = k < sp.head_blocks ? k : sp.from + (k - sp.head_blocks);
+      const int token0 = blk * kKv8Block;
+      team_block<FMT, D, NT>(st, ts, ring + (size_t)stage * kRecord, queries, coef, low, token0,
+                             token0 < low_max && token0 + kKv8Block > p.sinks, p.sinks, buf, wi, team, lane);
+      __syncwarp();
+      if (ok && lane == 0) dev::mbar_arrive(&misc.empty[stage]);
+    }
+    if (!ok && lane == 0) misc.fail = 1;
+    taken += blocks;
+
+    // join: the sums over a column's lanes and the team's warps, the weighted values as they are
+#pragma unroll
+    for (int q = 0; q < NT; ++q)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float l = st.l[q][c];
+        l += __shfl_xor_sync(~0u, l, 4);
+        l += __shfl_xor_sync(~0u, l, 8);
+        l += __shfl_xor_sync(~0u, l, 16);
+        if (g == 0) ts.top[wi][8 * q + 2 * t + c] = l;
+      }
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+      for (int q = 0; q < NT; ++q)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          merge[(size_t)(team * kQueries + 8 * q + 2 * t + (c & 1)) * kRow + 16 * (wi * (D / 64) + j) + g + 8 * (c >> 1)] =
+              st.o[j][q][c];
+    dev::named_barrier_sync(1, W * 32);
+    if (wi == 0) {
+#pragma unroll
+      for (int q = 0; q < NT; ++q)
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          if (g == 0) {
+            const int n = 8 * q + 2 * t + c;
+            team_ml[2 * (team * kQueries + n)] = st.m[q][c];
+            team_ml[2 * (team * kQueries + n) + 1] = (ts.top[0][n] + ts.top[1][n]) + (ts.top[2][n] + ts.top[3][n]);
+          }
+    }
+    dev::named_barrier_sync(1, W * 32);
+    if (misc.fail) {  // a wait ran out: nothing of this item is written
+      if (tid == 0) flag(v, WOQ_DEVERR_TIMEOUT);
+      return;
+    }
+    finish<D>(p, misc, pl, merge, team_ml, kTeams, kQueries, e, head, ib, per, tid, W * 32);
+    dev::named_barrier_sync(1, W * 32);  // the buffers are free again
+    u = stop;
+  }
+}
+
+template <void (*KERNEL)(Kv8Attn)>
 cudaError_t launch_attn(const Kv8Attn& p, int ctas, int smem, cudaStream_t stream) {
-  auto kernel = attn_kernel<FMT, D, QT>;
   static std::atomic<unsigned long long> configured{0};
   int device = 0;
   cudaError_t e = cudaGetDevice(&device);
   if (e != cudaSuccess) return e;
   const unsigned long long bit = 1ull << (device & 63);
   if (!(configured.load(std::memory_order_relaxed) & bit)) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, max_dynamic_smem());
+    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, max_dynamic_smem());
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit);
   }
-  return launch(kernel, dim3((unsigned)ctas), (p.warps + 1) * 32, (size_t)smem, stream, p);
+  return launch(KERNEL, dim3((unsigned)ctas), (p.warps + 1) * 32, (size_t)smem, stream, p);
+}
+
+// The instances of a cache of FMT codes, by head size and query tiles (of a warp, or of a team).
+template <int FMT>
+cudaError_t launch_attn_any(const Kv8Attn& p, int ctas, int smem, cudaStream_t s) {
+  switch (p.v.dim * 8 + p.tiles) {
+    case 64 * 8 + 1: return launch_attn<attn_kernel<FMT, 64, 1>>(p, ctas, smem, s);
+    case 64 * 8 + 2: return launch_attn<attn_kernel<FMT, 64, 2>>(p, ctas, smem, s);
+    case 128 * 8 + 1: return launch_attn<attn_kernel<FMT, 128, 1>>(p, ctas, smem, s);
+    case 128 * 8 + 2: return launch_attn<attn_kernel<FMT, 128, 2>>(p, ctas, smem, s);
+    case 256 * 8 + 1: return launch_attn<attn_kernel<FMT, 256, 1>>(p, ctas, smem, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+template <int FMT>
+cudaError_t launch_team_any(const Kv8Attn& p, int ctas, int smem, cudaStream_t s) {
+  switch (p.v.dim * 8 + p.tiles) {
+    case 64 * 8 + 2: return launch_attn<attn_team_kernel<FMT, 64, 2>>(p, ctas, smem, s);
+    case 64 * 8 + 3: return launch_attn<attn_team_kernel<FMT, 64, 3>>(p, ctas, smem, s);
+    case 64 * 8 + 4: return launch_attn<attn_team_kernel<FMT, 64, 4>>(p, ctas, smem, s);
+    case 64 * 8 + 5: return launch_attn<attn_team_kernel<FMT, 64, 5>>(p, ctas, smem, s);
+    case 128 * 8 + 2: return launch_attn<attn_team_kernel<FMT, 128, 2>>(p, ctas, smem, s);
+    case 128 * 8 + 3: return launch_attn<attn_team_kernel<FMT, 128, 3>>(p, ctas, smem, s);
+    case 128 * 8 + 4: return launch_attn<attn_team_kernel<FMT, 128, 4>>(p, ctas, smem, s);
+    case 128 * 8 + 5: return launch_attn<attn_team_kernel<FMT, 128, 5>>(p, ctas, smem, s);
+    default: return cudaErrorInvalidValue;
+  }
 }
 
 }  // namespace kv8

@@ -105,7 +105,8 @@ struct Kv8Attn {
   float* parts;       // [2 CTAs][rows * group][dim + 2]
   float scale_log2;
   int layer, n, rows, q_heads, group, window, sinks;
-  int tiles;         // tiles of 8 queries per warp
+  int team;          // 1: a team of four warps per block, 0: a warp
+  int tiles;         // tiles of 8 queries of a warp (of a team)
   int warps, query_groups, stages;
   int least_units;   // units a CTA takes at least (while there are more CTAs than that needs, they idle)
 };
@@ -130,5 +131,7 @@ cudaError_t launch_kv8_read(const Kv8View& v, int layer, int layers, int seq, in
 int kv8_attn_plan(Kv8Attn* p, int smem_max);
 cudaError_t launch_kv8_attn_int8(const Kv8Attn& p, int ctas, int smem, cudaStream_t s);
 cudaError_t launch_kv8_attn_e4m3(const Kv8Attn& p, int ctas, int smem, cudaStream_t s);
+cudaError_t launch_kv8_team_int8(const Kv8Attn& p, int ctas, int smem, cudaStream_t s);
+cudaError_t launch_kv8_team_e4m3(const Kv8Attn& p, int ctas, int smem, cudaStream_t s);
 
 }  // namespace woq
