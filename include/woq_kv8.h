@@ -142,7 +142,7 @@ WOQ_API int woq_kv8_append_prompt(const woq_kv8_config* cfg, void* cache, size_t
  * Attention of `rows` rows of each of n sequences (the draft rows' queries).
  *   q, out: device bf16 [n][rows][q_heads][head_dim]; q_heads a multiple of kv_heads, query head
  *   i reads kv head i / (q_heads / kv_heads); rows * q_heads / kv_heads <= 128 (head_dim 256: 56);
- *   n * kv_heads * (ceil(max_tokens / 64) + 2) < 2^31 - 2^16.
+ *   n * kv_heads * (ceil(max_tokens / 64) + 8) < 2^31 - 2^16.
  *   vis: device uint32 [n][rows], bit j: draft row j is seen (bits 0 .. 7); NULL: row m sees
  *   draft rows 0 .. m.  Only rows that were appended may be seen.
  *   A row sees, in this order, the sequence's tokens and the draft rows of its vis; with

@@ -107,7 +107,7 @@ int query_limit(int dim) { return dim == 256 ? 56 : 128; }  // one group of 8 qu
 bool attn_shape_ok(const Kv8View& v, int n, int rows, int q_heads) {
   return n >= 0 && n <= kKv8MaxSeqs && rows >= 1 && rows <= WOQ_KV8_ROWS && q_heads >= 1 && q_heads <= 4096 &&
          q_heads % v.heads == 0 && rows * (q_heads / v.heads) <= query_limit(v.dim) &&
-         (long long)n * v.heads * (v.blocks + 2) <= 0x7FFF0000ll;
+         (long long)n * v.heads * (v.blocks + kv8::kTailUnits) <= 0x7FFF0000ll;
 }
 
 // Workspace of the attention: [status 256 B][tickets][partials]
@@ -245,7 +245,7 @@ size_t woq_kv8_attention_workspace(const woq_kv8_config* cfg, int n, int rows, i
   if (!cfg || !make_view(*cfg, &v) || !attn_shape_ok(v, n, rows, q_heads)) return 0;
   const int sms = sm_count();
   if (sms <= 0) return 0;
-  return attn_parts_offset(v, n) + (size_t)2 * sms * rows * (q_heads / v.heads) * (v.dim + 2) * 4;
+  return attn_parts_offset(v, n) + (size_t)2 * sms * rows * (q_heads / v.heads) * (v.dim + 4) * 4;
 }
 
 int woq_kv8_plan_attention(const woq_kv8_config* cfg, int n, int rows, int q_heads, int sms, int smem_max,

@@ -76,8 +76,12 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 
 // What an entry's rows see of its blocks: [0, head_blocks) and [from, full).
 struct Span {
-  int len, full, head_blocks, from, units;  // units: blocks seen and the tail
+  int len, full, head_blocks, from, units;  // units: blocks seen, and kTailUnits for the tail
 };
+
+// Units that the tail counts for: it takes a CTA as long as so many blocks (3 to 4 us).  They lie behind the
+// item's blocks; whoever has the last of them does the tail.
+constexpr int kTailUnits = 8;
 
 __device__ __forceinline__ Span span_of(int len, int window, int sinks) {
   Span s;
@@ -90,7 +94,7 @@ __device__ __forceinline__ Span span_of(int len, int window, int sinks) {
     s.head_blocks = (sinks + kKv8Block - 1) / kKv8Block;
     if (s.head_blocks >= s.from) s.head_blocks = s.from;
   }
-  s.units = s.head_blocks + (s.full - s.from) + 1;
+  s.units = s.head_blocks + (s.full - s.from) + kTailUnits;
   return s;
 }
 
@@ -422,7 +426,7 @@ struct Misc {
   int entries[];
 };
 __host__ __device__ inline int misc_bytes(int n) { return (int)((sizeof(Misc) + (size_t)(3 * n + 2) * 4 + 127) / 128 * 128); }
-constexpr int kWhole = 24;  // units of an item that is not cut
+constexpr int kWhole = 32;  // units of an item that is not cut
 
 __device__ __forceinline__ int pieces_of(int units, int share) { return units <= kWhole ? 1 : (units + share - 1) / share; }
 __host__ __device__ inline int merge_bytes(int warps, int qt, int dim) {
@@ -455,6 +459,36 @@ __device__ __forceinline__ bool make_plan(const Kv8Attn& p, Misc& misc, int tid,
   // lengths and units of the entries (the header's check is read beside them, not before)
   const uint4 header = *reinterpret_cast<const uint4*>(v.base);
   const bool ours = header.y == kKv8Magic && header.z == v.hash;
+  if (p.n == 1) {  // one sequence: every thread works it out for itself
+    const int seq = p.seqs ? p.seqs[0] : 0;
+    const bool there = seq >= 0 && seq < v.seqs;
+    const int len = there ? v.lens_p()[seq] : -1;
+    if (!ours) {
+      if (header.y == kKv8Magic && tid == 0) flag(v, WOQ_DEVERR_HEADER);
+      return false;
+    }
+    if (!there && blockIdx.x == 0 && tid == 0) flag(v, WOQ_DEVERR_STATE);
+    const int per = there ? span_of(len, p.window, p.sinks).units : kTailUnits;
+    if (tid == 0) {
+      misc.entries[0] = 0;
+      misc.entries[1] = per;
+      lens[0] = len;
+    }
+    __syncthreads();
+    const int ctas = (int)gridDim.x;
+    if (v.heads <= ctas) {
+      const int room = ctas / v.heads, share = max(p.least_units, (per + room - 1) / room);
+      const int pieces = pieces_of(per, share), head = (int)blockIdx.x / pieces, j = (int)blockIdx.x - head * pieces;
+      if (head >= v.heads) return false;
+      pl = Plan{head * per + (int)((long long)per * j / pieces), head * per + (int)((long long)per * (j + 1) / pieces), true,
+                (int)blockIdx.x - j, pieces, 0};
+      return true;
+    }
+    const int share = max(p.least_units, (per * v.heads + ctas - 1) / ctas), begin = (int)blockIdx.x * share;
+    if (begin >= per * v.heads) return false;
+    pl = Plan{begin, min(begin + share, per * v.heads), false, 0, 0, share};
+    return true;
+  }
   if (warp == 0) {
     int run = 0;
     for (int e0 = 0; e0 < p.n; e0 += 32) {
@@ -465,7 +499,7 @@ __device__ __forceinline__ bool make_plan(const Kv8Attn& p, Misc& misc, int tid,
         const bool there = seq >= 0 && seq < v.seqs;
         if (!there && ours && blockIdx.x == 0) flag(v, WOQ_DEVERR_STATE);
         lens[e] = there ? v.lens_p()[seq] : -1;
-        units = there ? span_of(lens[e], p.window, p.sinks).units : 1;
+        units = there ? span_of(lens[e], p.window, p.sinks).units : kTailUnits;
       }
       int y = units;
 #pragma unroll
@@ -477,30 +511,35 @@ __device__ __forceinline__ bool make_plan(const Kv8Attn& p, Misc& misc, int tid,
       run += __shfl_sync(~0u, y, 31);
     }
     if (lane == 0) misc.entries[p.n] = run;
-    // the least share with which all pieces have a CTA
+    // The least share with which all pieces have a CTA, to 1/32: the lanes try 32 of them at once.
     int share = 0;
     if (ours && p.n * v.heads <= (int)gridDim.x) {
       __syncwarp();
       const int room = (int)gridDim.x / v.heads;  // pieces of one head
       share = max(p.least_units, (run + room - 1) / room);
-      for (;;) {
+      for (;;) {  // ends: with a share beyond the longest item there are n <= room pieces
+        const int mine = share + (int)((long long)share * lane / 32);
         int total = 0;
-        for (int e0 = 0; e0 < p.n; e0 += 32) {
-          const int e = e0 + lane;
-          int y = e < p.n ? pieces_of(misc.entries[e + 1] - misc.entries[e], share) : 0;
-          const int own = y;
-#pragma unroll
-          for (int d = 1; d < 32; d <<= 1) {
-            const int z = __shfl_up_sync(~0u, y, d);
-            if (lane >= d) y += z;
-          }
-          if (e < p.n) cuts[e] = (total + y - own) * v.heads;
-          total += __shfl_sync(~0u, y, 31);
-        }
-        if (lane == 0) cuts[p.n] = total * v.heads;
-        if (total <= room) break;
-        share += share / 8 + 1;  // ends: with a share beyond the longest item there are n <= room pieces
+        for (int e = 0; e < p.n; ++e) total += pieces_of(misc.entries[e + 1] - misc.entries[e], mine);
+        const uint32_t fits = __ballot_sync(~0u, total <= room);
+        share = __shfl_sync(~0u, mine, fits ? __ffs((int)fits) - 1 : 31);
+        if (fits) break;
+        ++share;
       }
+      int total = 0;
+      for (int e0 = 0; e0 < p.n; e0 += 32) {
+        const int e = e0 + lane;
+        int y = e < p.n ? pieces_of(misc.entries[e + 1] - misc.entries[e], share) : 0;
+        const int own = y;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int z = __shfl_up_sync(~0u, y, d);
+          if (lane >= d) y += z;
+        }
+        if (e < p.n) cuts[e] = (total + y - own) * v.heads;
+        total += __shfl_sync(~0u, y, 31);
+      }
+      if (lane == 0) cuts[p.n] = total * v.heads;
     }
     if (lane == 0) misc.share = share;
   }
@@ -562,7 +601,7 @@ __device__ __forceinline__ void produce(const Kv8Attn& p, Misc& misc, const Plan
     locate(p, misc, u, &e, &head, &ib);
     const int per = misc.entries[e + 1] - misc.entries[e];
     const int stop = min(ib + per, pl.end);
-    const int b0 = u - ib, b1 = min(stop - ib, per - 1);  // the tail is unit per - 1
+    const int b0 = u - ib, b1 = min(stop - ib, per - kTailUnits);
     if (b0 < b1) {
       const Span sp = span_of(lens_of(p, misc)[e], p.window, p.sinks);
       const int32_t* table = v.table_row(p.seqs ? p.seqs[e] : e);
@@ -600,107 +639,122 @@ __device__ __forceinline__ void produce(const Kv8Attn& p, Misc& misc, const Plan
 
 // The item's result, or this CTA's part of it, from `sets` sets of partials (at most 8) that the consumers left in
 // shared memory: set w, query n at row n + w * stride of merge ([D] floats) and of ml_of (maximum, sum).
-// All consumers; the caller has synchronised them.
+// merge holds `room` floats and is scratch afterwards.  All consumers; the caller has synchronised them.
+//
+// A part in p.parts: [R][D] values, [R][2] maxima and sums, in steps of R (D + 4) floats; two slots a CTA.
 template <int D>
-__device__ __forceinline__ void finish(const Kv8Attn& p, Misc& misc, const Plan& pl, const float* merge, const float* ml_of,
-                                       int sets, int stride, int e, int head, int ib, int per, int tid, int consumers) {
+__device__ __forceinline__ void finish(const Kv8Attn& p, Misc& misc, const Plan& plan, float* merge, int room,
+                                       const float* ml_of, int sets, int stride, int e, int head, int ib, int per, int tid,
+                                       int consumers) {
   constexpr int kRow = D + kMergePad;
-  const Kv8View& v = p.v;
   const int R = p.rows * p.group, lane = tid & 31;
-      const bool whole = pl.cut ? pl.pieces == 1 : ib >= pl.begin && ib + per <= pl.end;
-      const int mine = ib <= pl.begin || pl.cut ? 0 : 1;  // partial slots: the item that holds the share's first unit, and the other
-      float* part = p.parts + ((size_t)blockIdx.x * 2 + mine) * R * (D + 2);
-      uint16_t* out0 = p.out + ((size_t)e * p.rows * p.q_heads + (size_t)head * p.group) * D;
-      for (int x = tid; x < R * (D / 4); x += consumers) {
-        const int n = x / (D / 4), d = (x % (D / 4)) * 4;
-            float pm[8], pl[8], m = -INFINITY, l = 0.0f;
-  #pragma unroll
-        for (int w = 0; w < 8; ++w) {
-          const float2 ml = w < sets ? *reinterpret_cast<const float2*>(ml_of + 2 * (n + w * stride))
-                                   : make_float2(-INFINITY, 0.0f);
-          pm[w] = ml.x;
-          pl[w] = ml.y;
-          m = fmaxf(m, ml.x);
-        }
-        float4 o = {0, 0, 0, 0};
-  #pragma unroll
-        for (int w = 0; w < 8; ++w) {
-          if (w >= sets) break;
-          const float f = part_factor(pm[w], pl[w], m);
-          const float4 y = *reinterpret_cast<const float4*>(merge + (size_t)(n + w * stride) * kRow + d);
-          o.x += f * y.x;
-          o.y += f * y.y;
-          o.z += f * y.z;
-          o.w += f * y.w;
-          l += f * pl[w];
-        }
-        if (whole) {
-          const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-          *reinterpret_cast<uint2*>(out0 + ((size_t)(n / p.group) * p.q_heads + n % p.group) * D + d) =
-              make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-        } else {
-          float* to = part + (size_t)n * (D + 2);
-          *reinterpret_cast<float2*>(to + 2 + d) = make_float2(o.x, o.y);
-          *reinterpret_cast<float2*>(to + 4 + d) = make_float2(o.z, o.w);
-          if (d == 0) *reinterpret_cast<float2*>(to) = make_float2(m, l);
-        }
+  const bool whole = plan.cut ? plan.pieces == 1 : ib >= plan.begin && ib + per <= plan.end;
+  const int mine = plan.cut || ib <= plan.begin ? 0 : 1;  // the item that holds the share's first unit, and the other
+  const size_t slot = (size_t)R * (D + 4);
+  float* part = p.parts + ((size_t)blockIdx.x * 2 + mine) * slot;
+  uint16_t* out0 = p.out + ((size_t)e * p.rows * p.q_heads + (size_t)head * p.group) * D;
+  for (int x = tid; x < R * (D / 4); x += consumers) {
+    const int n = x / (D / 4), d = (x % (D / 4)) * 4;
+    float pm[8], ps[8], m = -INFINITY, l = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      const float2 ml = w < sets ? *reinterpret_cast<const float2*>(ml_of + 2 * (n + w * stride)) : make_float2(-INFINITY, 0.0f);
+      pm[w] = ml.x;
+      ps[w] = ml.y;
+      m = fmaxf(m, ml.x);
+    }
+    float4 o = {0, 0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      if (w >= sets) break;
+      const float f = part_factor(pm[w], ps[w], m);
+      const float4 y = *reinterpret_cast<const float4*>(merge + (size_t)(n + w * stride) * kRow + d);
+      o.x += f * y.x;
+      o.y += f * y.y;
+      o.z += f * y.z;
+      o.w += f * y.w;
+      l += f * ps[w];
+    }
+    if (whole) {
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      *reinterpret_cast<uint2*>(out0 + ((size_t)(n / p.group) * p.q_heads + n % p.group) * D + d) =
+          make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+    } else {
+      *reinterpret_cast<float4*>(part + (size_t)n * D + d) = o;
+      if (d == 0) *reinterpret_cast<float2*>(part + (size_t)R * D + 2 * n) = make_float2(m, l);
+    }
+  }
+  if (whole) return;
+  // CTAs c0 .. c1 share the item; the one that counts in last joins their parts in CTA order
+  const int c0 = plan.cut ? plan.piece0 : ib / plan.share;
+  const int c1 = plan.cut ? plan.piece0 + plan.pieces - 1 : (ib + per - 1) / plan.share;
+  dev::named_barrier_sync(1, consumers);
+  uint32_t* ticket = p.tickets + (size_t)e * p.v.heads + head;
+  if (tid == 0) misc.last = dev::atomic_add_acq_rel_gpu(ticket, 1u) == (uint32_t)(c1 - c0);
+  dev::named_barrier_sync(1, consumers);
+  if (!misc.last) return;
+  if (tid == 0) *ticket = 0u;
+  // The item is the first of each CTA's slots but perhaps of c0's, where it may be the second.
+  const size_t step = 2 * slot;
+  const float* parts = p.parts + (size_t)c0 * step;
+  const size_t first = !plan.cut && ib > c0 * plan.share ? slot : 0;
+  const int np = c1 - c0 + 1, warps = consumers >> 5;
+  const int some = min(R, room / (np + 1));  // queries at a time: np factors and a sum each in the scratch
+  for (int n0 = 0; n0 < R; n0 += some) {
+    const int n1 = min(R, n0 + some);
+    float* sums = merge + some * np;
+    for (int nb = n0 + (tid >> 5); nb < n1; nb += 4 * warps) {  // a warp per query, four of them under way
+      float2 ml[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int n = nb + j * warps;
+        ml[j] = n < n1 && lane < np
+                    ? __ldcg(reinterpret_cast<const float2*>(parts + lane * step + (lane == 0 ? first : 0) + (size_t)R * D + 2 * n))
+                    : make_float2(-INFINITY, 0.0f);
       }
-      if (!whole) {
-        // CTAs c0 .. c1 share the item; the one that counts in last joins their partials in CTA order
-        const int c0 = pl.cut ? pl.piece0 : ib / pl.share, c1 = pl.cut ? pl.piece0 + pl.pieces - 1 : (ib + per - 1) / pl.share;
-        dev::named_barrier_sync(1, consumers);
-        uint32_t* ticket = p.tickets + (size_t)e * v.heads + head;
-        if (tid == 0) misc.last = dev::atomic_add_acq_rel_gpu(ticket, 1u) == (uint32_t)(c1 - c0);
-        dev::named_barrier_sync(1, consumers);
-        if (misc.last) {
-          // a warp per query: lanes hold 32 parts' maxima and sums at a time, then a slice of the head each.
-          // The item is the first of each CTA's slots but perhaps of c0's, where it may be the second.
-          const size_t step = (size_t)2 * R * (D + 2);
-          const float* parts = p.parts + (size_t)c0 * step;
-          const size_t first = !pl.cut && ib > c0 * pl.share ? step / 2 : 0;
-          const int np = c1 - c0 + 1;
-          for (int n = tid >> 5; n < R; n += consumers >> 5) {
-            const float* at = parts + (size_t)n * (D + 2);
-            float m = -INFINITY;
-            for (int c = lane; c < np; c += 32) m = fmaxf(m, __ldcg(at + c * step + (c == 0 ? first : 0)));
-  #pragma unroll
-            for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
-            float l = 0.0f;
-            float2 o[D / 64];
-  #pragma unroll
-            for (int j = 0; j < D / 64; ++j) o[j] = make_float2(0.0f, 0.0f);
-            for (int cc = 0; cc < np; cc += 32) {
-              const int c = cc + lane;
-              float f = 0.0f;
-              if (c < np) {
-                const float2 ml = __ldcg(reinterpret_cast<const float2*>(at + c * step + (c == 0 ? first : 0)));
-                f = part_factor(ml.x, ml.y, m);
-                l += f * ml.y;
-              }
-              const int some = min(32, np - cc);
-  #pragma unroll 8
-              for (int i = 0; i < some; ++i) {
-                const float fi = __shfl_sync(~0u, f, i);
-                const float* from = at + (size_t)(cc + i) * step + (cc + i == 0 ? first : 0) + 2;
-  #pragma unroll
-                for (int j = 0; j < D / 64; ++j) {
-                  const float2 y = __ldcg(reinterpret_cast<const float2*>(from + 64 * j + 2 * lane));
-                  o[j].x += fi * y.x;
-                  o[j].y += fi * y.y;
-                }
-              }
-            }
-  #pragma unroll
-            for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
-            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  #pragma unroll
-            for (int j = 0; j < D / 64; ++j)
-              *reinterpret_cast<uint32_t*>(out0 + ((size_t)(n / p.group) * p.q_heads + n % p.group) * D + 64 * j + 2 * lane) =
-                  pack_bf16(o[j].x * inv, o[j].y * inv);
-          }
-          if (tid == 0) *ticket = 0u;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int n = nb + j * warps;
+        if (n >= n1) break;
+        const float* at = parts + (size_t)R * D + 2 * n;
+        float m = ml[j].x;
+        for (int c = lane + 32; c < np; c += 32) m = fmaxf(m, __ldcg(at + c * step));
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
+        float f = part_factor(ml[j].x, ml[j].y, m), l = f * ml[j].y;
+        if (lane < np) merge[(n - n0) * np + lane] = f;
+        for (int c = lane + 32; c < np; c += 32) {
+          const float2 x = __ldcg(reinterpret_cast<const float2*>(at + c * step));
+          f = part_factor(x.x, x.y, m);
+          l += f * x.y;
+          merge[(n - n0) * np + c] = f;
         }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
+        if (lane == 0) sums[n - n0] = l;
       }
+    }
+    dev::named_barrier_sync(1, consumers);
+    for (int x = tid; x < (n1 - n0) * (D / 4); x += consumers) {
+      const int n = n0 + x / (D / 4), d = (x % (D / 4)) * 4;
+      const float* from = parts + (size_t)n * D + d;
+      const float* fs = merge + (n - n0) * np;
+      float4 o = {0, 0, 0, 0};
+#pragma unroll 8
+      for (int c = 0; c < np; ++c) {
+        const float4 y = __ldcg(reinterpret_cast<const float4*>(from + c * step + (c == 0 ? first : 0)));
+        const float f = fs[c];
+        o.x += f * y.x;
+        o.y += f * y.y;
+        o.z += f * y.z;
+        o.w += f * y.w;
+      }
+      const float l = sums[n - n0], inv = l == 0.0f ? 0.0f : 1.0f / l;
+      *reinterpret_cast<uint2*>(out0 + ((size_t)(n / p.group) * p.q_heads + n % p.group) * D + d) =
+          make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+    }
+    if (n1 < R) dev::named_barrier_sync(1, consumers);
+  }
 }
 
 template <int FMT, int D, int QT>
@@ -745,7 +799,7 @@ __global__ void __launch_bounds__(32 * (max_warps(QT) + 1), 1) attn_kernel(const
     const bool there = len >= 0;
     const Span sp = span_of(there ? len : 0, p.window, p.sinks);
     const bool has_tail = stop == ib + per && there;
-    const int b0 = u - ib, b1 = min(stop - ib, per - 1);
+    const int b0 = u - ib, b1 = min(stop - ib, per - kTailUnits);
     const int seq = p.seqs ? p.seqs[e] : e;
 
     // queries and what their rows see
@@ -834,7 +888,7 @@ __global__ void __launch_bounds__(32 * (max_warps(QT) + 1), 1) attn_kernel(const
       if (tid == 0) flag(v, WOQ_DEVERR_TIMEOUT);
       return;
     }
-    finish<D>(p, misc, pl, merge, warp_ml, WG, G * 8 * QT, e, head, ib, per, tid, consumers);
+    finish<D>(p, misc, pl, merge, W * 8 * QT * kRow, warp_ml, WG, G * 8 * QT, e, head, ib, per, tid, consumers);
     dev::named_barrier_sync(1, consumers);  // the merge buffer is free again
     u = stop;
   }
@@ -1198,7 +1252,7 @@ __global__ void __launch_bounds__(32 * (4 * kTeams + 1), 1) attn_team_kernel(con
     const bool there = len >= 0;
     const Span sp = span_of(there ? len : 0, p.window, p.sinks);
     const bool has_tail = stop == ib + per && there;
-    const int b0 = u - ib, b1 = min(stop - ib, per - 1), blocks = max(0, b1 - b0);
+    const int b0 = u - ib, b1 = min(stop - ib, per - kTailUnits), blocks = max(0, b1 - b0);
     const uint16_t* q0 = p.q + ((size_t)e * p.rows * p.q_heads + (size_t)head * p.group) * D;
 
     // what the rows see
@@ -1326,7 +1380,7 @@ __global__ void __launch_bounds__(32 * (4 * kTeams + 1), 1) attn_team_kernel(con
       if (tid == 0) flag(v, WOQ_DEVERR_TIMEOUT);
       return;
     }
-    finish<D>(p, misc, pl, merge, team_ml, kTeams, kQueries, e, head, ib, per, tid, W * 32);
+    finish<D>(p, misc, pl, merge, kTeams * kQueries * kRow, team_ml, kTeams, kQueries, e, head, ib, per, tid, W * 32);
     dev::named_barrier_sync(1, W * 32);  // the buffers are free again
     u = stop;
   }

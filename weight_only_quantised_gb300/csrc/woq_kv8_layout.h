@@ -102,7 +102,7 @@ struct Kv8Attn {
   const uint32_t* vis;
   uint16_t* out;
   uint32_t* tickets;  // one word per (entry, head), zero between launches
-  float* parts;       // [2 CTAs][rows * group][dim + 2]
+  float* parts;       // two parts per CTA of rows * group * (dim + 4) floats
   float scale_log2;
   int layer, n, rows, q_heads, group, window, sinks;
   int team;          // 1: a team of four warps per block, 0: a warp
