@@ -1,6 +1,8 @@
 // C ABI of the 8-bit cache (include/woq_kv8.h): argument checks, layout and launch shapes.
 #include <math.h>
 
+#include <algorithm>
+
 #include "woq_internal.h"
 #include "woq_kv8_attn.cuh"
 
@@ -110,8 +112,9 @@ bool attn_shape_ok(const Kv8View& v, int n, int rows, int q_heads) {
          (long long)n * v.heads * (v.blocks + kv8::kTailUnits) <= 0x7FFF0000ll;
 }
 
-// Workspace of the attention: [status 256 B][tickets][partials]
-size_t attn_parts_offset(const Kv8View& v, int n) { return 256 + ((size_t)n * v.heads * 4 + 255) / 256 * 256; }
+// Workspace of the attention: [256 B][tickets][where parts are][parts]
+size_t attn_joins_offset(const Kv8View& v, int n) { return 256 + ((size_t)n * v.heads * 4 + 255) / 256 * 256; }
+size_t attn_parts_offset(const Kv8View& v, int n) { return attn_joins_offset(v, n) + ((size_t)n * v.heads * 8 + 255) / 256 * 256; }
 
 }  // namespace
 
@@ -289,6 +292,7 @@ int woq_kv8_attention(const woq_kv8_config* cfg, void* cache, size_t cache_bytes
   p.vis = vis;
   p.out = static_cast<uint16_t*>(out);
   p.tickets = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + 256);
+  p.joins = reinterpret_cast<int2*>(static_cast<uint8_t*>(ws) + attn_joins_offset(v, n));
   p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + attn_parts_offset(v, n));
   p.scale_log2 = (float)((double)scale * 1.4426950408889634);
   p.layer = layer;
@@ -300,6 +304,11 @@ int woq_kv8_attention(const woq_kv8_config* cfg, void* cache, size_t cache_bytes
   p.sinks = sinks;
   const int smem = kv8_attn_plan(&p, smem_max);
   if (smem == 0) return WOQ_ERR_SHAPE;
+  // whether an item can lie in several CTAs: there are more items than CTAs, or one has more units than stay whole
+  // (as far as max_tokens and the window tell)
+  long long most = v.max_tokens / kKv8Block;
+  if (window > 0) most = std::min(most, ((long long)window + kKv8Block - 1) / kKv8Block + 1 + ((long long)sinks + kKv8Block - 1) / kKv8Block);
+  p.joined = (long long)n * v.heads > sms || most + kv8::kTailUnits > kv8::kWhole;
   const bool int8 = v.fmt == WOQ_KV8_INT8;
   const auto launch = p.team ? (int8 ? launch_kv8_team_int8 : launch_kv8_team_e4m3)
                              : (int8 ? launch_kv8_attn_int8 : launch_kv8_attn_e4m3);

@@ -421,11 +421,12 @@ struct Misc {
   uint64_t full[kMaxStages], empty[kMaxStages];
   int fail, last;
   int share;      // units of a piece, 0: more items than CTAs
+  int redo;       // the plan made before the wait does not hold
   // [n + 1] units of one head of the entries before, [n] lengths (-1: out of range), [n + 1] pieces (CTAs) of
-  // the entries before
+  // the entries before, [n] sequence numbers (if they are given)
   int entries[];
 };
-__host__ __device__ inline int misc_bytes(int n) { return (int)((sizeof(Misc) + (size_t)(3 * n + 2) * 4 + 127) / 128 * 128); }
+__host__ __device__ inline int misc_bytes(int n) { return (int)((sizeof(Misc) + (size_t)(4 * n + 2) * 4 + 127) / 128 * 128); }
 constexpr int kWhole = 32;  // units of an item that is not cut
 
 __device__ __forceinline__ int pieces_of(int units, int share) { return units <= kWhole ? 1 : (units + share - 1) / share; }
@@ -440,6 +441,7 @@ __device__ __forceinline__ float part_factor(float pm, float pl, float m) {
 }
 
 __device__ __forceinline__ int* lens_of(const Kv8Attn& p, Misc& misc) { return misc.entries + p.n + 1; }
+__device__ __forceinline__ int* seqs_of(const Kv8Attn& p, Misc& misc) { return misc.entries + 3 * p.n + 2; }
 
 // This CTA's units [begin, end), of all items laid end to end.  All counts fit 32 bits (checked on the host).
 struct Plan {
@@ -449,129 +451,101 @@ struct Plan {
   int share;           // else: units of a CTA
 };
 
-// Waits for the prior grid, reads the lengths and finds this CTA's share; false: nothing to do.  All threads.
-__device__ __forceinline__ bool make_plan(const Kv8Attn& p, Misc& misc, int tid, Plan& pl) {
+// Number of entry e's sequence; its length, -1 if the number is out of range.
+__device__ __forceinline__ int number_of(const Kv8Attn& p, int e) { return p.seqs ? (int)dev::ld_relaxed_u32(p.seqs + e) : e; }
+__device__ __forceinline__ int length_of(const Kv8Attn& p, int seq) {
+  return seq >= 0 && seq < p.v.seqs ? (int)dev::ld_relaxed_u32(p.v.lens_p() + seq) : -1;
+}
+__device__ __forceinline__ bool is_ours(const Kv8View& v, uint32_t* magic) {
+  *magic = dev::ld_relaxed_u32(v.status() + 1);
+  return dev::ld_relaxed_u32(v.status() + 2) == v.hash && *magic == kKv8Magic;
+}
+
+// Reads the lengths and lays out the units and pieces of the entries.  Warp 0; lengths out of range (a cache
+// that is being changed, before the wait for who changes it) count as 0.
+__device__ __forceinline__ void lay_out(const Kv8Attn& p, Misc& misc, int lane) {
   const Kv8View& v = p.v;
-  const int lane = tid & 31, warp = tid >> 5;
   int* lens = lens_of(p, misc);
   int* cuts = lens + p.n;
-  begin_after_prior();
-  // lengths and units of the entries (the header's check is read beside them, not before)
-  const uint4 header = *reinterpret_cast<const uint4*>(v.base);
-  const bool ours = header.y == kKv8Magic && header.z == v.hash;
-  if (p.n == 1) {  // one sequence: every thread works it out for itself
-    const int seq = p.seqs ? p.seqs[0] : 0;
-    const bool there = seq >= 0 && seq < v.seqs;
-    const int len = there ? v.lens_p()[seq] : -1;
-    if (!ours) {
-      if (header.y == kKv8Magic && tid == 0) flag(v, WOQ_DEVERR_HEADER);
-      return false;
+  const int ctas = (int)gridDim.x;
+  int run = 0;
+  for (int e0 = 0; e0 < p.n; e0 += 32) {
+    const int e = e0 + lane;
+    int units = 0;
+    if (e < p.n) {
+      const int seq = number_of(p, e);
+      int len = length_of(p, seq);
+      if (len > v.max_tokens) len = 0;
+      if (len < -1) len = -1;
+      lens[e] = len;
+      if (p.seqs) seqs_of(p, misc)[e] = seq;
+      units = len >= 0 ? span_of(len, p.window, p.sinks).units : kTailUnits;
     }
-    if (!there && blockIdx.x == 0 && tid == 0) flag(v, WOQ_DEVERR_STATE);
-    const int per = there ? span_of(len, p.window, p.sinks).units : kTailUnits;
-    if (tid == 0) {
-      misc.entries[0] = 0;
-      misc.entries[1] = per;
-      lens[0] = len;
+    int y = units;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int z = __shfl_up_sync(~0u, y, d);
+      if (lane >= d) y += z;
     }
-    __syncthreads();
-    const int ctas = (int)gridDim.x;
-    if (v.heads <= ctas) {
-      const int room = ctas / v.heads, share = max(p.least_units, (per + room - 1) / room);
-      const int pieces = pieces_of(per, share), head = (int)blockIdx.x / pieces, j = (int)blockIdx.x - head * pieces;
-      if (head >= v.heads) return false;
-      pl = Plan{head * per + (int)((long long)per * j / pieces), head * per + (int)((long long)per * (j + 1) / pieces), true,
-                (int)blockIdx.x - j, pieces, 0};
-      return true;
-    }
-    const int share = max(p.least_units, (per * v.heads + ctas - 1) / ctas), begin = (int)blockIdx.x * share;
-    if (begin >= per * v.heads) return false;
-    pl = Plan{begin, min(begin + share, per * v.heads), false, 0, 0, share};
-    return true;
+    if (e < p.n) misc.entries[e] = run + y - units;
+    run += __shfl_sync(~0u, y, 31);
   }
-  if (warp == 0) {
-    int run = 0;
+  if (lane == 0) misc.entries[p.n] = run;
+  // The least share with which all pieces have a CTA, to 1/32: the lanes try 32 of them at once.
+  int share = 0;
+  if (p.n * v.heads <= ctas) {
+    __syncwarp();
+    const int room = ctas / v.heads;  // pieces of one head
+    share = max(p.least_units, (run + room - 1) / room);
+    while (p.n > 1) {  // ends: with a share beyond the longest item there are n <= room pieces
+      const int mine = share + (int)((long long)share * lane / 32);
+      int total = 0;
+      for (int e = 0; e < p.n; ++e) total += pieces_of(misc.entries[e + 1] - misc.entries[e], mine);
+      const uint32_t fits = __ballot_sync(~0u, total <= room);
+      share = __shfl_sync(~0u, mine, fits ? __ffs((int)fits) - 1 : 31);
+      if (fits) break;
+      ++share;
+    }
+    int total = 0;
     for (int e0 = 0; e0 < p.n; e0 += 32) {
       const int e = e0 + lane;
-      int units = 0;
-      if (e < p.n) {
-        const int seq = p.seqs ? p.seqs[e] : e;
-        const bool there = seq >= 0 && seq < v.seqs;
-        if (!there && ours && blockIdx.x == 0) flag(v, WOQ_DEVERR_STATE);
-        lens[e] = there ? v.lens_p()[seq] : -1;
-        units = there ? span_of(lens[e], p.window, p.sinks).units : kTailUnits;
-      }
-      int y = units;
+      int y = e < p.n ? pieces_of(misc.entries[e + 1] - misc.entries[e], share) : 0;
+      const int own = y;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const int z = __shfl_up_sync(~0u, y, d);
         if (lane >= d) y += z;
       }
-      if (e < p.n) misc.entries[e] = run + y - units;
-      run += __shfl_sync(~0u, y, 31);
+      if (e < p.n) cuts[e] = (total + y - own) * v.heads;
+      total += __shfl_sync(~0u, y, 31);
     }
-    if (lane == 0) misc.entries[p.n] = run;
-    // The least share with which all pieces have a CTA, to 1/32: the lanes try 32 of them at once.
-    int share = 0;
-    if (ours && p.n * v.heads <= (int)gridDim.x) {
-      __syncwarp();
-      const int room = (int)gridDim.x / v.heads;  // pieces of one head
-      share = max(p.least_units, (run + room - 1) / room);
-      for (;;) {  // ends: with a share beyond the longest item there are n <= room pieces
-        const int mine = share + (int)((long long)share * lane / 32);
-        int total = 0;
-        for (int e = 0; e < p.n; ++e) total += pieces_of(misc.entries[e + 1] - misc.entries[e], mine);
-        const uint32_t fits = __ballot_sync(~0u, total <= room);
-        share = __shfl_sync(~0u, mine, fits ? __ffs((int)fits) - 1 : 31);
-        if (fits) break;
-        ++share;
-      }
-      int total = 0;
-      for (int e0 = 0; e0 < p.n; e0 += 32) {
-        const int e = e0 + lane;
-        int y = e < p.n ? pieces_of(misc.entries[e + 1] - misc.entries[e], share) : 0;
-        const int own = y;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const int z = __shfl_up_sync(~0u, y, d);
-          if (lane >= d) y += z;
-        }
-        if (e < p.n) cuts[e] = (total + y - own) * v.heads;
-        total += __shfl_sync(~0u, y, 31);
-      }
-      if (lane == 0) cuts[p.n] = total * v.heads;
-    }
-    if (lane == 0) misc.share = share;
+    if (lane == 0) cuts[p.n] = total * v.heads;
   }
-  if (!ours) {
-    if (header.y == kKv8Magic && tid == 0) flag(v, WOQ_DEVERR_HEADER);
-    return false;
-  }
-  __syncthreads();
-  // this CTA's units [begin, end), of all items laid end to end; all counts fit 32 bits (checked on the host)
-  const bool cut = misc.share > 0;
-  int begin, end, share = 0, piece0 = 0, pieces = 0;
-  if (cut) {
-    if ((int)blockIdx.x >= cuts[p.n]) return false;
+  if (lane == 0) misc.share = share;
+}
+
+// This CTA's share of what lay_out left; false: none.
+__device__ __forceinline__ bool take_share(const Kv8Attn& p, Misc& misc, Plan& pl) {
+  const int heads = p.v.heads, block = (int)blockIdx.x;
+  const int* cuts = lens_of(p, misc) + p.n;
+  if (misc.share > 0) {
+    if (block >= cuts[p.n]) return false;
     int lo = 0, hi = p.n - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (cuts[mid] <= (int)blockIdx.x) lo = mid; else hi = mid - 1;
+      if (cuts[mid] <= block) lo = mid; else hi = mid - 1;
     }
-    const int per = misc.entries[lo + 1] - misc.entries[lo];
-    pieces = (cuts[lo + 1] - cuts[lo]) / v.heads;
-    const int head = ((int)blockIdx.x - cuts[lo]) / pieces, j = ((int)blockIdx.x - cuts[lo]) % pieces;
-    piece0 = (int)blockIdx.x - j;
-    begin = misc.entries[lo] * v.heads + head * per + (int)((long long)per * j / pieces);
-    end = misc.entries[lo] * v.heads + head * per + (int)((long long)per * (j + 1) / pieces);
-  } else {
-    const int units = misc.entries[p.n] * v.heads;
-    share = max(p.least_units, (units + (int)gridDim.x - 1) / (int)gridDim.x);
-    begin = (int)blockIdx.x * share;
-    end = min(begin + share, units);
-    if (begin >= units) return false;
+    const int per = misc.entries[lo + 1] - misc.entries[lo], pieces = (cuts[lo + 1] - cuts[lo]) / heads;
+    const int head = (block - cuts[lo]) / pieces, j = block - cuts[lo] - head * pieces;
+    const int first = misc.entries[lo] * heads + head * per;
+    pl = Plan{first + (int)((long long)per * j / pieces), first + (int)((long long)per * (j + 1) / pieces), true, block - j,
+              pieces, 0};
+    return true;
   }
-  pl = Plan{begin, end, cut, piece0, pieces, share};
+  const int units = misc.entries[p.n] * heads;
+  const int share = max(p.least_units, (units + (int)gridDim.x - 1) / (int)gridDim.x), begin = block * share;
+  if (begin >= units) return false;
+  pl = Plan{begin, min(begin + share, units), false, 0, 0, share};
   return true;
 }
 
@@ -587,6 +561,73 @@ __device__ __forceinline__ void locate(const Kv8Attn& p, const Misc& misc, int u
   *entry = lo;
   *head = (u - first) / per;
   *item_begin = first + *head * per;
+}
+
+// The records that fill the ring first, the queries and the tail, into L2.  One warp; nothing read here is relied on, so
+// numbers are only used if they are in range.
+__device__ __forceinline__ void prefetch_first(const Kv8Attn& p, Misc& misc, const Plan& pl, int lane) {
+  const Kv8View& v = p.v;
+  int e, head, ib;
+  locate(p, misc, pl.begin, &e, &head, &ib);
+  const int per = misc.entries[e + 1] - misc.entries[e], len = lens_of(p, misc)[e];
+  const int seq = p.seqs ? (int)dev::ld_relaxed_u32(p.seqs + e) : e;
+  if (len < 0 || seq < 0 || seq >= v.seqs) return;
+  const Span sp = span_of(len, p.window, p.sinks);
+  const int k = pl.begin - ib + lane, stop = min(pl.end - ib, per - kTailUnits);
+  if (lane < p.stages && k < stop) {
+    const int page = (int)dev::ld_relaxed_u32(v.table_row(seq) + (k < sp.head_blocks ? k : sp.from + (k - sp.head_blocks)));
+    if (page >= 0 && page < v.pages) dev::bulk_prefetch_l2(v.record(page, p.layer, head), (uint32_t)v.record_bytes());
+  }
+  const size_t q_bytes = (size_t)p.group * v.dim * 2;  // of one row
+  for (size_t x = (size_t)lane * 128; x < q_bytes * p.rows; x += 32 * 128)
+    dev::prefetch_l2(reinterpret_cast<const uint8_t*>(p.q) + (((size_t)e * p.rows + x / q_bytes) * p.q_heads * v.dim +
+                                                              (size_t)head * p.group * v.dim) * 2 + x % q_bytes);
+  if (lane == 31 && pl.end >= ib + per) dev::bulk_prefetch_l2(v.tail(p.layer, seq, head), (uint32_t)v.tail_elems() * 2u);
+}
+
+// This CTA's plan; false: nothing to do.  All threads.
+//
+// The chain sequence number, length, page number, record is four dependent reads, most of them from
+// HBM.  So before the wait for the prior grid the plan is made from what the cache holds then, and the first
+// records are brought into L2; after the wait the lengths are read again and, if one has changed,
+// the plan is made anew.  (In a step the CTA gets its SM while the grid before it ends; nothing but the
+// plan is kept from before the wait, and that is checked.)
+__device__ __forceinline__ bool make_plan(const Kv8Attn& p, Misc& misc, int tid, Plan& pl) {
+  const Kv8View& v = p.v;
+  const int lane = tid & 31, warp = tid >> 5;
+  uint32_t magic;
+  const bool guessed = __syncthreads_and(is_ours(v, &magic));
+  bool active = false;
+  if (guessed) {
+    if (warp == 0) lay_out(p, misc, lane);
+    __syncthreads();
+    active = take_share(p, misc, pl);
+    if (active && warp == p.warps) prefetch_first(p, misc, pl, lane);
+  }
+  begin_after_prior();
+  const bool ours = is_ours(v, &magic);
+  if (warp == 0) {
+    bool same = guessed;
+    for (int e = lane; e < p.n; e += 32) {
+      const int seq = number_of(p, e), before = guessed ? (p.seqs ? seqs_of(p, misc)[e] : e) : seq;
+      const int len = length_of(p, before);  // beside the number's read, not behind it
+      if (guessed) same &= seq == before && len == lens_of(p, misc)[e];
+      if (ours && (seq < 0 || seq >= v.seqs) && blockIdx.x == 0) flag(v, WOQ_DEVERR_STATE);
+    }
+    same = __all_sync(~0u, same);
+    if (lane == 0) misc.redo = !same;
+  }
+  if (!ours) {
+    if (magic == kKv8Magic && tid == 0) flag(v, WOQ_DEVERR_HEADER);
+    return false;
+  }
+  __syncthreads();
+  if (misc.redo) {
+    if (warp == 0) lay_out(p, misc, lane);
+    __syncthreads();
+    active = take_share(p, misc, pl);
+  }
+  return active;
 }
 
 // The producer warp: the records of this CTA's blocks, in order, into the ring's stages.
@@ -641,8 +682,11 @@ __device__ __forceinline__ void produce(const Kv8Attn& p, Misc& misc, const Plan
 // shared memory: set w, query n at row n + w * stride of merge ([D] floats) and of ml_of (maximum, sum).
 // merge holds `room` floats and is scratch afterwards.  All consumers; the caller has synchronised them.
 //
+// Joining parts is one CTA's work while the others have ended, so what counts is how many loads are under way.
 // A part in p.parts: [R][D] values, [R][2] maxima and sums, in steps of R (D + 4) floats; two slots a CTA.
-template <int D>
+//
+// LATER: parts are left for join_kernel, and the CTA that has the item's first unit says where they are.
+template <int D, bool LATER>
 __device__ __forceinline__ void finish(const Kv8Attn& p, Misc& misc, const Plan& plan, float* merge, int room,
                                        const float* ml_of, int sets, int stride, int e, int head, int ib, int per, int tid,
                                        int consumers) {
@@ -684,7 +728,12 @@ __device__ __forceinline__ void finish(const Kv8Attn& p, Misc& misc, const Plan&
       if (d == 0) *reinterpret_cast<float2*>(part + (size_t)R * D + 2 * n) = make_float2(m, l);
     }
   }
-  if (whole) return;
+  if (LATER && tid == 0 && ib >= plan.begin) {
+    const int c0 = (int)blockIdx.x;
+    const int pieces = whole ? 1 : plan.cut ? plan.pieces : (ib + per - 1) / plan.share - c0 + 1;
+    p.joins[(size_t)e * p.v.heads + head] = make_int2(2 * c0 + mine, pieces);
+  }
+  if (whole || LATER) return;
   // CTAs c0 .. c1 share the item; the one that counts in last joins their parts in CTA order
   const int c0 = plan.cut ? plan.piece0 : ib / plan.share;
   const int c1 = plan.cut ? plan.piece0 + plan.pieces - 1 : (ib + per - 1) / plan.share;
@@ -700,9 +749,17 @@ __device__ __forceinline__ void finish(const Kv8Attn& p, Misc& misc, const Plan&
   const size_t first = !plan.cut && ib > c0 * plan.share ? slot : 0;
   const int np = c1 - c0 + 1, warps = consumers >> 5;
   const int some = min(R, room / (np + 1));  // queries at a time: np factors and a sum each in the scratch
+  constexpr int kAhead = 20;  // loads under way per thread, the first unit's before the maxima and sums are read
+  float4 ahead[kAhead];
   for (int n0 = 0; n0 < R; n0 += some) {
     const int n1 = min(R, n0 + some);
     float* sums = merge + some * np;
+    const float* values = parts + (size_t)n0 * D;
+    if (tid < (n1 - n0) * (D / 4)) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (i < np) ahead[i] = __ldcg(reinterpret_cast<const float4*>(values + 4 * tid + i * step + (i == 0 ? first : 0)));
+    }
     for (int nb = n0 + (tid >> 5); nb < n1; nb += 4 * warps) {  // a warp per query, four of them under way
       float2 ml[4];
 #pragma unroll
@@ -737,18 +794,24 @@ __device__ __forceinline__ void finish(const Kv8Attn& p, Misc& misc, const Plan&
     dev::named_barrier_sync(1, consumers);
     for (int x = tid; x < (n1 - n0) * (D / 4); x += consumers) {
       const int n = n0 + x / (D / 4), d = (x % (D / 4)) * 4;
-      const float* from = parts + (size_t)n * D + d;
       const float* fs = merge + (n - n0) * np;
       float4 o = {0, 0, 0, 0};
-#pragma unroll 8
-      for (int c = 0; c < np; ++c) {
-        const float4 y = __ldcg(reinterpret_cast<const float4*>(from + c * step + (c == 0 ? first : 0)));
-        const float f = fs[c];
+      auto add = [&](float f, const float4& y) {
         o.x += f * y.x;
         o.y += f * y.y;
         o.z += f * y.z;
         o.w += f * y.w;
+      };
+      const float* from = values + 4 * x;
+      int c = 0;
+      if (x == tid) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+          if (i < np) add(fs[i], ahead[i]);
+        c = min(kAhead, np);
       }
+#pragma unroll 8
+      for (; c < np; ++c) add(fs[c], __ldcg(reinterpret_cast<const float4*>(from + c * step + (c == 0 ? first : 0))));
       const float l = sums[n - n0], inv = l == 0.0f ? 0.0f : 1.0f / l;
       *reinterpret_cast<uint2*>(out0 + ((size_t)(n / p.group) * p.q_heads + n % p.group) * D + d) =
           make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
@@ -888,7 +951,7 @@ __global__ void __launch_bounds__(32 * (max_warps(QT) + 1), 1) attn_kernel(const
       if (tid == 0) flag(v, WOQ_DEVERR_TIMEOUT);
       return;
     }
-    finish<D>(p, misc, pl, merge, W * 8 * QT * kRow, warp_ml, WG, G * 8 * QT, e, head, ib, per, tid, consumers);
+    finish<D, false>(p, misc, pl, merge, W * 8 * QT * kRow, warp_ml, WG, G * 8 * QT, e, head, ib, per, tid, consumers);
     dev::named_barrier_sync(1, consumers);  // the merge buffer is free again
     u = stop;
   }
@@ -1118,6 +1181,25 @@ __device__ void team_tail(TeamState<D, NT>& st, TeamShared<NT>& ts, const uint16
   const bool mine = !over || wi == 0;  // this warp has tokens
   const int r0 = over ? 64 + g : 16 * (g >> 1) + 4 * wi + (g & 1), r1 = over ? kKv8Tail : r0 + 2;
   const int R = p.rows * p.group;
+  // every load is issued before the first product: they go to L2 or HBM, one round trip instead of one each
+  const uint16_t* tv = tail + kKv8Tail * D + wi * (D / 4) * kKv8Tail;
+  uint4 vx[D / 64][2], vy[D / 64][2];
+#pragma unroll
+  for (int j = 0; j < D / 64; ++j) {
+    const uint16_t* v0 = tv + (16 * j + g) * kKv8Tail;
+    const uint16_t* v1 = v0 + 8 * kKv8Tail;
+    vx[j][0] = vx[j][1] = vy[j][0] = vy[j][1] = make_uint4(0, 0, 0, 0);
+    if (over) {
+      vx[j][0].x = *reinterpret_cast<const uint32_t*>(v0 + 64 + 2 * t);
+      vy[j][0].x = *reinterpret_cast<const uint32_t*>(v1 + 64 + 2 * t);
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        vx[j][h] = *reinterpret_cast<const uint4*>(v0 + 16 * t + 8 * h);
+        vy[j][h] = *reinterpret_cast<const uint4*>(v1 + 16 * t + 8 * h);
+      }
+    }
+  }
   float s[NT][4];
 #pragma unroll
   for (int q = 0; q < NT; ++q)
@@ -1126,28 +1208,26 @@ __device__ void team_tail(TeamState<D, NT>& st, TeamShared<NT>& ts, const uint16
   if (mine) {
 #pragma unroll
     for (int c = 0; c < D / 64; ++c) {
-      uint32_t x[8], y[8];
+      uint4 x[2], y[2], w[NT][2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        uint4 a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
-        if (r0 < there) a = *reinterpret_cast<const uint4*>(tail + r0 * D + 16 * (4 * c + t) + 8 * h);
-        if (r1 < there) b = *reinterpret_cast<const uint4*>(tail + r1 * D + 16 * (4 * c + t) + 8 * h);
-        x[4 * h] = a.x, x[4 * h + 1] = a.y, x[4 * h + 2] = a.z, x[4 * h + 3] = a.w;
-        y[4 * h] = b.x, y[4 * h + 1] = b.y, y[4 * h + 2] = b.z, y[4 * h + 3] = b.w;
+        const int d = 16 * (4 * c + t) + 8 * h;
+        x[h] = y[h] = make_uint4(0, 0, 0, 0);
+        if (r0 < there) x[h] = *reinterpret_cast<const uint4*>(tail + r0 * D + d);
+        if (r1 < there) y[h] = *reinterpret_cast<const uint4*>(tail + r1 * D + d);
+#pragma unroll
+        for (int q = 0; q < NT; ++q) {
+          const int n = min(8 * q + g, R - 1);  // columns from R on repeat the last query (their results are not used)
+          w[q][h] = *reinterpret_cast<const uint4*>(q0 + ((size_t)(n / p.group) * p.q_heads + n % p.group) * D + d);
+        }
       }
 #pragma unroll
-      for (int q = 0; q < NT; ++q) {
-        const int n = 8 * q + g;
-        const uint16_t* qr = n < R ? q0 + ((size_t)(n / p.group) * p.q_heads + n % p.group) * D : nullptr;
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t a0[4] = {x[h].x, y[h].x, x[h].y, y[h].y}, a1[4] = {x[h].z, y[h].z, x[h].w, y[h].w};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint4 b = {0, 0, 0, 0};
-          if (qr) b = *reinterpret_cast<const uint4*>(qr + 16 * (4 * c + t) + 8 * h);
-          const uint32_t a0[4] = {x[4 * h], y[4 * h], x[4 * h + 1], y[4 * h + 1]};
-          const uint32_t a1[4] = {x[4 * h + 2], y[4 * h + 2], x[4 * h + 3], y[4 * h + 3]};
-          mma_bf16(s[q], a0, b.x, b.y);
-          mma_bf16(s[q], a1, b.z, b.w);
-        }
+        for (int q = 0; q < NT; ++q) mma_bf16(s[q], a0, w[q][h].x, w[q][h].y);
+#pragma unroll
+        for (int q = 0; q < NT; ++q) mma_bf16(s[q], a1, w[q][h].z, w[q][h].w);
       }
     }
 #pragma unroll
@@ -1176,35 +1256,21 @@ __device__ void team_tail(TeamState<D, NT>& st, TeamShared<NT>& ts, const uint16
     }
   }
   team_sync(team);
-  const uint16_t* tv = tail + kKv8Tail * D + wi * (D / 4) * kKv8Tail;
 #pragma unroll
-  for (int j = 0; j < D / 64; ++j) {
-    const uint16_t* v0 = tv + (16 * j + g) * kKv8Tail;
-    const uint16_t* v1 = v0 + 8 * kKv8Tail;
-    uint4 x[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}}, y[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-    if (over) {
-      x[0].x = *reinterpret_cast<const uint32_t*>(v0 + 64 + 2 * t);
-      y[0].x = *reinterpret_cast<const uint32_t*>(v1 + 64 + 2 * t);
-    } else {
+  for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        x[h] = *reinterpret_cast<const uint4*>(v0 + 16 * t + 8 * h);
-        y[h] = *reinterpret_cast<const uint4*>(v1 + 16 * t + 8 * h);
-      }
-    }
+    for (int part = 0; part < 2; ++part)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t a0[4] = {x[h].x, y[h].x, x[h].y, y[h].y}, a1[4] = {x[h].z, y[h].z, x[h].w, y[h].w};
+      for (int q = 0; q < NT; ++q) {
+        const uint4 b = ts.weights[part][q][h][lane];
 #pragma unroll
-      for (int q = 0; q < NT; ++q)
-#pragma unroll
-        for (int part = 0; part < 2; ++part) {
-          const uint4 b = ts.weights[part][q][h][lane];
+        for (int j = 0; j < D / 64; ++j) {
+          const uint32_t a0[4] = {vx[j][h].x, vy[j][h].x, vx[j][h].y, vy[j][h].y};
+          const uint32_t a1[4] = {vx[j][h].z, vy[j][h].z, vx[j][h].w, vy[j][h].w};
           mma_bf16(st.o[j][q], a0, b.x, b.y);
           mma_bf16(st.o[j][q], a1, b.z, b.w);
         }
-    }
-  }
+      }
   team_sync(team);  // the buffers are free again
 }
 
@@ -1380,10 +1446,82 @@ __global__ void __launch_bounds__(32 * (4 * kTeams + 1), 1) attn_team_kernel(con
       if (tid == 0) flag(v, WOQ_DEVERR_TIMEOUT);
       return;
     }
-    finish<D>(p, misc, pl, merge, kTeams * kQueries * kRow, team_ml, kTeams, kQueries, e, head, ib, per, tid, W * 32);
+    finish<D, true>(p, misc, pl, merge, kTeams * kQueries * kRow, team_ml, kTeams, kQueries, e, head, ib, per, tid, W * 32);
     dev::named_barrier_sync(1, W * 32);  // the buffers are free again
     u = stop;
   }
+}
+
+// The parts that attn_team_kernel left, joined: a warp per query, grid (items, queries / kJoinWarps).  With 12 to 40
+// queries one CTA alone takes 5 to 13 us over an item's parts (up to 0.4 MB) while the others have ended.
+constexpr int kJoinWarps = 4;
+
+template <int D>
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ Kv8Attn p) {
+  begin_after_prior();
+  uint32_t magic;
+  if (!is_ours(p.v, &magic)) return;  // nothing was left
+  const int R = p.rows * p.group, lane = threadIdx.x & 31, n = (int)blockIdx.y * kJoinWarps + ((int)threadIdx.x >> 5);
+  const int2 where = p.joins[blockIdx.x];
+  const int np = where.y;
+  if (np <= 1 || n >= R) return;
+  // the first part's slot, and the first slots of the CTAs that follow
+  const size_t slot = (size_t)R * (D + 4), step = 2 * slot;
+  const float* parts = p.parts + (size_t)(where.x >> 1) * step;
+  const size_t first = (where.x & 1) ? slot : 0;
+  constexpr int kLanes = D / 4;  // lanes that hold four elements each
+  const float* at = parts + (size_t)R * D + 2 * n;
+  const float* from = parts + (size_t)n * D + 4 * (lane % kLanes);
+  constexpr int kAhead = 20;
+  float4 y[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i)
+    if (i < np) y[i] = __ldcg(reinterpret_cast<const float4*>(from + i * step + (i == 0 ? first : 0)));
+  float m = -INFINITY;
+  for (int c = lane; c < np; c += 32) m = fmaxf(m, __ldcg(at + c * step + (c == 0 ? first : 0)));
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
+  float4 o = {0, 0, 0, 0};
+  float l = 0.0f;
+  for (int cc = 0; cc < np; cc += 32) {
+    const int c = cc + lane;
+    float f = 0.0f;
+    if (c < np) {
+      const float2 ml = __ldcg(reinterpret_cast<const float2*>(at + c * step + (c == 0 ? first : 0)));
+      f = part_factor(ml.x, ml.y, m);
+      l += f * ml.y;
+    }
+    const int some = min(32, np - cc);
+    auto add = [&](int i, const float4& v) {
+      const float fi = __shfl_sync(~0u, f, i);
+      o.x += fi * v.x;
+      o.y += fi * v.y;
+      o.z += fi * v.z;
+      o.w += fi * v.w;
+    };
+    int i = 0;
+    if (cc == 0) {
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (k < some) add(k, y[k]);
+      i = min(some, kAhead);
+    }
+#pragma unroll 4
+    for (; i < some; ++i) add(i, __ldcg(reinterpret_cast<const float4*>(from + (cc + i) * step)));
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const int e = (int)blockIdx.x / p.v.heads, head = (int)blockIdx.x % p.v.heads;
+  uint16_t* out = p.out + (((size_t)e * p.rows + n / p.group) * p.q_heads + (size_t)head * p.group + n % p.group) * D;
+  if (lane < kLanes)
+    *reinterpret_cast<uint2*>(out + 4 * lane) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+}
+
+template <int D>
+cudaError_t launch_join(const Kv8Attn& p, cudaStream_t stream) {
+  const dim3 grid((unsigned)(p.n * p.v.heads), (unsigned)((p.rows * p.group + kJoinWarps - 1) / kJoinWarps));
+  return launch(join_kernel<D>, grid, 32 * kJoinWarps, 0, stream, p);
 }
 
 template <void (*KERNEL)(Kv8Attn)>
@@ -1414,19 +1552,22 @@ cudaError_t launch_attn_any(const Kv8Attn& p, int ctas, int smem, cudaStream_t s
   }
 }
 
+template <int FMT, int D>
+cudaError_t launch_team_dim(const Kv8Attn& p, int ctas, int smem, cudaStream_t s) {
+  cudaError_t e = cudaErrorInvalidValue;
+  switch (p.tiles) {
+    case 2: e = launch_attn<attn_team_kernel<FMT, D, 2>>(p, ctas, smem, s); break;
+    case 3: e = launch_attn<attn_team_kernel<FMT, D, 3>>(p, ctas, smem, s); break;
+    case 4: e = launch_attn<attn_team_kernel<FMT, D, 4>>(p, ctas, smem, s); break;
+    case 5: e = launch_attn<attn_team_kernel<FMT, D, 5>>(p, ctas, smem, s); break;
+    default: break;
+  }
+  return e != cudaSuccess || !p.joined ? e : launch_join<D>(p, s);
+}
+
 template <int FMT>
 cudaError_t launch_team_any(const Kv8Attn& p, int ctas, int smem, cudaStream_t s) {
-  switch (p.v.dim * 8 + p.tiles) {
-    case 64 * 8 + 2: return launch_attn<attn_team_kernel<FMT, 64, 2>>(p, ctas, smem, s);
-    case 64 * 8 + 3: return launch_attn<attn_team_kernel<FMT, 64, 3>>(p, ctas, smem, s);
-    case 64 * 8 + 4: return launch_attn<attn_team_kernel<FMT, 64, 4>>(p, ctas, smem, s);
-    case 64 * 8 + 5: return launch_attn<attn_team_kernel<FMT, 64, 5>>(p, ctas, smem, s);
-    case 128 * 8 + 2: return launch_attn<attn_team_kernel<FMT, 128, 2>>(p, ctas, smem, s);
-    case 128 * 8 + 3: return launch_attn<attn_team_kernel<FMT, 128, 3>>(p, ctas, smem, s);
-    case 128 * 8 + 4: return launch_attn<attn_team_kernel<FMT, 128, 4>>(p, ctas, smem, s);
-    case 128 * 8 + 5: return launch_attn<attn_team_kernel<FMT, 128, 5>>(p, ctas, smem, s);
-    default: return cudaErrorInvalidValue;
-  }
+  return p.v.dim == 64 ? launch_team_dim<FMT, 64>(p, ctas, smem, s) : launch_team_dim<FMT, 128>(p, ctas, smem, s);
 }
 
 }  // namespace kv8

@@ -102,9 +102,11 @@ struct Kv8Attn {
   const uint32_t* vis;
   uint16_t* out;
   uint32_t* tickets;  // one word per (entry, head), zero between launches
+  int2* joins;        // of each (entry, head): twice the first CTA with a part (+ 1: its second slot), number of parts
   float* parts;       // two parts per CTA of rows * group * (dim + 4) floats
   float scale_log2;
   int layer, n, rows, q_heads, group, window, sinks;
+  int joined;        // 0: no item lies in several CTAs
   int team;          // 1: a team of four warps per block, 0: a warp
   int tiles;         // tiles of 8 queries of a warp (of a team)
   int warps, query_groups, stages;
