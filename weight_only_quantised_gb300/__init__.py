@@ -573,7 +573,10 @@ def woq_kv8_plan_attention(cfg: KV8Config, n: int, rows: int, q_heads: int, sms:
 
 
 def _cache_args(cfg: KV8Config, cache):
-    return ctypes.byref(cfg), _dptr(cache, "cache", 1), _nbytes(cache)
+    device = -1 if cache is None else cache.get_device()
+    if device < 0 or device != _current_device() or not cache.is_contiguous() or cache.element_size() != 1:
+        return ctypes.byref(cfg), _dptr(cache, "cache", 1), _nbytes(cache)
+    return ctypes.byref(cfg), cache.data_ptr(), cache.nbytes
 
 
 _DTYPES = {}  # element type -> the torch dtypes that hold it (bound on first use)
@@ -592,7 +595,8 @@ def _typed(t, name: str, kind: str, numel: int):
         return None
     if t.dtype not in (_DTYPES.get(kind) or _dtypes(kind)):
         raise ValueError(f"{name}: expected {kind}, got {t.dtype}")
-    if not (t.is_cuda and t.is_contiguous() and t.get_device() == _current_device()) or t.numel() < numel:
+    device = t.get_device()  # -1 on the host
+    if device < 0 or device != _current_device() or not t.is_contiguous() or t.numel() < numel:
         return _dptr(t, name, 0, numel)  # says what is wrong
     return t.data_ptr()
 

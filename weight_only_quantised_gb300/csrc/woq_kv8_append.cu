@@ -216,8 +216,8 @@ struct BlockShared {
 // Scales and codes of the block in kt, vt (shared memory) into rec.  All threads; barriers inside.
 // bad: some row is not finite (its key NaN, its value 0): the key scale is NaN, so that every row
 // that sees the block gets NaN.
-template <int FMT>
-__device__ void quantise_block(const uint16_t* kt, const uint16_t* vt, int D, bool bad, uint8_t* rec, BlockShared& sh) {
+template <int FMT, int D>
+__device__ __forceinline__ void quantise_block(const uint16_t* kt, const uint16_t* vt, bool bad, uint8_t* rec, BlockShared& sh) {
   uint32_t top[2] = {0, 0};
   for (int u = threadIdx.x; u < 64 * D / 8; u += kThreads) {
     const uint4 a = reinterpret_cast<const uint4*>(kt)[u], b = reinterpret_cast<const uint4*>(vt)[u];
@@ -275,10 +275,18 @@ __device__ void quantise_block(const uint16_t* kt, const uint16_t* vt, int D, bo
   }
 }
 
-__device__ __forceinline__ void quantise_any(const Kv8View& v, const uint16_t* kt, const uint16_t* vt, bool bad,
-                                             uint8_t* rec, BlockShared& sh) {
-  if (v.fmt == WOQ_KV8_INT8) quantise_block<WOQ_KV8_INT8>(kt, vt, v.dim, bad, rec, sh);
-  else quantise_block<WOQ_KV8_E4M3>(kt, vt, v.dim, bad, rec, sh);
+// D: head_dim, or 0: as the cache says.
+template <int D>
+__device__ __forceinline__ void quantise_any(const Kv8View& v, const uint16_t* kt, const uint16_t* vt, bool bad, uint8_t* rec,
+                                             BlockShared& sh) {
+  if constexpr (D == 0) {
+    if (v.dim == 64) quantise_any<64>(v, kt, vt, bad, rec, sh);
+    else if (v.dim == 128) quantise_any<128>(v, kt, vt, bad, rec, sh);
+    else quantise_any<256>(v, kt, vt, bad, rec, sh);
+  } else {
+    if (v.fmt == WOQ_KV8_INT8) quantise_block<WOQ_KV8_INT8, D>(kt, vt, bad, rec, sh);
+    else quantise_block<WOQ_KV8_E4M3, D>(kt, vt, bad, rec, sh);
+  }
 }
 
 // Rows 0 .. r1 - 1 of a tail into the tiles, with the rows from `at` on taken at the set bits of keep behind it
@@ -325,34 +333,45 @@ __device__ __forceinline__ void stage_axes(const Kv8Rope& r, uint8_t* axis) {
   __syncthreads();
 }
 
-// Queries of a prompt: a warp per row, the row's angles in registers for all of its heads.  VEC: heads
-// rotated as a whole, half / 8 lanes a head (a warp turns 4 heads of 128 at once, with 16-byte loads, five
-// steps of them under way).
-template <bool F32, bool VEC>
-__global__ void __launch_bounds__(kThreads) prompt_q_kernel(const __grid_constant__ Kv8Append p) {
-  __shared__ uint8_t axis[128];
-  stage_axes(p.rope, axis);
-  begin_after_prior();
-  if (!header_ok(p.v)) return;
-  const int lane = threadIdx.x & 31, row = blockIdx.x * kWarps + (threadIdx.x >> 5), D = p.v.dim;
+// A prompt's rows in one launch: first the CTAs of the keys and values, one per (block, head), then those of the
+// queries, a warp per row.  LANES > 0: heads rotated as a whole, of 16 LANES elements, LANES lanes a head with
+// 16-byte loads; else element pairs.
+//
+// Bound by HBM, so by the bytes under way: a thread issues the loads of its part of a full block (8 to 16
+// vectors), or of kSteps heads, before it works on the first (8,191 rows of 40 + 2 x 8 heads: 91 us as two
+// launches with two to four vectors under way).
+
+// The row's angles stay in registers for all of its heads; a warp turns 32 / LANES heads at once.
+template <bool F32, int LANES>
+__device__ __forceinline__ void prompt_queries(const Kv8Append& p, const uint8_t* axis, int row, int lane) {
   if (row >= p.rows) return;
   bool bad = false;
   const long long at = (long long)row * p.row_stride;
+  const int D = p.v.dim;
   uint16_t* out = p.q_out + (size_t)row * p.q_heads * D;
-  if constexpr (VEC) {
+  if constexpr (LANES > 0) {
+    constexpr int kD = 16 * LANES, kStep = 32 / LANES, kSteps = F32 ? 3 : 5;
+    const int i0 = (lane % LANES) * 8;
+    const int d0 = p.rope.interleaved ? 2 * i0 : i0, d1 = p.rope.interleaved ? d0 + 8 : 8 * LANES + i0;
     const Places pl = load_places(p.rope, row, p.rows, &bad);
-    const int lanes = p.rope.half / 8, i0 = (lane % lanes) * 8, step = 32 / lanes;
-    const int d0 = p.rope.interleaved ? 2 * i0 : i0, d1 = p.rope.interleaved ? d0 + 8 : p.rope.half + i0;
     const Angles8 ang = load_angles8(p.rope, axis, pl, i0);
-#pragma unroll 5
-    for (int h = lane / lanes; h < p.q_heads; h += step) {
-      Run8<F32> x, y;
-      x.load(p.qkv, at + h * D + d0);
-      y.load(p.qkv, at + h * D + d1);
-      uint4 u, v;
-      rotate8<F32>(x, y, ang, p.rope.interleaved, &u, &v);
-      *reinterpret_cast<uint4*>(out + h * D + d0) = u;
-      *reinterpret_cast<uint4*>(out + h * D + d1) = v;
+    for (int h0 = lane / LANES; h0 < p.q_heads; h0 += kStep * kSteps) {
+      Run8<F32> x[kSteps], y[kSteps];
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        const int h = min(h0 + i * kStep, p.q_heads - 1);
+        x[i].load(p.qkv, at + h * kD + d0);
+        y[i].load(p.qkv, at + h * kD + d1);
+      }
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        const int h = h0 + i * kStep;
+        if (h >= p.q_heads) break;
+        uint4 u, v;
+        rotate8<F32>(x[i], y[i], ang, p.rope.interleaved, &u, &v);
+        *reinterpret_cast<uint4*>(out + h * kD + d0) = u;
+        *reinterpret_cast<uint4*>(out + h * kD + d1) = v;
+      }
     }
   } else {
     const Angles ang = load_angles(p.rope, axis, row, p.rows, lane, &bad);
@@ -364,20 +383,84 @@ __global__ void __launch_bounds__(kThreads) prompt_q_kernel(const __grid_constan
   if (__any_sync(~0u, bad) && lane == 0) flag(p.v, WOQ_DEVERR_POSITION);
 }
 
-// Keys and values of a prompt: grid (blocks, heads).  Block b of the sequence goes to its page if
-// it is full, else to the tail.  The first block may have rows in the tail already; the CTA that reads
-// those also writes the tail's new rows, after it (no other CTA writes what it reads).
-template <bool F32, bool VEC>
-__global__ void __launch_bounds__(kThreads) prompt_kv_kernel(const __grid_constant__ Kv8Append p) {
-  extern __shared__ __align__(16) uint16_t tiles[];
-  __shared__ uint8_t axis[128];
-  __shared__ int odd_row[kKv8Block];
-  __shared__ BlockShared sh;
+// Rows r0 .. r1 - 1 of block b (row r is row first_row + r of the call) into the tiles, keys rotated; a row with an
+// element that is not finite sets odd_row[r].
+template <bool F32, int LANES>
+__device__ __forceinline__ void rows_to_tiles(const Kv8Append& p, const uint8_t* axis, int head, int first_row, int r0, int r1,
+                                              uint16_t* kt, uint16_t* vt, int* odd_row, bool* far) {
+  constexpr int D = 16 * LANES, kKeyRows = kThreads / LANES, kValueRows = kThreads / (2 * LANES);
+  constexpr int kKeys = 64 / kKeyRows, kValues = 64 / kValueRows;  // passes
+  const int i0 = ((int)threadIdx.x % LANES) * 8, kr = (int)threadIdx.x / LANES;
+  const int d0 = p.rope.interleaved ? 2 * i0 : i0, d1 = p.rope.interleaved ? d0 + 8 : 8 * LANES + i0;
+  const int vd = ((int)threadIdx.x % (2 * LANES)) * 8, vr = (int)threadIdx.x / (2 * LANES);
+  const long long base = (long long)first_row * p.row_stride + (long long)(p.q_heads + head) * D;
+  const long long vbase = base + (long long)p.v.heads * D + vd;
+  Run8<F32> x[kKeys], y[kKeys], w[kValues];
+  Places pl[kKeys];
+#pragma unroll
+  for (int i = 0; i < kKeys; ++i) {
+    const int r = kr + i * kKeyRows;
+    if (r < r0 || r >= r1) continue;
+    x[i].load(p.qkv, base + (long long)r * p.row_stride + d0);
+    y[i].load(p.qkv, base + (long long)r * p.row_stride + d1);
+    pl[i] = load_places(p.rope, first_row + r, p.rows, far);
+  }
+#pragma unroll
+  for (int i = 0; i < kValues; ++i) {
+    const int r = vr + i * kValueRows;
+    if (r >= r0 && r < r1) w[i].load(p.qkv, vbase + (long long)r * p.row_stride);
+  }
+#pragma unroll
+  for (int i = 0; i < kKeys; ++i) {
+    const int r = kr + i * kKeyRows;
+    if (r < r0 || r >= r1) continue;
+    const Angles8 ang = load_angles8(p.rope, axis, pl[i], i0);
+    uint4 u, v;
+    rotate8<F32>(x[i], y[i], ang, p.rope.interleaved, &u, &v);
+    if (not_finite8(u) || not_finite8(v)) odd_row[r] = 1;
+    *reinterpret_cast<uint4*>(kt + tile_at(r, d0, D)) = u;
+    *reinterpret_cast<uint4*>(kt + tile_at(r, d1, D)) = v;
+  }
+#pragma unroll
+  for (int i = 0; i < kValues; ++i) {
+    const int r = vr + i * kValueRows;
+    if (r < r0 || r >= r1) continue;
+    const uint4 u = w[i].rounded();
+    if (not_finite8(u)) odd_row[r] = 1;
+    *reinterpret_cast<uint4*>(vt + tile_at(r, vd, D)) = u;
+  }
+}
+
+template <bool F32>
+__device__ __forceinline__ void rows_to_tiles_by_pairs(const Kv8Append& p, const uint8_t* axis, int head, int first_row, int r0,
+                                                       int r1, uint16_t* kt, uint16_t* vt, int* odd_row, bool* far) {
+  const int D = p.v.dim, lane = threadIdx.x & 31;
+#pragma unroll 2
+  for (int r = r0 + (int)(threadIdx.x >> 5); r < r1; r += kWarps) {
+    const int row = first_row + r;
+    const long long at = (long long)row * p.row_stride + (long long)(p.q_heads + head) * D;
+    bool odd = false;
+    const Angles ang = load_angles(p.rope, axis, row, p.rows, lane, far);
+    rotate_row<F32>(p.qkv, at, D, p.rope, ang, lane, [&](int d, uint32_t x) {
+      odd |= bf16_pair_not_finite(x);
+      *reinterpret_cast<uint32_t*>(kt + tile_at(r, d, D)) = x;
+    });
+    plain_row<F32>(p.qkv, at + (long long)p.v.heads * D, D, lane, [&](int d, uint32_t x) {
+      odd |= bf16_pair_not_finite(x);
+      *reinterpret_cast<uint32_t*>(vt + tile_at(r, d, D)) = x;
+    });
+    if (odd) odd_row[r] = 1;
+  }
+}
+
+// Block b of the sequence goes to its page if it is full, else to the tail.  The first block may have rows in the tail
+// already; the CTA that reads those also writes the tail's new rows, after it (no other CTA writes what it
+// reads).
+template <bool F32, int LANES>
+__device__ __forceinline__ void prompt_block(const Kv8Append& p, const uint8_t* axis, int block, int head, uint16_t* tiles,
+                                             int* odd_row, BlockShared& sh) {
   const Kv8View& v = p.v;
-  stage_axes(p.rope, axis);
-  begin_after_prior();
-  if (!header_ok(v)) return;
-  const int seq = p.n, T = p.rows, D = v.dim, head = blockIdx.y;
+  const int seq = p.n, T = p.rows, D = LANES > 0 ? 16 * LANES : v.dim;
   const int len = v.lens_p()[seq], start = len - T;
   if (v.reserved_p()[seq] != T || start < 0) {
     if (threadIdx.x == 0) flag(v, WOQ_DEVERR_STATE);
@@ -387,83 +470,33 @@ __global__ void __launch_bounds__(kThreads) prompt_kv_kernel(const __grid_consta
   uint16_t* tail = v.tail(p.layer, seq, head);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int first = start / kKv8Block, last = (len - 1) / kKv8Block, full = len / kKv8Block;
-  const bool joined = start % kKv8Block != 0 && first < full && last == full;  // CTA 0 does the last block too
-  int b = first + (int)blockIdx.x;
+  const bool joined = start % kKv8Block != 0 && first < full && last == full;  // the first CTA does the last block too
+  int b = first + block;
   if (b > last || (joined && b == last)) return;
   for (;;) {
     const int r0 = b == first ? start - first * kKv8Block : 0;  // rows of this call: r0 .. r1 - 1
     const int r1 = b == full ? len - full * kKv8Block : kKv8Block;
-    bool bad = b < full && tail_to_tiles(tail, r0, r0, 0, D, kt, vt);
-    if constexpr (VEC) {
-      if (threadIdx.x < kKv8Block) odd_row[threadIdx.x] = 0;
-      __syncthreads();
-      bool far = false;
-      const int lanes = p.rope.half / 8, per = kThreads / lanes, i0 = ((int)threadIdx.x % lanes) * 8;
-      const int d0 = p.rope.interleaved ? 2 * i0 : i0, d1 = p.rope.interleaved ? d0 + 8 : p.rope.half + i0;
-      const long long base = (long long)(b * kKv8Block - start) * p.row_stride + (long long)(p.q_heads + head) * D;
-#pragma unroll 2
-      for (int r = r0 + (int)threadIdx.x / lanes; r < r1; r += per) {
-        const int row = b * kKv8Block + r - start;
-        Run8<F32> x, y;
-        x.load(p.qkv, base + (long long)r * p.row_stride + d0);
-        y.load(p.qkv, base + (long long)r * p.row_stride + d1);
-        const Places pl = load_places(p.rope, row, T, &far);
-        const Angles8 ang = load_angles8(p.rope, axis, pl, i0);
-        uint4 u, w;
-        rotate8<F32>(x, y, ang, p.rope.interleaved, &u, &w);
-        if (not_finite8(u) || not_finite8(w)) odd_row[r] = 1;
-        *reinterpret_cast<uint4*>(kt + tile_at(r, d0, D)) = u;
-        *reinterpret_cast<uint4*>(kt + tile_at(r, d1, D)) = w;
-      }
-      const int vper = kThreads / (D / 8), vd = ((int)threadIdx.x % (D / 8)) * 8;
-#pragma unroll 4
-      for (int r = r0 + (int)threadIdx.x / (D / 8); r < r1; r += vper) {
-        Run8<F32> x;
-        x.load(p.qkv, base + (long long)r * p.row_stride + (long long)v.heads * D + vd);
-        const uint4 u = x.rounded();
-        if (not_finite8(u)) odd_row[r] = 1;
-        *reinterpret_cast<uint4*>(vt + tile_at(r, vd, D)) = u;
-      }
-      if (__any_sync(~0u, far) && lane == 0) flag(v, WOQ_DEVERR_POSITION);
-      __syncthreads();
-      const int mine = (int)threadIdx.x < kKv8Block ? odd_row[threadIdx.x] : 0;
-      if (__syncthreads_or(mine)) {  // a key that is not finite, or its value: the key becomes NaN and the value 0
-        bad = true;
-        for (int r = r0 + warp; r < r1; r += kWarps) {
-          if (!odd_row[r]) continue;
-          for (int d = 2 * lane; d < D; d += 64) {
-            *reinterpret_cast<uint32_t*>(kt + tile_at(r, d, D)) = 0x7FC07FC0u;
-            *reinterpret_cast<uint32_t*>(vt + tile_at(r, d, D)) = 0u;
-          }
-        }
-      }
-    }
-#pragma unroll 2
-    for (int r = r0 + warp; !VEC && r < r1; r += kWarps) {
-      const int row = b * kKv8Block + r - start;
-      const long long at = (long long)row * p.row_stride + (long long)(p.q_heads + head) * D;
-      bool far = false, odd = false;
-      const Angles ang = load_angles(p.rope, axis, row, T, lane, &far);
-      rotate_row<F32>(p.qkv, at, D, p.rope, ang, lane, [&](int d, uint32_t x) {
-        odd |= bf16_pair_not_finite(x);
-        *reinterpret_cast<uint32_t*>(kt + tile_at(r, d, D)) = x;
-      });
-      plain_row<F32>(p.qkv, at + (long long)v.heads * D, D, lane, [&](int d, uint32_t x) {
-        odd |= bf16_pair_not_finite(x);
-        *reinterpret_cast<uint32_t*>(vt + tile_at(r, d, D)) = x;
-      });
-      if (__any_sync(~0u, far) && lane == 0) flag(v, WOQ_DEVERR_POSITION);
-      if (__any_sync(~0u, odd)) {  // the row's key becomes NaN and its value 0
+    bool bad = b < full && tail_to_tiles(tail, r0, r0, 0, D, kt, vt), far = false;
+    if (threadIdx.x < kKv8Block) odd_row[threadIdx.x] = 0;
+    __syncthreads();
+    if constexpr (LANES > 0) rows_to_tiles<F32, LANES>(p, axis, head, b * kKv8Block - start, r0, r1, kt, vt, odd_row, &far);
+    else rows_to_tiles_by_pairs<F32>(p, axis, head, b * kKv8Block - start, r0, r1, kt, vt, odd_row, &far);
+    if (__any_sync(~0u, far) && lane == 0) flag(v, WOQ_DEVERR_POSITION);
+    __syncthreads();
+    const int mine = (int)threadIdx.x < kKv8Block ? odd_row[threadIdx.x] : 0;
+    if (__syncthreads_or(mine)) {  // a key that is not finite, or its value: the key becomes NaN and the value 0
+      bad = true;
+      for (int r = r0 + warp; r < r1; r += kWarps) {
+        if (!odd_row[r]) continue;
         for (int d = 2 * lane; d < D; d += 64) {
           *reinterpret_cast<uint32_t*>(kt + tile_at(r, d, D)) = 0x7FC07FC0u;
           *reinterpret_cast<uint32_t*>(vt + tile_at(r, d, D)) = 0u;
         }
-        bad = true;
       }
     }
     const bool any_bad = __syncthreads_or(bad);
     if (b < full) {
-      quantise_any(v, kt, vt, any_bad, v.record(v.table_row(seq)[b], p.layer, head), sh);
+      quantise_any<LANES * 16>(v, kt, vt, any_bad, v.record(v.table_row(seq)[b], p.layer, head), sh);
     } else {
       for (int u = threadIdx.x; u < (r1 - r0) * (D / 8); u += kThreads) {
         const int r = r0 + u / (D / 8), d = (u % (D / 8)) * 8;
@@ -475,10 +508,24 @@ __global__ void __launch_bounds__(kThreads) prompt_kv_kernel(const __grid_consta
         tv[(size_t)d * kKv8Tail + r] = vt[tile_at(r, d, D)];
       }
     }
-    if (!joined || b == last || blockIdx.x != 0) return;
+    if (!joined || b == last || block != 0) return;
     __syncthreads();
     b = last;
   }
+}
+
+template <bool F32, int LANES>
+__global__ void __launch_bounds__(kThreads) prompt_kernel(const __grid_constant__ Kv8Append p, int blocks) {
+  extern __shared__ __align__(16) uint16_t tiles[];
+  __shared__ uint8_t axis[128];
+  __shared__ int odd_row[kKv8Block];
+  __shared__ BlockShared sh;
+  stage_axes(p.rope, axis);
+  begin_after_prior();
+  if (!header_ok(p.v)) return;
+  const int block = (int)blockIdx.x - blocks * p.v.heads;
+  if (block < 0) prompt_block<F32, LANES>(p, axis, (int)blockIdx.x / p.v.heads, (int)blockIdx.x % p.v.heads, tiles, odd_row, sh);
+  else prompt_queries<F32, LANES>(p, axis, block * kWarps + (int)(threadIdx.x >> 5), threadIdx.x & 31);
 }
 
 // --------------------------------------------------------------------------- draft rows
@@ -564,7 +611,7 @@ __global__ void __launch_bounds__(kThreads) accept_kernel(const __grid_constant_
   if (m.z >= 0) {  // rows 0 .. 63 to the page
     uint16_t *kt = tiles, *vt = tiles + 64 * D;
     const bool bad = __syncthreads_or(tail_to_tiles(tail, kKv8Block, at, keep, D, kt, vt));
-    quantise_any(v, kt, vt, bad, v.record(m.z, blockIdx.z, blockIdx.y), sh);
+    quantise_any<0>(v, kt, vt, bad, v.record(m.z, blockIdx.z, blockIdx.y), sh);
   } else if ((keep & (keep + 1)) == 0) {
     return;  // in place already
   }
@@ -606,21 +653,26 @@ static cudaError_t allow_tiles(K kernel, int bytes) {
                            : cudaSuccess;
 }
 
-template <bool F32, bool VEC>
+template <bool F32, int LANES>
 static cudaError_t launch_prompt(const Kv8Append& p, cudaStream_t s) {
-  const int smem = 256 * p.v.dim;
-  const dim3 grid((unsigned)((p.rows - 1) / kKv8Block + 2), (unsigned)p.v.heads);
-  cudaError_t e = allow_tiles(kv8::prompt_kv_kernel<F32, VEC>, smem);
+  const int smem = 256 * p.v.dim, blocks = (p.rows - 1) / kKv8Block + 2;  // whatever the first token's place in its block
+  const cudaError_t e = allow_tiles(kv8::prompt_kernel<F32, LANES>, smem);
   if (e != cudaSuccess) return e;
-  e = kv8::launch(kv8::prompt_kv_kernel<F32, VEC>, grid, kv8::kThreads, smem, s, p);
-  if (e != cudaSuccess || p.q_heads == 0) return e;
-  const unsigned blocks = (unsigned)((p.rows + kv8::kWarps - 1) / kv8::kWarps);
-  return kv8::launch(kv8::prompt_q_kernel<F32, VEC>, blocks, kv8::kThreads, 0, s, p);
+  const long long ctas = (long long)blocks * p.v.heads + (p.q_heads > 0 ? (p.rows + kv8::kWarps - 1) / kv8::kWarps : 0);
+  return kv8::launch(kv8::prompt_kernel<F32, LANES>, (unsigned)ctas, kv8::kThreads, smem, s, p, blocks);
 }
 
 cudaError_t launch_kv8_prompt(const Kv8Append& p, cudaStream_t s) {
-  if (p.rope.half * 2 == p.v.dim) return p.f32 ? launch_prompt<true, true>(p, s) : launch_prompt<false, true>(p, s);
-  return p.f32 ? launch_prompt<true, false>(p, s) : launch_prompt<false, false>(p, s);
+  const int lanes = p.rope.half * 2 == p.v.dim ? p.v.dim / 16 : 0;
+  switch (lanes + (p.f32 ? 1 : 0)) {
+    case 4: return launch_prompt<false, 4>(p, s);
+    case 5: return launch_prompt<true, 4>(p, s);
+    case 8: return launch_prompt<false, 8>(p, s);
+    case 9: return launch_prompt<true, 8>(p, s);
+    case 16: return launch_prompt<false, 16>(p, s);
+    case 17: return launch_prompt<true, 16>(p, s);
+    default: return p.f32 ? launch_prompt<true, 0>(p, s) : launch_prompt<false, 0>(p, s);
+  }
 }
 
 cudaError_t launch_kv8_accept_rows(const Kv8View& v, int n, cudaStream_t s) {
