@@ -289,16 +289,14 @@ __device__ __forceinline__ void quantise_any(const Kv8View& v, const uint16_t* k
   }
 }
 
-// Rows 0 .. r1 - 1 of a tail into the tiles, with the rows from `at` on taken at the set bits of keep behind it
-// (row at + j: the j-th bit); returns whether this thread met a key that is not finite.
-__device__ __forceinline__ int kept_row(int r, int at, uint32_t keep) { return r < at ? r : at + (int)__fns(keep, 0, r - at + 1); }
-
-__device__ bool tail_to_tiles(const uint16_t* tail, int r1, int at, uint32_t keep, int D, uint16_t* kt, uint16_t* vt) {
+// Rows 0 .. r1 - 1 of a tail into the tiles, row r from row from[r] (shared memory; the first `at` are in place);
+// returns whether this thread met a key that is not finite.
+__device__ bool tail_to_tiles(const uint16_t* tail, int r1, int at, const uint8_t* from, int D, uint16_t* kt, uint16_t* vt) {
   bool bad = false;
 #pragma unroll 4
   for (int u = threadIdx.x; u < r1 * (D / 8); u += kThreads) {
     const int r = u / (D / 8), d = (u % (D / 8)) * 8;
-    const uint4 x = *reinterpret_cast<const uint4*>(tail + (size_t)kept_row(r, at, keep) * D + d);
+    const uint4 x = *reinterpret_cast<const uint4*>(tail + (size_t)(r < at ? r : from[r]) * D + d);
     bad |= not_finite8(x);
     *reinterpret_cast<uint4*>(kt + tile_at(r, d, D)) = x;
   }
@@ -314,8 +312,8 @@ __device__ bool tail_to_tiles(const uint16_t* tail, int r1, int at, uint32_t kee
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = r + 2 * i < r1 ? tv[(size_t)d * kKv8Tail + kept_row(r + 2 * i, at, keep)] : 0u;
-        const uint32_t hi = r + 2 * i + 1 < r1 ? tv[(size_t)d * kKv8Tail + kept_row(r + 2 * i + 1, at, keep)] : 0u;
+        const uint32_t lo = r + 2 * i < r1 ? tv[(size_t)d * kKv8Tail + (r + 2 * i < at ? r + 2 * i : from[r + 2 * i])] : 0u;
+        const uint32_t hi = r + 2 * i + 1 < r1 ? tv[(size_t)d * kKv8Tail + (r + 2 * i + 1 < at ? r + 2 * i + 1 : from[r + 2 * i + 1])] : 0u;
         x[i] = lo | hi << 16;
       }
     }
@@ -461,8 +459,9 @@ __device__ __forceinline__ void prompt_block(const Kv8Append& p, const uint8_t* 
                                              int* odd_row, BlockShared& sh) {
   const Kv8View& v = p.v;
   const int seq = p.n, T = p.rows, D = LANES > 0 ? 16 * LANES : v.dim;
-  const int len = v.lens_p()[seq], start = len - T;
-  if (v.reserved_p()[seq] != T || start < 0) {
+  const int len = v.lens_p()[seq], reserved = v.reserved_p()[seq], start = len - T;  // beside the header's read
+  if (!header_ok(v)) return;
+  if (reserved != T || start < 0) {
     if (threadIdx.x == 0) flag(v, WOQ_DEVERR_STATE);
     return;
   }
@@ -476,7 +475,8 @@ __device__ __forceinline__ void prompt_block(const Kv8Append& p, const uint8_t* 
   for (;;) {
     const int r0 = b == first ? start - first * kKv8Block : 0;  // rows of this call: r0 .. r1 - 1
     const int r1 = b == full ? len - full * kKv8Block : kKv8Block;
-    bool bad = b < full && tail_to_tiles(tail, r0, r0, 0, D, kt, vt), far = false;
+    const int page = b < full ? v.table_row(seq)[b] : 0;
+    bool bad = b < full && tail_to_tiles(tail, r0, r0, nullptr, D, kt, vt), far = false;
     if (threadIdx.x < kKv8Block) odd_row[threadIdx.x] = 0;
     __syncthreads();
     if constexpr (LANES > 0) rows_to_tiles<F32, LANES>(p, axis, head, b * kKv8Block - start, r0, r1, kt, vt, odd_row, &far);
@@ -496,7 +496,7 @@ __device__ __forceinline__ void prompt_block(const Kv8Append& p, const uint8_t* 
     }
     const bool any_bad = __syncthreads_or(bad);
     if (b < full) {
-      quantise_any<LANES * 16>(v, kt, vt, any_bad, v.record(v.table_row(seq)[b], p.layer, head), sh);
+      quantise_any<LANES * 16>(v, kt, vt, any_bad, v.record(page, p.layer, head), sh);
     } else {
       for (int u = threadIdx.x; u < (r1 - r0) * (D / 8); u += kThreads) {
         const int r = r0 + u / (D / 8), d = (u % (D / 8)) * 8;
@@ -515,17 +515,19 @@ __device__ __forceinline__ void prompt_block(const Kv8Append& p, const uint8_t* 
 }
 
 template <bool F32, int LANES>
-__global__ void __launch_bounds__(kThreads) prompt_kernel(const __grid_constant__ Kv8Append p, int blocks) {
+__global__ void __launch_bounds__(kThreads, F32 ? 2 : 3) prompt_kernel(const __grid_constant__ Kv8Append p, int blocks) {
   extern __shared__ __align__(16) uint16_t tiles[];
   __shared__ uint8_t axis[128];
   __shared__ int odd_row[kKv8Block];
   __shared__ BlockShared sh;
   stage_axes(p.rope, axis);
   begin_after_prior();
-  if (!header_ok(p.v)) return;
-  const int block = (int)blockIdx.x - blocks * p.v.heads;
-  if (block < 0) prompt_block<F32, LANES>(p, axis, (int)blockIdx.x / p.v.heads, (int)blockIdx.x % p.v.heads, tiles, odd_row, sh);
-  else prompt_queries<F32, LANES>(p, axis, block * kWarps + (int)(threadIdx.x >> 5), threadIdx.x & 31);
+  // the two kinds in turn, so that an SM has some of each (the ones wait for chains of loads, the others for bandwidth)
+  const int kv = blocks * p.v.heads, queries = (int)gridDim.x - kv, both = 2 * min(kv, queries), i = (int)blockIdx.x;
+  const bool is_kv = i < both ? (i & 1) == 0 : kv > queries;
+  const int k = i < both ? i >> 1 : i - both / 2;
+  if (is_kv) prompt_block<F32, LANES>(p, axis, k / p.v.heads, k % p.v.heads, tiles, odd_row, sh);
+  else if (header_ok(p.v)) prompt_queries<F32, LANES>(p, axis, k * kWarps + (int)(threadIdx.x >> 5), threadIdx.x & 31);
 }
 
 // --------------------------------------------------------------------------- draft rows
@@ -601,16 +603,19 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
 __global__ void __launch_bounds__(kThreads) accept_kernel(const __grid_constant__ Kv8View v) {
   extern __shared__ __align__(16) uint16_t tiles[];
   __shared__ BlockShared sh;
+  __shared__ uint8_t from[kKv8Tail];
   begin_after_prior();
-  if (!header_ok(v)) return;
-  const int4 m = v.moves_p()[blockIdx.x];
+  const int4 m = v.moves_p()[blockIdx.x];  // beside the header's read
   const uint32_t keep = (uint32_t)m.y;
-  if (keep == 0) return;
+  if (!header_ok(v) || keep == 0) return;
   const int D = v.dim, at = m.x % kKv8Block, kept = __popc(keep);
+  if (threadIdx.x < WOQ_KV8_ROWS && (int)threadIdx.x < kept)  // where the kept rows are
+    from[at + threadIdx.x] = (uint8_t)(at + __fns(keep, 0, (int)threadIdx.x + 1));
+  __syncthreads();
   uint16_t* tail = v.tail(blockIdx.z, m.w, blockIdx.y);
   if (m.z >= 0) {  // rows 0 .. 63 to the page
     uint16_t *kt = tiles, *vt = tiles + 64 * D;
-    const bool bad = __syncthreads_or(tail_to_tiles(tail, kKv8Block, at, keep, D, kt, vt));
+    const bool bad = __syncthreads_or(tail_to_tiles(tail, kKv8Block, at, from, D, kt, vt));
     quantise_any<0>(v, kt, vt, bad, v.record(m.z, blockIdx.z, blockIdx.y), sh);
   } else if ((keep & (keep + 1)) == 0) {
     return;  // in place already
@@ -624,7 +629,7 @@ __global__ void __launch_bounds__(kThreads) accept_kernel(const __grid_constant_
     uint16_t y[WOQ_KV8_ROWS];
 #pragma unroll
     for (int j = 0; j < WOQ_KV8_ROWS; ++j)
-      if (j < count) y[j] = x[kept_row(first + j, at, keep) * step];
+      if (j < count) y[j] = x[from[first + j] * step];
 #pragma unroll
     for (int j = 0; j < WOQ_KV8_ROWS; ++j)
       if (j < count) x[(to + j) * step] = y[j];

@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kMetaThreads)
   v.moves_p()[e] = make_int4(len, (int)k, page, seq);
 }
 
-// fork and copy, bookkeeping.  moves[e] = {source, destination, 1 or 0, full blocks}
+// fork and copy, bookkeeping.  moves[e] = {source, destination, 1 or 0, length}
 __device__ __forceinline__ bool check_pairs(const Kv8View& sv, const Kv8View& dv, const int32_t* src,
                                             const int32_t* dst, int n, bool same, MetaShared& sh, int* s, int* d,
                                             int* len) {
@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kMetaThreads)
   if (!ok && threadIdx.x == 0) flag(v, WOQ_DEVERR_STATE);
   const int e = threadIdx.x;
   if (e >= n) return;
-  v.moves_p()[e] = make_int4(s, d, ok, len / kKv8Block);
+  v.moves_p()[e] = make_int4(s, d, ok, len);
   if (ok) {
     v.lens_p()[d] = len;
     v.reserved_p()[d] = 0;
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kMetaThreads)
     }
   }
   if (e < n) {
-    dv.moves_p()[e] = make_int4(s, d, ok, len / kKv8Block);
+    dv.moves_p()[e] = make_int4(s, d, ok, len);
     if (ok) {
       dv.lens_p()[d] = len;
       dv.reserved_p()[d] = 0;
@@ -353,13 +353,12 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(Kv8View sv, Kv
 // a reference on each of its pages (fork).
 __global__ void __launch_bounds__(256) copy_tails_kernel(Kv8View sv, Kv8View dv, int share) {
   begin_after_prior();
-  if (!header_ok(dv)) return;
-  const int4 m = dv.moves_p()[blockIdx.x];
-  if (!m.z) return;
+  const int4 m = dv.moves_p()[blockIdx.x];  // beside the header's read
+  if (!header_ok(dv) || !m.z) return;
   const uint16_t* from = sv.tail(blockIdx.z, m.x, blockIdx.y);
   uint16_t* to = dv.tail(blockIdx.z, m.y, blockIdx.y);
   // the tokens and the draft rows behind them: so many rows of keys, and octets of the values' rows
-  const int D = dv.dim, rows = dv.lens_p()[m.y] % kKv8Block + WOQ_KV8_ROWS, octets = (rows + 7) / 8;
+  const int D = dv.dim, rows = m.w % kKv8Block + WOQ_KV8_ROWS, octets = (rows + 7) / 8;
 #pragma unroll 4
   for (int i = threadIdx.x; i < rows * (D / 8); i += blockDim.x)
     reinterpret_cast<uint4*>(to)[i] = reinterpret_cast<const uint4*>(from)[i];
@@ -369,7 +368,7 @@ __global__ void __launch_bounds__(256) copy_tails_kernel(Kv8View sv, Kv8View dv,
     *reinterpret_cast<uint4*>(to + at) = *reinterpret_cast<const uint4*>(from + at);
   }
   if (share && blockIdx.y == 0 && blockIdx.z == 0) {
-    for (int b = threadIdx.x; b < m.w; b += blockDim.x) {
+    for (int b = threadIdx.x; b < m.w / kKv8Block; b += blockDim.x) {
       const int page = sv.table_row(m.x)[b];
       dv.table_row(m.y)[b] = page;
       atomicAdd(&dv.refs_p()[page], 1);
@@ -435,20 +434,21 @@ __global__ void __launch_bounds__(256)
     read_kernel(Kv8View v, int layer, int seq, int first, int count, uint16_t* k, uint16_t* vals) {
   __shared__ uint32_t smem[64 * 256 / 128 * 33];
   begin_after_prior();
+  // length and page beside the header's read (a row of the table is all there, though only its first entries are set)
+  const int b = first / kKv8Block + (int)blockIdx.x;
+  const int len = v.lens_p()[seq], page = b < v.blocks ? v.table_row(seq)[b] : 0;
   if (!header_ok(v)) return;
-  const int len = v.lens_p()[seq];
   if ((long long)first + count > (long long)len + WOQ_KV8_ROWS) {
     if (threadIdx.x == 0) flag(v, WOQ_DEVERR_STATE);
     return;
   }
   const int D = v.dim, head = blockIdx.y, full = len / kKv8Block;
-  const int b = first / kKv8Block + (int)blockIdx.x;
   const size_t row = (size_t)v.heads * D;
   k += ((size_t)blockIdx.z * count * v.heads + head) * D;
   vals += ((size_t)blockIdx.z * count * v.heads + head) * D;
   const int l = layer + (int)blockIdx.z;
   if (b < full) {
-    const uint8_t* rec = v.record(v.table_row(seq)[b], l, head);
+    const uint8_t* rec = v.record(page, l, head);
     if (v.fmt == WOQ_KV8_INT8) read_record<WOQ_KV8_INT8>(v, rec, smem, first, first + count, k, vals, row, b * kKv8Block);
     else read_record<WOQ_KV8_E4M3>(v, rec, smem, first, first + count, k, vals, row, b * kKv8Block);
     return;
