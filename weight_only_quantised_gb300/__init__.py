@@ -505,8 +505,8 @@ class Rope:
         axis_of = None if axis_of is None else np.array(axis_of, dtype=np.uint8)
         if axis_of is not None and axis_of.size != table.shape[1]:
             raise ValueError(f"rope axis_of: expected {table.shape[1]} entries, got {axis_of.size}")
-        self._args = _Rope(_f32(table, "rope table", -1), table.shape[0], 2 * table.shape[1], int(bool(interleaved)),
-                           pos.shape[0], _ints(pos, "rope positions", -1),
+        self._args = _Rope(_typed(table, "rope table", _F32, -1), table.shape[0], 2 * table.shape[1], int(bool(interleaved)),
+                           pos.shape[0], _typed(pos, "rope positions", _INT32, -1),
                            None if axis_of is None else axis_of.ctypes.data)
         self._held = table, pos, axis_of
         self._rows, self._device = pos.shape[1], pos.get_device()
@@ -572,20 +572,16 @@ def woq_kv8_plan_attention(cfg: KV8Config, n: int, rows: int, q_heads: int, sms:
     return {name: getattr(plan, name) for name, _ in KV8Plan._fields_}
 
 
-def _cache_args(cfg: KV8Config, cache):
-    device = -1 if cache is None else cache.get_device()
-    if device < 0 or device != _current_device() or not cache.is_contiguous() or cache.element_size() != 1:
-        return ctypes.byref(cfg), _dptr(cache, "cache", 1), _nbytes(cache)
-    return ctypes.byref(cfg), cache.data_ptr(), cache.nbytes
-
-
+# The cache's calls come many to a step, so their checks are written to cost little (about half a microsecond a
+# tensor): one pass over what has to hold, and _dptr's messages where something does not.
+_INT32, _BF16, _F32 = "int32", "bfloat16", "float32"
 _DTYPES = {}  # element type -> the torch dtypes that hold it (bound on first use)
 
 
 def _dtypes(kind: str):
     import torch
-    _DTYPES.update(int32=(torch.int32, getattr(torch, "uint32", torch.int32)), bfloat16=(torch.bfloat16,),
-                   float32=(torch.float32,), qkv={torch.bfloat16: 0, torch.float32: 1})
+    _DTYPES.update({_INT32: (torch.int32, getattr(torch, "uint32", torch.int32)), _BF16: (torch.bfloat16,),
+                    _F32: (torch.float32,), "qkv": {torch.bfloat16: 0, torch.float32: 1}})
     return _DTYPES[kind]
 
 
@@ -601,16 +597,20 @@ def _typed(t, name: str, kind: str, numel: int):
     return t.data_ptr()
 
 
-def _ints(t, name: str, numel: int):
-    return _typed(t, name, "int32", numel)
+def _bytes(t, name: str):
+    """Device pointer of a contiguous tensor of bytes (None -> NULL)."""
+    device = -1 if t is None else t.get_device()
+    if device < 0 or device != _current_device() or not t.is_contiguous() or t.element_size() != 1:
+        return _dptr(t, name, 1)
+    return t.data_ptr()
 
 
-def _bf16(t, name: str, numel: int):
-    return _typed(t, name, "bfloat16", numel)
+def _cache_args(cfg: KV8Config, cache):
+    return ctypes.byref(cfg), _bytes(cache, "cache"), _nbytes(cache)
 
 
-def _f32(t, name: str, numel: int):
-    return _typed(t, name, "float32", numel)
+def _raise(status: int, what: str):
+    raise WoqError(status, what)
 
 
 def woq_kv8_init(cfg: KV8Config, cache, stream=None) -> None:
@@ -642,7 +642,7 @@ def _qkv(cfg, qkv, q_heads, q_out, rope):
     # the rows may be strided: the first alone is contiguous
     ptr = _dptr(qkv if qkv.is_contiguous() else qkv[0], "qkv")
     return (ptr, kind, stride, q_heads, None if rope is None else rope._ref(rows),
-            _bf16(q_out, "q_out", rows * q_heads * cfg.head_dim))
+            _typed(q_out, "q_out", _BF16, rows * q_heads * cfg.head_dim))
 
 
 def woq_kv8_append_rows(cfg: KV8Config, cache, layer: int, seqs, rows: int, qkv, q_heads: int, q_out, rope=None,
@@ -654,7 +654,7 @@ def woq_kv8_append_rows(cfg: KV8Config, cache, layer: int, seqs, rows: int, qkv,
     if n * rows != total:
         raise ValueError(f"qkv: {total} rows, the call needs {n} x {rows}")
     args = _qkv(cfg, qkv, q_heads, q_out, rope)
-    _check(lib.woq_kv8_append_rows(*_cache_args(cfg, cache), layer, _ints(seqs, "seqs", n), n, rows, *args,
+    _check(lib.woq_kv8_append_rows(*_cache_args(cfg, cache), layer, _typed(seqs, "seqs", _INT32, n), n, rows, *args,
                                    _stream(stream)), "woq_kv8_append_rows")
 
 
@@ -675,7 +675,7 @@ def woq_kv8_accept(cfg: KV8Config, cache, seqs, keep, stream=None) -> None:
     n = keep.numel()
     if seqs is not None and seqs.numel() != n:
         raise ValueError(f"keep: {n} entries for {seqs.numel()} sequences")
-    _check(lib.woq_kv8_accept(*_cache_args(cfg, cache), _ints(seqs, "seqs", n), n, _ints(keep, "keep", n),
+    _check(lib.woq_kv8_accept(*_cache_args(cfg, cache), _typed(seqs, "seqs", _INT32, n), n, _typed(keep, "keep", _INT32, n),
                               _stream(stream)), "woq_kv8_accept")
 
 
@@ -684,31 +684,34 @@ def woq_kv8_attention(cfg: KV8Config, cache, layer: int, seqs, rows: int, q, q_h
     """Attention of `rows` rows of each sequence of seqs (int32 [n]; None: as many as q has, from 0 on):
     q, out bf16 [n * rows, q_heads, head_dim]; vis int32 [n, rows], the draft rows each row sees (None: a chain)."""
     per = max(1, rows * q_heads * cfg.head_dim)
-    n = q.numel() // per if seqs is None else seqs.numel()
-    if n * per != q.numel():
-        raise ValueError(f"q: {q.numel()} elements, the call needs {n} x {per}")
-    _check(lib.woq_kv8_attention(*_cache_args(cfg, cache), layer, _ints(seqs, "seqs", n), n, rows,
-                                 _bf16(q, "q", n * per), q_heads, _ints(vis, "vis", n * rows), float(scale), window,
-                                 sinks, _bf16(out, "out", n * per), _dptr(ws, "ws", 1), _nbytes(ws),
-                                 _stream(stream)), "woq_kv8_attention")
+    total = q.numel()
+    n = total // per if seqs is None else seqs.numel()
+    if n * per != total:
+        raise ValueError(f"q: {total} elements, the call needs {n} x {per}")
+    status = lib.woq_kv8_attention(
+        ctypes.byref(cfg), _bytes(cache, "cache"), _nbytes(cache), layer, _typed(seqs, "seqs", _INT32, n), n, rows,
+        _typed(q, "q", _BF16, total), q_heads, _typed(vis, "vis", _INT32, n * rows), scale, window, sinks,
+        _typed(out, "out", _BF16, total), _bytes(ws, "ws"), _nbytes(ws), _stream(stream))
+    if status:
+        _raise(status, "woq_kv8_attention")
 
 
 def woq_kv8_fork(cfg: KV8Config, cache, src, dst, stream=None) -> None:
     n = dst.numel()
-    _check(lib.woq_kv8_fork(*_cache_args(cfg, cache), _ints(src, "src", n), _ints(dst, "dst", n), n,
+    _check(lib.woq_kv8_fork(*_cache_args(cfg, cache), _typed(src, "src", _INT32, n), _typed(dst, "dst", _INT32, n), n,
                             _stream(stream)), "woq_kv8_fork")
 
 
 def woq_kv8_free(cfg: KV8Config, cache, seqs, stream=None) -> None:
-    _check(lib.woq_kv8_free(*_cache_args(cfg, cache), _ints(seqs, "seqs", seqs.numel()), seqs.numel(),
+    _check(lib.woq_kv8_free(*_cache_args(cfg, cache), _typed(seqs, "seqs", _INT32, seqs.numel()), seqs.numel(),
                             _stream(stream)), "woq_kv8_free")
 
 
 def woq_kv8_copy(src_cfg: KV8Config, src, dst_cfg: KV8Config, dst, src_seqs, dst_seqs, stream=None) -> None:
     """Copies of sequences, with pages of their own, in the same cache or another."""
     n = dst_seqs.numel()
-    _check(lib.woq_kv8_copy(*_cache_args(src_cfg, src), *_cache_args(dst_cfg, dst), _ints(src_seqs, "src_seqs", n),
-                            _ints(dst_seqs, "dst_seqs", n), n, _stream(stream)), "woq_kv8_copy")
+    _check(lib.woq_kv8_copy(*_cache_args(src_cfg, src), *_cache_args(dst_cfg, dst), _typed(src_seqs, "src_seqs", _INT32, n),
+                            _typed(dst_seqs, "dst_seqs", _INT32, n), n, _stream(stream)), "woq_kv8_copy")
 
 
 def woq_kv8_compact(cfg: KV8Config, cache, limit: int, stream=None) -> None:
@@ -723,12 +726,12 @@ def woq_kv8_read(cfg: KV8Config, cache, layer: int, seq: int, first: int, k, v, 
     count = k.numel() // max(per, 1)
     if count * per != k.numel() or v.numel() != k.numel():
         raise ValueError(f"k, v: {k.numel()} and {v.numel()} elements, expected the same multiple of {per}")
-    _check(lib.woq_kv8_read(*_cache_args(cfg, cache), layer, seq, first, count, _bf16(k, "k", -1), _bf16(v, "v", -1),
+    _check(lib.woq_kv8_read(*_cache_args(cfg, cache), layer, seq, first, count, _typed(k, "k", _BF16, -1), _typed(v, "v", _BF16, -1),
                             _stream(stream)), "woq_kv8_read")
 
 
 def woq_kv8_state(cfg: KV8Config, cache, lens=None, refs=None, table=None, stream=None) -> None:
     """Copies of the lengths [seqs], page reference counts [pages] and page tables [seqs, ceil(max_tokens / 64)]."""
     blocks = -(-cfg.max_tokens // KV8_BLOCK)
-    _check(lib.woq_kv8_state(*_cache_args(cfg, cache), _ints(lens, "lens", cfg.seqs), _ints(refs, "refs", cfg.pages),
-                             _ints(table, "table", cfg.seqs * blocks), _stream(stream)), "woq_kv8_state")
+    _check(lib.woq_kv8_state(*_cache_args(cfg, cache), _typed(lens, "lens", _INT32, cfg.seqs), _typed(refs, "refs", _INT32, cfg.pages),
+                             _typed(table, "table", _INT32, cfg.seqs * blocks), _stream(stream)), "woq_kv8_state")
