@@ -469,6 +469,7 @@ __device__ __forceinline__ void lay_out(const Kv8Attn& p, Misc& misc, int lane) 
   int* cuts = lens + p.n;
   const int ctas = (int)gridDim.x;
   int run = 0;
+#pragma unroll 1
   for (int e0 = 0; e0 < p.n; e0 += 32) {
     const int e = e0 + lane;
     int units = 0;
@@ -497,9 +498,11 @@ __device__ __forceinline__ void lay_out(const Kv8Attn& p, Misc& misc, int lane) 
     __syncwarp();
     const int room = ctas / v.heads;  // pieces of one head
     share = max(p.least_units, (run + room - 1) / room);
+#pragma unroll 1
     while (p.n > 1) {  // ends: with a share beyond the longest item there are n <= room pieces
       const int mine = share + (int)((long long)share * lane / 32);
       int total = 0;
+#pragma unroll 1
       for (int e = 0; e < p.n; ++e) total += pieces_of(misc.entries[e + 1] - misc.entries[e], mine);
       const uint32_t fits = __ballot_sync(~0u, total <= room);
       share = __shfl_sync(~0u, mine, fits ? __ffs((int)fits) - 1 : 31);
@@ -507,6 +510,7 @@ __device__ __forceinline__ void lay_out(const Kv8Attn& p, Misc& misc, int lane) 
       ++share;
     }
     int total = 0;
+#pragma unroll 1
     for (int e0 = 0; e0 < p.n; e0 += 32) {
       const int e = e0 + lane;
       int y = e < p.n ? pieces_of(misc.entries[e + 1] - misc.entries[e], share) : 0;
@@ -531,6 +535,7 @@ __device__ __forceinline__ bool take_share(const Kv8Attn& p, Misc& misc, Plan& p
   if (misc.share > 0) {
     if (block >= cuts[p.n]) return false;
     int lo = 0, hi = p.n - 1;
+#pragma unroll 1
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (cuts[mid] <= block) lo = mid; else hi = mid - 1;
@@ -538,8 +543,8 @@ __device__ __forceinline__ bool take_share(const Kv8Attn& p, Misc& misc, Plan& p
     const int per = misc.entries[lo + 1] - misc.entries[lo], pieces = (cuts[lo + 1] - cuts[lo]) / heads;
     const int head = (block - cuts[lo]) / pieces, j = block - cuts[lo] - head * pieces;
     const int first = misc.entries[lo] * heads + head * per;
-    pl = Plan{first + (int)((long long)per * j / pieces), first + (int)((long long)per * (j + 1) / pieces), true, block - j,
-              pieces, 0};
+    const int some = per / pieces, rest = per - some * pieces;  // per * j / pieces, in 32 bits
+    pl = Plan{first + some * j + rest * j / pieces, first + some * (j + 1) + rest * (j + 1) / pieces, true, block - j, pieces, 0};
     return true;
   }
   const int units = misc.entries[p.n] * heads;
@@ -553,6 +558,7 @@ __device__ __forceinline__ bool take_share(const Kv8Attn& p, Misc& misc, Plan& p
 __device__ __forceinline__ void locate(const Kv8Attn& p, const Misc& misc, int u, int* entry, int* head, int* item_begin) {
   const int* prefix = misc.entries;
   int lo = 0, hi = p.n - 1;
+#pragma unroll 1
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (prefix[mid] * p.v.heads <= u) lo = mid; else hi = mid - 1;
@@ -578,10 +584,12 @@ __device__ __forceinline__ void prefetch_first(const Kv8Attn& p, Misc& misc, con
     const int page = (int)dev::ld_relaxed_u32(v.table_row(seq) + (k < sp.head_blocks ? k : sp.from + (k - sp.head_blocks)));
     if (page >= 0 && page < v.pages) dev::bulk_prefetch_l2(v.record(page, p.layer, head), (uint32_t)v.record_bytes());
   }
-  const size_t q_bytes = (size_t)p.group * v.dim * 2;  // of one row
-  for (size_t x = (size_t)lane * 128; x < q_bytes * p.rows; x += 32 * 128)
-    dev::prefetch_l2(reinterpret_cast<const uint8_t*>(p.q) + (((size_t)e * p.rows + x / q_bytes) * p.q_heads * v.dim +
-                                                              (size_t)head * p.group * v.dim) * 2 + x % q_bytes);
+  const int q_elems = p.group * v.dim;  // of one row
+#pragma unroll 1
+  for (int x = lane * 64; x < q_elems * p.rows; x += 32 * 64) {
+    const int row = x / q_elems;
+    dev::prefetch_l2(p.q + (((size_t)e * p.rows + row) * p.q_heads + (size_t)head * p.group) * v.dim + (x - row * q_elems));
+  }
   if (lane == 31 && pl.end >= ib + per) dev::bulk_prefetch_l2(v.tail(p.layer, seq, head), (uint32_t)v.tail_elems() * 2u);
 }
 
@@ -596,38 +604,38 @@ __device__ __forceinline__ bool make_plan(const Kv8Attn& p, Misc& misc, int tid,
   const Kv8View& v = p.v;
   const int lane = tid & 31, warp = tid >> 5;
   uint32_t magic;
-  const bool guessed = __syncthreads_and(is_ours(v, &magic));
-  bool active = false;
-  if (guessed) {
-    if (warp == 0) lay_out(p, misc, lane);
-    __syncthreads();
-    active = take_share(p, misc, pl);
-    if (active && warp == p.warps) prefetch_first(p, misc, pl, lane);
-  }
-  begin_after_prior();
-  const bool ours = is_ours(v, &magic);
-  if (warp == 0) {
-    bool same = guessed;
-    for (int e = lane; e < p.n; e += 32) {
-      const int seq = number_of(p, e), before = guessed ? (p.seqs ? seqs_of(p, misc)[e] : e) : seq;
-      const int len = length_of(p, before);  // beside the number's read, not behind it
-      if (guessed) same &= seq == before && len == lens_of(p, misc)[e];
-      if (ours && (seq < 0 || seq >= v.seqs) && blockIdx.x == 0) flag(v, WOQ_DEVERR_STATE);
+  bool known = __syncthreads_and(is_ours(v, &magic)), active = false;
+  const bool guessed = known;
+#pragma unroll 1
+  for (int pass = 0;; ++pass) {  // (once more, if the first plan does not hold)
+    if (known) {
+      if (warp == 0) lay_out(p, misc, lane);
+      __syncthreads();
+      active = take_share(p, misc, pl);
     }
-    same = __all_sync(~0u, same);
-    if (lane == 0) misc.redo = !same;
-  }
-  if (!ours) {
-    if (magic == kKv8Magic && tid == 0) flag(v, WOQ_DEVERR_HEADER);
-    return false;
-  }
-  __syncthreads();
-  if (misc.redo) {
-    if (warp == 0) lay_out(p, misc, lane);
+    if (pass > 0) return active;
+    if (active && warp == p.warps) prefetch_first(p, misc, pl, lane);
+    begin_after_prior();
+    known = is_ours(v, &magic);
+    if (warp == 0) {
+      bool same = guessed;
+#pragma unroll 1
+      for (int e = lane; e < p.n; e += 32) {
+        const int seq = number_of(p, e), before = guessed ? (p.seqs ? seqs_of(p, misc)[e] : e) : seq;
+        const int len = length_of(p, before);  // beside the number's read, not behind it
+        if (guessed) same &= seq == before && len == lens_of(p, misc)[e];
+        if (known && (seq < 0 || seq >= v.seqs) && blockIdx.x == 0) flag(v, WOQ_DEVERR_STATE);
+      }
+      same = __all_sync(~0u, same);
+      if (lane == 0) misc.redo = !same;
+    }
+    if (!known) {
+      if (magic == kKv8Magic && tid == 0) flag(v, WOQ_DEVERR_HEADER);
+      return false;
+    }
     __syncthreads();
-    active = take_share(p, misc, pl);
+    if (!misc.redo) return active;
   }
-  return active;
 }
 
 // The producer warp: the records of this CTA's blocks, in order, into the ring's stages.
@@ -637,6 +645,7 @@ __device__ __forceinline__ void produce(const Kv8Attn& p, Misc& misc, const Plan
   const Kv8View& v = p.v;
   const int S = p.stages;
   int issued = 0;
+#pragma unroll 1
   for (int u = pl.begin; u < pl.end;) {
     int e, head, ib;
     locate(p, misc, u, &e, &head, &ib);
@@ -646,11 +655,13 @@ __device__ __forceinline__ void produce(const Kv8Attn& p, Misc& misc, const Plan
     if (b0 < b1) {
       const Span sp = span_of(lens_of(p, misc)[e], p.window, p.sinks);
       const int32_t* table = v.table_row(p.seqs ? p.seqs[e] : e);
+#pragma unroll 1
       for (int c0 = b0; c0 < b1; c0 += 32) {
         const int k = c0 + lane;
         int page = 0;
         if (k < b1) page = table[k < sp.head_blocks ? k : sp.from + (k - sp.head_blocks)];
         const int some = b1 - c0 < 32 ? b1 - c0 : 32;
+#pragma unroll 1
         for (int i = 0; i < some; ++i) {
           const int pg = __shfl_sync(~0u, page, i);
           const int stage = issued % S;
@@ -674,6 +685,7 @@ __device__ __forceinline__ void produce(const Kv8Attn& p, Misc& misc, const Plan
     u = stop;
   }
   // copies in flight end before this CTA's shared memory is given up
+#pragma unroll 1
   for (int i = issued > S ? issued - S : 0; i < issued; ++i)
     dev::mbar_wait_bounded(&misc.full[i % S], (uint32_t)((i / S) & 1));
 }
@@ -697,6 +709,7 @@ __device__ __forceinline__ void finish(const Kv8Attn& p, Misc& misc, const Plan&
   const size_t slot = (size_t)R * (D + 4);
   float* part = p.parts + ((size_t)blockIdx.x * 2 + mine) * slot;
   uint16_t* out0 = p.out + ((size_t)e * p.rows * p.q_heads + (size_t)head * p.group) * D;
+#pragma unroll 1
   for (int x = tid; x < R * (D / 4); x += consumers) {
     const int n = x / (D / 4), d = (x % (D / 4)) * 4;
     float pm[8], ps[8], m = -INFINITY, l = 0.0f;
@@ -751,6 +764,7 @@ __device__ __forceinline__ void finish(const Kv8Attn& p, Misc& misc, const Plan&
   const int some = min(R, room / (np + 1));  // queries at a time: np factors and a sum each in the scratch
   constexpr int kAhead = 20;  // loads under way per thread, the first unit's before the maxima and sums are read
   float4 ahead[kAhead];
+#pragma unroll 1
   for (int n0 = 0; n0 < R; n0 += some) {
     const int n1 = min(R, n0 + some);
     float* sums = merge + some * np;
@@ -760,6 +774,7 @@ __device__ __forceinline__ void finish(const Kv8Attn& p, Misc& misc, const Plan&
       for (int i = 0; i < kAhead; ++i)
         if (i < np) ahead[i] = __ldcg(reinterpret_cast<const float4*>(values + 4 * tid + i * step + (i == 0 ? first : 0)));
     }
+#pragma unroll 1
     for (int nb = n0 + (tid >> 5); nb < n1; nb += 4 * warps) {  // a warp per query, four of them under way
       float2 ml[4];
 #pragma unroll
@@ -775,11 +790,13 @@ __device__ __forceinline__ void finish(const Kv8Attn& p, Misc& misc, const Plan&
         if (n >= n1) break;
         const float* at = parts + (size_t)R * D + 2 * n;
         float m = ml[j].x;
+#pragma unroll 1
         for (int c = lane + 32; c < np; c += 32) m = fmaxf(m, __ldcg(at + c * step));
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
         float f = part_factor(ml[j].x, ml[j].y, m), l = f * ml[j].y;
         if (lane < np) merge[(n - n0) * np + lane] = f;
+#pragma unroll 1
         for (int c = lane + 32; c < np; c += 32) {
           const float2 x = __ldcg(reinterpret_cast<const float2*>(at + c * step));
           f = part_factor(x.x, x.y, m);
@@ -792,6 +809,7 @@ __device__ __forceinline__ void finish(const Kv8Attn& p, Misc& misc, const Plan&
       }
     }
     dev::named_barrier_sync(1, consumers);
+#pragma unroll 1
     for (int x = tid; x < (n1 - n0) * (D / 4); x += consumers) {
       const int n = n0 + x / (D / 4), d = (x % (D / 4)) * 4;
       const float* fs = merge + (n - n0) * np;
@@ -835,6 +853,7 @@ __global__ void __launch_bounds__(32 * (max_warps(QT) + 1), 1) attn_kernel(const
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   if (tid == 0) {
+#pragma unroll 1
     for (int i = 0; i < S; ++i) {
       dev::mbar_init(&misc.full[i], 1);
       dev::mbar_init(&misc.empty[i], (uint32_t)G);
@@ -853,6 +872,7 @@ __global__ void __launch_bounds__(32 * (max_warps(QT) + 1), 1) attn_kernel(const
   const int g = lane >> 2, t = lane & 3;
   const int consumers = W * 32;
   int taken = 0;  // blocks of this CTA that earlier items had
+#pragma unroll 1
   for (int u = pl.begin; u < pl.end;) {
     int e, head, ib;
     locate(p, misc, u, &e, &head, &ib);
@@ -901,12 +921,14 @@ __global__ void __launch_bounds__(32 * (max_warps(QT) + 1), 1) attn_kernel(const
       const uint16_t* tail = v.tail(p.layer, seq, head);
       const int in_tail = len - sp.full * kKv8Block;
       const int there = in_tail + 32 - __clz((int)__reduce_or_sync(~0u, any_vis));  // at most 63 + 8
+#pragma unroll 1
       for (int i = slot; i < 5; i += WG)
         if (there > (i < 4 ? 4 * i : 64))
           tail_step<D, QT>(st, tail, i, in_tail, len, there, qrow, p.scale_log2, col, p.sinks, lane);
     }
     bool ok = true;
     int k = b0 + ((slot - taken) % WG + WG) % WG;  // ring positions taken + (k - b0) = slot mod WG (S a multiple of WG)
+#pragma unroll 1
     for (; k < b1 && ok; k += WG) {
       const int at = taken + (k - b0), stage = at % S;
       ok = dev::mbar_wait_bounded(&misc.full[stage], (uint32_t)((at / S) & 1));
@@ -971,7 +993,16 @@ __global__ void __launch_bounds__(32 * (max_warps(QT) + 1), 1) attn_kernel(const
 // The running maxima belong to the team: weights are formed against them at once, and a score
 // that passes its maximum by more than kRaise raises a flag that all four warps see behind that
 // barrier; then (rarely) they agree on new maxima and form the weights again.
-constexpr int kTeams = 2;
+//
+// Three teams: at 65,531 tokens x 40 queries 61 us (two: 64), 32,785 x 12 24 (two: 26, four: 27).
+constexpr int kTeams = 3;
+// Registers: 16 warps have 128 a thread at launch.  The last four, of which one copies records and the others end,
+// give up most of theirs to the teams (128 for all spill: two teams at 168 took 73 us, with 232 64).
+constexpr int kTeamThreads = 32 * (4 * kTeams + 4);
+constexpr int kLaunchRegisters = 128, kProducerRegisters = 40, kTeamRegisters = 152;
+static_assert(kTeamThreads * kLaunchRegisters <= 65536 &&
+                  128 * kProducerRegisters + 128 * kTeams * kTeamRegisters <= kTeamThreads * kLaunchRegisters,
+              "more registers than the launch has: the teams would wait for them for ever");
 
 // Shared memory of one team: weights, twice (for two blocks in turn), column maxima of its warps, flags.
 template <int NT>
@@ -1275,7 +1306,7 @@ __device__ void team_tail(TeamState<D, NT>& st, TeamShared<NT>& ts, const uint16
 }
 
 template <int FMT, int D, int NT>
-__global__ void __launch_bounds__(32 * (4 * kTeams + 1), 1) attn_team_kernel(const __grid_constant__ Kv8Attn p) {
+__global__ void __launch_bounds__(kTeamThreads, 1) attn_team_kernel(const __grid_constant__ Kv8Attn p) {
   extern __shared__ __align__(128) uint8_t smem[];
   constexpr bool kShared = NT >= 4;  // queries in shared memory
   constexpr int kRecord = 128 * D + 16, kRow = D + kMergePad, W = 4 * kTeams, kQueries = 8 * NT;
@@ -1291,6 +1322,7 @@ __global__ void __launch_bounds__(32 * (4 * kTeams + 1), 1) attn_team_kernel(con
   const int S = p.stages, R = p.rows * p.group;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   if (tid == 0) {
+#pragma unroll 1
     for (int i = 0; i < S; ++i) {
       dev::mbar_init(&misc.full[i], 1);
       dev::mbar_init(&misc.empty[i], 4);
@@ -1303,12 +1335,15 @@ __global__ void __launch_bounds__(32 * (4 * kTeams + 1), 1) attn_team_kernel(con
   if (warp < W && wi == 0 && lane < 2) ts.raise[lane] = 0;
   Plan pl;
   if (!make_plan(p, misc, tid, pl)) return;
-  if (warp == W) {
-    produce<D>(p, misc, pl, ring, lane);
+  if (warp >= W) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegisters));
+    if (warp == W) produce<D>(p, misc, pl, ring, lane);
     return;
   }
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTeamRegisters));
 
   int taken = 0;
+#pragma unroll 1
   for (int u = pl.begin; u < pl.end;) {
     int e, head, ib;
     locate(p, misc, u, &e, &head, &ib);
@@ -1324,6 +1359,7 @@ __global__ void __launch_bounds__(32 * (4 * kTeams + 1), 1) attn_team_kernel(con
     // what the rows see
     int low_max = 0;
     uint32_t any_vis = 0;
+#pragma unroll 1
     for (int k = lane; k < kQueries; k += 32) {
       const int m = k < R ? k / p.group : 0;
       const uint32_t x = (p.vis ? p.vis[(size_t)e * p.rows + m] : (2u << m) - 1u) & 0xFFu;
@@ -1342,6 +1378,7 @@ __global__ void __launch_bounds__(32 * (4 * kTeams + 1), 1) attn_team_kernel(con
     float coef[NT][2];
     if constexpr (kShared) {
       float* units = team_ml;  // [8 NT], until the first join
+#pragma unroll 1
       for (int q = warp; q < NT; q += W) {
         const int n = 8 * q + g;
         const uint16_t* qrow[1] = {n < R ? q0 + ((size_t)(n / p.group) * p.q_heads + n % p.group) * D : nullptr};
@@ -1478,11 +1515,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
   for (int i = 0; i < kAhead; ++i)
     if (i < np) y[i] = __ldcg(reinterpret_cast<const float4*>(from + i * step + (i == 0 ? first : 0)));
   float m = -INFINITY;
+#pragma unroll 1
   for (int c = lane; c < np; c += 32) m = fmaxf(m, __ldcg(at + c * step + (c == 0 ? first : 0)));
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
   float4 o = {0, 0, 0, 0};
   float l = 0.0f;
+#pragma unroll 1
   for (int cc = 0; cc < np; cc += 32) {
     const int c = cc + lane;
     float f = 0.0f;
@@ -1524,8 +1563,9 @@ cudaError_t launch_join(const Kv8Attn& p, cudaStream_t stream) {
   return launch(join_kernel<D>, grid, 32 * kJoinWarps, 0, stream, p);
 }
 
-template <void (*KERNEL)(Kv8Attn)>
-cudaError_t launch_attn(const Kv8Attn& p, int ctas, int smem, cudaStream_t stream) {
+// REGISTERS: what a kernel that hands registers from warp to warp was written for; with fewer its waits for them would not end.
+template <void (*KERNEL)(Kv8Attn), int REGISTERS = 0>
+cudaError_t launch_attn(const Kv8Attn& p, int ctas, int threads, int smem, cudaStream_t stream) {
   static std::atomic<unsigned long long> configured{0};
   int device = 0;
   cudaError_t e = cudaGetDevice(&device);
@@ -1534,20 +1574,27 @@ cudaError_t launch_attn(const Kv8Attn& p, int ctas, int smem, cudaStream_t strea
   if (!(configured.load(std::memory_order_relaxed) & bit)) {
     e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, max_dynamic_smem());
     if (e != cudaSuccess) return e;
+    if (REGISTERS) {
+      cudaFuncAttributes attr;
+      e = cudaFuncGetAttributes(&attr, KERNEL);
+      if (e != cudaSuccess) return e;
+      if (attr.numRegs != REGISTERS) return cudaErrorLaunchOutOfResources;
+    }
     configured.fetch_or(bit);
   }
-  return launch(KERNEL, dim3((unsigned)ctas), (p.warps + 1) * 32, (size_t)smem, stream, p);
+  return launch(KERNEL, dim3((unsigned)ctas), threads, (size_t)smem, stream, p);
 }
 
 // The instances of a cache of FMT codes, by head size and query tiles (of a warp, or of a team).
 template <int FMT>
 cudaError_t launch_attn_any(const Kv8Attn& p, int ctas, int smem, cudaStream_t s) {
+  const int threads = (p.warps + 1) * 32;
   switch (p.v.dim * 8 + p.tiles) {
-    case 64 * 8 + 1: return launch_attn<attn_kernel<FMT, 64, 1>>(p, ctas, smem, s);
-    case 64 * 8 + 2: return launch_attn<attn_kernel<FMT, 64, 2>>(p, ctas, smem, s);
-    case 128 * 8 + 1: return launch_attn<attn_kernel<FMT, 128, 1>>(p, ctas, smem, s);
-    case 128 * 8 + 2: return launch_attn<attn_kernel<FMT, 128, 2>>(p, ctas, smem, s);
-    case 256 * 8 + 1: return launch_attn<attn_kernel<FMT, 256, 1>>(p, ctas, smem, s);
+    case 64 * 8 + 1: return launch_attn<attn_kernel<FMT, 64, 1>>(p, ctas, threads, smem, s);
+    case 64 * 8 + 2: return launch_attn<attn_kernel<FMT, 64, 2>>(p, ctas, threads, smem, s);
+    case 128 * 8 + 1: return launch_attn<attn_kernel<FMT, 128, 1>>(p, ctas, threads, smem, s);
+    case 128 * 8 + 2: return launch_attn<attn_kernel<FMT, 128, 2>>(p, ctas, threads, smem, s);
+    case 256 * 8 + 1: return launch_attn<attn_kernel<FMT, 256, 1>>(p, ctas, threads, smem, s);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -1556,10 +1603,10 @@ template <int FMT, int D>
 cudaError_t launch_team_dim(const Kv8Attn& p, int ctas, int smem, cudaStream_t s) {
   cudaError_t e = cudaErrorInvalidValue;
   switch (p.tiles) {
-    case 2: e = launch_attn<attn_team_kernel<FMT, D, 2>>(p, ctas, smem, s); break;
-    case 3: e = launch_attn<attn_team_kernel<FMT, D, 3>>(p, ctas, smem, s); break;
-    case 4: e = launch_attn<attn_team_kernel<FMT, D, 4>>(p, ctas, smem, s); break;
-    case 5: e = launch_attn<attn_team_kernel<FMT, D, 5>>(p, ctas, smem, s); break;
+    case 2: e = launch_attn<attn_team_kernel<FMT, D, 2>, kLaunchRegisters>(p, ctas, kTeamThreads, smem, s); break;
+    case 3: e = launch_attn<attn_team_kernel<FMT, D, 3>, kLaunchRegisters>(p, ctas, kTeamThreads, smem, s); break;
+    case 4: e = launch_attn<attn_team_kernel<FMT, D, 4>, kLaunchRegisters>(p, ctas, kTeamThreads, smem, s); break;
+    case 5: e = launch_attn<attn_team_kernel<FMT, D, 5>, kLaunchRegisters>(p, ctas, kTeamThreads, smem, s); break;
     default: break;
   }
   return e != cudaSuccess || !p.joined ? e : launch_join<D>(p, s);
