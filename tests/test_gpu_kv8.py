@@ -113,7 +113,7 @@ class Cache:
                     held[p] += 1
             assert refs == held
 
-    def attend(self, seqs, rows, group, g, window=0, sinks=0, vis=None, scale=None, layer=0, q=None):
+    def attend(self, seqs, rows, group, g, window=0, sinks=0, vis=None, scale=None, layer=0, q=None, ws=None):
         """Runs the attention (twice: the results must be the same) and checks it against the model."""
         hq = self.heads * group
         if q is None:
@@ -121,7 +121,8 @@ class Cache:
         scale = self.dim ** -0.5 if scale is None else scale
         masks = [[(2 << m) - 1 for m in range(rows)]] * len(seqs) if vis is None else vis
         outs = []
-        ws = torch.zeros(woq.woq_kv8_attention_workspace(self.cfg, len(seqs), rows, hq), dtype=torch.uint8, device=DEV)
+        if ws is None:
+            ws = torch.zeros(woq.woq_kv8_attention_workspace(self.cfg, len(seqs), rows, hq), dtype=torch.uint8, device=DEV)
         for _ in range(2):
             out = torch.full((len(seqs) * rows + 2, hq, self.dim), 7.0, dtype=torch.bfloat16, device=DEV)
             woq.woq_kv8_attention(self.cfg, self.buf, layer, ints(seqs), rows, q.to(DEV), hq, out[1:-1], ws, scale,
@@ -320,6 +321,65 @@ def test_long_context_over_many_ctas(fmt, group, rows):
     c.prompt(0, g, 9000 - 3)
     c.draft([0], g, rows)
     c.attend([0], rows, group, g)
+
+
+def test_one_workspace_for_every_shape():
+    """What a launch needs zero is where every shape has it, and left zero."""
+    c = Cache(heads=4, seqs=12, max_tokens=4000, pages=200)
+    g = gen(11)
+    lens = [3990, 0, 640, 1999, 63, 64, 1000, 5, 130, 200, 300, 1]
+    for s, n in enumerate(lens):
+        c.prompt(s, g, n)
+    everyone = list(range(12))
+    c.draft(everyone, g, 8)
+    shapes = [([0], 1, 4), (everyone, 8, 16), ([0], 8, 5), (everyone, 1, 4), ([3, 0, 6], 3, 4), ([0], 8, 7), (everyone, 2, 4), ([2], 1, 2)]
+    size = max(woq.woq_kv8_attention_workspace(c.cfg, len(s), rows, 4 * group) for s, rows, group in shapes)
+    ws = torch.zeros(size, dtype=torch.uint8, device=DEV)
+    for s, rows, group in shapes:
+        c.attend(s, rows, group, g, ws=ws)
+
+
+@pytest.mark.parametrize("rows,group", [(1, 4), (3, 4), (8, 16)])
+def test_more_items_than_ctas(rows, group):
+    """Contiguous shares: items that begin in one CTA and end in another, one long among many short and empty ones."""
+    c = Cache(fmt=1, heads=8, seqs=24, max_tokens=3000, pages=120)
+    g = gen(12)
+    lens = [(37 * s) % 200 for s in range(24)]
+    lens[9], lens[10], lens[20] = 2999, 0, 0
+    for s, n in enumerate(lens):
+        c.prompt(s, g, n)
+    c.draft(list(range(24)), g, rows)
+    c.attend(list(range(24)), rows, group, g)
+    c.attend([(7 * s) % 24 for s in range(40)], rows, group, g)
+    c.attend([9] * 20, rows, group, g, window=700, sinks=70)
+
+
+def test_two_streams_over_one_cache():
+    """Reads of one cache may overlap; each stream has its own workspace."""
+    c = Cache(heads=4, seqs=2, max_tokens=3000, pages=100)
+    g = gen(13)
+    c.prompt(0, g, 2990)
+    c.prompt(1, g, 777)
+    c.draft([0, 1], g, 8)
+    runs = []
+    for rows, group, seqs in ((1, 5, [0, 1]), (8, 5, [1, 0])):
+        hq = 4 * group
+        q = torch.randn((2 * rows, hq, 128), generator=g).to(torch.bfloat16).to(DEV)
+        ws = torch.zeros(woq.woq_kv8_attention_workspace(c.cfg, 2, rows, hq), dtype=torch.uint8, device=DEV)
+        want = torch.empty_like(q)
+        args = (c.cfg, c.buf, 0, ints(seqs), rows, q, hq)
+        woq.woq_kv8_attention(*args, want, ws, 0.1)
+        outs = [torch.empty_like(q) for _ in range(20)]
+        runs.append((torch.cuda.Stream(), args, ws, want, outs))
+    torch.cuda.synchronize()
+    for i in range(20):
+        for stream, args, ws, _, outs in runs:
+            with torch.cuda.stream(stream):
+                woq.woq_kv8_attention(*args, outs[i], ws, 0.1)
+    torch.cuda.synchronize()
+    for _, _, _, want, outs in runs:
+        assert all(torch.equal(want, out) for out in outs)
+    c.sound()
 
 
 @pytest.mark.parametrize("hq", [4, 20, 48])

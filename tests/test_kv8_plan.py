@@ -30,8 +30,11 @@ def test_every_shape_has_a_plan_that_fits(woq, n):
     for dim, rows, group in SHAPES:
         p = plan(woq, dim, rows, group, n)
         per = p["warps"] // p["query_groups"]
-        queries = 8 * p["query_groups"] * (2 if rows * group > 8 and dim < 256 else 1)
-        assert queries >= rows * group and p["warps"] == per * p["query_groups"] and 1 <= p["warps"] <= 12
+        if rows * group > 8 and dim < 256:  # teams of four warps
+            assert p["query_groups"] == 4
+        else:  # a warp has a tile of 8 queries
+            assert p["query_groups"] == -(-rows * group // 8)
+        assert p["warps"] == per * p["query_groups"] and 1 <= p["warps"] <= 12
         assert p["stages"] % per == 0 and 2 * per <= p["stages"] <= 32, (dim, rows, group, p)
         assert p["stages"] * (128 * dim + 16) < p["smem_bytes"] <= SMEM
         assert p["ctas"] == SMS

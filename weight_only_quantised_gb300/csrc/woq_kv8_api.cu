@@ -103,25 +103,32 @@ int fill_append(const Kv8View& v, int layer, const void* qkv, int dtype, int row
   return WOQ_OK;
 }
 
+// Parts that rows * group queries are worked on in: up to 5 tiles of 8 each (head_dim 256: all at once).
+int attn_chunks(int dim, int queries) { return dim == 256 ? 1 : ((queries + 7) / 8 + 4) / 5; }
+
 int query_limit(int dim) { return dim == 256 ? 56 : 128; }  // one group of 8 queries per warp, 7 warps
 
 // What the attention takes of sequences, rows and heads (its unit counts fit 32 bits).
 bool attn_shape_ok(const Kv8View& v, int n, int rows, int q_heads) {
   return n >= 0 && n <= kKv8MaxSeqs && rows >= 1 && rows <= WOQ_KV8_ROWS && q_heads >= 1 && q_heads <= 4096 &&
          q_heads % v.heads == 0 && rows * (q_heads / v.heads) <= query_limit(v.dim) &&
-         (long long)n * v.heads * (v.blocks + kv8::kTailUnits) <= 0x7FFF0000ll;
+         (long long)n * v.heads * attn_chunks(v.dim, rows * (q_heads / v.heads)) * (v.blocks + kv8::kTailUnits) <= 0x7FFF0000ll;
 }
 
-// Workspace of the attention: [256 B][tickets][where parts are][parts]
-size_t attn_joins_offset(const Kv8View& v, int n) { return 256 + ((size_t)n * v.heads * 4 + 255) / 256 * 256; }
-size_t attn_parts_offset(const Kv8View& v, int n) { return attn_joins_offset(v, n) + ((size_t)n * v.heads * 8 + 255) / 256 * 256; }
+// Workspace of the attention: [256 B][tickets][where parts are][parts].  What has to be zero at the beginning of a launch,
+// the tickets, lies in the same place for every shape, so launches of different shapes may share a workspace.
+size_t attn_joins_offset(int sms) { return 256 + ((size_t)sms * 4 + 255) / 256 * 256; }
+size_t attn_parts_offset(const Kv8View& v, int n, int chunks, int sms) {
+  return attn_joins_offset(sms) + ((size_t)n * v.heads * chunks * 8 + 255) / 256 * 256;
+}
 
 }  // namespace
 
-// A team per block for 2 to 5 tiles of 8 queries (head_dim 64 and 128), else a warp per block.  There query
-// tiles per warp: two as soon as there is more than one tile (head_dim 256: always one; its 16
-// fragments of weighted values take twice the registers).  Warps come in whole groups, as many
-// as leave each warp two stages of the ring at least.
+// A team per block for more than 8 queries (head_dim 64 and 128), in chunks of at most 40; else a warp per block.
+// 8 heads x 32,768 tokens, head_dim 128: 12 queries 24 us (a warp per block: 48), 24 33 (61), 40 38 (86); and in two
+// chunks of 24 or 32 queries, four of 32: 48 queries 51 us (89), 64 53 (116), 128 103 (220).
+// head_dim 256: a warp per block, one tile of queries each; with more than one, groups of warps read the same blocks.
+// Warps come in whole groups, as many as leave each warp two stages of the ring at least.
 //
 // The stages are a multiple of a group's warps.  Block b goes to warp b % per of each group and to stage
 // b % stages, so then a stage always serves the same warps.  Otherwise a warp could wait for
@@ -130,26 +137,29 @@ size_t attn_parts_offset(const Kv8View& v, int n) { return attn_joins_offset(v, 
 int kv8_attn_plan(Kv8Attn* p, int smem_max) {
   const int queries = p->rows * p->group, dim = p->v.dim;
   const int tiles = (queries + 7) / 8;
-  p->team = tiles > 1 && tiles <= 5 && dim < 256;
+  p->team = tiles > 1 && dim < 256;
+  p->chunks = attn_chunks(dim, queries);
+  p->heads = p->v.heads * p->chunks;
+  p->tiles = (tiles + p->chunks - 1) / p->chunks;
+  p->queries = p->chunks > 1 ? 8 * p->tiles : queries;
   p->least_units = 8;
   const int record = 128 * dim + 16;
   if (p->team) {
-    p->tiles = tiles;
     p->query_groups = 4;  // the team's warps all read its blocks
     p->warps = 4 * kv8::kTeams;
-    const int fixed = kv8::misc_bytes(p->n) + kv8::team_fixed_bytes(tiles, dim);
+    const int fixed = kv8::misc_bytes(p->n) + kv8::team_fixed_bytes(p->tiles, dim);
     int stages = (smem_max - fixed) / record;
     stages = (stages < kv8::kMaxStages ? stages : kv8::kMaxStages) / kv8::kTeams * kv8::kTeams;
     if (stages < 2 * kv8::kTeams) return 0;
     p->stages = stages;
     return fixed + stages * record;
   }
-  p->tiles = tiles > 1 && dim < 256 ? 2 : 1;
-  p->query_groups = (tiles + p->tiles - 1) / p->tiles;
-  const int most = kv8::max_warps(p->tiles);
+  p->tiles = 1;
+  p->query_groups = tiles;
+  const int most = kv8::kMaxWarps;
   for (int per = most / p->query_groups; per >= 1; --per) {
     const int warps = per * p->query_groups;
-    const int fixed = kv8::misc_bytes(p->n) + kv8::merge_bytes(warps, p->tiles, dim);
+    const int fixed = kv8::misc_bytes(p->n) + kv8::merge_bytes(warps, 1, dim);
     int stages = (smem_max - fixed) / record;
     stages = (stages < kv8::kMaxStages ? stages : kv8::kMaxStages) / per * per;
     if (stages < 2 * per) continue;
@@ -248,7 +258,9 @@ size_t woq_kv8_attention_workspace(const woq_kv8_config* cfg, int n, int rows, i
   if (!cfg || !make_view(*cfg, &v) || !attn_shape_ok(v, n, rows, q_heads)) return 0;
   const int sms = sm_count();
   if (sms <= 0) return 0;
-  return attn_parts_offset(v, n) + (size_t)2 * sms * rows * (q_heads / v.heads) * (v.dim + 4) * 4;
+  const int all = rows * (q_heads / v.heads), chunks = attn_chunks(v.dim, all);
+  const int queries = chunks > 1 ? ((all + 7) / 8 + chunks - 1) / chunks * 8 : all;
+  return attn_parts_offset(v, n, chunks, sms) + (size_t)2 * sms * queries * (v.dim + 4) * 4;
 }
 
 int woq_kv8_plan_attention(const woq_kv8_config* cfg, int n, int rows, int q_heads, int sms, int smem_max,
@@ -292,8 +304,7 @@ int woq_kv8_attention(const woq_kv8_config* cfg, void* cache, size_t cache_bytes
   p.vis = vis;
   p.out = static_cast<uint16_t*>(out);
   p.tickets = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + 256);
-  p.joins = reinterpret_cast<int2*>(static_cast<uint8_t*>(ws) + attn_joins_offset(v, n));
-  p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + attn_parts_offset(v, n));
+  p.joins = reinterpret_cast<int2*>(static_cast<uint8_t*>(ws) + attn_joins_offset(sms));
   p.scale_log2 = (float)((double)scale * 1.4426950408889634);
   p.layer = layer;
   p.n = n;
@@ -302,13 +313,15 @@ int woq_kv8_attention(const woq_kv8_config* cfg, void* cache, size_t cache_bytes
   p.group = q_heads / v.heads;
   p.window = window;
   p.sinks = sinks;
+  p.ctas = sms;
   const int smem = kv8_attn_plan(&p, smem_max);
   if (smem == 0) return WOQ_ERR_SHAPE;
+  p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + attn_parts_offset(v, n, p.chunks, sms));
   // whether an item can lie in several CTAs: there are more items than CTAs, or one has more units than stay whole
   // (as far as max_tokens and the window tell)
   long long most = v.max_tokens / kKv8Block;
   if (window > 0) most = std::min(most, ((long long)window + kKv8Block - 1) / kKv8Block + 1 + ((long long)sinks + kKv8Block - 1) / kKv8Block);
-  p.joined = (long long)n * v.heads > sms || most + kv8::kTailUnits > kv8::kWhole;
+  p.joined = (long long)n * p.heads > sms || most + kv8::kTailUnits > kv8::kWhole;
   const bool int8 = v.fmt == WOQ_KV8_INT8;
   const auto launch = p.team ? (int8 ? launch_kv8_team_int8 : launch_kv8_team_e4m3)
                              : (int8 ? launch_kv8_attn_int8 : launch_kv8_attn_e4m3);

@@ -10,16 +10,16 @@
 // Split: an item (entry, kv head) is its blocks and one unit for its tail.  With at most as many items
 // as CTAs (one CTA per SM) every item is cut into equal pieces, one piece per CTA, the longer items
 // into more; a CTA that held the end of one item and the beginning of another would wait twice for
-// the tail, the joining of its warps and the counting in (131,071 tokens, 8 heads: 62 us against 5x).
+// the tail, the joining of its warps and the counting in (131,071 tokens, 8 heads: 62 us against 54).
 // Items of up to kWhole units stay whole: joining partials costs as much as those blocks.  With more items the
 // units are laid end to end and every CTA takes an equal share.  Lengths are read on the device, so
 // this plan is made there.  An item in several CTAs leaves fp32 partials (maximum, sum, weighted
 // values); the CTA that counts in last joins them in CTA order, so the result does not depend on the run.
 //
-// CTA: one producer warp copies whole records (16 KB at D = 128, one bulk copy each) into a ring;
-// each consumer warp takes whole blocks by itself (always from the same stages, in order), with its own running
-// maximum and sums in registers, so the main loop has no barrier but the ring's.  With more than 8 QT queries the
-// warps form groups, each for its own queries, that all read the block from shared memory.
+// CTA: one producer warp copies whole records (16 KB at D = 128, one bulk copy each) into a ring; with up to 8
+// queries each consumer warp takes whole blocks by itself (always from the same stages, in order), with its own
+// running maximum and sums in registers, so the main loop has no barrier but the ring's.  With more (D = 256) the
+// warps form groups, each for its own 8 queries, that all read the block from shared memory.
 //
 // Block: scores transposed, S^T = K Q^T (tokens x queries), so that both codes operands are the
 // 16-row one and the 8-wide one is the queries: nothing is padded beyond 8 queries.  Codes
@@ -99,52 +99,41 @@ __device__ __forceinline__ Span span_of(int len, int window, int sinks) {
 }
 
 // Running state of a warp's queries: columns 2t, 2t + 1 of each tile of 8.
-template <int D, int QT>
+template <int D>
 struct State {
-  float m[QT][2], l[QT][2];
-  float o[D / 16][QT][4];  // rows g, g + 8 of each 16 elements
+  float m[2], l[2];
+  float o[D / 16][4];  // rows g, g + 8 of each 16 elements
 };
 
-template <int D, int QT>
-__device__ __forceinline__ void clear(State<D, QT>& st) {
-#pragma unroll
-  for (int q = 0; q < QT; ++q) {
-    st.m[q][0] = st.m[q][1] = -INFINITY;
-    st.l[q][0] = st.l[q][1] = 0.0f;
-  }
+template <int D>
+__device__ __forceinline__ void clear(State<D>& st) {
+  st.m[0] = st.m[1] = -INFINITY;
+  st.l[0] = st.l[1] = 0.0f;
 #pragma unroll
   for (int j = 0; j < D / 16; ++j)
 #pragma unroll
-    for (int q = 0; q < QT; ++q)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) st.o[j][q][i] = 0.0f;
+    for (int i = 0; i < 4; ++i) st.o[j][i] = 0.0f;
 }
 
 // Raise the maxima to cover mx (per column, the same in the lanes of a column) where it passes them
 // by more than kRaise, and scale what was summed.
-template <int D, int QT>
-__device__ __forceinline__ void raise(State<D, QT>& st, const float (&mx)[QT][2]) {
-  bool up = false;
+template <int D>
+__device__ __forceinline__ void raise(State<D>& st, const float (&mx)[2]) {
+  if (!__any_sync(~0u, mx[0] > st.m[0] + kRaise || mx[1] > st.m[1] + kRaise)) return;
+  float a[2];
 #pragma unroll
-  for (int q = 0; q < QT; ++q) up |= mx[q][0] > st.m[q][0] + kRaise || mx[q][1] > st.m[q][1] + kRaise;
-  if (!__any_sync(~0u, up)) return;
+  for (int c = 0; c < 2; ++c) {
+    const float n = fmaxf(st.m[c], mx[c]);
+    a[c] = n == -INFINITY ? 1.0f : exp2_approx(st.m[c] - n);
+    st.m[c] = n;
+    st.l[c] *= a[c];
+  }
 #pragma unroll
-  for (int q = 0; q < QT; ++q) {
-    float a[2];
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const float n = fmaxf(st.m[q][c], mx[q][c]);
-      a[c] = n == -INFINITY ? 1.0f : exp2_approx(st.m[q][c] - n);
-      st.m[q][c] = n;
-      st.l[q][c] *= a[c];
-    }
-#pragma unroll
-    for (int j = 0; j < D / 16; ++j) {
-      st.o[j][q][0] *= a[0];
-      st.o[j][q][1] *= a[1];
-      st.o[j][q][2] *= a[0];
-      st.o[j][q][3] *= a[1];
-    }
+  for (int j = 0; j < D / 16; ++j) {
+    st.o[j][0] *= a[0];
+    st.o[j][1] *= a[1];
+    st.o[j][2] *= a[0];
+    st.o[j][3] *= a[1];
   }
 }
 
@@ -155,28 +144,25 @@ __device__ __forceinline__ float column_max(float x) {  // over the lanes that s
 }
 
 // What the lane knows about its columns' rows for the masks: first place seen by the window, draft mask.
-template <int QT>
 struct Columns {
-  int low[QT][2];       // places >= low are in the window
-  uint32_t vis[QT][2];  // draft rows seen
+  int low[2];       // places >= low are in the window
+  uint32_t vis[2];  // draft rows seen
 };
 
 // One block of codes at `rec` (shared memory), first token `token0`.
-template <int FMT, int D, int QT>
-__device__ __forceinline__ void block_step(State<D, QT>& st, const uint8_t* rec, const uint32_t (&qf)[QT][D / 16][2],
-                                           const float (&coef)[QT][2], const Columns<QT>& col, int token0, bool masked,
-                                           int sinks, int lane) {
+template <int FMT, int D>
+__device__ __forceinline__ void block_step(State<D>& st, const uint8_t* rec, const uint32_t (&qf)[D / 16][2],
+                                           const float (&coef)[2], const Columns& col, int token0, bool masked, int sinks,
+                                           int lane) {
   const int g = lane >> 2, t = lane & 3;
   const float ks = *reinterpret_cast<const float*>(rec + 128 * D);
   const float vs = *reinterpret_cast<const float*>(rec + 128 * D + 4);
   const uint8_t* kc = rec + t * 128 + g * 16;
-  float s[4][QT][4];
+  float s[4][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int q = 0; q < QT; ++q)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) s[i][q][c] = 0.0f;
+    for (int c = 0; c < 4; ++c) s[i][c] = 0.0f;
 #pragma unroll
   for (int c = 0; c < D / 64; ++c) {
 #pragma unroll
@@ -189,54 +175,47 @@ __device__ __forceinline__ void block_step(State<D, QT>& st, const uint8_t* rec,
         uint32_t a[4];
         f16x4_of_codes<FMT>(xs[k], a[0], a[2]);
         f16x4_of_codes<FMT>(ys[k], a[1], a[3]);
-#pragma unroll
-        for (int q = 0; q < QT; ++q) mma_f16(s[i][q], a, qf[q][4 * c + k][0], qf[q][4 * c + k][1]);
+        mma_f16(s[i], a, qf[4 * c + k][0], qf[4 * c + k][1]);
       }
     }
   }
-  float mx[QT][2];
+  float mx[2];
+  const float f0 = coef[0] * ks, f1 = coef[1] * ks;
+  mx[0] = mx[1] = -INFINITY;
 #pragma unroll
-  for (int q = 0; q < QT; ++q) {
-    const float f0 = coef[q][0] * ks, f1 = coef[q][1] * ks;
-    mx[q][0] = mx[q][1] = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      s[i][q][0] *= f0;
-      s[i][q][1] *= f1;
-      s[i][q][2] *= f0;
-      s[i][q][3] *= f1;
-      if (masked) {
-        const int tok = token0 + 16 * (g >> 1) + 4 * i + (g & 1);
-        if (tok >= sinks) {
-          if (tok < col.low[q][0]) s[i][q][0] = -INFINITY;
-          if (tok < col.low[q][1]) s[i][q][1] = -INFINITY;
-        }
-        if (tok + 2 >= sinks) {
-          if (tok + 2 < col.low[q][0]) s[i][q][2] = -INFINITY;
-          if (tok + 2 < col.low[q][1]) s[i][q][3] = -INFINITY;
-        }
+  for (int i = 0; i < 4; ++i) {
+    s[i][0] *= f0;
+    s[i][1] *= f1;
+    s[i][2] *= f0;
+    s[i][3] *= f1;
+    if (masked) {
+      const int tok = token0 + 16 * (g >> 1) + 4 * i + (g & 1);
+      if (tok >= sinks) {
+        if (tok < col.low[0]) s[i][0] = -INFINITY;
+        if (tok < col.low[1]) s[i][1] = -INFINITY;
       }
-      mx[q][0] = fmaxf(mx[q][0], fmaxf(s[i][q][0], s[i][q][2]));
-      mx[q][1] = fmaxf(mx[q][1], fmaxf(s[i][q][1], s[i][q][3]));
+      if (tok + 2 >= sinks) {
+        if (tok + 2 < col.low[0]) s[i][2] = -INFINITY;
+        if (tok + 2 < col.low[1]) s[i][3] = -INFINITY;
+      }
     }
-    mx[q][0] = column_max(mx[q][0]);
-    mx[q][1] = column_max(mx[q][1]);
+    mx[0] = fmaxf(mx[0], fmaxf(s[i][0], s[i][2]));
+    mx[1] = fmaxf(mx[1], fmaxf(s[i][1], s[i][3]));
   }
+  mx[0] = column_max(mx[0]);
+  mx[1] = column_max(mx[1]);
   raise(st, mx);
-  uint32_t pb[4][QT][2];
+  uint32_t pb[4][2];
+  const float r0 = (st.m[0] == -INFINITY ? 0.0f : st.m[0]) - kOffset;
+  const float r1 = (st.m[1] == -INFINITY ? 0.0f : st.m[1]) - kOffset;
 #pragma unroll
-  for (int q = 0; q < QT; ++q) {
-    const float r0 = (st.m[q][0] == -INFINITY ? 0.0f : st.m[q][0]) - kOffset;
-    const float r1 = (st.m[q][1] == -INFINITY ? 0.0f : st.m[q][1]) - kOffset;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float p0 = exp2_approx(s[i][q][0] - r0), p1 = exp2_approx(s[i][q][1] - r1);
-      const float p2 = exp2_approx(s[i][q][2] - r0), p3 = exp2_approx(s[i][q][3] - r1);
-      st.l[q][0] += p0 + p2;
-      st.l[q][1] += p1 + p3;
-      pb[i][q][0] = transpose8x8(pack_f16(p0, p1));
-      pb[i][q][1] = transpose8x8(pack_f16(p2, p3));
-    }
+  for (int i = 0; i < 4; ++i) {
+    const float p0 = exp2_approx(s[i][0] - r0), p1 = exp2_approx(s[i][1] - r1);
+    const float p2 = exp2_approx(s[i][2] - r0), p3 = exp2_approx(s[i][3] - r1);
+    st.l[0] += p0 + p2;
+    st.l[1] += p1 + p3;
+    pb[i][0] = transpose8x8(pack_f16(p0, p1));
+    pb[i][1] = transpose8x8(pack_f16(p2, p3));
   }
   const uint8_t* vc = rec + 64 * D + t * 128 + g * 16;
 #pragma unroll
@@ -244,23 +223,18 @@ __device__ __forceinline__ void block_step(State<D, QT>& st, const uint8_t* rec,
     const uint4 x = *reinterpret_cast<const uint4*>(vc + 2 * j * 512);
     const uint4 y = *reinterpret_cast<const uint4*>(vc + (2 * j + 1) * 512);
     const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-    float acc[QT][4];
+    float acc[4];
 #pragma unroll
-    for (int q = 0; q < QT; ++q)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) acc[q][c] = 0.0f;
+    for (int c = 0; c < 4; ++c) acc[c] = 0.0f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       uint32_t a[4];
       f16x4_of_codes<FMT>(xs[i], a[0], a[2]);
       f16x4_of_codes<FMT>(ys[i], a[1], a[3]);
-#pragma unroll
-      for (int q = 0; q < QT; ++q) mma_f16(acc[q], a, pb[i][q][0], pb[i][q][1]);
+      mma_f16(acc, a, pb[i][0], pb[i][1]);
     }
 #pragma unroll
-    for (int q = 0; q < QT; ++q)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) st.o[j][q][c] = fmaf(vs, acc[q][c], st.o[j][q][c]);
+    for (int c = 0; c < 4; ++c) st.o[j][c] = fmaf(vs, acc[c], st.o[j][c]);
   }
 }
 
@@ -278,10 +252,10 @@ __device__ __forceinline__ bool tail_sees(int r, uint32_t vis, int low, int in_t
 
 // Tail tile i: i < 4: tokens 16 t' + 4 i + {0 .. 3} of the tail (t' = 0 .. 3), in the order of the
 // key rows of a block; i = 4: tail rows 64 .. 71.  there: rows of the tail that anything may be seen of.
-template <int D, int QT>
-__device__ __forceinline__ void tail_step(State<D, QT>& st, const uint16_t* tail, int i, int in_tail, int len, int there,
-                                          const uint16_t* const (&qrow)[QT], float scale_log2, const Columns<QT>& col,
-                                          int sinks, int lane) {
+template <int D>
+__device__ __forceinline__ void tail_step(State<D>& st, const uint16_t* tail, int i, int in_tail, int len, int there,
+                                          const uint16_t* qrow, float scale_log2, const Columns& col, int sinks,
+                                          int lane) {
   const int g = lane >> 2, t = lane & 3;
   const int r0 = i < 4 ? 16 * (g >> 1) + 4 * i + (g & 1) : 64 + g;
   const int r1 = i < 4 ? r0 + 2 : kKv8Tail;
@@ -302,11 +276,9 @@ __device__ __forceinline__ void tail_step(State<D, QT>& st, const uint16_t* tail
       va[j][2] = va[j][3] = 0u;
     }
   }
-  float s[QT][4];
+  float s[4];
 #pragma unroll
-  for (int q = 0; q < QT; ++q)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) s[q][c] = 0.0f;
+  for (int c = 0; c < 4; ++c) s[c] = 0.0f;
 #pragma unroll
   for (int c = 0; c < D / 64; ++c) {
     uint32_t x[8], y[8];
@@ -318,104 +290,87 @@ __device__ __forceinline__ void tail_step(State<D, QT>& st, const uint16_t* tail
       x[4 * h] = a.x, x[4 * h + 1] = a.y, x[4 * h + 2] = a.z, x[4 * h + 3] = a.w;
       y[4 * h] = b.x, y[4 * h + 1] = b.y, y[4 * h + 2] = b.z, y[4 * h + 3] = b.w;
     }
-#pragma unroll
-    for (int q = 0; q < QT; ++q) {
-      uint32_t w[8];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint4 a = {0, 0, 0, 0};
-        if (qrow[q]) a = *reinterpret_cast<const uint4*>(qrow[q] + 16 * (4 * c + t) + 8 * h);
-        w[4 * h] = a.x, w[4 * h + 1] = a.y, w[4 * h + 2] = a.z, w[4 * h + 3] = a.w;
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t a[4] = {x[2 * k], y[2 * k], x[2 * k + 1], y[2 * k + 1]};
-        mma_bf16(s[q], a, w[2 * k], w[2 * k + 1]);
-      }
-    }
-  }
-  float mx[QT][2];
-#pragma unroll
-  for (int q = 0; q < QT; ++q) {
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      s[q][c] = tail_sees(r0, col.vis[q][c], col.low[q][c], in_tail, there, len, sinks) ? s[q][c] * scale_log2 : -INFINITY;
-      s[q][2 + c] =
-          tail_sees(r1, col.vis[q][c], col.low[q][c], in_tail, there, len, sinks) ? s[q][2 + c] * scale_log2 : -INFINITY;
-      mx[q][c] = column_max(fmaxf(s[q][c], s[q][2 + c]));
-    }
-  }
-  raise(st, mx);
-  uint32_t hi[QT][2], lo[QT][2];
-#pragma unroll
-  for (int q = 0; q < QT; ++q) {
-    float p[4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const float r = (st.m[q][c & 1] == -INFINITY ? 0.0f : st.m[q][c & 1]) - kOffset;
-      p[c] = exp2_approx(s[q][c] - r);
-      st.l[q][c & 1] += p[c];
-    }
+    uint32_t w[8];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const uint32_t u = pack_bf16(p[2 * h], p[2 * h + 1]);
-      const float f0 = __uint_as_float(u << 16), f1 = __uint_as_float(u & 0xFFFF0000u);
-      hi[q][h] = transpose8x8(u);
-      lo[q][h] = transpose8x8(pack_bf16(p[2 * h] - f0, p[2 * h + 1] - f1));
+      uint4 a = {0, 0, 0, 0};
+      if (qrow) a = *reinterpret_cast<const uint4*>(qrow + 16 * (4 * c + t) + 8 * h);
+      w[4 * h] = a.x, w[4 * h + 1] = a.y, w[4 * h + 2] = a.z, w[4 * h + 3] = a.w;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t a[4] = {x[2 * k], y[2 * k], x[2 * k + 1], y[2 * k + 1]};
+      mma_bf16(s, a, w[2 * k], w[2 * k + 1]);
     }
   }
+  float mx[2];
 #pragma unroll
-  for (int j = 0; j < D / 16; ++j)
+  for (int c = 0; c < 2; ++c) {
+    s[c] = tail_sees(r0, col.vis[c], col.low[c], in_tail, there, len, sinks) ? s[c] * scale_log2 : -INFINITY;
+    s[2 + c] = tail_sees(r1, col.vis[c], col.low[c], in_tail, there, len, sinks) ? s[2 + c] * scale_log2 : -INFINITY;
+    mx[c] = column_max(fmaxf(s[c], s[2 + c]));
+  }
+  raise(st, mx);
+  uint32_t hi[2], lo[2];
+  float p[4];
 #pragma unroll
-    for (int q = 0; q < QT; ++q) {
-      mma_bf16(st.o[j][q], va[j], hi[q][0], hi[q][1]);
-      mma_bf16(st.o[j][q], va[j], lo[q][0], lo[q][1]);
-    }
+  for (int c = 0; c < 4; ++c) {
+    const float r = (st.m[c & 1] == -INFINITY ? 0.0f : st.m[c & 1]) - kOffset;
+    p[c] = exp2_approx(s[c] - r);
+    st.l[c & 1] += p[c];
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t u = pack_bf16(p[2 * h], p[2 * h + 1]);
+    const float f0 = __uint_as_float(u << 16), f1 = __uint_as_float(u & 0xFFFF0000u);
+    hi[h] = transpose8x8(u);
+    lo[h] = transpose8x8(pack_bf16(p[2 * h] - f0, p[2 * h + 1] - f1));
+  }
+#pragma unroll
+  for (int j = 0; j < D / 16; ++j) {
+    mma_bf16(st.o[j], va[j], hi[0], hi[1]);
+    mma_bf16(st.o[j], va[j], lo[0], lo[1]);
+  }
 }
 
-// Queries of the lane's column n = g as operands, scaled by 2^-e to below 2; returns 2^e.
-template <int D, int QT>
-__device__ __forceinline__ void load_queries(uint32_t (&qf)[QT][D / 16][2], float (&unit)[QT],
-                                             const uint16_t* const (&qrow)[QT], int lane) {
+// Query row of the lane's column (nullptr: zeros) as operands, scaled by 2^-e to below 2; returns 2^e.
+template <int D>
+__device__ __forceinline__ float load_query(uint32_t (&qf)[D / 16][2], const uint16_t* qrow, int lane) {
   const int t = lane & 3;
+  uint32_t top = 0;
 #pragma unroll
-  for (int q = 0; q < QT; ++q) {
-    uint32_t top = 0;
+  for (int c = 0; c < D / 64; ++c) {
 #pragma unroll
-    for (int c = 0; c < D / 64; ++c) {
+    for (int h = 0; h < 2; ++h) {
+      uint4 a = {0, 0, 0, 0};
+      if (qrow) a = *reinterpret_cast<const uint4*>(qrow + 16 * (4 * c + t) + 8 * h);
+      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint4 a = {0, 0, 0, 0};
-        if (qrow[q]) a = *reinterpret_cast<const uint4*>(qrow[q] + 16 * (4 * c + t) + 8 * h);
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          qf[q][4 * c + 2 * h + (k >> 1)][k & 1] = w[k];
-          top = dev::bf16x2_absmax(top, w[k]);
-        }
+      for (int k = 0; k < 4; ++k) {
+        qf[4 * c + 2 * h + (k >> 1)][k & 1] = w[k];
+        top = dev::bf16x2_absmax(top, w[k]);
       }
     }
-    float m = dev::bf16x2_absmax_to_float(top);
-    m = fmaxf(m, __shfl_xor_sync(~0u, m, 1));
-    m = fmaxf(m, __shfl_xor_sync(~0u, m, 2));
-    int e = (int)(__float_as_uint(m) >> 23) - 127;  // m = 0 or subnormal: -127
-    e = e < -126 ? -126 : e > 126 ? 126 : e;
-    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-    unit[q] = __uint_as_float((uint32_t)(127 + e) << 23);
-#pragma unroll
-    for (int k = 0; k < D / 16; ++k)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t w = qf[q][k][h];
-        qf[q][k][h] = pack_f16(__uint_as_float(w << 16) * down, __uint_as_float(w & 0xFFFF0000u) * down);
-      }
   }
+  float m = dev::bf16x2_absmax_to_float(top);
+  m = fmaxf(m, __shfl_xor_sync(~0u, m, 1));
+  m = fmaxf(m, __shfl_xor_sync(~0u, m, 2));
+  int e = (int)(__float_as_uint(m) >> 23) - 127;  // m = 0 or subnormal: -127
+  e = e < -126 ? -126 : e > 126 ? 126 : e;
+  const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+  for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t w = qf[k][h];
+      qf[k][h] = pack_f16(__uint_as_float(w << 16) * down, __uint_as_float(w & 0xFFFF0000u) * down);
+    }
+  return __uint_as_float((uint32_t)(127 + e) << 23);
 }
 
 constexpr int kMaxStages = 32;
-// Most consumer warps: with one query tile per warp 7 (and the producer: two per sub-partition, so 255
-// registers each); with two, where the tensor cores set the pace, 10.
-__host__ __device__ constexpr int max_warps(int tiles) { return tiles == 1 ? 7 : 10; }
+// Most warps that each take a block: two per sub-partition with the producer, so 255 registers each.
+constexpr int kMaxWarps = 7;
 // Shared memory: barriers, flags, units and lengths of the entries; the merge buffer; the ring.
 struct Misc {
   uint64_t full[kMaxStages], empty[kMaxStages];
@@ -442,6 +397,12 @@ __device__ __forceinline__ float part_factor(float pm, float pl, float m) {
 
 __device__ __forceinline__ int* lens_of(const Kv8Attn& p, Misc& misc) { return misc.entries + p.n + 1; }
 __device__ __forceinline__ int* seqs_of(const Kv8Attn& p, Misc& misc) { return misc.entries + 3 * p.n + 2; }
+
+// Where query n of a kv head is in p.q and p.out.
+template <int D>
+__device__ __forceinline__ size_t query_at(const Kv8Attn& p, int e, int kv_head, int n) {
+  return (((size_t)e * p.rows + n / p.group) * p.q_heads + (size_t)kv_head * p.group + n % p.group) * D;
+}
 
 // This CTA's units [begin, end), of all items laid end to end.  All counts fit 32 bits (checked on the host).
 struct Plan {
@@ -494,9 +455,9 @@ __device__ __forceinline__ void lay_out(const Kv8Attn& p, Misc& misc, int lane) 
   if (lane == 0) misc.entries[p.n] = run;
   // The least share with which all pieces have a CTA, to 1/32: the lanes try 32 of them at once.
   int share = 0;
-  if (p.n * v.heads <= ctas) {
+  if (p.n * p.heads <= ctas) {
     __syncwarp();
-    const int room = ctas / v.heads;  // pieces of one head
+    const int room = ctas / p.heads;  // pieces of one head
     share = max(p.least_units, (run + room - 1) / room);
 #pragma unroll 1
     while (p.n > 1) {  // ends: with a share beyond the longest item there are n <= room pieces
@@ -520,17 +481,17 @@ __device__ __forceinline__ void lay_out(const Kv8Attn& p, Misc& misc, int lane) 
         const int z = __shfl_up_sync(~0u, y, d);
         if (lane >= d) y += z;
       }
-      if (e < p.n) cuts[e] = (total + y - own) * v.heads;
+      if (e < p.n) cuts[e] = (total + y - own) * p.heads;
       total += __shfl_sync(~0u, y, 31);
     }
-    if (lane == 0) cuts[p.n] = total * v.heads;
+    if (lane == 0) cuts[p.n] = total * p.heads;
   }
   if (lane == 0) misc.share = share;
 }
 
 // This CTA's share of what lay_out left; false: none.
 __device__ __forceinline__ bool take_share(const Kv8Attn& p, Misc& misc, Plan& pl) {
-  const int heads = p.v.heads, block = (int)blockIdx.x;
+  const int heads = p.heads, block = (int)blockIdx.x;
   const int* cuts = lens_of(p, misc) + p.n;
   if (misc.share > 0) {
     if (block >= cuts[p.n]) return false;
@@ -561,9 +522,9 @@ __device__ __forceinline__ void locate(const Kv8Attn& p, const Misc& misc, int u
 #pragma unroll 1
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (prefix[mid] * p.v.heads <= u) lo = mid; else hi = mid - 1;
+    if (prefix[mid] * p.heads <= u) lo = mid; else hi = mid - 1;
   }
-  const int per = prefix[lo + 1] - prefix[lo], first = prefix[lo] * p.v.heads;
+  const int per = prefix[lo + 1] - prefix[lo], first = prefix[lo] * p.heads;
   *entry = lo;
   *head = (u - first) / per;
   *item_begin = first + *head * per;
@@ -582,15 +543,16 @@ __device__ __forceinline__ void prefetch_first(const Kv8Attn& p, Misc& misc, con
   const int k = pl.begin - ib + lane, stop = min(pl.end - ib, per - kTailUnits);
   if (lane < p.stages && k < stop) {
     const int page = (int)dev::ld_relaxed_u32(v.table_row(seq) + (k < sp.head_blocks ? k : sp.from + (k - sp.head_blocks)));
-    if (page >= 0 && page < v.pages) dev::bulk_prefetch_l2(v.record(page, p.layer, head), (uint32_t)v.record_bytes());
+    if (page >= 0 && page < v.pages) dev::bulk_prefetch_l2(v.record(page, p.layer, head / p.chunks), (uint32_t)v.record_bytes());
   }
-  const int q_elems = p.group * v.dim;  // of one row
+  const int kv_head = head / p.chunks, q_elems = p.group * v.dim;  // of one row
 #pragma unroll 1
   for (int x = lane * 64; x < q_elems * p.rows; x += 32 * 64) {
     const int row = x / q_elems;
-    dev::prefetch_l2(p.q + (((size_t)e * p.rows + row) * p.q_heads + (size_t)head * p.group) * v.dim + (x - row * q_elems));
+    dev::prefetch_l2(p.q + (((size_t)e * p.rows + row) * p.q_heads + (size_t)kv_head * p.group) * v.dim + (x - row * q_elems));
   }
-  if (lane == 31 && pl.end >= ib + per) dev::bulk_prefetch_l2(v.tail(p.layer, seq, head), (uint32_t)v.tail_elems() * 2u);
+  if (lane == 31 && pl.end >= ib + per)
+    dev::bulk_prefetch_l2(v.tail(p.layer, seq, kv_head), (uint32_t)v.tail_elems() * 2u);
 }
 
 // This CTA's plan; false: nothing to do.  All threads.
@@ -655,6 +617,7 @@ __device__ __forceinline__ void produce(const Kv8Attn& p, Misc& misc, const Plan
     if (b0 < b1) {
       const Span sp = span_of(lens_of(p, misc)[e], p.window, p.sinks);
       const int32_t* table = v.table_row(p.seqs ? p.seqs[e] : e);
+      const int kv_head = head / p.chunks;
 #pragma unroll 1
       for (int c0 = b0; c0 < b1; c0 += 32) {
         const int k = c0 + lane;
@@ -674,7 +637,7 @@ __device__ __forceinline__ void produce(const Kv8Attn& p, Misc& misc, const Plan
           }
           if (lane == 0) {
             dev::mbar_arrive_expect_tx(&misc.full[stage], kRecord);
-            dev::bulk_copy_g2s(ring + (size_t)stage * kRecord, v.record(pg, p.layer, head), kRecord, &misc.full[stage]);
+            dev::bulk_copy_g2s(ring + (size_t)stage * kRecord, v.record(pg, p.layer, kv_head), kRecord, &misc.full[stage]);
           }
           ++issued;
         }
@@ -703,12 +666,13 @@ __device__ __forceinline__ void finish(const Kv8Attn& p, Misc& misc, const Plan&
                                        const float* ml_of, int sets, int stride, int e, int head, int ib, int per, int tid,
                                        int consumers) {
   constexpr int kRow = D + kMergePad;
-  const int R = p.rows * p.group, lane = tid & 31;
+  // this item's queries: [base, base + R) of the kv head
+  const int kv_head = LATER ? head / p.chunks : head, base = LATER ? head % p.chunks * p.queries : 0;
+  const int Q = p.queries, R = LATER ? min(Q, p.rows * p.group - base) : Q, lane = tid & 31;
   const bool whole = plan.cut ? plan.pieces == 1 : ib >= plan.begin && ib + per <= plan.end;
   const int mine = plan.cut || ib <= plan.begin ? 0 : 1;  // the item that holds the share's first unit, and the other
-  const size_t slot = (size_t)R * (D + 4);
+  const size_t slot = (size_t)Q * (D + 4);
   float* part = p.parts + ((size_t)blockIdx.x * 2 + mine) * slot;
-  uint16_t* out0 = p.out + ((size_t)e * p.rows * p.q_heads + (size_t)head * p.group) * D;
 #pragma unroll 1
   for (int x = tid; x < R * (D / 4); x += consumers) {
     const int n = x / (D / 4), d = (x % (D / 4)) * 4;
@@ -734,24 +698,24 @@ __device__ __forceinline__ void finish(const Kv8Attn& p, Misc& misc, const Plan&
     }
     if (whole) {
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-      *reinterpret_cast<uint2*>(out0 + ((size_t)(n / p.group) * p.q_heads + n % p.group) * D + d) =
+      *reinterpret_cast<uint2*>(p.out + query_at<D>(p, e, kv_head, base + n) + d) =
           make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
     } else {
       *reinterpret_cast<float4*>(part + (size_t)n * D + d) = o;
-      if (d == 0) *reinterpret_cast<float2*>(part + (size_t)R * D + 2 * n) = make_float2(m, l);
+      if (d == 0) *reinterpret_cast<float2*>(part + (size_t)Q * D + 2 * n) = make_float2(m, l);
     }
   }
   if (LATER && tid == 0 && ib >= plan.begin) {
     const int c0 = (int)blockIdx.x;
     const int pieces = whole ? 1 : plan.cut ? plan.pieces : (ib + per - 1) / plan.share - c0 + 1;
-    p.joins[(size_t)e * p.v.heads + head] = make_int2(2 * c0 + mine, pieces);
+    p.joins[(size_t)e * p.heads + head] = make_int2(2 * c0 + mine, pieces);
   }
   if (whole || LATER) return;
   // CTAs c0 .. c1 share the item; the one that counts in last joins their parts in CTA order
   const int c0 = plan.cut ? plan.piece0 : ib / plan.share;
   const int c1 = plan.cut ? plan.piece0 + plan.pieces - 1 : (ib + per - 1) / plan.share;
   dev::named_barrier_sync(1, consumers);
-  uint32_t* ticket = p.tickets + (size_t)e * p.v.heads + head;
+  uint32_t* ticket = p.tickets + c0;
   if (tid == 0) misc.last = dev::atomic_add_acq_rel_gpu(ticket, 1u) == (uint32_t)(c1 - c0);
   dev::named_barrier_sync(1, consumers);
   if (!misc.last) return;
@@ -831,15 +795,15 @@ __device__ __forceinline__ void finish(const Kv8Attn& p, Misc& misc, const Plan&
 #pragma unroll 8
       for (; c < np; ++c) add(fs[c], __ldcg(reinterpret_cast<const float4*>(from + c * step + (c == 0 ? first : 0))));
       const float l = sums[n - n0], inv = l == 0.0f ? 0.0f : 1.0f / l;
-      *reinterpret_cast<uint2*>(out0 + ((size_t)(n / p.group) * p.q_heads + n % p.group) * D + d) =
+      *reinterpret_cast<uint2*>(p.out + query_at<D>(p, e, kv_head, base + n) + d) =
           make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
     }
     if (n1 < R) dev::named_barrier_sync(1, consumers);
   }
 }
 
-template <int FMT, int D, int QT>
-__global__ void __launch_bounds__(32 * (max_warps(QT) + 1), 1) attn_kernel(const __grid_constant__ Kv8Attn p) {
+template <int FMT, int D>
+__global__ void __launch_bounds__(32 * (kMaxWarps + 1), 1) attn_kernel(const __grid_constant__ Kv8Attn p) {
   extern __shared__ __align__(128) uint8_t smem[];
   Misc& misc = *reinterpret_cast<Misc*>(smem);
   const Kv8View& v = p.v;
@@ -847,9 +811,9 @@ __global__ void __launch_bounds__(32 * (max_warps(QT) + 1), 1) attn_kernel(const
   const int R = p.rows * p.group;
   constexpr int kRecord = 128 * D + 16;
   constexpr int kRow = D + kMergePad;
-  float* merge = reinterpret_cast<float*>(smem + misc_bytes(p.n));  // [W][8 QT][D + pad]
-  float* warp_ml = merge + (size_t)W * 8 * QT * kRow;               // [W][8 QT][2]
-  uint8_t* ring = smem + misc_bytes(p.n) + merge_bytes(W, QT, D);
+  float* merge = reinterpret_cast<float*>(smem + misc_bytes(p.n));  // [W][8][D + pad]
+  float* warp_ml = merge + (size_t)W * 8 * kRow;                    // [W][8][2]
+  uint8_t* ring = smem + misc_bytes(p.n) + merge_bytes(W, 1, D);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   if (tid == 0) {
@@ -886,37 +850,28 @@ __global__ void __launch_bounds__(32 * (max_warps(QT) + 1), 1) attn_kernel(const
     const int seq = p.seqs ? p.seqs[e] : e;
 
     // queries and what their rows see
-    const uint16_t* qrow[QT];
-    Columns<QT> col;
+    Columns col;
     int low_max = 0;
     uint32_t any_vis = 0;
+    const int base = 8 * group, n = base + g;
+    const uint16_t* qrow = n < R ? p.q + query_at<D>(p, e, head, n) : nullptr;
 #pragma unroll
-    for (int q = 0; q < QT; ++q) {
-      const int base = (group * QT + q) * 8;
-      const int n = base + g;
-      qrow[q] = n < R ? p.q + (((size_t)e * p.rows + n / p.group) * p.q_heads + (size_t)head * p.group + n % p.group) * D
-                      : nullptr;
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int k = base + 2 * t + c, m = k < R ? k / p.group : 0;
-        const uint32_t vis = (p.vis ? p.vis[(size_t)e * p.rows + m] : (2u << m) - 1u) & 0xFFu;
-        col.vis[q][c] = vis;
-        any_vis |= vis;
-        col.low[q][c] = p.window > 0 ? len + __popc(vis) - p.window : 0;
-        low_max = max(low_max, col.low[q][c]);
-      }
+    for (int c = 0; c < 2; ++c) {
+      const int k = base + 2 * t + c, m = k < R ? k / p.group : 0;
+      const uint32_t vis = (p.vis ? p.vis[(size_t)e * p.rows + m] : (2u << m) - 1u) & 0xFFu;
+      col.vis[c] = vis;
+      any_vis |= vis;
+      col.low[c] = p.window > 0 ? len + __popc(vis) - p.window : 0;
+      low_max = max(low_max, col.low[c]);
     }
     low_max = __reduce_max_sync(~0u, low_max);
-    State<D, QT> st;
+    State<D> st;
     clear(st);
-    uint32_t qf[QT][D / 16][2];
-    float unit[QT], coef[QT][2];
-    load_queries<D, QT>(qf, unit, qrow, lane);
-#pragma unroll
-    for (int q = 0; q < QT; ++q) {
-      coef[q][0] = __shfl_sync(~0u, unit[q], 8 * t) * p.scale_log2;  // lane 4 g' holds column g'
-      coef[q][1] = __shfl_sync(~0u, unit[q], 8 * t + 4) * p.scale_log2;
-    }
+    uint32_t qf[D / 16][2];
+    const float unit = load_query<D>(qf, qrow, lane);
+    float coef[2];
+    coef[0] = __shfl_sync(~0u, unit, 8 * t) * p.scale_log2;  // lane 4 g' holds column g'
+    coef[1] = __shfl_sync(~0u, unit, 8 * t + 4) * p.scale_log2;
     if (has_tail) {
       const uint16_t* tail = v.tail(p.layer, seq, head);
       const int in_tail = len - sp.full * kKv8Block;
@@ -924,7 +879,7 @@ __global__ void __launch_bounds__(32 * (max_warps(QT) + 1), 1) attn_kernel(const
 #pragma unroll 1
       for (int i = slot; i < 5; i += WG)
         if (there > (i < 4 ? 4 * i : 64))
-          tail_step<D, QT>(st, tail, i, in_tail, len, there, qrow, p.scale_log2, col, p.sinks, lane);
+          tail_step<D>(st, tail, i, in_tail, len, there, qrow, p.scale_log2, col, p.sinks, lane);
     }
     bool ok = true;
     int k = b0 + ((slot - taken) % WG + WG) % WG;  // ring positions taken + (k - b0) = slot mod WG (S a multiple of WG)
@@ -938,8 +893,8 @@ __global__ void __launch_bounds__(32 * (max_warps(QT) + 1), 1) attn_kernel(const
       }
       const int blk = k < sp.head_blocks ? k : sp.from + (k - sp.head_blocks);
       const int token0 = blk * kKv8Block;
-      block_step<FMT, D, QT>(st, ring + (size_t)stage * kRecord, qf, coef, col, token0,
-                             token0 < low_max && token0 + kKv8Block > p.sinks, p.sinks, lane);
+      block_step<FMT, D>(st, ring + (size_t)stage * kRecord, qf, coef, col, token0,
+                         token0 < low_max && token0 + kKv8Block > p.sinks, p.sinks, lane);
       __syncwarp();
       if (lane == 0) dev::mbar_arrive(&misc.empty[stage]);
     }
@@ -948,32 +903,28 @@ __global__ void __launch_bounds__(32 * (max_warps(QT) + 1), 1) attn_kernel(const
 
     // join the warps: sums over the lanes of a column, then over the warps of the group
 #pragma unroll
-    for (int q = 0; q < QT; ++q)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float l = st.l[q][c];
-        l += __shfl_xor_sync(~0u, l, 4);
-        l += __shfl_xor_sync(~0u, l, 8);
-        l += __shfl_xor_sync(~0u, l, 16);
-        if (g == 0) {
-          const int row = warp * 8 * QT + 8 * q + 2 * t + c;
-          warp_ml[2 * row] = st.m[q][c];
-          warp_ml[2 * row + 1] = l;
-        }
+    for (int c = 0; c < 2; ++c) {
+      float l = st.l[c];
+      l += __shfl_xor_sync(~0u, l, 4);
+      l += __shfl_xor_sync(~0u, l, 8);
+      l += __shfl_xor_sync(~0u, l, 16);
+      if (g == 0) {
+        const int row = warp * 8 + 2 * t + c;
+        warp_ml[2 * row] = st.m[c];
+        warp_ml[2 * row + 1] = l;
       }
+    }
 #pragma unroll
     for (int j = 0; j < D / 16; ++j)
 #pragma unroll
-      for (int q = 0; q < QT; ++q)
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          merge[(size_t)(warp * 8 * QT + 8 * q + 2 * t + (c & 1)) * kRow + 16 * j + g + 8 * (c >> 1)] = st.o[j][q][c];
+      for (int c = 0; c < 4; ++c)
+        merge[(size_t)(warp * 8 + 2 * t + (c & 1)) * kRow + 16 * j + g + 8 * (c >> 1)] = st.o[j][c];
     dev::named_barrier_sync(1, consumers);
     if (misc.fail) {  // a wait ran out: nothing of this item is written
       if (tid == 0) flag(v, WOQ_DEVERR_TIMEOUT);
       return;
     }
-    finish<D, false>(p, misc, pl, merge, W * 8 * QT * kRow, warp_ml, WG, G * 8 * QT, e, head, ib, per, tid, consumers);
+    finish<D, false>(p, misc, pl, merge, W * 8 * kRow, warp_ml, WG, G * 8, e, head, ib, per, tid, consumers);
     dev::named_barrier_sync(1, consumers);  // the merge buffer is free again
     u = stop;
   }
@@ -1206,12 +1157,11 @@ __device__ __forceinline__ void team_block(TeamState<D, NT>& st, TeamShared<NT>&
 // bf16 parts, the high ones in buffer 0 and the low ones in buffer 1.
 template <int D, int NT>
 __device__ void team_tail(TeamState<D, NT>& st, TeamShared<NT>& ts, const uint16_t* tail, bool over, int in_tail, int len,
-                          int there, const Kv8Attn& p, const uint16_t* q0, const int* low, const uint32_t* vis, int wi, int team,
+                          int there, const Kv8Attn& p, int e, int kv_head, int base, int R, const int* low, const uint32_t* vis, int wi, int team,
                           int lane) {
   const int g = lane >> 2, t = lane & 3;
   const bool mine = !over || wi == 0;  // this warp has tokens
   const int r0 = over ? 64 + g : 16 * (g >> 1) + 4 * wi + (g & 1), r1 = over ? kKv8Tail : r0 + 2;
-  const int R = p.rows * p.group;
   // every load is issued before the first product: they go to L2 or HBM, one round trip instead of one each
   const uint16_t* tv = tail + kKv8Tail * D + wi * (D / 4) * kKv8Tail;
   uint4 vx[D / 64][2], vy[D / 64][2];
@@ -1249,7 +1199,7 @@ __device__ void team_tail(TeamState<D, NT>& st, TeamShared<NT>& ts, const uint16
 #pragma unroll
         for (int q = 0; q < NT; ++q) {
           const int n = min(8 * q + g, R - 1);  // columns from R on repeat the last query (their results are not used)
-          w[q][h] = *reinterpret_cast<const uint4*>(q0 + ((size_t)(n / p.group) * p.q_heads + n % p.group) * D + d);
+          w[q][h] = *reinterpret_cast<const uint4*>(p.q + query_at<D>(p, e, kv_head, base + n) + d);
         }
       }
 #pragma unroll
@@ -1319,7 +1269,7 @@ __global__ void __launch_bounds__(kTeamThreads, 1) attn_team_kernel(const __grid
   uint32_t* vis = reinterpret_cast<uint32_t*>(low + kQueries);                                                 // [8 NT]
   uint8_t* ring = smem + misc_bytes(p.n) + team_fixed_bytes(NT, D);
   const Kv8View& v = p.v;
-  const int S = p.stages, R = p.rows * p.group;
+  const int S = p.stages;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   if (tid == 0) {
 #pragma unroll 1
@@ -1354,14 +1304,15 @@ __global__ void __launch_bounds__(kTeamThreads, 1) attn_team_kernel(const __grid
     const Span sp = span_of(there ? len : 0, p.window, p.sinks);
     const bool has_tail = stop == ib + per && there;
     const int b0 = u - ib, b1 = min(stop - ib, per - kTailUnits), blocks = max(0, b1 - b0);
-    const uint16_t* q0 = p.q + ((size_t)e * p.rows * p.q_heads + (size_t)head * p.group) * D;
+    // this item's queries: [base, base + R) of the kv head
+    const int kv_head = head / p.chunks, base = head % p.chunks * kQueries, R = min(kQueries, p.rows * p.group - base);
 
     // what the rows see
     int low_max = 0;
     uint32_t any_vis = 0;
 #pragma unroll 1
     for (int k = lane; k < kQueries; k += 32) {
-      const int m = k < R ? k / p.group : 0;
+      const int m = (base + min(k, R - 1)) / p.group;
       const uint32_t x = (p.vis ? p.vis[(size_t)e * p.rows + m] : (2u << m) - 1u) & 0xFFu;
       const int lo = p.window > 0 ? len + __popc(x) - p.window : 0;
       any_vis |= x;
@@ -1381,13 +1332,11 @@ __global__ void __launch_bounds__(kTeamThreads, 1) attn_team_kernel(const __grid
 #pragma unroll 1
       for (int q = warp; q < NT; q += W) {
         const int n = 8 * q + g;
-        const uint16_t* qrow[1] = {n < R ? q0 + ((size_t)(n / p.group) * p.q_heads + n % p.group) * D : nullptr};
-        float unit[1];
-        uint32_t f[1][D / 16][2];
-        load_queries<D, 1>(f, unit, qrow, lane);
-        if (t == 0) units[n] = unit[0];
+        uint32_t f[D / 16][2];
+        const float unit = load_query<D>(f, n < R ? p.q + query_at<D>(p, e, kv_head, base + n) : nullptr, lane);
+        if (t == 0) units[n] = unit;
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) shared_q[(q * (D / 16) + k) * 32 + lane] = make_uint2(f[0][k][0], f[0][k][1]);
+        for (int k = 0; k < D / 16; ++k) shared_q[(q * (D / 16) + k) * 32 + lane] = make_uint2(f[k][0], f[k][1]);
       }
       dev::named_barrier_sync(1, W * 32);
 #pragma unroll
@@ -1395,18 +1344,12 @@ __global__ void __launch_bounds__(kTeamThreads, 1) attn_team_kernel(const __grid
 #pragma unroll
         for (int c = 0; c < 2; ++c) coef[q][c] = units[8 * q + 2 * t + c] * p.scale_log2;
     } else {
-      const uint16_t* qrow[NT];
-      float unit[NT];
 #pragma unroll
       for (int q = 0; q < NT; ++q) {
         const int n = 8 * q + g;
-        qrow[q] = n < R ? q0 + ((size_t)(n / p.group) * p.q_heads + n % p.group) * D : nullptr;
-      }
-      load_queries<D, NT>(qf, unit, qrow, lane);
-#pragma unroll
-      for (int q = 0; q < NT; ++q) {
-        coef[q][0] = __shfl_sync(~0u, unit[q], 8 * t) * p.scale_log2;
-        coef[q][1] = __shfl_sync(~0u, unit[q], 8 * t + 4) * p.scale_log2;
+        const float unit = load_query<D>(qf[q], n < R ? p.q + query_at<D>(p, e, kv_head, base + n) : nullptr, lane);
+        coef[q][0] = __shfl_sync(~0u, unit, 8 * t) * p.scale_log2;
+        coef[q][1] = __shfl_sync(~0u, unit, 8 * t + 4) * p.scale_log2;
       }
       dev::named_barrier_sync(1, W * 32);
     }
@@ -1425,10 +1368,10 @@ __global__ void __launch_bounds__(kTeamThreads, 1) attn_team_kernel(const __grid
         for (int c = 0; c < 4; ++c) st.o[j][q][c] = 0.0f;
     }
     if (has_tail && team == (taken + blocks) % kTeams) {  // the team whose turn comes next after the blocks
-      const uint16_t* tail = v.tail(p.layer, p.seqs ? p.seqs[e] : e, head);
+      const uint16_t* tail = v.tail(p.layer, p.seqs ? p.seqs[e] : e, kv_head);
       const int in_tail = len - sp.full * kKv8Block, rows = in_tail + 32 - __clz((int)any_vis);  // at most 63 + 8
-      if (rows > 0) team_tail<D, NT>(st, ts, tail, false, in_tail, len, rows, p, q0, low, vis, wi, team, lane);
-      if (rows > 64) team_tail<D, NT>(st, ts, tail, true, in_tail, len, rows, p, q0, low, vis, wi, team, lane);
+      if (rows > 0) team_tail<D, NT>(st, ts, tail, false, in_tail, len, rows, p, e, kv_head, base, R, low, vis, wi, team, lane);
+      if (rows > 64) team_tail<D, NT>(st, ts, tail, true, in_tail, len, rows, p, e, kv_head, base, R, low, vis, wi, team, lane);
     }
     bool ok = true;
     int k = b0 + ((team - taken) % kTeams + kTeams) % kTeams;  // S is a multiple of the teams
@@ -1498,16 +1441,19 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
   begin_after_prior();
   uint32_t magic;
   if (!is_ours(p.v, &magic)) return;  // nothing was left
-  const int R = p.rows * p.group, lane = threadIdx.x & 31, n = (int)blockIdx.y * kJoinWarps + ((int)threadIdx.x >> 5);
+  const int e = (int)blockIdx.x / p.heads, head = (int)blockIdx.x % p.heads, base = head % p.chunks * p.queries;
+  const int Q = p.queries, lane = threadIdx.x & 31, n = (int)blockIdx.y * kJoinWarps + ((int)threadIdx.x >> 5);
   const int2 where = p.joins[blockIdx.x];
   const int np = where.y;
-  if (np <= 1 || n >= R) return;
+  // (after a wait that ran out, flagged, a place may be one of an earlier launch: nothing outside the parts is read)
+  if (where.x < 0 || np > p.ctas - (where.x >> 1)) return;
+  if (np <= 1 || n >= min(Q, p.rows * p.group - base)) return;
   // the first part's slot, and the first slots of the CTAs that follow
-  const size_t slot = (size_t)R * (D + 4), step = 2 * slot;
+  const size_t slot = (size_t)Q * (D + 4), step = 2 * slot;
   const float* parts = p.parts + (size_t)(where.x >> 1) * step;
   const size_t first = (where.x & 1) ? slot : 0;
   constexpr int kLanes = D / 4;  // lanes that hold four elements each
-  const float* at = parts + (size_t)R * D + 2 * n;
+  const float* at = parts + (size_t)Q * D + 2 * n;
   const float* from = parts + (size_t)n * D + 4 * (lane % kLanes);
   constexpr int kAhead = 20;
   float4 y[kAhead];
@@ -1551,15 +1497,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  const int e = (int)blockIdx.x / p.v.heads, head = (int)blockIdx.x % p.v.heads;
-  uint16_t* out = p.out + (((size_t)e * p.rows + n / p.group) * p.q_heads + (size_t)head * p.group + n % p.group) * D;
+  uint16_t* out = p.out + query_at<D>(p, e, head / p.chunks, base + n);
   if (lane < kLanes)
     *reinterpret_cast<uint2*>(out + 4 * lane) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
 }
 
 template <int D>
 cudaError_t launch_join(const Kv8Attn& p, cudaStream_t stream) {
-  const dim3 grid((unsigned)(p.n * p.v.heads), (unsigned)((p.rows * p.group + kJoinWarps - 1) / kJoinWarps));
+  const dim3 grid((unsigned)(p.n * p.heads), (unsigned)((p.queries + kJoinWarps - 1) / kJoinWarps));
   return launch(join_kernel<D>, grid, 32 * kJoinWarps, 0, stream, p);
 }
 
@@ -1585,16 +1530,14 @@ cudaError_t launch_attn(const Kv8Attn& p, int ctas, int threads, int smem, cudaS
   return launch(KERNEL, dim3((unsigned)ctas), threads, (size_t)smem, stream, p);
 }
 
-// The instances of a cache of FMT codes, by head size and query tiles (of a warp, or of a team).
+// The instances of a cache of FMT codes, by head size (and a team's query tiles).
 template <int FMT>
 cudaError_t launch_attn_any(const Kv8Attn& p, int ctas, int smem, cudaStream_t s) {
   const int threads = (p.warps + 1) * 32;
-  switch (p.v.dim * 8 + p.tiles) {
-    case 64 * 8 + 1: return launch_attn<attn_kernel<FMT, 64, 1>>(p, ctas, threads, smem, s);
-    case 64 * 8 + 2: return launch_attn<attn_kernel<FMT, 64, 2>>(p, ctas, threads, smem, s);
-    case 128 * 8 + 1: return launch_attn<attn_kernel<FMT, 128, 1>>(p, ctas, threads, smem, s);
-    case 128 * 8 + 2: return launch_attn<attn_kernel<FMT, 128, 2>>(p, ctas, threads, smem, s);
-    case 256 * 8 + 1: return launch_attn<attn_kernel<FMT, 256, 1>>(p, ctas, threads, smem, s);
+  switch (p.v.dim) {
+    case 64: return launch_attn<attn_kernel<FMT, 64>>(p, ctas, threads, smem, s);
+    case 128: return launch_attn<attn_kernel<FMT, 128>>(p, ctas, threads, smem, s);
+    case 256: return launch_attn<attn_kernel<FMT, 256>>(p, ctas, threads, smem, s);
     default: return cudaErrorInvalidValue;
   }
 }

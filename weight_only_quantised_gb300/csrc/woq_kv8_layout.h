@@ -101,15 +101,17 @@ struct Kv8Attn {
   const uint16_t* q;
   const uint32_t* vis;
   uint16_t* out;
-  uint32_t* tickets;  // one word per (entry, head), zero between launches
-  int2* joins;        // of each (entry, head): twice the first CTA with a part (+ 1: its second slot), number of parts
-  float* parts;       // two parts per CTA of rows * group * (dim + 4) floats
+  uint32_t* tickets;  // one word per CTA, that an item begins in and does not end in: zero between launches
+  int2* joins;        // of each item: twice the first CTA with a part (+ 1: its second slot), number of parts
+  float* parts;       // two parts per CTA of queries * (dim + 4) floats
   float scale_log2;
   int layer, n, rows, q_heads, group, window, sinks;
+  int chunks, queries;  // parts that a kv head's rows * group queries are worked on in, and the queries of one
+  int heads;         // items of an entry: kv heads * chunks, the chunks of one head next to each other
   int joined;        // 0: no item lies in several CTAs
   int team;          // 1: a team of four warps per block, 0: a warp
-  int tiles;         // tiles of 8 queries of a warp (of a team)
-  int warps, query_groups, stages;
+  int tiles;         // tiles of 8 queries of a team (a warp has one)
+  int warps, query_groups, stages, ctas;
   int least_units;   // units a CTA takes at least (while there are more CTAs than that needs, they idle)
 };
 
