@@ -215,8 +215,9 @@ WOQ_API int woq_kv8_compact(const woq_kv8_config* cfg, void* cache, size_t cache
  * other up to woq_kv8_bytes(cfg).  0 for invalid arguments. */
 WOQ_API size_t woq_kv8_page_offset(const woq_kv8_config* cfg, int page);
 
-/* Tokens first .. first + count - 1 of a sequence, back in bf16 (RN(code * s), or as held in
- * the tail): k, v device bf16 [layers read][count][kv_heads][head_dim], 16-byte aligned.
+/* Tokens first .. first + count - 1 of a sequence, back in bf16 (code * s rounded to fp32 and then
+ * to bf16, or as held in the tail; of a token that was not finite the value is 0 and the key NaN,
+ * and so are the other keys of its block and head once the block is full): k, v device bf16 [layers read][count][kv_heads][head_dim], 16-byte aligned.
  * layer -1: all layers.  Places up to 7 behind the sequence's end are its draft rows; if
  * first + count goes beyond them nothing is written (WOQ_DEVERR_STATE). */
 WOQ_API int woq_kv8_read(const woq_kv8_config* cfg, void* cache, size_t cache_bytes, int layer, int seq, int first,

@@ -31,6 +31,10 @@
 // product's operand: O^T = V^T P^T, from the transposed value codes.  Each block's product is
 // scaled by its value scale in fp32.
 //
+// Measured (8 heads, D = 128, launches back to back): 131,071 tokens x 5 queries 50 us (5.4 TB/s of codes and scales; the
+// copy rate alone would be 39.5), x 1 head's 4 of 8 sequences up to 20,000 42.  Of these about 4.5 us pass before the
+// first block (plan, queries, code that is not in the instruction cache) and 4 in the joins.
+//
 // Tail: at most 63 tokens and the draft rows, bf16, straight from global memory; same fragments with
 // bf16 products, 16 tokens per warp, weights as two bf16 parts (16 bits).
 #pragma once
@@ -945,6 +949,8 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + 1), 1) attn_kernel(const __g
 // that passes its maximum by more than kRaise raises a flag that all four warps see behind that
 // barrier; then (rarely) they agree on new maxima and form the weights again.
 //
+// Measured: issue 0.32 to 0.37 per cycle, tensor pipe 16 % (12 queries) to 31 % (40); what limits it is the chain products,
+// exponentials, exchange, products of a block, which three teams in different blocks cover in part.
 // Three teams: at 65,531 tokens x 40 queries 61 us (two: 64), 32,785 x 12 24 (two: 26, four: 27).
 constexpr int kTeams = 3;
 // Registers: 16 warps have 128 a thread at launch.  The last four, of which one copies records and the others end,
