@@ -246,7 +246,8 @@ def test_one_token(fmt, dim, length):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
-@pytest.mark.parametrize("rows,group", [(1, 1), (2, 4), (3, 4), (3, 5), (4, 5), (5, 5), (7, 1), (8, 1), (8, 4), (8, 5), (8, 7), (8, 16)])
+@pytest.mark.parametrize("rows,group", [(1, 1), (2, 4), (3, 4), (3, 5), (4, 5), (5, 5), (7, 1), (8, 1), (8, 4), (8, 5), (8, 7), (8, 16),
+                                        (1, 41), (1, 128), (5, 25), (3, 27)])
 def test_rows_and_groups(fmt, rows, group):
     """Every number of query tiles, warps and groups."""
     c = Cache(fmt=fmt, heads=2)
