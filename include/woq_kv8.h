@@ -141,9 +141,9 @@ WOQ_API int woq_kv8_append_prompt(const woq_kv8_config* cfg, void* cache, size_t
 /* ---------------------------------------------------------------------------
  * Attention of `rows` rows of each of n sequences (the draft rows' queries).
  *   q, out: device bf16 [n][rows][q_heads][head_dim]; q_heads a multiple of kv_heads, query head
- *   i reads kv head i / (q_heads / kv_heads); rows * q_heads / kv_heads <= 128 (head_dim 256: 56);
- *   n * kv_heads * c * (ceil(max_tokens / 64) + 8) < 2^31 - 2^16, where c = 1 up to 40 rows *
- *   q_heads / kv_heads and for head_dim 256, else 2 to 4.
+ *   i reads kv head i / (q_heads / kv_heads); rows * q_heads / kv_heads <= 128;
+ *   n * kv_heads * c * (ceil(max_tokens / 64) + 8) < 2^31 - 2^16, where c is the number of
+ *   parts that rows * q_heads / kv_heads queries are worked on in (1 up to 40, else up to 4; head_dim 256: one for each 16).
  *   vis: device uint32 [n][rows], bit j: draft row j is seen (bits 0 .. 7); NULL: row m sees
  *   draft rows 0 .. m.  Only rows that were appended may be seen.
  *   A row sees, in this order, the sequence's tokens and the draft rows of its vis; with
@@ -172,7 +172,7 @@ WOQ_API int woq_kv8_attention(const woq_kv8_config* cfg, void* cache, size_t cac
 typedef struct {
   int ctas;         /* grid: one CTA per SM; those beyond the work end at once */
   int warps;        /* consumer warps of a CTA (one more copies) */
-  int query_groups; /* warps that read the same block: each for its own queries, or a team that shares it out */
+  int query_groups; /* warps that read the same block: 1, or a team of 4 that shares it out */
   int stages;       /* ring stages of one block each: a multiple of warps / query_groups */
   int least_units;  /* blocks (and tails) a CTA takes at least */
   int smem_bytes;   /* dynamic shared memory of a CTA */

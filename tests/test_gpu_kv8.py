@@ -258,7 +258,7 @@ def test_rows_and_groups(fmt, rows, group):
 
 
 @pytest.mark.parametrize("dim,rows,group", [(64, 8, 16), (64, 2, 7), (64, 6, 4), (64, 7, 4), (64, 8, 5), (256, 8, 7), (256, 3, 4),
-                                            (256, 5, 5)])
+                                            (256, 5, 5), (256, 8, 16), (256, 2, 4), (256, 1, 100), (256, 3, 3), (64, 1, 100)])
 def test_rows_and_groups_of_other_heads(dim, rows, group):
     c = Cache(fmt=rows % 2, dim=dim, heads=1)
     g = gen(rows * 31 + group)
@@ -322,6 +322,16 @@ def test_long_context_over_many_ctas(fmt, group, rows):
     c.prompt(0, g, 9000 - 3)
     c.draft([0], g, rows)
     c.attend([0], rows, group, g)
+
+
+@pytest.mark.parametrize("dim,rows,group", [(256, 1, 4), (256, 8, 4), (64, 8, 16)])
+def test_long_context_of_other_heads(dim, rows, group):
+    c = Cache(fmt=1, heads=2, dim=dim, max_tokens=9000, pages=150)
+    g = gen(3)
+    c.prompt(0, g, 9000 - 40)
+    c.draft([0], g, rows)
+    c.attend([0], rows, group, g)
+    c.attend([0], rows, group, g, window=3000, sinks=100)
 
 
 def test_one_workspace_for_every_shape():

@@ -129,7 +129,7 @@ def test_attention_arguments(woq):
                 dict(rows=8, hq=4 * 17), dict(scale=float("inf")), dict(scale=float("nan")), dict(window=-1), dict(sinks=-1),
                 dict(window=(1 << 30) + 1), dict(sinks=(1 << 30) + 1)):
         assert call(**bad) == S, bad
-    assert call(cfg=config(woq, head_dim=256), rows=8, hq=4 * 9) == S
+    assert call(cfg=config(woq, head_dim=256), rows=8, hq=4 * 17) == S
     assert call(n=0, q=None) == woq.WOQ_OK
     assert call(q=None) == N and call(out=None) == N and call(ws=None) == N
     assert call(q=P(FAKE + 2)) == A and call(out=P(FAKE + 8)) == A and call(ws=P(FAKE + 8)) == A and call(vis=P(FAKE + 1)) == A

@@ -103,15 +103,18 @@ int fill_append(const Kv8View& v, int layer, const void* qkv, int dtype, int row
   return WOQ_OK;
 }
 
-// Parts that rows * group queries are worked on in: up to 5 tiles of 8 each (head_dim 256: all at once).
-int attn_chunks(int dim, int queries) { return dim == 256 ? 1 : ((queries + 7) / 8 + 4) / 5; }
+constexpr int kMostQueries = 128;  // of one kv head
 
-int query_limit(int dim) { return dim == 256 ? 56 : 128; }  // one group of 8 queries per warp, 7 warps
+// Parts that rows * group queries are worked on in.
+int attn_chunks(int dim, int queries) {
+  const int most = kv8::team_tiles(dim);
+  return ((queries + 7) / 8 + most - 1) / most;
+}
 
 // What the attention takes of sequences, rows and heads (its unit counts fit 32 bits).
 bool attn_shape_ok(const Kv8View& v, int n, int rows, int q_heads) {
   return n >= 0 && n <= kKv8MaxSeqs && rows >= 1 && rows <= WOQ_KV8_ROWS && q_heads >= 1 && q_heads <= 4096 &&
-         q_heads % v.heads == 0 && rows * (q_heads / v.heads) <= query_limit(v.dim) &&
+         q_heads % v.heads == 0 && rows * (q_heads / v.heads) <= kMostQueries &&
          (long long)n * v.heads * attn_chunks(v.dim, rows * (q_heads / v.heads)) * (v.blocks + kv8::kTailUnits) <= 0x7FFF0000ll;
 }
 
@@ -124,20 +127,21 @@ size_t attn_parts_offset(const Kv8View& v, int n, int chunks, int sms) {
 
 }  // namespace
 
-// A team per block for more than 8 queries (head_dim 64 and 128), in chunks of at most 40; else a warp per block.
+// A team per block for more than 8 queries, in chunks of at most 40 (head_dim 256: 16), and for head_dim 256; else a warp per
+// block, and as many warps as leave each two stages of the ring at least.
 // 8 heads x 32,768 tokens, head_dim 128: 12 queries 24 us (a warp per block: 48), 24 33 (61), 40 38 (86); and in two
-// chunks of 24 or 32 queries, four of 32: 48 queries 51 us (89), 64 53 (116), 128 103 (220).
-// head_dim 256: a warp per block, one tile of queries each; with more than one, groups of warps read the same blocks.
-// Warps come in whole groups, as many as leave each warp two stages of the ring at least.
+// chunks of 24 or 32 queries, four of 32: 48 queries 51 us (89), 64 53 (116), 128 103 (220).  head_dim 256: 32 queries
+// 67 us (130), 4 35 (45).  Up to 8 queries of head_dim 128 the other way round: 131,072 tokens x 5 queries 57 us in
+// teams, 50 in warps, 1,000 tokens 11.5 and 10.4; head_dim 64, 65,536 x 7 29 and 26.
 //
-// The stages are a multiple of a group's warps.  Block b goes to warp b % per of each group and to stage
-// b % stages, so then a stage always serves the same warps.  Otherwise a warp could wait for
+// The stages are a multiple of the warps (the teams).  Block b goes to warp (team) b % per and to stage
+// b % stages, so then a stage always serves the same.  Otherwise a warp could wait for
 // block b while the copy of block b - stages, another warp's, is still under way (copies end in
 // any order): a wait on a barrier's parity two phases ahead returns at once.
 int kv8_attn_plan(Kv8Attn* p, int smem_max) {
   const int queries = p->rows * p->group, dim = p->v.dim;
   const int tiles = (queries + 7) / 8;
-  p->team = tiles > 1 && dim < 256;
+  p->team = tiles > 1 || dim == 256;
   p->chunks = attn_chunks(dim, queries);
   p->heads = p->v.heads * p->chunks;
   p->tiles = (tiles + p->chunks - 1) / p->chunks;
@@ -146,23 +150,21 @@ int kv8_attn_plan(Kv8Attn* p, int smem_max) {
   const int record = 128 * dim + 16;
   if (p->team) {
     p->query_groups = 4;  // the team's warps all read its blocks
-    p->warps = 4 * kv8::kTeams;
+    const int teams = kv8::teams_of(dim);
+    p->warps = 4 * teams;
     const int fixed = kv8::misc_bytes(p->n) + kv8::team_fixed_bytes(p->tiles, dim);
     int stages = (smem_max - fixed) / record;
-    stages = (stages < kv8::kMaxStages ? stages : kv8::kMaxStages) / kv8::kTeams * kv8::kTeams;
-    if (stages < 2 * kv8::kTeams) return 0;
+    stages = (stages < kv8::kMaxStages ? stages : kv8::kMaxStages) / teams * teams;
+    if (stages < 2 * teams) return 0;
     p->stages = stages;
     return fixed + stages * record;
   }
-  p->tiles = 1;
-  p->query_groups = tiles;
-  const int most = kv8::kMaxWarps;
-  for (int per = most / p->query_groups; per >= 1; --per) {
-    const int warps = per * p->query_groups;
+  p->query_groups = 1;
+  for (int warps = kv8::kMaxWarps; warps >= 1; --warps) {
     const int fixed = kv8::misc_bytes(p->n) + kv8::merge_bytes(warps, 1, dim);
     int stages = (smem_max - fixed) / record;
-    stages = (stages < kv8::kMaxStages ? stages : kv8::kMaxStages) / per * per;
-    if (stages < 2 * per) continue;
+    stages = (stages < kv8::kMaxStages ? stages : kv8::kMaxStages) / warps * warps;
+    if (stages < 2 * warps) continue;
     p->warps = warps;
     p->stages = stages;
     return fixed + stages * record;

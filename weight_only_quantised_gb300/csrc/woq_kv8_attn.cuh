@@ -18,8 +18,7 @@
 //
 // CTA: one producer warp copies whole records (16 KB at D = 128, one bulk copy each) into a ring; with up to 8
 // queries each consumer warp takes whole blocks by itself (always from the same stages, in order), with its own
-// running maximum and sums in registers, so the main loop has no barrier but the ring's.  With more (D = 256) the
-// warps form groups, each for its own 8 queries, that all read the block from shared memory.
+// running maximum and sums in registers, so the main loop has no barrier but the ring's.
 //
 // Block: scores transposed, S^T = K Q^T (tokens x queries), so that both codes operands are the
 // 16-row one and the 8-wide one is the queries: nothing is padded beyond 8 queries.  Codes
@@ -811,8 +810,7 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + 1), 1) attn_kernel(const __g
   extern __shared__ __align__(128) uint8_t smem[];
   Misc& misc = *reinterpret_cast<Misc*>(smem);
   const Kv8View& v = p.v;
-  const int W = p.warps, G = p.query_groups, WG = W / G, S = p.stages;
-  const int R = p.rows * p.group;
+  const int W = p.warps, S = p.stages, R = p.rows * p.group;
   constexpr int kRecord = 128 * D + 16;
   constexpr int kRow = D + kMergePad;
   float* merge = reinterpret_cast<float*>(smem + misc_bytes(p.n));  // [W][8][D + pad]
@@ -824,7 +822,7 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + 1), 1) attn_kernel(const __g
 #pragma unroll 1
     for (int i = 0; i < S; ++i) {
       dev::mbar_init(&misc.full[i], 1);
-      dev::mbar_init(&misc.empty[i], (uint32_t)G);
+      dev::mbar_init(&misc.empty[i], 1);
     }
     misc.fail = 0;
     dev::fence_mbar_init();
@@ -836,9 +834,7 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + 1), 1) attn_kernel(const __g
     return;
   }
 
-  const int group = warp % G, slot = warp / G;
-  const int g = lane >> 2, t = lane & 3;
-  const int consumers = W * 32;
+  const int g = lane >> 2, t = lane & 3, consumers = W * 32;
   int taken = 0;  // blocks of this CTA that earlier items had
 #pragma unroll 1
   for (int u = pl.begin; u < pl.end;) {
@@ -857,11 +853,10 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + 1), 1) attn_kernel(const __g
     Columns col;
     int low_max = 0;
     uint32_t any_vis = 0;
-    const int base = 8 * group, n = base + g;
-    const uint16_t* qrow = n < R ? p.q + query_at<D>(p, e, head, n) : nullptr;
+    const uint16_t* qrow = g < R ? p.q + query_at<D>(p, e, head, g) : nullptr;
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      const int k = base + 2 * t + c, m = k < R ? k / p.group : 0;
+      const int k = 2 * t + c, m = k < R ? k / p.group : 0;
       const uint32_t vis = (p.vis ? p.vis[(size_t)e * p.rows + m] : (2u << m) - 1u) & 0xFFu;
       col.vis[c] = vis;
       any_vis |= vis;
@@ -881,14 +876,14 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + 1), 1) attn_kernel(const __g
       const int in_tail = len - sp.full * kKv8Block;
       const int there = in_tail + 32 - __clz((int)__reduce_or_sync(~0u, any_vis));  // at most 63 + 8
 #pragma unroll 1
-      for (int i = slot; i < 5; i += WG)
+      for (int i = warp; i < 5; i += W)
         if (there > (i < 4 ? 4 * i : 64))
           tail_step<D>(st, tail, i, in_tail, len, there, qrow, p.scale_log2, col, p.sinks, lane);
     }
     bool ok = true;
-    int k = b0 + ((slot - taken) % WG + WG) % WG;  // ring positions taken + (k - b0) = slot mod WG (S a multiple of WG)
+    int k = b0 + ((warp - taken) % W + W) % W;  // ring positions taken + (k - b0) = warp mod W (S a multiple of W)
 #pragma unroll 1
-    for (; k < b1 && ok; k += WG) {
+    for (; k < b1 && ok; k += W) {
       const int at = taken + (k - b0), stage = at % S;
       ok = dev::mbar_wait_bounded(&misc.full[stage], (uint32_t)((at / S) & 1));
       if (!__all_sync(~0u, ok)) {
@@ -905,7 +900,7 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + 1), 1) attn_kernel(const __g
     if (!ok && lane == 0) misc.fail = 1;
     taken += b1 > b0 ? b1 - b0 : 0;
 
-    // join the warps: sums over the lanes of a column, then over the warps of the group
+    // join the warps: sums over the lanes of a column, then over the warps
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       float l = st.l[c];
@@ -928,14 +923,14 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + 1), 1) attn_kernel(const __g
       if (tid == 0) flag(v, WOQ_DEVERR_TIMEOUT);
       return;
     }
-    finish<D, false>(p, misc, pl, merge, W * 8 * kRow, warp_ml, WG, G * 8, e, head, ib, per, tid, consumers);
+    finish<D, false>(p, misc, pl, merge, W * 8 * kRow, warp_ml, W, 8, e, head, ib, per, tid, consumers);
     dev::named_barrier_sync(1, consumers);  // the merge buffer is free again
     u = stop;
   }
 }
 
 // ---------------------------------------------------------------------------------------------------
-// More than 8 queries: teams of four warps per block.
+// More than 8 queries, or head_dim 256: teams of four warps per block.
 //
 // With more tiles of queries, warps that each take a whole block would have to share out the
 // queries and every one of them would turn the block's codes into f16 again, and few warps of many
@@ -951,15 +946,20 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + 1), 1) attn_kernel(const __g
 //
 // Measured: issue 0.32 to 0.37 per cycle, tensor pipe 16 % (12 queries) to 31 % (40); what limits it is the chain products,
 // exponentials, exchange, products of a block, which three teams in different blocks cover in part.
-// Three teams: at 65,531 tokens x 40 queries 61 us (two: 64), 32,785 x 12 24 (two: 26, four: 27).
-constexpr int kTeams = 3;
-// Registers: 16 warps have 128 a thread at launch.  The last four, of which one copies records and the others end,
-// give up most of theirs to the teams (128 for all spill: two teams at 168 took 73 us, with 232 64).
-constexpr int kTeamThreads = 32 * (4 * kTeams + 4);
-constexpr int kLaunchRegisters = 128, kProducerRegisters = 40, kTeamRegisters = 152;
-static_assert(kTeamThreads * kLaunchRegisters <= 65536 &&
-                  128 * kProducerRegisters + 128 * kTeams * kTeamRegisters <= kTeamThreads * kLaunchRegisters,
-              "more registers than the launch has: the teams would wait for them for ever");
+// Three teams: at 65,531 tokens x 40 queries 61 us (two: 64), 32,785 x 12 24 (two: 26, four: 27).  With head_dim 256 two,
+// of two tiles: shared memory holds four records beside what they exchange.
+//
+// Registers: the warps have 128 (168) a thread at launch.  The last four, of which one copies records and the others
+// end, give up most of theirs to the teams (128 for all spill: two teams at 168 took 73 us, with 232 64).
+__host__ __device__ constexpr int teams_of(int dim) { return dim == 256 ? 2 : 3; }
+__host__ __device__ constexpr int team_tiles(int dim) { return dim == 256 ? 2 : 5; }  // most tiles of 8 queries
+template <int D>
+struct TeamShape {
+  static constexpr int kTeams = teams_of(D), kThreads = 32 * (4 * kTeams + 4);
+  static constexpr int kLaunch = kTeams == 2 ? 168 : 128, kCopying = 40, kTeam = kTeams == 2 ? 232 : 152;
+  static_assert(kThreads * kLaunch <= 65536 && 128 * kCopying + 128 * kTeams * kTeam <= kThreads * kLaunch,
+                "more registers than the launch has: the teams would wait for them for ever");
+};
 
 // Shared memory of one team: weights, twice (for two blocks in turn), column maxima of its warps, flags.
 template <int NT>
@@ -970,12 +970,13 @@ struct TeamShared {
 };
 
 __host__ __device__ constexpr int team_bytes(int nt) { return (2 * nt * 2 * 32 * 16 + 4 * 8 * nt * 4 + 8 + 127) / 128 * 128; }
-// Queries as operands in shared memory: [tile][16 elements each][lane][2], kept there from four tiles on.
-__host__ __device__ constexpr int query_bytes(int nt, int dim) { return nt >= 4 ? nt * (dim / 16) * 32 * 8 : 0; }
+// Queries as operands in shared memory: [tile][16 elements each][lane][2], kept there if they are many.
+__host__ __device__ constexpr bool shared_queries(int nt, int dim) { return nt >= 4 || dim == 256; }
+__host__ __device__ constexpr int query_bytes(int nt, int dim) { return shared_queries(nt, dim) ? nt * (dim / 16) * 32 * 8 : 0; }
 // All that is not the ring: the join's buffer, the teams', the queries, and what their rows see.
 __host__ __device__ constexpr int sight_bytes(int nt) { return (2 * 8 * nt * 4 + 127) / 128 * 128; }
 __host__ __device__ inline int team_fixed_bytes(int nt, int dim) {
-  return merge_bytes(kTeams, nt, dim) + kTeams * team_bytes(nt) + query_bytes(nt, dim) + sight_bytes(nt);
+  return merge_bytes(teams_of(dim), nt, dim) + teams_of(dim) * team_bytes(nt) + query_bytes(nt, dim) + sight_bytes(nt);
 }
 
 template <int D, int NT>
@@ -1262,10 +1263,11 @@ __device__ void team_tail(TeamState<D, NT>& st, TeamShared<NT>& ts, const uint16
 }
 
 template <int FMT, int D, int NT>
-__global__ void __launch_bounds__(kTeamThreads, 1) attn_team_kernel(const __grid_constant__ Kv8Attn p) {
+__global__ void __launch_bounds__(TeamShape<D>::kThreads, 1) attn_team_kernel(const __grid_constant__ Kv8Attn p) {
   extern __shared__ __align__(128) uint8_t smem[];
-  constexpr bool kShared = NT >= 4;  // queries in shared memory
-  constexpr int kRecord = 128 * D + 16, kRow = D + kMergePad, W = 4 * kTeams, kQueries = 8 * NT;
+  using Shape = TeamShape<D>;
+  constexpr bool kShared = shared_queries(NT, D);
+  constexpr int kTeams = Shape::kTeams, kRecord = 128 * D + 16, kRow = D + kMergePad, W = 4 * kTeams, kQueries = 8 * NT;
   Misc& misc = *reinterpret_cast<Misc*>(smem);
   float* merge = reinterpret_cast<float*>(smem + misc_bytes(p.n));  // [teams][8 NT][D + pad]
   float* team_ml = merge + kTeams * kQueries * kRow;                // [teams][8 NT][2]
@@ -1292,11 +1294,11 @@ __global__ void __launch_bounds__(kTeamThreads, 1) attn_team_kernel(const __grid
   Plan pl;
   if (!make_plan(p, misc, tid, pl)) return;
   if (warp >= W) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegisters));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Shape::kCopying));
     if (warp == W) produce<D>(p, misc, pl, ring, lane);
     return;
   }
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTeamRegisters));
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Shape::kTeam));
 
   int taken = 0;
 #pragma unroll 1
@@ -1438,7 +1440,7 @@ __global__ void __launch_bounds__(kTeamThreads, 1) attn_team_kernel(const __grid
   }
 }
 
-// The parts that attn_team_kernel left, joined: a warp per query, grid (items, queries / kJoinWarps).  With 12 to 40
+// The parts that attn_team_kernel left, joined: a warp per query (head_dim 256: two), grid (items, warps / kJoinWarps).  With 12 to 40
 // queries one CTA alone takes 5 to 13 us over an item's parts (up to 0.4 MB) while the others have ended.
 constexpr int kJoinWarps = 4;
 
@@ -1448,7 +1450,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
   uint32_t magic;
   if (!is_ours(p.v, &magic)) return;  // nothing was left
   const int e = (int)blockIdx.x / p.heads, head = (int)blockIdx.x % p.heads, base = head % p.chunks * p.queries;
-  const int Q = p.queries, lane = threadIdx.x & 31, n = (int)blockIdx.y * kJoinWarps + ((int)threadIdx.x >> 5);
+  constexpr int kParts = D > 128 ? D / 128 : 1;  // warps of one query
+  const int Q = p.queries, lane = threadIdx.x & 31, w = (int)blockIdx.y * kJoinWarps + ((int)threadIdx.x >> 5);
+  const int n = w / kParts, d0 = w % kParts * 128;
   const int2 where = p.joins[blockIdx.x];
   const int np = where.y;
   // (after a wait that ran out, flagged, a place may be one of an earlier launch: nothing outside the parts is read)
@@ -1458,9 +1462,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
   const size_t slot = (size_t)Q * (D + 4), step = 2 * slot;
   const float* parts = p.parts + (size_t)(where.x >> 1) * step;
   const size_t first = (where.x & 1) ? slot : 0;
-  constexpr int kLanes = D / 4;  // lanes that hold four elements each
+  constexpr int kLanes = D / kParts / 4;  // lanes that hold four elements each
   const float* at = parts + (size_t)Q * D + 2 * n;
-  const float* from = parts + (size_t)n * D + 4 * (lane % kLanes);
+  const float* from = parts + (size_t)n * D + d0 + 4 * (lane % kLanes);
   constexpr int kAhead = 20;
   float4 y[kAhead];
 #pragma unroll
@@ -1503,14 +1507,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  uint16_t* out = p.out + query_at<D>(p, e, head / p.chunks, base + n);
+  uint16_t* out = p.out + query_at<D>(p, e, head / p.chunks, base + n) + d0;
   if (lane < kLanes)
     *reinterpret_cast<uint2*>(out + 4 * lane) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
 }
 
 template <int D>
 cudaError_t launch_join(const Kv8Attn& p, cudaStream_t stream) {
-  const dim3 grid((unsigned)(p.n * p.heads), (unsigned)((p.queries + kJoinWarps - 1) / kJoinWarps));
+  const dim3 grid((unsigned)(p.n * p.heads), (unsigned)((p.queries * (D > 128 ? D / 128 : 1) + kJoinWarps - 1) / kJoinWarps));
   return launch(join_kernel<D>, grid, 32 * kJoinWarps, 0, stream, p);
 }
 
@@ -1543,27 +1547,32 @@ cudaError_t launch_attn_any(const Kv8Attn& p, int ctas, int smem, cudaStream_t s
   switch (p.v.dim) {
     case 64: return launch_attn<attn_kernel<FMT, 64>>(p, ctas, threads, smem, s);
     case 128: return launch_attn<attn_kernel<FMT, 128>>(p, ctas, threads, smem, s);
-    case 256: return launch_attn<attn_kernel<FMT, 256>>(p, ctas, threads, smem, s);
     default: return cudaErrorInvalidValue;
   }
 }
 
-template <int FMT, int D>
-cudaError_t launch_team_dim(const Kv8Attn& p, int ctas, int smem, cudaStream_t s) {
-  cudaError_t e = cudaErrorInvalidValue;
-  switch (p.tiles) {
-    case 2: e = launch_attn<attn_team_kernel<FMT, D, 2>, kLaunchRegisters>(p, ctas, kTeamThreads, smem, s); break;
-    case 3: e = launch_attn<attn_team_kernel<FMT, D, 3>, kLaunchRegisters>(p, ctas, kTeamThreads, smem, s); break;
-    case 4: e = launch_attn<attn_team_kernel<FMT, D, 4>, kLaunchRegisters>(p, ctas, kTeamThreads, smem, s); break;
-    case 5: e = launch_attn<attn_team_kernel<FMT, D, 5>, kLaunchRegisters>(p, ctas, kTeamThreads, smem, s); break;
-    default: break;
-  }
+template <int FMT, int D, int NT>
+cudaError_t launch_team(const Kv8Attn& p, int ctas, int smem, cudaStream_t s) {
+  using Shape = TeamShape<D>;
+  const cudaError_t e = launch_attn<attn_team_kernel<FMT, D, NT>, Shape::kLaunch>(p, ctas, Shape::kThreads, smem, s);
   return e != cudaSuccess || !p.joined ? e : launch_join<D>(p, s);
 }
 
 template <int FMT>
 cudaError_t launch_team_any(const Kv8Attn& p, int ctas, int smem, cudaStream_t s) {
-  return p.v.dim == 64 ? launch_team_dim<FMT, 64>(p, ctas, smem, s) : launch_team_dim<FMT, 128>(p, ctas, smem, s);
+  switch (p.v.dim * 8 + p.tiles) {
+    case 64 * 8 + 2: return launch_team<FMT, 64, 2>(p, ctas, smem, s);
+    case 64 * 8 + 3: return launch_team<FMT, 64, 3>(p, ctas, smem, s);
+    case 64 * 8 + 4: return launch_team<FMT, 64, 4>(p, ctas, smem, s);
+    case 64 * 8 + 5: return launch_team<FMT, 64, 5>(p, ctas, smem, s);
+    case 128 * 8 + 2: return launch_team<FMT, 128, 2>(p, ctas, smem, s);
+    case 128 * 8 + 3: return launch_team<FMT, 128, 3>(p, ctas, smem, s);
+    case 128 * 8 + 4: return launch_team<FMT, 128, 4>(p, ctas, smem, s);
+    case 128 * 8 + 5: return launch_team<FMT, 128, 5>(p, ctas, smem, s);
+    case 256 * 8 + 1: return launch_team<FMT, 256, 1>(p, ctas, smem, s);
+    case 256 * 8 + 2: return launch_team<FMT, 256, 2>(p, ctas, smem, s);
+    default: return cudaErrorInvalidValue;
+  }
 }
 
 }  // namespace kv8
