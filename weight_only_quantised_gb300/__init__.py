@@ -576,10 +576,13 @@ def woq_kv8_plan_attention(cfg: KV8Config, n: int, rows: int, q_heads: int, sms:
 # tensor): one pass over what has to hold, and _dptr's messages where something does not.
 _INT32, _BF16, _F32 = "int32", "bfloat16", "float32"
 _DTYPES = {}  # element type -> the torch dtypes that hold it (bound on first use)
+_bf16 = _i32 = None  # torch.bfloat16, torch.int32 (bound with them)
 
 
 def _dtypes(kind: str):
+    global _bf16, _i32
     import torch
+    _bf16, _i32 = torch.bfloat16, torch.int32
     _DTYPES.update({_INT32: (torch.int32, getattr(torch, "uint32", torch.int32)), _BF16: (torch.bfloat16,),
                     _F32: (torch.float32,), "qkv": {torch.bfloat16: 0, torch.float32: 1}})
     return _DTYPES[kind]
@@ -603,6 +606,19 @@ def _bytes(t, name: str):
     if device < 0 or device != _current_device() or not t.is_contiguous() or t.element_size() != 1:
         return _dptr(t, name, 1)
     return t.data_ptr()
+
+
+# The calls of a step are short, so theirs try each tensor in one expression and leave what fails it to _typed and
+# _bytes, which say what is wrong.
+
+def _shared_device(t) -> int:
+    """The current device if t is there, else one that no tensor is on."""
+    device = t.get_device()
+    return device if device >= 0 and device == _current_device() else -2
+
+
+def _is_bytes(t, on: int) -> bool:
+    return t is not None and t.get_device() == on and t.element_size() == 1 and t.is_contiguous()
 
 
 def _cache_args(cfg: KV8Config, cache):
@@ -639,10 +655,12 @@ def _qkv(cfg, qkv, q_heads, q_out, rope):
         stride = -(-width // 8) * 8  # one row: its stride says nothing
     if stride < need:
         raise ValueError(f"qkv: rows overlap (row stride {stride}, {need} elements a row)")
-    # the rows may be strided: the first alone is contiguous
-    ptr = _dptr(qkv if qkv.is_contiguous() else qkv[0], "qkv")
-    return (ptr, kind, stride, q_heads, None if rope is None else rope._ref(rows),
-            _typed(q_out, "q_out", _BF16, rows * q_heads * cfg.head_dim))
+    on = _shared_device(qkv)
+    ptr = qkv.data_ptr() if on >= 0 else _dptr(qkv[:1], "qkv")  # the rows may be strided
+    count = rows * q_heads * cfg.head_dim
+    q = (q_out.data_ptr() if q_out is not None and q_out.dtype is _bf16 and q_out.get_device() == on and q_out.is_contiguous()
+         and q_out.numel() >= count else _typed(q_out, "q_out", _BF16, count))
+    return ptr, kind, stride, q_heads, None if rope is None else rope._ref(rows), q
 
 
 def woq_kv8_append_rows(cfg: KV8Config, cache, layer: int, seqs, rows: int, qkv, q_heads: int, q_out, rope=None,
@@ -654,8 +672,14 @@ def woq_kv8_append_rows(cfg: KV8Config, cache, layer: int, seqs, rows: int, qkv,
     if n * rows != total:
         raise ValueError(f"qkv: {total} rows, the call needs {n} x {rows}")
     args = _qkv(cfg, qkv, q_heads, q_out, rope)
-    _check(lib.woq_kv8_append_rows(*_cache_args(cfg, cache), layer, _typed(seqs, "seqs", _INT32, n), n, rows, *args,
-                                   _stream(stream)), "woq_kv8_append_rows")
+    on = _shared_device(qkv)
+    c = cache.data_ptr() if _is_bytes(cache, on) else _bytes(cache, "cache")
+    e = (seqs.data_ptr() if seqs is not None and seqs.dtype is _i32 and seqs.get_device() == on and seqs.is_contiguous()
+         else _typed(seqs, "seqs", _INT32, n))
+    status = lib.woq_kv8_append_rows(ctypes.byref(cfg), c, _nbytes(cache), layer, e, n, rows, *args,
+                                     _current_raw_stream(on) if stream is None and on >= 0 else _stream(stream))
+    if status:
+        _raise(status, "woq_kv8_append_rows")
 
 
 def woq_kv8_append_prompt(cfg: KV8Config, cache, layer: int, seq: int, qkv, q_heads: int, q_out, rope=None,
@@ -683,15 +707,25 @@ def woq_kv8_attention(cfg: KV8Config, cache, layer: int, seqs, rows: int, q, q_h
                       window: int = 0, sinks: int = 0, vis=None, stream=None) -> None:
     """Attention of `rows` rows of each sequence of seqs (int32 [n]; None: as many as q has, from 0 on):
     q, out bf16 [n * rows, q_heads, head_dim]; vis int32 [n, rows], the draft rows each row sees (None: a chain)."""
-    per = max(1, rows * q_heads * cfg.head_dim)
+    per = rows * q_heads * cfg.head_dim
+    if per < 1:
+        per = 1
     total = q.numel()
     n = total // per if seqs is None else seqs.numel()
     if n * per != total:
         raise ValueError(f"q: {total} elements, the call needs {n} x {per}")
+    on = _shared_device(q)
+    c = cache.data_ptr() if _is_bytes(cache, on) else _bytes(cache, "cache")
+    w = ws.data_ptr() if _is_bytes(ws, on) else _bytes(ws, "ws")
+    a = q.data_ptr() if q.dtype is _bf16 and on >= 0 and q.is_contiguous() else _typed(q, "q", _BF16, total)
+    b = (out.data_ptr() if out is not None and out.dtype is _bf16 and out.get_device() == on and out.is_contiguous()
+         and out.numel() >= total else _typed(out, "out", _BF16, total))
+    e = (seqs.data_ptr() if seqs is not None and seqs.dtype is _i32 and seqs.get_device() == on and seqs.is_contiguous()
+         else _typed(seqs, "seqs", _INT32, n))
     status = lib.woq_kv8_attention(
-        ctypes.byref(cfg), _bytes(cache, "cache"), _nbytes(cache), layer, _typed(seqs, "seqs", _INT32, n), n, rows,
-        _typed(q, "q", _BF16, total), q_heads, _typed(vis, "vis", _INT32, n * rows), scale, window, sinks,
-        _typed(out, "out", _BF16, total), _bytes(ws, "ws"), _nbytes(ws), _stream(stream))
+        ctypes.byref(cfg), c, _nbytes(cache), layer, e, n, rows, a, q_heads,
+        None if vis is None else _typed(vis, "vis", _INT32, n * rows), scale, window, sinks, b, w, _nbytes(ws),
+        _current_raw_stream(on) if stream is None and on >= 0 else _stream(stream))
     if status:
         _raise(status, "woq_kv8_attention")
 
@@ -721,13 +755,19 @@ def woq_kv8_compact(cfg: KV8Config, cache, limit: int, stream=None) -> None:
 def woq_kv8_read(cfg: KV8Config, cache, layer: int, seq: int, first: int, k, v, stream=None) -> None:
     """Tokens first .. of a sequence back in bf16: k, v [count, kv_heads, head_dim], or with layer = -1
     [layers, count, kv_heads, head_dim]."""
-    layers = cfg.layers if layer < 0 else 1
-    per = layers * cfg.kv_heads * cfg.head_dim
-    count = k.numel() // max(per, 1)
-    if count * per != k.numel() or v.numel() != k.numel():
-        raise ValueError(f"k, v: {k.numel()} and {v.numel()} elements, expected the same multiple of {per}")
-    _check(lib.woq_kv8_read(*_cache_args(cfg, cache), layer, seq, first, count, _typed(k, "k", _BF16, -1), _typed(v, "v", _BF16, -1),
-                            _stream(stream)), "woq_kv8_read")
+    per = (cfg.layers if layer < 0 else 1) * cfg.kv_heads * cfg.head_dim
+    total = k.numel()
+    count = total // per if per > 0 else 0
+    if count * per != total or v.numel() != total:
+        raise ValueError(f"k, v: {total} and {v.numel()} elements, expected the same multiple of {per}")
+    on = _shared_device(k)
+    c = cache.data_ptr() if _is_bytes(cache, on) else _bytes(cache, "cache")
+    a = k.data_ptr() if k.dtype is _bf16 and on >= 0 and k.is_contiguous() else _typed(k, "k", _BF16, -1)
+    b = (v.data_ptr() if v.dtype is _bf16 and v.get_device() == on and v.is_contiguous() else _typed(v, "v", _BF16, -1))
+    status = lib.woq_kv8_read(ctypes.byref(cfg), c, _nbytes(cache), layer, seq, first, count, a, b,
+                              _current_raw_stream(on) if stream is None and on >= 0 else _stream(stream))
+    if status:
+        _raise(status, "woq_kv8_read")
 
 
 def woq_kv8_state(cfg: KV8Config, cache, lens=None, refs=None, table=None, stream=None) -> None:
