@@ -970,8 +970,9 @@ struct TeamShared {
 };
 
 __host__ __device__ constexpr int team_bytes(int nt) { return (2 * nt * 2 * 32 * 16 + 4 * 8 * nt * 4 + 8 + 127) / 128 * 128; }
-// Queries as operands in shared memory: [tile][16 elements each][lane][2], kept there if they are many.
-__host__ __device__ constexpr bool shared_queries(int nt, int dim) { return nt >= 4 || dim == 256; }
+// Queries as operands in shared memory: [tile][16 elements each][lane][2], kept there from three tiles on (24 queries,
+// 32,768 tokens: 29 us, in registers, which then spill, 33; with two tiles 24 in registers, 25 in shared memory).
+__host__ __device__ constexpr bool shared_queries(int nt, int dim) { return nt >= 3 || dim == 256; }
 __host__ __device__ constexpr int query_bytes(int nt, int dim) { return shared_queries(nt, dim) ? nt * (dim / 16) * 32 * 8 : 0; }
 // All that is not the ring: the join's buffer, the teams', the queries, and what their rows see.
 __host__ __device__ constexpr int sight_bytes(int nt) { return (2 * 8 * nt * 4 + 127) / 128 * 128; }
@@ -1123,41 +1124,34 @@ __device__ __forceinline__ void team_block(TeamState<D, NT>& st, TeamShared<NT>&
     st.l[q][1] += l[q][1];
   }
   const uint8_t* vc = rec + 64 * D + t * 128 + g * 16 + wi * (D / 64) * 1024;
-  uint4 vx[D / 64], vy[D / 64];
-  float acc[D / 64][NT][4];
+  // one strip of 16 elements after the other: the weights are read once for each, but the sums of one are all that is held
 #pragma unroll
   for (int j = 0; j < D / 64; ++j) {
-    vx[j] = *reinterpret_cast<const uint4*>(vc + 2 * j * 512);
-    vy[j] = *reinterpret_cast<const uint4*>(vc + (2 * j + 1) * 512);
+    const uint4 x = *reinterpret_cast<const uint4*>(vc + 2 * j * 512), y = *reinterpret_cast<const uint4*>(vc + (2 * j + 1) * 512);
+    float acc[NT][4];
 #pragma unroll
     for (int q = 0; q < NT; ++q)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) acc[j][q][c] = 0.0f;
-  }
+      for (int c = 0; c < 4; ++c) acc[q][c] = 0.0f;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint4 pb[NT];
+    for (int h = 0; h < 2; ++h) {
+      uint32_t a0[4], a1[4];
+      f16x4_of_codes<FMT>(h ? x.z : x.x, a0[0], a0[2]);
+      f16x4_of_codes<FMT>(h ? y.z : y.x, a0[1], a0[3]);
+      f16x4_of_codes<FMT>(h ? x.w : x.y, a1[0], a1[2]);
+      f16x4_of_codes<FMT>(h ? y.w : y.y, a1[1], a1[3]);
 #pragma unroll
-    for (int q = 0; q < NT; ++q) pb[q] = ts.weights[buf][q][h][lane];
-#pragma unroll
-    for (int j = 0; j < D / 64; ++j) {
-      uint32_t a[4];
-      f16x4_of_codes<FMT>(h ? vx[j].z : vx[j].x, a[0], a[2]);
-      f16x4_of_codes<FMT>(h ? vy[j].z : vy[j].x, a[1], a[3]);
-#pragma unroll
-      for (int q = 0; q < NT; ++q) mma_f16(acc[j][q], a, pb[q].x, pb[q].y);
-      f16x4_of_codes<FMT>(h ? vx[j].w : vx[j].y, a[0], a[2]);
-      f16x4_of_codes<FMT>(h ? vy[j].w : vy[j].y, a[1], a[3]);
-#pragma unroll
-      for (int q = 0; q < NT; ++q) mma_f16(acc[j][q], a, pb[q].z, pb[q].w);
+      for (int q = 0; q < NT; ++q) {
+        const uint4 pb = ts.weights[buf][q][h][lane];
+        mma_f16(acc[q], a0, pb.x, pb.y);
+        mma_f16(acc[q], a1, pb.z, pb.w);
+      }
     }
-  }
-#pragma unroll
-  for (int j = 0; j < D / 64; ++j)
 #pragma unroll
     for (int q = 0; q < NT; ++q)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) st.o[j][q][c] = fmaf(vs, acc[j][q][c], st.o[j][q][c]);
+      for (int c = 0; c < 4; ++c) st.o[j][q][c] = fmaf(vs, acc[q][c], st.o[j][q][c]);
+  }
 }
 
 // The tail, or (over = true) its rows 64 .. 71: as team_block, from bf16 in global memory; weights as two
