@@ -278,6 +278,20 @@ def test_draft_trees(widths, length):
     c.attend([0], 8, 4, g, vis=[M.tree_masks(widths)])
 
 
+@pytest.mark.parametrize("dim,group", [(128, 12), (64, 16), (256, 6)])
+def test_draft_trees_and_windows_in_chunks(dim, group):
+    """More queries than are worked on at once: each chunk has its own rows, masks and windows, and rows of two chunks meet in one row."""
+    c = Cache(fmt=1, heads=2, dim=dim, seqs=3)
+    g = gen(dim)
+    for s, n in enumerate((500, 0, 127)):
+        c.prompt(s, g, n)
+    c.draft([0, 1, 2], g, 8)
+    tree = M.tree_masks((3, 2, 1, 1))
+    c.attend([2, 0, 1], 8, group, g, vis=[tree, [0] + tree[1:], tree])
+    c.attend([2, 0, 1], 8, group, g, vis=[tree] * 3, window=70, sinks=3)
+    c.attend([0, 1], 7, group, g, window=1)
+
+
 def test_rows_that_see_nothing_and_old_drafts():
     c = Cache(heads=2)
     g = gen(0)

@@ -129,8 +129,8 @@ size_t attn_parts_offset(const Kv8View& v, int n, int chunks, int sms) {
 
 // A team per block for more than 8 queries, in chunks of at most 40 (head_dim 256: 16), and for head_dim 256; else a warp per
 // block, and as many warps as leave each two stages of the ring at least.
-// 8 heads x 32,768 tokens, head_dim 128: 12 queries 24 us (a warp per block: 48), 24 33 (61), 40 38 (86); and in two
-// chunks of 24 or 32 queries, four of 32: 48 queries 51 us (89), 64 53 (116), 128 103 (220).  head_dim 256: 32 queries
+// 8 heads x 32,768 tokens, head_dim 128: 12 queries 24 us (a warp per block: 48), 24 29 (61), 40 36 (86); and in two
+// chunks of 24 or 32 queries, four of 32: 48 queries 45 us (89), 64 53 (116), 128 103 (220).  head_dim 256: 32 queries
 // 67 us (130), 4 35 (45).  Up to 8 queries of head_dim 128 the other way round: 131,072 tokens x 5 queries 57 us in
 // teams, 50 in warps, 1,000 tokens 11.5 and 10.4; head_dim 64, 65,536 x 7 29 and 26.
 //

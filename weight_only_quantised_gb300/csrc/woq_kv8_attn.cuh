@@ -944,9 +944,9 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + 1), 1) attn_kernel(const __g
 // that passes its maximum by more than kRaise raises a flag that all four warps see behind that
 // barrier; then (rarely) they agree on new maxima and form the weights again.
 //
-// Measured: issue 0.32 to 0.37 per cycle, tensor pipe 16 % (12 queries) to 31 % (40); what limits it is the chain products,
+// Measured: issue 0.32 to 0.37 per cycle, tensor pipe 17 % (12 queries) to 32 % (40); what limits it is the chain products,
 // exponentials, exchange, products of a block, which three teams in different blocks cover in part.
-// Three teams: at 65,531 tokens x 40 queries 61 us (two: 64), 32,785 x 12 24 (two: 26, four: 27).  With head_dim 256 two,
+// Three teams: at 65,531 tokens x 40 queries 57 us (61 when two took 64), 32,785 x 12 24 (two: 26, four: 25 to 27).  With head_dim 256 two,
 // of two tiles: shared memory holds four records beside what they exchange.
 //
 // Registers: the warps have 128 (168) a thread at launch.  The last four, of which one copies records and the others
