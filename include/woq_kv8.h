@@ -143,7 +143,8 @@ WOQ_API int woq_kv8_append_prompt(const woq_kv8_config* cfg, void* cache, size_t
  *   q, out: device bf16 [n][rows][q_heads][head_dim]; q_heads a multiple of kv_heads, query head
  *   i reads kv head i / (q_heads / kv_heads); rows * q_heads / kv_heads <= 128;
  *   n * kv_heads * c * (ceil(max_tokens / 64) + 8) < 2^31 - 2^16, where c is the number of
- *   parts that rows * q_heads / kv_heads queries are worked on in (1 up to 40, else up to 4; head_dim 256: one for each 16).
+ *   parts that rows * q_heads / kv_heads queries are worked on in (1 up to 40, else up to 4;
+ *   head_dim 256: one for each 16).
  *   vis: device uint32 [n][rows], bit j: draft row j is seen (bits 0 .. 7); NULL: row m sees
  *   draft rows 0 .. m.  Only rows that were appended may be seen.
  *   A row sees, in this order, the sequence's tokens and the draft rows of its vis; with
@@ -217,8 +218,8 @@ WOQ_API size_t woq_kv8_page_offset(const woq_kv8_config* cfg, int page);
 
 /* Tokens first .. first + count - 1 of a sequence, back in bf16 (code * s rounded to fp32 and then
  * to bf16, or as held in the tail; of a token that was not finite the value is 0 and the key NaN,
- * and so are the other keys of its block and head once the block is full): k, v device bf16 [layers read][count][kv_heads][head_dim], 16-byte aligned.
- * layer -1: all layers.  Places up to 7 behind the sequence's end are its draft rows; if
+ * and so are the other keys of its block and head once the block is full): k, v device bf16
+ * [layers read][count][kv_heads][head_dim], 16-byte aligned.  layer -1: all layers.  Places up to 7 behind the sequence's end are its draft rows; if
  * first + count goes beyond them nothing is written (WOQ_DEVERR_STATE). */
 WOQ_API int woq_kv8_read(const woq_kv8_config* cfg, void* cache, size_t cache_bytes, int layer, int seq, int first,
                          int count, void* k, void* v, woq_stream_t stream);

@@ -944,10 +944,10 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + 1), 1) attn_kernel(const __g
 // that passes its maximum by more than kRaise raises a flag that all four warps see behind that
 // barrier; then (rarely) they agree on new maxima and form the weights again.
 //
-// Measured: issue 0.32 to 0.37 per cycle, tensor pipe 17 % (12 queries) to 32 % (40); what limits it is the chain products,
-// exponentials, exchange, products of a block, which three teams in different blocks cover in part.
-// Three teams: at 65,531 tokens x 40 queries 57 us (61 when two took 64), 32,785 x 12 24 (two: 26, four: 25 to 27).  With head_dim 256 two,
-// of two tiles: shared memory holds four records beside what they exchange.
+// Measured: issue 0.32 to 0.38 per cycle, tensor pipe 17 % (12 queries) to 32 % (40); what limits it is the chain
+// products, exponentials, exchange, products of a block, which three teams in different blocks cover in part.
+// Three teams: at 65,531 tokens x 40 queries 57 us (61 when two took 64), 32,785 x 12 24 (two: 26, four: 25 to
+// 27).  With head_dim 256 two, of two tiles: shared memory holds four records beside what they exchange.
 //
 // Registers: the warps have 128 (168) a thread at launch.  The last four, of which one copies records and the others
 // end, give up most of theirs to the teams (128 for all spill: two teams at 168 took 73 us, with 232 64).
@@ -1434,8 +1434,9 @@ __global__ void __launch_bounds__(TeamShape<D>::kThreads, 1) attn_team_kernel(co
   }
 }
 
-// The parts that attn_team_kernel left, joined: a warp per query (head_dim 256: two), grid (items, warps / kJoinWarps).  With 12 to 40
-// queries one CTA alone takes 5 to 13 us over an item's parts (up to 0.4 MB) while the others have ended.
+// The parts that attn_team_kernel left, joined: a warp per query (head_dim 256: two), grid (items, warps /
+// kJoinWarps).  With 12 to 40 queries one CTA alone takes 5 to 13 us over an item's parts (up to 0.4 MB) while
+// the others have ended.
 constexpr int kJoinWarps = 4;
 
 template <int D>

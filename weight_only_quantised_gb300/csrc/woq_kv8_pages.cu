@@ -5,7 +5,8 @@
 // (so page numbers do not depend on the run), and either changes everything or nothing.  What
 // it decided is left in the cache (moves, pairs) for the copying kernels, which are plain
 // streams bound by HBM: 16-byte vectors, four in flight per thread, one 16 KB segment of a page
-// at a time over all SMs (with the bookkeeping, 0.8 of the measured copy rate over a whole copy and compaction).  Launch order on the stream is the only synchronisation.
+// at a time over all SMs (with the bookkeeping, 0.8 of the measured copy rate over a whole copy
+// and compaction).  Launch order on the stream is the only synchronisation.
 #include "woq_internal.h"
 #include "woq_kv8_device.cuh"
 
