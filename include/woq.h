@@ -350,12 +350,15 @@ typedef struct {
 WOQ_API int woq_plan_launch(int bits, int M, int N, int K, int entry, int sms, int smem_max, woq_launch_plan* out);
 
 /* Tests of the bounded waits (the pages describe no failure handling; every wait of a woq
- * kernel on another CTA is bounded so that a stuck CTA never hangs a shared GPU).  Injects one fault into the following launches of this
+ * kernel on another CTA or on a copy is bounded so that a stuck CTA never hangs a shared GPU).  Injects one fault into the following launches of this
  * process, made by CTA `cta` (a block index), and bounds the waits it makes run out by
  * wait_limit_us microseconds (0 = the default, 2 s):
  *   kind 1: GEMV / linear launches - that CTA never publishes its split-tile partial
  *           sums; the combiner of such a tile gives up, sets WOQ_DEVERR_TIMEOUT and
  *           leaves that tile's rows of y untouched;
+ *           woq_kv8_attention - that CTA copies none of its blocks; its waits for them run
+ *           out, it sets WOQ_DEVERR_TIMEOUT in the cache's status, and the rows of out that
+ *           it had a part in keep what they held;
  *   kind 2: SwiGLU linears - that CTA (one of the first half of the grid, the CTAs that
  *           form the row maxima) never counts itself in; every CTA gives up, sets
  *           WOQ_DEVERR_TIMEOUT and leaves y untouched;

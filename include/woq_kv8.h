@@ -156,7 +156,8 @@ WOQ_API int woq_kv8_append_prompt(const woq_kv8_config* cfg, void* cache, size_t
  *   ws: device, 16-byte aligned, woq_kv8_attention_workspace(...) bytes, zero-filled once before
  *   first use (woq_workspace_init); each launch leaves zero what has to be, so launches of
  *   different shapes may use one that is large enough.  Not shared by launches that can overlap.
- *   A wait that runs out sets WOQ_DEVERR_TIMEOUT: what was then being worked on has no result (zero-fill ws).
+ *   A wait that runs out sets WOQ_DEVERR_TIMEOUT: rows of out whose result is not complete keep what they held, and ws
+ *   has to be zero-filled before it is used again.
  * The result does not depend on the run (fixed order of summation).  Launched with
  * programmatic dependent launch.
  * --------------------------------------------------------------------------- */

@@ -31,16 +31,11 @@ std::atomic<int> g_override_stages{0};
 std::atomic<int> g_override_prefetch_kb{-1};
 std::atomic<int> g_override_path{0};  // 0: table, else 1 + kern::Consumer
 std::atomic<int> g_launch_counter{0};  // numbers GEMV launches (trace builds key their stamps by it)
-// woq_tune_fault: a fault to inject (0 none, 1 split-tile publish, 2 SwiGLU arrival, 3 relayout
+// woq_tune_fault: a fault to inject (0 none, 1 split-tile publish or records of the cache, 2 SwiGLU arrival, 3 relayout
 // barrier arrival) by one CTA, and the bound of the waits it makes run out (0 = the default)
 std::atomic<int> g_fault_kind{0};
 std::atomic<int> g_fault_cta{0};
 std::atomic<long long> g_wait_ns{0};
-uint64_t wait_bound_ns() {
-  const long long v = g_wait_ns.load(std::memory_order_relaxed);
-  return v > 0 ? (uint64_t)v : dev::kWaitLimitNs;
-}
-
 int current_device() {
   int d = 0;
   if (const cudaError_t e = cudaGetDevice(&d); e != cudaSuccess) {
@@ -54,6 +49,14 @@ inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintp
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 }  // namespace
+
+uint64_t wait_bound_ns() {
+  const long long v = g_wait_ns.load(std::memory_order_relaxed);
+  return v > 0 ? (uint64_t)v : dev::kWaitLimitNs;
+}
+int fault_cta(int kind) {
+  return g_fault_kind.load(std::memory_order_relaxed) == kind ? g_fault_cta.load(std::memory_order_relaxed) : -1;
+}
 
 int sm_count() {
   const int d = current_device();
@@ -336,8 +339,7 @@ int woq_relayout_inplace(int bits, void* buf, size_t buf_bytes, int N, int K, wo
     return cuda_result(e);
   }
   int too_large = 0;
-  const int fault_cta = g_fault_kind.load(std::memory_order_relaxed) == 3 ? g_fault_cta.load(std::memory_order_relaxed) : -1;
-  cudaError_t e = launch_relayout(bits, buf, N, K, &too_large, (cudaStream_t)stream, wait_bound_ns(), fault_cta);
+  cudaError_t e = launch_relayout(bits, buf, N, K, &too_large, (cudaStream_t)stream, wait_bound_ns(), fault_cta(3));
   if (too_large) return WOQ_ERR_SHAPE;
   if (e == cudaSuccess) e = cudaStreamSynchronize((cudaStream_t)stream);
   uint32_t head[4] = {0u, 0u, 0u, 0u};

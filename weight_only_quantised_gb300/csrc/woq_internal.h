@@ -35,6 +35,8 @@ constexpr int kMaxStages = 8;
 // WOQ_OK or WOQ_ERR_CUDA; a failure is kept for woq_last_cuda_error (per thread) and cleared from
 // the runtime's error state
 int cuda_result(cudaError_t e);
+uint64_t wait_bound_ns();             // of device waits (woq_tune_fault; 2 s otherwise)
+int fault_cta(int kind);              // the CTA that makes this kind of fault (woq_tune_fault), -1: none
 int sm_count();                       // SMs of the current device (cached per device)
 int max_dynamic_smem();               // opt-in shared memory per block of the current device
 int choose_consumer(int bits, int M);  // kern::Consumer the launch table picks for (bits, M)

@@ -118,8 +118,8 @@ bool attn_shape_ok(const Kv8View& v, int n, int rows, int q_heads) {
          (long long)n * v.heads * attn_chunks(v.dim, rows * (q_heads / v.heads)) * (v.blocks + kv8::kTailUnits) <= 0x7FFF0000ll;
 }
 
-// Workspace of the attention: [256 B][tickets][where parts are][parts].  What has to be zero at the beginning of a launch,
-// the tickets, lies in the same place for every shape, so launches of different shapes may share a workspace.
+// Workspace of the attention: [256 B: word 1 says that a wait ran out][tickets][where parts are][parts].  What has to be zero at the
+// beginning of a launch, that word and the tickets, lies in the same place for every shape, so launches of different shapes may share a workspace.
 size_t attn_joins_offset(int sms) { return 256 + ((size_t)sms * 4 + 255) / 256 * 256; }
 size_t attn_parts_offset(const Kv8View& v, int n, int chunks, int sms) {
   return attn_joins_offset(sms) + ((size_t)n * v.heads * chunks * 8 + 255) / 256 * 256;
@@ -305,6 +305,7 @@ int woq_kv8_attention(const woq_kv8_config* cfg, void* cache, size_t cache_bytes
   p.q = static_cast<const uint16_t*>(q);
   p.vis = vis;
   p.out = static_cast<uint16_t*>(out);
+  p.failed = reinterpret_cast<uint32_t*>(ws) + 1;
   p.tickets = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + 256);
   p.joins = reinterpret_cast<int2*>(static_cast<uint8_t*>(ws) + attn_joins_offset(sms));
   p.scale_log2 = (float)((double)scale * 1.4426950408889634);
@@ -316,6 +317,8 @@ int woq_kv8_attention(const woq_kv8_config* cfg, void* cache, size_t cache_bytes
   p.window = window;
   p.sinks = sinks;
   p.ctas = sms;
+  p.fault_cta = fault_cta(1);
+  p.wait_ns = wait_bound_ns();
   const int smem = kv8_attn_plan(&p, smem_max);
   if (smem == 0) return WOQ_ERR_SHAPE;
   p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + attn_parts_offset(v, n, p.chunks, sms));

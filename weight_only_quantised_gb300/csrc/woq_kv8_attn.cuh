@@ -610,6 +610,7 @@ __device__ __forceinline__ void produce(const Kv8Attn& p, Misc& misc, const Plan
   const Kv8View& v = p.v;
   const int S = p.stages;
   int issued = 0;
+  if ((int)blockIdx.x == p.fault_cta) return;  // injected fault: the consumers' waits run out
 #pragma unroll 1
   for (int u = pl.begin; u < pl.end;) {
     int e, head, ib;
@@ -632,7 +633,7 @@ __device__ __forceinline__ void produce(const Kv8Attn& p, Misc& misc, const Plan
           const int pg = __shfl_sync(~0u, page, i);
           const int stage = issued % S;
           bool ok = true;
-          if (issued >= S) ok = dev::mbar_wait_bounded(&misc.empty[stage], (uint32_t)((issued / S - 1) & 1));
+          if (issued >= S) ok = dev::mbar_wait_bounded(&misc.empty[stage], (uint32_t)((issued / S - 1) & 1), p.wait_ns);
           if (!__all_sync(~0u, ok)) {
             // the consumers stopped (they report it): nothing more is issued; copies in flight are waited for below
               u = pl.end;
@@ -805,6 +806,12 @@ __device__ __forceinline__ void finish(const Kv8Attn& p, Misc& misc, const Plan&
   }
 }
 
+// A wait of this CTA ran out: its item, and those behind it, are not written.  One thread.
+__device__ __forceinline__ void report_wait(const Kv8Attn& p) {
+  flag(p.v, WOQ_DEVERR_TIMEOUT);
+  atomicOr(p.failed, 1u);
+}
+
 template <int FMT, int D>
 __global__ void __launch_bounds__(32 * (kMaxWarps + 1), 1) attn_kernel(const __grid_constant__ Kv8Attn p) {
   extern __shared__ __align__(128) uint8_t smem[];
@@ -885,7 +892,7 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + 1), 1) attn_kernel(const __g
 #pragma unroll 1
     for (; k < b1 && ok; k += W) {
       const int at = taken + (k - b0), stage = at % S;
-      ok = dev::mbar_wait_bounded(&misc.full[stage], (uint32_t)((at / S) & 1));
+      ok = dev::mbar_wait_bounded(&misc.full[stage], (uint32_t)((at / S) & 1), p.wait_ns);
       if (!__all_sync(~0u, ok)) {
         ok = false;
         break;
@@ -919,8 +926,8 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + 1), 1) attn_kernel(const __g
       for (int c = 0; c < 4; ++c)
         merge[(size_t)(warp * 8 + 2 * t + (c & 1)) * kRow + 16 * j + g + 8 * (c >> 1)] = st.o[j][c];
     dev::named_barrier_sync(1, consumers);
-    if (misc.fail) {  // a wait ran out: nothing of this item is written
-      if (tid == 0) flag(v, WOQ_DEVERR_TIMEOUT);
+    if (misc.fail) {
+      if (tid == 0) report_wait(p);
       return;
     }
     finish<D, false>(p, misc, pl, merge, W * 8 * kRow, warp_ml, W, 8, e, head, ib, per, tid, consumers);
@@ -1380,8 +1387,8 @@ __global__ void __launch_bounds__(TeamShape<D>::kThreads, 1) attn_team_kernel(co
     for (int buf = 0; k < b1; k += kTeams, buf ^= 1) {
       const int at = taken + (k - b0), stage = at % S;
       // after a wait that ran out the warp goes on without waits (the team's barriers need it) but releases no stage,
-      // so that the producer stops too; nothing of the item is written
-      if (ok) ok = __all_sync(~0u, dev::mbar_wait_bounded(&misc.full[stage], (uint32_t)((at / S) & 1)));
+      // so that the producer stops too; what it sums is not used
+      if (ok) ok = __all_sync(~0u, dev::mbar_wait_bounded(&misc.full[stage], (uint32_t)((at / S) & 1), p.wait_ns));
       const int blk = k < sp.head_blocks ? k : sp.from + (k - sp.head_blocks);
       const int token0 = blk * kKv8Block;
       team_block<FMT, D, NT>(st, ts, ring + (size_t)stage * kRecord, queries, coef, low, token0,
@@ -1424,8 +1431,8 @@ __global__ void __launch_bounds__(TeamShape<D>::kThreads, 1) attn_team_kernel(co
           }
     }
     dev::named_barrier_sync(1, W * 32);
-    if (misc.fail) {  // a wait ran out: nothing of this item is written
-      if (tid == 0) flag(v, WOQ_DEVERR_TIMEOUT);
+    if (misc.fail) {
+      if (tid == 0) report_wait(p);
       return;
     }
     finish<D, true>(p, misc, pl, merge, kTeams * kQueries * kRow, team_ml, kTeams, kQueries, e, head, ib, per, tid, W * 32);
@@ -1444,13 +1451,19 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
   begin_after_prior();
   uint32_t magic;
   if (!is_ours(p.v, &magic)) return;  // nothing was left
+  // After a wait that ran out some CTA left no parts, or no place of them: what is there may be an earlier launch's, of this
+  // item or of another.  So nothing is joined, in this launch or (it is reported again) before the workspace is zero-filled.
+  if (dev::ld_relaxed_u32(p.failed) != 0) {
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) flag(p.v, WOQ_DEVERR_TIMEOUT);
+    return;
+  }
   const int e = (int)blockIdx.x / p.heads, head = (int)blockIdx.x % p.heads, base = head % p.chunks * p.queries;
   constexpr int kParts = D > 128 ? D / 128 : 1;  // warps of one query
   const int Q = p.queries, lane = threadIdx.x & 31, w = (int)blockIdx.y * kJoinWarps + ((int)threadIdx.x >> 5);
   const int n = w / kParts, d0 = w % kParts * 128;
   const int2 where = p.joins[blockIdx.x];
   const int np = where.y;
-  // (after a wait that ran out, flagged, a place may be one of an earlier launch: nothing outside the parts is read)
+  // (whatever wrote to the workspace: nothing outside the parts is read)
   if (where.x < 0 || np > p.ctas - (where.x >> 1)) return;
   if (np <= 1 || n >= min(Q, p.rows * p.group - base)) return;
   // the first part's slot, and the first slots of the CTAs that follow

@@ -102,6 +102,7 @@ struct Kv8Attn {
   const uint32_t* vis;
   uint16_t* out;
   uint32_t* tickets;  // one word per CTA, that an item begins in and does not end in: zero between launches
+  uint32_t* failed;   // not zero: a wait of a launch with this workspace ran out since it was zero-filled
   int2* joins;        // of each item: twice the first CTA with a part (+ 1: its second slot), number of parts
   float* parts;       // two parts per CTA of queries * (dim + 4) floats
   float scale_log2;
@@ -113,6 +114,8 @@ struct Kv8Attn {
   int tiles;         // tiles of 8 queries of a team (a warp has one)
   int warps, query_groups, stages, ctas;
   int least_units;   // units a CTA takes at least (while there are more CTAs than that needs, they idle)
+  int fault_cta;     // tests of the waits' bound: this CTA copies no records (-1: none)
+  uint64_t wait_ns;  // bound of the waits in the ring
 };
 
 cudaError_t launch_kv8_init(const Kv8View& v, cudaStream_t s);
