@@ -151,7 +151,8 @@ WOQ_API int woq_kv8_append_prompt(const woq_kv8_config* cfg, void* cache, size_t
  *   window > 0 only the first `sinks` and the last `window` of them (window 0: all, sinks not
  *   used; window, sinks <= 2^30).  out = sum_j softmax_j(scale q . k_j) v_j over what it sees, in fp32 with 8-bit codes
  *   taken exactly (weights in f16, 11 significant bits), rounded to bf16; a row that sees
- *   nothing gives 0.  scale finite; q finite, scores below 2^100 in magnitude.
+ *   nothing gives 0.  scale finite; q finite; sums of |q_i k_i| and
+ *   scale times them below 2^100, sums of |v| over the tokens seen below 2^127.
  *   seqs: as above, but entries may repeat; one out of range gives 0 and WOQ_DEVERR_STATE.
  *   ws: device, 16-byte aligned, woq_kv8_attention_workspace(...) bytes, zero-filled once before
  *   first use (woq_workspace_init); each launch leaves zero what has to be, so launches of

@@ -1,0 +1,44 @@
+"""The 8-bit key/value cache where it is easily wrong: values near the ends of bf16's range, plans of many entries
+and plans that are made again, refused calls, another config's cache."""
+import pytest
+import torch
+
+from tests import kv8_model as M
+from tests import test_gpu_kv8 as base
+from tests.test_gpu_kv8 import DEV, FMTS, Cache, gen, ints, kv
+
+pytestmark = pytest.mark.gpu
+
+woq = None
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    global woq
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    import weight_only_quantised_gb300 as w
+    woq = base.woq = w
+    torch.cuda.set_device(0)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dim,hq,tokens,top", [(128, 4, 640, 117), (128, 20, 640, 117), (64, 48, 650, 117), (256, 3, 700, 117),
+                                               (128, 5, 9000, 113), (128, 12, 9000, 113), (128, 5, 1000, -100), (128, 12, 1000, -100)])
+def test_values_near_the_ends_of_the_range(fmt, dim, hq, tokens, top):
+    """Magnitudes times tokens just below 2^127 (equal, rising and falling scores, so that weights pass the running
+    maximum), and values near the other end.  The tail and the draft rows hold them too."""
+    c = Cache(fmt=fmt, heads=1, dim=dim, max_tokens=tokens + 8, pages=160)
+    g = gen(tokens + hq)
+
+    def values(n):
+        x = (1 + torch.rand((n, 1, dim), generator=g) * 0.5) * 2.0 ** (top - 1)
+        return (x * torch.sign(torch.randn((1, 1, dim), generator=g))).to(torch.bfloat16)
+
+    k = kv(g, tokens, 1, dim, 0.1)
+    k[:, 0, :] += (torch.arange(tokens) / tokens * 4 / dim)[:, None].to(torch.bfloat16)
+    woq.woq_kv8_extend(c.cfg, c.buf, 0, tokens)
+    c.fill(0, 0, k, values(tokens))
+    c.place(0, [0], 2, kv(g, 2, 1, dim, 0.1), values(2))
+    q = torch.ones((2, hq, dim), dtype=torch.bfloat16)
+    for scale in (0.0, 1.0, -1.0):
+        c.attend([0], 2, hq, g, q=q, scale=scale)

@@ -48,6 +48,10 @@ namespace kv8 {
 
 constexpr float kRaise = 7.0f;    // a score may pass the running maximum by this (log2) before it is raised
 constexpr float kOffset = 7.0f;   // weights carry 2^kOffset
+// What weights are at most is taken off again where they meet the values' scale in fp32, so that weighted values never
+// pass the sum of their magnitudes, as if weights were at most 1 (a power of two: exact, but for value scales below 2^-112,
+// of which bits are lost under 2^-149).
+constexpr float kUnit = 0x1p-14f, kWeightTop = 0x1p14f;  // 2^(kRaise + kOffset)
 constexpr int kMergePad = 4;      // floats behind each row of the merge buffer (bank spread)
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -159,7 +163,7 @@ __device__ __forceinline__ void block_step(State<D>& st, const uint8_t* rec, con
                                            int lane) {
   const int g = lane >> 2, t = lane & 3;
   const float ks = *reinterpret_cast<const float*>(rec + 128 * D);
-  const float vs = *reinterpret_cast<const float*>(rec + 128 * D + 4);
+  const float vs = *reinterpret_cast<const float*>(rec + 128 * D + 4) * kUnit;
   const uint8_t* kc = rec + t * 128 + g * 16;
   float s[4][4];
 #pragma unroll
@@ -324,10 +328,11 @@ __device__ __forceinline__ void tail_step(State<D>& st, const uint16_t* tail, in
   }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const uint32_t u = pack_bf16(p[2 * h], p[2 * h + 1]);
+    const float w0 = p[2 * h] * kUnit, w1 = p[2 * h + 1] * kUnit;
+    const uint32_t u = pack_bf16(w0, w1);
     const float f0 = __uint_as_float(u << 16), f1 = __uint_as_float(u & 0xFFFF0000u);
     hi[h] = transpose8x8(u);
-    lo[h] = transpose8x8(pack_bf16(p[2 * h] - f0, p[2 * h + 1] - f1));
+    lo[h] = transpose8x8(pack_bf16(w0 - f0, w1 - f1));
   }
 #pragma unroll
   for (int j = 0; j < D / 16; ++j) {
@@ -701,7 +706,7 @@ __device__ __forceinline__ void finish(const Kv8Attn& p, Misc& misc, const Plan&
       l += f * ps[w];
     }
     if (whole) {
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l * kWeightTop;
       *reinterpret_cast<uint2*>(p.out + query_at<D>(p, e, kv_head, base + n) + d) =
           make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
     } else {
@@ -798,7 +803,7 @@ __device__ __forceinline__ void finish(const Kv8Attn& p, Misc& misc, const Plan&
       }
 #pragma unroll 8
       for (; c < np; ++c) add(fs[c], __ldcg(reinterpret_cast<const float4*>(from + c * step + (c == 0 ? first : 0))));
-      const float l = sums[n - n0], inv = l == 0.0f ? 0.0f : 1.0f / l;
+      const float l = sums[n - n0], inv = l == 0.0f ? 0.0f : 1.0f / l * kWeightTop;
       *reinterpret_cast<uint2*>(p.out + query_at<D>(p, e, kv_head, base + n) + d) =
           make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
     }
@@ -1070,7 +1075,7 @@ __device__ __forceinline__ void team_block(TeamState<D, NT>& st, TeamShared<NT>&
                                            int buf, int wi, int team, int lane) {
   const int g = lane >> 2, t = lane & 3;
   const float ks = *reinterpret_cast<const float*>(rec + 128 * D);
-  const float vs = *reinterpret_cast<const float*>(rec + 128 * D + 4);
+  const float vs = *reinterpret_cast<const float*>(rec + 128 * D + 4) * kUnit;
   const uint8_t* kc = rec + (2 * wi * (D / 16) + t) * 128 + g * 16;
   float s[NT][4];
 #pragma unroll
@@ -1237,11 +1242,12 @@ __device__ void team_tail(TeamState<D, NT>& st, TeamShared<NT>& ts, const uint16
     st.l[q][1] += l[q][1];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const uint32_t u = pack_bf16(w[q][2 * h], w[q][2 * h + 1]);
+      const float w0 = w[q][2 * h] * kUnit, w1 = w[q][2 * h + 1] * kUnit;
+      const uint32_t u = pack_bf16(w0, w1);
       const float f0 = __uint_as_float(u << 16), f1 = __uint_as_float(u & 0xFFFF0000u);
       reinterpret_cast<uint32_t*>(&ts.weights[0][q][wi >> 1][lane])[2 * (wi & 1) + h] = transpose8x8(u);
       reinterpret_cast<uint32_t*>(&ts.weights[1][q][wi >> 1][lane])[2 * (wi & 1) + h] =
-          transpose8x8(pack_bf16(w[q][2 * h] - f0, w[q][2 * h + 1] - f1));
+          transpose8x8(pack_bf16(w0 - f0, w1 - f1));
     }
   }
   team_sync(team);
@@ -1514,7 +1520,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
   }
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l * kWeightTop;
   uint16_t* out = p.out + query_at<D>(p, e, head / p.chunks, base + n) + d0;
   if (lane < kLanes)
     *reinterpret_cast<uint2*>(out + 4 * lane) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
