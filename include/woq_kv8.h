@@ -127,12 +127,14 @@ WOQ_API int woq_kv8_accept(const woq_kv8_config* cfg, void* cache, size_t cache_
 
 /* Make room for `tokens` more tokens of sequence seq (the prompt), in every layer: pages are
  * taken (lowest numbers first) and the length grows.  Then woq_kv8_append_prompt must fill each
- * layer once, before the sequence is used otherwise. */
+ * layer once, before the sequence is used otherwise.  A refused one (WOQ_DEVERR_STATE: longer than
+ * max_tokens; WOQ_DEVERR_PAGES) changes nothing, but that a prompt before it of as many tokens
+ * is over: what is then filled could not be told from the refused one's, and is refused too. */
 WOQ_API int woq_kv8_extend(const woq_kv8_config* cfg, void* cache, size_t cache_bytes, int seq, int tokens,
                            woq_stream_t stream);
 
 /* Fill the `tokens` last tokens of sequence seq, in one layer.  tokens must be what the
- * sequence's last woq_kv8_extend was given, with no accept, fork or free of it since
+ * sequence's last woq_kv8_extend (refused ones aside) was given, with no accept, fork or free of it since
  * (WOQ_DEVERR_STATE otherwise, and then nothing is written but q_out). */
 WOQ_API int woq_kv8_append_prompt(const woq_kv8_config* cfg, void* cache, size_t cache_bytes, int layer, int seq,
                                   int tokens, const void* qkv, int dtype, int row_stride, int q_heads,

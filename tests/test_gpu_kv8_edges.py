@@ -42,3 +42,29 @@ def test_values_near_the_ends_of_the_range(fmt, dim, hq, tokens, top):
     q = torch.ones((2, hq, dim), dtype=torch.bfloat16)
     for scale in (0.0, 1.0, -1.0):
         c.attend([0], 2, hq, g, q=q, scale=scale)
+
+
+def test_a_refused_extend_leaves_the_pending_prompt():
+    """More tokens than fit, or than there are pages for: what the extend before it reserved can still be filled.  A
+    prompt that was meant for the refused one is refused, even if it has as many tokens."""
+    c = Cache(layers=2, heads=2, seqs=2, pages=5, max_tokens=400)
+    g = gen(41)
+    woq.woq_kv8_extend(c.cfg, c.buf, 0, 100)
+    c.fill(0, 0, kv(g, 100, 2, 128), kv(g, 100, 2, 128))
+    woq.woq_kv8_extend(c.cfg, c.buf, 0, 301)
+    c.sound(woq.WOQ_DEVERR_STATE)
+    woq.woq_kv8_extend(c.cfg, c.buf, 0, 290)
+    c.sound(woq.WOQ_DEVERR_PAGES)
+    c.fill(1, 0, kv(g, 100, 2, 128), kv(g, 100, 2, 128))
+    c.check(0)
+    c.prompt(1, g, 192)
+    woq.woq_kv8_extend(c.cfg, c.buf, 0, 100)  # two pages, one is left
+    c.sound(woq.WOQ_DEVERR_PAGES)
+    x = torch.ones((100, 2 * 2 * 128), dtype=torch.bfloat16, device=DEV)
+    for layer in range(2):
+        woq.woq_kv8_append_prompt(c.cfg, c.buf, layer, 0, x, 0, None)
+        c.sound(woq.WOQ_DEVERR_STATE)
+    c.check(0)
+    c.check(1)
+    c.prompt(0, g, 50)
+    c.check(0)

@@ -103,8 +103,11 @@ __global__ void __launch_bounds__(kMetaThreads) extend_kernel(Kv8View v, int seq
     }
   }
   if (threadIdx.x == 0) {
+    // Refused: the pending prompt stays, unless it has as many tokens; fills that follow could then be meant for the
+    // refused one, and would go over the earlier one's tokens.
     if (ok) v.lens_p()[seq] = len + tokens;
-    v.reserved_p()[seq] = ok ? tokens : 0;
+    if (ok) v.reserved_p()[seq] = tokens;
+    else if (v.reserved_p()[seq] == tokens) v.reserved_p()[seq] = 0;
   }
 }
 
