@@ -68,3 +68,18 @@ def test_a_refused_extend_leaves_the_pending_prompt():
     c.check(1)
     c.prompt(0, g, 50)
     c.check(0)
+
+
+def test_state_of_another_configs_cache_and_of_no_cache():
+    c = Cache(heads=1, seqs=2)
+    other = woq.KV8Config(format=0, layers=1, kv_heads=1, head_dim=128, seqs=2, max_tokens=999, pages=32)
+    junk = torch.full((woq.woq_kv8_bytes(c.cfg),), 0x5A, dtype=torch.uint8, device=DEV)
+    c.prompt(0, gen(1), 70)
+    lens, refs, table = ints([9] * 2), ints([9] * 32), torch.full((2, 16), 9, dtype=torch.int32, device=DEV)
+    for cfg, buf in ((c.cfg, junk), (other, c.buf)):
+        woq.woq_kv8_state(cfg, buf, lens, refs, table)
+        torch.cuda.synchronize()
+        assert (lens == 9).all() and (refs == 9).all() and (table == 9).all()
+    assert (junk == 0x5A).all()
+    assert woq.woq_read_status(c.buf, clear=True) == woq.WOQ_DEVERR_HEADER
+    c.check(0)

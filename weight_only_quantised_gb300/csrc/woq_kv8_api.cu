@@ -393,13 +393,8 @@ int woq_kv8_state(const woq_kv8_config* cfg, const void* cache, size_t cache_byt
   Kv8View v;
   if (const int e = open_cache(cfg, cache, cache_bytes, &v)) return e;
   if (!aligned(lens, 4) || !aligned(refs, 4) || !aligned(table, 4)) return WOQ_ERR_ALIGN;
-  const cudaStream_t s = (cudaStream_t)stream;
-  cudaError_t e = cudaSuccess;
-  if (lens) e = cudaMemcpyAsync(lens, v.lens_p(), (size_t)v.seqs * 4, cudaMemcpyDeviceToDevice, s);
-  if (e == cudaSuccess && refs) e = cudaMemcpyAsync(refs, v.refs_p(), (size_t)v.pages * 4, cudaMemcpyDeviceToDevice, s);
-  if (e == cudaSuccess && table)
-    e = cudaMemcpyAsync(table, v.table_row(0), (size_t)v.seqs * v.blocks * 4, cudaMemcpyDeviceToDevice, s);
-  return cuda_result(e);
+  if (!lens && !refs && !table) return WOQ_OK;
+  return cuda_result(launch_kv8_state(v, lens, refs, table, (cudaStream_t)stream));
 }
 
 }  // extern "C"

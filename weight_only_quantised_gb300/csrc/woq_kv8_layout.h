@@ -130,6 +130,7 @@ cudaError_t launch_kv8_free(const Kv8View& v, const int32_t* seqs, int n, cudaSt
 cudaError_t launch_kv8_copy(const Kv8View& src, const Kv8View& dst, const int32_t* src_seqs, const int32_t* dst_seqs,
                             int n, cudaStream_t s);
 cudaError_t launch_kv8_compact(const Kv8View& v, int limit, cudaStream_t s);
+cudaError_t launch_kv8_state(const Kv8View& v, int32_t* lens, int32_t* refs, int32_t* table, cudaStream_t s);
 cudaError_t launch_kv8_read(const Kv8View& v, int layer, int layers, int seq, int first, int count, uint16_t* k,
                             uint16_t* vals, cudaStream_t s);
 

@@ -7,6 +7,8 @@
 // streams bound by HBM: 16-byte vectors, four in flight per thread, one 16 KB segment of a page
 // at a time over all SMs (with the bookkeeping, 0.8 of the measured copy rate over a whole copy
 // and compaction).  Launch order on the stream is the only synchronisation.
+#include <algorithm>
+
 #include "woq_internal.h"
 #include "woq_kv8_device.cuh"
 
@@ -486,6 +488,22 @@ __global__ void __launch_bounds__(256)
   }
 }
 
+// Words of the bookkeeping to the caller (whose buffer may begin at any word); all threads of the grid.
+__device__ __forceinline__ void copy_words(int32_t* to, const int32_t* from, size_t n) {
+  if (!to) return;
+  const size_t step = (size_t)gridDim.x * blockDim.x;
+#pragma unroll 4
+  for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += step) to[i] = from[i];
+}
+
+__global__ void __launch_bounds__(256) state_kernel(Kv8View v, int32_t* lens, int32_t* refs, int32_t* table) {
+  begin_after_prior();
+  if (!header_ok(v)) return;
+  copy_words(lens, v.lens_p(), (size_t)v.seqs);
+  copy_words(refs, v.refs_p(), (size_t)v.pages);
+  copy_words(table, v.table_row(0), (size_t)v.seqs * v.blocks);
+}
+
 }  // namespace kv8
 
 cudaError_t launch_kv8_init(const Kv8View& v, cudaStream_t s) {
@@ -532,6 +550,17 @@ cudaError_t launch_kv8_compact(const Kv8View& v, int limit, cudaStream_t s) {
   const dim3 grid(8, (unsigned)(v.seqs < 256 ? v.seqs : 256));
   if (e == cudaSuccess) e = kv8::launch(kv8::remap_kernel, grid, 256, 0, s, v, limit);
   return e != cudaSuccess ? e : copy_pages(v, v, s);
+}
+
+cudaError_t launch_kv8_state(const Kv8View& v, int32_t* lens, int32_t* refs, int32_t* table, cudaStream_t s) {
+  const int sms = sm_count();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  size_t words = 1;
+  if (lens) words = std::max(words, (size_t)v.seqs);
+  if (refs) words = std::max(words, (size_t)v.pages);
+  if (table) words = std::max(words, (size_t)v.seqs * v.blocks);
+  const size_t blocks = std::min((words + 4 * 256 - 1) / (4 * 256), (size_t)8 * sms);
+  return kv8::launch(kv8::state_kernel, (unsigned)blocks, 256, 0, s, v, lens, refs, table);
 }
 
 cudaError_t launch_kv8_read(const Kv8View& v, int layer, int layers, int seq, int first, int count, uint16_t* k,
