@@ -83,3 +83,83 @@ def test_state_of_another_configs_cache_and_of_no_cache():
     assert (junk == 0x5A).all()
     assert woq.woq_read_status(c.buf, clear=True) == woq.WOQ_DEVERR_HEADER
     c.check(0)
+
+
+def test_subnormal_values_in_e4m3():
+    """Scales stop at 2^-126, and the codes below are the value's multiples of 2^-126 in e4m3."""
+    c = Cache(fmt=1, heads=2)
+    c.prompt(0, gen(3), 130, 2.0 ** -130)
+    assert (c.model[0][0].k != 0).any()
+    c.check(0)
+
+
+@pytest.mark.parametrize("rows,group", [(1, 4), (3, 4), (8, 6)])
+@pytest.mark.parametrize("n,heads", [(33, 2), (64, 2), (70, 2), (70, 1), (129, 1)])
+def test_many_entries_that_are_cut(n, heads, rows, group):
+    """No more items than CTAs, but more entries than a warp lays out at once; one of them is cut into pieces."""
+    c = Cache(fmt=n % 2, heads=heads, seqs=n, max_tokens=4000, pages=70 + 3 * n, dim=64)
+    g = gen(n)
+    for s in range(n):
+        c.prompt(s, g, 3990 if s == n - 2 else (53 * s) % 190)
+    c.draft(list(range(n)), g, rows)
+    c.attend(list(range(n)), rows, group, g)
+    c.attend([(5 * s) % n for s in range(n)], rows, group, g, window=300, sinks=5)
+
+
+@pytest.mark.parametrize("rows,group", [(1, 4), (3, 4), (8, 6)])
+@pytest.mark.parametrize("captured", [False, True])
+def test_attention_directly_behind_what_changes_lengths(rows, group, captured):
+    """No kernel between a change of lengths and the attention: a plan made from the lengths before is made again."""
+    heads, hq, n = 2, 2 * group, 4
+    g = gen(31)
+    c = Cache(heads=heads, seqs=n, max_tokens=2000, pages=100)
+    lens = [1900, 130, 0, 700]
+    for s, t in enumerate(lens):
+        c.prompt(s, g, t)
+    c.draft(list(range(n)), g, 8)
+    q = torch.randn((n * rows, hq, 128), generator=g).to(torch.bfloat16)
+    qd, seqs, vis = q.to(DEV), ints([3, 0, 2, 1]), torch.zeros((n, rows), dtype=torch.int32, device=DEV)
+    ws = torch.zeros(woq.woq_kv8_attention_workspace(c.cfg, n, rows, hq), dtype=torch.uint8, device=DEV)
+    outs = [torch.empty_like(qd), torch.empty_like(qd)]
+    empty = lambda: M.Seq(heads, 128)  # noqa: E731
+    m = c.model[0]
+
+    def step(call, change):
+        """attention, call, attention"""
+        def run():
+            for i in range(2):
+                woq.woq_kv8_attention(c.cfg, c.buf, 0, seqs, rows, qd, hq, outs[i], ws, 0.1, vis=vis)
+                if i == 0:
+                    call()
+        if captured:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                run()
+            run = graph.replay
+        torch.cuda.synchronize()
+        run()
+        torch.cuda.synchronize()
+        for i in range(2):
+            if i == 1:
+                change()
+            for e, s in enumerate([3, 0, 2, 1]):
+                ref, bound = M.attention(m[s], 0, q[e * rows:(e + 1) * rows], [0] * rows, 0.1)
+                assert ((outs[i][e * rows:(e + 1) * rows].cpu().double() - ref).abs() <= bound).all(), (i, e)
+        c.sound()
+
+    def becomes(**new):
+        def change():
+            for name, s in new.items():
+                m[int(name[1:])] = s()
+        return change
+
+    def accept():
+        m[0].accept(0xFF), m[1].accept(3), m[3].accept(0x81)
+
+    lists = {k: ints(v) for k, v in dict(a=[0], b=[3], c=[1], d=[2], e=[0, 1, 3], f=[0xFF, 3, 0x81], g=[1, 3]).items()}
+    step(lambda: woq.woq_kv8_accept(c.cfg, c.buf, lists["e"], lists["f"]), accept)
+    step(lambda: woq.woq_kv8_free(c.cfg, c.buf, lists["a"]), becomes(s0=empty))
+    step(lambda: woq.woq_kv8_fork(c.cfg, c.buf, lists["b"], lists["a"]), becomes(s0=lambda: m[3].clone()))
+    step(lambda: woq.woq_kv8_copy(c.cfg, c.buf, c.cfg, c.buf, lists["c"], lists["d"]), becomes(s2=lambda: m[1].clone()))
+    step(lambda: woq.woq_kv8_free(c.cfg, c.buf, lists["g"]), becomes(s1=empty, s3=empty))
+    step(lambda: seqs.copy_(seqs), lambda: None)
