@@ -109,7 +109,7 @@ def test_many_entries_that_are_cut(n, heads, rows, group):
 @pytest.mark.parametrize("rows,group", [(1, 4), (3, 4), (8, 6)])
 @pytest.mark.parametrize("captured", [False, True])
 def test_attention_directly_behind_what_changes_lengths(rows, group, captured):
-    """No kernel between a change of lengths and the attention: a plan made from the lengths before is made again."""
+    """No kernel between a change of lengths and the attention."""
     heads, hq, n = 2, 2 * group, 4
     g = gen(31)
     c = Cache(heads=heads, seqs=n, max_tokens=2000, pages=100)
@@ -163,3 +163,42 @@ def test_attention_directly_behind_what_changes_lengths(rows, group, captured):
     step(lambda: woq.woq_kv8_copy(c.cfg, c.buf, c.cfg, c.buf, lists["c"], lists["d"]), becomes(s2=lambda: m[1].clone()))
     step(lambda: woq.woq_kv8_free(c.cfg, c.buf, lists["g"]), becomes(s1=empty, s3=empty))
     step(lambda: seqs.copy_(seqs), lambda: None)
+
+
+@pytest.mark.parametrize("rows,group", [(1, 4), (3, 4)])
+@pytest.mark.parametrize("captured", [False, True])
+def test_attention_behind_the_end_of_a_long_sequence(rows, group, captured):
+    """Freeing a long sequence takes some microseconds and ends with its length, so the attention behind it, in a
+    graph, plans with the old length and has to plan anew (in 151 of 152 CTAs when this was written)."""
+    g = gen(32)
+    c = Cache(heads=1, seqs=3, dim=64, max_tokens=40000, pages=700)
+    for s, t in enumerate((39990, 500, 190)):
+        c.prompt(s, g, t)
+    hq, n = group, 3
+    q = torch.randn((n * rows, hq, 64), generator=g).to(torch.bfloat16)
+    qd, seqs, gone = q.to(DEV), ints([1, 0, 2]), ints([0])
+    vis = torch.zeros((n, rows), dtype=torch.int32, device=DEV)
+    ws = torch.zeros(woq.woq_kv8_attention_workspace(c.cfg, n, rows, hq), dtype=torch.uint8, device=DEV)
+    outs = [torch.empty_like(qd), torch.empty_like(qd)]
+
+    def run():
+        for i in range(2):
+            woq.woq_kv8_attention(c.cfg, c.buf, 0, seqs, rows, qd, hq, outs[i], ws, 0.1, vis=vis)
+            if i == 0:
+                woq.woq_kv8_free(c.cfg, c.buf, gone)
+
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run()
+        run = graph.replay
+    torch.cuda.synchronize()
+    run()
+    torch.cuda.synchronize()
+    for i in range(2):
+        if i == 1:
+            c.model[0][0] = M.Seq(1, 64)
+        for e, s in enumerate((1, 0, 2)):
+            ref, bound = M.attention(c.model[0][s], 0, q[e * rows:(e + 1) * rows], [0] * rows, 0.1)
+            assert ((outs[i][e * rows:(e + 1) * rows].cpu().double() - ref).abs() <= bound).all(), (i, e)
+    c.sound()
