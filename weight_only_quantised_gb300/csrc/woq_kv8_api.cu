@@ -318,7 +318,7 @@ int woq_kv8_attention(const woq_kv8_config* cfg, void* cache, size_t cache_bytes
   p.sinks = sinks;
   p.ctas = sms;
   p.fault_cta = fault_cta(1);
-  p.wait_ns = wait_bound_ns();
+  p.wait_ns = (uint32_t)wait_bound_ns();  // at most 2 s
   const int smem = kv8_attn_plan(&p, smem_max);
   if (smem == 0) return WOQ_ERR_SHAPE;
   p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + attn_parts_offset(v, n, p.chunks, sms));

@@ -271,7 +271,7 @@ __device__ __forceinline__ void quantise_block(const uint16_t* kt, const uint16_
   }
   if (threadIdx.x == 0) {
     const uint32_t ks = bad ? 0x7FC00000u : __float_as_uint(s0);
-    *reinterpret_cast<uint4*>(rec + 128 * (size_t)D) = make_uint4(ks, __float_as_uint(s1), 0u, 0u);
+    *reinterpret_cast<uint4*>(rec + 128 * (size_t)D) = make_uint4(ks, __float_as_uint(s1), __float_as_uint(s1 * kUnit), 0u);
   }
 }
 

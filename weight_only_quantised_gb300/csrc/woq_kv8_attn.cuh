@@ -48,10 +48,7 @@ namespace kv8 {
 
 constexpr float kRaise = 7.0f;    // a score may pass the running maximum by this (log2) before it is raised
 constexpr float kOffset = 7.0f;   // weights carry 2^kOffset
-// What weights are at most is taken off again where they meet the values' scale in fp32, so that weighted values never
-// pass the sum of their magnitudes, as if weights were at most 1 (a power of two: exact, but for value scales below 2^-112,
-// of which bits are lost under 2^-149).
-constexpr float kUnit = 0x1p-14f, kWeightTop = 0x1p14f;  // 2^(kRaise + kOffset)
+static_assert(kRaise + kOffset == 14.0f && kUnit == 0x1p-14f, "weights are at most 1 / kUnit");
 constexpr int kMergePad = 4;      // floats behind each row of the merge buffer (bank spread)
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -163,7 +160,7 @@ __device__ __forceinline__ void block_step(State<D>& st, const uint8_t* rec, con
                                            int lane) {
   const int g = lane >> 2, t = lane & 3;
   const float ks = *reinterpret_cast<const float*>(rec + 128 * D);
-  const float vs = *reinterpret_cast<const float*>(rec + 128 * D + 4) * kUnit;
+  const float vs = *reinterpret_cast<const float*>(rec + 128 * D + 8);  // times kUnit
   const uint8_t* kc = rec + t * 128 + g * 16;
   float s[4][4];
 #pragma unroll
@@ -383,6 +380,7 @@ constexpr int kMaxWarps = 7;
 struct Misc {
   uint64_t full[kMaxStages], empty[kMaxStages];
   int fail, last;
+  uint32_t wait_ns;  // bound of the teams' waits
   int share;      // units of a piece, 0: more items than CTAs
   int redo;       // the plan made before the wait does not hold
   // [n + 1] units of one head of the entries before, [n] lengths (-1: out of range), [n + 1] pieces (CTAs) of
@@ -706,7 +704,7 @@ __device__ __forceinline__ void finish(const Kv8Attn& p, Misc& misc, const Plan&
       l += f * ps[w];
     }
     if (whole) {
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l * kWeightTop;
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
       *reinterpret_cast<uint2*>(p.out + query_at<D>(p, e, kv_head, base + n) + d) =
           make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
     } else {
@@ -803,7 +801,7 @@ __device__ __forceinline__ void finish(const Kv8Attn& p, Misc& misc, const Plan&
       }
 #pragma unroll 8
       for (; c < np; ++c) add(fs[c], __ldcg(reinterpret_cast<const float4*>(from + c * step + (c == 0 ? first : 0))));
-      const float l = sums[n - n0], inv = l == 0.0f ? 0.0f : 1.0f / l * kWeightTop;
+      const float l = sums[n - n0], inv = l == 0.0f ? 0.0f : 1.0f / l;
       *reinterpret_cast<uint2*>(p.out + query_at<D>(p, e, kv_head, base + n) + d) =
           make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
     }
@@ -922,7 +920,7 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + 1), 1) attn_kernel(const __g
       if (g == 0) {
         const int row = warp * 8 + 2 * t + c;
         warp_ml[2 * row] = st.m[c];
-        warp_ml[2 * row + 1] = l;
+        warp_ml[2 * row + 1] = l * kUnit;  // as the weighted values
       }
     }
 #pragma unroll
@@ -1075,7 +1073,7 @@ __device__ __forceinline__ void team_block(TeamState<D, NT>& st, TeamShared<NT>&
                                            int buf, int wi, int team, int lane) {
   const int g = lane >> 2, t = lane & 3;
   const float ks = *reinterpret_cast<const float*>(rec + 128 * D);
-  const float vs = *reinterpret_cast<const float*>(rec + 128 * D + 4) * kUnit;
+  const float vs = *reinterpret_cast<const float*>(rec + 128 * D + 8);  // times kUnit
   const uint8_t* kc = rec + (2 * wi * (D / 16) + t) * 128 + g * 16;
   float s[NT][4];
 #pragma unroll
@@ -1293,6 +1291,7 @@ __global__ void __launch_bounds__(TeamShape<D>::kThreads, 1) attn_team_kernel(co
       dev::mbar_init(&misc.empty[i], 4);
     }
     misc.fail = 0;
+    misc.wait_ns = p.wait_ns;
     dev::fence_mbar_init();
   }
   const int team = (warp >> 2) % kTeams, wi = warp & 3;
@@ -1394,7 +1393,7 @@ __global__ void __launch_bounds__(TeamShape<D>::kThreads, 1) attn_team_kernel(co
       const int at = taken + (k - b0), stage = at % S;
       // after a wait that ran out the warp goes on without waits (the team's barriers need it) but releases no stage,
       // so that the producer stops too; what it sums is not used
-      if (ok) ok = __all_sync(~0u, dev::mbar_wait_bounded(&misc.full[stage], (uint32_t)((at / S) & 1), p.wait_ns));
+      if (ok) ok = __all_sync(~0u, dev::mbar_wait_bounded(&misc.full[stage], (uint32_t)((at / S) & 1), &misc.wait_ns));
       const int blk = k < sp.head_blocks ? k : sp.from + (k - sp.head_blocks);
       const int token0 = blk * kKv8Block;
       team_block<FMT, D, NT>(st, ts, ring + (size_t)stage * kRecord, queries, coef, low, token0,
@@ -1433,7 +1432,7 @@ __global__ void __launch_bounds__(TeamShape<D>::kThreads, 1) attn_team_kernel(co
           if (g == 0) {
             const int n = 8 * q + 2 * t + c;
             team_ml[2 * (team * kQueries + n)] = st.m[q][c];
-            team_ml[2 * (team * kQueries + n) + 1] = (ts.top[0][n] + ts.top[1][n]) + (ts.top[2][n] + ts.top[3][n]);
+            team_ml[2 * (team * kQueries + n) + 1] = ((ts.top[0][n] + ts.top[1][n]) + (ts.top[2][n] + ts.top[3][n])) * kUnit;
           }
     }
     dev::named_barrier_sync(1, W * 32);
@@ -1455,21 +1454,16 @@ constexpr int kJoinWarps = 4;
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ Kv8Attn p) {
   begin_after_prior();
+  const uint32_t failed = dev::ld_relaxed_u32(p.failed);  // beside the header's read and the place's
+  const int2 where = p.joins[blockIdx.x];
   uint32_t magic;
   if (!is_ours(p.v, &magic)) return;  // nothing was left
-  // After a wait that ran out some CTA left no parts, or no place of them: what is there may be an earlier launch's, of this
-  // item or of another.  So nothing is joined, in this launch or (it is reported again) before the workspace is zero-filled.
-  if (dev::ld_relaxed_u32(p.failed) != 0) {
-    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) flag(p.v, WOQ_DEVERR_TIMEOUT);
-    return;
-  }
   const int e = (int)blockIdx.x / p.heads, head = (int)blockIdx.x % p.heads, base = head % p.chunks * p.queries;
   constexpr int kParts = D > 128 ? D / 128 : 1;  // warps of one query
   const int Q = p.queries, lane = threadIdx.x & 31, w = (int)blockIdx.y * kJoinWarps + ((int)threadIdx.x >> 5);
   const int n = w / kParts, d0 = w % kParts * 128;
-  const int2 where = p.joins[blockIdx.x];
   const int np = where.y;
-  // (whatever wrote to the workspace: nothing outside the parts is read)
+  // (after a wait that ran out a place may be one of an earlier launch: nothing outside the parts is read)
   if (where.x < 0 || np > p.ctas - (where.x >> 1)) return;
   if (np <= 1 || n >= min(Q, p.rows * p.group - base)) return;
   // the first part's slot, and the first slots of the CTAs that follow
@@ -1520,7 +1514,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
   }
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l * kWeightTop;
+  // After a wait that ran out some CTA left no parts, or no place of them: what is there may be an earlier launch's, of this
+  // item or of another.  So nothing is joined, in this launch or (it is reported again) before the workspace is zero-filled.
+  if (failed != 0) {
+    if (lane == 0) flag(p.v, WOQ_DEVERR_TIMEOUT);
+    return;
+  }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   uint16_t* out = p.out + query_at<D>(p, e, head / p.chunks, base + n) + d0;
   if (lane < kLanes)
     *reinterpret_cast<uint2*>(out + 4 * lane) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));

@@ -10,7 +10,7 @@
 //     row p holding token kv8_token_of_row(p);
 //   64 D bytes of value codes, transposed, the same cores: element d, token j at
 //     ((d / 8) 4 + j / 16) 128 + (d % 8) 16 + j % 16;
-//   16 bytes: key scale, value scale (fp32), zero.
+//   16 bytes: key scale, value scale, value scale times kUnit (fp32), zero.
 // A lane (g = lane / 4, t = lane % 4) of the m16n8k16 pattern reads 16 bytes of row g of core
 // t: the warp's 512 bytes are contiguous, so the reads are free of bank conflicts, and
 // those 16 bytes are the lane's operands of four k-steps.  The token order of the key rows is the one
@@ -32,6 +32,10 @@ namespace woq {
 constexpr int kKv8Block = WOQ_KV8_BLOCK;
 constexpr int kKv8Tail = 72;  // 63 tokens and 8 draft rows, rounded up to whole 16-byte vectors
 constexpr int kKv8MaxSeqs = 1024;
+// The attention's weights are up to 2^14 in f16, which the value scale that they meet in fp32 takes off again: so the sums of
+// weighted values never pass the sum of the values' magnitudes, as if weights were at most 1 (a power of two: exact, but for
+// value scales below 2^-112, of which bits are lost under 2^-149).
+constexpr float kUnit = 1.0f / 16384;
 constexpr uint32_t kKv8Magic = 0x384B5657u;
 
 #if defined(__CUDACC__)
@@ -115,7 +119,7 @@ struct Kv8Attn {
   int warps, query_groups, stages, ctas;
   int least_units;   // units a CTA takes at least (while there are more CTAs than that needs, they idle)
   int fault_cta;     // tests of the waits' bound: this CTA copies no records (-1: none)
-  uint64_t wait_ns;  // bound of the waits in the ring
+  uint32_t wait_ns;  // bound of the waits in the ring
 };
 
 cudaError_t launch_kv8_init(const Kv8View& v, cudaStream_t s);
