@@ -202,3 +202,72 @@ def test_attention_behind_the_end_of_a_long_sequence(rows, group, captured):
             ref, bound = M.attention(c.model[0][s], 0, q[e * rows:(e + 1) * rows], [0] * rows, 0.1)
             assert ((outs[i][e * rows:(e + 1) * rows].cpu().double() - ref).abs() <= bound).all(), (i, e)
     c.sound()
+
+
+@pytest.mark.parametrize("rows,group", [(1, 4), (3, 4)])
+def test_a_full_list_of_sequences(rows, group):
+    """1024 entries: the most that a call takes."""
+    n = 1024
+    c = Cache(fmt=1, heads=2, dim=64, seqs=n, max_tokens=200, pages=2 * n)
+    g = gen(51)
+    for s in range(n):
+        c.prompt(s, g, (37 * s) % 140)
+    c.draft(list(range(n)), g, rows)
+    c.attend([(5 * s) % n for s in range(n)], rows, group, g)
+    keep = [(s * 7) % (1 << rows) for s in range(n)]
+    c.accept(list(range(n)), keep)
+    for s in (0, 1, 511, 1023):
+        c.check(s)
+    woq.woq_kv8_free(c.cfg, c.buf, ints(list(range(n))))
+    c.model = [[M.Seq(2, 64) for _ in range(n)]]
+    c.sound()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_offsets_past_32_bits(fmt):
+    """The last layer of a cache of 11 GB holds what a cache of one layer holds, before and after its pages move."""
+    heads, tokens, dim = 8, 40000, 128
+    big = woq.KV8Config(format=fmt, layers=64, kv_heads=heads, head_dim=dim, seqs=3, max_tokens=tokens + 8, pages=1300)
+    small = woq.KV8Config(format=fmt, layers=1, kv_heads=heads, head_dim=dim, seqs=1, max_tokens=tokens + 8, pages=630)
+    assert woq.woq_kv8_page_offset(big, 626) > 1 << 32
+    qkv = torch.randn((tokens, 2 * heads * dim), dtype=torch.bfloat16, device=DEV, generator=torch.Generator(DEV).manual_seed(1))
+    new = torch.randn((8, 2 * heads * dim), dtype=torch.bfloat16, device=DEV, generator=torch.Generator(DEV).manual_seed(2))
+    q = torch.randn((8, 5 * heads, dim), dtype=torch.bfloat16, device=DEV, generator=torch.Generator(DEV).manual_seed(3))
+
+    def results(cfg, buf, layer, seq):
+        out = []
+        for rows in (1, 8):
+            ws = torch.zeros(woq.woq_kv8_attention_workspace(cfg, 1, rows, 5 * heads), dtype=torch.uint8, device=DEV)
+            out.append(torch.empty_like(q[:rows]))
+            woq.woq_kv8_attention(cfg, buf, layer, ints([seq]), rows, q[:rows], 5 * heads, out[-1], ws, 0.09,
+                                  vis=torch.zeros((1, rows), dtype=torch.int32, device=DEV))
+        for _ in range(2):
+            out.append(torch.empty((tokens + 8, heads, dim), dtype=torch.bfloat16, device=DEV))
+        woq.woq_kv8_read(cfg, buf, layer, seq, 0, *out[2:])
+        assert woq.woq_read_status(buf) == 0
+        return out
+
+    def filled(cfg, layer, seq, first):
+        buf = torch.empty(woq.woq_kv8_bytes(cfg), dtype=torch.uint8, device=DEV)
+        woq.woq_kv8_init(cfg, buf)
+        for s in first + [seq]:
+            woq.woq_kv8_extend(cfg, buf, s, tokens)
+        woq.woq_kv8_append_prompt(cfg, buf, layer, seq, qkv, 0, None)
+        woq.woq_kv8_append_rows(cfg, buf, layer, ints([seq]), 8, new, 0, None)
+        woq.woq_kv8_accept(cfg, buf, ints([seq]), ints([0xFF]))
+        return buf
+
+    one = filled(small, 0, 0, [])
+    want = results(small, one, 0, 0)
+    buf = filled(big, 63, 2, [1])
+    same = lambda seq: all(torch.equal(a, b) for a, b in zip(want, results(big, buf, 63, seq)))  # noqa: E731
+    assert same(2)
+    woq.woq_kv8_fork(big, buf, ints([2]), ints([0]))
+    assert same(0)
+    woq.woq_kv8_free(big, buf, ints([1]))
+    woq.woq_kv8_compact(big, buf, 650)
+    assert same(2) and same(0)
+    woq.woq_kv8_compact(big, buf, 1300)
+    woq.woq_kv8_copy(big, buf, big, buf, ints([0]), ints([1]))
+    woq.woq_kv8_free(big, buf, ints([0, 2]))
+    assert same(1)
