@@ -151,10 +151,13 @@ WOQ_API int woq_kv8_append_prompt(const woq_kv8_config* cfg, void* cache, size_t
  *   draft rows 0 .. m.  Only rows that were appended may be seen.
  *   A row sees, in this order, the sequence's tokens and the draft rows of its vis; with
  *   window > 0 only the first `sinks` and the last `window` of them (window 0: all, sinks not
- *   used; window, sinks <= 2^30).  out = sum_j softmax_j(scale q . k_j) v_j over what it sees, in fp32 with 8-bit codes
- *   taken exactly (weights in f16, 11 significant bits), rounded to bf16; a row that sees
- *   nothing gives 0.  scale finite; q finite; sums of |q_i k_i| and
- *   scale times them below 2^100, sums of |v| over the tokens seen below 2^127.
+ *   used; window, sinks <= 2^30).  out = sum_j softmax_j(scale q . k_j) v_j over what it sees, rounded to bf16; a row
+ *   that sees nothing gives 0.  Scores, maxima and sums are fp32 and 8-bit codes exact; fewer bits are held of
+ *   queries against 8-bit keys (f16 under the row's power of two: exact but for elements below 2^-17 of the row's
+ *   largest, rounded to multiples of 2^-24 of it), and of the weights in the product with the
+ *   values (f16, 11 significant bits; 16 for tokens and draft rows that are held in bf16).
+ *   scale finite; q finite; sums of |q_i k_i| and scale times them below 2^100, sums of |v| over
+ *   the tokens seen below 2^127.
  *   seqs: as above, but entries may repeat; one out of range gives 0 and WOQ_DEVERR_STATE.
  *   ws: device, 16-byte aligned, woq_kv8_attention_workspace(...) bytes, zero-filled once before
  *   first use (woq_workspace_init); each launch leaves zero what has to be, so launches of
@@ -204,7 +207,8 @@ WOQ_API int woq_kv8_free(const woq_kv8_config* cfg, void* cache, size_t cache_by
  * own (lowest free numbers first, in the order of the list).  The caches may be one and the
  * same, or must not overlap; their configs may differ in seqs, max_tokens and pages only
  * (WOQ_ERR_SHAPE).  Conditions on dst as for woq_kv8_fork; a pair that does not fit sets
- * WOQ_DEVERR_PAGES or WOQ_DEVERR_STATE in dst.  All entries or none. */
+ * WOQ_DEVERR_PAGES or WOQ_DEVERR_STATE in dst, a source that is no cache of src_cfg WOQ_DEVERR_HEADER
+ * in dst.  All entries or none. */
 WOQ_API int woq_kv8_copy(const woq_kv8_config* src_cfg, const void* src, size_t src_bytes,
                          const woq_kv8_config* dst_cfg, void* dst, size_t dst_bytes, const int32_t* src_seqs,
                          const int32_t* dst_seqs, int n, woq_stream_t stream);

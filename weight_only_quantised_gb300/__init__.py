@@ -1,7 +1,8 @@
-"""Python binding of libwoq.so, the weight-only-quantised skinny linear for GB300.
+"""Python binding of libwoq.so: the weight-only-quantised skinny linears for GB300, the draft-tree
+planner, and the 8-bit key/value cache with its attention.
 
 Argument marshalling only: every function forwards to the C ABI of the same
-name declared in include/woq.h, passing raw pointers (torch tensors'
+name declared in include/woq.h, woq_tree.h and woq_kv8.h, passing raw pointers (torch tensors'
 ``data_ptr()`` for device buffers, numpy arrays for host buffers), sizes and the
 current CUDA stream.  Every step of the computation runs in the library's CUDA
 kernels; there is no Python or CPU fallback.  Importing this package loads the

@@ -7,7 +7,7 @@
 // tensor cores do in that time for up to 16 queries (mma.sync m16n8k16 f16 with fp32 sums runs at
 // about 512 multiply-adds a clock and SM here; 16 queries need 440 at the copy peak).
 //
-// Split: an item (entry, kv head) is its blocks and one unit for its tail.  With at most as many items
+// Split: an item (entry, kv head) is its blocks and kTailUnits units for its tail.  With at most as many items
 // as CTAs (one CTA per SM) every item is cut into equal pieces, one piece per CTA, the longer items
 // into more; a CTA that held the end of one item and the beginning of another would wait twice for
 // the tail, the joining of its warps and the counting in (131,071 tokens, 8 heads: 62 us against 54).
@@ -23,10 +23,12 @@
 // Block: scores transposed, S^T = K Q^T (tokens x queries), so that both codes operands are the
 // 16-row one and the 8-wide one is the queries: nothing is padded beyond 8 queries.  Codes
 // become f16 in registers, exactly (int8: a byte permute into 1024 + 128 + c and a subtraction; e4m3: one
-// conversion); queries are bf16 scaled by a power of two into f16, exactly but for elements below
-// 2^-24 of the row's largest.  Weights are 2^(s - m) in fp32 for the sum, rounded to f16 (11 bits) for
-// the product; m is raised only when a score passes it by 7, and weights carry a factor 2^7, so
-// f16 holds them to 2^-31 of the largest.  movmatrix turns the score fragments into the other
+// conversion); queries are bf16 scaled into f16 by the power of two that brings the row's largest to [1, 2):
+// exactly, but for elements below 2^-17 of it, which f16 holds to multiples of 2^-24.  Weights are 2^(s - m) in
+// fp32 (ex2.approx, good to 2^-22) for the sum, rounded to f16 for the product: half a step is 2^-11, an eighth of the
+// result's own in bf16, and a second product for their low parts would double the work on values.
+// m is raised only when a score passes it by 7, and weights carry a factor 2^7, so
+// f16 holds them to 2^-31 of the largest; the value scale takes their greatest factor off again (kUnit).  movmatrix turns the score fragments into the other
 // product's operand: O^T = V^T P^T, from the transposed value codes.  Each block's product is
 // scaled by its value scale in fp32.
 //
@@ -35,7 +37,8 @@
 // first block (plan, queries, code that is not in the instruction cache) and 4 in the joins.
 //
 // Tail: at most 63 tokens and the draft rows, bf16, straight from global memory; same fragments with
-// bf16 products, 16 tokens per warp, weights as two bf16 parts (16 bits).
+// bf16 products, 16 tokens per warp, queries as they are, weights as two bf16 parts (16 bits, half a step 2^-17: values may
+// be any bf16, so the product is one of bf16).
 #pragma once
 
 #include <atomic>
@@ -960,7 +963,8 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + 1), 1) attn_kernel(const __g
 // 27).  With head_dim 256 two, of two tiles: shared memory holds four records beside what they exchange.
 //
 // Registers: the warps have 128 (168) a thread at launch.  The last four, of which one copies records and the others
-// end, give up most of theirs to the teams (128 for all spill: two teams at 168 took 73 us, with 232 64).
+// end, give up most of theirs to the teams (128 for all spill: two teams at 168 took 73 us, with 232 64).  With 152 the
+// instances of head_dim 128 still spill, 36 to 68 bytes a thread with two to four tiles and 288 with five (455 thousand requests in 57 us).
 __host__ __device__ constexpr int teams_of(int dim) { return dim == 256 ? 2 : 3; }
 __host__ __device__ constexpr int team_tiles(int dim) { return dim == 256 ? 2 : 5; }  // most tiles of 8 queries
 template <int D>

@@ -11,8 +11,9 @@
 namespace woq {
 namespace kv8 {
 
-// Every kernel of the cache is launched with programmatic dependent launch and begins with this: it may be
-// scheduled while the kernel before it ends, reads and writes nothing until that one has completed, and only then
+// Every kernel of the cache is launched with programmatic dependent launch and passes through this: it may be
+// scheduled while the kernel before it ends, writes nothing and keeps nothing that it read until that one has completed (the
+// attention plans from lengths that it read before, and checks them afterwards), and only then
 // lets its own successor be scheduled (in that order: a linear reads its weights before its own wait, so
 // whoever wrote them must be complete by the time this kernel lets it start).
 __device__ __forceinline__ void begin_after_prior() {

@@ -23,7 +23,7 @@ struct MetaShared {
 };
 
 // The `need` lowest free pages below `limit` into out; returns how many there are (at most need).
-// out may be the map array: page numbers below a written rank were read before.
+// out may be the map array: only reference counts are read.
 __device__ int find_free(const Kv8View& v, int limit, int need, int32_t* out, MetaShared& sh) {
   const int32_t* refs = v.refs_p();
   int found = 0;
