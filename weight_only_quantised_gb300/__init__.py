@@ -637,9 +637,10 @@ def woq_kv8_init(cfg: KV8Config, cache, stream=None) -> None:
 
 def woq_rope_table(theta: float, rot_dim: int, table, stream=None) -> None:
     """Fill table (fp32 [positions, rot_dim / 2, 2]) with cos and sin of each position and frequency."""
-    positions = table.shape[0]
-    _check(lib.woq_rope_table(theta, rot_dim, positions, _dptr(table, "table", 4, positions * rot_dim),
-                              _stream(stream)), "woq_rope_table")
+    if table.dim() != 3 or 2 * table.shape[1] != rot_dim or table.shape[2] != 2:
+        raise ValueError(f"table: expected [positions, {rot_dim} / 2, 2], got {tuple(table.shape)}")
+    _check(lib.woq_rope_table(theta, rot_dim, table.shape[0], _typed(table, "table", _F32, -1), _stream(stream)),
+           "woq_rope_table")
 
 
 def _qkv(cfg, qkv, q_heads, q_out, rope):
@@ -733,6 +734,8 @@ def woq_kv8_attention(cfg: KV8Config, cache, layer: int, seqs, rows: int, q, q_h
 
 def woq_kv8_fork(cfg: KV8Config, cache, src, dst, stream=None) -> None:
     n = dst.numel()
+    if src.numel() != n:
+        raise ValueError(f"src: {src.numel()} entries for {n} in dst")
     _check(lib.woq_kv8_fork(*_cache_args(cfg, cache), _typed(src, "src", _INT32, n), _typed(dst, "dst", _INT32, n), n,
                             _stream(stream)), "woq_kv8_fork")
 
@@ -745,6 +748,8 @@ def woq_kv8_free(cfg: KV8Config, cache, seqs, stream=None) -> None:
 def woq_kv8_copy(src_cfg: KV8Config, src, dst_cfg: KV8Config, dst, src_seqs, dst_seqs, stream=None) -> None:
     """Copies of sequences, with pages of their own, in the same cache or another."""
     n = dst_seqs.numel()
+    if src_seqs.numel() != n:
+        raise ValueError(f"src_seqs: {src_seqs.numel()} entries for {n} in dst_seqs")
     _check(lib.woq_kv8_copy(*_cache_args(src_cfg, src), *_cache_args(dst_cfg, dst), _typed(src_seqs, "src_seqs", _INT32, n),
                             _typed(dst_seqs, "dst_seqs", _INT32, n), n, _stream(stream)), "woq_kv8_copy")
 
