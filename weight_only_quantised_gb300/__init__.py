@@ -7,7 +7,7 @@ name declared in include/woq.h, woq_tree.h and woq_kv8.h, passing raw pointers (
 current CUDA stream.  Every step of the computation runs in the library's CUDA
 kernels; there is no Python or CPU fallback.  Importing this package loads the
 in-tree ``libwoq.so`` and raises if it has not been built
-(``python -m weight_only_quantised_gb300._build`` or ``__graft_entry__.build()``).
+(``python weight_only_quantised_gb300/_build.py`` or ``__graft_entry__.build()``).
 """
 from __future__ import annotations
 
@@ -34,7 +34,7 @@ GROUP = 128
 TILE_ROWS = 128
 
 if not os.path.exists(LIB_PATH):
-    raise ImportError(f"{LIB_PATH} is missing: build it first (python -m weight_only_quantised_gb300._build)")
+    raise ImportError(f"{LIB_PATH} is missing: build it first (python weight_only_quantised_gb300/_build.py)")
 
 lib = ctypes.CDLL(LIB_PATH)
 
