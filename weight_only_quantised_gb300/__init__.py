@@ -1,8 +1,8 @@
 """Python binding of libwoq.so: the weight-only-quantised skinny linears for GB300, the draft-tree
-planner, and the 8-bit key/value cache with its attention.
+planner, the 8-bit key/value cache with its attention, and a block's norms, routing and experts.
 
 Argument marshalling only: every function forwards to the C ABI of the same
-name declared in include/woq.h, woq_tree.h and woq_kv8.h, passing raw pointers (torch tensors'
+name declared in include/woq.h, woq_tree.h, woq_kv8.h and woq_block.h, passing raw pointers (torch tensors'
 ``data_ptr()`` for device buffers, numpy arrays for host buffers), sizes and the
 current CUDA stream.  Every step of the computation runs in the library's CUDA
 kernels; there is no Python or CPU fallback.  Importing this package loads the
@@ -781,3 +781,120 @@ def woq_kv8_state(cfg: KV8Config, cache, lens=None, refs=None, table=None, strea
     blocks = -(-cfg.max_tokens // KV8_BLOCK)
     _check(lib.woq_kv8_state(*_cache_args(cfg, cache), _typed(lens, "lens", _INT32, cfg.seqs), _typed(refs, "refs", _INT32, cfg.pages),
                              _typed(table, "table", _INT32, cfg.seqs * blocks), _stream(stream)), "woq_kv8_state")
+
+
+# ----------------------------------------------------------------------------- a block around its linears
+# (include/woq_block.h)
+
+ROUTE_SOFTMAX, ROUTE_SIGMOID = 0, 1
+
+
+class _Router(ctypes.Structure):
+    _fields_ = [("score", _I), ("experts", _I), ("k", _I), ("groups", _I), ("top_groups", _I), ("group_best", _I),
+                ("renormalise", _I), ("scale", ctypes.c_float)]
+
+
+_FL = ctypes.c_float
+for _name, (_args, _res) in {
+    "woq_block_norm": ([_P, _I, _P, _P, _I, _P, _I, _I, _P, _P, _I, _P, _FL, _FL, _FL, _FL, _P], _I),
+    "woq_route": ([ctypes.POINTER(_Router), _P, _I, _I, _I, _P, _P, _P, _P, _P], _I),
+    "woq_experts_bytes": ([_I, _I, _I, _I], _Z),
+    "woq_experts_workspace": ([_I, _I, _I, _I, _I], _Z),
+    "woq_experts_swiglu": ([_I, _I, _P, _Z, _P, _Z, _P, _P, _P, _I, _I, _I, _I, _P, _P, _Z, _P], _I),
+}.items():
+    _f = getattr(lib, _name)
+    _f.argtypes = _args
+    _f.restype = _res
+
+
+def _kind(t, name: str) -> int:
+    """WOQ_KV8_BF16 or WOQ_KV8_F32 of a tensor."""
+    kind = (_DTYPES.get("qkv") or _dtypes("qkv")).get(t.dtype)
+    if kind is None:
+        raise ValueError(f"{name}: expected bfloat16 or float32, got {t.dtype}")
+    return kind
+
+
+def _shaped(t, name: str, kind: str, shape: tuple, on: int):
+    """Device pointer of a contiguous tensor of the kind and shape on device `on` (None -> NULL)."""
+    if t is None:
+        return None
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name}: expected {list(shape)}, got {list(t.shape)}")
+    if t.get_device() == on and t.is_contiguous() and t.dtype in (_DTYPES.get(kind) or _dtypes(kind)):
+        return t.data_ptr()
+    return _typed(t, name, kind, -1)
+
+
+def woq_block_norm(u, r, r_out, out, post=None, gate=None, pre=None, alpha: float = 1.0, beta: float = 1.0,
+                   offset: float = 0.0, eps: float = 1e-6, stream=None) -> None:
+    """r_out = alpha r + beta gate RMSNorm(u; post + offset), out = RMSNorm(r_out; pre + offset), in one pass:
+    u, r, r_out [T, D] bf16 or fp32 (r_out may be r), out [T, D] bf16 (None: not formed); post, pre [D] and gate
+    [gate_rows, D] bf16, row t of u taking gate row t // (T // gate_rows)."""
+    T = _rows(u, "u")
+    D = u.shape[1]
+    ukind, rkind = _kind(u, "u"), _kind(r, "r")
+    on = _shared_device(u)
+    if r_out is not r and r_out.dtype is not r.dtype:
+        raise ValueError(f"r_out: expected {r.dtype}, got {r_out.dtype}")
+    shape, rname = (T, D), _F32 if rkind else _BF16
+    if gate is not None and (gate.dim() != 2 or gate.shape[1] != D or (T > 0 and (gate.shape[0] < 1 or T % gate.shape[0]))):
+        raise ValueError(f"gate: expected [rows, {D}] with rows a divisor of {T}, got {list(gate.shape)}")
+    status = lib.woq_block_norm(
+        _shaped(u, "u", _F32 if ukind else _BF16, shape, on), ukind, _shaped(r, "r", rname, shape, on),
+        _shaped(r_out, "r_out", rname, shape, on), rkind, _shaped(out, "out", _BF16, shape, on), T, D,
+        _shaped(post, "post", _BF16, (D,), on), None if gate is None else _shaped(gate, "gate", _BF16, tuple(gate.shape), on),
+        1 if gate is None else gate.shape[0], _shaped(pre, "pre", _BF16, (D,), on), alpha, beta, offset, eps,
+        _current_raw_stream(on) if stream is None and on >= 0 else _stream(stream))
+    if status:
+        _raise(status, "woq_block_norm")
+
+
+def woq_route(logits, k: int, ids, weights, score: int = ROUTE_SOFTMAX, bias=None, groups: int = 1, top_groups: int = 1,
+              group_best: int = 1, renormalise: bool = True, scale: float = 1.0, live=None, stream=None) -> None:
+    """Each row's k experts of largest score (+ bias [E] fp32) and their weights: logits [T, E] bf16 or fp32 (rows may be
+    strided) -> ids [T, k] int32, weights [T, k] fp32; live: int32 [1], rows from it on get id -1 and weight 0."""
+    T = _rows(logits, "logits")
+    E = logits.shape[1]
+    kind = _kind(logits, "logits")
+    on = _shared_device(logits)
+    stride, inner = logits.stride()
+    if T <= 1:
+        stride = E  # one row: its stride says nothing
+    if E > 1 and inner != 1 or stride < E:
+        raise ValueError(f"logits: expected rows of neighbouring elements, got strides {logits.stride()}")
+    ptr = logits.data_ptr() if on >= 0 else _dptr(logits[:1], "logits")
+    cfg = _Router(score, E, k, groups, top_groups, group_best, 1 if renormalise else 0, scale)
+    status = lib.woq_route(ctypes.byref(cfg), ptr, kind, stride, T, _shaped(bias, "bias", _F32, (E,), on),
+                           _shaped(live, "live", _INT32, (1,), on), _shaped(ids, "ids", _INT32, (T, k), on),
+                           _shaped(weights, "weights", _F32, (T, k), on),
+                           _current_raw_stream(on) if stream is None and on >= 0 else _stream(stream))
+    if status:
+        _raise(status, "woq_route")
+
+
+def woq_experts_bytes(bits: int, E: int, N: int, K: int) -> int:
+    """Bytes of E packed matrices one behind the other; matrix e (woq_pack_device) starts at e / E of them."""
+    return lib.woq_experts_bytes(bits, E, N, K)
+
+
+def woq_experts_workspace(E: int, T: int, k: int, H: int, I: int) -> int:
+    return lib.woq_experts_workspace(E, T, k, H, I)
+
+
+def woq_experts_swiglu(bits: int, E: int, gate_up, down, x_bf16, ids, weights, I: int, y_bf16, ws, stream=None) -> None:
+    """y = sum of each row's experts: x_bf16 [T, H], ids int32 [T, k] (-1: none), weights fp32 [T, k], y_bf16 [T, H];
+    gate_up: E packed matrices of (2 I, H), down: of (H, I), one behind the other (uint8)."""
+    T = _rows(x_bf16, "x_bf16")
+    H = x_bf16.shape[1]
+    k = ids.shape[1] if ids.dim() == 2 else -1
+    on = _shared_device(x_bf16)
+    status = lib.woq_experts_swiglu(
+        bits, E, gate_up.data_ptr() if _is_bytes(gate_up, on) else _bytes(gate_up, "gate_up"), _nbytes(gate_up),
+        down.data_ptr() if _is_bytes(down, on) else _bytes(down, "down"), _nbytes(down),
+        _shaped(x_bf16, "x_bf16", _BF16, (T, H), on), _shaped(ids, "ids", _INT32, (T, k), on),
+        _shaped(weights, "weights", _F32, (T, k), on), T, k, H, I, _shaped(y_bf16, "y_bf16", _BF16, (T, H), on),
+        ws.data_ptr() if _is_bytes(ws, on) else _bytes(ws, "ws"), _nbytes(ws),
+        _current_raw_stream(on) if stream is None and on >= 0 else _stream(stream))
+    if status:
+        _raise(status, "woq_experts_swiglu")

@@ -1,0 +1,164 @@
+// C ABI of the parts of a block around its linears (include/woq_block.h): argument checks and layout.
+#include <math.h>
+
+#include "woq_block.h"
+#include "woq_block_internal.h"
+#include "woq_internal.h"
+#include "woq_layout.h"
+
+namespace woq {
+namespace {
+
+inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+inline bool known_type(int t) { return t == WOQ_KV8_BF16 || t == WOQ_KV8_F32; }
+
+// Where the parts of the experts' workspace lie: [256 B: status, counts][items][order][h][parts].
+struct ExpertsLayout {
+  size_t item, order, h, parts, total;
+  int items;
+};
+
+bool experts_layout(int E, int T, int k, int H, int I, ExpertsLayout* l) {
+  if (E < 1 || E > 1024 || k < 1 || k > 32 || T < 0 || (long long)T * k > kMostEntries) return false;
+  for (const int d : {H, I})
+    if (d < kGroup || d > 32768 || d % kGroup) return false;
+  const size_t n = (size_t)T * k;
+  // an item holds kExpertRows places of one expert, its last one fewer
+  const size_t most = n / kExpertRows + (size_t)E;
+  l->items = (int)(n < most ? n : most);
+  size_t at = 256;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at = (at + bytes + 255) / 256 * 256;
+    return here;
+  };
+  l->item = take((size_t)l->items * sizeof(ExpertItem));
+  l->order = take(n * 4);
+  l->h = take(n * I * 2);
+  l->parts = take(n * H * 4);
+  l->total = at;
+  return true;
+}
+
+}  // namespace
+}  // namespace woq
+
+using namespace woq;
+
+extern "C" {
+
+int woq_block_norm(const void* u, int u_dtype, const void* r, void* r_out, int r_dtype, void* out, int T, int D,
+                   const void* post, const void* gate, int gate_rows, const void* pre, float alpha, float beta,
+                   float offset, float eps, woq_stream_t stream) {
+  if (!known_type(u_dtype) || !known_type(r_dtype) || T < 0 || D < 8 || D > 16384 || D % 8) return WOQ_ERR_SHAPE;
+  if (!isfinite(alpha) || !isfinite(beta) || !isfinite(offset) || !isfinite(eps) || eps < 0.0f) return WOQ_ERR_SHAPE;
+  if (gate && (gate_rows < 1 || T % gate_rows)) return WOQ_ERR_SHAPE;
+  if (T == 0) return WOQ_OK;
+  if (!u || !r || !r_out || (out && !pre)) return WOQ_ERR_NULL;
+  for (const void* p : {u, r, (const void*)r_out, (const void*)out, post, gate, pre})
+    if (!aligned(p, 16)) return WOQ_ERR_ALIGN;
+  BlockNorm a = {};
+  a.u = u;
+  a.r = r;
+  a.r_out = r_out;
+  a.out = static_cast<uint16_t*>(out);
+  a.post = static_cast<const uint16_t*>(post);
+  a.gate = static_cast<const uint16_t*>(gate);
+  a.pre = static_cast<const uint16_t*>(pre);
+  a.u_f32 = u_dtype == WOQ_KV8_F32;
+  a.r_f32 = r_dtype == WOQ_KV8_F32;
+  a.rows = T;
+  a.dim = D;
+  a.rows_per_gate = gate ? T / gate_rows : 1;
+  a.alpha = alpha;
+  a.beta = beta;
+  a.offset = offset;
+  a.eps = eps;
+  return cuda_result(launch_block_norm(a, (cudaStream_t)stream));
+}
+
+int woq_route(const woq_router* cfg, const void* logits, int dtype, int row_stride, int T, const float* bias,
+              const int32_t* live, int32_t* ids, float* weights, woq_stream_t stream) {
+  if (!cfg) return WOQ_ERR_NULL;
+  const woq_router& c = *cfg;
+  if (c.score != WOQ_ROUTE_SOFTMAX && c.score != WOQ_ROUTE_SIGMOID) return WOQ_ERR_SHAPE;
+  if (!known_type(dtype) || T < 0 || c.experts < 1 || c.experts > 1024 || row_stride < c.experts) return WOQ_ERR_SHAPE;
+  if (c.groups < 1 || c.groups > 32 || c.experts % c.groups || c.top_groups < 1 || c.top_groups > c.groups) return WOQ_ERR_SHAPE;
+  const int size = c.experts / c.groups;
+  if ((c.group_best != 1 && c.group_best != 2) || c.group_best > size) return WOQ_ERR_SHAPE;
+  if (c.k < 1 || c.k > 32 || c.k > c.top_groups * size) return WOQ_ERR_SHAPE;
+  if ((c.renormalise != 0 && c.renormalise != 1) || !isfinite(c.scale)) return WOQ_ERR_SHAPE;
+  if (T == 0) return WOQ_OK;
+  if (!logits || !ids || !weights) return WOQ_ERR_NULL;
+  if (!aligned(logits, 16) || !aligned(bias, 4) || !aligned(live, 4) || !aligned(ids, 4) || !aligned(weights, 4))
+    return WOQ_ERR_ALIGN;
+  Route a = {};
+  a.logits = logits;
+  a.bias = bias;
+  a.live = live;
+  a.ids = ids;
+  a.weights = weights;
+  a.stride = row_stride;
+  a.f32 = dtype == WOQ_KV8_F32;
+  a.softmax = c.score == WOQ_ROUTE_SOFTMAX;
+  a.rows = T;
+  a.experts = c.experts;
+  a.k = c.k;
+  a.groups = c.groups;
+  a.group_size = size;
+  a.top_groups = c.top_groups;
+  a.group_best = c.group_best;
+  a.renormalise = c.renormalise;
+  a.scale = c.scale;
+  return cuda_result(launch_route(a, (cudaStream_t)stream));
+}
+
+size_t woq_experts_bytes(int bits, int E, int N, int K) {
+  if (E < 1 || E > 1024) return 0;
+  return packed_bytes(bits, N, K) * (size_t)E;
+}
+
+size_t woq_experts_workspace(int E, int T, int k, int H, int I) {
+  ExpertsLayout l;
+  return experts_layout(E, T, k, H, I, &l) ? l.total : 0;
+}
+
+int woq_experts_swiglu(int bits, int E, const void* gate_up, size_t gate_up_bytes, const void* down, size_t down_bytes,
+                       const void* x_bf16, const int32_t* ids, const float* weights, int T, int k, int H, int I,
+                       void* y_bf16, void* ws, size_t ws_bytes, woq_stream_t stream) {
+  ExpertsLayout l;
+  if ((bits != 4 && bits != 6) || !experts_layout(E, T, k, H, I, &l)) return WOQ_ERR_SHAPE;
+  if (T == 0) return WOQ_OK;
+  if (!gate_up || !down || !x_bf16 || !ids || !weights || !y_bf16 || !ws) return WOQ_ERR_NULL;
+  for (const void* p : {gate_up, down, x_bf16, (const void*)y_bf16, (const void*)ws})
+    if (!aligned(p, 16)) return WOQ_ERR_ALIGN;
+  if (!aligned(ids, 4) || !aligned(weights, 4)) return WOQ_ERR_ALIGN;
+  Experts a = {};
+  a.gate_up_stride = packed_bytes(bits, 2 * I, H);
+  a.down_stride = packed_bytes(bits, H, I);
+  if (gate_up_bytes < a.gate_up_stride * E || down_bytes < a.down_stride * E) return WOQ_ERR_LAYOUT;
+  if (ws_bytes < l.total) return WOQ_ERR_WORKSPACE;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  a.gate_up = static_cast<const uint8_t*>(gate_up);
+  a.down = static_cast<const uint8_t*>(down);
+  a.x = static_cast<const uint16_t*>(x_bf16);
+  a.ids = ids;
+  a.weights = weights;
+  a.y = static_cast<uint16_t*>(y_bf16);
+  a.bits = bits;
+  a.experts = E;
+  a.rows = T;
+  a.k = k;
+  a.hidden = H;
+  a.inner = I;
+  a.entries = T * k;
+  a.items = l.items;
+  a.status = reinterpret_cast<uint32_t*>(w);
+  a.item = reinterpret_cast<ExpertItem*>(w + l.item);
+  a.order = reinterpret_cast<int32_t*>(w + l.order);
+  a.h = reinterpret_cast<uint16_t*>(w + l.h);
+  a.parts = reinterpret_cast<float*>(w + l.parts);
+  return cuda_result(launch_experts(a, (cudaStream_t)stream));
+}
+
+}  // extern "C"
