@@ -87,12 +87,13 @@ WOQ_API int woq_route(const woq_router* cfg, const void* logits, int dtype, int 
  *   so has one with an id outside [-1, E), which sets WOQ_DEVERR_STATE in the workspace.
  *   Activations are not quantised (the matrix instructions take them as bf16 at the same cost, as these products are bound by
  *   the weights' bytes): products are exact, sums fp32, a group of 128 times its scale in fp32; silu(g) * u is
- *   rounded to bf16 before the down projection, and y once.  What a row gives does not depend on the run
- *   nor on the values of the others.
+ *   rounded to bf16 before the down projection, and y once.  What a row gives does not depend on the run, nor on the other
+ *   rows of the call.
  *   bits 4 or 6; 1 <= E <= 1024; 1 <= k <= 32; H, I multiples of 128 in [128, 32768]; 0 <= T, T k <= 32768.
  *   ws: device, 16-byte aligned, woq_experts_workspace(...) bytes, zero-filled once before first use
  *   (woq_workspace_init); launches of different shapes may use one that is large enough, launches that can overlap must not.
- *   A packed matrix whose header does not match sets WOQ_DEVERR_HEADER (woq_read_status(ws, ...)), and y is left as it was.
+ *   A chosen expert with a packed matrix whose header does not match sets WOQ_DEVERR_HEADER (woq_read_status(ws, ...)), and
+ *   the rows of y that chose it are left as they were.
  * Errors: WOQ_ERR_NULL, WOQ_ERR_ALIGN, WOQ_ERR_SHAPE, WOQ_ERR_LAYOUT (gate_up_bytes or down_bytes too
  * small), WOQ_ERR_WORKSPACE, WOQ_ERR_CUDA.
  * --------------------------------------------------------------------------- */

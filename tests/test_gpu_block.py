@@ -328,6 +328,10 @@ def test_experts_rows_go_by_themselves(T):
     assert c[2].isnan().all() and not c[5].isfinite().any()
     keep = [i for i in range(T) if i not in (2, 5)]
     assert torch.equal(a[keep], c[keep])
+    other = ids.clone()
+    other[2], other[5] = torch.tensor([-1, 3]), torch.tensor([1, 1])     # nor does what the others chose
+    c, _ = m.run(x, other, w)
+    assert torch.equal(a[keep], c[keep])
     w[3, 1] = float("nan")
     d, _ = m.run(x, ids, w)
     assert d[3].isnan().all() and torch.equal(d[keep][[i for i in range(len(keep)) if keep[i] != 3]], a[[i for i in keep if i != 3]])
@@ -341,24 +345,35 @@ def test_experts_large_and_small_activations():
         m.check((torch.randn((5, 128), generator=g) * s).to(BF), ids, w)
 
 
-def test_experts_headers():
-    """A matrix of another shape: y stays as it was, and the workspace says so."""
+@pytest.mark.parametrize("T", [3, 200])
+def test_experts_headers(T):
+    """A matrix of another shape: the rows that chose it keep their y, and the workspace says so; one that nobody chose
+    says nothing."""
     m = Experts(4, 256, 128)
     g = gen(5)
-    ids, w = chosen(g, 3, 4, 2)
-    x = torch.randn((3, 256), generator=g).to(BF)
+    ids, w = chosen(g, T, 3, 2)
+    ids[0] = torch.tensor([2, 1])
+    ids[1] = torch.tensor([0, 1])
+    x = torch.randn((T, 256), generator=g).to(BF)
     before, _ = m.run(x, ids, w)
+    hit = (ids == 2).any(1)
+    ws = m.ws(T, 2)
     for buf in (m.gate_up, m.down):
-        word = buf.view(4, -1)[2][16:20]          # N of the third expert's header
-        held = word.clone()
-        word += 1
-        y = torch.full((3, 256), 7.0, dtype=BF, device=DEV)
-        ws = m.ws(3, 2)
-        m.call(x.to(DEV), ids.to(DEV), w.to(DEV), y, ws)
-        assert (y == 7.0).all() and woq.woq_read_status(ws, clear=True) == woq.WOQ_DEVERR_HEADER
-        word.copy_(held)
-        m.call(x.to(DEV), ids.to(DEV), w.to(DEV), y, ws)
-        assert torch.equal(y.cpu(), before) and woq.woq_read_status(ws) == 0
+        for e, at in ((2, 0), (2, 8), (2, 16), (2, 20), (3, 16)):   # magic, bits, N, K of the third expert; the fourth's N
+            word = buf.view(4, -1)[e][at: at + 4]
+            held = word.clone()
+            word += 1
+            y = torch.full((T, 256), 7.0, dtype=BF, device=DEV)
+            m.call(x.to(DEV), ids.to(DEV), w.to(DEV), y, ws)
+            y = y.cpu()
+            if e == 2:
+                assert (y[hit] == 7.0).all() and torch.equal(y[~hit], before[~hit])
+            else:
+                assert torch.equal(y, before)
+            assert woq.woq_read_status(ws, clear=True) == (woq.WOQ_DEVERR_HEADER if e == 2 else 0)
+            word.copy_(held)
+            m.call(x.to(DEV), ids.to(DEV), w.to(DEV), y := y.to(DEV), ws)
+            assert torch.equal(y.cpu(), before) and woq.woq_read_status(ws) == 0
 
 
 def test_experts_share_a_workspace_between_shapes():
@@ -385,12 +400,12 @@ def test_experts_beyond_4_gb():
         big.view(E, -1)[e], small.view(E, -1)[e] = m.gate_up, m.down
     g = gen(7)
     x = torch.randn((2, H), generator=g).to(BF)
-    want, _ = m.run(x, torch.zeros((2, 1), dtype=torch.int32), torch.ones((2, 1)))
+    want, bound = M.experts(x, torch.zeros((2, 1), dtype=torch.int32), torch.ones((2, 1)), m.gu, m.d)
     y = torch.empty((2, H), dtype=BF, device=DEV)
     ws = torch.zeros(woq.woq_experts_workspace(E, 2, 2, H, I), dtype=torch.uint8, device=DEV)
     ids = torch.tensor([[E - 1, 5], [7, E - 1]], dtype=torch.int32, device=DEV)      # the others' weights are 0
     woq.woq_experts_swiglu(4, E, big, small, x.to(DEV), ids, torch.ones((2, 2), device=DEV), I, y, ws)
-    assert torch.equal(y.cpu(), want)
+    M.close(y, want, bound, M.B)
 
 
 # ---------------------------------------------------------------------------------------- together

@@ -55,8 +55,9 @@ struct Experts {
   int bits, experts, rows, k, hidden, inner;  // T, k, H, I
   int entries;                                // T k
   int items;                                  // most items there can be
+  int split_up, split_down;                   // warps that share a unit's groups (set by the launcher)
   // workspace
-  uint32_t* status;   // word 0: WOQ_DEVERR_*; word 1: items; word 2: a header that does not match
+  uint32_t* status;   // word 0: WOQ_DEVERR_*; word 1: items
   ExpertItem* item;
   int32_t* order;     // [entries]: places (t k + j) by expert
   uint16_t* h;        // bf16 [entries][I]
