@@ -91,20 +91,28 @@ def experts(x, ids, weights, gate_up, down):
     # a sum of K products: 128 of a group in the matrix unit (which may cut instead of round: a whole step each), then
     # the group's scale, the groups one behind another and the warps' sums
     steps = lambda n: (128 + n // 128 + 16) * 2 * U  # noqa: E731
+
+    # a bf16 is held as two e4m3 under the power of two of the largest in its group of 128: exact down to 2^-13 of that power of
+    # two, below it off by half a step of the first (2^-10 of 2^7) and of the second (a sixteenth of that)
+    def lost(v):
+        top = v.abs().reshape(-1, 128).amax(1, keepdim=True).expand(-1, 128).reshape(-1)
+        return torch.where(v.abs() < 2.0 ** -12 * top, 2.0 ** -17 * (17 / 16) * top, 0.0)
+
     for row in range(t):
         for j in range(ids.shape[1]):
             e = int(ids[row, j])
             if e < 0 or e >= gate_up.shape[0]:
                 continue
             g, u = (gate_up[e] @ x[row]).split(inner)
+            lg, lu = (gate_up[e].abs() @ lost(x[row])).split(inner)
             ag, au = (gate_up[e].abs() @ x[row].abs()).split(inner)
             s = g * torch.sigmoid(g)
             hid = s * u
             # |silu'| <= 1.1
-            e_hid = steps(h) * (1.1 * ag * u.abs() + s.abs() * au) + 8 * U * hid.abs()
+            e_hid = 1.1 * (steps(h) * ag + lg) * u.abs() + s.abs() * (steps(h) * au + lu) + 8 * U * hid.abs()
             w = float(weights[row, j])
             y[row] += w * (down[e] @ hid)
-            lin[row] += abs(w) * (down[e].abs() @ (e_hid + steps(inner) * hid.abs()))
+            lin[row] += abs(w) * (down[e].abs() @ (e_hid + steps(inner) * hid.abs() + lost(hid)))
             var[row] += w * w * (down[e].pow(2) @ hid.pow(2))
     # each h is rounded by at most B relative, evenly spread: a standard deviation of B / sqrt(3); six of them
     return y, lin + 6 * B / math.sqrt(3) * var.sqrt() + 40 * U * y.abs()

@@ -21,7 +21,7 @@ SOURCES = ["woq_api.cu", "woq_gemv_w4.cu", "woq_gemv_w4_pro.cu", "woq_gemv_w4_mm
            "woq_gemv_w6.cu", "woq_gemv_w6_pro.cu", "woq_small_kernels.cu", "woq_pack.cpp", "woq_tree.cpp",
            "woq_kv8_api.cu", "woq_kv8_append.cu", "woq_kv8_pages.cu", "woq_kv8_attn_int8.cu", "woq_kv8_attn_e4m3.cu",
            "woq_kv8_team_int8.cu", "woq_kv8_team_e4m3.cu", "woq_block_api.cu", "woq_block_norm.cu", "woq_route.cu",
-           "woq_experts.cu"]
+           "woq_experts.cu", "woq_experts_w4.cu", "woq_experts_w6.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

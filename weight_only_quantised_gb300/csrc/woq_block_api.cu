@@ -12,29 +12,42 @@ namespace {
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 inline bool known_type(int t) { return t == WOQ_KV8_BF16 || t == WOQ_KV8_F32; }
 
-// Where the parts of the experts' workspace lie: [256 B: status, counts][items][order][h][parts].
+// Where the parts of the experts' workspace lie.  What has to be zero between launches comes first and lies in the same place for every shape, so launches of different shapes may share a workspace.
 struct ExpertsLayout {
-  size_t item, order, h, parts, total;
-  int items;
+  size_t split_counts, split_sums, item, order, x_halves, x_meta, h_halves, h_meta, parts, total;
+  int few, item_rows;
 };
+
+// Rows of an item: the fewest columns of B that hold what an expert has where every one is as likely.  Up to kFewEntries places
+// of few rows an expert nothing is launched before the products.
+void choose_items(int E, size_t n, ExpertsLayout* l) {
+  const double rows = n / (E * (1.0 - pow(1.0 - 1.0 / E, (double)n)));
+  l->few = n <= (size_t)kFewEntries && rows <= 6.0;
+  l->item_rows = rows <= 6.0 ? 8 : rows <= 12.0 ? 16 : 32;
+}
 
 bool experts_layout(int E, int T, int k, int H, int I, ExpertsLayout* l) {
   if (E < 1 || E > 1024 || k < 1 || k > 32 || T < 0 || (long long)T * k > kMostEntries) return false;
   for (const int d : {H, I})
     if (d < kGroup || d > 32768 || d % kGroup) return false;
   const size_t n = (size_t)T * k;
-  // an item holds kExpertRows places of one expert, its last one fewer
-  const size_t most = n / kExpertRows + (size_t)E;
-  l->items = (int)(n < most ? n : most);
+  choose_items(E, n, l);
+  // an item holds kLeastItemRows places of one expert at least, an expert's last one fewer
+  const size_t most = n / kLeastItemRows + (size_t)E;
   size_t at = 256;
   auto take = [&](size_t bytes) {
     const size_t here = at;
     at = (at + bytes + 255) / 256 * 256;
     return here;
   };
-  l->item = take((size_t)l->items * sizeof(ExpertItem));
+  l->split_counts = take((size_t)kMostCtas * 4);
+  l->split_sums = take((size_t)kMostCtas * 2 * l->item_rows * 256 * 4);
+  l->item = take((n < most ? n : most) * sizeof(ExpertItem));
   l->order = take(n * 4);
-  l->h = take(n * I * 2);
+  l->x_halves = take((size_t)T * H * 2);
+  l->x_meta = take((size_t)T * (H / kGroup) * 8);
+  l->h_halves = take(n * I * 2);
+  l->h_meta = take(n * (I / kGroup) * 8);
   l->parts = take(n * H * 4);
   l->total = at;
   return true;
@@ -152,11 +165,19 @@ int woq_experts_swiglu(int bits, int E, const void* gate_up, size_t gate_up_byte
   a.hidden = H;
   a.inner = I;
   a.entries = T * k;
-  a.items = l.items;
+  a.few = l.few;
+  a.item_rows = bits == 6 && l.item_rows > 16 ? 16 : l.item_rows;  // int6 has two sums a column: tensor memory holds those of 16 rows
+  a.wait_ns = wait_bound_ns();
+  a.fault_cta = fault_cta(1);
   a.status = reinterpret_cast<uint32_t*>(w);
+  a.split_counts = reinterpret_cast<uint32_t*>(w + l.split_counts);
+  a.split_sums = reinterpret_cast<float*>(w + l.split_sums);
   a.item = reinterpret_cast<ExpertItem*>(w + l.item);
   a.order = reinterpret_cast<int32_t*>(w + l.order);
-  a.h = reinterpret_cast<uint16_t*>(w + l.h);
+  a.x_halves = w + l.x_halves;
+  a.x_meta = reinterpret_cast<float2*>(w + l.x_meta);
+  a.h_halves = w + l.h_halves;
+  a.h_meta = reinterpret_cast<float2*>(w + l.h_meta);
   a.parts = reinterpret_cast<float*>(w + l.parts);
   return cuda_result(launch_experts(a, (cudaStream_t)stream));
 }

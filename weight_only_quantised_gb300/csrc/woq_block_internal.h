@@ -54,16 +54,25 @@ struct Experts {
   uint16_t* y;
   int bits, experts, rows, k, hidden, inner;  // T, k, H, I
   int entries;                                // T k
-  int items;                                  // most items there can be
-  int split_up, split_down;                   // warps that share a unit's groups (set by the launcher)
+  int item_rows;                              // most places of an item: 8, 16 or 32
+  int few;                                    // few places: no plan in memory
+  unsigned long long wait_ns;                 // bound of device waits
+  int fault_cta;                              // a CTA that copies no weights (tests), -1: none
   // workspace
-  uint32_t* status;   // word 0: WOQ_DEVERR_*; word 1: items
+  uint32_t* status;   // word 0: WOQ_DEVERR_*; word 1: items; word 2: a wait ran out, and y is not written
+  uint32_t* split_counts;  // [CTAs]: parts of a unit that have been written (zero between launches)
+  float* split_sums;       // [CTAs][2][item rows][256]
   ExpertItem* item;
   int32_t* order;     // [entries]: places (t k + j) by expert
-  uint16_t* h;        // bf16 [entries][I]
+  uint8_t* x_halves;  // [rows][H / 128][256]: x in two e4m3 halves
+  float2* x_meta;     // [rows][H / 128]: what undoes their factor, and what the codes' offset adds
+  uint8_t* h_halves;  // [entries][I / 128][256]
+  float2* h_meta;     // [entries][I / 128]
   float* parts;       // [entries][H]
 };
-constexpr int kExpertRows = 8;  // most rows of an item
+constexpr int kLeastItemRows = 8;  // rows of an item, where they are fewest
+constexpr int kFewEntries = 256;   // places that every CTA of the products may sort out for itself
+constexpr int kMostCtas = 256;
 constexpr int kMostEntries = 32768;
 cudaError_t launch_experts(const Experts& p, cudaStream_t stream);
 

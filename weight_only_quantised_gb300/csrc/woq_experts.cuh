@@ -1,0 +1,704 @@
+// Experts' products over packed int4 / int6 weights (include/woq_block.h):
+//   h_e,t = silu(G_e x_t) * U_e x_t,   part = D_e h,   y_t = sum_j w_tj part_tj.
+//
+// A decode step's few rows choose many experts, so a launch is bound by the bytes of the chosen experts' weights, each read
+// once: a block of 128 x 128 weights arrives at an SM every 380 cycles or so, and what is done for it has to stay below that.
+//   - A, the weights, as 8-bit floats: the codes 0 .. 15 of e4m3 are themselves times 2^-9 (the subnormals, and the least
+//     exponent), so a nibble with its top bit flipped is w + 8 with nothing but a mask: 3 operations per 8 weights.  (mma.sync has no
+//     8-bit floats here: the compiler converts them; bf16 takes 9 operations per 8 weights and was issue bound, 48 us where this takes
+//     KERNEL_US.)  int6's two top bits are a product of their own, worth 16.
+//   - B, the rows: x is the sum of a high and a low half in e4m3 (4 significant bits each, bf16 has 8), two columns of B, under
+//     a power of two per row and group of 128.  Exact, but for elements below 2^-13 of the group's largest, which are off by at most
+//     2^-17 of it.  h is taken apart the same way from fp32, with one rounding to about 8 bits (2^-8 at most).
+//   - tcgen05.mma kind::f8f6f4 multiplies in fp32: D[128 rows of weights][2 columns a row], one per group, then
+//     acc += scale (D_high + D_low / 16 - 8 sum(x)) 2^e in fp32, a thread a row of weights.
+// Roles of a CTA (one per SM): two teams of four warps that make A from a block (shared memory -> registers -> tensor memory) and
+// add up D, one for gate and one for up (down: two neighbouring tiles); a warp that copies blocks (bulk copies, 8 KB each); a
+// thread that issues the products; two warps that bring B.
+// The steps (a group of a pair of tiles of an item) are dealt out evenly to the CTAs; a pair that several share is finished
+// by the one that comes last, from all their sums in CTA order, and nobody waits for another CTA.
+#pragma once
+
+#include <math.h>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "woq_block.h"
+#include "woq_block_internal.h"
+#include "woq_device.cuh"
+#include "woq_internal.h"
+#include "woq_kv8_device.cuh"
+#include "woq_layout.h"
+#include "woq_prologue.cuh"
+
+namespace woq {
+namespace experts {
+
+constexpr int kTeamThreads = 128;
+constexpr int kProducer = 8, kIssuer = 9, kBringer = 10, kBringers = 2;  // warps 0 .. 7: the teams
+constexpr int kThreads = (kBringer + kBringers) * 32;
+constexpr int kSmallEntries = kFewEntries;
+constexpr int kFewRows = 8;   // rows of an item then
+constexpr int kColumns = 512;       // of tensor memory
+
+// ---------------------------------------------------------------------------------------- halves
+
+// What a group's elements are multiplied by before they become e4m3: 2^7 over the power of two of the largest magnitude
+// (e: its exponent field), 16 times that for the low halves; and what undoes it.  Groups below 2^-116 share one factor.
+__device__ __forceinline__ int group_exponent(uint32_t field) { return max((int)field, 11); }
+__device__ __forceinline__ float group_factor(int e) { return __int_as_float((261 - e) << 23); }
+__device__ __forceinline__ float group_undo(int e) { return __int_as_float(e == 255 ? 0x7FC00000 : (e - 7) << 23); }  // inf, NaN: NaN
+
+__device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+// Largest magnitudes of two pairs of bf16, NaN if there is one (signs are not kept).
+__device__ __forceinline__ uint32_t most2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t most_field(uint32_t m) { return max(m & 0x7FFFu, m >> 16 & 0x7FFFu) >> 7; }
+
+__device__ __forceinline__ uint16_t e4m3x2(float lo, float hi) {
+  uint16_t d;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ uint32_t e4m3x4(uint32_t p01, uint32_t p23) {
+  return (uint32_t)e4m3x2(__uint_as_float(p01 << 16), __uint_as_float(p01 & 0xFFFF0000u)) |
+         (uint32_t)e4m3x2(__uint_as_float(p23 << 16), __uint_as_float(p23 & 0xFFFF0000u)) << 16;
+}
+
+// Of four bf16 (two pairs): their high halves (the value without its last four bits), their low ones (the rest, times 16), and
+// the sum of the scaled values.
+__device__ __forceinline__ void halves4(uint32_t x01, uint32_t x23, int e, uint32_t& high, uint32_t& low, float& sum) {
+  const uint32_t f = (uint32_t)(261 - e) << 7, f2 = f | f << 16, f16 = f2 + 0x02000200u, zero = 0x80008000u;
+  const uint32_t h01 = x01 & 0xFFF0FFF0u, h23 = x23 & 0xFFF0FFF0u;
+  high = e4m3x4(fma2(h01, f2, zero), fma2(h23, f2, zero));
+  low = e4m3x4(fma2(h01, f16 ^ zero, fma2(x01, f16, zero)), fma2(h23, f16 ^ zero, fma2(x23, f16, zero)));
+  const float s = group_factor(e);
+  sum = fmaf(__uint_as_float(x01 << 16), s, sum);
+  sum = fmaf(__uint_as_float(x01 & 0xFFFF0000u), s, sum);
+  sum = fmaf(__uint_as_float(x23 << 16), s, sum);
+  sum = fmaf(__uint_as_float(x23 & 0xFFFF0000u), s, sum);
+}
+
+// A group of a row in halves: 8 x [16 high][16 low], 256 bytes; beside it what undoes the factor and what takes the codes'
+// offset off (-8 or -32 times the sum, in codes' units).
+__device__ __forceinline__ float2 group_meta(int e, float sum, int bits) {
+  return make_float2(group_undo(e), sum * (bits == 4 ? -0x1p-6f : -0x1p-4f));
+}
+
+// ------------------------------------------------------------------------------------------ plan
+
+// Which experts are worked on, and for which places, in items of one expert: with up to kSmallEntries places every CTA
+// sorts them out for itself, else begin_kernel has (global memory).
+struct Plan {
+  int items;
+  int expert[kSmallEntries];
+  int rows[kSmallEntries];
+  int place[kSmallEntries][kFewRows];
+  // scratch
+  alignas(16) int ids[kSmallEntries];
+  int number[kSmallEntries];
+  int starts[kSmallEntries / 32];
+};
+
+// One place a thread.  A place's turn is the number of places before it with the same expert; every kFewRows-th starts an item.
+__device__ __forceinline__ void plan_here(const Experts& p, Plan& s) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const bool here = tid < kSmallEntries;
+  int e = -1;
+  if (tid < p.entries) {
+    e = p.ids[tid];
+    if ((unsigned)e >= (unsigned)p.experts) e = -1;
+  }
+  if (here) s.ids[tid] = e, s.rows[tid] = 0;
+  __syncthreads();
+  int turn = 0, leader = tid;
+  if (e >= 0) {
+    const int4* v = reinterpret_cast<const int4*>(s.ids);
+    for (int i = 0; i < tid; i += 4) {
+      const int4 o = v[i >> 2];
+      const int w[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (w[j] == e && i + j < tid) {
+          if (turn % kFewRows == 0) leader = i + j;
+          ++turn;
+        }
+    }
+    if (turn % kFewRows == 0) leader = tid;
+  }
+  const bool start = e >= 0 && leader == tid;
+  const unsigned starts = __ballot_sync(~0u, start);
+  if (here && lane == 0) s.starts[warp] = __popc(starts);
+  __syncthreads();
+  if (here) {
+    int number = __popc(starts & ((1u << lane) - 1));
+    for (int w = 0; w < warp; ++w) number += s.starts[w];
+    s.number[tid] = number;
+    if (start) s.expert[number] = e;
+    if (tid == kSmallEntries - 1) s.items = number + start;
+  }
+  __syncthreads();
+  if (e >= 0) {
+    const int item = s.number[leader];
+    s.place[item][turn % kFewRows] = tid;
+    atomicAdd(&s.rows[item], 1);
+  }
+  __syncthreads();
+}
+
+// ----------------------------------------------------------------------------------- tensor memory
+
+__device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, "
+      "%19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
+      "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
+      "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_stores() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Sixteen columns of the thread's row, complete.
+__device__ __forceinline__ void tmem_load16(uint32_t at, float (&d)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(at)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) d[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// D (128 x N, fp32) = or += A (tensor memory, 128 x 32 e4m3) B (shared memory, N x 32 e4m3).
+__device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{.reg .pred p; setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(dev::smem_addr(bar)) : "memory");
+}
+// B as core matrices of 8 columns x 16 bytes: 128 bytes from one to the next along k, 1024 from 8 columns to the next 8.
+__device__ __forceinline__ uint64_t b_descriptor(uint32_t at) {
+  return (uint64_t)(at >> 4 & 0x3FFF) | (uint64_t)(128 >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46;
+}
+template <int N>
+constexpr uint32_t kIdesc = 1u << 4 | (uint32_t)(N >> 3) << 17 | (uint32_t)(128 >> 4) << 24;  // fp32 sums, A and B e4m3 along k, M = 128
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void fence_for_products() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// ---------------------------------------------------------------------------------------- products
+
+// FEW: up to kSmallEntries places: the plan is made in the kernel, and the bringers take x apart as they go.
+template <int BITS, int N, bool FEW>
+struct Shape {
+  static constexpr int kRows = N / 2;  // of an item
+  static constexpr int kBlock = BITS == 4 ? kBlockBytesW4 : kBlockBytesW6;
+  static constexpr int kB = 2 * kBlock, kMeta = kB + N * 128, kStage = (kMeta + kRows * 8 + 127) / 128 * 128;
+  static constexpr int kACols = BITS == 4 ? 32 : 64, kDCols = BITS == 4 ? N : 2 * N;
+  static constexpr int kBuffers = 2 * 4 * (kACols + kDCols) <= kColumns ? 4 : 2;  // of A and D, a team
+  static_assert(2 * kBuffers * (kACols + kDCols) <= kColumns, "tensor memory");
+  // [stages][exchange: up's values, then the warps' maxima and sums][barriers and flags][plan]
+  static constexpr int kExchange = kRows * kTeamThreads * 4 + 2 * 4 * kRows * 4;
+  static constexpr int kMisc = 1024;
+  static constexpr int kPlan = FEW ? (int)((sizeof(Plan) + 127) / 128 * 128) : 0;
+  static constexpr int kRoom = 227 * 1024 - kExchange - kMisc - kPlan;
+  static constexpr int kStages = kRoom / kStage < 12 ? kRoom / kStage : 12;
+  static_assert(kStages >= kBuffers + 2, "a stage is held until its sums are taken");
+  static constexpr int kBytes = kStages * kStage + kExchange + kMisc + kPlan;
+};
+
+struct Barriers {
+  uint64_t weights[12], rows[12], empty[12];
+  uint64_t ready[2][4], done[2][4];
+  uint64_t teams, first_team;  // where all warps of the teams (of the first) meet
+  uint32_t tmem;
+  int fail, last;
+};
+static_assert(sizeof(Barriers) <= 1024, "misc");
+
+template <int BITS, bool GATED, int N, bool FEW>
+__global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
+  typedef Shape<BITS, N, FEW> Z;
+  extern __shared__ __align__(128) uint8_t s_mem[];
+  float* const s_up = reinterpret_cast<float*>(s_mem + Z::kStages * Z::kStage);
+  uint32_t* const s_most = reinterpret_cast<uint32_t*>(s_up + Z::kRows * kTeamThreads);
+  float* const s_sums = reinterpret_cast<float*>(s_most + 4 * Z::kRows);
+  Barriers& s = *reinterpret_cast<Barriers*>(s_mem + Z::kStages * Z::kStage + Z::kExchange);
+  Plan& plan = *reinterpret_cast<Plan*>(s_mem + Z::kStages * Z::kStage + Z::kExchange + Z::kMisc);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint64_t limit = p.wait_ns;
+
+  if (tid == 0) {
+    for (int i = 0; i < Z::kStages; ++i) {
+      dev::mbar_init(&s.weights[i], 1);
+      dev::mbar_init(&s.rows[i], 1);
+      dev::mbar_init(&s.empty[i], 8);
+    }
+    for (int w = 0; w < 2; ++w)
+      for (int i = 0; i < Z::kBuffers; ++i) {
+        dev::mbar_init(&s.ready[w][i], 4);
+        dev::mbar_init(&s.done[w][i], 1);
+      }
+    dev::mbar_init(&s.teams, 8);
+    dev::mbar_init(&s.first_team, 4);
+    s.fail = 0;
+    dev::fence_mbar_init();
+  }
+  if (warp == kIssuer)
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dev::smem_addr(&s.tmem)), "n"(kColumns) : "memory");
+  // The down projection's launch may read the ids (or the plan), which were there before the one it waits for began.
+  if (GATED) dev::pdl_wait_prior_grids();
+  dev::pdl_launch_dependents();
+  int items;
+  if constexpr (FEW) {
+    plan_here(p, plan);
+    items = plan.items;
+  } else {
+    items = (int)p.status[1];
+  }
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  const uint32_t tmem = s.tmem;
+
+  const int K = GATED ? p.hidden : p.inner, groups = K / kGroup;
+  const int tiles = GATED ? p.inner / kTileRows : p.hidden / kTileRows, slices = GATED ? tiles : (tiles + 1) / 2;
+  const int total = items * slices * groups;
+  const int ctas = total < (int)gridDim.x ? total : (int)gridDim.x, cta = blockIdx.x;
+  const int begin = cta < ctas ? (int)((long long)total * cta / ctas) : 0, end = cta < ctas ? (int)((long long)total * (cta + 1) / ctas) : 0;
+  const auto rows_of = [&](int item) { return FEW ? plan.rows[item] : p.item[item].rows; };
+  const auto place_of = [&](int item, int row) { return FEW ? plan.place[item][row] : p.order[p.item[item].first + row]; };
+  const auto failed = [&]() {
+    *(volatile int*)&s.fail = 1;
+    atomicOr(p.status, (uint32_t)WOQ_DEVERR_TIMEOUT);
+    p.status[2] = 1;  // y is not written then
+  };
+  const auto gave_up = [&]() { return *(volatile int*)&s.fail != 0; };
+
+  if (warp == kProducer) {
+    if (lane == 0 && begin < end) {
+      const uint8_t* const matrices = GATED ? p.gate_up : p.down;
+      const size_t stride = GATED ? p.gate_up_stride : p.down_stride;
+      int unit = begin / groups, g = begin - unit * groups, issued = 0;
+      const uint8_t* src[2];
+      const auto locate = [&]() {
+        const int item = unit / slices, slice = unit - item * slices;
+        const int expert = FEW ? plan.expert[item] : p.item[item].expert;
+        const uint8_t* const m = matrices + (size_t)expert * stride + kHeaderBytes;
+        const int t0 = GATED ? slice : 2 * slice, t1 = GATED ? slice + tiles : 2 * slice + 1;
+        src[0] = m + ((size_t)t0 * groups + g) * Z::kBlock;
+        src[1] = GATED || t1 < tiles ? m + ((size_t)t1 * groups + g) * Z::kBlock : nullptr;
+      };
+      locate();
+      int stage = 0;
+      uint32_t parity = 1;
+      for (int i = begin; i < end; ++i) {
+        if (!dev::mbar_wait_bounded(&s.empty[stage], parity, limit)) {
+          failed();
+          break;
+        }
+        if (gave_up()) break;
+        uint8_t* const at = s_mem + (size_t)stage * Z::kStage;
+        if (p.fault_cta != cta) {
+          dev::mbar_arrive_expect_tx(&s.weights[stage], src[1] ? 2 * Z::kBlock : Z::kBlock);
+          dev::bulk_copy_g2s(at, src[0], Z::kBlock, &s.weights[stage]);
+          if (src[1]) dev::bulk_copy_g2s(at + Z::kBlock, src[1], Z::kBlock, &s.weights[stage]);
+          ++issued;
+        }
+        if (++g == groups) {
+          g = 0;
+          ++unit;
+          if (i + 1 < end) locate();
+        } else {
+          src[0] += Z::kBlock;
+          if (src[1]) src[1] += Z::kBlock;
+        }
+        if (++stage == Z::kStages) stage = 0, parity ^= 1;
+      }
+      // nothing may be in flight when the CTA ends, whatever went wrong
+      if (gave_up())
+        for (int n = issued > Z::kStages ? issued - Z::kStages : 0; n < issued; ++n)
+          dev::mbar_wait_bounded(&s.weights[n % Z::kStages], (uint32_t)(n / Z::kStages) & 1u, limit);
+    }
+  } else if (warp == kIssuer) {
+    if (lane == 0) {
+      int stage = 0, buffer = 0;
+      uint32_t stage_parity = 0, buffer_parity = 0;
+      const uint32_t base = dev::smem_addr(s_mem);
+      bool ok = true;
+      int last = -1;            // the newest product's buffer, team and parity
+      for (int i = begin; i < end && ok; ++i) {
+        ok = dev::mbar_wait_bounded(&s.rows[stage], stage_parity, limit);
+        const uint64_t b = b_descriptor(base + stage * Z::kStage + Z::kB);
+        for (int w = 0; w < 2 && ok; ++w) {
+          ok = dev::mbar_wait_bounded(&s.ready[w][buffer], buffer_parity, limit);
+          if (!ok || gave_up()) {
+            ok = false;
+            break;
+          }
+          tmem_fence_after();
+          const uint32_t a = tmem + (w * Z::kBuffers + buffer) * (Z::kACols + Z::kDCols), d = a + Z::kACols;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mma(d, a + 8 * k, b + k * (256 >> 4), kIdesc<N>, k > 0);
+          if (BITS == 6)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mma(d + N, a + 32 + 8 * k, b + k * (256 >> 4), kIdesc<N>, k > 0);
+          mma_commit(&s.done[w][buffer]);
+          last = (buffer * 2 + w) * 2 + (int)buffer_parity;
+        }
+        if (++stage == Z::kStages) stage = 0, stage_parity ^= 1;
+        if (++buffer == Z::kBuffers) buffer = 0, buffer_parity ^= 1;
+      }
+      if (!ok) {
+        failed();
+        // products end in order: with the newest, all have
+        if (last >= 0) dev::mbar_wait_bounded(&s.done[last >> 1 & 1][last >> 2], (uint32_t)last & 1u, limit);
+      }
+    }
+  } else if (warp >= kBringer) {
+    if (!GATED) dev::pdl_wait_prior_grids();  // h
+    // the two warps take the steps in turn
+    const int me = warp - kBringer;
+    bool ok = true;
+    const auto arrive = [&](int stage) {
+      fence_for_products();
+      __syncwarp();
+      if (lane == 0) dev::mbar_arrive(&s.rows[stage]);
+    };
+    const auto free_stage = [&](int n) {  // step n of this CTA
+      if (!dev::mbar_wait_bounded(&s.empty[n % Z::kStages], ((uint32_t)(n / Z::kStages) & 1u) ^ 1u, limit)) {
+        failed();
+        ok = false;
+      }
+      if (__any_sync(~0u, !ok || gave_up())) ok = false;
+      return ok;
+    };
+    if constexpr (GATED && FEW) {
+      // lane 4 t + quarter: 32 elements of row t
+      const int t = lane >> 2, quarter = lane & 3;
+      uint4 v[4] = {};
+      const auto load = [&](int i) {
+        const int unit = i / groups, g = i - unit * groups, item = unit / slices;
+        const bool here = t < rows_of(item);
+        const uint4* src = reinterpret_cast<const uint4*>(p.x + (size_t)(here ? place_of(item, t) / p.k : 0) * K + g * kGroup + quarter * 32);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = here ? src[j] : make_uint4(0u, 0u, 0u, 0u);
+      };
+      if (begin + me < end) load(begin + me);
+      for (int i = begin + me; i < end && ok; i += kBringers) {
+        const uint32_t x[16] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w,
+                                v[2].x, v[2].y, v[2].z, v[2].w, v[3].x, v[3].y, v[3].z, v[3].w};
+        uint32_t m = most2(x[0], x[1]);
+#pragma unroll
+        for (int j = 2; j < 16; ++j) m = most2(m, x[j]);
+        m = most_field(m);
+        m = max(m, __shfl_xor_sync(~0u, m, 1));
+        m = max(m, __shfl_xor_sync(~0u, m, 2));
+        const int e = group_exponent(m);
+        uint32_t high[8], low[8];
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) halves4(x[2 * j], x[2 * j + 1], e, high[j], low[j], sum);
+        sum += __shfl_xor_sync(~0u, sum, 1);
+        sum += __shfl_xor_sync(~0u, sum, 2);
+        if (i + kBringers < end) load(i + kBringers);
+        const int n = i - begin, stage = n % Z::kStages;
+        if (!free_stage(n)) break;
+        uint8_t* const at = s_mem + (size_t)stage * Z::kStage + Z::kB + (t >> 2) * 1024 + (t & 3) * 32 + quarter * 256;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          *reinterpret_cast<uint4*>(at + j * 128) = make_uint4(high[4 * j], high[4 * j + 1], high[4 * j + 2], high[4 * j + 3]);
+          *reinterpret_cast<uint4*>(at + j * 128 + 16) = make_uint4(low[4 * j], low[4 * j + 1], low[4 * j + 2], low[4 * j + 3]);
+        }
+        if (quarter == 0) *reinterpret_cast<float2*>(s_mem + (size_t)stage * Z::kStage + Z::kMeta + t * 8) = group_meta(e, sum, BITS);
+        arrive(stage);
+      }
+    } else {
+      // pieces of 16 bytes: piece lane & 15 of two rows at a time
+      const uint8_t* const halves = GATED ? p.x_halves : p.h_halves;
+      const float2* const meta = GATED ? p.x_meta : p.h_meta;
+      const int piece = lane & 15;
+      const uint32_t base = dev::smem_addr(s_mem);
+      int unit = -1, rows = 0;
+      size_t from[Z::kRows / 2];  // of rows 2 j + (lane >> 4)
+      constexpr int kAhead = 2;   // copies of this many steps are under way
+      int pending = 0;
+      int i = begin + me;
+      for (; i < end && ok; i += kBringers) {
+        const int u = i / groups, g = i - u * groups;
+        if (u != unit) {
+          unit = u;
+          const int item = u / slices;
+          rows = rows_of(item);
+#pragma unroll
+          for (int j = 0; j < Z::kRows / 2; ++j) {
+            const int r = 2 * j + (lane >> 4);
+            const int place = r < rows ? place_of(item, r) : 0;
+            from[j] = (size_t)(GATED ? place / p.k : place) * groups;
+          }
+        }
+        const int n = i - begin;
+        if (!free_stage(n)) break;
+        const uint32_t at = base + (n % Z::kStages) * Z::kStage;
+#pragma unroll
+        for (int j = 0; j < Z::kRows / 2; ++j) {
+          const int r = 2 * j + (lane >> 4);
+          if (r < rows) {
+            copy16(at + Z::kB + (r >> 2) * 1024 + (piece >> 1) * 128 + (r & 3) * 32 + (piece & 1) * 16, halves + (from[j] + g) * 256 + piece * 16);
+            if (piece == 0) copy8(at + Z::kMeta + r * 8, meta + from[j] + g);
+          }
+        }
+        copies_commit();
+        if (++pending > kAhead) {
+          copies_wait<kAhead>();
+          arrive((n - kAhead * kBringers) % Z::kStages);
+          --pending;
+        }
+      }
+      copies_wait<0>();
+      // the last steps (if the loop ended early nobody waits for them any more)
+      if (ok)
+        for (; pending > 0; --pending) arrive((i - begin - pending * kBringers) % Z::kStages);
+    }
+  } else {
+    // ------------------------------------------------------------------------------- the teams
+    if (!GATED) dev::pdl_wait_prior_grids();  // the sums of split pairs lie where the launch before had its own
+    const int team = warp >> 2, quad = warp & 3, row = quad * 32 + lane;  // row of the tile
+    const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+    const uint32_t my_tmem = tmem + lanes + team * Z::kBuffers * (Z::kACols + Z::kDCols);
+    float acc[Z::kRows] = {};
+    bool ok = true;
+    uint32_t teams_phase = 0, first_phase = 0;
+    const auto meet = [&](uint64_t* bar, uint32_t& phase) {  // false: something has failed, here or elsewhere
+      __syncwarp();
+      if (lane == 0) dev::mbar_arrive(bar);
+      const bool good = dev::mbar_wait_bounded(bar, phase, limit);
+      phase ^= 1;
+      if (!good) failed();
+      return !__any_sync(~0u, !good || gave_up());
+    };
+    const auto finish = [&](int unit) {
+      const int first_step = unit * groups;
+      // the CTAs of the unit's first and last step
+      const int a = (int)(((long long)(first_step + 1) * ctas - 1) / total);
+      const int b = (int)(((long long)(first_step + groups) * ctas - 1) / total);
+      if (a != b) {
+        const size_t words = (size_t)Z::kRows * 256;
+        float* const part = p.split_sums + ((size_t)cta * 2 + (first_step >= begin ? 1 : 0)) * words + tid;
+#pragma unroll
+        for (int j = 0; j < Z::kRows; ++j) __stcg(part + j * 256, acc[j]);
+        __threadfence();
+        if (!meet(&s.teams, teams_phase)) return false;
+        if (tid == 0) {
+          const uint32_t before = dev::atomic_add_acq_rel_gpu(p.split_counts + a, 1u);
+          s.last = before == (uint32_t)(b - a);
+          if (s.last) p.split_counts[a] = 0;
+        }
+        if (!meet(&s.teams, teams_phase)) return false;
+        if (!s.last) return true;
+        __threadfence();
+#pragma unroll
+        for (int j = 0; j < Z::kRows; ++j) acc[j] = 0.0f;
+        for (int c = a; c <= b; ++c) {
+          const float* const from = p.split_sums + ((size_t)c * 2 + (c == a ? 1 : 0)) * words + tid;
+#pragma unroll
+          for (int j = 0; j < Z::kRows; ++j) acc[j] += __ldcg(from + j * 256);
+        }
+      }
+      const int item = unit / slices, slice = unit - item * slices, rows = rows_of(item);
+      // codes were taken as 2^-9 of themselves
+      if constexpr (!GATED) {
+        const int tile = 2 * slice + team;
+        if (tile < tiles) {
+#pragma unroll
+          for (int t = 0; t < Z::kRows; ++t)
+            if (t < rows) p.parts[(size_t)place_of(item, t) * p.hidden + tile * kTileRows + row] = 512.0f * acc[t];
+        }
+        return true;
+      } else {
+        // h = silu(gate) up: the second team's sums go to the first, which has the group of 128 of each row and takes it apart
+        if (team == 1) {
+#pragma unroll
+          for (int t = 0; t < Z::kRows; ++t) s_up[t * kTeamThreads + row] = 512.0f * acc[t];
+        }
+        if (!meet(&s.teams, teams_phase)) return false;
+        if (team == 0) {
+#pragma unroll
+          for (int t = 0; t < Z::kRows; ++t) {
+            const float v = 512.0f * acc[t];
+            acc[t] = v / (1.0f + expf(-v)) * s_up[t * kTeamThreads + row];
+            const uint32_t m = __reduce_max_sync(~0u, __float_as_uint(acc[t]) & 0x7FFFFFFFu);
+            if (lane == 0) s_most[quad * Z::kRows + t] = m;
+          }
+          if (!meet(&s.first_team, first_phase)) return false;
+          const auto exponent = [&](int t) {
+            const uint32_t* const m = s_most + t;
+            return group_exponent(max(max(m[0], m[Z::kRows]), max(m[2 * Z::kRows], m[3 * Z::kRows])) >> 23);
+          };
+#pragma unroll
+          for (int t = 0; t < Z::kRows; ++t) {
+            if (t >= rows) break;
+            const float v = acc[t] * group_factor(exponent(t));
+            const uint16_t high = e4m3x2(v, 0.0f);
+            uint32_t back;
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(high));
+            const uint16_t low = e4m3x2((v - dev::half_bits_to_float(back & 0xFFFFu)) * 16.0f, 0.0f);
+            uint8_t* const to = p.h_halves + ((size_t)place_of(item, t) * (p.inner / kGroup) + slice) * 256 + (row >> 4) * 32 + (row & 15);
+            to[0] = (uint8_t)high;
+            to[16] = (uint8_t)low;
+            float sum = v;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+            if (lane == 0) s_sums[quad * Z::kRows + t] = sum;
+          }
+          if (!meet(&s.first_team, first_phase)) return false;
+          if (row < rows) {
+            const float* const q = s_sums + row;
+            p.h_meta[(size_t)place_of(item, row) * (p.inner / kGroup) + slice] =
+                group_meta(exponent(row), q[0] + q[Z::kRows] + q[2 * Z::kRows] + q[3 * Z::kRows], BITS);
+          }
+        }
+        return meet(&s.teams, teams_phase);  // s_up and the rest may be written again
+      }
+    };
+    constexpr int kLag = Z::kBuffers - 1;  // steps from making A to adding up D
+    const int steps = end - begin;
+    int unit = begin / groups, g = begin - unit * groups;  // of the step that is added up
+    for (int n = 0; n < steps + kLag && ok; ++n) {
+      if (n < steps) {
+        const int stage = n % Z::kStages, buffer = n % Z::kBuffers;
+        if (!dev::mbar_wait_bounded(&s.weights[stage], (uint32_t)(n / Z::kStages) & 1u, limit)) {
+          failed();
+          ok = false;
+        }
+        if (__any_sync(~0u, !ok || gave_up())) {
+          ok = false;
+          break;
+        }
+        const uint8_t* const block = s_mem + (size_t)stage * Z::kStage + team * Z::kBlock;
+        const uint32_t at = my_tmem + buffer * (Z::kACols + Z::kDCols);
+        uint32_t a[32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint4 w4 = *reinterpret_cast<const uint4*>(block + w4_chunk_offset(c, quad, lane));
+          const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+          constexpr uint32_t flip = BITS == 4 ? 0x08080808u : 0u;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            a[c * 8 + 2 * j] = (w[j] & 0x0F0F0F0Fu) ^ flip;
+            a[c * 8 + 2 * j + 1] = (w[j] >> 4 & 0x0F0F0F0Fu) ^ flip;
+          }
+        }
+        tmem_store(at, a);
+        if (BITS == 6) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint2 u2 = *reinterpret_cast<const uint2*>(block + hi_chunk_offset(c, quad, lane));
+            const uint32_t u[2] = {u2.x, u2.y};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) a[c * 8 + j] = (u[j >> 2] >> (2 * (j & 3)) & 0x03030303u) ^ 0x02020202u;
+          }
+          tmem_store(at + 32, a);
+        }
+        tmem_wait_stores();
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) dev::mbar_arrive(&s.ready[team][buffer]);
+      }
+      if (n < kLag) continue;
+      const int k = n - kLag, stage = k % Z::kStages, buffer = k % Z::kBuffers;
+      if (!dev::mbar_wait_bounded(&s.done[team][buffer], (uint32_t)(k / Z::kBuffers) & 1u, limit)) {
+        failed();
+        ok = false;
+      }
+      if (__any_sync(~0u, !ok || gave_up())) {
+        ok = false;
+        break;
+      }
+      tmem_fence_after();
+      {
+        const uint8_t* const st = s_mem + (size_t)stage * Z::kStage;
+        const float scale = dev::half_bits_to_float(reinterpret_cast<const uint16_t*>(st + team * Z::kBlock)[scale_index(row)]);
+        const float4* const meta = reinterpret_cast<const float4*>(st + Z::kMeta);  // two rows each
+        const uint32_t at = my_tmem + buffer * (Z::kACols + Z::kDCols) + Z::kACols;
+#pragma unroll
+        for (int c = 0; c < N / 16; ++c) {
+          float d[16];
+          tmem_load16(at + 16 * c, d);
+          if (BITS == 6) {
+            float t[16];
+            tmem_load16(at + N + 16 * c, t);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) d[j] = fmaf(16.0f, t[j], d[j]);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float4 m = meta[c * 4 + j];
+            acc[c * 8 + 2 * j] = fmaf(scale * m.x, fmaf(0.0625f, d[4 * j + 1], d[4 * j] + m.y), acc[c * 8 + 2 * j]);
+            acc[c * 8 + 2 * j + 1] = fmaf(scale * m.z, fmaf(0.0625f, d[4 * j + 3], d[4 * j + 2] + m.w), acc[c * 8 + 2 * j + 1]);
+          }
+        }
+      }
+      tmem_fence_before();
+      __syncwarp();
+      if (lane == 0) dev::mbar_arrive(&s.empty[stage]);
+      if (++g < groups && k + 1 < steps) continue;
+
+      // The unit's last step here: complete, or a part of it.
+      ok = finish(unit);
+      if (!ok) break;
+#pragma unroll
+      for (int t = 0; t < Z::kRows; ++t) acc[t] = 0.0f;
+      ++unit;
+      g = 0;
+    }
+  }
+  __syncwarp();
+  tmem_fence_before();
+  __syncthreads();
+  if (warp == kIssuer) {
+    tmem_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kColumns) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+}
+
+template <int BITS, bool GATED, int N, bool FEW>
+inline cudaError_t launch_product(const Experts& p, int sms, cudaStream_t s) {
+  typedef Shape<BITS, N, FEW> Z;
+  const cudaError_t e = cudaFuncSetAttribute(product_kernel<BITS, GATED, N, FEW>, cudaFuncAttributeMaxDynamicSharedMemorySize, Z::kBytes);
+  if (e != cudaSuccess) return e;
+  return kv8::launch(product_kernel<BITS, GATED, N, FEW>, dim3((unsigned)sms), kThreads, Z::kBytes, s, p);
+}
+
+}  // namespace experts
+}  // namespace woq
