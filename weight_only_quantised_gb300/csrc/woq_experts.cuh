@@ -13,8 +13,10 @@
 //   - tcgen05.mma kind::f8f6f4 multiplies in fp32: D[128 rows of weights][2 columns a row], one per group, then
 //     acc += scale (D_high + D_low / 16 - 8 sum(x)) 2^e in fp32, a thread a row of weights.
 // Roles of a CTA (one per SM): two teams of four warps that make A from a block (shared memory -> registers -> tensor memory) and
-// add up D, one for gate and one for up (down: two neighbouring tiles); a warp that copies blocks (bulk copies, 8 KB each); a
-// thread that issues the products; two warps that bring B.
+// add up D, one for gate and one for up (down: two neighbouring tiles); a warp that copies blocks (bulk copies, 8 KB each); one
+// that issues the products; two that bring B; and four that take a pair's sums from the teams and finish it (3.5 us and
+// more of latency, during which the teams go on).  The copying and the issuing warp run as whole warps with one elected lane: from a
+// branch on the lane, two copies took 700 cycles and eight products 1,400.
 // The steps (a group of a pair of tiles of an item) are dealt out evenly to the CTAs; a pair that several share is finished
 // by the one that comes last, from all their sums in CTA order, and nobody waits for another CTA.
 #pragma once
@@ -36,8 +38,9 @@ namespace woq {
 namespace experts {
 
 constexpr int kTeamThreads = 128;
-constexpr int kProducer = 8, kIssuer = 9, kBringer = 10, kBringers = 2;  // warps 0 .. 7: the teams
-constexpr int kThreads = (kBringer + kBringers) * 32;
+// warps 0 .. 7: the teams
+constexpr int kProducer = 8, kIssuer = 9, kBringer = 10, kBringers = 2, kFinisher = 12, kFinishers = 4;
+constexpr int kThreads = (kFinisher + kFinishers) * 32;
 constexpr int kSmallEntries = kFewEntries;
 constexpr int kFewRows = 8;   // rows of an item then
 constexpr int kColumns = 512;       // of tensor memory
@@ -168,18 +171,20 @@ __device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t (&r)[32])
 }
 __device__ __forceinline__ void tmem_wait_stores() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Sixteen columns of the thread's row, complete.
-__device__ __forceinline__ void tmem_load16(uint32_t at, float (&d)[16]) {
-  uint32_t r[16];
+// Sixteen columns of the thread's row: there after tmem_loaded.
+__device__ __forceinline__ void tmem_load16(uint32_t at, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
         "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(at)
       : "memory");
-#pragma unroll
-  for (int i = 0; i < 16; ++i) d[i] = __uint_as_float(r[i]);
+}
+// Waits for every load of the thread; r: so that nothing uses them before.
+__device__ __forceinline__ void tmem_loaded(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]),
+                 "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
 }
 __device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -213,6 +218,11 @@ template <int N>
 __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+__device__ __forceinline__ bool elected() {
+  uint32_t one;
+  asm volatile("{.reg .pred p; elect.sync _|p, 0xFFFFFFFF; selp.b32 %0, 1, 0, p;}" : "=r"(one));
+  return one != 0;
+}
 __device__ __forceinline__ void fence_for_products() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // ---------------------------------------------------------------------------------------- products
@@ -226,8 +236,8 @@ struct Shape {
   static constexpr int kACols = BITS == 4 ? 32 : 64, kDCols = BITS == 4 ? N : 2 * N;
   static constexpr int kBuffers = 2 * 4 * (kACols + kDCols) <= kColumns ? 4 : 2;  // of A and D, a team
   static_assert(2 * kBuffers * (kACols + kDCols) <= kColumns, "tensor memory");
-  // [stages][exchange: up's values, then the warps' maxima and sums][barriers and flags][plan]
-  static constexpr int kExchange = kRows * kTeamThreads * 4 + 2 * 4 * kRows * 4;
+  // [stages][exchange: two units' sums, then the finishers' maxima and sums][barriers and flags][plan]
+  static constexpr int kSums = kRows * 256 * 4, kExchange = 2 * kSums + 2 * 4 * kRows * 4;
   static constexpr int kMisc = 1024;
   static constexpr int kPlan = FEW ? (int)((sizeof(Plan) + 127) / 128 * 128) : 0;
   static constexpr int kRoom = 227 * 1024 - kExchange - kMisc - kPlan;
@@ -239,7 +249,8 @@ struct Shape {
 struct Barriers {
   uint64_t weights[12], rows[12], empty[12];
   uint64_t ready[2][4], done[2][4];
-  uint64_t teams, first_team;  // where all warps of the teams (of the first) meet
+  uint64_t given[2], taken[2];  // a unit's sums, from the teams to the finishers
+  uint64_t finishers;           // where their warps meet
   uint32_t tmem;
   int fail, last;
 };
@@ -249,8 +260,8 @@ template <int BITS, bool GATED, int N, bool FEW>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
   typedef Shape<BITS, N, FEW> Z;
   extern __shared__ __align__(128) uint8_t s_mem[];
-  float* const s_up = reinterpret_cast<float*>(s_mem + Z::kStages * Z::kStage);
-  uint32_t* const s_most = reinterpret_cast<uint32_t*>(s_up + Z::kRows * kTeamThreads);
+  float* const s_unit = reinterpret_cast<float*>(s_mem + Z::kStages * Z::kStage);  // [2][rows][256]
+  uint32_t* const s_most = reinterpret_cast<uint32_t*>(s_unit + 2 * Z::kRows * 256);
   float* const s_sums = reinterpret_cast<float*>(s_most + 4 * Z::kRows);
   Barriers& s = *reinterpret_cast<Barriers*>(s_mem + Z::kStages * Z::kStage + Z::kExchange);
   Plan& plan = *reinterpret_cast<Plan*>(s_mem + Z::kStages * Z::kStage + Z::kExchange + Z::kMisc);
@@ -268,8 +279,11 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
         dev::mbar_init(&s.ready[w][i], 4);
         dev::mbar_init(&s.done[w][i], 1);
       }
-    dev::mbar_init(&s.teams, 8);
-    dev::mbar_init(&s.first_team, 4);
+    for (int i = 0; i < 2; ++i) {
+      dev::mbar_init(&s.given[i], 8);
+      dev::mbar_init(&s.taken[i], kFinishers);
+    }
+    dev::mbar_init(&s.finishers, kFinishers);
     s.fail = 0;
     dev::fence_mbar_init();
   }
@@ -292,9 +306,17 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
 
   const int K = GATED ? p.hidden : p.inner, groups = K / kGroup;
   const int tiles = GATED ? p.inner / kTileRows : p.hidden / kTileRows, slices = GATED ? tiles : (tiles + 1) / 2;
-  const int total = items * slices * groups;
+  const int units = items * slices, total = units * groups;
   const int ctas = total < (int)gridDim.x ? total : (int)gridDim.x, cta = blockIdx.x;
-  const int begin = cta < ctas ? (int)((long long)total * cta / ctas) : 0, end = cta < ctas ? (int)((long long)total * (cta + 1) / ctas) : 0;
+  int begin = cta < ctas ? (int)((long long)total * cta / ctas) : 0, end = cta < ctas ? (int)((long long)total * (cta + 1) / ctas) : 0;
+  // Whole units where the longest share is not much longer then: putting a unit together takes as long as some eight steps.
+  const int most_units = (units + (int)gridDim.x - 1) / (int)gridDim.x;
+  const bool whole = most_units * groups <= total / (int)gridDim.x + 8;
+  if (whole) {
+    const int g = (int)gridDim.x;
+    begin = (int)((long long)units * cta / g) * groups;
+    end = (int)((long long)units * (cta + 1) / g) * groups;
+  }
   const auto rows_of = [&](int item) { return FEW ? plan.rows[item] : p.item[item].rows; };
   const auto place_of = [&](int item, int row) { return FEW ? plan.place[item][row] : p.order[p.item[item].first + row]; };
   const auto failed = [&]() {
@@ -303,35 +325,44 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
     p.status[2] = 1;  // y is not written then
   };
   const auto gave_up = [&]() { return *(volatile int*)&s.fail != 0; };
+  // By whole warps: false once a wait has run out, here or elsewhere in the CTA.
+  const auto wait = [&](uint64_t* bar, uint32_t parity) {
+    bool ok = dev::mbar_try_wait(bar, parity);
+    if (!ok) {
+      const uint64_t t0 = dev::global_timer_ns();
+      while (!(ok = dev::mbar_try_wait(bar, parity)) && !gave_up())
+        if (dev::global_timer_ns() - t0 > limit) failed();
+    }
+    return (bool)__all_sync(~0u, ok);
+  };
 
   if (warp == kProducer) {
-    if (lane == 0 && begin < end) {
+    if (begin < end) {
       const uint8_t* const matrices = GATED ? p.gate_up : p.down;
       const size_t stride = GATED ? p.gate_up_stride : p.down_stride;
       int unit = begin / groups, g = begin - unit * groups, issued = 0;
-      const uint8_t* src[2];
+      const uint8_t *src0, *src1;
       const auto locate = [&]() {
         const int item = unit / slices, slice = unit - item * slices;
         const int expert = FEW ? plan.expert[item] : p.item[item].expert;
         const uint8_t* const m = matrices + (size_t)expert * stride + kHeaderBytes;
         const int t0 = GATED ? slice : 2 * slice, t1 = GATED ? slice + tiles : 2 * slice + 1;
-        src[0] = m + ((size_t)t0 * groups + g) * Z::kBlock;
-        src[1] = GATED || t1 < tiles ? m + ((size_t)t1 * groups + g) * Z::kBlock : nullptr;
+        src0 = m + ((size_t)t0 * groups + g) * Z::kBlock;
+        src1 = GATED || t1 < tiles ? m + ((size_t)t1 * groups + g) * Z::kBlock : nullptr;
       };
       locate();
       int stage = 0;
       uint32_t parity = 1;
       for (int i = begin; i < end; ++i) {
-        if (!dev::mbar_wait_bounded(&s.empty[stage], parity, limit)) {
-          failed();
-          break;
-        }
-        if (gave_up()) break;
-        uint8_t* const at = s_mem + (size_t)stage * Z::kStage;
+        if (!wait(&s.empty[stage], parity)) break;
         if (p.fault_cta != cta) {
-          dev::mbar_arrive_expect_tx(&s.weights[stage], src[1] ? 2 * Z::kBlock : Z::kBlock);
-          dev::bulk_copy_g2s(at, src[0], Z::kBlock, &s.weights[stage]);
-          if (src[1]) dev::bulk_copy_g2s(at + Z::kBlock, src[1], Z::kBlock, &s.weights[stage]);
+          if (elected()) {
+            uint8_t* const at = s_mem + (size_t)stage * Z::kStage;
+            dev::mbar_arrive_expect_tx(&s.weights[stage], src1 ? 2 * Z::kBlock : Z::kBlock);
+            dev::bulk_copy_g2s(at, src0, Z::kBlock, &s.weights[stage]);
+            if (src1) dev::bulk_copy_g2s(at + Z::kBlock, src1, Z::kBlock, &s.weights[stage]);
+          }
+          __syncwarp();
           ++issued;
         }
         if (++g == groups) {
@@ -339,82 +370,92 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
           ++unit;
           if (i + 1 < end) locate();
         } else {
-          src[0] += Z::kBlock;
-          if (src[1]) src[1] += Z::kBlock;
+          src0 += Z::kBlock;
+          if (src1) src1 += Z::kBlock;
         }
         if (++stage == Z::kStages) stage = 0, parity ^= 1;
       }
       // nothing may be in flight when the CTA ends, whatever went wrong
-      if (gave_up())
+      if (__any_sync(~0u, gave_up()))
         for (int n = issued > Z::kStages ? issued - Z::kStages : 0; n < issued; ++n)
           dev::mbar_wait_bounded(&s.weights[n % Z::kStages], (uint32_t)(n / Z::kStages) & 1u, limit);
     }
   } else if (warp == kIssuer) {
-    if (lane == 0) {
-      int stage = 0, buffer = 0;
-      uint32_t stage_parity = 0, buffer_parity = 0;
-      const uint32_t base = dev::smem_addr(s_mem);
-      bool ok = true;
-      int last = -1;            // the newest product's buffer, team and parity
-      for (int i = begin; i < end && ok; ++i) {
-        ok = dev::mbar_wait_bounded(&s.rows[stage], stage_parity, limit);
-        const uint64_t b = b_descriptor(base + stage * Z::kStage + Z::kB);
-        for (int w = 0; w < 2 && ok; ++w) {
-          ok = dev::mbar_wait_bounded(&s.ready[w][buffer], buffer_parity, limit);
-          if (!ok || gave_up()) {
-            ok = false;
-            break;
-          }
-          tmem_fence_after();
-          const uint32_t a = tmem + (w * Z::kBuffers + buffer) * (Z::kACols + Z::kDCols), d = a + Z::kACols;
+    int stage = 0, buffer = 0, last = -1;  // last: the newest product's buffer, team and parity
+    uint32_t stage_parity = 0, buffer_parity = 0;
+    const uint32_t base = dev::smem_addr(s_mem);
+    bool ok = true;
+    for (int i = begin; i < end && ok; ++i) {
+      ok = wait(&s.rows[stage], stage_parity);
+      const uint64_t b = b_descriptor(base + stage * Z::kStage + Z::kB);
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        ok = ok && wait(&s.ready[w][buffer], buffer_parity);
+        if (!ok) break;
+        tmem_fence_after();
+        const uint32_t a = tmem + (w * Z::kBuffers + buffer) * (Z::kACols + Z::kDCols), d = a + Z::kACols;
+        if (elected()) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) mma(d, a + 8 * k, b + k * (256 >> 4), kIdesc<N>, k > 0);
-          if (BITS == 6)
+          if (BITS == 6) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) mma(d + N, a + 32 + 8 * k, b + k * (256 >> 4), kIdesc<N>, k > 0);
+          }
           mma_commit(&s.done[w][buffer]);
-          last = (buffer * 2 + w) * 2 + (int)buffer_parity;
         }
-        if (++stage == Z::kStages) stage = 0, stage_parity ^= 1;
-        if (++buffer == Z::kBuffers) buffer = 0, buffer_parity ^= 1;
+        __syncwarp();
+        last = (buffer * 2 + w) * 2 + (int)buffer_parity;
       }
-      if (!ok) {
-        failed();
-        // products end in order: with the newest, all have
-        if (last >= 0) dev::mbar_wait_bounded(&s.done[last >> 1 & 1][last >> 2], (uint32_t)last & 1u, limit);
-      }
+      if (++stage == Z::kStages) stage = 0, stage_parity ^= 1;
+      if (++buffer == Z::kBuffers) buffer = 0, buffer_parity ^= 1;
     }
-  } else if (warp >= kBringer) {
+    // products end in order: with the newest, all have
+    if (!ok && last >= 0) dev::mbar_wait_bounded(&s.done[last >> 1 & 1][last >> 2], (uint32_t)last & 1u, limit);
+  } else if (warp >= kBringer && warp < kFinisher) {
     if (!GATED) dev::pdl_wait_prior_grids();  // h
-    // the two warps take the steps in turn
     const int me = warp - kBringer;
-    bool ok = true;
     const auto arrive = [&](int stage) {
       fence_for_products();
       __syncwarp();
       if (lane == 0) dev::mbar_arrive(&s.rows[stage]);
     };
-    const auto free_stage = [&](int n) {  // step n of this CTA
-      if (!dev::mbar_wait_bounded(&s.empty[n % Z::kStages], ((uint32_t)(n / Z::kStages) & 1u) ^ 1u, limit)) {
-        failed();
-        ok = false;
-      }
-      if (__any_sync(~0u, !ok || gave_up())) ok = false;
-      return ok;
-    };
+    const auto free_stage = [&](int n) { return wait(&s.empty[n % Z::kStages], ((uint32_t)(n / Z::kStages) & 1u) ^ 1u); };  // for step n of this CTA
     if constexpr (GATED && FEW) {
-      // lane 4 t + quarter: 32 elements of row t
-      const int t = lane >> 2, quarter = lane & 3;
-      uint4 v[4] = {};
-      const auto load = [&](int i) {
-        const int unit = i / groups, g = i - unit * groups, item = unit / slices;
-        const bool here = t < rows_of(item);
-        const uint4* src = reinterpret_cast<const uint4*>(p.x + (size_t)(here ? place_of(item, t) / p.k : 0) * K + g * kGroup + quarter * 32);
+      // Four lanes a row of a group, 32 elements each.  With fewer than 8 rows in an item the other lanes take the next groups, so that
+      // a warp is full: the warps take such runs of steps in turn.
+      const int slot = lane >> 2, quarter = lane & 3;
+      struct Run {
+        int first, steps, shift, rows;  // 2^shift >= rows
+      };
+      const auto run_at = [&](int i) {
+        Run r;
+        const int unit = i / groups, left = min((unit + 1) * groups, end) - i;
+        r.first = i;
+        r.rows = rows_of(unit / slices);
+        r.shift = r.rows > 4 ? 3 : r.rows > 2 ? 2 : r.rows > 1 ? 1 : 0;
+        r.steps = min(8 >> r.shift, left);
+        return r;
+      };
+      uint4 v[4];
+      const auto load = [&](const Run& r) {
+        const int t = slot & ((1 << r.shift) - 1), i = r.first + (slot >> r.shift), unit = i / groups, g = i - unit * groups;
+        const bool here = t < r.rows && (slot >> r.shift) < r.steps;
+        const uint4* src = reinterpret_cast<const uint4*>(p.x + (size_t)(here ? place_of(unit / slices, t) / p.k : 0) * K + g * kGroup + quarter * 32);
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = here ? src[j] : make_uint4(0u, 0u, 0u, 0u);
       };
-      if (begin + me < end) load(begin + me);
-      for (int i = begin + me; i < end && ok; i += kBringers) {
+      const auto next = [&](Run r) { return r.first + r.steps < end ? run_at(r.first + r.steps) : Run{end, 0, 0, 0}; };
+      Run r = begin < end ? run_at(begin) : Run{end, 0, 0, 0};
+      bool ok = true;
+      if (me) {
+        const Run other = r;
+        r = next(r);
+        if (r.first < end) load(r);
+        for (int j = 0; j < other.steps && ok; ++j) ok = free_stage(other.first + j - begin);
+      } else if (r.first < end) {
+        load(r);
+      }
+      while (r.first < end && ok) {
         const uint32_t x[16] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w,
                                 v[2].x, v[2].y, v[2].z, v[2].w, v[3].x, v[3].y, v[3].z, v[3].w};
         uint32_t m = most2(x[0], x[1]);
@@ -430,17 +471,29 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
         for (int j = 0; j < 8; ++j) halves4(x[2 * j], x[2 * j + 1], e, high[j], low[j], sum);
         sum += __shfl_xor_sync(~0u, sum, 1);
         sum += __shfl_xor_sync(~0u, sum, 2);
-        if (i + kBringers < end) load(i + kBringers);
-        const int n = i - begin, stage = n % Z::kStages;
-        if (!free_stage(n)) break;
-        uint8_t* const at = s_mem + (size_t)stage * Z::kStage + Z::kB + (t >> 2) * 1024 + (t & 3) * 32 + quarter * 256;
+        const Run now = r;
+        r = next(r);
+        const Run other = r;  // the other warp's
+        if (r.first < end) r = next(r);
+        if (r.first < end) load(r);
+        const int t = slot & ((1 << now.shift) - 1);
+        for (int j = 0; j < now.steps; ++j) {
+          const int n = now.first + j - begin, stage = n % Z::kStages;
+          if (!(ok = free_stage(n))) break;
+          if (slot >> now.shift == j) {
+            uint8_t* const st = s_mem + (size_t)stage * Z::kStage;
+            uint8_t* const at = st + Z::kB + (t >> 2) * 1024 + (t & 3) * 32 + quarter * 256;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          *reinterpret_cast<uint4*>(at + j * 128) = make_uint4(high[4 * j], high[4 * j + 1], high[4 * j + 2], high[4 * j + 3]);
-          *reinterpret_cast<uint4*>(at + j * 128 + 16) = make_uint4(low[4 * j], low[4 * j + 1], low[4 * j + 2], low[4 * j + 3]);
+            for (int c = 0; c < 2; ++c) {
+              *reinterpret_cast<uint4*>(at + c * 128) = make_uint4(high[4 * c], high[4 * c + 1], high[4 * c + 2], high[4 * c + 3]);
+              *reinterpret_cast<uint4*>(at + c * 128 + 16) = make_uint4(low[4 * c], low[4 * c + 1], low[4 * c + 2], low[4 * c + 3]);
+            }
+            if (quarter == 0) *reinterpret_cast<float2*>(st + Z::kMeta + t * 8) = group_meta(e, sum, BITS);
+          }
+          arrive(stage);
         }
-        if (quarter == 0) *reinterpret_cast<float2*>(s_mem + (size_t)stage * Z::kStage + Z::kMeta + t * 8) = group_meta(e, sum, BITS);
-        arrive(stage);
+        // Each stage's every phase is waited for, the other's too: a wait for a parity two phases ahead returns at once.
+        for (int j = 0; j < other.steps && ok; ++j) ok = free_stage(other.first + j - begin);
       }
     } else {
       // pieces of 16 bytes: piece lane & 15 of two rows at a time
@@ -452,8 +505,9 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
       size_t from[Z::kRows / 2];  // of rows 2 j + (lane >> 4)
       constexpr int kAhead = 2;   // copies of this many steps are under way
       int pending = 0;
+      bool ok = true;
       int i = begin + me;
-      for (; i < end && ok; i += kBringers) {
+      for (; i < end; i += kBringers) {
         const int u = i / groups, g = i - u * groups;
         if (u != unit) {
           unit = u;
@@ -467,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
           }
         }
         const int n = i - begin;
-        if (!free_stage(n)) break;
+        if (!(ok = free_stage(n))) break;
         const uint32_t at = base + (n % Z::kStages) * Z::kStage;
 #pragma unroll
         for (int j = 0; j < Z::kRows / 2; ++j) {
@@ -489,90 +543,78 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
       if (ok)
         for (; pending > 0; --pending) arrive((i - begin - pending * kBringers) % Z::kStages);
     }
-  } else {
-    // ------------------------------------------------------------------------------- the teams
-    if (!GATED) dev::pdl_wait_prior_grids();  // the sums of split pairs lie where the launch before had its own
-    const int team = warp >> 2, quad = warp & 3, row = quad * 32 + lane;  // row of the tile
-    const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-    const uint32_t my_tmem = tmem + lanes + team * Z::kBuffers * (Z::kACols + Z::kDCols);
-    float acc[Z::kRows] = {};
-    bool ok = true;
-    uint32_t teams_phase = 0, first_phase = 0;
-    const auto meet = [&](uint64_t* bar, uint32_t& phase) {  // false: something has failed, here or elsewhere
+  } else if (warp >= kFinisher) {
+    if (!GATED) dev::pdl_wait_prior_grids();  // the sums of split units lie where the launch before had its own
+    const int me = tid - kFinisher * 32, quad = warp - kFinisher;
+    uint32_t phase = 0;
+    const auto meet = [&]() {  // false: something has failed, here or elsewhere
       __syncwarp();
-      if (lane == 0) dev::mbar_arrive(bar);
-      const bool good = dev::mbar_wait_bounded(bar, phase, limit);
+      if (lane == 0) dev::mbar_arrive(&s.finishers);
       phase ^= 1;
-      if (!good) failed();
-      return !__any_sync(~0u, !good || gave_up());
+      return wait(&s.finishers, phase ^ 1);
     };
-    const auto finish = [&](int unit) {
-      const int first_step = unit * groups;
+    int n = 0;
+    for (int step = begin; step < end; ++n) {
+      const int unit = step / groups, first_step = unit * groups, buffer = n & 1;
+      step = first_step + groups;
+      float* const sums = s_unit + buffer * (Z::kRows * 256) + me;  // this thread's rows: me of the first tile, and of the second 128 on
+      if (!wait(&s.given[buffer], (uint32_t)(n >> 1) & 1u)) break;
+      const int item = unit / slices, slice = unit - item * slices, rows = rows_of(item);
       // the CTAs of the unit's first and last step
-      const int a = (int)(((long long)(first_step + 1) * ctas - 1) / total);
-      const int b = (int)(((long long)(first_step + groups) * ctas - 1) / total);
+      const int a = whole ? cta : (int)(((long long)(first_step + 1) * ctas - 1) / total);
+      const int b = whole ? cta : (int)(((long long)(first_step + groups) * ctas - 1) / total);
+      bool mine = true;
       if (a != b) {
-        const size_t words = (size_t)Z::kRows * 256;
-        float* const part = p.split_sums + ((size_t)cta * 2 + (first_step >= begin ? 1 : 0)) * words + tid;
-#pragma unroll
-        for (int j = 0; j < Z::kRows; ++j) __stcg(part + j * 256, acc[j]);
+        constexpr size_t kWords = (size_t)Z::kRows * 256;
+        float* const part = p.split_sums + ((size_t)cta * 2 + (first_step >= begin ? 1 : 0)) * kWords + me;
+        for (int i = 0; i < 2 * rows; ++i) __stcg(part + i * 128, sums[i * 128]);
         __threadfence();
-        if (!meet(&s.teams, teams_phase)) return false;
-        if (tid == 0) {
+        if (!meet()) break;
+        if (me == 0) {
           const uint32_t before = dev::atomic_add_acq_rel_gpu(p.split_counts + a, 1u);
           s.last = before == (uint32_t)(b - a);
           if (s.last) p.split_counts[a] = 0;
         }
-        if (!meet(&s.teams, teams_phase)) return false;
-        if (!s.last) return true;
-        __threadfence();
-#pragma unroll
-        for (int j = 0; j < Z::kRows; ++j) acc[j] = 0.0f;
-        for (int c = a; c <= b; ++c) {
-          const float* const from = p.split_sums + ((size_t)c * 2 + (c == a ? 1 : 0)) * words + tid;
-#pragma unroll
-          for (int j = 0; j < Z::kRows; ++j) acc[j] += __ldcg(from + j * 256);
+        if (!meet()) break;
+        mine = s.last;
+        if (mine) {
+          __threadfence();
+          for (int i = 0; i < 2 * rows; ++i) {
+            float v = 0.0f;
+            for (int c = a; c <= b; ++c) v += __ldcg(p.split_sums + ((size_t)c * 2 + (c == a ? 1 : 0)) * kWords + me + i * 128);
+            sums[i * 128] = v;
+          }
         }
       }
-      const int item = unit / slices, slice = unit - item * slices, rows = rows_of(item);
       // codes were taken as 2^-9 of themselves
-      if constexpr (!GATED) {
-        const int tile = 2 * slice + team;
-        if (tile < tiles) {
-#pragma unroll
-          for (int t = 0; t < Z::kRows; ++t)
-            if (t < rows) p.parts[(size_t)place_of(item, t) * p.hidden + tile * kTileRows + row] = 512.0f * acc[t];
-        }
-        return true;
-      } else {
-        // h = silu(gate) up: the second team's sums go to the first, which has the group of 128 of each row and takes it apart
-        if (team == 1) {
-#pragma unroll
-          for (int t = 0; t < Z::kRows; ++t) s_up[t * kTeamThreads + row] = 512.0f * acc[t];
-        }
-        if (!meet(&s.teams, teams_phase)) return false;
-        if (team == 0) {
-#pragma unroll
-          for (int t = 0; t < Z::kRows; ++t) {
-            const float v = 512.0f * acc[t];
-            acc[t] = v / (1.0f + expf(-v)) * s_up[t * kTeamThreads + row];
-            const uint32_t m = __reduce_max_sync(~0u, __float_as_uint(acc[t]) & 0x7FFFFFFFu);
+      if (mine) {
+        if constexpr (!GATED) {
+          const bool second = 2 * slice + 1 < tiles;
+          for (int t = 0; t < rows; ++t) {
+            float* const to = p.parts + (size_t)place_of(item, t) * p.hidden + 2 * slice * kTileRows + me;
+            to[0] = 512.0f * sums[t * 256];
+            if (second) to[kTileRows] = 512.0f * sums[t * 256 + 128];
+          }
+        } else {
+          // h = silu(gate) up of 128 neighbouring elements of each row: a group of down's, taken apart here
+          for (int t = 0; t < rows; ++t) {
+            const float v = 512.0f * sums[t * 256], h = v / (1.0f + expf(-v)) * (512.0f * sums[t * 256 + 128]);
+            sums[t * 256] = h;
+            const uint32_t m = __reduce_max_sync(~0u, __float_as_uint(h) & 0x7FFFFFFFu);
             if (lane == 0) s_most[quad * Z::kRows + t] = m;
           }
-          if (!meet(&s.first_team, first_phase)) return false;
+          if (!meet()) break;
           const auto exponent = [&](int t) {
             const uint32_t* const m = s_most + t;
             return group_exponent(max(max(m[0], m[Z::kRows]), max(m[2 * Z::kRows], m[3 * Z::kRows])) >> 23);
           };
-#pragma unroll
-          for (int t = 0; t < Z::kRows; ++t) {
-            if (t >= rows) break;
-            const float v = acc[t] * group_factor(exponent(t));
+          for (int t = 0; t < rows; ++t) {
+            const float v = sums[t * 256] * group_factor(exponent(t));
             const uint16_t high = e4m3x2(v, 0.0f);
             uint32_t back;
             asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(high));
             const uint16_t low = e4m3x2((v - dev::half_bits_to_float(back & 0xFFFFu)) * 16.0f, 0.0f);
-            uint8_t* const to = p.h_halves + ((size_t)place_of(item, t) * (p.inner / kGroup) + slice) * 256 + (row >> 4) * 32 + (row & 15);
+            uint8_t* const to = p.h_halves + ((size_t)place_of(item, t) * (p.inner / kGroup) + slice) * 256 + (me >> 4) * 32 + (me & 15);
             to[0] = (uint8_t)high;
             to[16] = (uint8_t)low;
             float sum = v;
@@ -580,33 +622,53 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
             for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
             if (lane == 0) s_sums[quad * Z::kRows + t] = sum;
           }
-          if (!meet(&s.first_team, first_phase)) return false;
-          if (row < rows) {
-            const float* const q = s_sums + row;
-            p.h_meta[(size_t)place_of(item, row) * (p.inner / kGroup) + slice] =
-                group_meta(exponent(row), q[0] + q[Z::kRows] + q[2 * Z::kRows] + q[3 * Z::kRows], BITS);
+          if (!meet()) break;
+          if (me < rows) {
+            const float* const q = s_sums + me;
+            p.h_meta[(size_t)place_of(item, me) * (p.inner / kGroup) + slice] =
+                group_meta(exponent(me), q[0] + q[Z::kRows] + q[2 * Z::kRows] + q[3 * Z::kRows], BITS);
           }
+          if (!meet()) break;  // the maxima and sums may be written again
         }
-        return meet(&s.teams, teams_phase);  // s_up and the rest may be written again
       }
-    };
+      __syncwarp();
+      if (lane == 0) dev::mbar_arrive(&s.taken[buffer]);
+    }
+  } else {
+    // ------------------------------------------------------------------------------- the teams
+    const int team = warp >> 2, quad = warp & 3, row = quad * 32 + lane;  // row of the tile
+    const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+    const uint32_t my_tmem = tmem + lanes + team * Z::kBuffers * (Z::kACols + Z::kDCols);
+    float acc[Z::kRows] = {};
     constexpr int kLag = Z::kBuffers - 1;  // steps from making A to adding up D
+    // With four buffers nothing is waited for as soon as it is begun: a step's D is on its way while the next block becomes A, and
+    // that A's store while D is added up; the products learn of it a step later.
+    constexpr bool kDefer = Z::kBuffers == 4;
     const int steps = end - begin;
-    int unit = begin / groups, g = begin - unit * groups;  // of the step that is added up
-    for (int n = 0; n < steps + kLag && ok; ++n) {
+    int g = begin % groups, unit_buffer = 0;  // of the step that is added up
+    uint32_t unit_parity = 0;
+    int stage = 0, buffer = 0, added_stage = 0, added_buffer = 0, stored = -1;
+    uint32_t parity = 0, added_parity = 0;
+    const auto announce = [&]() {  // the A that was stored last
+      tmem_wait_stores();
+      tmem_fence_before();
+      __syncwarp();
+      if (lane == 0) dev::mbar_arrive(&s.ready[team][stored]);
+      stored = -1;
+    };
+    for (int n = 0; n < steps + kLag; ++n) {
+      uint32_t a[32], top[BITS == 6 ? 32 : 1], d[16], d2[16];
+      const bool adds = n >= kLag;
+      const uint32_t added_at = my_tmem + added_buffer * (Z::kACols + Z::kDCols) + Z::kACols;
+      if (kDefer && adds) {
+        if (!wait(&s.done[team][added_buffer], added_parity)) break;
+        tmem_fence_after();
+        tmem_load16(added_at, d);
+        if (BITS == 6) tmem_load16(added_at + N, d2);
+      }
       if (n < steps) {
-        const int stage = n % Z::kStages, buffer = n % Z::kBuffers;
-        if (!dev::mbar_wait_bounded(&s.weights[stage], (uint32_t)(n / Z::kStages) & 1u, limit)) {
-          failed();
-          ok = false;
-        }
-        if (__any_sync(~0u, !ok || gave_up())) {
-          ok = false;
-          break;
-        }
+        if (!wait(&s.weights[stage], parity)) break;
         const uint8_t* const block = s_mem + (size_t)stage * Z::kStage + team * Z::kBlock;
-        const uint32_t at = my_tmem + buffer * (Z::kACols + Z::kDCols);
-        uint32_t a[32];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const uint4 w4 = *reinterpret_cast<const uint4*>(block + w4_chunk_offset(c, quad, lane));
@@ -617,68 +679,76 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
             a[c * 8 + 2 * j] = (w[j] & 0x0F0F0F0Fu) ^ flip;
             a[c * 8 + 2 * j + 1] = (w[j] >> 4 & 0x0F0F0F0Fu) ^ flip;
           }
-        }
-        tmem_store(at, a);
-        if (BITS == 6) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          if constexpr (BITS == 6) {
             const uint2 u2 = *reinterpret_cast<const uint2*>(block + hi_chunk_offset(c, quad, lane));
             const uint32_t u[2] = {u2.x, u2.y};
 #pragma unroll
-            for (int j = 0; j < 8; ++j) a[c * 8 + j] = (u[j >> 2] >> (2 * (j & 3)) & 0x03030303u) ^ 0x02020202u;
+            for (int j = 0; j < 8; ++j) top[c * 8 + j] = (u[j >> 2] >> (2 * (j & 3)) & 0x03030303u) ^ 0x02020202u;
           }
-          tmem_store(at + 32, a);
         }
-        tmem_wait_stores();
-        tmem_fence_before();
-        __syncwarp();
-        if (lane == 0) dev::mbar_arrive(&s.ready[team][buffer]);
+        if (++stage == Z::kStages) stage = 0, parity ^= 1;
       }
-      if (n < kLag) continue;
-      const int k = n - kLag, stage = k % Z::kStages, buffer = k % Z::kBuffers;
-      if (!dev::mbar_wait_bounded(&s.done[team][buffer], (uint32_t)(k / Z::kBuffers) & 1u, limit)) {
-        failed();
-        ok = false;
-      }
-      if (__any_sync(~0u, !ok || gave_up())) {
-        ok = false;
-        break;
-      }
-      tmem_fence_after();
-      {
-        const uint8_t* const st = s_mem + (size_t)stage * Z::kStage;
+      if (kDefer && stored >= 0) announce();
+      const auto add = [&]() {
+        const uint8_t* const st = s_mem + (size_t)added_stage * Z::kStage;
         const float scale = dev::half_bits_to_float(reinterpret_cast<const uint16_t*>(st + team * Z::kBlock)[scale_index(row)]);
         const float4* const meta = reinterpret_cast<const float4*>(st + Z::kMeta);  // two rows each
-        const uint32_t at = my_tmem + buffer * (Z::kACols + Z::kDCols) + Z::kACols;
 #pragma unroll
         for (int c = 0; c < N / 16; ++c) {
-          float d[16];
-          tmem_load16(at + 16 * c, d);
+          if (!kDefer || c > 0) {
+            tmem_load16(added_at + 16 * c, d);
+            if (BITS == 6) tmem_load16(added_at + N + 16 * c, d2);
+          }
+          tmem_loaded(d);
           if (BITS == 6) {
-            float t[16];
-            tmem_load16(at + N + 16 * c, t);
+            tmem_loaded(d2);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) d[j] = fmaf(16.0f, t[j], d[j]);
+            for (int j = 0; j < 16; ++j) d[j] = __float_as_uint(fmaf(16.0f, __uint_as_float(d2[j]), __uint_as_float(d[j])));
           }
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const float4 m = meta[c * 4 + j];
-            acc[c * 8 + 2 * j] = fmaf(scale * m.x, fmaf(0.0625f, d[4 * j + 1], d[4 * j] + m.y), acc[c * 8 + 2 * j]);
-            acc[c * 8 + 2 * j + 1] = fmaf(scale * m.z, fmaf(0.0625f, d[4 * j + 3], d[4 * j + 2] + m.w), acc[c * 8 + 2 * j + 1]);
+            const float t0 = fmaf(0.0625f, __uint_as_float(d[4 * j + 1]), __uint_as_float(d[4 * j]) + m.y);
+            const float t1 = fmaf(0.0625f, __uint_as_float(d[4 * j + 3]), __uint_as_float(d[4 * j + 2]) + m.w);
+            acc[c * 8 + 2 * j] = fmaf(scale * m.x, t0, acc[c * 8 + 2 * j]);
+            acc[c * 8 + 2 * j + 1] = fmaf(scale * m.z, t1, acc[c * 8 + 2 * j + 1]);
           }
         }
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) dev::mbar_arrive(&s.empty[added_stage]);
+      };
+      if (kDefer && adds) add();
+      if (n < steps) {
+        const uint32_t at = my_tmem + buffer * (Z::kACols + Z::kDCols);
+        tmem_store(at, a);
+        if constexpr (BITS == 6) tmem_store(at + 32, top);
+        stored = buffer;
+        if (++buffer == Z::kBuffers) buffer = 0;
+        if (!kDefer) announce();
       }
-      tmem_fence_before();
-      __syncwarp();
-      if (lane == 0) dev::mbar_arrive(&s.empty[stage]);
-      if (++g < groups && k + 1 < steps) continue;
+      if (!adds) continue;
+      if (!kDefer) {
+        if (!wait(&s.done[team][added_buffer], added_parity)) break;
+        tmem_fence_after();
+        add();
+      }
+      if (++added_stage == Z::kStages) added_stage = 0;
+      if (++added_buffer == Z::kBuffers) added_buffer = 0, added_parity ^= 1;
+      if (++g < groups && n + 1 < steps + kLag) continue;
 
-      // The unit's last step here: complete, or a part of it.
-      ok = finish(unit);
-      if (!ok) break;
+      // The unit's last step here: the sums go to the finishers.
+      if (!wait(&s.taken[unit_buffer], unit_parity ^ 1u)) break;
+      float* const to = s_unit + unit_buffer * (Z::kRows * 256) + tid;
 #pragma unroll
-      for (int t = 0; t < Z::kRows; ++t) acc[t] = 0.0f;
-      ++unit;
+      for (int t = 0; t < Z::kRows; ++t) {
+        to[t * 256] = acc[t];
+        acc[t] = 0.0f;
+      }
+      __syncwarp();
+      if (lane == 0) dev::mbar_arrive(&s.given[unit_buffer]);
+      unit_buffer ^= 1;
+      if (!unit_buffer) unit_parity ^= 1;
       g = 0;
     }
   }
