@@ -23,7 +23,7 @@ struct ExpertsLayout {
 void choose_items(int E, size_t n, ExpertsLayout* l) {
   const double rows = n / (E * (1.0 - pow(1.0 - 1.0 / E, (double)n)));
   l->few = n <= (size_t)kFewEntries && rows <= 6.0;
-  l->item_rows = rows <= 6.0 ? 8 : rows <= 12.0 ? 16 : 32;
+  l->item_rows = rows <= 6.0 ? 8 : 16;
 }
 
 bool experts_layout(int E, int T, int k, int H, int I, ExpertsLayout* l) {
@@ -166,7 +166,7 @@ int woq_experts_swiglu(int bits, int E, const void* gate_up, size_t gate_up_byte
   a.inner = I;
   a.entries = T * k;
   a.few = l.few;
-  a.item_rows = bits == 6 && l.item_rows > 16 ? 16 : l.item_rows;  // int6 has two sums a column: tensor memory holds those of 16 rows
+  a.item_rows = l.item_rows;
   a.wait_ns = wait_bound_ns();
   a.fault_cta = fault_cta(1);
   a.status = reinterpret_cast<uint32_t*>(w);

@@ -12,10 +12,10 @@
 //     2^-17 of it.  h is taken apart the same way from fp32, with one rounding to about 8 bits (2^-8 at most).
 //   - tcgen05.mma kind::f8f6f4 multiplies in fp32: D[128 rows of weights][2 columns a row], one per group, then
 //     acc += scale (D_high + D_low / 16 - 8 sum(x)) 2^e in fp32, a thread a row of weights.
-// Roles of a CTA (one per SM): two teams of four warps that make A from a block (shared memory -> registers -> tensor memory) and
-// add up D, one for gate and one for up (down: two neighbouring tiles); a warp that copies blocks (bulk copies, 8 KB each); one
-// that issues the products; two that bring B; and four that take a pair's sums from the teams and finish it (3.5 us and
-// more of latency, during which the teams go on).  The copying and the issuing warp run as whole warps with one elected lane: from a
+// Roles of a CTA (one per SM): two pairs of teams of four warps that make A from a block (shared memory -> registers -> tensor memory)
+// and add up D, in each pair one for gate and one for up (down: two neighbouring tiles), the pairs in turn (a step takes a team 1,200 cycles of
+// latency, a block's bytes 380); a warp that copies blocks (bulk copies, 8 KB each); one that issues the products; two that bring
+// B; and four that take a unit's sums from the teams and finish it (3.5 us and more of latency, during which the teams go on).  The copying and the issuing warp run as whole warps with one elected lane: from a
 // branch on the lane, two copies took 700 cycles and eight products 1,400.
 // The steps (a group of a pair of tiles of an item) are dealt out evenly to the CTAs; a pair that several share is finished
 // by the one that comes last, from all their sums in CTA order, and nobody waits for another CTA.
@@ -38,8 +38,8 @@ namespace woq {
 namespace experts {
 
 constexpr int kTeamThreads = 128;
-// warps 0 .. 7: the teams
-constexpr int kProducer = 8, kIssuer = 9, kBringer = 10, kBringers = 2, kFinisher = 12, kFinishers = 4;
+// warps 0 .. 15: the teams
+constexpr int kProducer = 16, kIssuer = 17, kBringer = 18, kBringers = 2, kFinisher = 20, kFinishers = 4;
 constexpr int kThreads = (kFinisher + kFinishers) * 32;
 constexpr int kSmallEntries = kFewEntries;
 constexpr int kFewRows = 8;   // rows of an item then
@@ -159,14 +159,11 @@ __device__ __forceinline__ void plan_here(const Experts& p, Plan& s) {
 
 // ----------------------------------------------------------------------------------- tensor memory
 
-__device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, "
-      "%19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(at),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(at),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
-      "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
-      "r"(r[31])
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_stores() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -234,22 +231,24 @@ struct Shape {
   static constexpr int kBlock = BITS == 4 ? kBlockBytesW4 : kBlockBytesW6;
   static constexpr int kB = 2 * kBlock, kMeta = kB + N * 128, kStage = (kMeta + kRows * 8 + 127) / 128 * 128;
   static constexpr int kACols = BITS == 4 ? 32 : 64, kDCols = BITS == 4 ? N : 2 * N;
-  static constexpr int kBuffers = 2 * 4 * (kACols + kDCols) <= kColumns ? 4 : 2;  // of A and D, a team
-  static_assert(2 * kBuffers * (kACols + kDCols) <= kColumns, "tensor memory");
-  // [stages][exchange: two units' sums, then the finishers' maxima and sums][barriers and flags][plan]
-  static constexpr int kSums = kRows * 256 * 4, kExchange = 2 * kSums + 2 * 4 * kRows * 4;
+  static constexpr int kBuffers = kColumns / 4 / (kACols + kDCols);  // of A and D, a team
+  static_assert(kBuffers == 1 || kBuffers == 2, "tensor memory");
+  // [stages][exchange: units' sums by pairs, then the finishers' maxima and sums][barriers and flags][plan]
+  static constexpr int kUnits = N == 16 ? 2 : 1;  // units' sums that there is room for
+  static constexpr int kExchange = kUnits * 2 * kRows * 256 * 4 + 2 * 4 * kRows * 4;
   static constexpr int kMisc = 1024;
   static constexpr int kPlan = FEW ? (int)((sizeof(Plan) + 127) / 128 * 128) : 0;
   static constexpr int kRoom = 227 * 1024 - kExchange - kMisc - kPlan;
-  static constexpr int kStages = kRoom / kStage < 12 ? kRoom / kStage : 12;
-  static_assert(kStages >= kBuffers + 2, "a stage is held until its sums are taken");
+  // An even number, so that a stage always serves the same pair: a wait for a parity two phases ahead returns at once.
+  static constexpr int kStages = (kRoom / kStage < 12 ? kRoom / kStage : 12) / 2 * 2;
+  static_assert(kStages >= 2 * kBuffers + 2, "a stage is held until its sums are taken");
   static constexpr int kBytes = kStages * kStage + kExchange + kMisc + kPlan;
 };
 
 struct Barriers {
-  uint64_t weights[12], rows[12], empty[12];
-  uint64_t ready[2][4], done[2][4];
-  uint64_t given[2], taken[2];  // a unit's sums, from the teams to the finishers
+  uint64_t weights[12], operands[12], empty[12];  // operands: a step's B (one arrival) and its two A (eight)
+  uint64_t done[2][2];                             // a pair's products
+  uint64_t given[2][2], taken[2][2];  // a pair's sums of a unit, to the finishers
   uint64_t finishers;           // where their warps meet
   uint32_t tmem;
   int fail, last;
@@ -260,8 +259,8 @@ template <int BITS, bool GATED, int N, bool FEW>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
   typedef Shape<BITS, N, FEW> Z;
   extern __shared__ __align__(128) uint8_t s_mem[];
-  float* const s_unit = reinterpret_cast<float*>(s_mem + Z::kStages * Z::kStage);  // [2][rows][256]
-  uint32_t* const s_most = reinterpret_cast<uint32_t*>(s_unit + 2 * Z::kRows * 256);
+  float* const s_unit = reinterpret_cast<float*>(s_mem + Z::kStages * Z::kStage);  // [units][pair][rows][256]
+  uint32_t* const s_most = reinterpret_cast<uint32_t*>(s_unit + Z::kUnits * 2 * Z::kRows * 256);
   float* const s_sums = reinterpret_cast<float*>(s_most + 4 * Z::kRows);
   Barriers& s = *reinterpret_cast<Barriers*>(s_mem + Z::kStages * Z::kStage + Z::kExchange);
   Plan& plan = *reinterpret_cast<Plan*>(s_mem + Z::kStages * Z::kStage + Z::kExchange + Z::kMisc);
@@ -271,17 +270,13 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
   if (tid == 0) {
     for (int i = 0; i < Z::kStages; ++i) {
       dev::mbar_init(&s.weights[i], 1);
-      dev::mbar_init(&s.rows[i], 1);
+      dev::mbar_init(&s.operands[i], 9);
       dev::mbar_init(&s.empty[i], 8);
     }
-    for (int w = 0; w < 2; ++w)
-      for (int i = 0; i < Z::kBuffers; ++i) {
-        dev::mbar_init(&s.ready[w][i], 4);
-        dev::mbar_init(&s.done[w][i], 1);
-      }
-    for (int i = 0; i < 2; ++i) {
-      dev::mbar_init(&s.given[i], 8);
-      dev::mbar_init(&s.taken[i], kFinishers);
+    for (int i = 0; i < 4; ++i) dev::mbar_init(&s.done[i >> 1][i & 1], 1);
+    for (int i = 0; i < 4; ++i) {
+      dev::mbar_init(&s.given[i >> 1][i & 1], 8);
+      dev::mbar_init(&s.taken[i >> 1][i & 1], kFinishers);
     }
     dev::mbar_init(&s.finishers, kFinishers);
     s.fail = 0;
@@ -325,13 +320,17 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
     p.status[2] = 1;  // y is not written then
   };
   const auto gave_up = [&]() { return *(volatile int*)&s.fail != 0; };
-  // By whole warps: false once a wait has run out, here or elsewhere in the CTA.
+  // By whole warps: false once a wait has run out, here or elsewhere in the CTA.  Warps that run ahead or behind sleep a little between
+  // tries: with 23 warps that try all the time, a wait that is over at once takes 72 cycles instead of 16.
+  const bool sleeps = warp == kProducer || warp >= kBringer;
   const auto wait = [&](uint64_t* bar, uint32_t parity) {
     bool ok = dev::mbar_try_wait(bar, parity);
     if (!ok) {
       const uint64_t t0 = dev::global_timer_ns();
-      while (!(ok = dev::mbar_try_wait(bar, parity)) && !gave_up())
+      while (!(ok = dev::mbar_try_wait(bar, parity)) && !gave_up()) {
+        if (sleeps) __nanosleep(40);
         if (dev::global_timer_ns() - t0 > limit) failed();
+      }
     }
     return (bool)__all_sync(~0u, ok);
   };
@@ -381,43 +380,40 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
           dev::mbar_wait_bounded(&s.weights[n % Z::kStages], (uint32_t)(n / Z::kStages) & 1u, limit);
     }
   } else if (warp == kIssuer) {
-    int stage = 0, buffer = 0, last = -1;  // last: the newest product's buffer, team and parity
-    uint32_t stage_parity = 0, buffer_parity = 0;
+    int stage = 0, last = -1;  // last: the newest products' pair, buffer and parity
+    uint32_t stage_parity = 0;
     const uint32_t base = dev::smem_addr(s_mem);
-    bool ok = true;
-    for (int i = begin; i < end && ok; ++i) {
-      ok = wait(&s.rows[stage], stage_parity);
+    for (int i = 0; i < end - begin; ++i) {
+      if (!wait(&s.operands[stage], stage_parity)) break;
+      tmem_fence_after();
       const uint64_t b = b_descriptor(base + stage * Z::kStage + Z::kB);
+      const int pair = i & 1, turn = i >> 1, buffer = turn % Z::kBuffers;
+      if (elected()) {
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        ok = ok && wait(&s.ready[w][buffer], buffer_parity);
-        if (!ok) break;
-        tmem_fence_after();
-        const uint32_t a = tmem + (w * Z::kBuffers + buffer) * (Z::kACols + Z::kDCols), d = a + Z::kACols;
-        if (elected()) {
+        for (int w = 0; w < 2; ++w) {
+          const uint32_t a = tmem + ((pair * 2 + w) * Z::kBuffers + buffer) * (Z::kACols + Z::kDCols), d = a + Z::kACols;
 #pragma unroll
           for (int k = 0; k < 4; ++k) mma(d, a + 8 * k, b + k * (256 >> 4), kIdesc<N>, k > 0);
           if (BITS == 6) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) mma(d + N, a + 32 + 8 * k, b + k * (256 >> 4), kIdesc<N>, k > 0);
           }
-          mma_commit(&s.done[w][buffer]);
         }
-        __syncwarp();
-        last = (buffer * 2 + w) * 2 + (int)buffer_parity;
+        mma_commit(&s.done[pair][buffer]);
       }
+      __syncwarp();
+      last = (pair * 2 + buffer) * 2 + (turn / Z::kBuffers & 1);
       if (++stage == Z::kStages) stage = 0, stage_parity ^= 1;
-      if (++buffer == Z::kBuffers) buffer = 0, buffer_parity ^= 1;
     }
     // products end in order: with the newest, all have
-    if (!ok && last >= 0) dev::mbar_wait_bounded(&s.done[last >> 1 & 1][last >> 2], (uint32_t)last & 1u, limit);
+    if (__any_sync(~0u, gave_up()) && last >= 0) dev::mbar_wait_bounded(&s.done[last >> 2][last >> 1 & 1], (uint32_t)last & 1u, limit);
   } else if (warp >= kBringer && warp < kFinisher) {
     if (!GATED) dev::pdl_wait_prior_grids();  // h
     const int me = warp - kBringer;
     const auto arrive = [&](int stage) {
       fence_for_products();
       __syncwarp();
-      if (lane == 0) dev::mbar_arrive(&s.rows[stage]);
+      if (lane == 0) dev::mbar_arrive(&s.operands[stage]);
     };
     const auto free_stage = [&](int n) { return wait(&s.empty[n % Z::kStages], ((uint32_t)(n / Z::kStages) & 1u) ^ 1u); };  // for step n of this CTA
     if constexpr (GATED && FEW) {
@@ -553,16 +549,30 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
       phase ^= 1;
       return wait(&s.finishers, phase ^ 1);
     };
-    int n = 0;
-    for (int step = begin; step < end; ++n) {
-      const int unit = step / groups, first_step = unit * groups, buffer = n & 1;
-      step = first_step + groups;
-      float* const sums = s_unit + buffer * (Z::kRows * 256) + me;  // this thread's rows: me of the first tile, and of the second 128 on
-      if (!wait(&s.given[buffer], (uint32_t)(n >> 1) & 1u)) break;
+    int turns[2] = {0, 0};  // units that each pair has given
+    for (int step = begin; step < end;) {
+      const int unit = step / groups, first_step = unit * groups, last_step = min(first_step + groups, end);
+      // a pair that had a step of it
+      const bool gave[2] = {last_step - step > 1 || !((step - begin) & 1), last_step - step > 1 || ((step - begin) & 1)};
+      int buffer[2];
+      bool ok = true;
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        buffer[w] = turns[w] % Z::kUnits;
+        if (gave[w]) ok = ok && wait(&s.given[buffer[w]][w], (uint32_t)(turns[w] / Z::kUnits) & 1u);
+      }
+      if (!ok) break;
+      step = last_step;
+      // this thread's rows: me of the first tile, and of the second 128 on
+      float* const sums0 = s_unit + (buffer[0] * 2) * (Z::kRows * 256) + me;
+      float* const sums1 = s_unit + (buffer[1] * 2 + 1) * (Z::kRows * 256) + me;
+      float* const sums = gave[0] ? sums0 : sums1;
       const int item = unit / slices, slice = unit - item * slices, rows = rows_of(item);
       // the CTAs of the unit's first and last step
       const int a = whole ? cta : (int)(((long long)(first_step + 1) * ctas - 1) / total);
       const int b = whole ? cta : (int)(((long long)(first_step + groups) * ctas - 1) / total);
+      if (gave[0] && gave[1])
+        for (int i = 0; i < 2 * rows; ++i) sums[i * 128] += sums1[i * 128];
       bool mine = true;
       if (a != b) {
         constexpr size_t kWords = (size_t)Z::kRows * 256;
@@ -632,75 +642,82 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
         }
       }
       __syncwarp();
-      if (lane == 0) dev::mbar_arrive(&s.taken[buffer]);
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+        if (gave[w]) {
+          if (lane == 0) dev::mbar_arrive(&s.taken[buffer[w]][w]);
+          ++turns[w];
+        }
     }
   } else {
     // ------------------------------------------------------------------------------- the teams
-    const int team = warp >> 2, quad = warp & 3, row = quad * 32 + lane;  // row of the tile
-    const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-    const uint32_t my_tmem = tmem + lanes + team * Z::kBuffers * (Z::kACols + Z::kDCols);
+    const int team = warp >> 2, pair = team >> 1, side = team & 1, quad = warp & 3, row = quad * 32 + lane;  // row of the tile
+    const uint32_t my_tmem = tmem + ((uint32_t)(quad * 32) << 16) + team * Z::kBuffers * (Z::kACols + Z::kDCols);
     float acc[Z::kRows] = {};
-    constexpr int kLag = Z::kBuffers - 1;  // steps from making A to adding up D
-    // With four buffers nothing is waited for as soon as it is begun: a step's D is on its way while the next block becomes A, and
-    // that A's store while D is added up; the products learn of it a step later.
-    constexpr bool kDefer = Z::kBuffers == 4;
-    const int steps = end - begin;
-    int g = begin % groups, unit_buffer = 0;  // of the step that is added up
+    constexpr int kLag = Z::kBuffers - 1;  // the pair's steps from making A to adding up D
+    const int steps = end - begin > pair ? (end - begin - pair + 1) / 2 : 0;  // the pair's: every other one
+    int g = (begin + pair) % groups, unit_buffer = 0;                         // of the step that is added up
     uint32_t unit_parity = 0;
-    int stage = 0, buffer = 0, added_stage = 0, added_buffer = 0, stored = -1;
+    int stage = pair, stored = 0, added_stage = pair, buffer = 0, added_buffer = 0;
     uint32_t parity = 0, added_parity = 0;
-    const auto announce = [&]() {  // the A that was stored last
-      tmem_wait_stores();
-      tmem_fence_before();
-      __syncwarp();
-      if (lane == 0) dev::mbar_arrive(&s.ready[team][stored]);
-      stored = -1;
-    };
     for (int n = 0; n < steps + kLag; ++n) {
-      uint32_t a[32], top[BITS == 6 ? 32 : 1], d[16], d2[16];
-      const bool adds = n >= kLag;
-      const uint32_t added_at = my_tmem + added_buffer * (Z::kACols + Z::kDCols) + Z::kACols;
-      if (kDefer && adds) {
-        if (!wait(&s.done[team][added_buffer], added_parity)) break;
-        tmem_fence_after();
-        tmem_load16(added_at, d);
-        if (BITS == 6) tmem_load16(added_at + N, d2);
-      }
       if (n < steps) {
         if (!wait(&s.weights[stage], parity)) break;
-        const uint8_t* const block = s_mem + (size_t)stage * Z::kStage + team * Z::kBlock;
+        const uint8_t* const block = s_mem + (size_t)stage * Z::kStage + side * Z::kBlock;
+        const uint32_t at = my_tmem + buffer * (Z::kACols + Z::kDCols);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint4 w4 = *reinterpret_cast<const uint4*>(block + w4_chunk_offset(c, quad, lane));
-          const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-          constexpr uint32_t flip = BITS == 4 ? 0x08080808u : 0u;
+        for (int half = 0; half < 2; ++half) {
+          uint32_t a[16];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            a[c * 8 + 2 * j] = (w[j] & 0x0F0F0F0Fu) ^ flip;
-            a[c * 8 + 2 * j + 1] = (w[j] >> 4 & 0x0F0F0F0Fu) ^ flip;
+          for (int c = 0; c < 2; ++c) {
+            const uint4 w4 = *reinterpret_cast<const uint4*>(block + w4_chunk_offset(half * 2 + c, quad, lane));
+            const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+            constexpr uint32_t flip = BITS == 4 ? 0x08080808u : 0u;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              a[c * 8 + 2 * j] = (w[j] & 0x0F0F0F0Fu) ^ flip;
+              a[c * 8 + 2 * j + 1] = (w[j] >> 4 & 0x0F0F0F0Fu) ^ flip;
+            }
           }
+          tmem_store16(at + half * 16, a);
           if constexpr (BITS == 6) {
-            const uint2 u2 = *reinterpret_cast<const uint2*>(block + hi_chunk_offset(c, quad, lane));
-            const uint32_t u[2] = {u2.x, u2.y};
 #pragma unroll
-            for (int j = 0; j < 8; ++j) top[c * 8 + j] = (u[j >> 2] >> (2 * (j & 3)) & 0x03030303u) ^ 0x02020202u;
+            for (int c = 0; c < 2; ++c) {
+              const uint2 u2 = *reinterpret_cast<const uint2*>(block + hi_chunk_offset(half * 2 + c, quad, lane));
+              const uint32_t u[2] = {u2.x, u2.y};
+#pragma unroll
+              for (int j = 0; j < 8; ++j) a[c * 8 + j] = (u[j >> 2] >> (2 * (j & 3)) & 0x03030303u) ^ 0x02020202u;
+            }
+            tmem_store16(at + 32 + half * 16, a);
           }
         }
-        if (++stage == Z::kStages) stage = 0, parity ^= 1;
+        stored = stage;
+        if ((stage += 2) >= Z::kStages) stage -= Z::kStages, parity ^= 1;
       }
-      if (kDefer && stored >= 0) announce();
-      const auto add = [&]() {
+      const auto announce = [&]() {  // the A that was stored
+        tmem_wait_stores();
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) dev::mbar_arrive(&s.operands[stored]);
+        if (++buffer == Z::kBuffers) buffer = 0;
+      };
+      if (kLag == 0) announce();
+      if (n >= kLag) {
+        // with two buffers the store goes on meanwhile
+        if (!wait(&s.done[pair][added_buffer], added_parity)) break;
+        tmem_fence_after();
         const uint8_t* const st = s_mem + (size_t)added_stage * Z::kStage;
-        const float scale = dev::half_bits_to_float(reinterpret_cast<const uint16_t*>(st + team * Z::kBlock)[scale_index(row)]);
+        const uint32_t at = my_tmem + added_buffer * (Z::kACols + Z::kDCols) + Z::kACols;
+        const float scale = dev::half_bits_to_float(reinterpret_cast<const uint16_t*>(st + side * Z::kBlock)[scale_index(row)]);
         const float4* const meta = reinterpret_cast<const float4*>(st + Z::kMeta);  // two rows each
 #pragma unroll
         for (int c = 0; c < N / 16; ++c) {
-          if (!kDefer || c > 0) {
-            tmem_load16(added_at + 16 * c, d);
-            if (BITS == 6) tmem_load16(added_at + N + 16 * c, d2);
-          }
+          uint32_t d[16];
+          tmem_load16(at + 16 * c, d);
           tmem_loaded(d);
           if (BITS == 6) {
+            uint32_t d2[16];
+            tmem_load16(at + N + 16 * c, d2);
             tmem_loaded(d2);
 #pragma unroll
             for (int j = 0; j < 16; ++j) d[j] = __float_as_uint(fmaf(16.0f, __uint_as_float(d2[j]), __uint_as_float(d[j])));
@@ -717,39 +734,26 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
         tmem_fence_before();
         __syncwarp();
         if (lane == 0) dev::mbar_arrive(&s.empty[added_stage]);
-      };
-      if (kDefer && adds) add();
-      if (n < steps) {
-        const uint32_t at = my_tmem + buffer * (Z::kACols + Z::kDCols);
-        tmem_store(at, a);
-        if constexpr (BITS == 6) tmem_store(at + 32, top);
-        stored = buffer;
-        if (++buffer == Z::kBuffers) buffer = 0;
-        if (!kDefer) announce();
       }
-      if (!adds) continue;
-      if (!kDefer) {
-        if (!wait(&s.done[team][added_buffer], added_parity)) break;
-        tmem_fence_after();
-        add();
-      }
-      if (++added_stage == Z::kStages) added_stage = 0;
+      if (kLag > 0 && n < steps) announce();
+      if (n < kLag) continue;
+      if ((added_stage += 2) >= Z::kStages) added_stage -= Z::kStages;
       if (++added_buffer == Z::kBuffers) added_buffer = 0, added_parity ^= 1;
-      if (++g < groups && n + 1 < steps + kLag) continue;
+      g += 2;
+      if (g < groups && n + 1 < steps + kLag) continue;
 
-      // The unit's last step here: the sums go to the finishers.
-      if (!wait(&s.taken[unit_buffer], unit_parity ^ 1u)) break;
-      float* const to = s_unit + unit_buffer * (Z::kRows * 256) + tid;
+      // The pair's last step of the unit: the sums go to the finishers.
+      if (!wait(&s.taken[unit_buffer][pair], unit_parity ^ 1u)) break;
+      float* const to = s_unit + (unit_buffer * 2 + pair) * (Z::kRows * 256) + side * kTeamThreads + row;
 #pragma unroll
       for (int t = 0; t < Z::kRows; ++t) {
         to[t * 256] = acc[t];
         acc[t] = 0.0f;
       }
       __syncwarp();
-      if (lane == 0) dev::mbar_arrive(&s.given[unit_buffer]);
-      unit_buffer ^= 1;
-      if (!unit_buffer) unit_parity ^= 1;
-      g = 0;
+      if (lane == 0) dev::mbar_arrive(&s.given[unit_buffer][pair]);
+      if (++unit_buffer == Z::kUnits) unit_buffer = 0, unit_parity ^= 1;
+      while (g >= groups) g -= groups;
     }
   }
   __syncwarp();
