@@ -15,15 +15,13 @@ inline bool known_type(int t) { return t == WOQ_KV8_BF16 || t == WOQ_KV8_F32; }
 // Where the parts of the experts' workspace lie.  What has to be zero between launches comes first and lies in the same place for every shape, so launches of different shapes may share a workspace.
 struct ExpertsLayout {
   size_t split_counts, split_sums, item, order, x_halves, x_meta, h_halves, h_meta, parts, total;
-  int few, item_rows;
+  int item_rows;
 };
 
-// Rows of an item: the fewest columns of B that hold what an expert has where every one is as likely.  Up to kFewEntries places
-// of few rows an expert nothing is launched before the products.
-void choose_items(int E, size_t n, ExpertsLayout* l) {
+// Rows of an item: the fewest columns of B that hold what an expert has where every one is as likely.
+int choose_item_rows(int E, size_t n) {
   const double rows = n / (E * (1.0 - pow(1.0 - 1.0 / E, (double)n)));
-  l->few = n <= (size_t)kFewEntries && rows <= 6.0;
-  l->item_rows = rows <= 6.0 ? 8 : 16;
+  return rows <= 6.0 ? 8 : 16;
 }
 
 bool experts_layout(int E, int T, int k, int H, int I, ExpertsLayout* l) {
@@ -31,7 +29,7 @@ bool experts_layout(int E, int T, int k, int H, int I, ExpertsLayout* l) {
   for (const int d : {H, I})
     if (d < kGroup || d > 32768 || d % kGroup) return false;
   const size_t n = (size_t)T * k;
-  choose_items(E, n, l);
+  l->item_rows = choose_item_rows(E, n);
   // an item holds kLeastItemRows places of one expert at least, an expert's last one fewer
   const size_t most = n / kLeastItemRows + (size_t)E;
   size_t at = 256;
@@ -165,7 +163,6 @@ int woq_experts_swiglu(int bits, int E, const void* gate_up, size_t gate_up_byte
   a.hidden = H;
   a.inner = I;
   a.entries = T * k;
-  a.few = l.few;
   a.item_rows = l.item_rows;
   a.wait_ns = wait_bound_ns();
   a.fault_cta = fault_cta(1);

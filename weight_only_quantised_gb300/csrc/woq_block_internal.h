@@ -55,7 +55,6 @@ struct Experts {
   int bits, experts, rows, k, hidden, inner;  // T, k, H, I
   int entries;                                // T k
   int item_rows;                              // most places of an item: 8 or 16
-  int few;                                    // few places: no plan in memory
   unsigned long long wait_ns;                 // bound of device waits
   int fault_cta;                              // a CTA that copies no weights (tests), -1: none
   // workspace
@@ -71,7 +70,6 @@ struct Experts {
   float* parts;       // [entries][H]
 };
 constexpr int kLeastItemRows = 8;  // rows of an item, where they are fewest
-constexpr int kFewEntries = 256;   // places that every CTA of the products may sort out for itself
 constexpr int kMostCtas = 256;
 constexpr int kMostEntries = 32768;
 cudaError_t launch_experts(const Experts& p, cudaStream_t stream);

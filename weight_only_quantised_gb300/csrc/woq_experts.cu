@@ -1,7 +1,5 @@
-// Experts' products: what surrounds the products of woq_experts.cuh (the plan and x in halves for many places; the weighted
-// sum), and the launches.
-#include <stdlib.h>
-
+// Experts' products: what surrounds the products of woq_experts.cuh (the plan and x in halves; the weighted sum), and the
+// launches.
 #include "woq_experts.cuh"
 
 namespace woq {
@@ -10,45 +8,58 @@ namespace experts {
 cudaError_t launch_products_w4(const Experts& p, bool gated, int sms, cudaStream_t s);
 cudaError_t launch_products_w6(const Experts& p, bool gated, int sms, cudaStream_t s);
 
-constexpr int kPlanThreads = 1024;
+constexpr int kBeginThreads = 256;
+constexpr int kExpertsPerThread = 1024 / kBeginThreads;
 
-// One CTA: places by expert, and the items (up to p.item_rows places of one expert).
-__device__ __forceinline__ void plan_all(const Experts& p) {
+// One CTA: places by expert, and the items (up to p.item_rows places of one expert).  Thread i looks after experts 4 i .. 4 i + 3.
+__device__ __forceinline__ void plan(const Experts& p) {
   __shared__ int s_next[1024], s_sums[33];
   const int tid = threadIdx.x;
-  s_next[tid] = 0;
+  reinterpret_cast<int4*>(s_next)[tid] = make_int4(0, 0, 0, 0);
   __syncthreads();
-  for (int i = tid; i < p.entries; i += kPlanThreads) {
+  for (int i = tid; i < p.entries; i += kBeginThreads) {
     const int e = p.ids[i];
     if ((unsigned)e < (unsigned)p.experts) atomicAdd(&s_next[e], 1);
   }
   __syncthreads();
-  const int count = s_next[tid], most = p.item_rows;
-  int total, items;
-  const int first = kv8::block_exclusive_sum(count, s_sums, &total);
+  const int most = p.item_rows;
+  int count[kExpertsPerThread], sum = 0, items = 0;
+#pragma unroll
+  for (int j = 0; j < kExpertsPerThread; ++j) {
+    count[j] = s_next[tid * kExpertsPerThread + j];
+    sum += count[j];
+    items += (count[j] + most - 1) / most;
+  }
+  // both sums in one scan: entries (at most 32,768) above items (at most 5,120)
+  int total;
+  const int before = kv8::block_exclusive_sum(sum << 13 | items, s_sums, &total);
+  int first = before >> 13, item = before & 0x1FFF;
+#pragma unroll
+  for (int j = 0; j < kExpertsPerThread; ++j) {
+    s_next[tid * kExpertsPerThread + j] = first;
+    for (int i = 0; i < count[j]; i += most, ++item)
+      p.item[item] = ExpertItem{tid * kExpertsPerThread + j, first + i, count[j] - i < most ? count[j] - i : most, 0};
+    first += count[j];
+  }
   __syncthreads();
-  const int item = kv8::block_exclusive_sum((count + most - 1) / most, s_sums, &items);
-  s_next[tid] = first;
-  __syncthreads();
-  for (int i = 0, n = item; i < count; i += most, ++n) p.item[n] = ExpertItem{tid, first + i, count - i < most ? count - i : most, 0};
   // The order of an expert's places may differ from run to run; each is a column of its own, so no result does.
-  for (int i = tid; i < p.entries; i += kPlanThreads) {
+  for (int i = tid; i < p.entries; i += kBeginThreads) {
     const int e = p.ids[i];
     if ((unsigned)e < (unsigned)p.experts) p.order[atomicAdd(&s_next[e], 1)] = i;
   }
-  if (tid == 0) p.status[1] = (uint32_t)items;
+  if (tid == 0) p.status[1] = (uint32_t)(total & 0x1FFF);
 }
 
-// For many places, before gate and up: the plan (CTA 0), and x in halves, a warp per group.
-__global__ void __launch_bounds__(kPlanThreads) begin_kernel(const Experts p) {
-  dev::pdl_wait_prior_grids();
+// Before gate and up: the plan (CTA 0), and x in halves, a warp per group.
+__global__ void __launch_bounds__(kBeginThreads) begin_kernel(const Experts p) {
   dev::pdl_launch_dependents();
+  dev::pdl_wait_prior_grids();
   if (blockIdx.x == 0) {
-    plan_all(p);
+    plan(p);
     return;
   }
   const int lane = threadIdx.x & 31;
-  const size_t group = (size_t)(blockIdx.x - 1) * (kPlanThreads / 32) + (threadIdx.x >> 5);
+  const size_t group = (size_t)(blockIdx.x - 1) * (kBeginThreads / 32) + (threadIdx.x >> 5);
   if (group >= (size_t)p.rows * (p.hidden / kGroup)) return;
   const uint2 x = *reinterpret_cast<const uint2*>(p.x + group * kGroup + lane * 4);
   const int e = group_exponent(__reduce_max_sync(~0u, most_field(most2(x.x, x.y))));
@@ -107,17 +118,14 @@ __global__ void __launch_bounds__(256) sum_kernel(const Experts p) {
 
 }  // namespace experts
 
-cudaError_t launch_experts(const Experts& args, cudaStream_t s) {
+cudaError_t launch_experts(const Experts& p, cudaStream_t s) {
   using namespace experts;
   int sms = sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
   if (sms > kMostCtas) sms = kMostCtas;
-  Experts p = args;
-  if (const char* v = getenv("XN"); v && atoi(v)) p.few = atoi(v) == 1, p.item_rows = p.few ? 8 : atoi(v);
   const auto products = p.bits == 4 ? launch_products_w4 : launch_products_w6;
   const long long groups = (long long)p.rows * (p.hidden / kGroup);
-  cudaError_t e = cudaSuccess;
-  if (!p.few) e = kv8::launch(begin_kernel, dim3((unsigned)(1 + (groups + 31) / 32)), kPlanThreads, 0, s, p);
+  cudaError_t e = kv8::launch(begin_kernel, dim3((unsigned)(1 + (groups + 7) / 8)), kBeginThreads, 0, s, p);
   if (e != cudaSuccess) return e;
   e = products(p, true, sms, s);
   if (e != cudaSuccess) return e;

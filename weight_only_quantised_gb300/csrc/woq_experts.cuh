@@ -41,8 +41,6 @@ constexpr int kTeamThreads = 128;
 // warps 0 .. 15: the teams
 constexpr int kProducer = 16, kIssuer = 17, kBringer = 18, kBringers = 2, kFinisher = 20, kFinishers = 4;
 constexpr int kThreads = (kFinisher + kFinishers) * 32;
-constexpr int kSmallEntries = kFewEntries;
-constexpr int kFewRows = 8;   // rows of an item then
 constexpr int kColumns = 512;       // of tensor memory
 
 // ---------------------------------------------------------------------------------------- halves
@@ -94,67 +92,6 @@ __device__ __forceinline__ void halves4(uint32_t x01, uint32_t x23, int e, uint3
 // offset off (-8 or -32 times the sum, in codes' units).
 __device__ __forceinline__ float2 group_meta(int e, float sum, int bits) {
   return make_float2(group_undo(e), sum * (bits == 4 ? -0x1p-6f : -0x1p-4f));
-}
-
-// ------------------------------------------------------------------------------------------ plan
-
-// Which experts are worked on, and for which places, in items of one expert: with up to kSmallEntries places every CTA
-// sorts them out for itself, else begin_kernel has (global memory).
-struct Plan {
-  int items;
-  int expert[kSmallEntries];
-  int rows[kSmallEntries];
-  int place[kSmallEntries][kFewRows];
-  // scratch
-  alignas(16) int ids[kSmallEntries];
-  int number[kSmallEntries];
-  int starts[kSmallEntries / 32];
-};
-
-// One place a thread.  A place's turn is the number of places before it with the same expert; every kFewRows-th starts an item.
-__device__ __forceinline__ void plan_here(const Experts& p, Plan& s) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const bool here = tid < kSmallEntries;
-  int e = -1;
-  if (tid < p.entries) {
-    e = p.ids[tid];
-    if ((unsigned)e >= (unsigned)p.experts) e = -1;
-  }
-  if (here) s.ids[tid] = e, s.rows[tid] = 0;
-  __syncthreads();
-  int turn = 0, leader = tid;
-  if (e >= 0) {
-    const int4* v = reinterpret_cast<const int4*>(s.ids);
-    for (int i = 0; i < tid; i += 4) {
-      const int4 o = v[i >> 2];
-      const int w[4] = {o.x, o.y, o.z, o.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (w[j] == e && i + j < tid) {
-          if (turn % kFewRows == 0) leader = i + j;
-          ++turn;
-        }
-    }
-    if (turn % kFewRows == 0) leader = tid;
-  }
-  const bool start = e >= 0 && leader == tid;
-  const unsigned starts = __ballot_sync(~0u, start);
-  if (here && lane == 0) s.starts[warp] = __popc(starts);
-  __syncthreads();
-  if (here) {
-    int number = __popc(starts & ((1u << lane) - 1));
-    for (int w = 0; w < warp; ++w) number += s.starts[w];
-    s.number[tid] = number;
-    if (start) s.expert[number] = e;
-    if (tid == kSmallEntries - 1) s.items = number + start;
-  }
-  __syncthreads();
-  if (e >= 0) {
-    const int item = s.number[leader];
-    s.place[item][turn % kFewRows] = tid;
-    atomicAdd(&s.rows[item], 1);
-  }
-  __syncthreads();
 }
 
 // ----------------------------------------------------------------------------------- tensor memory
@@ -224,8 +161,7 @@ __device__ __forceinline__ void fence_for_products() { asm volatile("fence.proxy
 
 // ---------------------------------------------------------------------------------------- products
 
-// FEW: up to kSmallEntries places: the plan is made in the kernel, and the bringers take x apart as they go.
-template <int BITS, int N, bool FEW>
+template <int BITS, int N>
 struct Shape {
   static constexpr int kRows = N / 2;  // of an item
   static constexpr int kBlock = BITS == 4 ? kBlockBytesW4 : kBlockBytesW6;
@@ -233,16 +169,15 @@ struct Shape {
   static constexpr int kACols = BITS == 4 ? 32 : 64, kDCols = BITS == 4 ? N : 2 * N;
   static constexpr int kBuffers = kColumns / 4 / (kACols + kDCols);  // of A and D, a team
   static_assert(kBuffers == 1 || kBuffers == 2, "tensor memory");
-  // [stages][exchange: units' sums by pairs, then the finishers' maxima and sums][barriers and flags][plan]
+  // [stages][exchange: units' sums by pairs, then the finishers' maxima and sums][barriers and flags]
   static constexpr int kUnits = N == 16 ? 2 : 1;  // units' sums that there is room for
   static constexpr int kExchange = kUnits * 2 * kRows * 256 * 4 + 2 * 4 * kRows * 4;
   static constexpr int kMisc = 1024;
-  static constexpr int kPlan = FEW ? (int)((sizeof(Plan) + 127) / 128 * 128) : 0;
-  static constexpr int kRoom = 227 * 1024 - kExchange - kMisc - kPlan;
+  static constexpr int kRoom = 227 * 1024 - kExchange - kMisc;
   // An even number, so that a stage always serves the same pair: a wait for a parity two phases ahead returns at once.
   static constexpr int kStages = (kRoom / kStage < 12 ? kRoom / kStage : 12) / 2 * 2;
   static_assert(kStages >= 2 * kBuffers + 2, "a stage is held until its sums are taken");
-  static constexpr int kBytes = kStages * kStage + kExchange + kMisc + kPlan;
+  static constexpr int kBytes = kStages * kStage + kExchange + kMisc;
 };
 
 struct Barriers {
@@ -255,15 +190,14 @@ struct Barriers {
 };
 static_assert(sizeof(Barriers) <= 1024, "misc");
 
-template <int BITS, bool GATED, int N, bool FEW>
+template <int BITS, bool GATED, int N>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
-  typedef Shape<BITS, N, FEW> Z;
+  typedef Shape<BITS, N> Z;
   extern __shared__ __align__(128) uint8_t s_mem[];
   float* const s_unit = reinterpret_cast<float*>(s_mem + Z::kStages * Z::kStage);  // [units][pair][rows][256]
   uint32_t* const s_most = reinterpret_cast<uint32_t*>(s_unit + Z::kUnits * 2 * Z::kRows * 256);
   float* const s_sums = reinterpret_cast<float*>(s_most + 4 * Z::kRows);
   Barriers& s = *reinterpret_cast<Barriers*>(s_mem + Z::kStages * Z::kStage + Z::kExchange);
-  Plan& plan = *reinterpret_cast<Plan*>(s_mem + Z::kStages * Z::kStage + Z::kExchange + Z::kMisc);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint64_t limit = p.wait_ns;
 
@@ -284,16 +218,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
   }
   if (warp == kIssuer)
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dev::smem_addr(&s.tmem)), "n"(kColumns) : "memory");
-  // The down projection's launch may read the ids (or the plan), which were there before the one it waits for began.
+  // The down projection's launch may read the plan, which was there before the one it waits for began.
   if (GATED) dev::pdl_wait_prior_grids();
   dev::pdl_launch_dependents();
-  int items;
-  if constexpr (FEW) {
-    plan_here(p, plan);
-    items = plan.items;
-  } else {
-    items = (int)p.status[1];
-  }
+  const int items = (int)p.status[1];
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
@@ -312,8 +240,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
     begin = (int)((long long)units * cta / g) * groups;
     end = (int)((long long)units * (cta + 1) / g) * groups;
   }
-  const auto rows_of = [&](int item) { return FEW ? plan.rows[item] : p.item[item].rows; };
-  const auto place_of = [&](int item, int row) { return FEW ? plan.place[item][row] : p.order[p.item[item].first + row]; };
+  const auto rows_of = [&](int item) { return p.item[item].rows; };
+  const auto place_of = [&](int item, int row) { return p.order[p.item[item].first + row]; };
   const auto failed = [&]() {
     *(volatile int*)&s.fail = 1;
     atomicOr(p.status, (uint32_t)WOQ_DEVERR_TIMEOUT);
@@ -343,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
       const uint8_t *src0, *src1;
       const auto locate = [&]() {
         const int item = unit / slices, slice = unit - item * slices;
-        const int expert = FEW ? plan.expert[item] : p.item[item].expert;
+        const int expert = p.item[item].expert;
         const uint8_t* const m = matrices + (size_t)expert * stride + kHeaderBytes;
         const int t0 = GATED ? slice : 2 * slice, t1 = GATED ? slice + tiles : 2 * slice + 1;
         src0 = m + ((size_t)t0 * groups + g) * Z::kBlock;
@@ -416,82 +344,6 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
       if (lane == 0) dev::mbar_arrive(&s.operands[stage]);
     };
     const auto free_stage = [&](int n) { return wait(&s.empty[n % Z::kStages], ((uint32_t)(n / Z::kStages) & 1u) ^ 1u); };  // for step n of this CTA
-    if constexpr (GATED && FEW) {
-      // Four lanes a row of a group, 32 elements each.  With fewer than 8 rows in an item the other lanes take the next groups, so that
-      // a warp is full: the warps take such runs of steps in turn.
-      const int slot = lane >> 2, quarter = lane & 3;
-      struct Run {
-        int first, steps, shift, rows;  // 2^shift >= rows
-      };
-      const auto run_at = [&](int i) {
-        Run r;
-        const int unit = i / groups, left = min((unit + 1) * groups, end) - i;
-        r.first = i;
-        r.rows = rows_of(unit / slices);
-        r.shift = r.rows > 4 ? 3 : r.rows > 2 ? 2 : r.rows > 1 ? 1 : 0;
-        r.steps = min(8 >> r.shift, left);
-        return r;
-      };
-      uint4 v[4];
-      const auto load = [&](const Run& r) {
-        const int t = slot & ((1 << r.shift) - 1), i = r.first + (slot >> r.shift), unit = i / groups, g = i - unit * groups;
-        const bool here = t < r.rows && (slot >> r.shift) < r.steps;
-        const uint4* src = reinterpret_cast<const uint4*>(p.x + (size_t)(here ? place_of(unit / slices, t) / p.k : 0) * K + g * kGroup + quarter * 32);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = here ? src[j] : make_uint4(0u, 0u, 0u, 0u);
-      };
-      const auto next = [&](Run r) { return r.first + r.steps < end ? run_at(r.first + r.steps) : Run{end, 0, 0, 0}; };
-      Run r = begin < end ? run_at(begin) : Run{end, 0, 0, 0};
-      bool ok = true;
-      if (me) {
-        const Run other = r;
-        r = next(r);
-        if (r.first < end) load(r);
-        for (int j = 0; j < other.steps && ok; ++j) ok = free_stage(other.first + j - begin);
-      } else if (r.first < end) {
-        load(r);
-      }
-      while (r.first < end && ok) {
-        const uint32_t x[16] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w,
-                                v[2].x, v[2].y, v[2].z, v[2].w, v[3].x, v[3].y, v[3].z, v[3].w};
-        uint32_t m = most2(x[0], x[1]);
-#pragma unroll
-        for (int j = 2; j < 16; ++j) m = most2(m, x[j]);
-        m = most_field(m);
-        m = max(m, __shfl_xor_sync(~0u, m, 1));
-        m = max(m, __shfl_xor_sync(~0u, m, 2));
-        const int e = group_exponent(m);
-        uint32_t high[8], low[8];
-        float sum = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) halves4(x[2 * j], x[2 * j + 1], e, high[j], low[j], sum);
-        sum += __shfl_xor_sync(~0u, sum, 1);
-        sum += __shfl_xor_sync(~0u, sum, 2);
-        const Run now = r;
-        r = next(r);
-        const Run other = r;  // the other warp's
-        if (r.first < end) r = next(r);
-        if (r.first < end) load(r);
-        const int t = slot & ((1 << now.shift) - 1);
-        for (int j = 0; j < now.steps; ++j) {
-          const int n = now.first + j - begin, stage = n % Z::kStages;
-          if (!(ok = free_stage(n))) break;
-          if (slot >> now.shift == j) {
-            uint8_t* const st = s_mem + (size_t)stage * Z::kStage;
-            uint8_t* const at = st + Z::kB + (t >> 2) * 1024 + (t & 3) * 32 + quarter * 256;
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              *reinterpret_cast<uint4*>(at + c * 128) = make_uint4(high[4 * c], high[4 * c + 1], high[4 * c + 2], high[4 * c + 3]);
-              *reinterpret_cast<uint4*>(at + c * 128 + 16) = make_uint4(low[4 * c], low[4 * c + 1], low[4 * c + 2], low[4 * c + 3]);
-            }
-            if (quarter == 0) *reinterpret_cast<float2*>(st + Z::kMeta + t * 8) = group_meta(e, sum, BITS);
-          }
-          arrive(stage);
-        }
-        // Each stage's every phase is waited for, the other's too: a wait for a parity two phases ahead returns at once.
-        for (int j = 0; j < other.steps && ok; ++j) ok = free_stage(other.first + j - begin);
-      }
-    } else {
       // pieces of 16 bytes: piece lane & 15 of two rows at a time
       const uint8_t* const halves = GATED ? p.x_halves : p.h_halves;
       const float2* const meta = GATED ? p.x_meta : p.h_meta;
@@ -538,7 +390,6 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
       // the last steps (if the loop ended early nobody waits for them any more)
       if (ok)
         for (; pending > 0; --pending) arrive((i - begin - pending * kBringers) % Z::kStages);
-    }
   } else if (warp >= kFinisher) {
     if (!GATED) dev::pdl_wait_prior_grids();  // the sums of split units lie where the launch before had its own
     const int me = tid - kFinisher * 32, quad = warp - kFinisher;
@@ -766,12 +617,12 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
   }
 }
 
-template <int BITS, bool GATED, int N, bool FEW>
+template <int BITS, bool GATED, int N>
 inline cudaError_t launch_product(const Experts& p, int sms, cudaStream_t s) {
-  typedef Shape<BITS, N, FEW> Z;
-  const cudaError_t e = cudaFuncSetAttribute(product_kernel<BITS, GATED, N, FEW>, cudaFuncAttributeMaxDynamicSharedMemorySize, Z::kBytes);
+  typedef Shape<BITS, N> Z;
+  const cudaError_t e = cudaFuncSetAttribute(product_kernel<BITS, GATED, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, Z::kBytes);
   if (e != cudaSuccess) return e;
-  return kv8::launch(product_kernel<BITS, GATED, N, FEW>, dim3((unsigned)sms), kThreads, Z::kBytes, s, p);
+  return kv8::launch(product_kernel<BITS, GATED, N>, dim3((unsigned)sms), kThreads, Z::kBytes, s, p);
 }
 
 }  // namespace experts

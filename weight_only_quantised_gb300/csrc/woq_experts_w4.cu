@@ -5,9 +5,8 @@ namespace woq {
 namespace experts {
 
 cudaError_t launch_products_w4(const Experts& p, bool gated, int sms, cudaStream_t s) {
-  if (p.few) return gated ? launch_product<4, true, 16, true>(p, sms, s) : launch_product<4, false, 16, true>(p, sms, s);
-  if (p.item_rows == 8) return gated ? launch_product<4, true, 16, false>(p, sms, s) : launch_product<4, false, 16, false>(p, sms, s);
-  return gated ? launch_product<4, true, 32, false>(p, sms, s) : launch_product<4, false, 32, false>(p, sms, s);
+  if (p.item_rows == 8) return gated ? launch_product<4, true, 16>(p, sms, s) : launch_product<4, false, 16>(p, sms, s);
+  return gated ? launch_product<4, true, 32>(p, sms, s) : launch_product<4, false, 32>(p, sms, s);
 }
 
 }  // namespace experts
