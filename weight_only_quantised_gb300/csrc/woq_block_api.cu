@@ -18,10 +18,11 @@ struct ExpertsLayout {
   int item_rows;
 };
 
-// Rows of an item: the fewest columns of B that hold what an expert has where every one is as likely.
+// Rows of an item: the fewest columns of B that hold what an expert has where every one is as likely (16 at most with int6: its two
+// sums a column fill tensor memory).
 int choose_item_rows(int E, size_t n) {
   const double rows = n / (E * (1.0 - pow(1.0 - 1.0 / E, (double)n)));
-  return rows <= 6.0 ? 8 : 16;
+  return rows <= 6.0 ? 8 : rows <= 12.0 ? 16 : 32;
 }
 
 bool experts_layout(int E, int T, int k, int H, int I, ExpertsLayout* l) {
@@ -163,7 +164,7 @@ int woq_experts_swiglu(int bits, int E, const void* gate_up, size_t gate_up_byte
   a.hidden = H;
   a.inner = I;
   a.entries = T * k;
-  a.item_rows = l.item_rows;
+  a.item_rows = bits == 6 && l.item_rows > 16 ? 16 : l.item_rows;
   a.wait_ns = wait_bound_ns();
   a.fault_cta = fault_cta(1);
   a.status = reinterpret_cast<uint32_t*>(w);

@@ -54,7 +54,7 @@ struct Experts {
   uint16_t* y;
   int bits, experts, rows, k, hidden, inner;  // T, k, H, I
   int entries;                                // T k
-  int item_rows;                              // most places of an item: 8 or 16
+  int item_rows;                              // most places of an item: 8, 16 or 32
   unsigned long long wait_ns;                 // bound of device waits
   int fault_cta;                              // a CTA that copies no weights (tests), -1: none
   // workspace

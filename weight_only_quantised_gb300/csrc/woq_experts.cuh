@@ -144,8 +144,8 @@ constexpr uint32_t kIdesc = 1u << 4 | (uint32_t)(N >> 3) << 17 | (uint32_t)(128 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void copy8(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -165,7 +165,7 @@ template <int BITS, int N>
 struct Shape {
   static constexpr int kRows = N / 2;  // of an item
   static constexpr int kBlock = BITS == 4 ? kBlockBytesW4 : kBlockBytesW6;
-  static constexpr int kB = 2 * kBlock, kMeta = kB + N * 128, kStage = (kMeta + kRows * 8 + 127) / 128 * 128;
+  static constexpr int kB = 2 * kBlock, kUndo = kB + N * 128, kLess = kUndo + kRows * 4, kStage = (kLess + kRows * 4 + 127) / 128 * 128;
   static constexpr int kACols = BITS == 4 ? 32 : 64, kDCols = BITS == 4 ? N : 2 * N;
   static constexpr int kBuffers = kColumns / 4 / (kACols + kDCols);  // of A and D, a team
   static_assert(kBuffers == 1 || kBuffers == 2, "tensor memory");
@@ -230,16 +230,13 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
   const int K = GATED ? p.hidden : p.inner, groups = K / kGroup;
   const int tiles = GATED ? p.inner / kTileRows : p.hidden / kTileRows, slices = GATED ? tiles : (tiles + 1) / 2;
   const int units = items * slices, total = units * groups;
-  const int ctas = total < (int)gridDim.x ? total : (int)gridDim.x, cta = blockIdx.x;
-  int begin = cta < ctas ? (int)((long long)total * cta / ctas) : 0, end = cta < ctas ? (int)((long long)total * (cta + 1) / ctas) : 0;
-  // Whole units where the longest share is not much longer then: putting a unit together takes as long as some eight steps.
-  const int most_units = (units + (int)gridDim.x - 1) / (int)gridDim.x;
-  const bool whole = most_units * groups <= total / (int)gridDim.x + 8;
-  if (whole) {
-    const int g = (int)gridDim.x;
-    begin = (int)((long long)units * cta / g) * groups;
-    end = (int)((long long)units * (cta + 1) / g) * groups;
-  }
+  const int cta = blockIdx.x, grid = gridDim.x;
+  // Shares of whole units where the longest is not much longer than those of steps: putting a unit together takes as long as
+  // some eight steps.  Share c has `each` of them, and one more if c < more.
+  const bool whole = (units + grid - 1) / grid * groups <= total / grid + 8;
+  const int least = whole ? groups : 1, each = (whole ? units : total) / grid, more = (whole ? units : total) - each * grid;
+  const int begin = (each * cta + min(cta, more)) * least, end = begin + (each + (cta < more)) * least;
+  const auto cta_of = [&](int step) { return step < more * (each + 1) ? step / (each + 1) : more + (step - more * (each + 1)) / each; };
   const auto rows_of = [&](int item) { return p.item[item].rows; };
   const auto place_of = [&](int item, int row) { return p.order[p.item[item].first + row]; };
   const auto failed = [&]() {
@@ -376,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
           const int r = 2 * j + (lane >> 4);
           if (r < rows) {
             copy16(at + Z::kB + (r >> 2) * 1024 + (piece >> 1) * 128 + (r & 3) * 32 + (piece & 1) * 16, halves + (from[j] + g) * 256 + piece * 16);
-            if (piece == 0) copy8(at + Z::kMeta + r * 8, meta + from[j] + g);
+            if (piece < 2) copy4(at + (piece ? Z::kLess : Z::kUndo) + r * 4, reinterpret_cast<const float*>(meta + from[j] + g) + piece);
           }
         }
         copies_commit();
@@ -420,8 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
       float* const sums = gave[0] ? sums0 : sums1;
       const int item = unit / slices, slice = unit - item * slices, rows = rows_of(item);
       // the CTAs of the unit's first and last step
-      const int a = whole ? cta : (int)(((long long)(first_step + 1) * ctas - 1) / total);
-      const int b = whole ? cta : (int)(((long long)(first_step + groups) * ctas - 1) / total);
+      const int a = whole ? cta : cta_of(first_step), b = whole ? cta : cta_of(first_step + groups - 1);
       if (gave[0] && gave[1])
         for (int i = 0; i < 2 * rows; ++i) sums[i * 128] += sums1[i * 128];
       bool mine = true;
@@ -504,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
     // ------------------------------------------------------------------------------- the teams
     const int team = warp >> 2, pair = team >> 1, side = team & 1, quad = warp & 3, row = quad * 32 + lane;  // row of the tile
     const uint32_t my_tmem = tmem + ((uint32_t)(quad * 32) << 16) + team * Z::kBuffers * (Z::kACols + Z::kDCols);
-    float acc[Z::kRows] = {};
+    dev::f32x2 acc[Z::kRows / 2] = {};  // two rows each
     constexpr int kLag = Z::kBuffers - 1;  // the pair's steps from making A to adding up D
     const int steps = end - begin > pair ? (end - begin - pair + 1) / 2 : 0;  // the pair's: every other one
     int g = (begin + pair) % groups, unit_buffer = 0;                         // of the step that is added up
@@ -560,7 +556,9 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
         const uint8_t* const st = s_mem + (size_t)added_stage * Z::kStage;
         const uint32_t at = my_tmem + added_buffer * (Z::kACols + Z::kDCols) + Z::kACols;
         const float scale = dev::half_bits_to_float(reinterpret_cast<const uint16_t*>(st + side * Z::kBlock)[scale_index(row)]);
-        const float4* const meta = reinterpret_cast<const float4*>(st + Z::kMeta);  // two rows each
+        const dev::f32x2 scales = dev::f2_splat(scale);
+        const ulonglong2* const undo = reinterpret_cast<const ulonglong2*>(st + Z::kUndo);  // of four rows each
+        const ulonglong2* const less = reinterpret_cast<const ulonglong2*>(st + Z::kLess);
 #pragma unroll
         for (int c = 0; c < N / 16; ++c) {
           uint32_t d[16];
@@ -574,12 +572,17 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
             for (int j = 0; j < 16; ++j) d[j] = __float_as_uint(fmaf(16.0f, __uint_as_float(d2[j]), __uint_as_float(d[j])));
           }
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float4 m = meta[c * 4 + j];
-            const float t0 = fmaf(0.0625f, __uint_as_float(d[4 * j + 1]), __uint_as_float(d[4 * j]) + m.y);
-            const float t1 = fmaf(0.0625f, __uint_as_float(d[4 * j + 3]), __uint_as_float(d[4 * j + 2]) + m.w);
-            acc[c * 8 + 2 * j] = fmaf(scale * m.x, t0, acc[c * 8 + 2 * j]);
-            acc[c * 8 + 2 * j + 1] = fmaf(scale * m.z, t1, acc[c * 8 + 2 * j + 1]);
+          for (int j = 0; j < 2; ++j) {
+            const ulonglong2 u = undo[c * 2 + j], l = less[c * 2 + j];
+            const dev::f32x2 us[2] = {u.x, u.y}, ls[2] = {l.x, l.y};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t* const v = d + 8 * j + 4 * i;
+              const float t0 = fmaf(0.0625f, __uint_as_float(v[1]), __uint_as_float(v[0]));
+              const float t1 = fmaf(0.0625f, __uint_as_float(v[3]), __uint_as_float(v[2]));
+              dev::f32x2& to = acc[c * 4 + 2 * j + i];
+              to = dev::f2_fma(dev::f2_mul(scales, us[i]), dev::f2_add(dev::f2_pack(__float_as_uint(t0), __float_as_uint(t1)), ls[i]), to);
+            }
           }
         }
         tmem_fence_before();
@@ -597,9 +600,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
       if (!wait(&s.taken[unit_buffer][pair], unit_parity ^ 1u)) break;
       float* const to = s_unit + (unit_buffer * 2 + pair) * (Z::kRows * 256) + side * kTeamThreads + row;
 #pragma unroll
-      for (int t = 0; t < Z::kRows; ++t) {
-        to[t * 256] = acc[t];
-        acc[t] = 0.0f;
+      for (int t = 0; t < Z::kRows / 2; ++t) {
+        to[t * 512] = __uint_as_float(dev::f2_lo(acc[t]));
+        to[t * 512 + 256] = __uint_as_float(dev::f2_hi(acc[t]));
+        acc[t] = 0;
       }
       __syncwarp();
       if (lane == 0) dev::mbar_arrive(&s.given[unit_buffer][pair]);
