@@ -237,8 +237,6 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
   const int least = whole ? groups : 1, each = (whole ? units : total) / grid, more = (whole ? units : total) - each * grid;
   const int begin = (each * cta + min(cta, more)) * least, end = begin + (each + (cta < more)) * least;
   const auto cta_of = [&](int step) { return step < more * (each + 1) ? step / (each + 1) : more + (step - more * (each + 1)) / each; };
-  const auto rows_of = [&](int item) { return p.item[item].rows; };
-  const auto place_of = [&](int item, int row) { return p.order[p.item[item].first + row]; };
   const auto failed = [&]() {
     *(volatile int*)&s.fail = 1;
     atomicOr(p.status, (uint32_t)WOQ_DEVERR_TIMEOUT);
@@ -265,10 +263,11 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
       const uint8_t* const matrices = GATED ? p.gate_up : p.down;
       const size_t stride = GATED ? p.gate_up_stride : p.down_stride;
       int unit = begin / groups, g = begin - unit * groups, issued = 0;
+      int at_item = -1, expert = 0;
       const uint8_t *src0, *src1;
       const auto locate = [&]() {
         const int item = unit / slices, slice = unit - item * slices;
-        const int expert = p.item[item].expert;
+        if (item != at_item) expert = p.item[item].expert, at_item = item;
         const uint8_t* const m = matrices + (size_t)expert * stride + kHeaderBytes;
         const int t0 = GATED ? slice : 2 * slice, t1 = GATED ? slice + tiles : 2 * slice + 1;
         src0 = m + ((size_t)t0 * groups + g) * Z::kBlock;
@@ -341,52 +340,51 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
       if (lane == 0) dev::mbar_arrive(&s.operands[stage]);
     };
     const auto free_stage = [&](int n) { return wait(&s.empty[n % Z::kStages], ((uint32_t)(n / Z::kStages) & 1u) ^ 1u); };  // for step n of this CTA
-      // pieces of 16 bytes: piece lane & 15 of two rows at a time
-      const uint8_t* const halves = GATED ? p.x_halves : p.h_halves;
-      const float2* const meta = GATED ? p.x_meta : p.h_meta;
-      const int piece = lane & 15;
-      const uint32_t base = dev::smem_addr(s_mem);
-      int unit = -1, rows = 0;
-      size_t from[Z::kRows / 2];  // of rows 2 j + (lane >> 4)
-      constexpr int kAhead = 2;   // copies of this many steps are under way
-      int pending = 0;
-      bool ok = true;
-      int i = begin + me;
-      for (; i < end; i += kBringers) {
-        const int u = i / groups, g = i - u * groups;
-        if (u != unit) {
-          unit = u;
-          const int item = u / slices;
-          rows = rows_of(item);
-#pragma unroll
-          for (int j = 0; j < Z::kRows / 2; ++j) {
-            const int r = 2 * j + (lane >> 4);
-            const int place = r < rows ? place_of(item, r) : 0;
-            from[j] = (size_t)(GATED ? place / p.k : place) * groups;
-          }
-        }
-        const int n = i - begin;
-        if (!(ok = free_stage(n))) break;
-        const uint32_t at = base + (n % Z::kStages) * Z::kStage;
+    // pieces of 16 bytes: piece lane & 15 of two rows at a time
+    const uint8_t* const halves = GATED ? p.x_halves : p.h_halves;
+    const float* const meta = reinterpret_cast<const float*>(GATED ? p.x_meta : p.h_meta);
+    const int half = lane >> 4, piece = lane & 15;
+    const uint32_t base = dev::smem_addr(s_mem), to = Z::kB + (piece >> 1) * 128 + half * 32 + (piece & 1) * 16;
+    constexpr int kAhead = Z::kStages >= 10 ? 2 : 1;  // copies of this many steps are under way
+    uint32_t from[Z::kRows / 2], from_meta = 0;       // of rows 2 j + half, bytes (below 2^31); of row `lane`, floats
+    int item = -1, rows = 0, pending = 0, i = begin + me;
+    bool ok = true;
+    for (; i < end; i += kBringers) {
+      const int unit = i / groups, g = i - unit * groups, at_item = unit / slices;
+      if (at_item != item) {
+        item = at_item;
+        const ExpertItem it = p.item[item];
+        rows = it.rows;
 #pragma unroll
         for (int j = 0; j < Z::kRows / 2; ++j) {
-          const int r = 2 * j + (lane >> 4);
-          if (r < rows) {
-            copy16(at + Z::kB + (r >> 2) * 1024 + (piece >> 1) * 128 + (r & 3) * 32 + (piece & 1) * 16, halves + (from[j] + g) * 256 + piece * 16);
-            if (piece < 2) copy4(at + (piece ? Z::kLess : Z::kUndo) + r * 4, reinterpret_cast<const float*>(meta + from[j] + g) + piece);
-          }
+          const int r = 2 * j + half, place = r < rows ? p.order[it.first + r] : 0;
+          from[j] = (uint32_t)(GATED ? place / p.k : place) * (uint32_t)groups * 256u + (uint32_t)piece * 16u;
         }
-        copies_commit();
-        if (++pending > kAhead) {
-          copies_wait<kAhead>();
-          arrive((n - kAhead * kBringers) % Z::kStages);
-          --pending;
-        }
+        const int place = lane < rows ? p.order[it.first + lane] : 0;
+        from_meta = (uint32_t)(GATED ? place / p.k : place) * (uint32_t)groups * 2u;
       }
-      copies_wait<0>();
-      // the last steps (if the loop ended early nobody waits for them any more)
-      if (ok)
-        for (; pending > 0; --pending) arrive((i - begin - pending * kBringers) % Z::kStages);
+      const int n = i - begin;
+      if (!(ok = free_stage(n))) break;
+      const uint32_t at = base + (n % Z::kStages) * Z::kStage;
+      const uint8_t* const src = halves + (size_t)g * 256;
+#pragma unroll
+      for (int j = 0; j < Z::kRows / 2; ++j)
+        if (2 * j + half < rows) copy16(at + to + (j >> 1) * 1024 + (j & 1) * 64, src + from[j]);
+      if (lane < rows) {
+        copy4(at + Z::kUndo + lane * 4, meta + from_meta + 2 * g);
+        copy4(at + Z::kLess + lane * 4, meta + from_meta + 2 * g + 1);
+      }
+      copies_commit();
+      if (++pending > kAhead) {
+        copies_wait<kAhead>();
+        arrive((n - kAhead * kBringers) % Z::kStages);
+        --pending;
+      }
+    }
+    copies_wait<0>();
+    // the last steps (if the loop ended early nobody waits for them any more)
+    if (ok)
+      for (; pending > 0; --pending) arrive((i - begin - pending * kBringers) % Z::kStages);
   } else if (warp >= kFinisher) {
     if (!GATED) dev::pdl_wait_prior_grids();  // the sums of split units lie where the launch before had its own
     const int me = tid - kFinisher * 32, quad = warp - kFinisher;
@@ -402,6 +400,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
       const int unit = step / groups, first_step = unit * groups, last_step = min(first_step + groups, end);
       // a pair that had a step of it
       const bool gave[2] = {last_step - step > 1 || !((step - begin) & 1), last_step - step > 1 || ((step - begin) & 1)};
+      const int item = unit / slices, slice = unit - item * slices;
+      const ExpertItem it = p.item[item];
+      const int rows = it.rows, places = lane < rows ? p.order[it.first + lane] : 0;  // lane t: of row t
+      const auto place_of = [&](int t) { return (size_t)__shfl_sync(~0u, places, t); };
       int buffer[2];
       bool ok = true;
 #pragma unroll
@@ -415,19 +417,21 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
       float* const sums0 = s_unit + (buffer[0] * 2) * (Z::kRows * 256) + me;
       float* const sums1 = s_unit + (buffer[1] * 2 + 1) * (Z::kRows * 256) + me;
       float* const sums = gave[0] ? sums0 : sums1;
-      const int item = unit / slices, slice = unit - item * slices, rows = rows_of(item);
       // the CTAs of the unit's first and last step
       const int a = whole ? cta : cta_of(first_step), b = whole ? cta : cta_of(first_step + groups - 1);
-      if (gave[0] && gave[1])
+      if (gave[0] && gave[1]) {
+#pragma unroll 4
         for (int i = 0; i < 2 * rows; ++i) sums[i * 128] += sums1[i * 128];
+      }
       bool mine = true;
       if (a != b) {
         constexpr size_t kWords = (size_t)Z::kRows * 256;
         float* const part = p.split_sums + ((size_t)cta * 2 + (first_step >= begin ? 1 : 0)) * kWords + me;
+#pragma unroll 4
         for (int i = 0; i < 2 * rows; ++i) __stcg(part + i * 128, sums[i * 128]);
-        __threadfence();
         if (!meet()) break;
         if (me == 0) {
+          __threadfence();  // of all that the meeting has brought together
           const uint32_t before = dev::atomic_add_acq_rel_gpu(p.split_counts + a, 1u);
           s.last = before == (uint32_t)(b - a);
           if (s.last) p.split_counts[a] = 0;
@@ -435,11 +439,23 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
         if (!meet()) break;
         mine = s.last;
         if (mine) {
-          __threadfence();
-          for (int i = 0; i < 2 * rows; ++i) {
-            float v = 0.0f;
-            for (int c = a; c <= b; ++c) v += __ldcg(p.split_sums + ((size_t)c * 2 + (c == a ? 1 : 0)) * kWords + me + i * 128);
-            sums[i * 128] = v;
+          // in CTA order; eight loads are under way at a time
+          const float* const parts = p.split_sums + me;
+          for (int i = 0; i < 2 * rows; i += 2) {
+            float v0 = 0.0f, v1 = 0.0f;
+            for (int c = a; c <= b; c += 4) {
+              float w[4][2];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float* const from = parts + ((size_t)(c + j) * 2 + (c + j == a ? 1 : 0)) * kWords + i * 128;
+                w[j][0] = c + j <= b ? __ldcg(from) : 0.0f;
+                w[j][1] = c + j <= b ? __ldcg(from + 128) : 0.0f;
+              }
+#pragma unroll
+              for (int j = 0; j < 4; ++j) v0 += w[j][0], v1 += w[j][1];
+            }
+            sums[i * 128] = v0;
+            sums[i * 128 + 128] = v1;
           }
         }
       }
@@ -447,13 +463,15 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
       if (mine) {
         if constexpr (!GATED) {
           const bool second = 2 * slice + 1 < tiles;
+#pragma unroll 4
           for (int t = 0; t < rows; ++t) {
-            float* const to = p.parts + (size_t)place_of(item, t) * p.hidden + 2 * slice * kTileRows + me;
+            float* const to = p.parts + place_of(t) * p.hidden + 2 * slice * kTileRows + me;
             to[0] = 512.0f * sums[t * 256];
             if (second) to[kTileRows] = 512.0f * sums[t * 256 + 128];
           }
         } else {
           // h = silu(gate) up of 128 neighbouring elements of each row: a group of down's, taken apart here
+#pragma unroll 4
           for (int t = 0; t < rows; ++t) {
             const float v = 512.0f * sums[t * 256], h = v / (1.0f + expf(-v)) * (512.0f * sums[t * 256 + 128]);
             sums[t * 256] = h;
@@ -465,13 +483,14 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
             const uint32_t* const m = s_most + t;
             return group_exponent(max(max(m[0], m[Z::kRows]), max(m[2 * Z::kRows], m[3 * Z::kRows])) >> 23);
           };
+#pragma unroll 4
           for (int t = 0; t < rows; ++t) {
             const float v = sums[t * 256] * group_factor(exponent(t));
             const uint16_t high = e4m3x2(v, 0.0f);
             uint32_t back;
             asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(high));
             const uint16_t low = e4m3x2((v - dev::half_bits_to_float(back & 0xFFFFu)) * 16.0f, 0.0f);
-            uint8_t* const to = p.h_halves + ((size_t)place_of(item, t) * (p.inner / kGroup) + slice) * 256 + (me >> 4) * 32 + (me & 15);
+            uint8_t* const to = p.h_halves + (place_of(t) * (p.inner / kGroup) + slice) * 256 + (me >> 4) * 32 + (me & 15);
             to[0] = (uint8_t)high;
             to[16] = (uint8_t)low;
             float sum = v;
@@ -482,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
           if (!meet()) break;
           if (me < rows) {
             const float* const q = s_sums + me;
-            p.h_meta[(size_t)place_of(item, me) * (p.inner / kGroup) + slice] =
+            p.h_meta[(size_t)places * (p.inner / kGroup) + slice] =
                 group_meta(exponent(me), q[0] + q[Z::kRows] + q[2 * Z::kRows] + q[3 * Z::kRows], BITS);
           }
           if (!meet()) break;  // the maxima and sums may be written again
