@@ -167,8 +167,10 @@ struct Shape {
   static constexpr int kBlock = BITS == 4 ? kBlockBytesW4 : kBlockBytesW6;
   static constexpr int kB = 2 * kBlock, kUndo = kB + N * 128, kLess = kUndo + kRows * 4, kStage = (kLess + kRows * 4 + 127) / 128 * 128;
   static constexpr int kACols = BITS == 4 ? 32 : 64, kDCols = BITS == 4 ? N : 2 * N;
-  static constexpr int kBuffers = kColumns / 4 / (kACols + kDCols);  // of A and D, a team
-  static_assert(kBuffers == 1 || kBuffers == 2, "tensor memory");
+  // Of A and of D, a team: with two of A the next block becomes A while the last one's products are under way.
+  static constexpr int kTeamCols = kColumns / 4, kBuffers = 2 * kACols + kDCols <= kTeamCols ? 2 : 1;
+  static constexpr int kSums = kBuffers * (kACols + kDCols) <= kTeamCols ? kBuffers : 1;
+  static_assert(kBuffers * kACols + kSums * kDCols <= kTeamCols, "tensor memory");
   // [stages][exchange: units' sums by pairs, then the finishers' maxima and sums][barriers and flags]
   static constexpr int kUnits = N == 16 ? 2 : 1;  // units' sums that there is room for
   static constexpr int kExchange = kUnits * 2 * kRows * 256 * 4 + 2 * 4 * kRows * 4;
@@ -196,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
   extern __shared__ __align__(128) uint8_t s_mem[];
   float* const s_unit = reinterpret_cast<float*>(s_mem + Z::kStages * Z::kStage);  // [units][pair][rows][256]
   uint32_t* const s_most = reinterpret_cast<uint32_t*>(s_unit + Z::kUnits * 2 * Z::kRows * 256);
-  float* const s_sums = reinterpret_cast<float*>(s_most + 4 * Z::kRows);
+  int* const s_sums = reinterpret_cast<int*>(s_most + 4 * Z::kRows);
   Barriers& s = *reinterpret_cast<Barriers*>(s_mem + Z::kStages * Z::kStage + Z::kExchange);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint64_t limit = p.wait_ns;
@@ -315,7 +317,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
       if (elected()) {
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
-          const uint32_t a = tmem + ((pair * 2 + w) * Z::kBuffers + buffer) * (Z::kACols + Z::kDCols), d = a + Z::kACols;
+          const uint32_t at = tmem + (pair * 2 + w) * Z::kTeamCols, a = at + buffer * Z::kACols;
+          const uint32_t d = at + Z::kBuffers * Z::kACols + turn % Z::kSums * Z::kDCols;
 #pragma unroll
           for (int k = 0; k < 4; ++k) mma(d, a + 8 * k, b + k * (256 >> 4), kIdesc<N>, k > 0);
           if (BITS == 6) {
@@ -473,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
           // h = silu(gate) up of 128 neighbouring elements of each row: a group of down's, taken apart here
 #pragma unroll 4
           for (int t = 0; t < rows; ++t) {
-            const float v = 512.0f * sums[t * 256], h = v / (1.0f + expf(-v)) * (512.0f * sums[t * 256 + 128]);
+            const float v = 512.0f * sums[t * 256], h = __fdividef(v, 1.0f + expf(-v)) * (512.0f * sums[t * 256 + 128]);
             sums[t * 256] = h;
             const uint32_t m = __reduce_max_sync(~0u, __float_as_uint(h) & 0x7FFFFFFFu);
             if (lane == 0) s_most[quad * Z::kRows + t] = m;
@@ -493,16 +496,15 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
             uint8_t* const to = p.h_halves + (place_of(t) * (p.inner / kGroup) + slice) * 256 + (me >> 4) * 32 + (me & 15);
             to[0] = (uint8_t)high;
             to[16] = (uint8_t)low;
-            float sum = v;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+            // the sum in units of 2^-13, the low halves' last bit (|v| <= 2^8)
+            const int sum = __reduce_add_sync(~0u, __float2int_rn(v * 8192.0f));
             if (lane == 0) s_sums[quad * Z::kRows + t] = sum;
           }
           if (!meet()) break;
           if (me < rows) {
-            const float* const q = s_sums + me;
+            const int* const q = s_sums + me;
             p.h_meta[(size_t)places * (p.inner / kGroup) + slice] =
-                group_meta(exponent(me), q[0] + q[Z::kRows] + q[2 * Z::kRows] + q[3 * Z::kRows], BITS);
+                group_meta(exponent(me), (float)(q[0] + q[Z::kRows] + q[2 * Z::kRows] + q[3 * Z::kRows]) * 0x1p-13f, BITS);
           }
           if (!meet()) break;  // the maxima and sums may be written again
         }
@@ -518,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
   } else {
     // ------------------------------------------------------------------------------- the teams
     const int team = warp >> 2, pair = team >> 1, side = team & 1, quad = warp & 3, row = quad * 32 + lane;  // row of the tile
-    const uint32_t my_tmem = tmem + ((uint32_t)(quad * 32) << 16) + team * Z::kBuffers * (Z::kACols + Z::kDCols);
+    const uint32_t my_tmem = tmem + ((uint32_t)(quad * 32) << 16) + team * Z::kTeamCols;
     dev::f32x2 acc[Z::kRows / 2] = {};  // two rows each
     constexpr int kLag = Z::kBuffers - 1;  // the pair's steps from making A to adding up D
     const int steps = end - begin > pair ? (end - begin - pair + 1) / 2 : 0;  // the pair's: every other one
@@ -530,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
       if (n < steps) {
         if (!wait(&s.weights[stage], parity)) break;
         const uint8_t* const block = s_mem + (size_t)stage * Z::kStage + side * Z::kBlock;
-        const uint32_t at = my_tmem + buffer * (Z::kACols + Z::kDCols);
+        const uint32_t at = my_tmem + buffer * Z::kACols;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           uint32_t a[16];
@@ -569,11 +571,11 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
       };
       if (kLag == 0) announce();
       if (n >= kLag) {
-        // with two buffers the store goes on meanwhile
+        // with two buffers the store goes on meanwhile (and is announced behind this: there may be one D only)
         if (!wait(&s.done[pair][added_buffer], added_parity)) break;
         tmem_fence_after();
         const uint8_t* const st = s_mem + (size_t)added_stage * Z::kStage;
-        const uint32_t at = my_tmem + added_buffer * (Z::kACols + Z::kDCols) + Z::kACols;
+        const uint32_t at = my_tmem + Z::kBuffers * Z::kACols + (Z::kSums > 1 ? added_buffer * Z::kDCols : 0);
         const float scale = dev::half_bits_to_float(reinterpret_cast<const uint16_t*>(st + side * Z::kBlock)[scale_index(row)]);
         const dev::f32x2 scales = dev::f2_splat(scale);
         const ulonglong2* const undo = reinterpret_cast<const ulonglong2*>(st + Z::kUndo);  // of four rows each
