@@ -819,7 +819,7 @@ def _shaped(t, name: str, kind: str, shape: tuple, on: int):
     """Device pointer of a contiguous tensor of the kind and shape on device `on` (None -> NULL)."""
     if t is None:
         return None
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name}: expected {list(shape)}, got {list(t.shape)}")
     if t.get_device() == on and t.is_contiguous() and t.dtype in (_DTYPES.get(kind) or _dtypes(kind)):
         return t.data_ptr()

@@ -86,6 +86,7 @@ int woq_block_norm(const void* u, int u_dtype, const void* r, void* r_out, int r
   a.beta = beta;
   a.offset = offset;
   a.eps = eps;
+  a.inv_dim = 1.0f / (float)D;
   return cuda_result(launch_block_norm(a, (cudaStream_t)stream));
 }
 

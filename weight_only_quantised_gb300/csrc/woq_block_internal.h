@@ -20,7 +20,7 @@ struct BlockNorm {
   int u_f32, r_f32;
   int rows, dim;
   int rows_per_gate;
-  float alpha, beta, offset, eps;
+  float alpha, beta, offset, eps, inv_dim;
 };
 cudaError_t launch_block_norm(const BlockNorm& p, cudaStream_t stream);
 
@@ -36,6 +36,7 @@ struct Route {
   int groups, group_size, top_groups, group_best;
   int renormalise;
   float scale;
+  int scratch, group_magic, group_share;  // set by the launcher
 };
 cudaError_t launch_route(const Route& p, cudaStream_t stream);
 

@@ -8,43 +8,35 @@
 
 #include "woq_block_internal.h"
 #include "woq_device.cuh"
+#include "woq_internal.h"
 #include "woq_kv8_device.cuh"
 #include "woq_prologue.cuh"
 
 namespace woq {
 namespace block {
 
-template <bool F32>
-__device__ __forceinline__ void load8(const void* base, size_t at, float* v) {
-  if constexpr (F32) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
-    const float4 a = p[0], b = p[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  } else {
-    const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-  }
+typedef dev::f32x2 Pair;
+
+__device__ __forceinline__ Pair pair_of(uint32_t bf16x2) { return dev::f2_pack(bf16x2 << 16, bf16x2 & 0xFFFF0000u); }
+
+__device__ __forceinline__ uint32_t bf16_of(Pair v) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(__uint_as_float(dev::f2_hi(v))), "f"(__uint_as_float(dev::f2_lo(v))));
+  return d;
 }
 
 template <bool F32>
-__device__ __forceinline__ void store8(void* base, size_t at, const float* v) {
+__device__ __forceinline__ void store8(void* base, size_t at, const Pair* v) {
   if constexpr (F32) {
-    float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + at);
-    p[0] = make_float4(v[0], v[1], v[2], v[3]);
-    p[1] = make_float4(v[4], v[5], v[6], v[7]);
+    ulonglong2* p = reinterpret_cast<ulonglong2*>(static_cast<float*>(base) + at);
+    p[0] = make_ulonglong2(v[0], v[1]);
+    p[1] = make_ulonglong2(v[2], v[3]);
   } else {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = pro::f32_to_bf16_bits(v[2 * i]) | pro::f32_to_bf16_bits(v[2 * i + 1]) << 16;
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + at) = make_uint4(bf16_of(v[0]), bf16_of(v[1]), bf16_of(v[2]), bf16_of(v[3]));
   }
 }
+
+__device__ __forceinline__ float sum_of(Pair v) { return __uint_as_float(dev::f2_lo(v)) + __uint_as_float(dev::f2_hi(v)); }
 
 // Sum over the CTA, the same in every thread (fixed order).
 __device__ __forceinline__ float block_sum(float x, float* parts) {
@@ -52,94 +44,112 @@ __device__ __forceinline__ float block_sum(float x, float* parts) {
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
   if ((threadIdx.x & 31) == 0) parts[threadIdx.x >> 5] = x;
   __syncthreads();
-  const int lane = threadIdx.x & 31;
-  x = lane < (int)(blockDim.x >> 5) ? parts[lane] : 0.0f;
+  x = parts[threadIdx.x & 31];  // behind the last warp's there are zeros
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
   return x;
 }
 
-template <bool UF32, bool RF32, int VECS>
-__global__ void __launch_bounds__(1024) norm_kernel(const BlockNorm p) {
+// Eight elements as they lie in memory (bf16 takes half the registers so, and a third CTA fits an SM).
+template <bool F32>
+struct Raw {
+  uint4 v[F32 ? 2 : 1];
+  __device__ __forceinline__ void load(const void* base, size_t at) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + at * (F32 ? 4 : 2));
+    v[0] = p[0];
+    if (F32) v[F32] = p[1];
+  }
+  __device__ __forceinline__ Pair pair(int j) const {
+    const uint4 w = v[F32 ? j >> 1 : 0];
+    if constexpr (F32) return j & 1 ? dev::f2_pack(w.z, w.w) : dev::f2_pack(w.x, w.y);
+    else return pair_of(j == 0 ? w.x : j == 1 ? w.y : j == 2 ? w.z : w.w);
+  }
+};
+
+// A row a CTA, VECS vectors of 8 a thread; everything that a row takes is asked for at once, its weights before the wait for the
+// prior grid.  Bound by DRAM with what the two sums cost in latency: three CTAs of 640 threads an SM.
+template <bool UF32, bool RF32, int VECS, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS > 640 ? 1 : THREADS > 512 ? (UF32 || RF32 ? 2 : 3) : (UF32 || RF32 ? 3 : 4)) norm_kernel(const BlockNorm p) {
   __shared__ float s_parts[2][32];
-  const int row = blockIdx.x;
-  const size_t at = (size_t)row * p.dim;
+  const int warps = blockDim.x >> 5;
+  if (threadIdx.x < 64 && (int)(threadIdx.x & 31) >= warps) s_parts[threadIdx.x >> 5][threadIdx.x & 31] = 0.0f;
+  if (blockDim.x == 32) s_parts[1][threadIdx.x] = 0.0f;
+  const size_t at = (size_t)blockIdx.x * p.dim;
+  uint4 post[VECS] = {}, gate[VECS] = {}, pre[VECS] = {};
+#pragma unroll
+  for (int i = 0; i < VECS; ++i) {
+    const int c = (i * (int)blockDim.x + (int)threadIdx.x) * 8;
+    if (p.post && c < p.dim) post[i] = __ldg(reinterpret_cast<const uint4*>(p.post + c));
+    if (p.out && c < p.dim) pre[i] = __ldg(reinterpret_cast<const uint4*>(p.pre + c));
+  }
   dev::pdl_wait_prior_grids();
   dev::pdl_launch_dependents();
-  float u[VECS][8], r[VECS][8];
-  float ss = 0.0f;
+  Raw<UF32> u[VECS] = {};
+  Raw<RF32> r0[VECS] = {};
 #pragma unroll
   for (int i = 0; i < VECS; ++i) {
     const int c = (i * (int)blockDim.x + (int)threadIdx.x) * 8;
     if (c < p.dim) {
-      load8<UF32>(p.u, at + c, u[i]);
-      load8<RF32>(p.r, at + c, r[i]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) u[i][j] = r[i][j] = 0.0f;
+      u[i].load(p.u, at + c);
+      r0[i].load(p.r, at + c);
+      if (p.gate) gate[i] = *reinterpret_cast<const uint4*>(p.gate + (size_t)((int)blockIdx.x / p.rows_per_gate) * p.dim + c);
     }
   }
-  float f = 1.0f;
+  float f = p.beta;
+  Pair ss = 0;
   if (p.post) {
 #pragma unroll
     for (int i = 0; i < VECS; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(u[i][j], u[i][j], ss);
-    f = 1.0f / sqrtf(block_sum(ss, s_parts[0]) / (float)p.dim + p.eps);
+      for (int j = 0; j < 4; ++j) ss = dev::f2_fma(u[i].pair(j), u[i].pair(j), ss);
+    f *= rsqrtf(fmaf(block_sum(sum_of(ss), s_parts[0]), p.inv_dim, p.eps));
   }
-  const size_t gate_at = (size_t)(row / p.rows_per_gate) * p.dim;
-  ss = 0.0f;
+  const Pair fs = dev::f2_splat(f), alpha = dev::f2_splat(p.alpha), offset = dev::f2_splat(p.offset);
+  Pair r[VECS][4];
+  ss = 0;
 #pragma unroll
   for (int i = 0; i < VECS; ++i) {
     const int c = (i * (int)blockDim.x + (int)threadIdx.x) * 8;
     if (c >= p.dim) continue;
-    float w[8];
-    if (p.post) {
-      load8<false>(p.post, c, w);
+    const uint32_t pw[4] = {post[i].x, post[i].y, post[i].z, post[i].w}, gw[4] = {gate[i].x, gate[i].y, gate[i].z, gate[i].w};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) u[i][j] = u[i][j] * f * (w[j] + p.offset);
-    }
-    if (p.gate) {
-      load8<false>(p.gate, gate_at + c, w);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) u[i][j] *= w[j];
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      r[i][j] = fmaf(p.alpha, r[i][j], p.beta * u[i][j]);
-      ss = fmaf(r[i][j], r[i][j], ss);
+    for (int j = 0; j < 4; ++j) {
+      Pair v = dev::f2_mul(u[i].pair(j), fs);
+      if (p.post) v = dev::f2_mul(v, dev::f2_add(pair_of(pw[j]), offset));
+      if (p.gate) v = dev::f2_mul(v, pair_of(gw[j]));
+      r[i][j] = dev::f2_fma(alpha, r0[i].pair(j), v);
+      ss = dev::f2_fma(r[i][j], r[i][j], ss);
     }
     store8<RF32>(p.r_out, at + c, r[i]);
   }
   if (!p.out) return;
-  f = 1.0f / sqrtf(block_sum(ss, s_parts[1]) / (float)p.dim + p.eps);
+  const Pair g = dev::f2_splat(rsqrtf(fmaf(block_sum(sum_of(ss), s_parts[1]), p.inv_dim, p.eps)));
 #pragma unroll
   for (int i = 0; i < VECS; ++i) {
     const int c = (i * (int)blockDim.x + (int)threadIdx.x) * 8;
     if (c >= p.dim) continue;
-    float w[8];
-    load8<false>(p.pre, c, w);
+    const uint32_t qw[4] = {pre[i].x, pre[i].y, pre[i].z, pre[i].w};
+    Pair w[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) r[i][j] = r[i][j] * f * (w[j] + p.offset);
-    store8<false>(p.out, at + c, r[i]);
+    for (int j = 0; j < 4; ++j) w[j] = dev::f2_mul(dev::f2_mul(r[i][j], g), dev::f2_add(pair_of(qw[j]), offset));
+    store8<false>(p.out, at + c, w);
   }
 }
 
-template <int VECS>
-static cudaError_t launch_vecs(const BlockNorm& p, cudaStream_t s) {
-  const int vectors = p.dim / 8;
-  const int threads = ((vectors + VECS - 1) / VECS + 31) / 32 * 32;
-  auto kernel = p.u_f32 ? (p.r_f32 ? norm_kernel<true, true, VECS> : norm_kernel<true, false, VECS>)
-                        : (p.r_f32 ? norm_kernel<false, true, VECS> : norm_kernel<false, false, VECS>);
+template <bool UF32, bool RF32>
+static cudaError_t launch_types(const BlockNorm& p, cudaStream_t s) {
+  const int vectors = p.dim / 8, vecs = vectors <= 1024 ? 1 : 2;
+  const int threads = ((vectors + vecs - 1) / vecs + 31) / 32 * 32;
+  // a vector a thread up to 8,192 elements (with two or four, 8,190 x 5120 takes 77 or 89 us instead of 72)
+  auto kernel = vecs == 2 ? norm_kernel<UF32, RF32, 2, 1024> : threads <= 512 ? norm_kernel<UF32, RF32, 1, 512> : threads <= 640 ? norm_kernel<UF32, RF32, 1, 640> : norm_kernel<UF32, RF32, 1, 1024>;
   return kv8::launch(kernel, dim3((unsigned)p.rows), threads, 0, s, p);
 }
 
 }  // namespace block
 
 cudaError_t launch_block_norm(const BlockNorm& p, cudaStream_t s) {
-  const int vectors = p.dim / 8;
-  if (vectors <= 1024) return block::launch_vecs<1>(p, s);
-  return block::launch_vecs<2>(p, s);
+  if (p.u_f32) return p.r_f32 ? block::launch_types<true, true>(p, s) : block::launch_types<true, false>(p, s);
+  return p.r_f32 ? block::launch_types<false, true>(p, s) : block::launch_types<false, false>(p, s);
 }
 
 }  // namespace woq

@@ -33,10 +33,10 @@ __device__ __forceinline__ unsigned long long warp_max(unsigned long long v) {
   const uint32_t lo = __reduce_max_sync(kAll, (uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
   return (unsigned long long)hi << 32 | lo;
 }
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
-  return v;
+__device__ __forceinline__ float warp_max(float v) {  // NaN aside
+  float d;
+  asm("redux.sync.max.f32 %0, %1, 0xFFFFFFFF;" : "=f"(d) : "f"(v));
+  return d;
 }
 template <class F>
 __device__ __forceinline__ F warp_sum(F v) {
@@ -72,10 +72,12 @@ __device__ __forceinline__ float logit(const Route& p, size_t at) {
 }
 
 template <int PER>
-__device__ __forceinline__ void load_row(const Route& p, int row, int lane, float (&l)[PER]) {
+__device__ __forceinline__ void load_row(const Route& p, int row, int lane, float (&l)[PER], float (&b)[PER]) {
   const size_t at = (size_t)row * p.stride;
 #pragma unroll
   for (int j = 0; j < PER; ++j) l[j] = lane + 32 * j < p.experts ? logit(p, at + lane + 32 * j) : -kInf;
+#pragma unroll
+  for (int j = 0; j < PER; ++j) b[j] = p.bias && lane + 32 * j < p.experts ? __ldg(p.bias + lane + 32 * j) : 0.0f;
 }
 
 // Largest logit and the softmax's denominator (0 and 1 for the sigmoid, and for a row without experts).
@@ -96,124 +98,244 @@ __device__ __forceinline__ void softmax_terms(const Route& p, const float (&l)[P
   *sum = warp_sum(t);
 }
 
+__device__ __forceinline__ float inverse(float x) { return __fdividef(1.0f, x); }  // within 2 ulp; 0 from 2^126 on
+__device__ __forceinline__ double inverse(double x) { return 1.0 / x; }
+
 // c of one expert that may be chosen (NaN and, under softmax, +inf come first).
 template <class F>
-__device__ __forceinline__ F value(const Route& p, float l, int e, float m, F sum) {
+__device__ __forceinline__ F value(const Route& p, float l, float b, float m, F sum) {
   if (l != l || (p.softmax && l == kInf)) return (F)kInf;
   F s;
-  if (p.softmax) s = m == kInf ? (F)0 : exp_of((F)l - (F)m) / sum;
-  else s = (F)1 / ((F)1 + exp_of(-(F)l));
-  const F c = s + (p.bias ? (F)__ldg(p.bias + e) : (F)0);
+  if (p.softmax) s = m == kInf ? (F)0 : exp_of((F)l - (F)m) * inverse(sum);
+  else s = inverse((F)1 + exp_of(-(F)l));
+  const F c = s + (F)b;
   return c != c ? (F)kInf : c;
 }
 
-// The choice of one row.  l: the lane's logits (expert lane + 32 j); chosen: lane i < k gets the i-th expert, else -1.
-// Returns whether F tells every score that matters from its neighbour.
+// Scores c of the lane's experts (bit j of `can`: it may be chosen), without a bias the logits themselves.
 template <class F, int PER>
-__device__ __forceinline__ bool choose(const Route& p, const float (&l)[PER], float m, F sum, F* shared, int lane, int* chosen) {
-  typedef typename Key<F>::type K;
-  const bool by_logit = p.bias == nullptr;
-  const float rel = p.softmax ? 0x1p-16f : 0x1p-19f;  // twice the relative error of s in fp32, and more
-  bool sure = true;
-  unsigned kept = kAll;
-  if (p.groups > 1) {
-    const bool max_logit = by_logit && p.group_best == 1;
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      const int e = lane + 32 * j;
-      if (e >= p.experts) continue;
-      shared[e] = l[j] == -kInf ? (F)-kInf : max_logit ? (l[j] != l[j] ? (F)kInf : (F)l[j]) : value<F>(p, l[j], e, m, sum);
-    }
-    __syncwarp();
-    F best = -kInf, next = -kInf;  // of group `lane`
-    if (lane < p.groups) {
-      const F* c = shared + lane * p.group_size;
-      int i = lane % p.group_size;  // lanes start at different members: fewer bank conflicts
-      for (int n = 0; n < p.group_size; ++n) {
-        next = fmax(next, fmin(best, c[i]));
-        best = fmax(best, c[i]);
-        if (++i == p.group_size) i = 0;
-      }
-    }
-    __syncwarp();
-    const F score = p.group_best == 1 ? best : next == (F)-kInf ? (F)-kInf : best + next;
-    int rank = 0;
-    for (int g = 0; g < p.groups; ++g) {
-      const F other = __shfl_sync(kAll, score, g);
-      rank += other > score || (other == score && g < lane);
-    }
-    const bool group = lane < p.groups, in = group && rank < p.top_groups;
-    kept = __ballot_sync(kAll, in);
-    if (sizeof(F) == 4 && !max_logit && p.top_groups < p.groups) {
-      const float big = warp_max(group && score > -kInf && score < kInf ? fmaxf(fabsf((float)best), fabsf((float)next)) : 0.0f);
-      const float low = -warp_max(in ? -(float)score : -kInf);  // of the kept
-      const float high = warp_max(group && !in ? (float)score : -kInf);
-      // s <= 1, and two of them at most make a group's score
-      if (low < kInf && high > -kInf && low - high <= 4.0f * rel + 0x1p-20f * big) sure = false;
-    }
-  }
-  K key[PER];
-#pragma unroll
-  for (int j = 0; j < PER; ++j) {
-    const int e = lane + 32 * j;
-    key[j] = 0;
-    if (l[j] == -kInf || e >= p.experts || (p.groups > 1 && !(kept >> (e / p.group_size) & 1))) continue;
-    key[j] = order(by_logit ? (l[j] != l[j] ? (F)kInf : (F)l[j]) : value<F>(p, l[j], e, m, sum) + (F)0);
-  }
-  K top = 0;
-  int at = 0;
+__device__ __forceinline__ void scores(const Route& p, const float (&l)[PER], const float (&b)[PER], float m, F sum, bool by_logit, F (&c)[PER],
+                                       uint32_t& can) {
+  can = 0;
 #pragma unroll
   for (int j = 0; j < PER; ++j)
-    if (key[j] > top) top = key[j], at = j;
-  *chosen = -1;
-  float last = 0.0f, last_l = 0.0f, last_b = 0.0f;
-  const bool check = sizeof(F) == 4 && !by_logit;
-  const int rounds = check ? p.k + 1 : p.k;  // the next one too, to compare with
+    if (l[j] != -kInf) can |= 1u << j;  // experts that there are not have -inf too
+  if (by_logit) {
+#pragma unroll
+    for (int j = 0; j < PER; ++j) c[j] = l[j] != l[j] ? (F)kInf : (F)l[j];
+  } else {
+#pragma unroll
+    for (int j = 0; j < PER; ++j) c[j] = l[j] == -kInf ? (F)-kInf : value<F>(p, l[j], b[j], m, sum);
+  }
+}
+
+// Which groups are kept (bit g).  c: as of scores (without a bias and with group_best 2: of the scores proper).  Returns whether F
+// tells the last one kept from the first one dropped.
+template <class F, int PER>
+__device__ __forceinline__ bool keep_groups(const Route& p, const F (&c)[PER], F* shared, int lane, unsigned* kept) {
+#pragma unroll
+  for (int j = 0; j < PER; ++j)
+    if (lane + 32 * j < p.experts) shared[lane + 32 * j] = c[j];
+  __syncwarp();
+  // `share` lanes look at each group's members in turn, each beginning at another one (fewer bank conflicts)
+  const int share = p.group_share, group = lane / share, part = lane & (share - 1);
+  F best = -kInf, next = -kInf;
+  if (group < p.groups) {
+    const F* const of = shared + group * p.group_size;
+    int i = part + share * (group % max(1, p.group_size / share));
+    for (int n = part; n < p.group_size; n += share) {
+      if (i >= p.group_size) i = part;
+      next = fmax(next, fmin(best, of[i]));
+      best = fmax(best, of[i]);
+      i += share;
+    }
+  }
+  __syncwarp();
+  for (int o = 1; o < share; o <<= 1) {
+    const F other = __shfl_xor_sync(kAll, best, o), other_next = __shfl_xor_sync(kAll, next, o);
+    next = fmax(fmax(next, other_next), fmin(best, other));
+    best = fmax(best, other);
+  }
+  // lane g takes group g
+  best = __shfl_sync(kAll, best, min(lane * share, 31));
+  next = __shfl_sync(kAll, next, min(lane * share, 31));
+  const F score = p.group_best == 1 ? best : next == (F)-kInf ? (F)-kInf : best + next;
+  int rank = 0;
+  for (int g = 0; g < p.groups; ++g) {
+    const F other = __shfl_sync(kAll, score, g);
+    rank += other > score || (other == score && g < lane);
+  }
+  const bool real = lane < p.groups, in = real && rank < p.top_groups;
+  *kept = __ballot_sync(kAll, in);
+  if (sizeof(F) == 8 || (!p.bias && p.group_best == 1) || p.top_groups == p.groups) return true;
+  const float rel = p.softmax ? 0x1p-16f : 0x1p-19f;
+  const float big = warp_max(real && score > -kInf && score < kInf ? fmaxf(fabsf((float)best), fabsf((float)next)) : 0.0f);
+  const float low = -warp_max(in ? -(float)score : -kInf);  // of the kept
+  const float high = warp_max(real && !in ? (float)score : -kInf);
+  // s <= 1, and two of them at most make a group's score
+  return !(low < kInf && high > -kInf && low - high <= 4.0f * rel + 0x1p-20f * big);
+}
+
+template <int PER>
+__device__ __forceinline__ uint32_t in_kept_groups(const Route& p, unsigned kept, int lane) {
+  uint32_t in = 0;
+#pragma unroll
+  for (int j = 0; j < PER; ++j)
+    in |= (kept >> ((lane + 32 * j) * p.group_magic >> 20 & 31) & 1u) << j;  // (places behind the last expert: any)
+  return in;
+}
+
+// The k best of those that `can`; one more where `extra`.  Lane i gets the i-th one's expert (else -1) and order.
+template <class F, int PER>
+__device__ __forceinline__ int best_of(const Route& p, const F (&c)[PER], uint32_t can, bool extra, int lane, typename Key<F>::type* mine,
+                                       uint32_t* shared) {
+  typedef typename Key<F>::type K;
+  K key[PER];
+#pragma unroll
+  for (int j = 0; j < PER; ++j) key[j] = can >> j & 1u ? order(c[j] + (F)0) : (K)0;
+  K top = 0;
+#pragma unroll
+  for (int j = 0; j < PER; ++j) top = key[j] > top ? key[j] : top;
+  int chosen = -1;
+  *mine = 0;
+  const int rounds = p.k + (extra && p.k < 32);
+  if constexpr (sizeof(F) == 4 && PER > 2) {
+    // As many lanes' largest as are wanted: nothing below the least of these is among the best.  What is not below (some ten
+    // experts) goes to a lane each, and is placed by comparing all with all.
+    K rest = top, least = 0;
+    int lanes = 0;
+    while (lanes < rounds) {
+      const K best = warp_max(rest);
+      if (best == 0) break;
+      least = best;
+      lanes += __popc(__ballot_sync(kAll, rest == best));
+      if (rest == best) rest = 0;
+    }
+    if (lanes < rounds) least = 1;  // all that can be chosen
+    unsigned has[PER];
+    int total = 0;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      has[j] = __ballot_sync(kAll, key[j] >= least);
+      total += __popc(has[j]);
+    }
+    if (total <= 32) {
+      int base = 0;
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        if (key[j] >= least) {
+          const int at = base + __popc(has[j] & ((1u << lane) - 1));
+          shared[at] = key[j];
+          shared[32 + at] = lane + 32 * j;
+        }
+        base += __popc(has[j]);
+      }
+      __syncwarp();
+      const K k = lane < total ? shared[lane] : 0;
+      const uint32_t e = shared[32 + lane];
+      int place = 0;
+      // among equals the lower number first: the list runs over j, then over lanes
+      for (int i = 0; i < total; ++i) {
+        const K other = shared[i];
+        place += other > k || (other == k && i < lane);
+      }
+      if (lane < total) {
+        shared[64 + place] = k;
+        shared[96 + place] = e;
+      }
+      __syncwarp();
+      const bool mine_too = lane < total && lane < rounds;
+      if (mine_too) *mine = shared[64 + lane], chosen = (int)shared[96 + lane];
+      __syncwarp();
+      return chosen;
+    }
+  }
   for (int n = 0; n < rounds; ++n) {
     const K best = warp_max(top);
     if (best == 0) break;
-    const int e = (int)__reduce_min_sync(kAll, top == best ? (unsigned)(lane + 32 * at) : kAll);
-    if (lane == n && n < p.k) *chosen = e;
-    if (check) {
-      float mine = l[0];
+    int at = 0;
 #pragma unroll
-      for (int j = 1; j < PER; ++j)
-        if (j == e >> 5) mine = l[j];
-      const float el = __shfl_sync(kAll, mine, e & 31), eb = __ldg(p.bias + e);
-      const uint32_t bits = (uint32_t)best;
-      const float c = __uint_as_float(bits & 0x80000000u ? bits ^ 0x80000000u : ~bits);
-      if (n > 0 && last < kInf && !(el == last_l && eb == last_b)) {
-        const float near = rel * (fabsf(last - last_b) + fabsf(c - eb)) + 0x1p-21f * (fabsf(last) + fabsf(c));
-        if (last - c <= near) sure = false;
-      }
-      last = c, last_l = el, last_b = eb;
-    }
+    for (int j = PER - 1; j >= 0; --j) at = key[j] == best ? j : at;
+    const unsigned owners = __ballot_sync(kAll, top == best);
+    // one lane has it, or the lowest number of those that have
+    int e;
+    if ((owners & (owners - 1)) == 0) e = __shfl_sync(kAll, lane + 32 * at, __ffs(owners) - 1);
+    else e = (int)__reduce_min_sync(kAll, top == best ? (unsigned)(lane + 32 * at) : kAll);
+    if (lane == n) chosen = e, *mine = best;
     if ((e & 31) == lane) {
       top = 0;
 #pragma unroll
       for (int j = 0; j < PER; ++j) {
         if (j == e >> 5) key[j] = 0;
-        if (key[j] > top) top = key[j], at = j;
+        top = key[j] > top ? key[j] : top;
       }
     }
   }
-  return sure;
+  return chosen;
 }
 
+// All of a row in 64 bits.
 template <int PER>
 __device__ __noinline__ int choose_in_64_bits(const Route& p, int row, double* shared, int lane) {
-  float l[PER], m;
-  load_row<PER>(p, row, lane, l);
-  double sum;
-  int chosen;
+  float l[PER], b[PER], m;
+  load_row<PER>(p, row, lane, l, b);
+  double sum, c[PER];
   softmax_terms<double, PER>(p, l, &m, &sum);
-  choose<double, PER>(p, l, m, sum, shared, lane, &chosen);
+  uint32_t can;
+  if (p.groups > 1) {
+    unsigned kept;
+    scores<double, PER>(p, l, b, m, sum, !p.bias && p.group_best == 1, c, can);
+    keep_groups<double, PER>(p, c, shared, lane, &kept);
+    can &= in_kept_groups<PER>(p, kept, lane);
+  }
+  uint32_t all;
+  scores<double, PER>(p, l, b, m, sum, !p.bias, c, all);
+  unsigned long long key;
+  const int e = best_of<double, PER>(p, c, p.groups > 1 ? can : all, false, lane, &key, nullptr);
+  return lane < p.k ? e : -1;
+}
+
+// The order of a few experts in 64 bits: those whose fp32 score is not surely below the k-th's (bits of `few`, 64 at most;
+// sigmoid only).  Lane i gets the i-th.
+template <int PER>
+__device__ __noinline__ int choose_few(const Route& p, int row, uint32_t few, double* shared, int lane) {
+  float l[PER], b[PER];
+  load_row<PER>(p, row, lane, l, b);
+  int before = __popc(few), total;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(kAll, before, o);
+    if (lane >= o) before += y;
+  }
+  total = __shfl_sync(kAll, before, 31);
+  before -= __popc(few);
+  int* const experts = reinterpret_cast<int*>(shared + 64);
+#pragma unroll
+  for (int j = 0; j < PER; ++j)
+    if (few >> j & 1u) experts[before++] = lane + 32 * j;
+  __syncwarp();
+  for (int i = lane; i < total; i += 32) {
+    const float x = logit(p, (size_t)row * p.stride + experts[i]);
+    shared[i] = value<double>(p, x, __ldg(p.bias + experts[i]), 0.0f, 1.0);
+  }
+  __syncwarp();
+  int chosen = -1;
+  int* const out = experts + 64;
+  for (int i = lane; i < total; i += 32) {
+    const double v = shared[i];
+    const int e = experts[i];
+    int rank = 0;
+    for (int j = 0; j < total; ++j) rank += shared[j] > v || (shared[j] == v && experts[j] < e);
+    if (rank < 32) out[rank] = e;
+  }
+  __syncwarp();
+  if (lane < p.k && lane < total) chosen = out[lane];
   return chosen;
 }
 
 template <int PER>
 __global__ void __launch_bounds__(kWarps * 32) route_kernel(const Route p) {
-  extern __shared__ double s_scores[];  // with groups: [kWarps][experts]
+  extern __shared__ double s_scores[];  // [kWarps][scratch]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int row = blockIdx.x * kWarps + warp;
   dev::pdl_wait_prior_grids();
@@ -227,32 +349,74 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const Route p) {
     }
     return;
   }
-  double* shared = s_scores + warp * p.experts;
-  float l[PER], m, sum;
-  load_row<PER>(p, row, lane, l);
+  double* const shared = s_scores + warp * p.scratch;
+  float l[PER], b[PER], m, sum, c[PER];
+  load_row<PER>(p, row, lane, l, b);
   bool bad = false;
 #pragma unroll
-  for (int j = 0; j < PER; ++j) bad |= l[j] != l[j] || (p.softmax && l[j] == kInf);
+  for (int j = 0; j < PER; ++j) bad |= !(l[j] < kInf) && (l[j] != l[j] || p.softmax);
   bad = __any_sync(kAll, bad);
   softmax_terms<float, PER>(p, l, &m, &sum);
-  int chosen;
-  if (!choose<float, PER>(p, l, m, sum, reinterpret_cast<float*>(shared), lane, &chosen))
-    chosen = choose_in_64_bits<PER>(p, row, shared, lane);
+  uint32_t can, kept_members = kAll;
+  bool sure = true;
+  if (p.groups > 1) {
+    unsigned kept;
+    scores<float, PER>(p, l, b, m, sum, !p.bias && p.group_best == 1, c, can);
+    sure = keep_groups<float, PER>(p, c, reinterpret_cast<float*>(shared), lane, &kept);
+    kept_members = in_kept_groups<PER>(p, kept, lane);
+    if (!p.bias && p.group_best == 2) scores<float, PER>(p, l, b, m, sum, true, c, can);
+  } else {
+    scores<float, PER>(p, l, b, m, sum, !p.bias, c, can);
+  }
+  can &= kept_members;
+  uint32_t key;
+  int chosen = best_of<float, PER>(p, c, can, p.bias != nullptr, lane, &key, reinterpret_cast<uint32_t*>(shared));
+  const bool has_x = chosen >= 0;
+  const float x = has_x ? logit(p, (size_t)row * p.stride + chosen) : -kInf;
+  bool again = !sure;
+  uint32_t few = 0;
+  if (p.bias) {
+    // each chosen one (and the next) against the one before it
+    const float eb = has_x ? __ldg(p.bias + chosen) : 0.0f;
+    const float v = __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
+    const float v0 = __shfl_up_sync(kAll, v, 1), b0 = __shfl_up_sync(kAll, eb, 1), x0 = __shfl_up_sync(kAll, x, 1);
+    const float rel = p.softmax ? 0x1p-16f : 0x1p-19f;  // twice the relative error of s in fp32, and more
+    const float slack = rel * (fabsf(v0 - b0) + fabsf(v - eb)) + 0x1p-21f * (fabsf(v0) + fabsf(v)) + 0x1p-120f;  // s may underflow
+    const bool near = lane > 0 && has_x && v0 < kInf && !(x == x0 && eb == b0) && v0 - v <= slack;
+    if (p.k == 32 && !again) again = true;  // there is no lane for the next one
+    if (__any_sync(kAll, near)) {
+      // what is not surely below the k-th: the scores' own errors are rel (c - b) / 2 and 2^-22 c at most
+      const float kth = __shfl_sync(kAll, v, p.k - 1);
+      const bool full = __shfl_sync(kAll, has_x, p.k - 1);
+      if (!p.softmax && !again && !bad) {
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+          if ((can >> j & 1u) && (!full || c[j] + 2.0f * (rel * (1.0f + fabsf(kth) + fabsf(c[j])))  >= kth)) few |= 1u << j;
+        if (__reduce_add_sync(kAll, (unsigned)__popc(few)) > 64u) few = 0, again = true;
+        else again = false;
+        if (!again) chosen = choose_few<PER>(p, row, few, shared, lane);
+      } else {
+        again = true;
+      }
+    }
+  }
+  if (again) chosen = choose_in_64_bits<PER>(p, row, shared, lane);
+  if (lane >= p.k) chosen = -1;
   // weights, from the chosen logits
   const bool has = chosen >= 0;
-  const float x = has ? logit(p, (size_t)row * p.stride + chosen) : -kInf;
+  const float y = has ? logit(p, (size_t)row * p.stride + chosen) : -kInf;
   float w = 0.0f;
   if (p.renormalise) {
     // s up to a factor that all share, such that the largest is near 1 (softmax) or its s (a sigmoid that has not underflowed)
-    const float most = warp_max(x);
+    const float most = warp_max(y);
     if (has) {
-      if (p.softmax) w = expf(x - most);
-      else w = expf(fminf(x, 0.0f) - fminf(most, 0.0f)) / (1.0f + expf(-fabsf(x)));
+      if (p.softmax) w = expf(y - most);
+      else w = expf(fminf(y, 0.0f) - fminf(most, 0.0f)) / (1.0f + expf(-fabsf(y)));
     }
     const float total = warp_sum(w);
     w = has ? w / total : 0.0f;
   } else if (has) {
-    w = p.softmax ? expf(x - m) / sum : 1.0f / (1.0f + expf(-x));
+    w = p.softmax ? expf(y - m) / sum : 1.0f / (1.0f + expf(-y));
   }
   if (lane < p.k) {
     p.ids[out] = chosen;
@@ -261,8 +425,13 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const Route p) {
 }
 
 template <int PER>
-static cudaError_t launch_per(const Route& p, cudaStream_t s) {
-  const size_t smem = p.groups > 1 ? (size_t)kWarps * p.experts * 8 : 0;  // 32 KB at most
+static cudaError_t launch_per(Route p, cudaStream_t s) {
+  // scores of a row in 64 bits, and at least room for 64 of them with their experts and places
+  p.scratch = p.groups > 1 && p.experts > 128 ? p.experts : 128;
+  p.group_magic = (int)(((1u << 20) + p.group_size - 1) / p.group_size);  // e * magic >> 20 = e / group_size for e < 1024
+  p.group_share = 1;
+  while (p.group_share * 2 * p.groups <= 32) p.group_share *= 2;
+  const size_t smem = (size_t)kWarps * p.scratch * 8;  // 32 KB at most
   return kv8::launch(route_kernel<PER>, dim3((unsigned)((p.rows + kWarps - 1) / kWarps)), kWarps * 32, smem, s, p);
 }
 
