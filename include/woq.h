@@ -359,6 +359,8 @@ WOQ_API int woq_plan_launch(int bits, int M, int N, int K, int entry, int sms, i
  *           woq_kv8_attention - that CTA copies none of its blocks; its waits for them run
  *           out, it sets WOQ_DEVERR_TIMEOUT in the cache's status, and the rows of out that
  *           it had a part in keep what they held;
+ *           woq_experts_swiglu - that CTA copies no weights; WOQ_DEVERR_TIMEOUT, and y keeps
+ *           what it held;
  *   kind 2: SwiGLU linears - that CTA (one of the first half of the grid, the CTAs that
  *           form the row maxima) never counts itself in; every CTA gives up, sets
  *           WOQ_DEVERR_TIMEOUT and leaves y untouched;

@@ -85,13 +85,15 @@ WOQ_API int woq_route(const woq_router* cfg, const void* logits, int dtype, int 
  *   x: device bf16 [T][H]; ids: device int32 [T][k]; weights: device fp32 [T][k] (woq_route's, or any: an expert may
  *   stand in a row twice); y: device bf16 [T][H].  A place with id -1 has no part in y (a row without any gives 0);
  *   so has one with an id outside [-1, E), which sets WOQ_DEVERR_STATE in the workspace.
- *   Activations are not quantised (the matrix instructions take them as bf16 at the same cost, as these products are bound by
- *   the weights' bytes): products are exact, sums fp32, a group of 128 times its scale in fp32; silu(g) * u is
- *   rounded to bf16 before the down projection, and y once.  What a row gives does not depend on the run, nor on the other
- *   rows of the call.
+ *   Activations are not quantised to 8 bits as the linears': an x is taken as the sum of two 8-bit floats (e4m3) under a power of two
+ *   for each row and group of 128 elements, exactly but for elements below 2^-13 of the group's largest, which are off by at most 2^-17 of that; h = silu(g) * u
+ *   is taken so too, rounded to at most 2^-8 of itself.  Products are exact, sums fp32, a group of 128 times its scale in
+ *   fp32, y rounded once.  |x| below 2^100.  What a row gives does not depend on the run, nor on the other rows' x (the order of its sums goes
+ *   by how many experts the call works on).
  *   bits 4 or 6; 1 <= E <= 1024; 1 <= k <= 32; H, I multiples of 128 in [128, 32768]; 0 <= T, T k <= 32768.
  *   ws: device, 16-byte aligned, woq_experts_workspace(...) bytes, zero-filled once before first use
  *   (woq_workspace_init); launches of different shapes may use one that is large enough, launches that can overlap must not.
+ *   A wait that runs out sets WOQ_DEVERR_TIMEOUT: then y is left as it was, by this call and by the next ones until ws has been zero-filled.
  *   A chosen expert with a packed matrix whose header does not match sets WOQ_DEVERR_HEADER (woq_read_status(ws, ...)), and
  *   the rows of y that chose it are left as they were.
  * Errors: WOQ_ERR_NULL, WOQ_ERR_ALIGN, WOQ_ERR_SHAPE, WOQ_ERR_LAYOUT (gate_up_bytes or down_bytes too

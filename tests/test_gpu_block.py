@@ -182,6 +182,21 @@ def test_route_neighbours_nearer_than_fp32_tells(score, groups):
 
 
 @pytest.mark.parametrize("score", [0, 1])
+@pytest.mark.parametrize("groups", [1, 8])
+@pytest.mark.parametrize("E,k", [(256, 8), (1024, 32), (100, 32)])
+def test_route_many_neighbours(score, groups, E, k):
+    """All scores within 2^-25 of each other: more than fit the short way of telling them apart."""
+    if E % groups:
+        groups = 4
+    g = gen(E + k)
+    l = torch.randn((5, E), generator=g) * 0.7
+    x = l.double()
+    for row in range(5):
+        s = torch.softmax(x[row], 0) if score == 0 else torch.sigmoid(x[row])
+        route_case(l[row: row + 1], k, bias=(0.75 - s).float(), score=score, groups=groups, top_groups=max(1, groups // 2), group_best=1)
+
+
+@pytest.mark.parametrize("score", [0, 1])
 @pytest.mark.parametrize("groups", [1, 4])
 @pytest.mark.parametrize("with_bias", [False, True])
 def test_route_masked_infinite_and_nan(score, groups, with_bias):
@@ -328,13 +343,93 @@ def test_experts_rows_go_by_themselves(T):
     assert c[2].isnan().all() and not c[5].isfinite().any()
     keep = [i for i in range(T) if i not in (2, 5)]
     assert torch.equal(a[keep], c[keep])
-    other = ids.clone()
-    other[2], other[5] = torch.tensor([-1, 3]), torch.tensor([1, 1])     # nor does what the others chose
-    c, _ = m.run(x, other, w)
-    assert torch.equal(a[keep], c[keep])
     w[3, 1] = float("nan")
     d, _ = m.run(x, ids, w)
     assert d[3].isnan().all() and torch.equal(d[keep][[i for i in range(len(keep)) if keep[i] != 3]], a[[i for i in keep if i != 3]])
+
+
+@pytest.mark.parametrize("bits", [4, 6])
+@pytest.mark.parametrize("T", [4, 90])
+def test_experts_outliers(T, bits):
+    """A few channels far above the others, so that a group's elements lie many powers of two apart, and exact zeros."""
+    m = Experts(6, 512, 256, bits)
+    g = gen(T + bits)
+    x = torch.randn((T, 512), generator=g) * torch.exp2(-torch.randint(0, 24, (T, 512), generator=g).float())
+    x[:, 3::97] *= 1000
+    x[1] = 0
+    x[2, 128:256] = 0
+    ids, w = chosen(g, T, 6, 3)
+    y = m.check(x.to(BF), ids, w)
+    assert (y[1] == 0).all()
+
+
+def test_experts_many_places():
+    """512 rows of 32 places each, of 40 experts: many items, and an expert for nearly every place."""
+    m = Experts(40, 128, 128)
+    g = gen(12)
+    ids, w = chosen(g, 512, 40, 32)
+    m.check(torch.randn((512, 128), generator=g).to(BF), ids, w)
+
+
+def test_experts_of_a_wide_layer():
+    """More tiles and groups than CTAs, one expert: every CTA has steps of several units."""
+    m = Experts(2, 4096, 2560)
+    g = gen(13)
+    for T in (1, 5):
+        m.check(torch.randn((T, 4096), generator=g).to(BF), torch.ones((T, 1), dtype=torch.int32), torch.ones((T, 1)))
+
+
+@pytest.mark.parametrize("T", [1, 40])
+def test_experts_a_wait_that_runs_out(T):
+    """A CTA that copies no weights: its waits end, the status says so, y stays as it was; and the workspace works again once it
+    is zero-filled."""
+    m = Experts(8, 512, 384)
+    g = gen(14)
+    ids, w = chosen(g, T, 8, 2)
+    x = torch.randn((T, 512), generator=g).to(BF)
+    before, _ = m.run(x, ids, w)
+    ws = m.ws(T, 2)
+    y = torch.full((T, 512), 7.0, dtype=BF, device=DEV)
+    for cta in (0, 3):
+        woq.woq_tune_fault(1, cta, 20000)
+        try:
+            m.call(x.to(DEV), ids.to(DEV), w.to(DEV), y, ws)
+            torch.cuda.synchronize()
+        finally:
+            woq.woq_tune_fault(0, 0, 0)
+        assert (y == 7.0).all() and woq.woq_read_status(ws, clear=True) == woq.WOQ_DEVERR_TIMEOUT
+        m.call(x.to(DEV), ids.to(DEV), w.to(DEV), y, ws)      # not yet zero-filled: nothing is written
+        assert (y == 7.0).all()
+        woq.woq_workspace_init(ws)
+    m.call(x.to(DEV), ids.to(DEV), w.to(DEV), y, ws)
+    assert torch.equal(y.cpu(), before) and woq.woq_read_status(ws) == 0
+
+
+def test_two_graphs_share_a_workspace():
+    """Graphs of two shapes that share a workspace, replayed in turn."""
+    a, b = Experts(6, 256, 384), Experts(5, 384, 128, bits=6)
+    g = gen(15)
+    ws = torch.zeros(max(a.ws(30, 2).numel(), b.ws(3, 3).numel()), dtype=torch.uint8, device=DEV)
+    jobs, want = [], []
+    s = torch.cuda.Stream()
+    for m, T, k in ((a, 30, 2), (b, 3, 3)):
+        ids, w = chosen(g, T, m.E, k)
+        x = torch.randn((T, m.H), generator=g).to(BF)
+        want.append(m.run(x, ids, w)[0])
+        args = [x.to(DEV), ids.to(DEV), w.to(DEV), torch.zeros((T, m.H), dtype=BF, device=DEV)]
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=s):
+                m.call(*args, ws)
+        jobs.append((graph, args[3], args))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for graph, _, _ in jobs:
+            graph.replay()
+    torch.cuda.synchronize()
+    for (_, y, _), ref in zip(jobs, want):
+        assert torch.equal(y.cpu(), ref)
 
 
 def test_experts_large_and_small_activations():

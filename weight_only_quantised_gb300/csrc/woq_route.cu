@@ -9,6 +9,7 @@
 
 #include "woq_block_internal.h"
 #include "woq_device.cuh"
+#include "woq_internal.h"
 #include "woq_kv8_device.cuh"
 
 namespace woq {
@@ -172,8 +173,8 @@ __device__ __forceinline__ bool keep_groups(const Route& p, const F (&c)[PER], F
   const float big = warp_max(real && score > -kInf && score < kInf ? fmaxf(fabsf((float)best), fabsf((float)next)) : 0.0f);
   const float low = -warp_max(in ? -(float)score : -kInf);  // of the kept
   const float high = warp_max(real && !in ? (float)score : -kInf);
-  // s <= 1, and two of them at most make a group's score
-  return !(low < kInf && high > -kInf && low - high <= 4.0f * rel + 0x1p-20f * big);
+  // s <= 1 (two of softmax's together), so two groups' scores are off by 2^-18.9 (2^-16) and their roundings at most
+  return !(low < kInf && high > -kInf && low - high <= 1.25f * rel + 0x1p-20f * big);
 }
 
 template <int PER>
@@ -281,17 +282,16 @@ __device__ __noinline__ int choose_in_64_bits(const Route& p, int row, double* s
   load_row<PER>(p, row, lane, l, b);
   double sum, c[PER];
   softmax_terms<double, PER>(p, l, &m, &sum);
-  uint32_t can;
+  uint32_t can, in = kAll;
+  scores<double, PER>(p, l, b, m, sum, !p.bias && (p.groups == 1 || p.group_best == 1), c, can);
   if (p.groups > 1) {
     unsigned kept;
-    scores<double, PER>(p, l, b, m, sum, !p.bias && p.group_best == 1, c, can);
     keep_groups<double, PER>(p, c, shared, lane, &kept);
-    can &= in_kept_groups<PER>(p, kept, lane);
+    in = in_kept_groups<PER>(p, kept, lane);
+    if (!p.bias && p.group_best == 2) scores<double, PER>(p, l, b, m, sum, true, c, can);
   }
-  uint32_t all;
-  scores<double, PER>(p, l, b, m, sum, !p.bias, c, all);
   unsigned long long key;
-  const int e = best_of<double, PER>(p, c, p.groups > 1 ? can : all, false, lane, &key, nullptr);
+  const int e = best_of<double, PER>(p, c, can & in, false, lane, &key, nullptr);
   return lane < p.k ? e : -1;
 }
 
@@ -334,13 +334,7 @@ __device__ __noinline__ int choose_few(const Route& p, int row, uint32_t few, do
 }
 
 template <int PER>
-__global__ void __launch_bounds__(kWarps * 32) route_kernel(const Route p) {
-  extern __shared__ double s_scores[];  // [kWarps][scratch]
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int row = blockIdx.x * kWarps + warp;
-  dev::pdl_wait_prior_grids();
-  dev::pdl_launch_dependents();
-  if (row >= p.rows) return;
+__device__ __forceinline__ void route_row(const Route& p, int row, int lane, double* shared) {
   const size_t out = (size_t)row * p.k + lane;
   if (p.live && row >= __ldg(p.live)) {
     if (lane < p.k) {
@@ -349,7 +343,6 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const Route p) {
     }
     return;
   }
-  double* const shared = s_scores + warp * p.scratch;
   float l[PER], b[PER], m, sum, c[PER];
   load_row<PER>(p, row, lane, l, b);
   bool bad = false;
@@ -425,6 +418,18 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const Route p) {
 }
 
 template <int PER>
+__global__ void __launch_bounds__(kWarps * 32) route_kernel(const Route p) {
+  extern __shared__ double s_scores[];  // [kWarps][scratch]
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  dev::pdl_wait_prior_grids();
+  dev::pdl_launch_dependents();
+  for (long long row = (long long)blockIdx.x * kWarps + warp; row < p.rows; row += (long long)gridDim.x * kWarps) {
+    route_row<PER>(p, (int)row, lane, s_scores + warp * p.scratch);
+    __syncwarp();  // the next row takes the same scratch
+  }
+}
+
+template <int PER>
 static cudaError_t launch_per(Route p, cudaStream_t s) {
   // scores of a row in 64 bits, and at least room for 64 of them with their experts and places
   p.scratch = p.groups > 1 && p.experts > 128 ? p.experts : 128;
@@ -432,7 +437,10 @@ static cudaError_t launch_per(Route p, cudaStream_t s) {
   p.group_share = 1;
   while (p.group_share * 2 * p.groups <= 32) p.group_share *= 2;
   const size_t smem = (size_t)kWarps * p.scratch * 8;  // 32 KB at most
-  return kv8::launch(route_kernel<PER>, dim3((unsigned)((p.rows + kWarps - 1) / kWarps)), kWarps * 32, smem, s, p);
+  const int sms = sm_count();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  const long long ctas = (p.rows + kWarps - 1) / kWarps, most = (long long)sms * 12;
+  return kv8::launch(route_kernel<PER>, dim3((unsigned)(ctas < most ? ctas : most)), kWarps * 32, smem, s, p);
 }
 
 }  // namespace route
