@@ -80,16 +80,21 @@ __device__ __forceinline__ bool matrix_ok(const uint8_t* m, int bits, int N, int
          h->K == (uint32_t)K;
 }
 
-// y_t = sum over its places, in their order.  The headers of the row's matrices are looked at here, before the wait for
-// the products: a row with one that does not match keeps its y.
+// y_t = sum over its places, in their order.  The row's ids, weights and the headers of its matrices are looked at before the
+// wait for the products: a row with a header that does not match keeps its y.
 __global__ void __launch_bounds__(256) sum_kernel(const Experts p) {
+  __shared__ int s_here[32];
+  __shared__ float s_weight[32];
   const int row = blockIdx.x, tid = threadIdx.x, c = (blockIdx.y * 256 + tid) * 4;
   const size_t first = (size_t)row * p.k;
   dev::pdl_launch_dependents();
   int flags = 0;
   if (tid < p.k) {
     const int e = p.ids[first + tid];
-    if ((unsigned)e < (unsigned)p.experts) {
+    const bool here = (unsigned)e < (unsigned)p.experts;
+    s_here[tid] = here;
+    s_weight[tid] = p.weights[first + tid];
+    if (here) {
       if (!matrix_ok(p.gate_up + (size_t)e * p.gate_up_stride, p.bits, 2 * p.inner, p.hidden) ||
           !matrix_ok(p.down + (size_t)e * p.down_stride, p.bits, p.hidden, p.inner))
         flags = WOQ_DEVERR_HEADER;
@@ -97,19 +102,26 @@ __global__ void __launch_bounds__(256) sum_kernel(const Experts p) {
       flags = WOQ_DEVERR_STATE;
     }
   }
+  const bool bad = __syncthreads_or(flags & WOQ_DEVERR_HEADER);
   dev::pdl_wait_prior_grids();
   if (flags) atomicOr(p.status, (uint32_t)flags);
-  if (__syncthreads_or(flags & WOQ_DEVERR_HEADER) || c >= p.hidden || p.status[2]) return;
+  if (bad || c >= p.hidden || p.status[2]) return;
   float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (int j = 0; j < p.k; ++j) {
-    const size_t place = first + j;
-    if ((unsigned)p.ids[place] >= (unsigned)p.experts) continue;
-    const float w = p.weights[place];
-    const float4 v = *reinterpret_cast<const float4*>(p.parts + place * p.hidden + c);
-    y.x = fmaf(w, v.x, y.x);
-    y.y = fmaf(w, v.y, y.y);
-    y.z = fmaf(w, v.z, y.z);
-    y.w = fmaf(w, v.w, y.w);
+  const float* const parts = p.parts + first * p.hidden + c;
+  for (int j = 0; j < p.k; j += 8) {
+    float4 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (j + i < p.k && s_here[j + i]) v[i] = *reinterpret_cast<const float4*>(parts + (size_t)(j + i) * p.hidden);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (j + i < p.k && s_here[j + i]) {
+        const float w = s_weight[j + i];
+        y.x = fmaf(w, v[i].x, y.x);
+        y.y = fmaf(w, v[i].y, y.y);
+        y.z = fmaf(w, v[i].z, y.z);
+        y.w = fmaf(w, v[i].w, y.w);
+      }
   }
   *reinterpret_cast<uint2*>(p.y + (size_t)row * p.hidden + c) =
       make_uint2(pro::f32_to_bf16_bits(y.x) | pro::f32_to_bf16_bits(y.y) << 16,
