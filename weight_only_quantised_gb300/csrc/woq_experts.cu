@@ -17,10 +17,18 @@ __device__ __forceinline__ void plan(const Experts& p) {
   const int tid = threadIdx.x;
   reinterpret_cast<int4*>(s_next)[tid] = make_int4(0, 0, 0, 0);
   __syncthreads();
-  for (int i = tid; i < p.entries; i += kBeginThreads) {
-    const int e = p.ids[i];
-    if ((unsigned)e < (unsigned)p.experts) atomicAdd(&s_next[e], 1);
-  }
+  // eight ids are on their way at a time
+  const auto each = [&](auto&& take) {
+    for (int i = tid; i < p.entries; i += 8 * kBeginThreads) {
+      int e[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) e[j] = i + j * kBeginThreads < p.entries ? p.ids[i + j * kBeginThreads] : -1;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if ((unsigned)e[j] < (unsigned)p.experts) take(e[j], i + j * kBeginThreads);
+    }
+  };
+  each([&](int e, int) { atomicAdd(&s_next[e], 1); });
   __syncthreads();
   const int most = p.item_rows;
   int count[kExpertsPerThread], sum = 0, items = 0;
@@ -43,10 +51,7 @@ __device__ __forceinline__ void plan(const Experts& p) {
   }
   __syncthreads();
   // The order of an expert's places may differ from run to run; each is a column of its own, so no result does.
-  for (int i = tid; i < p.entries; i += kBeginThreads) {
-    const int e = p.ids[i];
-    if ((unsigned)e < (unsigned)p.experts) p.order[atomicAdd(&s_next[e], 1)] = i;
-  }
+  each([&](int e, int place) { p.order[atomicAdd(&s_next[e], 1)] = place; });
   if (tid == 0) p.status[1] = (uint32_t)(total & 0x1FFF);
 }
 
