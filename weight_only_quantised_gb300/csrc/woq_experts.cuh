@@ -2,26 +2,26 @@
 //   h_e,t = silu(G_e x_t) * U_e x_t,   part = D_e h,   y_t = sum_j w_tj part_tj.
 //
 // A decode step's few rows choose many experts, so a launch is bound by the bytes of the chosen experts' weights, each read
-// once: a block of 128 x 128 weights arrives at an SM every 380 cycles or so, and what is done for it has to stay below that.
+// once: two blocks of 128 x 128 weights arrive at an SM every 740 cycles, and what is done for them has to stay below that.
 //   - A, the weights, as 8-bit floats: the codes 0 .. 15 of e4m3 are themselves times 2^-9 (the subnormals, and the least
-//     exponent), so a nibble with its top bit flipped is w + 8 with nothing but a mask: 3 operations per 8 weights.  (mma.sync has no
-//     8-bit floats here: the compiler converts them; bf16 takes 9 operations per 8 weights and was issue bound, 48 us where this takes
-//     KERNEL_US.)  int6's two top bits are a product of their own, worth 16.
+//     exponent), so a nibble with its top bit flipped is w + 8 with nothing but a mask: 3 operations per 8 weights.  int6's two
+//     top bits are a product of their own, worth 16.  (mma.sync has no 8-bit floats on this part, the compiler converts them to
+//     f16; with bf16 operands, 9 to 11 operations per 8 weights, it was issue bound: 8 rows of 128 experts 48 us, here 37.)
 //   - B, the rows: x is the sum of a high and a low half in e4m3 (4 significant bits each, bf16 has 8), two columns of B, under
-//     a power of two per row and group of 128.  Exact, but for elements below 2^-13 of the group's largest, which are off by at most
-//     2^-17 of it.  h is taken apart the same way from fp32, with one rounding to about 8 bits (2^-8 at most).
-//   - tcgen05.mma kind::f8f6f4 multiplies in fp32: D[128 rows of weights][2 columns a row], one per group, then
-//     acc += scale (D_high + D_low / 16 - 8 sum(x)) 2^e in fp32, a thread a row of weights.
-// Roles of a CTA (one per SM): two pairs of teams of four warps that make A from a block (shared memory -> registers -> tensor memory)
-// and add up D, in each pair one for gate and one for up (down: two neighbouring tiles), the pairs in turn (a step takes a team 1,200 cycles of
-// latency, a block's bytes 380); a warp that copies blocks (bulk copies, 8 KB each); one that issues the products; two that bring
-// B; and four that take a unit's sums from the teams and finish it (3.5 us and more of latency, during which the teams go on).  The copying and the issuing warp run as whole warps with one elected lane: from a
-// branch on the lane, two copies took 700 cycles and eight products 1,400.
-// The steps (a group of a pair of tiles of an item) are dealt out evenly to the CTAs; a pair that several share is finished
+//     a power of two per row and group of 128.  Exact, but for elements below 2^-13 of the group's largest, which are off by at
+//     most 2^-17 of it.  h is taken apart the same way from fp32, with one rounding (2^-8 at most, of a bf16's kind).
+//   - tcgen05.mma kind::f8f6f4, A in tensor memory: D[128 rows of weights][2 columns a row] in fp32, one per group, then
+//     acc += scale (D_high + D_low / 16 - 8 sum(x)) 2^e in fp32, a thread a row of weights.  M 128, N 16 to 64, K 32 takes 32 cycles
+//     whatever N is.
+// Roles of a CTA (one per SM): two pairs of teams of four warps, which make A from a block (shared memory -> registers -> tensor
+// memory) and add up D, in each pair one team for gate and one for up (down: two neighbouring tiles), the pairs in turn, as
+// a step takes a team 1,500 cycles of latency; a warp that copies blocks (bulk copies of 8 KB); one that issues the
+// products; two that bring B; and four that take a unit's sums from the teams and finish it (2 us and more of latency,
+// during which the teams go on).  The copying and the issuing warp run as whole warps with one elected lane: from a branch on the
+// lane, two copies took 700 cycles and eight products 1,400.
+// The steps (a group of a pair of tiles of an item) are dealt out evenly to the CTAs; a unit that several share is finished
 // by the one that comes last, from all their sums in CTA order, and nobody waits for another CTA.
 #pragma once
-
-#include <math.h>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -41,7 +41,7 @@ constexpr int kTeamThreads = 128;
 // warps 0 .. 15: the teams
 constexpr int kProducer = 16, kIssuer = 17, kBringer = 18, kBringers = 2, kFinisher = 20, kFinishers = 4;
 constexpr int kThreads = (kFinisher + kFinishers) * 32;
-constexpr int kColumns = 512;       // of tensor memory
+constexpr int kColumns = 512;  // of tensor memory
 
 // ---------------------------------------------------------------------------------------- halves
 
@@ -161,6 +161,7 @@ __device__ __forceinline__ void fence_for_products() { asm volatile("fence.proxy
 
 // ---------------------------------------------------------------------------------------- products
 
+// Sizes of a kernel for N columns of B (items of N / 2 rows).
 template <int BITS, int N>
 struct Shape {
   static constexpr int kRows = N / 2;  // of an item
@@ -184,14 +185,15 @@ struct Shape {
 
 struct Barriers {
   uint64_t weights[12], operands[12], empty[12];  // operands: a step's B (one arrival) and its two A (eight)
-  uint64_t done[2][2];                             // a pair's products
-  uint64_t given[2][2], taken[2][2];  // a pair's sums of a unit, to the finishers
-  uint64_t finishers;           // where their warps meet
+  uint64_t done[2][2];                            // a pair's products
+  uint64_t given[2][2], taken[2][2];              // a pair's sums of a unit, to the finishers
+  uint64_t finishers;                             // where their warps meet
   uint32_t tmem;
   int fail, last;
 };
 static_assert(sizeof(Barriers) <= 1024, "misc");
 
+// GATED: rows of gate and up, silu and product, h in halves; else the down projection's parts.
 template <int BITS, bool GATED, int N>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
   typedef Shape<BITS, N> Z;
