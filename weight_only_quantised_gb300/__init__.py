@@ -835,8 +835,8 @@ def woq_block_norm(u, r, r_out, out, post=None, gate=None, pre=None, alpha: floa
     D = u.shape[1]
     ukind, rkind = _kind(u, "u"), _kind(r, "r")
     on = _shared_device(u)
-    if r_out is not r and r_out.dtype is not r.dtype:
-        raise ValueError(f"r_out: expected {r.dtype}, got {r_out.dtype}")
+    if getattr(r_out, "dtype", None) is not r.dtype:
+        raise ValueError(f"r_out: expected {r.dtype}, got {getattr(r_out, 'dtype', r_out)}")
     shape, rname = (T, D), _F32 if rkind else _BF16
     if gate is not None and (gate.dim() != 2 or gate.shape[1] != D or (T > 0 and (gate.shape[0] < 1 or T % gate.shape[0]))):
         raise ValueError(f"gate: expected [rows, {D}] with rows a divisor of {T}, got {list(gate.shape)}")
