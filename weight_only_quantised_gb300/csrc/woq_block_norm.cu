@@ -4,7 +4,7 @@
 //   h = r' rsqrt(mean(r'^2) + eps) (pre + offset)
 //
 // A row is read once: one CTA holds its u and r in registers through both sums.  Bound by DRAM and the latency of the
-// sums: 8,190 x 5120 bf16 62 us (0.81 of the copy rate), 2,049 x 4096 fp32 21.6 (0.81), one row 2.1 on the device.
+// sums: 8,190 x 5120 bf16 62 us (0.81 of the copy rate), 2,049 x 4096 fp32 21.6 (0.81), one row 2.2 on the device.
 // Rows that stay with a CTA, the next one on its way meanwhile (in registers or through cp.async), were slower: 80 us.
 #include <cuda_bf16.h>
 
