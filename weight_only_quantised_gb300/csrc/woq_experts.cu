@@ -69,10 +69,9 @@ __global__ void __launch_bounds__(kBeginThreads) begin_kernel(const Experts p) {
   const uint2 x = *reinterpret_cast<const uint2*>(p.x + group * kGroup + lane * 4);
   const int e = group_exponent(__reduce_max_sync(~0u, most_field(most2(x.x, x.y))));
   uint32_t high, low;
-  float sum = 0.0f;
+  int sum;
   halves4(x.x, x.y, e, high, low, sum);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+  sum = __reduce_add_sync(~0u, sum);
   uint8_t* const to = p.x_halves + group * 256 + (lane >> 2) * 32 + (lane & 3) * 4;
   *reinterpret_cast<uint32_t*>(to) = high;
   *reinterpret_cast<uint32_t*>(to + 16) = low;

@@ -11,7 +11,7 @@
 //     a power of two per row and group of 128.  Exact, but for elements below 2^-13 of the group's largest, which are off by at
 //     most 2^-17 of it.  h is taken apart the same way from fp32, with one rounding (2^-8 at most, of a bf16's kind).
 //   - tcgen05.mma kind::f8f6f4, A in tensor memory: D[128 rows of weights][2 columns a row] in fp32, one per group, then
-//     acc += scale (D_high + D_low / 16 - 8 sum(x)) 2^e in fp32, a thread a row of weights.  M 128, N 16 to 64, K 32 takes 32 cycles
+//     acc += scale (D_high + D_low / 16 - 8 sum(high + low / 16)) 2^e in fp32, a thread a row of weights.  M 128, N 16 to 64, K 32 takes 32 cycles
 //     whatever N is.
 // Roles of a CTA (one per SM): two pairs of teams of four warps, which make A from a block (shared memory -> registers -> tensor
 // memory) and add up D, in each pair one team for gate and one for up (down: two neighbouring tiles), the pairs in turn, as
@@ -74,24 +74,33 @@ __device__ __forceinline__ uint32_t e4m3x4(uint32_t p01, uint32_t p23) {
          (uint32_t)e4m3x2(__uint_as_float(p23 << 16), __uint_as_float(p23 & 0xFFFF0000u)) << 16;
 }
 
+// Four e4m3 summed: a multiple of 2^-9 below 2^11, exact in fp32.
+__device__ __forceinline__ float sum_of_codes(uint32_t c) {
+  uint32_t lo, hi;
+  kv8::f16x4_of_codes<WOQ_KV8_E4M3>(c, lo, hi);
+  return (dev::half_bits_to_float(lo & 0xFFFFu) + dev::half_bits_to_float(lo >> 16)) +
+         (dev::half_bits_to_float(hi & 0xFFFFu) + dev::half_bits_to_float(hi >> 16));
+}
+// What halves hold, high + low / 16, in units of 2^-13 (the low ones' last bit): whole numbers, so sums of them are exact
+// and go by no order.
+__device__ __forceinline__ int held_units(float high, float low) { return __float2int_rn(fmaf(high, 8192.0f, low * 512.0f)); }
+
 // Of four bf16 (two pairs): their high halves (the value without its last four bits), their low ones (the rest, times 16), and
-// the sum of the scaled values.
-__device__ __forceinline__ void halves4(uint32_t x01, uint32_t x23, int e, uint32_t& high, uint32_t& low, float& sum) {
+// the sum of what both hold, in units of 2^-13.
+__device__ __forceinline__ void halves4(uint32_t x01, uint32_t x23, int e, uint32_t& high, uint32_t& low, int& sum) {
   const uint32_t f = (uint32_t)(261 - e) << 7, f2 = f | f << 16, f16 = f2 + 0x02000200u, zero = 0x80008000u;
   const uint32_t h01 = x01 & 0xFFF0FFF0u, h23 = x23 & 0xFFF0FFF0u;
   high = e4m3x4(fma2(h01, f2, zero), fma2(h23, f2, zero));
   low = e4m3x4(fma2(h01, f16 ^ zero, fma2(x01, f16, zero)), fma2(h23, f16 ^ zero, fma2(x23, f16, zero)));
-  const float s = group_factor(e);
-  sum = fmaf(__uint_as_float(x01 << 16), s, sum);
-  sum = fmaf(__uint_as_float(x01 & 0xFFFF0000u), s, sum);
-  sum = fmaf(__uint_as_float(x23 << 16), s, sum);
-  sum = fmaf(__uint_as_float(x23 & 0xFFFF0000u), s, sum);
+  sum = held_units(sum_of_codes(high), sum_of_codes(low));
 }
 
 // A group of a row in halves: 8 x [16 high][16 low], 256 bytes; beside it what undoes the factor and what takes the codes'
-// offset off (-8 or -32 times the sum, in codes' units).
-__device__ __forceinline__ float2 group_meta(int e, float sum, int bits) {
-  return make_float2(group_undo(e), sum * (bits == 4 ? -0x1p-6f : -0x1p-4f));
+// offset off: -8 or -32 times the sum of what the halves hold (not of what they were made from: the products see the halves, and a
+// rounding must not count w + 8 times), in codes' units.  Rounded once from the whole number, as a sum of products with codes
+// that are all 0 is, so those give 0.
+__device__ __forceinline__ float2 group_meta(int e, int units, int bits) {
+  return make_float2(group_undo(e), (float)units * (bits == 4 ? -0x1p-19f : -0x1p-17f));
 }
 
 // ----------------------------------------------------------------------------------- tensor memory
@@ -492,21 +501,22 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
           for (int t = 0; t < rows; ++t) {
             const float v = sums[t * 256] * group_factor(exponent(t));
             const uint16_t high = e4m3x2(v, 0.0f);
-            uint32_t back;
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(high));
-            const uint16_t low = e4m3x2((v - dev::half_bits_to_float(back & 0xFFFFu)) * 16.0f, 0.0f);
+            uint32_t held;
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(held) : "h"(high));
+            const float first = dev::half_bits_to_float(held & 0xFFFFu);
+            const uint16_t low = e4m3x2((v - first) * 16.0f, 0.0f);
             uint8_t* const to = p.h_halves + (place_of(t) * (p.inner / kGroup) + slice) * 256 + (me >> 4) * 32 + (me & 15);
             to[0] = (uint8_t)high;
             to[16] = (uint8_t)low;
-            // the sum in units of 2^-13, the low halves' last bit (|v| <= 2^8)
-            const int sum = __reduce_add_sync(~0u, __float2int_rn(v * 8192.0f));
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(held) : "h"(low));
+            const int sum = __reduce_add_sync(~0u, held_units(first, dev::half_bits_to_float(held & 0xFFFFu)));
             if (lane == 0) s_sums[quad * Z::kRows + t] = sum;
           }
           if (!meet()) break;
           if (me < rows) {
             const int* const q = s_sums + me;
             p.h_meta[(size_t)places * (p.inner / kGroup) + slice] =
-                group_meta(exponent(me), (float)(q[0] + q[Z::kRows] + q[2 * Z::kRows] + q[3 * Z::kRows]) * 0x1p-13f, BITS);
+                group_meta(exponent(me), q[0] + q[Z::kRows] + q[2 * Z::kRows] + q[3 * Z::kRows], BITS);
           }
           if (!meet()) break;  // the maxima and sums may be written again
         }
