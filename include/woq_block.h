@@ -55,8 +55,8 @@ WOQ_API int woq_block_norm(const void* u, int u_dtype, const void* r, void* r_ou
  * ids: device int32 [T][k]; weights: device fp32 [T][k].  Places left over (fewer than k experts may be
  * chosen) get id -1 and weight 0, as do all places of rows from *live on (device int32; NULL: T).
  * A NaN logit counts as the largest, and makes the weights of its row's chosen NaN; so does +inf under softmax.
- * The choice is that of exact arithmetic: scores are compared in fp32 where they are further apart than its error,
- * else in fp64.  bias finite.
+ * The choice is that of scores formed in fp64: they are compared in fp32 where they are further apart than its error, else in
+ * fp64 (where sigmoids of logits above 36 can tie under a bias).  bias finite.
  *   1 <= E <= 1024; 1 <= k <= 32, k <= E; groups 1 .. 32 divides E; 1 <= top_groups <= groups, k <= top_groups * E / groups;
  *   group_best 1 or 2 (2: E / groups >= 2); scale finite; row_stride >= E.  logits 16-byte aligned, the others 4.
  * Errors: WOQ_ERR_NULL, WOQ_ERR_ALIGN, WOQ_ERR_SHAPE, WOQ_ERR_CUDA.

@@ -88,3 +88,51 @@ def test_small_codes(T, bits):
     g = B.gen(T)
     ids, w = B.chosen(g, T, 3, 1)
     m.check(torch.randn((T, 256), generator=g).to(BF), ids, w)
+
+
+# --------------------------------------------------------------------------------------- near scores
+
+
+@pytest.mark.parametrize("E", [0, 64, 100, 256, 1024])
+@pytest.mark.parametrize("l,k", [([20.0, 20, 21], 1), ([18.0] * 9 + [19], 8), ([25.0] + [18.0] * 40 + [19] + [18.0] * 20, 4)])
+def test_route_equal_scores_hide_none(l, k, E):
+    """Sigmoids that fp32 rounds to 1, most of them of the very same logit: the greater one behind them is chosen."""
+    for at in (0, E // 3):
+        row = torch.full((1, max(E, len(l))), 3.0)
+        row[0, at: at + len(l)] = torch.tensor(l)[: row.shape[1] - at]
+        B.route_case(row, k, bias=torch.zeros(row.shape[1]), score=1)
+
+
+@pytest.mark.parametrize("groups", [1, 3])
+def test_route_softmax_rounds_logits_together(groups):
+    """l - m is the same in fp32 for the logits near 0."""
+    l = torch.tensor([[20.0, 1e-7, 1e-7, 2e-7, 1e-7, -1.0]])
+    B.route_case(l, 2, bias=torch.zeros(6), score=0, groups=groups, top_groups=max(1, groups - 1))
+
+
+def test_route_a_larger_error_behind_the_next():
+    route = lambda l, b: B.route_case(torch.tensor([l]), 1, bias=torch.tensor(b), score=1)  # noqa: E731
+    route([-6.906785, -6.906797, 16.55], [0.0, 0.0, -0.998999])
+    route([-17.9, -19.5, 1.1547612], [0.010547847, 0.010547847, -0.7498316])
+
+
+@pytest.mark.parametrize("score", [0, 1])
+@pytest.mark.parametrize("E,k", [(6, 1), (6, 2), (24, 3), (60, 8), (200, 4), (256, 8), (700, 31), (900, 32)])
+@pytest.mark.parametrize("t", [0.0, 0.01, -0.3])
+def test_route_small_and_large_scores_about_one_value(E, k, score, t):
+    """Scores of some 1e-9 under a bias of t, and large ones whose bias brings them to t within their error in fp32 (far more than
+    the gaps of the small ones): which are chosen, and in what order, is not told by neighbours."""
+    g = B.gen(E + k + int(100 * t))
+    T, large = 150, max(2, E // 12)
+    rows = torch.empty((T, E))
+    rows[:] = torch.rand(E, generator=g) * 3 - 20 - (score == 0) * 2
+    few = torch.randperm(E, generator=g)[:large]
+    rows[:, few] = torch.rand(large, generator=g) * 2.5 - 0.5
+    rows += (torch.rand((T, E), generator=g) < 0.3) * torch.randint(-2, 3, (T, E), generator=g) * 2.0 ** -23   # some ulps here and there
+    x = rows[0].double()
+    s = torch.softmax(x, 0) if score == 0 else torch.sigmoid(x)
+    bias = torch.full((E,), t)
+    bias[few] = (t - s[few] + (torch.rand(large, generator=g).double() - 0.5) * 2e-7).float()
+    B.route_case(rows, k, bias=bias, score=score)
+    if E % 4 == 0 and E // 2 >= k:
+        B.route_case(rows, k, bias=bias, score=score, groups=4, top_groups=2, group_best=2)

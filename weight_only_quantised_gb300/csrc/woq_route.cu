@@ -1,11 +1,12 @@
 // Routing of rows to experts (include/woq_block.h): scores, groups, the k best and their weights, a warp per row.
 //
-// Which experts are chosen is decided as in exact arithmetic.  Without a bias the choice goes by the logits, which both scores grow
+// Which experts are chosen is decided as by scores in fp64.  Without a bias the choice goes by the logits, which both scores grow
 // with.  With one, scores c are formed in fp32; e^x and 1 / x are good to 2 ulp (CUDA's expf and __fdividef), so that
-//   sigmoid: s is within 2^-20.9 s; softmax: within 2^-17 s (the sum's rounding and the exponent's included); c within that and 2^-24 |c|.
-// Where two neighbours of the order (the k chosen and the next) lie nearer than both errors and do not have the very same logit
-// and bias, those that may be among the k are put in order in fp64 (sigmoid: some ten scores, a lane each), or the whole row is done
-// again in fp64 (softmax, more than 64 such scores, groups too near to tell): one row in some hundreds.
+//   sigmoid: s is within 2^-20.8 s; softmax: within 2^-16.7 s (the sum's rounding and the exponent's included); c within that and 2^-24 |c|.
+// Sure is an order whose neighbours lie further apart than both errors (or have the very same logit and bias), and a choice that leaves
+// nothing out that its own error (a large s under a negative bias has a large one) could lift to the k-th. Else those that may be among
+// the k are put in order in fp64 (sigmoid: some ten scores, a lane each), or the whole row is done again in fp64 (softmax, more than
+// 64 such scores, groups too near to tell): one row in some hundreds.
 // The k best: as many lanes' largest scores as are wanted bound them from below; what is not below (some ten) goes to a lane each
 // and finds its place by comparing all with all.  Bound by issue and latency: 8,191 rows x 256 experts in groups 27 us (some 1,500
 // instructions a row; the same with one argument of the maximum after another 35, the first right version 57), 16,000 x 60 12 us.
@@ -190,9 +191,9 @@ __device__ __forceinline__ uint32_t in_kept_groups(const Route& p, unsigned kept
   return in;
 }
 
-// The k best of those that `can`; one more where `extra`.  Lane i gets the i-th one's expert (else -1) and order.
+// The k best of those that `can`.  Lane i gets the i-th one's expert (else -1) and order.
 template <class F, int PER>
-__device__ __forceinline__ int best_of(const Route& p, const F (&c)[PER], uint32_t can, bool extra, int lane, typename Key<F>::type* mine,
+__device__ __forceinline__ int best_of(const Route& p, const F (&c)[PER], uint32_t can, int lane, typename Key<F>::type* mine,
                                        uint32_t* shared) {
   typedef typename Key<F>::type K;
   K key[PER];
@@ -203,7 +204,7 @@ __device__ __forceinline__ int best_of(const Route& p, const F (&c)[PER], uint32
   for (int j = 0; j < PER; ++j) top = key[j] > top ? key[j] : top;
   int chosen = -1;
   *mine = 0;
-  const int rounds = p.k + (extra && p.k < 32);
+  const int rounds = p.k;
   if constexpr (sizeof(F) == 4 && PER > 2) {
     // As many lanes' largest as are wanted: nothing below the least of these is among the best.  What is not below (some ten
     // experts) goes to a lane each, and is placed by comparing all with all.
@@ -279,6 +280,11 @@ __device__ __forceinline__ int best_of(const Route& p, const F (&c)[PER], uint32
   return chosen;
 }
 
+// How far a score in fp32 may be off; s is c - b, 2^-120 covers one that underflows.
+__device__ __forceinline__ float error_of(const Route& p, float c, float b) {
+  return fmaf(p.softmax ? 0x1p-16f : 0x1p-20f, fabsf(c - b), fmaf(0x1p-22f, fabsf(c), 0x1p-120f));
+}
+
 // All of a row in 64 bits.
 template <int PER>
 __device__ __noinline__ int choose_in_64_bits(const Route& p, int row, double* shared, int lane) {
@@ -295,7 +301,7 @@ __device__ __noinline__ int choose_in_64_bits(const Route& p, int row, double* s
     if (!p.bias && p.group_best == 2) scores<double, PER>(p, l, b, m, sum, true, c, can);
   }
   unsigned long long key;
-  const int e = best_of<double, PER>(p, c, can & in, false, lane, &key, nullptr);
+  const int e = best_of<double, PER>(p, c, can & in, lane, &key, nullptr);
   return lane < p.k ? e : -1;
 }
 
@@ -367,34 +373,38 @@ __device__ __forceinline__ void route_row(const Route& p, int row, int lane, dou
   }
   can &= kept_members;
   uint32_t key;
-  int chosen = best_of<float, PER>(p, c, can, p.bias != nullptr, lane, &key, reinterpret_cast<uint32_t*>(shared));
+  int chosen = best_of<float, PER>(p, c, can, lane, &key, reinterpret_cast<uint32_t*>(shared));
   const bool has_x = chosen >= 0;
   const float x = has_x ? logit(p, (size_t)row * p.stride + chosen) : -kInf;
   bool again = !sure;
   uint32_t few = 0;
   if (p.bias) {
-    // each chosen one (and the next) against the one before it
     const float eb = has_x ? __ldg(p.bias + chosen) : 0.0f;
     const float v = __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
-    const float v0 = __shfl_up_sync(kAll, v, 1), b0 = __shfl_up_sync(kAll, eb, 1), x0 = __shfl_up_sync(kAll, x, 1);
-    const float rel = p.softmax ? 0x1p-16f : 0x1p-19f;  // twice the relative error of s in fp32, and more
-    const float slack = rel * (fabsf(v0 - b0) + fabsf(v - eb)) + 0x1p-21f * (fabsf(v0) + fabsf(v)) + 0x1p-120f;  // s may underflow
-    const bool near = lane > 0 && has_x && v0 < kInf && !(x == x0 && eb == b0) && v0 - v <= slack;
-    if (p.k == 32 && !again) again = true;  // there is no lane for the next one
-    if (__any_sync(kAll, near)) {
-      // what is not surely below the k-th: the scores' own errors are rel (c - b) / 2 and 2^-22 c at most
-      const float kth = __shfl_sync(kAll, v, p.k - 1);
-      const bool full = __shfl_sync(kAll, has_x, p.k - 1);
-      if (!p.softmax && !again && !bad) {
+    const float err = error_of(p, v, eb);
+    // their order: each chosen one against the one before it
+    const float v0 = __shfl_up_sync(kAll, v, 1), b0 = __shfl_up_sync(kAll, eb, 1), x0 = __shfl_up_sync(kAll, x, 1), err0 = __shfl_up_sync(kAll, err, 1);
+    bool near = lane > 0 && has_x && v0 < kInf && !(x == x0 && eb == b0) && v0 - v <= err0 + err;
+    // the choice: what is not surely below all of them, apart from the k-th's equals (the lower numbers of these are chosen)
+    const float kth = __shfl_sync(kAll, v, p.k - 1), kth_x = __shfl_sync(kAll, x, p.k - 1), kth_b = __shfl_sync(kAll, eb, p.k - 1);
+    const bool full = __shfl_sync(kAll, has_x, p.k - 1);  // else all that can be chosen are
+    if (full && kth < kInf) {
+      const float least = -warp_max(has_x && v < kInf ? err - v : -kInf);
+      uint32_t equal = 0;
 #pragma unroll
-        for (int j = 0; j < PER; ++j)
-          if ((can >> j & 1u) && (!full || c[j] + 2.0f * (rel * (1.0f + fabsf(kth) + fabsf(c[j])))  >= kth)) few |= 1u << j;
-        if (__reduce_add_sync(kAll, (unsigned)__popc(few)) > 64u) few = 0, again = true;
-        else again = false;
-        if (!again) chosen = choose_few<PER>(p, row, few, shared, lane);
-      } else {
-        again = true;
+      for (int j = 0; j < PER; ++j) {
+        few |= (uint32_t)(c[j] + error_of(p, c[j], b[j]) >= least) << j;
+        equal |= (uint32_t)(l[j] == kth_x && b[j] == kth_b) << j;
       }
+      few &= can;
+      const unsigned others = __reduce_add_sync(kAll, (unsigned)__popc(few & ~equal));
+      near |= others != (unsigned)__popc(__ballot_sync(kAll, has_x && !(x == kth_x && eb == kth_b)));
+    } else {
+      few = can;
+    }
+    if (__any_sync(kAll, near) && !again) {
+      again = p.softmax || bad || __reduce_add_sync(kAll, (unsigned)__popc(few)) > 64u;
+      if (!again) chosen = choose_few<PER>(p, row, few, shared, lane);
     }
   }
   if (again) chosen = choose_in_64_bits<PER>(p, row, shared, lane);
