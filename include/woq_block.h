@@ -88,8 +88,8 @@ WOQ_API int woq_route(const woq_router* cfg, const void* logits, int dtype, int 
  *   Activations are not quantised to 8 bits as the linears': an x is taken as the sum of two 8-bit floats (e4m3) under a power of two
  *   for each row and group of 128 elements, exactly but for elements below 2^-13 of the group's largest, which are off by at most 2^-17 of that; h = silu(g) * u
  *   is taken so too, rounded to at most 2^-8 of itself.  Products are exact, sums fp32, a group of 128 times its scale in
- *   fp32, y rounded once.  |x| below 2^100.  What a row gives does not depend on the run, nor on the other rows' x (the order of its sums goes
- *   by how many experts the call works on).
+ *   fp32, y rounded once.  |x| below 2^100.  What a row gives does not depend on the run, nor on the other rows' x and weights; the
+ *   order of its sums goes by the ids of all rows of the call (how many places each expert has), so its last bits can go by those.
  *   bits 4 or 6; 1 <= E <= 1024; 1 <= k <= 32; H, I multiples of 128 in [128, 32768]; 0 <= T, T k <= 32768.
  *   ws: device, 16-byte aligned, woq_experts_workspace(...) bytes, zero-filled once before first use
  *   (woq_workspace_init); launches of different shapes may use one that is large enough, launches that can overlap must not.

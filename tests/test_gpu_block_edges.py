@@ -136,3 +136,36 @@ def test_route_small_and_large_scores_about_one_value(E, k, score, t):
     B.route_case(rows, k, bias=bias, score=score)
     if E % 4 == 0 and E // 2 >= k:
         B.route_case(rows, k, bias=bias, score=score, groups=4, top_groups=2, group_best=2)
+
+
+# ------------------------------------------------------------------------------------- run to run
+
+
+@pytest.mark.parametrize("bits", [4, 6])
+@pytest.mark.parametrize("E,k,T", [(2, 2, 200), (2, 2, 2000), (5, 2, 33), (40, 8, 700)])
+def test_experts_repeat_bit_for_bit(E, k, T, bits):
+    """Several items of an expert, whose products are cut between CTAs at different steps: no sum goes by which warp or CTA
+    comes first."""
+    m = B.Experts(E, 2048, 640 if E < 40 else 256, bits)
+    g = B.gen(T)
+    ids, w = B.chosen(g, T, E, k)
+    x, ids, w, ws = torch.randn((T, 2048), generator=g).to(BF).to(DEV), ids.to(DEV), w.to(DEV), m.ws(T, k)
+    ys = torch.empty((60, T, 2048), dtype=BF, device=DEV)
+    for y in ys:
+        m.call(x, ids, w, y, ws)
+    assert all(torch.equal(y, ys[0]) for y in ys) and woq.woq_read_status(ws) == 0
+
+
+@pytest.mark.parametrize("T,k", [(1, 1), (1, 32), (3, 11), (9, 29), (257, 1), (600, 7), (1024, 32)])
+def test_experts_places_of_any_number(T, k):
+    """Runs of places of a warp that end anywhere; ids out of range and places without an expert among them."""
+    m = B.Experts(7, 128, 128)
+    g = B.gen(T * k)
+    ids = torch.randint(-1, 7, (T, k), generator=g).int()
+    w = torch.randn((T, k), generator=g)
+    x = torch.randn((T, 128), generator=g).to(BF)
+    keep = torch.randperm(T, generator=g)[:40]
+    y, status = m.run(x, ids, w)
+    want, bound = B.M.experts(x[keep], ids[keep], w[keep], m.gu, m.d)
+    B.M.close(y[keep], want, bound, B.M.B)
+    assert status == 0 and (y[(ids < 0).all(1)] == 0).all()

@@ -9,32 +9,47 @@ cudaError_t launch_products_w4(const Experts& p, bool gated, int sms, cudaStream
 cudaError_t launch_products_w6(const Experts& p, bool gated, int sms, cudaStream_t s);
 
 constexpr int kBeginThreads = 256;
-constexpr int kExpertsPerThread = 1024 / kBeginThreads;
+constexpr int kPlanWarps = kBeginThreads / 32;
+static_assert(kBeginThreads * 4 == 1024, "four experts a thread");
 
-// One CTA: places by expert, and the items (up to p.item_rows places of one expert).  Thread i looks after experts 4 i .. 4 i + 3.
+// One CTA: places by expert, in the order of their numbers, and the items (up to p.item_rows places of one expert).  Which places share
+// an item decides where the products of a row are cut between CTAs, and so the order of its sums: it must not go by which of
+// several warps comes first.  Each warp has a run of places and counts them for itself; thread i looks after experts 4 i .. 4 i + 3.
 __device__ __forceinline__ void plan(const Experts& p) {
-  __shared__ int s_next[1024], s_sums[33];
-  const int tid = threadIdx.x;
-  reinterpret_cast<int4*>(s_next)[tid] = make_int4(0, 0, 0, 0);
+  __shared__ int4 s_counts[kPlanWarps][1024 / 4];  // of each warp's run; then where the next of them goes
+  __shared__ int s_sums[33];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int steps = (p.entries + 31) / 32, warps = min(kPlanWarps, steps), run = (steps + warps - 1) / warps * 32;
+  for (int w = 0; w < warps; ++w) s_counts[w][tid] = make_int4(0, 0, 0, 0);
   __syncthreads();
-  // eight ids are on their way at a time
+  int* const mine = reinterpret_cast<int*>(s_counts[warp]);
+  const int begin = min(warp * run, p.entries), end = min(begin + run, p.entries);
+  // eight ids of a lane are on their way at a time, places i + 32 j; -1: none
   const auto each = [&](auto&& take) {
-    for (int i = tid; i < p.entries; i += 8 * kBeginThreads) {
+    for (int i = begin + lane; i - lane < end; i += 8 * 32) {
       int e[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) e[j] = i + j * kBeginThreads < p.entries ? p.ids[i + j * kBeginThreads] : -1;
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if ((unsigned)e[j] < (unsigned)p.experts) take(e[j], i + j * kBeginThreads);
+      for (int j = 0; j < 8; ++j) {
+        e[j] = i + 32 * j < end ? p.ids[i + 32 * j] : -1;
+        if ((unsigned)e[j] >= (unsigned)p.experts) e[j] = -1;
+      }
+      take(e, i);
     }
   };
-  each([&](int e, int) { atomicAdd(&s_next[e], 1); });
+  each([&](const int (&e)[8], int) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (e[j] >= 0) atomicAdd(mine + e[j], 1);
+  });
   __syncthreads();
   const int most = p.item_rows;
-  int count[kExpertsPerThread], sum = 0, items = 0;
+  int count[4] = {}, sum = 0, items = 0;
+  for (int w = 0; w < warps; ++w) {
+    const int4 c = s_counts[w][tid];
+    count[0] += c.x, count[1] += c.y, count[2] += c.z, count[3] += c.w;
+  }
 #pragma unroll
-  for (int j = 0; j < kExpertsPerThread; ++j) {
-    count[j] = s_next[tid * kExpertsPerThread + j];
+  for (int j = 0; j < 4; ++j) {
     sum += count[j];
     items += (count[j] + most - 1) / most;
   }
@@ -42,16 +57,34 @@ __device__ __forceinline__ void plan(const Experts& p) {
   int total;
   const int before = kv8::block_exclusive_sum(sum << 13 | items, s_sums, &total);
   int first = before >> 13, item = before & 0x1FFF;
+  int4 at = make_int4(first, first + count[0], first + count[0] + count[1], first + count[0] + count[1] + count[2]);
+  for (int w = 0; w < warps; ++w) {
+    const int4 c = s_counts[w][tid];
+    s_counts[w][tid] = at;
+    at.x += c.x, at.y += c.y, at.z += c.z, at.w += c.w;
+  }
 #pragma unroll
-  for (int j = 0; j < kExpertsPerThread; ++j) {
-    s_next[tid * kExpertsPerThread + j] = first;
+  for (int j = 0; j < 4; ++j) {
     for (int i = 0; i < count[j]; i += most, ++item)
-      p.item[item] = ExpertItem{tid * kExpertsPerThread + j, first + i, count[j] - i < most ? count[j] - i : most, 0};
+      p.item[item] = ExpertItem{4 * tid + j, first + i, count[j] - i < most ? count[j] - i : most, 0};
     first += count[j];
   }
   __syncthreads();
-  // The order of an expert's places may differ from run to run; each is a column of its own, so no result does.
-  each([&](int e, int place) { p.order[atomicAdd(&s_next[e], 1)] = place; });
+  each([&](const int (&e)[8], int place) {
+    unsigned same[8];  // the lanes with this expert
+#pragma unroll
+    for (int j = 0; j < 8; ++j) same[j] = __match_any_sync(~0u, e[j]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int next = e[j] >= 0 ? mine[e[j]] : 0, ahead = __popc(same[j] & ((1u << lane) - 1));
+      __syncwarp();
+      if (e[j] >= 0) {
+        if (ahead == 0) mine[e[j]] = next + __popc(same[j]);
+        p.order[next + ahead] = place + 32 * j;
+      }
+      __syncwarp();
+    }
+  });
   if (tid == 0) p.status[1] = (uint32_t)(total & 0x1FFF);
 }
 
