@@ -169,3 +169,33 @@ def test_experts_places_of_any_number(T, k):
     want, bound = B.M.experts(x[keep], ids[keep], w[keep], m.gu, m.d)
     B.M.close(y[keep], want, bound, B.M.B)
     assert status == 0 and (y[(ids < 0).all(1)] == 0).all()
+
+
+# ------------------------------------------------------------------------------ a wait that ran out
+
+
+@pytest.mark.parametrize("bits", [4, 6])
+@pytest.mark.parametrize("T", [1, 6])
+def test_experts_calls_directly_behind_one_that_gave_up(T, bits):
+    """CTAs with a few steps have issued all their copies before a wait runs out: they end with none under way, and the calls
+    behind them on another workspace, which take their place on the SMs, are right."""
+    m = B.Experts(8, 512, 384, bits)
+    g = B.gen(14)
+    ids, w = B.chosen(g, T, 8, 2)
+    x = torch.randn((T, 512), generator=g).to(BF)
+    want, _ = m.run(x, ids, w)
+    x, ids, w, ws, other = x.to(DEV), ids.to(DEV), w.to(DEV), m.ws(T, 2), m.ws(T, 2)
+    y = torch.full((T, 512), 7.0, dtype=BF, device=DEV)
+    for cta in range(4):
+        woq.woq_tune_fault(1, cta, 5000)
+        try:
+            m.call(x, ids, w, y, ws)
+        finally:
+            woq.woq_tune_fault(0, 0, 0)
+        behind = [torch.zeros((T, 512), dtype=BF, device=DEV) for _ in range(3)]
+        for z in behind:
+            m.call(x, ids, w, z, other)
+        assert all(torch.equal(z.cpu(), want) for z in behind) and woq.woq_read_status(other) == 0
+        assert woq.woq_read_status(ws, clear=True) & woq.WOQ_DEVERR_TIMEOUT
+        woq.woq_workspace_init(ws)
+    assert (y == 7.0).all()

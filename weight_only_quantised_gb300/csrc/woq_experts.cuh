@@ -271,11 +271,12 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
     return (bool)__all_sync(~0u, ok);
   };
 
+  int issued = 0, last = -1;  // the producer's copies; the issuer's newest products: pair, buffer and parity
   if (warp == kProducer) {
     if (begin < end) {
       const uint8_t* const matrices = GATED ? p.gate_up : p.down;
       const size_t stride = GATED ? p.gate_up_stride : p.down_stride;
-      int unit = begin / groups, g = begin - unit * groups, issued = 0;
+      int unit = begin / groups, g = begin - unit * groups;
       int at_item = -1, expert = 0;
       const uint8_t *src0, *src1;
       const auto locate = [&]() {
@@ -311,13 +312,9 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
         }
         if (++stage == Z::kStages) stage = 0, parity ^= 1;
       }
-      // nothing may be in flight when the CTA ends, whatever went wrong
-      if (__any_sync(~0u, gave_up()))
-        for (int n = issued > Z::kStages ? issued - Z::kStages : 0; n < issued; ++n)
-          dev::mbar_wait_bounded(&s.weights[n % Z::kStages], (uint32_t)(n / Z::kStages) & 1u, limit);
     }
   } else if (warp == kIssuer) {
-    int stage = 0, last = -1;  // last: the newest products' pair, buffer and parity
+    int stage = 0;
     uint32_t stage_parity = 0;
     const uint32_t base = dev::smem_addr(s_mem);
     for (int i = 0; i < end - begin; ++i) {
@@ -343,8 +340,6 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
       last = (pair * 2 + buffer) * 2 + (turn / Z::kBuffers & 1);
       if (++stage == Z::kStages) stage = 0, stage_parity ^= 1;
     }
-    // products end in order: with the newest, all have
-    if (__any_sync(~0u, gave_up()) && last >= 0) dev::mbar_wait_bounded(&s.done[last >> 2][last >> 1 & 1], (uint32_t)last & 1u, limit);
   } else if (warp >= kBringer && warp < kFinisher) {
     if (!GATED) dev::pdl_wait_prior_grids();  // h
     const int me = warp - kBringer;
@@ -643,10 +638,20 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
       if (++unit_buffer == Z::kUnits) unit_buffer = 0, unit_parity ^= 1;
       while (g >= groups) g -= groups;
     }
+    tmem_wait_stores();  // a step that was given up may have left some
   }
   __syncwarp();
   tmem_fence_before();
   __syncthreads();
+  // Every copy and product has been waited for by whoever takes what it gives, unless a wait ran out: nothing may be in flight when
+  // the CTA ends, so then whoever issued them waits for the last ones (their loops may have ended before).
+  if (s.fail) {
+    if (warp == kProducer)
+      for (int n = max(issued - Z::kStages, 0); n < issued; ++n) dev::mbar_wait_bounded(&s.weights[n % Z::kStages], (uint32_t)(n / Z::kStages) & 1u);
+    // products end in order: with the newest, all have
+    if (warp == kIssuer && last >= 0) dev::mbar_wait_bounded(&s.done[last >> 2][last >> 1 & 1], (uint32_t)last & 1u);
+    __syncthreads();
+  }
   if (warp == kIssuer) {
     tmem_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kColumns) : "memory");
