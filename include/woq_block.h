@@ -93,7 +93,8 @@ WOQ_API int woq_route(const woq_router* cfg, const void* logits, int dtype, int 
  *   bits 4 or 6; 1 <= E <= 1024; 1 <= k <= 32; H, I multiples of 128 in [128, 32768]; 0 <= T, T k <= 32768.
  *   ws: device, 16-byte aligned, woq_experts_workspace(...) bytes, zero-filled once before first use
  *   (woq_workspace_init); launches of different shapes may use one that is large enough, launches that can overlap must not.
- *   A wait that runs out sets WOQ_DEVERR_TIMEOUT: then y is left as it was, by this call and by the next ones until ws has been zero-filled.
+ *   A wait that runs out sets WOQ_DEVERR_TIMEOUT: then y is left as it was, by this call and by the next ones (which set it again,
+ *   whether or not it has been cleared) until ws has been zero-filled.
  *   A chosen expert with a packed matrix whose header does not match sets WOQ_DEVERR_HEADER (woq_read_status(ws, ...)), and
  *   the rows of y that chose it are left as they were.
  * Errors: WOQ_ERR_NULL, WOQ_ERR_ALIGN, WOQ_ERR_SHAPE, WOQ_ERR_LAYOUT (gate_up_bytes or down_bytes too

@@ -199,3 +199,24 @@ def test_experts_calls_directly_behind_one_that_gave_up(T, bits):
         assert woq.woq_read_status(ws, clear=True) & woq.WOQ_DEVERR_TIMEOUT
         woq.woq_workspace_init(ws)
     assert (y == 7.0).all()
+
+
+@pytest.mark.parametrize("T", [1, 40])
+def test_experts_every_call_that_writes_nothing_says_so(T):
+    """Behind a wait that ran out, and a status that was read and cleared: y is not written, and the status says it each time."""
+    m = B.Experts(8, 512, 384)
+    g = B.gen(16)
+    ids, w = B.chosen(g, T, 8, 2)
+    args = torch.randn((T, 512), generator=g).to(BF).to(DEV), ids.to(DEV), w.to(DEV)
+    ws, y = m.ws(T, 2), torch.full((T, 512), 7.0, dtype=BF, device=DEV)
+    woq.woq_tune_fault(1, 0, 5000)
+    try:
+        m.call(*args, y, ws)
+    finally:
+        woq.woq_tune_fault(0, 0, 0)
+    for _ in range(3):
+        assert (y == 7.0).all() and woq.woq_read_status(ws, clear=True) == woq.WOQ_DEVERR_TIMEOUT
+        m.call(*args, y, ws)
+    woq.woq_workspace_init(ws)
+    m.call(*args, y, ws)
+    assert torch.equal(y.cpu(), m.run(*(t.cpu() for t in args))[0]) and woq.woq_read_status(ws) == 0

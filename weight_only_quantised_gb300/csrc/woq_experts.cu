@@ -141,8 +141,11 @@ __global__ void __launch_bounds__(256) sum_kernel(const Experts p) {
   }
   const bool bad = __syncthreads_or(flags & WOQ_DEVERR_HEADER);
   dev::pdl_wait_prior_grids();
+  // a wait that ran out, in this call or in an earlier one: every call that writes nothing says so
+  const bool gave_up = p.status[2] != 0;
+  if (gave_up && tid == 0) flags |= WOQ_DEVERR_TIMEOUT;
   if (flags) atomicOr(p.status, (uint32_t)flags);
-  if (bad || c >= p.hidden || p.status[2]) return;
+  if (bad || c >= p.hidden || gave_up) return;
   float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   const float* const parts = p.parts + first * p.hidden + c;
   for (int j = 0; j < p.k; j += 8) {
