@@ -126,11 +126,18 @@ def _current_device() -> int:
     return _current_device()
 
 
+# Sizes and strides go to the C ABI as int, and ctypes would cut off what does not fit.
+_MOST = 2**31 - 1
+
+
 def _rows(t, name: str) -> int:
     """Row count M of a 2-D activation tensor."""
     if t is None or t.dim() != 2:
         raise ValueError(f"{name}: expected a 2-D [M, K] tensor")
-    return t.shape[0]
+    rows, width = t.shape
+    if rows > _MOST or width > _MOST:
+        raise ValueError(f"{name}: sizes up to {_MOST}, got {list(t.shape)}")
+    return rows
 
 
 def _nbytes(t) -> int:
@@ -657,6 +664,8 @@ def _qkv(cfg, qkv, q_heads, q_out, rope):
         stride = -(-width // 8) * 8  # one row: its stride says nothing
     if stride < need:
         raise ValueError(f"qkv: rows overlap (row stride {stride}, {need} elements a row)")
+    if stride > _MOST:
+        raise ValueError(f"qkv: row strides up to {_MOST}, got {stride}")
     on = _shared_device(qkv)
     ptr = qkv.data_ptr() if on >= 0 else _dptr(qkv[:1], "qkv")  # the rows may be strided
     count = rows * q_heads * cfg.head_dim
@@ -863,6 +872,8 @@ def woq_route(logits, k: int, ids, weights, score: int = ROUTE_SOFTMAX, bias=Non
         stride = E  # one row: its stride says nothing
     if E > 1 and inner != 1 or stride < E:
         raise ValueError(f"logits: expected rows of neighbouring elements, got strides {logits.stride()}")
+    if stride > _MOST:
+        raise ValueError(f"logits: row strides up to {_MOST}, got {stride}")
     ptr = logits.data_ptr() if on >= 0 else _dptr(logits[:1], "logits")
     cfg = _Router(score, E, k, groups, top_groups, group_best, 1 if renormalise else 0, scale)
     status = lib.woq_route(ctypes.byref(cfg), ptr, kind, stride, T, _shaped(bias, "bias", _F32, (E,), on),
@@ -888,6 +899,8 @@ def woq_experts_swiglu(bits: int, E: int, gate_up, down, x_bf16, ids, weights, I
     T = _rows(x_bf16, "x_bf16")
     H = x_bf16.shape[1]
     k = ids.shape[1] if ids.dim() == 2 else -1
+    if k > _MOST or abs(I) > _MOST:
+        raise ValueError(f"ids, I: sizes up to {_MOST}, got {k} places and I {I}")
     on = _shared_device(x_bf16)
     status = lib.woq_experts_swiglu(
         bits, E, gate_up.data_ptr() if _is_bytes(gate_up, on) else _bytes(gate_up, "gate_up"), _nbytes(gate_up),
