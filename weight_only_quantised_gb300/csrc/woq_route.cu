@@ -71,9 +71,10 @@ struct Key<double> {
   typedef unsigned long long type;
 };
 
+// Plain loads here and below: the kernel may be there before what it reads has been written (it waits for the prior grid), and the
+// read-only path is for what nobody writes while a kernel is there.
 __device__ __forceinline__ float logit(const Route& p, size_t at) {
-  const float v = p.f32 ? __ldg(static_cast<const float*>(p.logits) + at)
-                        : dev::bf16_bits_to_float(__ldg(static_cast<const uint16_t*>(p.logits) + at));
+  const float v = p.f32 ? static_cast<const float*>(p.logits)[at] : dev::bf16_bits_to_float(static_cast<const uint16_t*>(p.logits)[at]);
   return v + 0.0f;  // -0 and 0 are one value
 }
 
@@ -83,7 +84,7 @@ __device__ __forceinline__ void load_row(const Route& p, int row, int lane, floa
 #pragma unroll
   for (int j = 0; j < PER; ++j) l[j] = lane + 32 * j < p.experts ? logit(p, at + lane + 32 * j) : -kInf;
 #pragma unroll
-  for (int j = 0; j < PER; ++j) b[j] = p.bias && lane + 32 * j < p.experts ? __ldg(p.bias + lane + 32 * j) : 0.0f;
+  for (int j = 0; j < PER; ++j) b[j] = p.bias && lane + 32 * j < p.experts ? p.bias[lane + 32 * j] : 0.0f;
 }
 
 // Largest logit and the softmax's denominator (0 and 1 for the sigmoid, and for a row without experts).
@@ -326,7 +327,7 @@ __device__ __noinline__ int choose_few(const Route& p, int row, uint32_t few, do
   __syncwarp();
   for (int i = lane; i < total; i += 32) {
     const float x = logit(p, (size_t)row * p.stride + experts[i]);
-    shared[i] = value<double>(p, x, __ldg(p.bias + experts[i]), 0.0f, 1.0);
+    shared[i] = value<double>(p, x, p.bias[experts[i]], 0.0f, 1.0);
   }
   __syncwarp();
   int chosen = -1;
@@ -346,7 +347,7 @@ __device__ __noinline__ int choose_few(const Route& p, int row, uint32_t few, do
 template <int PER>
 __device__ __forceinline__ void route_row(const Route& p, int row, int lane, double* shared) {
   const size_t out = (size_t)row * p.k + lane;
-  if (p.live && row >= __ldg(p.live)) {
+  if (p.live && row >= *p.live) {
     if (lane < p.k) {
       p.ids[out] = -1;
       p.weights[out] = 0.0f;
@@ -379,7 +380,7 @@ __device__ __forceinline__ void route_row(const Route& p, int row, int lane, dou
   bool again = !sure;
   uint32_t few = 0;
   if (p.bias) {
-    const float eb = has_x ? __ldg(p.bias + chosen) : 0.0f;
+    const float eb = has_x ? p.bias[chosen] : 0.0f;
     const float v = __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
     const float err = error_of(p, v, eb);
     // their order: each chosen one against the one before it
