@@ -156,19 +156,19 @@ def test_experts_repeat_bit_for_bit(E, k, T, bits):
     assert all(torch.equal(y, ys[0]) for y in ys) and woq.woq_read_status(ws) == 0
 
 
-@pytest.mark.parametrize("T,k", [(1, 1), (1, 32), (3, 11), (9, 29), (257, 1), (600, 7), (1024, 32)])
+@pytest.mark.parametrize("T,k", [(1, 1), (1, 32), (3, 11), (9, 29), (255, 1), (256, 1), (8, 32), (257, 1), (600, 7), (1024, 32)])
 def test_experts_places_of_any_number(T, k):
-    """Runs of places of a warp that end anywhere; ids out of range and places without an expert among them."""
+    """Runs of places of a warp, and items, that end anywhere; places without an expert among them, or all of one expert."""
     m = B.Experts(7, 128, 128)
     g = B.gen(T * k)
-    ids = torch.randint(-1, 7, (T, k), generator=g).int()
     w = torch.randn((T, k), generator=g)
     x = torch.randn((T, 128), generator=g).to(BF)
     keep = torch.randperm(T, generator=g)[:40]
-    y, status = m.run(x, ids, w)
-    want, bound = B.M.experts(x[keep], ids[keep], w[keep], m.gu, m.d)
-    B.M.close(y[keep], want, bound, B.M.B)
-    assert status == 0 and (y[(ids < 0).all(1)] == 0).all()
+    for ids in (torch.randint(-1, 7, (T, k), generator=g).int(), torch.full((T, k), 6, dtype=torch.int32), torch.where(torch.rand((T, k), generator=g) < 0.9, -1, 5).int()):
+        y, status = m.run(x, ids, w)
+        want, bound = B.M.experts(x[keep], ids[keep], w[keep], m.gu, m.d)
+        B.M.close(y[keep], want, bound, B.M.B)
+        assert status == 0 and (y[(ids < 0).all(1)] == 0).all()
 
 
 # ------------------------------------------------------------------------------ a wait that ran out

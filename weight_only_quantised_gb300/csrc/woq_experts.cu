@@ -10,41 +10,99 @@ cudaError_t launch_products_w6(const Experts& p, bool gated, int sms, cudaStream
 
 constexpr int kBeginThreads = 256;
 constexpr int kPlanWarps = kBeginThreads / 32;
+// Up to so many places each is compared with all others: 64 places 37.6 us (a call of 8 rows of 128 experts), counted 38.9; 128 55.0
+// and 55.9, 256 68.5 and 69.0 (most of that difference the time that the longer code takes to arrive).
+constexpr int kFewEntries = kBeginThreads;
 static_assert(kBeginThreads * 4 == 1024, "four experts a thread");
 
-// One CTA: places by expert, in the order of their numbers, and the items (up to p.item_rows places of one expert).  Which places share
-// an item decides where the products of a row are cut between CTAs, and so the order of its sums: it must not go by which of
-// several warps comes first.  Each warp has a run of places and counts them for itself; thread i looks after experts 4 i .. 4 i + 3.
-__device__ __forceinline__ void plan(const Experts& p) {
+// The plan, made by one CTA: places by expert, in the order of their numbers, and the items (up to p.item_rows places of one expert).
+// Which places share an item decides where the products of a row are cut between CTAs, and so the order of its sums: it must not go by
+// which of several warps comes first.
+
+// Up to a place a thread: the rank of each by comparing it with all others, then a thread a rank.
+__device__ __forceinline__ void plan_few(const Experts& p) {
+  __shared__ int4 s_keys[kBeginThreads / 4];  // expert 256 + place
+  __shared__ int s_sorted[kBeginThreads + 1];
+  __shared__ uint32_t s_firsts[kBeginThreads / 32], s_lasts[kBeginThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = p.entries;
+  const bool busy = warp * 32 < n;
+  int e = tid < n ? p.ids[tid] : -1;
+  if ((unsigned)e >= (unsigned)p.experts) e = 1024;  // none: behind all
+  const int key = e << 8 | tid;
+  reinterpret_cast<int*>(s_keys)[tid] = key;
+  if (tid == 0) s_sorted[n] = 1024;
+  if (lane == 0) s_firsts[warp] = s_lasts[warp] = 0;
+  __syncthreads();
+  if (busy) {
+    int rank = 0;
+#pragma unroll 4
+    for (int j = 0; j < n; j += 4) {
+      const int4 o = s_keys[j >> 2];
+      rank += (o.x < key) + (o.y < key) + (o.z < key) + (o.w < key);
+    }
+    if (tid < n) {
+      s_sorted[rank] = e;
+      if (e < 1024) p.order[rank] = tid;
+    }
+  }
+  __syncthreads();
+  const int expert = busy && tid < n ? s_sorted[tid] : 1024;
+  const bool here = expert < 1024;
+  const unsigned firsts = __ballot_sync(~0u, here && (tid == 0 || s_sorted[tid - 1] != expert));
+  if (lane == 0) s_firsts[warp] = firsts;
+  __syncthreads();
+  int in_item = 0;  // places of the expert before this one, in its item
+  if (here) {
+    int w = warp;
+    uint32_t m = firsts & (2u << lane) - 1;
+    while (m == 0) m = s_firsts[--w];  // the expert's first place is in an earlier word
+    in_item = (tid - (w * 32 + 31 - __clz(m))) & (p.item_rows - 1);  // 8, 16 or 32
+  }
+  const bool last = here && (in_item == p.item_rows - 1 || s_sorted[tid + 1] != expert);
+  const unsigned lasts = __ballot_sync(~0u, last);
+  if (lane == 0) s_lasts[warp] = lasts;
+  __syncthreads();
+  int item = __popc(lasts & (1u << lane) - 1), items = 0;
+#pragma unroll
+  for (int i = 0; i < kBeginThreads / 32; ++i) {
+    const int here_too = __popc(s_lasts[i]);
+    item += i < warp ? here_too : 0;
+    items += here_too;
+  }
+  if (last) p.item[item] = ExpertItem{expert, tid - in_item, in_item + 1, 0};
+  if (tid == 0) p.status[1] = (uint32_t)items;
+}
+
+// Any number: each warp has a run of places and counts them for itself; thread i looks after experts 4 i .. 4 i + 3.
+__device__ __forceinline__ void plan_many(const Experts& p) {
   __shared__ int4 s_counts[kPlanWarps][1024 / 4];  // of each warp's run; then where the next of them goes
   __shared__ int s_sums[33];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int steps = (p.entries + 31) / 32, warps = min(kPlanWarps, steps), run = (steps + warps - 1) / warps * 32;
-  for (int w = 0; w < warps; ++w) s_counts[w][tid] = make_int4(0, 0, 0, 0);
+  const int run = (p.entries + 32 * kPlanWarps - 1) / (32 * kPlanWarps) * 32;
+  for (int w = 0; w < kPlanWarps; ++w) s_counts[w][tid] = make_int4(0, 0, 0, 0);
   __syncthreads();
   int* const mine = reinterpret_cast<int*>(s_counts[warp]);
   const int begin = min(warp * run, p.entries), end = min(begin + run, p.entries);
-  // eight ids of a lane are on their way at a time, places i + 32 j; -1: none
-  const auto each = [&](auto&& take) {
-    for (int i = begin + lane; i - lane < end; i += 8 * 32) {
-      int e[8];
+  // Sixteen ids of a lane are on their way at a time, of places from + lane + 32 j (-1: none); a run of no more is loaded once.
+  constexpr int kAtOnce = 16;
+  int e[kAtOnce];
+  const auto load = [&](int from) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        e[j] = i + 32 * j < end ? p.ids[i + 32 * j] : -1;
-        if ((unsigned)e[j] >= (unsigned)p.experts) e[j] = -1;
-      }
-      take(e, i);
-    }
+    for (int j = 0; j < kAtOnce; ++j) e[j] = from + 32 * j + lane < end ? p.ids[from + 32 * j + lane] : -1;
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j)
+      if ((unsigned)e[j] >= (unsigned)p.experts) e[j] = -1;
   };
-  each([&](const int (&e)[8], int) {
+  for (int from = begin; from < end; from += 32 * kAtOnce) {
+    load(from);
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+    for (int j = 0; j < kAtOnce; ++j)
       if (e[j] >= 0) atomicAdd(mine + e[j], 1);
-  });
+  }
   __syncthreads();
   const int most = p.item_rows;
   int count[4] = {}, sum = 0, items = 0;
-  for (int w = 0; w < warps; ++w) {
+  for (int w = 0; w < kPlanWarps; ++w) {
     const int4 c = s_counts[w][tid];
     count[0] += c.x, count[1] += c.y, count[2] += c.z, count[3] += c.w;
   }
@@ -58,7 +116,7 @@ __device__ __forceinline__ void plan(const Experts& p) {
   const int before = kv8::block_exclusive_sum(sum << 13 | items, s_sums, &total);
   int first = before >> 13, item = before & 0x1FFF;
   int4 at = make_int4(first, first + count[0], first + count[0] + count[1], first + count[0] + count[1] + count[2]);
-  for (int w = 0; w < warps; ++w) {
+  for (int w = 0; w < kPlanWarps; ++w) {
     const int4 c = s_counts[w][tid];
     s_counts[w][tid] = at;
     at.x += c.x, at.y += c.y, at.z += c.z, at.w += c.w;
@@ -70,21 +128,26 @@ __device__ __forceinline__ void plan(const Experts& p) {
     first += count[j];
   }
   __syncthreads();
-  each([&](const int (&e)[8], int place) {
-    unsigned same[8];  // the lanes with this expert
+  for (int from = begin; from < end; from += 32 * kAtOnce) {
+    if (run > 32 * kAtOnce) load(from);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) same[j] = __match_any_sync(~0u, e[j]);
+    for (int q = 0; q < kAtOnce; q += 4) {
+      if (from + 32 * q >= end) break;
+      unsigned same[4];  // the lanes with this expert
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int next = e[j] >= 0 ? mine[e[j]] : 0, ahead = __popc(same[j] & ((1u << lane) - 1));
-      __syncwarp();
-      if (e[j] >= 0) {
-        if (ahead == 0) mine[e[j]] = next + __popc(same[j]);
-        p.order[next + ahead] = place + 32 * j;
+      for (int j = 0; j < 4; ++j) same[j] = __match_any_sync(~0u, e[q + j]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int id = e[q + j], next = id >= 0 ? mine[id] : 0, ahead = __popc(same[j] & ((1u << lane) - 1));
+        __syncwarp();
+        if (id >= 0) {
+          if (ahead == 0) mine[id] = next + __popc(same[j]);
+          p.order[next + ahead] = from + 32 * (q + j) + lane;
+        }
+        __syncwarp();
       }
-      __syncwarp();
     }
-  });
+  }
   if (tid == 0) p.status[1] = (uint32_t)(total & 0x1FFF);
 }
 
@@ -93,7 +156,8 @@ __global__ void __launch_bounds__(kBeginThreads) begin_kernel(const Experts p) {
   dev::pdl_launch_dependents();
   dev::pdl_wait_prior_grids();
   if (blockIdx.x == 0) {
-    plan(p);
+    if (p.entries <= kFewEntries) plan_few(p);
+    else plan_many(p);
     return;
   }
   const int lane = threadIdx.x & 31;

@@ -81,6 +81,11 @@ __device__ __forceinline__ float sum_of_codes(uint32_t c) {
   return (dev::half_bits_to_float(lo & 0xFFFFu) + dev::half_bits_to_float(lo >> 16)) +
          (dev::half_bits_to_float(hi & 0xFFFFu) + dev::half_bits_to_float(hi >> 16));
 }
+__device__ __forceinline__ void of_codes(uint16_t c, float& lo, float& hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(c));
+  lo = dev::half_bits_to_float(d & 0xFFFFu), hi = dev::half_bits_to_float(d >> 16);
+}
 // What halves hold, high + low / 16, in units of 2^-13 (the low ones' last bit): whole numbers, so sums of them are exact
 // and go by no order.
 __device__ __forceinline__ int held_units(float high, float low) { return __float2int_rn(fmaf(high, 8192.0f, low * 512.0f)); }
@@ -492,20 +497,25 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const Experts p) {
             const uint32_t* const m = s_most + t;
             return group_exponent(max(max(m[0], m[Z::kRows]), max(m[2 * Z::kRows], m[3 * Z::kRows])) >> 23);
           };
-#pragma unroll 4
-          for (int t = 0; t < rows; ++t) {
-            const float v = sums[t * 256] * group_factor(exponent(t));
-            const uint16_t high = e4m3x2(v, 0.0f);
-            uint32_t held;
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(held) : "h"(high));
-            const float first = dev::half_bits_to_float(held & 0xFFFFu);
-            const uint16_t low = e4m3x2((v - first) * 16.0f, 0.0f);
-            uint8_t* const to = p.h_halves + (place_of(t) * (p.inner / kGroup) + slice) * 256 + (me >> 4) * 32 + (me & 15);
-            to[0] = (uint8_t)high;
-            to[16] = (uint8_t)low;
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(held) : "h"(low));
-            const int sum = __reduce_add_sync(~0u, held_units(first, dev::half_bits_to_float(held & 0xFFFFu)));
-            if (lane == 0) s_sums[quad * Z::kRows + t] = sum;
+          // two rows at a time (the last of an odd number twice)
+#pragma unroll 2
+          for (int t = 0; t < rows; t += 2) {
+            const int t1 = min(t + 1, rows - 1);
+            const float v0 = sums[t * 256] * group_factor(exponent(t)), v1 = sums[t1 * 256] * group_factor(exponent(t1));
+            const uint16_t high = e4m3x2(v0, v1);
+            float h0, h1, l0, l1;
+            of_codes(high, h0, h1);
+            const uint16_t low = e4m3x2((v0 - h0) * 16.0f, (v1 - h1) * 16.0f);
+            of_codes(low, l0, l1);
+            uint8_t* const to = p.h_halves + (size_t)slice * 256 + (me >> 4) * 32 + (me & 15);
+            const size_t row_bytes = (size_t)(p.inner / kGroup) * 256;
+            uint8_t *const to0 = to + place_of(t) * row_bytes, *const to1 = to + place_of(t1) * row_bytes;
+            to0[0] = (uint8_t)high;
+            to0[16] = (uint8_t)low;
+            to1[0] = (uint8_t)(high >> 8);
+            to1[16] = (uint8_t)(low >> 8);
+            const int sum0 = __reduce_add_sync(~0u, held_units(h0, l0)), sum1 = __reduce_add_sync(~0u, held_units(h1, l1));
+            if (lane == 0) s_sums[quad * Z::kRows + t] = sum0, s_sums[quad * Z::kRows + t1] = sum1;
           }
           if (!meet()) break;
           if (me < rows) {
