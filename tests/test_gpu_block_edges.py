@@ -220,3 +220,50 @@ def test_experts_every_call_that_writes_nothing_says_so(T):
     woq.woq_workspace_init(ws)
     m.call(*args, y, ws)
     assert torch.equal(y.cpu(), m.run(*(t.cpu() for t in args))[0]) and woq.woq_read_status(ws) == 0
+
+
+# ------------------------------------------------------------------------------------ largest calls
+
+
+def sampled(m, T, k, g, rows, **kw):
+    """A call of T rows, some of them against their definition."""
+    ids, w = B.chosen(g, T, m.E, k)
+    x = torch.randn((T, m.H), generator=g).to(BF)
+    y, status = m.run(x, ids, w)
+    keep = torch.randperm(T, generator=g)[:rows]
+    want, bound = B.M.experts(x[keep], ids[keep], w[keep], m.gu, m.d)
+    B.M.close(y[keep], want, bound, B.M.B)
+    assert status == 0
+
+
+@pytest.mark.parametrize("bits", [4, 6])
+@pytest.mark.parametrize("E,T,k", [(1024, 4096, 8), (1024, 2048, 16), (1, 32768, 1), (300, 1, 32)])
+def test_experts_most_places(E, T, k, bits):
+    sampled(B.Experts(E, 128, 128, bits), T, k, B.gen(E + T), 40)
+
+
+@pytest.mark.parametrize("bits", [4, 6])
+@pytest.mark.parametrize("H,I", [(32768, 128), (128, 32768)])
+def test_experts_widest(H, I, bits):
+    m = B.Experts(2, H, I, bits, scale=0.002)
+    for T in (1, 19):
+        sampled(m, T, 2, B.gen(T), 4)
+
+
+def test_norm_and_route_of_more_rows_than_a_grid_dimension_takes_in_y():
+    """70,000 rows and more: rows lie along x."""
+    T = 140000
+    g = B.gen(9)
+    l = torch.randn((T, 8), generator=g)
+    B.route_case(l, 2)
+    B.norm_case(T, 8, F32, BF)
+
+
+@pytest.mark.parametrize("bits", [4, 6])
+@pytest.mark.parametrize("scale", [1e-38, 1e-20, 1e12])
+def test_experts_of_very_small_and_large_rows(scale, bits):
+    """As far as gate times up is within fp32's range (and x among bf16's smallest)."""
+    m = B.Experts(2, 256, 128, bits, scale=0.1)
+    g = B.gen(4)
+    ids, w = B.chosen(g, 9, 2, 1)
+    m.check((torch.randn((9, 256), generator=g) * scale).to(BF), ids, w)
