@@ -30,7 +30,8 @@ extern "C" {
  *   h  = r' / sqrt(mean(r'^2) + eps) * (pre + offset)     (out NULL: not formed)
  * u is a block's output (a linear's fp32 y, or bf16), r the residual stream; r' is rounded to r's
  * type into r_out (which may be r itself), h to bf16 into out.  Everything between is fp32, and
- * h is formed from r' before that rounding; mean squares have to be finite in fp32.
+ * h is formed from r' before that rounding; mean squares have to be finite in fp32, and with eps 0 not below 2^-126 (a row of
+ * zeros is).
  *   u: device bf16 or fp32 [T][D]; r, r_out: device bf16 or fp32 [T][D]; out: device bf16 [T][D];
  *   post, pre: device bf16 [D]; gate: device bf16 [gate_rows][D], row t uses gate row
  *   t / (T / gate_rows) (1: one scale per channel; T: a gate per row); T % gate_rows == 0.
@@ -88,9 +89,11 @@ WOQ_API int woq_route(const woq_router* cfg, const void* logits, int dtype, int 
  *   Activations are not quantised to 8 bits as the linears': an x is taken as the sum of two 8-bit floats (e4m3) under a power of two
  *   for each row and group of 128 elements, exactly but for elements below 2^-13 of the group's largest, which are off by at most 2^-17 of that; h = silu(g) * u
  *   is taken so too, rounded to at most 2^-8 of itself.  Products are exact, sums fp32, a group of 128 times its scale in
- *   fp32, y rounded once.  |x| below 2^100.  What a row gives does not depend on the run, nor on the other rows' x and weights; the
+ *   fp32, y rounded once.  |x| below 2^100; a row whose gate or up, or their
+ *   product, passes fp32's range gets NaN.  What a row gives does not depend on the run, nor on the other rows' x and weights; the
  *   order of its sums goes by the ids of all rows of the call (how many places each expert has), so its last bits can go by those.
- *   bits 4 or 6; 1 <= E <= 1024; 1 <= k <= 32; H, I multiples of 128 in [128, 32768]; 0 <= T, T k <= 32768.
+ *   bits 4 or 6; 1 <= E <= 1024; 1 <= k <= 32; H, I multiples of 128 in [128, 32768]; 0 <= T, T k <= 32768 (a longer
+ *   prompt is cut by rows into several calls).
  *   ws: device, 16-byte aligned, woq_experts_workspace(...) bytes, zero-filled once before first use
  *   (woq_workspace_init); launches of different shapes may use one that is large enough, launches that can overlap must not.
  *   A wait that runs out sets WOQ_DEVERR_TIMEOUT: then y is left as it was, by this call and by the next ones (which set it again,

@@ -4,7 +4,8 @@
 //   h = r' rsqrt(mean(r'^2) + eps) (pre + offset)
 //
 // A row is read once: one CTA holds its u and r in registers through both sums.  Bound by DRAM and the latency of the
-// sums: 8,190 x 5120 bf16 62 us (0.81 of the copy rate), 2,049 x 4096 fp32 21.6 (0.81), one row 2.2 on the device.
+// sums: 8,190 x 5120 bf16 gated 62 to 63 us (0.80 of the copy rate), 2,049 x 4096 fp32 21.6 to 22.4 (0.80), one row 2.3 on the device.
+// Above 5,120 elements a row one CTA stays on an SM and nothing covers its sums: 7,000 x 6144 bf16 70 us (0.73), 5,000 x 7168 86 (0.50).
 // Rows that stay with a CTA, the next one on its way meanwhile (in registers or through cp.async), were slower: 80 us.
 #include <cuda_bf16.h>
 
@@ -142,7 +143,8 @@ template <bool UF32, bool RF32>
 static cudaError_t launch_types(const BlockNorm& p, cudaStream_t s) {
   const int vectors = p.dim / 8, vecs = vectors <= 1024 ? 1 : 2;
   const int threads = ((vectors + vecs - 1) / vecs + 31) / 32 * 32;
-  // a vector a thread up to 8,192 elements (with two or four, 8,190 x 5120 takes 77 or 89 us; with one 62)
+  // a vector a thread up to 8,192 elements (with two or four, 8,190 x 5120 takes 77 or 89 us; with one 62).  Bounds of 512 and 640 threads
+  // leave room for three and four CTAs: 9,000 x 4096 bf16 50.5 us, by the kernel of 1,024 56.6; 8,190 x 5120 60 and 73.5.
   auto kernel = vecs == 2 ? norm_kernel<UF32, RF32, 2, 1024> : threads <= 512 ? norm_kernel<UF32, RF32, 1, 512> : threads <= 640 ? norm_kernel<UF32, RF32, 1, 640> : norm_kernel<UF32, RF32, 1, 1024>;
   return kv8::launch(kernel, dim3((unsigned)p.rows), threads, 0, s, p);
 }
